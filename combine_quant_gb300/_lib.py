@@ -18,6 +18,11 @@ CONFIG_FIELDS = (
     "y_dtype",
 )
 
+EXPERT_CONFIG_FIELDS = (
+    "experts", "rows", "n", "k", "x_dtype", "w_dtype", "out_dtype", "act", "group", "rows_type",
+    "experts_per_rank",
+)
+
 CQ_OK = 0
 CQ_ERR_ARG = -1
 CQ_ERR_UNSUPPORTED = -2
@@ -29,6 +34,7 @@ CQ_ST_BAD_ID = 1
 CQ_ST_BAD_MASK = 2
 CQ_ST_INTERNAL = 4
 CQ_ST_TIMEOUT = 8
+CQ_ST_BAD_ROWS = 16
 CQ_INV_NONE = -1
 CQ_INV_COPY = -2
 CQ_INV_CONST_BASE = -3
@@ -41,11 +47,17 @@ EXPORTS = (
     "cq_dispatch_route", "cq_dispatch_permute", "cq_combine", "moe_dispatch", "moe_combine",
     "cq_read_status", "cq_strerror", "cq_dispatch_noalloc", "cq_combine_quant", "cq_combine_q8",
     "cq_read_combine_status", "cq_check_bounded_wait", "cq_combine_ws", "cq_dispatch_one_kernel",
+    "cq_check_expert_config", "cq_expert_matmul", "cq_expert_matmul_dx", "cq_expert_matmul_dw",
+    "cq_expert_matmul_w4", "cq_read_expert_status",
 )
 
 
 class CqConfig(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int32) for f in CONFIG_FIELDS]
+
+
+class CqExpertConfig(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in EXPERT_CONFIG_FIELDS]
 
 
 class CqError(RuntimeError):
@@ -68,6 +80,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             "(the CUDA path has no fallback)")
     L = ctypes.CDLL(path)
     P, cfgp = ctypes.c_void_p, ctypes.POINTER(CqConfig)
+    ecfgp = ctypes.POINTER(CqExpertConfig)
     i32, i64, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     sig = {
         "cq_check_config": ([cfgp], ctypes.c_int),
@@ -93,6 +106,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "cq_dispatch_noalloc": ([cfgp] + [P] * 13, ctypes.c_int),
         "cq_combine_quant": ([cfgp] + [P] * 5, ctypes.c_int),
         "cq_combine_q8": ([cfgp] + [P] * 9 + [i32, P, P], ctypes.c_int),
+        "cq_check_expert_config": ([ecfgp], ctypes.c_int),
+        "cq_expert_matmul": ([ecfgp] + [P] * 8, ctypes.c_int),
+        "cq_expert_matmul_dx": ([ecfgp] + [P] * 6, ctypes.c_int),
+        "cq_expert_matmul_dw": ([ecfgp] + [P] * 5, ctypes.c_int),
+        "cq_expert_matmul_w4": ([ecfgp] + [P] * 7, ctypes.c_int),
+        "cq_read_expert_status": ([P, P], ctypes.c_int),
         "cq_strerror": ([ctypes.c_int], ctypes.c_char_p),
     }
     for name, (args, res) in sig.items():

@@ -95,6 +95,56 @@ def _c_config(cfg: Config) -> _lib.CqConfig:
     return _lib.CqConfig(**asdict(cfg))
 
 
+@dataclass(frozen=True)
+class ExpertConfig:
+    """Attributes of the expert products (cq_expert_config in include/cq.h)."""
+    experts: int
+    rows: int
+    n: int
+    k: int
+    x_dtype: int = 0       # 0 bf16, 1 fp16, 2 mx fp8 e4m3, 3 mx fp8 e5m2
+    w_dtype: int = 0       # mx weight codes: 0 e4m3, 1 e5m2
+    out_dtype: int = -1    # -1 the token type, 0 bf16, 1 fp16, 2 f32 (expert_matmul_dw)
+    act: int = 0           # 1: SwiGLU, weights with 2n rows
+    group: int = 0         # 4-bit weights: inner elements per scale
+    rows_type: int = 1     # group_rows: 1 counts, 0 running sums per rank
+    experts_per_rank: int = 1
+
+    def as_c(self) -> _lib.CqExpertConfig:
+        return _c_expert_config(self)
+
+    def check(self) -> int:
+        return _lib.load().cq_check_expert_config(ctypes.byref(self.as_c()))
+
+    @property
+    def weight_rows(self) -> int:
+        return 2 * self.n if self.act == 1 else self.n
+
+    @property
+    def scale_cols(self) -> int:
+        """Scale columns of mx rows: Align2(k / 32), as Config.scale_cols."""
+        return (self.k // 32 + 1) // 2 * 2
+
+    @property
+    def mx(self) -> bool:
+        return self.x_dtype in (2, 3)
+
+    @property
+    def in_dtype(self) -> torch.dtype:
+        return {0: torch.bfloat16, 1: torch.float16}.get(self.x_dtype, torch.uint8)
+
+    @property
+    def result_dtype(self) -> torch.dtype:
+        d = self.out_dtype if self.out_dtype >= 0 else int(self.x_dtype == 1)
+        return {0: torch.bfloat16, 1: torch.float16}.get(d, torch.float32)
+
+
+@functools.lru_cache(maxsize=256)
+def _c_expert_config(cfg: ExpertConfig) -> _lib.CqExpertConfig:
+    """The C struct of an expert config, built once per distinct config (treat as read-only)."""
+    return _lib.CqExpertConfig(**asdict(cfg))
+
+
 class DispatchResult(NamedTuple):
     expand_x: torch.Tensor          # [R_max, H] bf16 / int8 / uint8 (e4m3 bytes)
     dynamic_scales: Optional[torch.Tensor]  # f32 [R_max] or uint8 [R_max, SC]
@@ -405,6 +455,122 @@ def combine_q8(cfg: Config, codes: torch.Tensor, scales: torch.Tensor, assist_in
     return y
 
 
+def _expert_buffers(cfg: ExpertConfig, group_rows: torch.Tensor, *tensors) -> torch.device:
+    """Checks the counts and (tensor, name, dtype, shape) quadruples; returns
+    the device."""
+    dev = group_rows.device
+    _need(group_rows, "group_rows", torch.int64)
+    if group_rows.numel() != cfg.experts:
+        raise ValueError(f"group_rows must have {cfg.experts} entries, got {group_rows.numel()}")
+    for t, name, dtype, shape in tensors:
+        if t is None:
+            raise ValueError(f"{name} is required")
+        _need(t, name, dtype, shape, dev)
+    return dev
+
+
+def expert_matmul(cfg: ExpertConfig, x: torch.Tensor, w: torch.Tensor, group_rows: torch.Tensor,
+                  x_scales: Optional[torch.Tensor] = None,
+                  w_scales: Optional[torch.Tensor] = None,
+                  pre: Optional[torch.Tensor] = None,
+                  y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Grouped matrix product over the experts' rows (cq_expert_matmul):
+    y [rows, n], with act 1 SwiGLU of the gate and up products (`pre`
+    [rows, 2n] receives them). `group_rows` is dispatch's expert_token_nums."""
+    R, G, WN, K = cfg.rows, cfg.experts, cfg.weight_rows, cfg.k
+    dev = _expert_buffers(cfg, group_rows, (x, "x", cfg.in_dtype, (R, K)),
+                          (w, "w", cfg.in_dtype, (G, WN, K)))
+    if cfg.mx:
+        _expert_buffers(cfg, group_rows, (x_scales, "x_scales", torch.uint8, (R, cfg.scale_cols)),
+                        (w_scales, "w_scales", torch.uint8, (G, WN, cfg.scale_cols)))
+    elif x_scales is not None or w_scales is not None:
+        raise ValueError("x_scales and w_scales go with mx types only")
+    if y is None:
+        y = torch.empty(R, cfg.n, dtype=cfg.result_dtype, device=dev)
+    _need(y, "y", cfg.result_dtype, (R, cfg.n), dev)
+    if pre is not None and cfg.act != 1:
+        raise ValueError("pre goes with act 1 only")
+    _need(pre, "pre", cfg.result_dtype, (R, WN), dev)
+    with torch.cuda.device(dev):  # the library looks up the current device
+        rc = _lib.load().cq_expert_matmul(ctypes.byref(cfg.as_c()), _ptr(x), _ptr(x_scales), _ptr(w),
+                                          _ptr(w_scales), _ptr(group_rows), _ptr(y), _ptr(pre),
+                                          _stream(dev))
+    _lib.check(rc, "cq_expert_matmul")
+    return y
+
+
+def expert_matmul_dx(cfg: ExpertConfig, dy: torch.Tensor, w: torch.Tensor,
+                     group_rows: torch.Tensor, pre: Optional[torch.Tensor] = None,
+                     dx: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of expert_matmul's input (cq_expert_matmul_dx): [rows, k], or
+    with `pre` [rows, 2k] (the input was SwiGLU of pre) the gradient of pre."""
+    R, G, WN, K = cfg.rows, cfg.experts, cfg.weight_rows, cfg.k
+    dev = _expert_buffers(cfg, group_rows, (dy, "dy", cfg.in_dtype, (R, WN)),
+                          (w, "w", cfg.in_dtype, (G, WN, K)))
+    _need(pre, "pre", cfg.in_dtype, (R, 2 * K), dev)
+    cols = K if pre is None else 2 * K
+    if dx is None:
+        dx = torch.empty(R, cols, dtype=cfg.in_dtype, device=dev)
+    _need(dx, "dx", cfg.in_dtype, (R, cols), dev)
+    with torch.cuda.device(dev):  # the library looks up the current device
+        rc = _lib.load().cq_expert_matmul_dx(ctypes.byref(cfg.as_c()), _ptr(dy), _ptr(w),
+                                             _ptr(group_rows), _ptr(pre), _ptr(dx), _stream(dev))
+    _lib.check(rc, "cq_expert_matmul_dx")
+    return dx
+
+
+def expert_matmul_dw(cfg: ExpertConfig, dy: torch.Tensor, x: torch.Tensor,
+                     group_rows: torch.Tensor, dw: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of expert_matmul's weights (cq_expert_matmul_dw), in the
+    config's out_dtype: the token type (default) or f32."""
+    R, G, WN, K = cfg.rows, cfg.experts, cfg.weight_rows, cfg.k
+    dev = _expert_buffers(cfg, group_rows, (dy, "dy", cfg.in_dtype, (R, WN)),
+                          (x, "x", cfg.in_dtype, (R, K)))
+    if dw is None:
+        dw = torch.empty(G, WN, K, dtype=cfg.result_dtype, device=dev)
+    _need(dw, "dw", cfg.result_dtype, (G, WN, K), dev)
+    with torch.cuda.device(dev):  # the library looks up the current device
+        rc = _lib.load().cq_expert_matmul_dw(ctypes.byref(cfg.as_c()), _ptr(dy), _ptr(x),
+                                             _ptr(group_rows), _ptr(dw), _stream(dev))
+    _lib.check(rc, "cq_expert_matmul_dw")
+    return dw
+
+
+def expert_matmul_w4(cfg: ExpertConfig, x: torch.Tensor, codes: torch.Tensor,
+                     scales: torch.Tensor, group_rows: torch.Tensor,
+                     zeros: Optional[torch.Tensor] = None,
+                     y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """expert_matmul with 4-bit weights (cq_expert_matmul_w4), for few rows per
+    expert: codes uint8 [G, n or 2n, k/2], scales (and uint8 zeros)
+    [G, n or 2n, k/group]."""
+    R, G, WN, K = cfg.rows, cfg.experts, cfg.weight_rows, cfg.k
+    cols = K // cfg.group if cfg.group > 0 else 0
+    dev = _expert_buffers(cfg, group_rows, (x, "x", cfg.in_dtype, (R, K)),
+                          (codes, "codes", torch.uint8, (G, WN, K // 2)),
+                          (scales, "scales", cfg.in_dtype, (G, WN, cols)))
+    _need(zeros, "zeros", torch.uint8, (G, WN, cols), dev)
+    if y is None:
+        y = torch.empty(R, cfg.n, dtype=cfg.in_dtype, device=dev)
+    _need(y, "y", cfg.in_dtype, (R, cfg.n), dev)
+    with torch.cuda.device(dev):  # the library looks up the current device
+        rc = _lib.load().cq_expert_matmul_w4(ctypes.byref(cfg.as_c()), _ptr(x), _ptr(codes),
+                                             _ptr(scales), _ptr(zeros), _ptr(group_rows), _ptr(y),
+                                             _stream(dev))
+    _lib.check(rc, "cq_expert_matmul_w4")
+    return y
+
+
+def read_expert_status(device=None) -> int:
+    """Synchronise the current stream of `device`, return and clear the expert
+    products' status bits (CQ_ST_BAD_ROWS, CQ_ST_TIMEOUT) of that device."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    st = ctypes.c_uint32(0)
+    with torch.cuda.device(dev):
+        rc = _lib.load().cq_read_expert_status(ctypes.byref(st), _stream(dev))
+    _lib.check(rc, "cq_read_expert_status")
+    return int(st.value)
+
+
 def read_status(workspace: torch.Tensor) -> int:
     """Synchronise the current stream, return and clear the sticky status bits."""
     st = ctypes.c_uint32(0)
@@ -473,6 +639,11 @@ cq_combine = moe_combine = combine
 cq_combine_ws = combine_ws
 cq_combine_quant = combine_quant
 cq_combine_q8 = combine_q8
+cq_expert_matmul = expert_matmul
+cq_expert_matmul_dx = expert_matmul_dx
+cq_expert_matmul_dw = expert_matmul_dw
+cq_expert_matmul_w4 = expert_matmul_w4
+cq_read_expert_status = read_expert_status
 cq_read_status = read_status
 cq_read_combine_status = read_combine_status
 cq_check_bounded_wait = check_bounded_wait

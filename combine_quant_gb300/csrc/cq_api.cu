@@ -497,7 +497,7 @@ const char* cq_strerror(int code) {
   switch (code) {
     case CQ_OK: return "ok";
     case CQ_ERR_ARG: return "invalid argument (range, divisibility, null or misaligned pointer)";
-    case CQ_ERR_UNSUPPORTED: return "unsupported hidden size (needs H % 16 == 0, H % 32 for mx modes)";
+    case CQ_ERR_UNSUPPORTED: return "unsupported size (hidden, n and k need multiples of 16, of 32 for mx and 4-bit types)";
     case CQ_ERR_CUDA: return "CUDA launch or query failed";
     case CQ_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case CQ_ERR_TOO_LARGE: return "problem needs more scratch than the built-in no-alloc buffer";

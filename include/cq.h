@@ -93,9 +93,12 @@ enum {
                          ([DV3] x_active_mask_optional); entries were honoured as given */
   CQ_ST_INTERNAL = 4,  /* a computed row or code fell outside its buffer (an internal
                           consistency guard); the access was skipped */
-  CQ_ST_TIMEOUT = 8    /* a kernel's bounded wait for its own bulk copies gave up (about
+  CQ_ST_TIMEOUT = 8,   /* a kernel's bounded wait for its own bulk copies gave up (about
                           one second); the kernel stopped early and its outputs are
                           incomplete */
+  CQ_ST_BAD_ROWS = 16  /* an expert product's group_rows held a negative count, or counts
+                          that sum to more than the config's rows; such counts were cut to
+                          what fits */
 };
 
 /* Codes stored in the inverse map for slots that own no dispatched row. */
@@ -335,6 +338,102 @@ int cq_check_bounded_wait(uint32_t* gave_up, double* seconds, void* stream);
  * permute kernels, or a negative CQ_ERR_* code for an invalid config.
  * with_smooth_scales: nonzero when the call passes smooth_scales. */
 int cq_dispatch_one_kernel(const cq_config* cfg, int with_smooth_scales);
+
+/*
+ * Expert products -- what runs between cq_dispatch and cq_combine: matrix
+ * products grouped by expert with ragged row counts, forward and backward,
+ * and their form for 4-bit weights. The pages leave the experts to the
+ * caller, so these have no counterpart there.
+ *
+ * Rows are grouped by expert: expert e owns the rows [b_e, b_e + c_e) with
+ * b_0 = 0, b_{e+1} = b_e + c_e, and c_e read on the device from group_rows.
+ * That is the row order of expand_x, and expert_token_nums (int64 [W, L]) is
+ * its group_rows with experts = W * L (a shared-expert rank's unused entries
+ * have no rows). The host never reads the counts: one launch covers every
+ * expert, any count from zero up.
+ */
+typedef struct cq_expert_config {
+  int32_t experts;          /* G in [1, 2048] */
+  int32_t rows;             /* R >= 0: rows of x and y (R_max of the dispatch); the counts may
+                               sum to fewer, the rows past the sum are left untouched */
+  int32_t n;                /* output columns, in [16, 65536], n % 16 == 0 */
+  int32_t k;                /* inner length, in [16, 65536], k % 16 == 0 (k % 32 for mx types) */
+  int32_t x_dtype;          /* 0 bf16, 1 fp16, 2 mx fp8 e4m3, 3 mx fp8 e5m2 (codes with one
+                               e8m0 scale per 32, as dispatch modes 4 and 5 write them) */
+  int32_t w_dtype;          /* mx weight codes: 0 e4m3, 1 e5m2; 0 for the other types */
+  int32_t out_dtype;        /* 0 bf16, 1 fp16, 2 f32 (cq_expert_matmul_dw only), -1 the token
+                               type (bf16 for mx). With bf16 / fp16 x only the token type (or
+                               2 in dw) is accepted. */
+  int32_t act;              /* 0 none; 1 SwiGLU: the weights have 2n rows, gates first */
+  int32_t group;            /* cq_expert_matmul_w4: 32, 64 or 128 inner elements per scale,
+                               k % group == 0; ignored elsewhere */
+  int32_t rows_type;        /* group_rows holds 1 counts, 0 running sums that restart every
+                               experts_per_rank entries (expert_token_nums_type) */
+  int32_t experts_per_rank; /* L >= 1, used with rows_type 0 */
+} cq_expert_config;
+
+/* Validate an expert config; CQ_OK, CQ_ERR_ARG or CQ_ERR_UNSUPPORTED (n or k
+ * not a multiple of 16, or of 32 for k of mx types). */
+int cq_check_expert_config(const cq_expert_config* cfg);
+
+/*
+ * cq_expert_matmul: y[r, :] = W[e] x[r, :] for every row r of every expert e.
+ * With act 1 (SwiGLU): p = W[e] x[r, :], g = p[0:n], u = p[n:2n],
+ * y = u * g / (1 + exp(-g)).
+ *   x          [R, k] token type, or mx codes (uint8)
+ *   x_scales   mx: uint8 [R, SC] with SC = Align2(k / 32), value 2^(s - 127); else NULL
+ *   w          [G, n or 2n, k] the type of x
+ *   w_scales   mx: uint8 [G, n or 2n, SC]; else NULL
+ *   group_rows int64 [G]
+ *   y          [R, n]
+ *   pre        NULL, or with act 1 [R, 2n]: receives p (for the backward pass)
+ * Products accumulate in 32 bits and are rounded once; SwiGLU takes the
+ * unrounded products.
+ */
+int cq_expert_matmul(const cq_expert_config* cfg, const void* x, const uint8_t* x_scales,
+                     const void* w, const uint8_t* w_scales, const int64_t* group_rows, void* y,
+                     void* pre, void* stream);
+
+/*
+ * cq_expert_matmul_dx: the gradient of the product's input, d[r, :] =
+ * W[e]^T dy[r, :] (dy is [R, n], with act 1 the gradient of p, [R, 2n]).
+ *   pre  NULL: dx [R, k] receives d. Not NULL (token type [R, 2k]; the input
+ *        was SwiGLU of pre = [g, u]): dx is [R, 2k] and receives the gradient
+ *        of pre, [d * u * (s + g * s * (1 - s)), d * g * s], s = 1 / (1 + exp(-g)).
+ * x_dtype 0 or 1.
+ */
+int cq_expert_matmul_dx(const cq_expert_config* cfg, const void* dy, const void* w,
+                        const int64_t* group_rows, const void* pre, void* dx, void* stream);
+
+/*
+ * cq_expert_matmul_dw: the gradient of the weights, dw[e] = sum over e's rows
+ * of dy[r, :]^T x[r, :] ([G, n or 2n, k], the token type or f32; zeros for an
+ * expert without rows). x_dtype 0 or 1. Rows of other experts, and rows past
+ * the sum of the counts, do not enter it, whatever they hold.
+ */
+int cq_expert_matmul_dw(const cq_expert_config* cfg, const void* dy, const void* x,
+                        const int64_t* group_rows, void* dw, void* stream);
+
+/*
+ * cq_expert_matmul_w4: cq_expert_matmul with 4-bit weights, for few rows per
+ * expert (decoding; experts = 1 is a plain matrix-vector product):
+ * W[e][i, j] = (q - z) * s.
+ *   codes   uint8 [G, n or 2n, k / 2], element j in the low half of byte j / 2
+ *           when j is even, else in the high half
+ *   scales  token type [G, n or 2n, k / group]
+ *   zeros   uint8 [G, n or 2n, k / group], or NULL for z = 8
+ * k % 32 == 0 and k % group == 0; x_dtype 0 or 1.
+ */
+int cq_expert_matmul_w4(const cq_expert_config* cfg, const void* x, const uint8_t* codes,
+                        const void* scales, const uint8_t* zeros, const int64_t* group_rows,
+                        void* y, void* stream);
+/* Pointers of the expert products (else CQ_ERR_ARG): 16-byte aligned, group_rows
+ * 8-byte. x, y, dy, pre and dx may be NULL when rows is 0. */
+
+/* The expert products take no workspace; their status word (CQ_ST_BAD_ROWS,
+ * CQ_ST_TIMEOUT) is one word per device. Synchronise `stream`, copy the word of
+ * the current device into *status and clear it. */
+int cq_read_expert_status(uint32_t* status, void* stream);
 
 /* Static description of an error code. */
 const char* cq_strerror(int code);
