@@ -11,8 +11,6 @@ namespace {
 
 __device__ uint32_t g_status;  // CQ_ST_* bits of the expert products on this device
 
-enum Op { kForward, kDx, kDw, kW4 };
-
 template <int T>
 __device__ __forceinline__ float load16(const void* p, size_t i) {
   const uint16_t v = static_cast<const uint16_t*>(p)[i];
@@ -231,6 +229,7 @@ int cq_expert_matmul(const cq_expert_config* cfg, const void* x, const uint8_t* 
   a.w_scales = w_scales;
   a.out = y;
   a.pre_out = pre;
+  if (cfg->x_dtype <= kF16) return launch_gemm(kForward, a, static_cast<cudaStream_t>(stream));
   return launch<kForward>(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -248,7 +247,7 @@ int cq_expert_matmul_dx(const cq_expert_config* cfg, const void* dy, const void*
   a.w = w;
   a.pre_in = pre;
   a.out = dx;
-  return launch<kDx>(a, static_cast<cudaStream_t>(stream));
+  return launch_gemm(kDx, a, static_cast<cudaStream_t>(stream));
 }
 
 int cq_expert_matmul_dw(const cq_expert_config* cfg, const void* dy, const void* x,
@@ -263,7 +262,7 @@ int cq_expert_matmul_dw(const cq_expert_config* cfg, const void* dy, const void*
   a.x = x;
   a.w = dy;
   a.out = dw;
-  return launch<kDw>(a, static_cast<cudaStream_t>(stream));
+  return launch_gemm(kDw, a, static_cast<cudaStream_t>(stream));
 }
 
 int cq_expert_matmul_w4(const cq_expert_config* cfg, const void* x, const uint8_t* codes,
@@ -296,7 +295,9 @@ int cq_read_expert_status(uint32_t* status, void* stream) {
           cudaSuccess ||
       cudaStreamSynchronize(s) != cudaSuccess)
     return CQ_ERR_CUDA;
-  *status = v;
+  const int rc = gemm_status(status, s);
+  if (rc != CQ_OK) return rc;
+  *status |= v;
   if (v && (cudaMemcpyToSymbolAsync(g_status, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s) !=
                 cudaSuccess ||
             cudaStreamSynchronize(s) != cudaSuccess))

@@ -1,0 +1,567 @@
+// cq_expert_gemm.cu -- grouped matrix products of the experts on the tensor
+// cores (tcgen05): forward, gradient of the input, gradient of the weights.
+//
+// One persistent kernel. An output tile is TILE_I x up to 256 elements of
+// out[j, i], i being the contiguous axis. The axis i lies on the accumulator's
+// 128 lanes (so a warp's store of one column is contiguous) and j on its
+// columns, whose number is free in steps of 16: the ragged axis of the forward
+// product and of the input's gradient, the tokens, is j, so an expert with 3
+// rows costs 16 columns, not a padded tile of 128.
+//
+//   forward  out = y,  i = weight rows, j = tokens, sum over k:  A = w (K-major),  B = x (K-major)
+//   dx       out = dx, i = weight cols, j = tokens, sum over n:  A = w (MN-major), B = dy (K-major)
+//   dw       out = dw, i = columns of x, j = columns of dy, sum over the expert's
+//            rows:  A = x (MN-major), B = dy (MN-major)
+//
+// Warp 0 fills a ring of shared-memory stages with tiled copies (64 of the
+// contraction, 128-byte swizzle), warp 1 issues the products into one of two
+// TMEM accumulators, warps 4-7 drain the other one. SwiGLU: the tile's weight
+// rows are 16 gate rows, 16 up rows, 16 gate rows, ... (one 5-D copy picks them
+// up in that order), so that a gate and its up product sit 16 lanes apart in
+// one warp. dw's last rows: those of the next expert that the copy brings in
+// are overwritten with zeros by warp 2 before the product reads them.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "cq_expert.cuh"
+#include "cq_tensor.cuh"
+
+namespace cq {
+namespace expert {
+namespace {
+
+using namespace tensor;
+using async::mbar_arrive_expect_tx;
+using async::mbar_init;
+using async::mbar_wait;
+
+__device__ uint32_t g_status;  // CQ_ST_* bits of these kernels on this device
+
+constexpr int kThreads = 256;
+constexpr int kNT = 256;                   // most columns (j) of a tile
+constexpr int kABytes = 128 * 128;         // A of one stage, one CTA
+constexpr uint32_t kTmemCols = 512;
+
+template <int CG>
+constexpr int kStageBytes = kABytes + kNT / CG * 128;
+template <int CG>
+constexpr int kStages = CG == 1 ? 4 : 6;
+
+struct Shape {
+  int I, J, KK;        // extents: out columns (physical A rows), dw: out rows, contraction
+  int n_out;           // forward: n
+  int tiles_i;         // tiles along i
+  int tiles_j;         // dw: tiles along j
+};
+
+struct Bars {
+  uint64_t full[8], empty[8], tail[8], tail_full[8];
+  uint64_t tfull[2], tempty[2];
+  uint32_t tmem;
+  uint32_t abort;
+};
+
+// A tile of the work list.
+struct Tile {
+  int e, begin, i0, j0, jn, nkb, kk;  // jn: real columns; kk: contraction length
+};
+
+template <Op OP, int CG>
+__device__ __forceinline__ Tile tile_at(const Shape& sh, const int* s_begin, const int* s_tile,
+                                        int G, int t) {
+  Tile x;
+  x.e = expert_of(s_tile, G, t);
+  const int l = t - s_tile[x.e];
+  const int ti = l % sh.tiles_i, tj = l / sh.tiles_i;
+  x.begin = s_begin[x.e];
+  const int rows = s_begin[x.e + 1] - x.begin;
+  x.i0 = ti * 128 * CG;
+  if (OP == kDw) {
+    x.kk = rows;
+    x.j0 = tj * kNT;
+    x.jn = min(kNT, sh.J - x.j0);
+  } else {
+    // equal parts, in steps of 32
+    const int parts = (rows + kNT - 1) / kNT;
+    const int step = ((rows + parts - 1) / parts + 31) / 32 * 32;
+    x.kk = sh.KK;
+    x.j0 = tj * step;
+    x.jn = min(step, rows - x.j0);
+  }
+  x.nkb = (x.kk + 63) / 64;
+  return x;
+}
+
+__device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + __expf(-g)); }
+
+// y = u * g / (1 + exp(-g)) in 32 bits.
+__device__ __forceinline__ float swiglu(float g, float u) {
+  return __fdividef(u * g, 1.f + __expf(-g));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack(float a, float b) { return T::pack2(a, b); }
+
+// The drained tile, column by column. acc[c] is this lane's row i of column c.
+// Pairs of lanes exchange so that each lane stores two neighbouring i of one
+// of two columns (4 bytes; a warp stores two runs of 64 bytes).
+template <Op OP, typename T, bool F32, bool ACT>
+__device__ __forceinline__ void store_chunk(const Args& a, const Shape& sh, const Tile& x,
+                                            int i_warp, int c0, uint32_t (&acc)[32]) {
+  const int lane = threadIdx.x & 31;
+  const bool odd = lane & 1;
+  const size_t row0 = OP == kDw ? (size_t)x.e * sh.J + x.j0 : (size_t)(x.begin + x.j0);
+  auto f = [&](int c) { return __uint_as_float(acc[c]); };
+  if constexpr (OP == kForward && ACT) {
+    // lanes 0-15 gates, 16-31 ups of outputs o0 .. o0 + 15
+    const int o0 = i_warp / 2;
+    const bool in = o0 < sh.n_out;
+    if (a.pre_out && in) {
+      uint16_t* pre = static_cast<uint16_t*>(a.pre_out);
+      const size_t col = (lane < 16 ? 0 : sh.n_out) + o0 + (lane & 14);
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        const float r = __shfl_xor_sync(~0u, odd ? f(c) : f(c + 1), 1);
+        const uint32_t v = odd ? pack<T>(r, f(c + 1)) : pack<T>(f(c), r);
+        const int j = c0 + c + odd;
+        if (j < x.jn)
+          *reinterpret_cast<uint32_t*>(pre + (row0 + j) * (2 * (size_t)sh.n_out) + col) = v;
+      }
+    }
+    uint16_t* out = static_cast<uint16_t*>(a.out);
+    const bool up = lane & 16;
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+      // lanes 0-15 take columns c and c + 2, lanes 16-31 c + 1 and c + 3
+      const float r0 = __shfl_xor_sync(~0u, up ? f(c) : f(c + 1), 16);
+      const float r1 = __shfl_xor_sync(~0u, up ? f(c + 2) : f(c + 3), 16);
+      const float h0 = up ? swiglu(r0, f(c + 1)) : swiglu(f(c), r0);
+      const float h1 = up ? swiglu(r1, f(c + 3)) : swiglu(f(c + 2), r1);
+      const float r = __shfl_xor_sync(~0u, odd ? h0 : h1, 1);
+      const uint32_t v = odd ? pack<T>(r, h1) : pack<T>(h0, r);
+      const int j = c0 + c + (up ? 1 : 0) + (odd ? 2 : 0);
+      if (in && j < x.jn)
+        *reinterpret_cast<uint32_t*>(out + (row0 + j) * (size_t)sh.n_out + o0 + (lane & 14)) = v;
+    }
+  } else if constexpr (OP == kDx && ACT) {
+    const int i = i_warp + (lane & 30);
+    const bool in = i < sh.I;
+    const uint16_t* pre = static_cast<const uint16_t*>(a.pre_in);
+    uint16_t* out = static_cast<uint16_t*>(a.out);
+    const size_t ld = 2 * (size_t)sh.I;
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+      uint32_t g[8], u[8];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        const int j = c0 + h + 2 * p + odd;
+        const bool ok = in && j < x.jn;
+        const uint16_t* at = pre + (row0 + j) * ld + i;
+        g[p] = ok ? __ldg(reinterpret_cast<const uint32_t*>(at)) : 0u;
+        u[p] = ok ? __ldg(reinterpret_cast<const uint32_t*>(at + sh.I)) : 0u;
+      }
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        const int c = h + 2 * p;
+        const float r = __shfl_xor_sync(~0u, odd ? f(c) : f(c + 1), 1);
+        const float d0 = odd ? r : f(c), d1 = odd ? f(c + 1) : r;
+        const float g0 = T::lo(g[p]), g1 = T::hi(g[p]), u0 = T::lo(u[p]), u1 = T::hi(u[p]);
+        const float s0 = sigmoid(g0), s1 = sigmoid(g1);
+        const int j = c0 + c + odd;
+        if (in && j < x.jn) {
+          uint16_t* at = out + (row0 + j) * ld + i;
+          *reinterpret_cast<uint32_t*>(at) =
+              pack<T>(d0 * u0 * (s0 + g0 * s0 * (1.f - s0)), d1 * u1 * (s1 + g1 * s1 * (1.f - s1)));
+          *reinterpret_cast<uint32_t*>(at + sh.I) = pack<T>(d0 * g0 * s0, d1 * g1 * s1);
+        }
+      }
+    }
+  } else if constexpr (F32) {
+    const int i = i_warp + lane;
+    float* out = static_cast<float*>(a.out);
+    if (i < sh.I)
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        if (c0 + c < x.jn) out[(row0 + c0 + c) * (size_t)sh.I + i] = f(c);
+  } else {
+    const int i = i_warp + (lane & 30);
+    uint16_t* out = static_cast<uint16_t*>(a.out);
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      const float r = __shfl_xor_sync(~0u, odd ? f(c) : f(c + 1), 1);
+      const uint32_t v = odd ? pack<T>(r, f(c + 1)) : pack<T>(f(c), r);
+      const int j = c0 + c + odd;
+      if (i < sh.I && j < x.jn)
+        *reinterpret_cast<uint32_t*>(out + (row0 + j) * (size_t)sh.I + i) = v;
+    }
+  }
+}
+
+template <Op OP, typename T, bool F32, bool ACT, int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
+            const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b) {
+  constexpr int S = kStages<CG>;
+  constexpr int SB = kStageBytes<CG>;
+  constexpr bool A_MN = OP != kForward, B_MN = OP == kDw;
+  extern __shared__ __align__(1024) uint8_t dyn[];
+  __shared__ Bars bars;
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+  int* s_begin = reinterpret_cast<int*>(ring + S * SB);
+  int* s_tile = s_begin + a.G + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+  if (threadIdx.x == 0) {
+    prefetch_map(&map_a);
+    prefetch_map(&map_b);
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&bars.full[s], 1);
+      mbar_init(&bars.empty[s], 1);
+      mbar_init(&bars.tail[s], 1);
+      mbar_init(&bars.tail_full[s], CG);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars.tfull[b], 1);
+      mbar_init(&bars.tempty[b], 4 * CG);
+    }
+    bars.abort = 0;
+    async::mbar_fence_init();
+  }
+  if (warp == 1) tmem_alloc<CG>(&bars.tmem, kTmemCols);
+  griddep_wait();
+  const bool bad = group_scan<kThreads>(a, s_begin, s_tile, [&](int rows) {
+    return OP == kDw ? sh.tiles_i * sh.tiles_j : sh.tiles_i * ((rows + kNT - 1) / kNT);
+  });
+  if (bad && blockIdx.x == 0) atomicOr(&g_status, (uint32_t)CQ_ST_BAD_ROWS);
+  if constexpr (CG == 2) {
+    fence_before();
+    cluster_sync();
+  } else {
+    fence_before();
+    __syncthreads();
+  }
+  fence_after();
+  const uint32_t tmem = bars.tmem;
+  const int n_tiles = s_tile[a.G];
+  const int first = blockIdx.x / CG, step = gridDim.x / CG;
+  volatile uint32_t* const aborted = &bars.abort;
+  auto wait = [&](uint64_t* bar, uint32_t parity, int rounds) {
+    for (int r = 0; r < rounds; ++r)
+      if (mbar_wait(bar, parity)) return true;
+    *aborted = 1;
+    atomicOr(&g_status, (uint32_t)CQ_ST_TIMEOUT);
+    return false;
+  };
+  auto lead = [&](uint64_t* bar) { return CG == 2 ? leader_addr(smem_u32(bar)) : smem_u32(bar); };
+
+  // Columns of B that this CTA loads for a tile: its half of jn, in copies of
+  // 32 rows (K-major) or 64 columns (MN-major).
+  auto half_cols = [&](const Tile& x) { return ((x.jn + 31) / 32 * 32) / CG; };
+
+  if (warp == 0 && lane == 0) {
+    // ---- copies ----
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = first; t < n_tiles && ok; t += step) {
+      const Tile x = tile_at<OP, CG>(sh, s_begin, s_tile, a.G, t);
+      const int i_cta = x.i0 + (int)rank * 128;
+      const int jh = half_cols(x), jb = x.j0 + (int)rank * jh;
+      constexpr int kBox = B_MN ? 64 : 32;
+      const int nbox = (jh + kBox - 1) / kBox;
+      const uint32_t bytes = kABytes + nbox * (B_MN ? 8192 : 4096);
+      for (int kb = 0; kb < x.nkb; ++kb, ++it) {
+        const int s = it % S;
+        if (it >= (uint32_t)S && !(ok = wait(&bars.empty[s], ((it / S) & 1) ^ 1, 1))) break;
+        const uint32_t sa = smem_u32(ring + s * SB), sb = sa + kABytes;
+        const bool tail = OP == kDw && kb == x.nkb - 1 && (x.kk & 15) != 0;
+        uint32_t bar;
+        if (tail) {
+          // zeros go in before the product may read: each CTA's copies complete
+          // on its own barrier, warp 2 takes it from there
+          bar = smem_u32(&bars.tail[s]);
+          mbar_arrive_expect_tx(&bars.tail[s], bytes);
+          if (rank == 0) async::mbar_arrive(&bars.full[s]);
+        } else {
+          bar = lead(&bars.full[s]);
+          if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], bytes * CG);
+        }
+        const int k0 = kb * 64;
+        if constexpr (OP == kForward && ACT) {
+          tma_load5<CG>(sa, &map_a, k0, 0, 0, i_cta / 32, x.e, bar);
+        } else if constexpr (OP == kForward) {
+          tma_load3<CG>(sa, &map_a, k0, i_cta, x.e, bar);
+        } else if constexpr (OP == kDx) {
+          tma_load3<CG>(sa, &map_a, i_cta, k0, x.e, bar);
+          tma_load3<CG>(sa + 8192, &map_a, i_cta + 64, k0, x.e, bar);
+        } else {
+          tma_load2<CG>(sa, &map_a, i_cta, x.begin + k0, bar);
+          tma_load2<CG>(sa + 8192, &map_a, i_cta + 64, x.begin + k0, bar);
+        }
+        for (int b = 0; b < nbox; ++b) {
+          if constexpr (B_MN)
+            tma_load2<CG>(sb + b * 8192, &map_b, jb + b * 64, x.begin + k0, bar);
+          else
+            tma_load2<CG>(sb + b * 4096, &map_b, k0, x.begin + jb + b * 32, bar);
+        }
+      }
+    }
+    if (ok) {
+      // the last uses of every stage: nothing may arrive here after the CTA has gone
+      for (uint32_t u = it < (uint32_t)S ? 0 : it - S; u < it && ok; ++u)
+        ok = wait(&bars.empty[u % S], (u / S) & 1, 1);
+    } else {
+      // gave up: let the copies in flight land (with a limit) before the CTA goes
+      for (uint32_t u = it < (uint32_t)S ? 0 : it - S; u < it; ++u) {
+        if (rank == 0) mbar_wait(&bars.full[u % S], (u / S) & 1);
+      }
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ---- products ----
+    const uint64_t da = desc_base(A_MN ? 8192 : 16), db = desc_base(B_MN ? 8192 : 16);
+    constexpr uint32_t ka = A_MN ? 2048 : 32, kb_step = B_MN ? 2048 : 32;
+    uint32_t it = 0, buf = 0, tail_uses[S] = {};
+    bool ok = true;
+    for (int t = first; t < n_tiles && ok; t += step) {
+      const Tile x = tile_at<OP, CG>(sh, s_begin, s_tile, a.G, t);
+      if (x.nkb == 0) continue;
+      const uint32_t b = buf & 1, use = buf >> 1;
+      ++buf;
+      if (use > 0 && !(ok = wait(&bars.tempty[b], (use - 1) & 1, 1))) break;
+      fence_after();
+      const uint32_t d = tmem + b * kNT;
+      const uint32_t idesc = idesc_f16(T::kBf16, A_MN, B_MN, 128 * CG, half_cols(x) * CG);
+      for (int kb = 0; kb < x.nkb; ++kb, ++it) {
+        const int s = it % S;
+        if (!(ok = wait(&bars.full[s], (it / S) & 1, 1))) break;
+        if (OP == kDw && kb == x.nkb - 1 && (x.kk & 15) != 0) {
+          uint32_t use_t = 0;
+#pragma unroll
+          for (int q = 0; q < S; ++q)
+            if (q == s) use_t = tail_uses[q]++;
+          if (!(ok = wait(&bars.tail_full[s], use_t & 1, 1))) break;
+        }
+        fence_after();
+        const uint32_t sa = smem_u32(ring + s * SB), sb = sa + kABytes;
+        const int steps = min(4, (x.kk - kb * 64 + 15) / 16);
+        for (int q = 0; q < steps; ++q)
+          mma_f16<CG>(d, desc_at(da, sa + q * ka), desc_at(db, sb + q * kb_step), idesc,
+                      kb > 0 || q > 0);
+        commit<CG>(smem_u32(&bars.empty[s]));
+      }
+      if (ok) commit<CG>(smem_u32(&bars.tfull[b]));
+    }
+  } else if (OP == kDw && warp == 2) {
+    // ---- zeros over the rows past an expert's last (up to the next 16) ----
+    uint32_t it = 0, tail_uses[S] = {};
+    bool ok = true;
+    for (int t = first; t < n_tiles && ok; t += step) {
+      const Tile x = tile_at<OP, CG>(sh, s_begin, s_tile, a.G, t);
+      it += x.nkb;
+      if (x.nkb == 0 || (x.kk & 15) == 0) continue;
+      const int s = (it - 1) % S;
+      uint32_t use_t = 0;
+#pragma unroll
+      for (int q = 0; q < S; ++q)
+        if (q == s) use_t = tail_uses[q]++;
+      if (!(ok = wait(&bars.tail[s], use_t & 1, 8))) break;
+      const int r0 = (x.kk - 1) % 64 + 1, r1 = (r0 + 15) / 16 * 16;
+      const int blocks = 2 + (half_cols(x) + 63) / 64;
+      uint8_t* base = ring + s * SB;
+      for (int v = lane; v < blocks * (r1 - r0) * 8; v += 32) {
+        const int blk = v / ((r1 - r0) * 8), r = r0 + v / 8 % (r1 - r0);
+        *reinterpret_cast<uint4*>(base + blk * 8192 + r * 128 + (v & 7) * 16) = make_uint4(0, 0, 0, 0);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2) arrive_cluster(leader_addr(smem_u32(&bars.tail_full[s])));
+        else async::mbar_arrive(&bars.tail_full[s]);
+      }
+    }
+  } else if (warp >= 4) {
+    // ---- results ----
+    const int q = warp - 4;
+    uint32_t buf = 0;
+    bool ok = true;
+    for (int t = first; t < n_tiles && ok; t += step) {
+      const Tile x = tile_at<OP, CG>(sh, s_begin, s_tile, a.G, t);
+      const int i_warp = x.i0 + (int)rank * 128 + q * 32;
+      if (x.nkb == 0) {
+        uint32_t zero[32] = {};
+        for (int c0 = 0; c0 < x.jn; c0 += 32)
+          store_chunk<OP, T, F32, ACT>(a, sh, x, i_warp, c0, zero);
+        continue;
+      }
+      const uint32_t b = buf & 1, use = buf >> 1;
+      ++buf;
+      if (!(ok = wait(&bars.tfull[b], use & 1, 2 + x.nkb / 65536))) break;
+      fence_after();
+      const uint32_t src = tmem + b * kNT + ((uint32_t)(q * 32) << 16);
+      for (int c0 = 0; c0 < x.jn; c0 += 32) {
+        uint32_t acc[32];
+        tmem_ld32(src + c0, acc);
+        store_chunk<OP, T, F32, ACT>(a, sh, x, i_warp, c0, acc);
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2) arrive_cluster(leader_addr(smem_u32(&bars.tempty[b])));
+        else async::mbar_arrive(&bars.tempty[b]);
+      }
+    }
+  }
+  __syncwarp();
+  fence_before();
+  if constexpr (CG == 2) cluster_sync();
+  else __syncthreads();
+  fence_after();
+  if (warp == 1) tmem_free<CG>(tmem, kTmemCols);
+}
+
+// ---- host ----
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static std::atomic<EncodeFn> cached;
+  EncodeFn f = cached.load(std::memory_order_relaxed);
+  if (f) return f;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult r;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) !=
+          cudaSuccess ||
+      r != cudaDriverEntryPointSuccess)
+    return nullptr;
+  f = reinterpret_cast<EncodeFn>(p);
+  cached.store(f, std::memory_order_relaxed);
+  return f;
+}
+
+// A tensor map of 16-bit elements; dims and box innermost first, strides of
+// dims 1.. in elements. The inner box is always 64 elements (128 bytes).
+bool make_map(CUtensorMap* m, const void* p, bool bf16, int nd, const uint64_t* dims,
+              const uint64_t* strides, const uint32_t* box) {
+  const EncodeFn f = encode_fn();
+  if (!f) return false;
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], es[5];
+  for (int i = 0; i < nd; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    es[i] = 1;
+    if (i > 0) st[i - 1] = strides[i - 1] * 2;
+  }
+  return f(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, nd,
+           const_cast<void*>(p), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <Op OP, typename T, bool F32, bool ACT, int CG>
+cudaError_t launch_t(const Args& a, const Shape& sh, const CUtensorMap& ma, const CUtensorMap& mb,
+                     cudaStream_t s) {
+  constexpr auto kernel = gemm_kernel<OP, T, F32, ACT, CG>;
+  const size_t smem = 1024 + (size_t)kStages<CG> * kStageBytes<CG> + 8 * ((size_t)a.G + 1);
+  cudaError_t e = prepare_kernel<kernel>(smem);
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorUnknown;
+  const int64_t most = OP == kDw ? (int64_t)a.G * sh.tiles_i * sh.tiles_j
+                                 : (int64_t)sh.tiles_i * (a.R / kNT + std::min(a.G, a.R));
+  const int clusters = (int)std::min<int64_t>(sms / CG, most);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(clusters * CG);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {CG, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, sh, ma, mb);
+}
+
+template <typename T, int CG>
+cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
+  const bool bf16 = T::kBf16;
+  const uint64_t G = a.G, R = a.R, N = a.N, K = a.K;
+  const int TI = 128 * CG;
+  CUtensorMap ma, mb;
+  Shape sh = {};
+  if (op == kForward) {
+    sh.n_out = a.act ? a.N / 2 : a.N;
+    sh.I = a.N;
+    sh.KK = a.K;
+    sh.tiles_i = (a.N + TI - 1) / TI;
+    const uint64_t db[] = {K, R}, sb[] = {K};
+    const uint32_t bb[] = {64, 32};
+    if (!make_map(&mb, a.x, bf16, 2, db, sb, bb)) return cudaErrorUnknown;
+    if (a.act) {
+      const uint64_t n = N / 2, d[] = {K, 16, 2, n / 16, G}, st[] = {K, n * K, 16 * K, N * K};
+      const uint32_t b[] = {64, 16, 2, 4, 1};
+      if (!make_map(&ma, a.w, bf16, 5, d, st, b)) return cudaErrorUnknown;
+      return launch_t<kForward, T, false, true, CG>(a, sh, ma, mb, s);
+    }
+    const uint64_t d[] = {K, N, G}, st[] = {K, N * K};
+    const uint32_t b[] = {64, 128, 1};
+    if (!make_map(&ma, a.w, bf16, 3, d, st, b)) return cudaErrorUnknown;
+    return launch_t<kForward, T, false, false, CG>(a, sh, ma, mb, s);
+  }
+  sh.I = a.K;
+  sh.tiles_i = (a.K + TI - 1) / TI;
+  if (op == kDx) {
+    sh.KK = a.N;
+    const uint64_t d[] = {K, N, G}, st[] = {K, N * K}, db[] = {N, R}, sb[] = {N};
+    const uint32_t b[] = {64, 64, 1}, bb[] = {64, 32};
+    if (!make_map(&ma, a.w, bf16, 3, d, st, b) || !make_map(&mb, a.x, bf16, 2, db, sb, bb))
+      return cudaErrorUnknown;
+    return a.pre_in ? launch_t<kDx, T, false, true, CG>(a, sh, ma, mb, s)
+                    : launch_t<kDx, T, false, false, CG>(a, sh, ma, mb, s);
+  }
+  sh.J = a.N;
+  sh.tiles_j = (a.N + kNT - 1) / kNT;
+  const uint64_t d[] = {K, R}, st[] = {K}, db[] = {N, R}, sb[] = {N};
+  const uint32_t b[] = {64, 64};
+  if (!make_map(&ma, a.x, bf16, 2, d, st, b) || !make_map(&mb, a.w, bf16, 2, db, sb, b))
+    return cudaErrorUnknown;
+  return a.out_dtype == 2 ? launch_t<kDw, T, true, false, CG>(a, sh, ma, mb, s)
+                          : launch_t<kDw, T, false, false, CG>(a, sh, ma, mb, s);
+}
+
+}  // namespace
+
+int launch_gemm(Op op, const Args& a, cudaStream_t s) {
+  cudaError_t e;
+  if (a.R == 0) {
+    if (op != kDw) return CQ_OK;
+    e = cudaMemsetAsync(a.out, 0, (size_t)a.G * a.N * a.K * (a.out_dtype == 2 ? 4 : 2), s);
+  } else {
+    e = a.x_dtype == kF16 ? launch_op<F16, 1>(op, a, s) : launch_op<BF16, 1>(op, a, s);
+  }
+  return e == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
+}
+
+int gemm_status(uint32_t* status, cudaStream_t s) {
+  uint32_t v = 0;
+  const uint32_t zero = 0;
+  if (cudaMemcpyFromSymbolAsync(&v, g_status, sizeof v, 0, cudaMemcpyDeviceToHost, s) !=
+          cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return CQ_ERR_CUDA;
+  *status = v;
+  if (v && (cudaMemcpyToSymbolAsync(g_status, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s) !=
+                cudaSuccess ||
+            cudaStreamSynchronize(s) != cudaSuccess))
+    return CQ_ERR_CUDA;
+  return CQ_OK;
+}
+
+}  // namespace expert
+}  // namespace cq

@@ -140,6 +140,7 @@ struct CombineArgs {
 // The two 16-bit token types. In a packed 32-bit word element 2t is the low
 // half. Conversions to fp32 are exact; pack2 rounds to nearest even.
 struct BF16 {
+  static constexpr bool kBf16 = true;
   static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
   static __device__ __forceinline__ float hi(uint32_t w) {
     return __uint_as_float(w & 0xffff0000u);
@@ -150,6 +151,7 @@ struct BF16 {
   }
 };
 struct F16 {
+  static constexpr bool kBf16 = false;
   static __device__ __forceinline__ float lo(uint32_t w) {
     return __half2float(__ushort_as_half((unsigned short)(w & 0xffffu)));
   }
