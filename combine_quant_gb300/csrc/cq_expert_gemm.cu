@@ -38,15 +38,17 @@ using async::mbar_wait;
 
 __device__ uint32_t g_status;  // CQ_ST_* bits of these kernels on this device
 
-constexpr int kThreads = 256;
+constexpr int kDrainWarps = 8;             // two for each quarter of the lanes
+constexpr int kThreads = 128 + 32 * kDrainWarps;
 constexpr int kNT = 256;                   // most columns (j) of a tile
 constexpr int kABytes = 128 * 128;         // A of one stage, one CTA
 constexpr uint32_t kTmemCols = 512;
 
 template <int CG>
 constexpr int kStageBytes = kABytes + kNT / CG * 128;
-template <int CG>
-constexpr int kStages = CG == 1 ? 4 : 6;
+// Stages of the ring: what is left beside the results' staging and the lists.
+template <Op OP, bool ACT, int CG>
+constexpr int kStages = CG == 1 ? 4 : OP == kDx && ACT ? 5 : 6;
 
 struct Shape {
   int I, J, KK;        // extents: out columns (physical A rows), dw: out rows, contraction
@@ -59,7 +61,6 @@ struct Bars {
   uint64_t full[8], empty[8], tail[8], tail_full[8];
   uint64_t tfull[2], tempty[2];
   uint32_t tmem;
-  uint32_t abort;
 };
 
 // A tile of the work list.
@@ -93,6 +94,28 @@ __device__ __forceinline__ Tile tile_at(const Shape& sh, const int* s_begin, con
   return x;
 }
 
+// Wait for a phase that the pair's other CTA takes part in (cluster scope).
+__device__ __forceinline__ bool try_pair(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity) {
+  const uint32_t b = smem_u32(bar);
+  if (try_pair(b, parity)) return true;
+  const uint64_t t0 = async::globaltimer_ns();
+  for (uint32_t polls = 0; polls < async::kWaitMaxPolls; ++polls) {
+    if (try_pair(b, parity)) return true;
+    if (async::globaltimer_ns() - t0 > async::kWaitLimitNs) return false;
+  }
+  return false;
+}
+
 __device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + __expf(-g)); }
 
 // y = u * g / (1 + exp(-g)) in 32 bits.
@@ -100,115 +123,153 @@ __device__ __forceinline__ float swiglu(float g, float u) {
   return __fdividef(u * g, 1.f + __expf(-g));
 }
 
-template <typename T>
-__device__ __forceinline__ uint32_t pack(float a, float b) { return T::pack2(a, b); }
+// Bytes of one results warp's staging buffer: 32 columns (j) of its 32 lanes
+// (i) in 16 bits, or in 32 where another factor still comes (rows of 36 floats,
+// so that neither the columns' stores nor the rows' loads meet in a bank).
+template <Op OP, bool ACT>
+constexpr int kStagingBytes = OP == kDx && ACT ? 32 * 36 * 4 : 32 * 64;
 
-// The drained tile, column by column. acc[c] is this lane's row i of column c.
-// Pairs of lanes exchange so that each lane stores two neighbouring i of one
-// of two columns (4 bytes; a warp stores two runs of 64 bytes).
+// Drains columns [c0, c0 + 32) of a tile: out[j][i .. i + 31] of 32 j. The
+// accumulator holds i on lanes and j on columns, memory wants i contiguous, so
+// the block is turned in shared memory (16-byte pieces of a 64-byte row, XORed
+// with bits of the row number: no bank conflicts either way) and written in
+// 16-byte stores, 64 bytes a row.
 template <Op OP, typename T, bool F32, bool ACT>
-__device__ __forceinline__ void store_chunk(const Args& a, const Shape& sh, const Tile& x,
-                                            int i_warp, int c0, uint32_t (&acc)[32]) {
+__device__ __forceinline__ void drain(const Args& a, const Shape& sh, const Tile& x, int i_warp,
+                                      int c0, uint32_t src, uint8_t* stage) {
   const int lane = threadIdx.x & 31;
-  const bool odd = lane & 1;
-  const size_t row0 = OP == kDw ? (size_t)x.e * sh.J + x.j0 : (size_t)(x.begin + x.j0);
-  auto f = [&](int c) { return __uint_as_float(acc[c]); };
-  if constexpr (OP == kForward && ACT) {
-    // lanes 0-15 gates, 16-31 ups of outputs o0 .. o0 + 15
-    const int o0 = i_warp / 2;
-    const bool in = o0 < sh.n_out;
-    if (a.pre_out && in) {
-      uint16_t* pre = static_cast<uint16_t*>(a.pre_out);
-      const size_t col = (lane < 16 ? 0 : sh.n_out) + o0 + (lane & 14);
-#pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        const float r = __shfl_xor_sync(~0u, odd ? f(c) : f(c + 1), 1);
-        const uint32_t v = odd ? pack<T>(r, f(c + 1)) : pack<T>(f(c), r);
-        const int j = c0 + c + odd;
-        if (j < x.jn)
-          *reinterpret_cast<uint32_t*>(pre + (row0 + j) * (2 * (size_t)sh.n_out) + col) = v;
-      }
-    }
-    uint16_t* out = static_cast<uint16_t*>(a.out);
-    const bool up = lane & 16;
-#pragma unroll
-    for (int c = 0; c < 32; c += 4) {
-      // lanes 0-15 take columns c and c + 2, lanes 16-31 c + 1 and c + 3
-      const float r0 = __shfl_xor_sync(~0u, up ? f(c) : f(c + 1), 16);
-      const float r1 = __shfl_xor_sync(~0u, up ? f(c + 2) : f(c + 3), 16);
-      const float h0 = up ? swiglu(r0, f(c + 1)) : swiglu(f(c), r0);
-      const float h1 = up ? swiglu(r1, f(c + 3)) : swiglu(f(c + 2), r1);
-      const float r = __shfl_xor_sync(~0u, odd ? h0 : h1, 1);
-      const uint32_t v = odd ? pack<T>(r, h1) : pack<T>(h0, r);
-      const int j = c0 + c + (up ? 1 : 0) + (odd ? 2 : 0);
-      if (in && j < x.jn)
-        *reinterpret_cast<uint32_t*>(out + (row0 + j) * (size_t)sh.n_out + o0 + (lane & 14)) = v;
-    }
-  } else if constexpr (OP == kDx && ACT) {
-    const int i = i_warp + (lane & 30);
-    const bool in = i < sh.I;
-    const uint16_t* pre = static_cast<const uint16_t*>(a.pre_in);
-    uint16_t* out = static_cast<uint16_t*>(a.out);
-    const size_t ld = 2 * (size_t)sh.I;
-#pragma unroll
-    for (int h = 0; h < 32; h += 16) {
-      uint32_t g[8], u[8];
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        const int j = c0 + h + 2 * p + odd;
-        const bool ok = in && j < x.jn;
-        const uint16_t* at = pre + (row0 + j) * ld + i;
-        g[p] = ok ? __ldg(reinterpret_cast<const uint32_t*>(at)) : 0u;
-        u[p] = ok ? __ldg(reinterpret_cast<const uint32_t*>(at + sh.I)) : 0u;
-      }
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        const int c = h + 2 * p;
-        const float r = __shfl_xor_sync(~0u, odd ? f(c) : f(c + 1), 1);
-        const float d0 = odd ? r : f(c), d1 = odd ? f(c + 1) : r;
-        const float g0 = T::lo(g[p]), g1 = T::hi(g[p]), u0 = T::lo(u[p]), u1 = T::hi(u[p]);
-        const float s0 = sigmoid(g0), s1 = sigmoid(g1);
-        const int j = c0 + c + odd;
-        if (in && j < x.jn) {
-          uint16_t* at = out + (row0 + j) * ld + i;
-          *reinterpret_cast<uint32_t*>(at) =
-              pack<T>(d0 * u0 * (s0 + g0 * s0 * (1.f - s0)), d1 * u1 * (s1 + g1 * s1 * (1.f - s1)));
-          *reinterpret_cast<uint32_t*>(at + sh.I) = pack<T>(d0 * g0 * s0, d1 * g1 * s1);
-        }
-      }
-    }
-  } else if constexpr (F32) {
+  const int jn = x.jn - c0;  // columns that exist
+  const size_t row0 = (OP == kDw ? (size_t)x.e * sh.J + x.j0 : (size_t)(x.begin + x.j0)) + c0;
+  const uint32_t st = smem_u32(stage);
+  if constexpr (F32) {
+    uint32_t acc[32];
+    tmem_ld32(src + c0, acc);
+    tmem_wait();
     const int i = i_warp + lane;
-    float* out = static_cast<float*>(a.out);
+    float* out = static_cast<float*>(a.out) + row0 * sh.I + i;
     if (i < sh.I)
 #pragma unroll
       for (int c = 0; c < 32; ++c)
-        if (c0 + c < x.jn) out[(row0 + c0 + c) * (size_t)sh.I + i] = f(c);
-  } else {
-    const int i = i_warp + (lane & 30);
-    uint16_t* out = static_cast<uint16_t*>(a.out);
+        if (c < jn) out[(size_t)c * sh.I] = __uint_as_float(acc[c]);
+  } else if constexpr (OP == kDx && ACT) {
+    const int r = lane >> 2, i = i_warp + 8 * (lane & 3);
+    const size_t ld = 2 * (size_t)sh.I, first = (row0 + r) * ld + i;
+    const uint16_t* pre = static_cast<const uint16_t*>(a.pre_in) + first;
+    uint16_t* out = static_cast<uint16_t*>(a.out) + first;
+    uint4 g[4], u[4];
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      const float r = __shfl_xor_sync(~0u, odd ? f(c) : f(c + 1), 1);
-      const uint32_t v = odd ? pack<T>(r, f(c + 1)) : pack<T>(f(c), r);
-      const int j = c0 + c + odd;
-      if (i < sh.I && j < x.jn)
-        *reinterpret_cast<uint32_t*>(out + (row0 + j) * (size_t)sh.I + i) = v;
+    for (int p = 0; p < 4; ++p) {
+      const bool ok = i < sh.I && 8 * p + r < jn;
+      g[p] = ok ? __ldg(reinterpret_cast<const uint4*>(pre + 8 * p * ld)) : make_uint4(0, 0, 0, 0);
+      u[p] = ok ? __ldg(reinterpret_cast<const uint4*>(pre + 8 * p * ld + sh.I)) : make_uint4(0, 0, 0, 0);
+    }
+    float* buf = reinterpret_cast<float*>(stage);
+    {
+      uint32_t acc[32];
+      tmem_ld32(src + c0, acc);
+      tmem_wait();
+#pragma unroll
+      for (int c = 0; c < 32; ++c) buf[c * 36 + lane] = __uint_as_float(acc[c]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const float4* at = reinterpret_cast<const float4*>(buf + (8 * p + r) * 36 + 8 * (lane & 3));
+      const float4 d0 = at[0], d1 = at[1];
+      const float d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+      const uint32_t gw[4] = {g[p].x, g[p].y, g[p].z, g[p].w}, uw[4] = {u[p].x, u[p].y, u[p].z, u[p].w};
+      uint32_t dg[4], du[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const float g0 = T::lo(gw[h]), g1 = T::hi(gw[h]), u0 = T::lo(uw[h]), u1 = T::hi(uw[h]);
+        const float s0 = sigmoid(g0), s1 = sigmoid(g1);
+        dg[h] = T::pack2(d[2 * h] * u0 * (s0 + g0 * s0 * (1.f - s0)),
+                         d[2 * h + 1] * u1 * (s1 + g1 * s1 * (1.f - s1)));
+        du[h] = T::pack2(d[2 * h] * g0 * s0, d[2 * h + 1] * g1 * s1);
+      }
+      if (i < sh.I && 8 * p + r < jn) {
+        *reinterpret_cast<uint4*>(out + 8 * p * ld) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
+        *reinterpret_cast<uint4*>(out + 8 * p * ld + sh.I) = make_uint4(du[0], du[1], du[2], du[3]);
+      }
+    }
+    __syncwarp();
+  } else {
+    uint32_t v0[16], v1[16];  // lanes 0-15 and 16-31 (SwiGLU: gates and ups of 16 outputs)
+    tmem_ld16(src + c0, v0);
+    tmem_ld16(src + c0 + (16u << 16), v1);
+    tmem_wait();
+    auto f = [](uint32_t w) { return __uint_as_float(w); };
+    constexpr bool kAct = OP == kForward && ACT;
+    const int r = lane >> 2, c = lane & 3;
+    if (!kAct || a.pre_out) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int j = 8 * n + (lane & 7);
+        st_matrix_t(st + j * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4),
+                    T::pack2(f(v0[4 * n]), f(v0[4 * n + 1])), T::pack2(f(v0[4 * n + 2]), f(v0[4 * n + 3])),
+                    T::pack2(f(v1[4 * n]), f(v1[4 * n + 1])), T::pack2(f(v1[4 * n + 2]), f(v1[4 * n + 3])));
+      }
+      __syncwarp();
+      const size_t ld = kAct ? 2 * (size_t)sh.n_out : (size_t)sh.I;
+      // SwiGLU: the first two pieces are gates, the others ups
+      const int i = kAct ? i_warp / 2 + 8 * (c & 1) + (c & 2 ? sh.n_out : 0) : i_warp + 8 * c;
+      const bool in = kAct ? i_warp / 2 < sh.n_out : i < sh.I;
+      uint16_t* out = static_cast<uint16_t*>(kAct ? a.pre_out : a.out) + (row0 + r) * ld + i;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const int j = 8 * p + r;
+        const uint4 w = async::ld_shared_v4(stage + j * 64 + ((c ^ ((j >> 1) & 3)) << 4));
+        if (in && j < jn) *reinterpret_cast<uint4*>(out + 8 * p * ld) = w;
+      }
+      __syncwarp();
+    }
+    if constexpr (kAct) {
+#pragma unroll
+      for (int n = 0; n < 16; ++n) v0[n] = __float_as_uint(swiglu(f(v0[n]), f(v1[n])));
+#pragma unroll
+      for (int n = 0; n < 4; n += 2) {
+        // rows of 32 bytes: block 0, 1 = outputs 0-7, 8-15 of columns 8 n.., 2, 3 of 8 (n + 1)..
+        const int j = 8 * (n + (lane >> 4)) + (lane & 7);
+        st_matrix_t(st + j * 32 + ((((lane >> 3) & 1) ^ ((j >> 2) & 1)) << 4),
+                    T::pack2(f(v0[4 * n]), f(v0[4 * n + 1])), T::pack2(f(v0[4 * n + 2]), f(v0[4 * n + 3])),
+                    T::pack2(f(v0[4 * n + 4]), f(v0[4 * n + 5])), T::pack2(f(v0[4 * n + 6]), f(v0[4 * n + 7])));
+      }
+      __syncwarp();
+      const int r2 = lane >> 1, c2 = lane & 1, o = i_warp / 2;
+      uint16_t* out = static_cast<uint16_t*>(a.out) + (row0 + r2) * (size_t)sh.n_out + o + 8 * c2;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int j = 16 * p + r2;
+        const uint4 w = async::ld_shared_v4(stage + j * 32 + ((c2 ^ ((j >> 2) & 1)) << 4));
+        if (o < sh.n_out && j < jn) *reinterpret_cast<uint4*>(out + 16 * p * (size_t)sh.n_out) = w;
+      }
+      __syncwarp();
     }
   }
+}
+
+// Zeros for a tile of an expert without rows (dw).
+template <bool F32>
+__device__ __forceinline__ void store_zeros(const Args& a, const Shape& sh, const Tile& x, int i0) {
+  const int per = F32 ? 4 : 8, size = F32 ? 4 : 2;  // elements per 16 bytes, bytes per element
+  const int cols = min(128, sh.I - i0) / per;
+  char* out = static_cast<char*>(a.out) + (((size_t)x.e * sh.J + x.j0) * sh.I + i0) * size;
+  for (int v = threadIdx.x - 128; v < x.jn * cols; v += kDrainWarps * 32)
+    *reinterpret_cast<uint4*>(out + ((size_t)(v / cols) * sh.I + v % cols * per) * size) = make_uint4(0, 0, 0, 0);
 }
 
 template <Op OP, typename T, bool F32, bool ACT, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
             const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b) {
-  constexpr int S = kStages<CG>;
+  constexpr int S = kStages<OP, ACT, CG>;
   constexpr int SB = kStageBytes<CG>;
   constexpr bool A_MN = OP != kForward, B_MN = OP == kDw;
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Bars bars;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
-  int* s_begin = reinterpret_cast<int*>(ring + S * SB);
+  uint8_t* staging = ring + S * SB;
+  int* s_begin = reinterpret_cast<int*>(staging + kDrainWarps * kStagingBytes<OP, ACT>);
   int* s_tile = s_begin + a.G + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -224,9 +285,8 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars.tfull[b], 1);
-      mbar_init(&bars.tempty[b], 4 * CG);
+      mbar_init(&bars.tempty[b], kDrainWarps * CG);
     }
-    bars.abort = 0;
     async::mbar_fence_init();
   }
   if (warp == 1) tmem_alloc<CG>(&bars.tmem, kTmemCols);
@@ -246,11 +306,9 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
   const uint32_t tmem = bars.tmem;
   const int n_tiles = s_tile[a.G];
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
-  volatile uint32_t* const aborted = &bars.abort;
   auto wait = [&](uint64_t* bar, uint32_t parity, int rounds) {
     for (int r = 0; r < rounds; ++r)
-      if (mbar_wait(bar, parity)) return true;
-    *aborted = 1;
+      if (CG == 2 ? wait_pair(bar, parity) : mbar_wait(bar, parity)) return true;
     atomicOr(&g_status, (uint32_t)CQ_ST_TIMEOUT);
     return false;
   };
@@ -382,16 +440,15 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     }
   } else if (warp >= 4) {
     // ---- results ----
-    const int q = warp - 4;
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    uint8_t* stage = staging + (warp - 4) * kStagingBytes<OP, ACT>;
     uint32_t buf = 0;
     bool ok = true;
     for (int t = first; t < n_tiles && ok; t += step) {
       const Tile x = tile_at<OP, CG>(sh, s_begin, s_tile, a.G, t);
-      const int i_warp = x.i0 + (int)rank * 128 + q * 32;
+      const int i_cta = x.i0 + (int)rank * 128;
       if (x.nkb == 0) {
-        uint32_t zero[32] = {};
-        for (int c0 = 0; c0 < x.jn; c0 += 32)
-          store_chunk<OP, T, F32, ACT>(a, sh, x, i_warp, c0, zero);
+        if (i_cta < sh.I) store_zeros<F32>(a, sh, x, i_cta);
         continue;
       }
       const uint32_t b = buf & 1, use = buf >> 1;
@@ -399,11 +456,8 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       if (!(ok = wait(&bars.tfull[b], use & 1, 2 + x.nkb / 65536))) break;
       fence_after();
       const uint32_t src = tmem + b * kNT + ((uint32_t)(q * 32) << 16);
-      for (int c0 = 0; c0 < x.jn; c0 += 32) {
-        uint32_t acc[32];
-        tmem_ld32(src + c0, acc);
-        store_chunk<OP, T, F32, ACT>(a, sh, x, i_warp, c0, acc);
-      }
+      for (int c0 = 32 * half; c0 < x.jn; c0 += 64)
+        drain<OP, T, F32, ACT>(a, sh, x, i_cta + 32 * q, c0, src, stage);
       fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -465,7 +519,8 @@ template <Op OP, typename T, bool F32, bool ACT, int CG>
 cudaError_t launch_t(const Args& a, const Shape& sh, const CUtensorMap& ma, const CUtensorMap& mb,
                      cudaStream_t s) {
   constexpr auto kernel = gemm_kernel<OP, T, F32, ACT, CG>;
-  const size_t smem = 1024 + (size_t)kStages<CG> * kStageBytes<CG> + 8 * ((size_t)a.G + 1);
+  const size_t smem = 1024 + (size_t)kStages<OP, ACT, CG> * kStageBytes<CG> +
+                      kDrainWarps * kStagingBytes<OP, ACT> + 8 * ((size_t)a.G + 1);
   cudaError_t e = prepare_kernel<kernel>(smem);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
@@ -543,7 +598,7 @@ int launch_gemm(Op op, const Args& a, cudaStream_t s) {
     if (op != kDw) return CQ_OK;
     e = cudaMemsetAsync(a.out, 0, (size_t)a.G * a.N * a.K * (a.out_dtype == 2 ? 4 : 2), s);
   } else {
-    e = a.x_dtype == kF16 ? launch_op<F16, 1>(op, a, s) : launch_op<BF16, 1>(op, a, s);
+    e = a.x_dtype == kF16 ? launch_op<F16, 2>(op, a, s) : launch_op<BF16, 2>(op, a, s);
   }
   return e == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
 }
