@@ -43,6 +43,7 @@ constexpr int kThreads = 128 + 32 * kDrainWarps;
 constexpr int kNT = 256;                   // most columns (j) of a tile
 constexpr int kABytes = 128 * 128;         // A of one stage, one CTA
 constexpr uint32_t kTmemCols = 512;
+constexpr int kBand = 8;                   // tiles along i taken together, for reuse in L2
 
 template <int CG>
 constexpr int kStageBytes = kABytes + kNT / CG * 128;
@@ -74,9 +75,12 @@ __device__ __forceinline__ Tile tile_at(const Shape& sh, const int* s_begin, con
   Tile x;
   x.e = expert_of(s_tile, G, t);
   const int l = t - s_tile[x.e];
-  const int ti = l % sh.tiles_i, tj = l / sh.tiles_i;
   x.begin = s_begin[x.e];
   const int rows = s_begin[x.e + 1] - x.begin;
+  const int nj = OP == kDw ? sh.tiles_j : (rows + kNT - 1) / kNT;
+  const int band = l / (kBand * nj), first_i = band * kBand;
+  const int wide = min(kBand, sh.tiles_i - first_i), m = l - first_i * nj;
+  const int ti = first_i + m % wide, tj = m / wide;
   x.i0 = ti * 128 * CG;
   if (OP == kDw) {
     x.kk = rows;
@@ -306,9 +310,9 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
   const uint32_t tmem = bars.tmem;
   const int n_tiles = s_tile[a.G];
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
-  auto wait = [&](uint64_t* bar, uint32_t parity, int rounds) {
+  auto wait = [&](uint64_t* bar, uint32_t parity, int rounds, bool pair = false) {
     for (int r = 0; r < rounds; ++r)
-      if (CG == 2 ? wait_pair(bar, parity) : mbar_wait(bar, parity)) return true;
+      if (CG == 2 && pair ? wait_pair(bar, parity) : mbar_wait(bar, parity)) return true;
     atomicOr(&g_status, (uint32_t)CQ_ST_TIMEOUT);
     return false;
   };
@@ -318,97 +322,108 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
   // 32 rows (K-major) or 64 columns (MN-major).
   auto half_cols = [&](const Tile& x) { return ((x.jn + 31) / 32 * 32) / CG; };
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ---- copies ----
-    uint32_t it = 0;
+    uint32_t s = 0, lap = 0;  // stage, times the ring has gone round
     bool ok = true;
     for (int t = first; t < n_tiles && ok; t += step) {
       const Tile x = tile_at<OP, CG>(sh, s_begin, s_tile, a.G, t);
       const int i_cta = x.i0 + (int)rank * 128;
       const int jh = half_cols(x), jb = x.j0 + (int)rank * jh;
-      constexpr int kBox = B_MN ? 64 : 32;
+      constexpr int kBox = B_MN ? 64 : 128;
       const int nbox = (jh + kBox - 1) / kBox;
-      const uint32_t bytes = kABytes + nbox * (B_MN ? 8192 : 4096);
-      for (int kb = 0; kb < x.nkb; ++kb, ++it) {
-        const int s = it % S;
-        if (it >= (uint32_t)S && !(ok = wait(&bars.empty[s], ((it / S) & 1) ^ 1, 1))) break;
-        const uint32_t sa = smem_u32(ring + s * SB), sb = sa + kABytes;
-        const bool tail = OP == kDw && kb == x.nkb - 1 && (x.kk & 15) != 0;
-        uint32_t bar;
-        if (tail) {
-          // zeros go in before the product may read: each CTA's copies complete
-          // on its own barrier, warp 2 takes it from there
-          bar = smem_u32(&bars.tail[s]);
-          mbar_arrive_expect_tx(&bars.tail[s], bytes);
-          if (rank == 0) async::mbar_arrive(&bars.full[s]);
-        } else {
-          bar = lead(&bars.full[s]);
-          if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], bytes * CG);
+      const uint32_t bytes = kABytes + nbox * (kBox * 128);
+      for (int kb = 0; kb < x.nkb; ++kb) {
+        if (lap > 0 && !(ok = wait(&bars.empty[s], (lap & 1) ^ 1, 1))) break;
+        if (elect_one()) {
+          const uint32_t sa = smem_u32(ring + s * SB), sb = sa + kABytes;
+          const bool tail = OP == kDw && kb == x.nkb - 1 && (x.kk & 15) != 0;
+          uint32_t bar;
+          if (tail) {
+            // zeros go in before the product may read: each CTA's copies complete
+            // on its own barrier, warp 2 takes it from there
+            bar = smem_u32(&bars.tail[s]);
+            mbar_arrive_expect_tx(&bars.tail[s], bytes);
+            if (rank == 0) async::mbar_arrive(&bars.full[s]);
+          } else {
+            bar = lead(&bars.full[s]);
+            if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], bytes * CG);
+          }
+          const int k0 = kb * 64;
+          if constexpr (OP == kForward && ACT) {
+            tma_load5<CG>(sa, &map_a, k0, 0, 0, i_cta / 32, x.e, bar);
+          } else if constexpr (OP == kForward) {
+            tma_load3<CG>(sa, &map_a, k0, i_cta, x.e, bar);
+          } else if constexpr (OP == kDx) {
+            tma_load3<CG>(sa, &map_a, i_cta, k0, x.e, bar);
+            tma_load3<CG>(sa + 8192, &map_a, i_cta + 64, k0, x.e, bar);
+          } else {
+            tma_load2<CG>(sa, &map_a, i_cta, x.begin + k0, bar);
+            tma_load2<CG>(sa + 8192, &map_a, i_cta + 64, x.begin + k0, bar);
+          }
+          for (int b = 0; b < nbox; ++b) {
+            if constexpr (B_MN)
+              tma_load2<CG>(sb + b * 8192, &map_b, jb + b * 64, x.begin + k0, bar);
+            else
+              tma_load2<CG>(sb + b * 16384, &map_b, k0, x.begin + jb + b * 128, bar);
+          }
         }
-        const int k0 = kb * 64;
-        if constexpr (OP == kForward && ACT) {
-          tma_load5<CG>(sa, &map_a, k0, 0, 0, i_cta / 32, x.e, bar);
-        } else if constexpr (OP == kForward) {
-          tma_load3<CG>(sa, &map_a, k0, i_cta, x.e, bar);
-        } else if constexpr (OP == kDx) {
-          tma_load3<CG>(sa, &map_a, i_cta, k0, x.e, bar);
-          tma_load3<CG>(sa + 8192, &map_a, i_cta + 64, k0, x.e, bar);
-        } else {
-          tma_load2<CG>(sa, &map_a, i_cta, x.begin + k0, bar);
-          tma_load2<CG>(sa + 8192, &map_a, i_cta + 64, x.begin + k0, bar);
-        }
-        for (int b = 0; b < nbox; ++b) {
-          if constexpr (B_MN)
-            tma_load2<CG>(sb + b * 8192, &map_b, jb + b * 64, x.begin + k0, bar);
-          else
-            tma_load2<CG>(sb + b * 4096, &map_b, k0, x.begin + jb + b * 32, bar);
-        }
+        __syncwarp();
+        if (++s == S) s = 0, ++lap;
       }
     }
-    if (ok) {
-      // the last uses of every stage: nothing may arrive here after the CTA has gone
-      for (uint32_t u = it < (uint32_t)S ? 0 : it - S; u < it && ok; ++u)
-        ok = wait(&bars.empty[u % S], (u / S) & 1, 1);
-    } else {
-      // gave up: let the copies in flight land (with a limit) before the CTA goes
-      for (uint32_t u = it < (uint32_t)S ? 0 : it - S; u < it; ++u) {
-        if (rank == 0) mbar_wait(&bars.full[u % S], (u / S) & 1);
-      }
+    // The last use of every stage, oldest first. Done: nothing may arrive here
+    // after the CTA has gone. Gave up: let the copies in flight land (with a
+    // limit) before it goes.
+    for (int v = 0; v < S; ++v) {
+      const uint32_t u = (s + v) % S, laps = lap + (u < s ? 1 : 0);  // uses of stage u
+      if (laps == 0) continue;
+      if (ok) ok = wait(&bars.empty[u], (laps - 1) & 1, 1);
+      else if (rank == 0) mbar_wait(&bars.full[u], (laps - 1) & 1);
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // ---- products ----
-    const uint64_t da = desc_base(A_MN ? 8192 : 16), db = desc_base(B_MN ? 8192 : 16);
-    constexpr uint32_t ka = A_MN ? 2048 : 32, kb_step = B_MN ? 2048 : 32;
-    uint32_t it = 0, buf = 0, tail_uses[S] = {};
+    constexpr uint32_t ka = (A_MN ? 2048 : 32) >> 4, kbs = (B_MN ? 2048 : 32) >> 4;
+    const uint64_t da = desc_at(desc_base(A_MN ? 8192 : 16), smem_u32(ring));
+    const uint64_t db = desc_at(desc_base(B_MN ? 8192 : 16), smem_u32(ring) + kABytes);
+    uint32_t s = 0, lap = 0, buf = 0, tail_uses[S] = {};
     bool ok = true;
     for (int t = first; t < n_tiles && ok; t += step) {
       const Tile x = tile_at<OP, CG>(sh, s_begin, s_tile, a.G, t);
       if (x.nkb == 0) continue;
       const uint32_t b = buf & 1, use = buf >> 1;
       ++buf;
-      if (use > 0 && !(ok = wait(&bars.tempty[b], (use - 1) & 1, 1))) break;
-      fence_after();
+      if (use > 0 && !(ok = wait(&bars.tempty[b], (use - 1) & 1, 1, true))) break;
       const uint32_t d = tmem + b * kNT;
       const uint32_t idesc = idesc_f16(T::kBf16, A_MN, B_MN, 128 * CG, half_cols(x) * CG);
-      for (int kb = 0; kb < x.nkb; ++kb, ++it) {
-        const int s = it % S;
-        if (!(ok = wait(&bars.full[s], (it / S) & 1, 1))) break;
+      for (int kb = 0; kb < x.nkb; ++kb) {
+        if (!(ok = wait(&bars.full[s], lap & 1, 1))) break;
         if (OP == kDw && kb == x.nkb - 1 && (x.kk & 15) != 0) {
           uint32_t use_t = 0;
 #pragma unroll
           for (int q = 0; q < S; ++q)
             if (q == s) use_t = tail_uses[q]++;
-          if (!(ok = wait(&bars.tail_full[s], use_t & 1, 1))) break;
+          if (!(ok = wait(&bars.tail_full[s], use_t & 1, 1, true))) break;
         }
         fence_after();
-        const uint32_t sa = smem_u32(ring + s * SB), sb = sa + kABytes;
-        const int steps = min(4, (x.kk - kb * 64 + 15) / 16);
-        for (int q = 0; q < steps; ++q)
-          mma_f16<CG>(d, desc_at(da, sa + q * ka), desc_at(db, sb + q * kb_step), idesc,
-                      kb > 0 || q > 0);
-        commit<CG>(smem_u32(&bars.empty[s]));
+        if (elect_one()) {
+          const uint64_t ad = da + s * (SB >> 4), bd = db + s * (SB >> 4);
+          const int left = x.kk - kb * 64;
+          if (left > 48) {
+            mma_f16<CG>(d, ad, bd, idesc, kb > 0);
+            mma_f16<CG>(d, ad + ka, bd + kbs, idesc, true);
+            mma_f16<CG>(d, ad + 2 * ka, bd + 2 * kbs, idesc, true);
+            mma_f16<CG>(d, ad + 3 * ka, bd + 3 * kbs, idesc, true);
+          } else {
+            for (int q = 0; 16 * q < left; ++q)
+              mma_f16<CG>(d, ad + q * ka, bd + q * kbs, idesc, kb > 0 || q > 0);
+          }
+          commit<CG>(smem_u32(&bars.empty[s]));
+          if (kb == x.nkb - 1) commit<CG>(smem_u32(&bars.tfull[b]));
+        }
+        __syncwarp();
+        if (++s == S) s = 0, ++lap;
       }
-      if (ok) commit<CG>(smem_u32(&bars.tfull[b]));
     }
   } else if (OP == kDw && warp == 2) {
     // ---- zeros over the rows past an expert's last (up to the next 16) ----
@@ -556,7 +571,7 @@ cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
     sh.KK = a.K;
     sh.tiles_i = (a.N + TI - 1) / TI;
     const uint64_t db[] = {K, R}, sb[] = {K};
-    const uint32_t bb[] = {64, 32};
+    const uint32_t bb[] = {64, 128};
     if (!make_map(&mb, a.x, bf16, 2, db, sb, bb)) return cudaErrorUnknown;
     if (a.act) {
       const uint64_t n = N / 2, d[] = {K, 16, 2, n / 16, G}, st[] = {K, n * K, 16 * K, N * K};
@@ -574,7 +589,7 @@ cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
   if (op == kDx) {
     sh.KK = a.N;
     const uint64_t d[] = {K, N, G}, st[] = {K, N * K}, db[] = {N, R}, sb[] = {N};
-    const uint32_t b[] = {64, 64, 1}, bb[] = {64, 32};
+    const uint32_t b[] = {64, 64, 1}, bb[] = {64, 128};
     if (!make_map(&ma, a.w, bf16, 3, d, st, b) || !make_map(&mb, a.x, bf16, 2, db, sb, bb))
       return cudaErrorUnknown;
     return a.pre_in ? launch_t<kDx, T, false, true, CG>(a, sh, ma, mb, s)

@@ -19,6 +19,13 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 // Shared-memory address of the pair's CTA 0 (the leader) for one of this CTA.
 __device__ __forceinline__ uint32_t leader_addr(uint32_t a) {
   uint32_t r;
