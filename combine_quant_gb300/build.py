@@ -23,7 +23,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcq.so")
 SOURCES = ["cq_api.cu", "cq_route.cu", "cq_permute_bf16.cu", "cq_permute_f16.cu", "cq_dispatch_small.cu",
            "cq_combine.cu", "cq_noalloc.cu", "cq_expert.cu",
-           "cq_expert_gemm.cu"]
+           "cq_expert_gemm.cu", "cq_expert_w4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -283,26 +283,18 @@ int cq_expert_matmul_w4(const cq_expert_config* cfg, const void* x, const uint8_
   a.scales4 = scales;
   a.zeros4 = zeros;
   a.out = y;
-  return launch<kW4>(a, static_cast<cudaStream_t>(stream));
+  return launch_w4(a, static_cast<cudaStream_t>(stream));
 }
 
 int cq_read_expert_status(uint32_t* status, void* stream) {
   if (!status) return CQ_ERR_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  uint32_t v = 0;
-  const uint32_t zero = 0;
-  if (cudaMemcpyFromSymbolAsync(&v, g_status, sizeof v, 0, cudaMemcpyDeviceToHost, s) !=
-          cudaSuccess ||
-      cudaStreamSynchronize(s) != cudaSuccess)
-    return CQ_ERR_CUDA;
-  const int rc = gemm_status(status, s);
-  if (rc != CQ_OK) return rc;
-  *status |= v;
-  if (v && (cudaMemcpyToSymbolAsync(g_status, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s) !=
-                cudaSuccess ||
-            cudaStreamSynchronize(s) != cudaSuccess))
-    return CQ_ERR_CUDA;
-  return CQ_OK;
+  uint32_t v[3] = {};
+  int rc = read_status_word(g_status, &v[0], s);
+  if (rc == CQ_OK) rc = gemm_status(&v[1], s);
+  if (rc == CQ_OK) rc = w4_status(&v[2], s);
+  if (rc == CQ_OK) *status = v[0] | v[1] | v[2];
+  return rc;
 }
 
 }  // extern "C"

@@ -111,9 +111,27 @@ __device__ __forceinline__ int expert_of(const int* tile, int G, int t) {
   return lo;
 }
 
+// Reads and clears a translation unit's status word, waiting for the stream.
+template <typename Word>
+int read_status_word(Word& word, uint32_t* status, cudaStream_t s) {
+  uint32_t v = 0;
+  const uint32_t zero = 0;
+  if (cudaMemcpyFromSymbolAsync(&v, word, sizeof v, 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return CQ_ERR_CUDA;
+  *status = v;
+  if (v &&
+      (cudaMemcpyToSymbolAsync(word, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+       cudaStreamSynchronize(s) != cudaSuccess))
+    return CQ_ERR_CUDA;
+  return CQ_OK;
+}
+
 // Launchers, and the status words of their kernels (read and cleared).
 int launch_gemm(Op op, const Args& a, cudaStream_t s);
+int launch_w4(const Args& a, cudaStream_t s);
 int gemm_status(uint32_t* status, cudaStream_t s);
+int w4_status(uint32_t* status, cudaStream_t s);
 
 }  // namespace expert
 }  // namespace cq

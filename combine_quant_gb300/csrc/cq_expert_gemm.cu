@@ -490,46 +490,6 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
 }
 
 // ---- host ----
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                              CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-  static std::atomic<EncodeFn> cached;
-  EncodeFn f = cached.load(std::memory_order_relaxed);
-  if (f) return f;
-  void* p = nullptr;
-  cudaDriverEntryPointQueryResult r;
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) !=
-          cudaSuccess ||
-      r != cudaDriverEntryPointSuccess)
-    return nullptr;
-  f = reinterpret_cast<EncodeFn>(p);
-  cached.store(f, std::memory_order_relaxed);
-  return f;
-}
-
-// A tensor map of 16-bit elements; dims and box innermost first, strides of
-// dims 1.. in elements. The inner box is always 64 elements (128 bytes).
-bool make_map(CUtensorMap* m, const void* p, bool bf16, int nd, const uint64_t* dims,
-              const uint64_t* strides, const uint32_t* box) {
-  const EncodeFn f = encode_fn();
-  if (!f) return false;
-  cuuint64_t d[5], st[4];
-  cuuint32_t b[5], es[5];
-  for (int i = 0; i < nd; ++i) {
-    d[i] = dims[i];
-    b[i] = box[i];
-    es[i] = 1;
-    if (i > 0) st[i - 1] = strides[i - 1] * 2;
-  }
-  return f(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, nd,
-           const_cast<void*>(p), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <Op OP, typename T, bool F32, bool ACT, int CG>
 cudaError_t launch_t(const Args& a, const Shape& sh, const CUtensorMap& ma, const CUtensorMap& mb,
                      cudaStream_t s) {
@@ -560,7 +520,7 @@ cudaError_t launch_t(const Args& a, const Shape& sh, const CUtensorMap& ma, cons
 
 template <typename T, int CG>
 cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
-  const bool bf16 = T::kBf16;
+  const MapType type = T::kBf16 ? kMapBF16 : kMapF16;
   const uint64_t G = a.G, R = a.R, N = a.N, K = a.K;
   const int TI = 128 * CG;
   CUtensorMap ma, mb;
@@ -570,36 +530,36 @@ cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
     sh.I = a.N;
     sh.KK = a.K;
     sh.tiles_i = (a.N + TI - 1) / TI;
-    const uint64_t db[] = {K, R}, sb[] = {K};
+    const uint64_t db[] = {K, R}, sb[] = {2 * K};
     const uint32_t bb[] = {64, 128};
-    if (!make_map(&mb, a.x, bf16, 2, db, sb, bb)) return cudaErrorUnknown;
+    if (!make_map(&mb, a.x, type, 2, db, sb, bb)) return cudaErrorUnknown;
     if (a.act) {
-      const uint64_t n = N / 2, d[] = {K, 16, 2, n / 16, G}, st[] = {K, n * K, 16 * K, N * K};
+      const uint64_t n = N / 2, d[] = {K, 16, 2, n / 16, G}, st[] = {2 * K, 2 * n * K, 32 * K, 2 * N * K};
       const uint32_t b[] = {64, 16, 2, 4, 1};
-      if (!make_map(&ma, a.w, bf16, 5, d, st, b)) return cudaErrorUnknown;
+      if (!make_map(&ma, a.w, type, 5, d, st, b)) return cudaErrorUnknown;
       return launch_t<kForward, T, false, true, CG>(a, sh, ma, mb, s);
     }
-    const uint64_t d[] = {K, N, G}, st[] = {K, N * K};
+    const uint64_t d[] = {K, N, G}, st[] = {2 * K, 2 * N * K};
     const uint32_t b[] = {64, 128, 1};
-    if (!make_map(&ma, a.w, bf16, 3, d, st, b)) return cudaErrorUnknown;
+    if (!make_map(&ma, a.w, type, 3, d, st, b)) return cudaErrorUnknown;
     return launch_t<kForward, T, false, false, CG>(a, sh, ma, mb, s);
   }
   sh.I = a.K;
   sh.tiles_i = (a.K + TI - 1) / TI;
   if (op == kDx) {
     sh.KK = a.N;
-    const uint64_t d[] = {K, N, G}, st[] = {K, N * K}, db[] = {N, R}, sb[] = {N};
+    const uint64_t d[] = {K, N, G}, st[] = {2 * K, 2 * N * K}, db[] = {N, R}, sb[] = {2 * N};
     const uint32_t b[] = {64, 64, 1}, bb[] = {64, 128};
-    if (!make_map(&ma, a.w, bf16, 3, d, st, b) || !make_map(&mb, a.x, bf16, 2, db, sb, bb))
+    if (!make_map(&ma, a.w, type, 3, d, st, b) || !make_map(&mb, a.x, type, 2, db, sb, bb))
       return cudaErrorUnknown;
     return a.pre_in ? launch_t<kDx, T, false, true, CG>(a, sh, ma, mb, s)
                     : launch_t<kDx, T, false, false, CG>(a, sh, ma, mb, s);
   }
   sh.J = a.N;
   sh.tiles_j = (a.N + kNT - 1) / kNT;
-  const uint64_t d[] = {K, R}, st[] = {K}, db[] = {N, R}, sb[] = {N};
+  const uint64_t d[] = {K, R}, st[] = {2 * K}, db[] = {N, R}, sb[] = {2 * N};
   const uint32_t b[] = {64, 64};
-  if (!make_map(&ma, a.x, bf16, 2, d, st, b) || !make_map(&mb, a.w, bf16, 2, db, sb, b))
+  if (!make_map(&ma, a.x, type, 2, d, st, b) || !make_map(&mb, a.w, type, 2, db, sb, b))
     return cudaErrorUnknown;
   return a.out_dtype == 2 ? launch_t<kDw, T, true, false, CG>(a, sh, ma, mb, s)
                           : launch_t<kDw, T, false, false, CG>(a, sh, ma, mb, s);
@@ -618,20 +578,7 @@ int launch_gemm(Op op, const Args& a, cudaStream_t s) {
   return e == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
 }
 
-int gemm_status(uint32_t* status, cudaStream_t s) {
-  uint32_t v = 0;
-  const uint32_t zero = 0;
-  if (cudaMemcpyFromSymbolAsync(&v, g_status, sizeof v, 0, cudaMemcpyDeviceToHost, s) !=
-          cudaSuccess ||
-      cudaStreamSynchronize(s) != cudaSuccess)
-    return CQ_ERR_CUDA;
-  *status = v;
-  if (v && (cudaMemcpyToSymbolAsync(g_status, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s) !=
-                cudaSuccess ||
-            cudaStreamSynchronize(s) != cudaSuccess))
-    return CQ_ERR_CUDA;
-  return CQ_OK;
-}
+int gemm_status(uint32_t* status, cudaStream_t s) { return read_status_word(g_status, status, s); }
 
 }  // namespace expert
 }  // namespace cq

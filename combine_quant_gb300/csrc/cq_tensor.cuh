@@ -5,6 +5,9 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
 
 #include "cq_async.cuh"
 
@@ -215,6 +218,54 @@ __device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t addr) {
 __device__ __forceinline__ uint32_t idesc_f16(bool bf16, bool a_mn, bool b_mn, int m, int n) {
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// ---- host: tensor maps ----
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+
+// The driver's encoder, found at run time (the library links no driver stub).
+inline EncodeFn encode_fn() {
+  static std::atomic<EncodeFn> cached;
+  EncodeFn f = cached.load(std::memory_order_relaxed);
+  if (f) return f;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult r;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) !=
+          cudaSuccess ||
+      r != cudaDriverEntryPointSuccess)
+    return nullptr;
+  f = reinterpret_cast<EncodeFn>(p);
+  cached.store(f, std::memory_order_relaxed);
+  return f;
+}
+
+enum MapType { kMapBF16, kMapF16, kMapU8 };
+enum MapSwizzle { kSwizzle128, kSwizzle64 };
+
+// Dims and box innermost first, in elements; strides of dims 1.. in bytes.
+// Elements outside the tensor read as zeros.
+inline bool make_map(CUtensorMap* m, const void* p, MapType type, int nd, const uint64_t* dims,
+                     const uint64_t* strides, const uint32_t* box, MapSwizzle swizzle = kSwizzle128) {
+  const EncodeFn f = encode_fn();
+  if (!f) return false;
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], es[5];
+  for (int i = 0; i < nd; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    es[i] = 1;
+    if (i > 0) st[i - 1] = strides[i - 1];
+  }
+  return f(m,
+           type == kMapBF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+           : type == kMapF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                             : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+           nd, const_cast<void*>(p), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           swizzle == kSwizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace tensor
