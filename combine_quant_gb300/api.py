@@ -145,6 +145,27 @@ def _c_expert_config(cfg: ExpertConfig) -> _lib.CqExpertConfig:
     return _lib.CqExpertConfig(**asdict(cfg))
 
 
+class _ExpertPlan:
+    """What the calls derive from an expert config, kept per distinct config."""
+
+    def __init__(self, cfg: ExpertConfig):
+        R, G, WN, K = cfg.rows, cfg.experts, cfg.weight_rows, cfg.k
+        self.struct = cfg.as_c()
+        self.ref = ctypes.byref(self.struct)
+        self.experts, self.act, self.mx = G, cfg.act, cfg.mx
+        self.dtype, self.result = cfg.in_dtype, cfg.result_dtype
+        self.x, self.w, self.y, self.dy = (R, K), (G, WN, K), (R, cfg.n), (R, WN)
+        self.pre_k = (R, 2 * K)  # SwiGLU's products when the input was its result
+        self.x_scales, self.w_scales = (R, cfg.scale_cols), (G, WN, cfg.scale_cols)
+        self.codes = (G, WN, K // 2)
+        self.groups = (G, WN, K // cfg.group if cfg.group > 0 else 0)
+
+
+@functools.lru_cache(maxsize=256)
+def _expert_plan(cfg: ExpertConfig) -> _ExpertPlan:
+    return _ExpertPlan(cfg)
+
+
 class DispatchResult(NamedTuple):
     expand_x: torch.Tensor          # [R_max, H] bf16 / int8 / uint8 (e4m3 bytes)
     dynamic_scales: Optional[torch.Tensor]  # f32 [R_max] or uint8 [R_max, SC]
@@ -455,18 +476,44 @@ def combine_q8(cfg: Config, codes: torch.Tensor, scales: torch.Tensor, assist_in
     return y
 
 
-def _expert_buffers(cfg: ExpertConfig, group_rows: torch.Tensor, *tensors) -> torch.device:
-    """Checks the counts and (tensor, name, dtype, shape) quadruples; returns
-    the device."""
-    dev = group_rows.device
-    _need(group_rows, "group_rows", torch.int64)
-    if group_rows.numel() != cfg.experts:
-        raise ValueError(f"group_rows must have {cfg.experts} entries, got {group_rows.numel()}")
-    for t, name, dtype, shape in tensors:
-        if t is None:
-            raise ValueError(f"{name} is required")
+def _arg(t, name, dtype, shape, dev: torch.device):
+    """The address of a tensor argument after _need's checks (which raise); None
+    for None. One pass over the common case: these calls may take only microseconds
+    on the GPU."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
         _need(t, name, dtype, shape, dev)
-    return dev
+    return t.data_ptr()
+
+
+def _required(t, name):
+    if t is None:
+        raise ValueError(f"{name} is required")
+
+
+def _group_rows(p: _ExpertPlan, group_rows: torch.Tensor) -> torch.device:
+    """Checks the counts; returns the device that the other tensors must be on."""
+    _need(group_rows, "group_rows", torch.int64)
+    if group_rows.numel() != p.experts:
+        raise ValueError(f"group_rows must have {p.experts} entries, got {group_rows.numel()}")
+    return group_rows.device
+
+
+# The handle of the current stream, without building a torch.cuda.Stream around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _expert_call(name: str, dev: torch.device, *args) -> None:
+    fn = getattr(_lib.load(), name)
+    if torch.cuda.current_device() == dev.index:  # the library looks up the current device
+        rc = fn(*args, _raw_stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev.index))
+    if rc != _lib.CQ_OK:
+        _lib.check(rc, name)
 
 
 def expert_matmul(cfg: ExpertConfig, x: torch.Tensor, w: torch.Tensor, group_rows: torch.Tensor,
@@ -477,25 +524,25 @@ def expert_matmul(cfg: ExpertConfig, x: torch.Tensor, w: torch.Tensor, group_row
     """Grouped matrix product over the experts' rows (cq_expert_matmul):
     y [rows, n], with act 1 SwiGLU of the gate and up products (`pre`
     [rows, 2n] receives them). `group_rows` is dispatch's expert_token_nums."""
-    R, G, WN, K = cfg.rows, cfg.experts, cfg.weight_rows, cfg.k
-    dev = _expert_buffers(cfg, group_rows, (x, "x", cfg.in_dtype, (R, K)),
-                          (w, "w", cfg.in_dtype, (G, WN, K)))
-    if cfg.mx:
-        _expert_buffers(cfg, group_rows, (x_scales, "x_scales", torch.uint8, (R, cfg.scale_cols)),
-                        (w_scales, "w_scales", torch.uint8, (G, WN, cfg.scale_cols)))
+    p = _expert_plan(cfg)
+    dev = _group_rows(p, group_rows)
+    _required(x, "x")
+    _required(w, "w")
+    px, pw = _arg(x, "x", p.dtype, p.x, dev), _arg(w, "w", p.dtype, p.w, dev)
+    pxs = pws = None
+    if p.mx:
+        _required(x_scales, "x_scales")
+        _required(w_scales, "w_scales")
+        pxs = _arg(x_scales, "x_scales", torch.uint8, p.x_scales, dev)
+        pws = _arg(w_scales, "w_scales", torch.uint8, p.w_scales, dev)
     elif x_scales is not None or w_scales is not None:
         raise ValueError("x_scales and w_scales go with mx types only")
     if y is None:
-        y = torch.empty(R, cfg.n, dtype=cfg.result_dtype, device=dev)
-    _need(y, "y", cfg.result_dtype, (R, cfg.n), dev)
-    if pre is not None and cfg.act != 1:
+        y = torch.empty(p.y, dtype=p.result, device=dev)
+    if pre is not None and p.act != 1:
         raise ValueError("pre goes with act 1 only")
-    _need(pre, "pre", cfg.result_dtype, (R, WN), dev)
-    with torch.cuda.device(dev):  # the library looks up the current device
-        rc = _lib.load().cq_expert_matmul(ctypes.byref(cfg.as_c()), _ptr(x), _ptr(x_scales), _ptr(w),
-                                          _ptr(w_scales), _ptr(group_rows), _ptr(y), _ptr(pre),
-                                          _stream(dev))
-    _lib.check(rc, "cq_expert_matmul")
+    _expert_call("cq_expert_matmul", dev, p.ref, px, pxs, pw, pws, group_rows.data_ptr(),
+                 _arg(y, "y", p.result, p.y, dev), _arg(pre, "pre", p.result, p.dy, dev))
     return y
 
 
@@ -504,18 +551,17 @@ def expert_matmul_dx(cfg: ExpertConfig, dy: torch.Tensor, w: torch.Tensor,
                      dx: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of expert_matmul's input (cq_expert_matmul_dx): [rows, k], or
     with `pre` [rows, 2k] (the input was SwiGLU of pre) the gradient of pre."""
-    R, G, WN, K = cfg.rows, cfg.experts, cfg.weight_rows, cfg.k
-    dev = _expert_buffers(cfg, group_rows, (dy, "dy", cfg.in_dtype, (R, WN)),
-                          (w, "w", cfg.in_dtype, (G, WN, K)))
-    _need(pre, "pre", cfg.in_dtype, (R, 2 * K), dev)
-    cols = K if pre is None else 2 * K
+    p = _expert_plan(cfg)
+    dev = _group_rows(p, group_rows)
+    _required(dy, "dy")
+    _required(w, "w")
+    pdy, pw = _arg(dy, "dy", p.dtype, p.dy, dev), _arg(w, "w", p.dtype, p.w, dev)
+    ppre = _arg(pre, "pre", p.dtype, p.pre_k, dev)
+    shape = p.x if pre is None else p.pre_k
     if dx is None:
-        dx = torch.empty(R, cols, dtype=cfg.in_dtype, device=dev)
-    _need(dx, "dx", cfg.in_dtype, (R, cols), dev)
-    with torch.cuda.device(dev):  # the library looks up the current device
-        rc = _lib.load().cq_expert_matmul_dx(ctypes.byref(cfg.as_c()), _ptr(dy), _ptr(w),
-                                             _ptr(group_rows), _ptr(pre), _ptr(dx), _stream(dev))
-    _lib.check(rc, "cq_expert_matmul_dx")
+        dx = torch.empty(shape, dtype=p.dtype, device=dev)
+    _expert_call("cq_expert_matmul_dx", dev, p.ref, pdy, pw, group_rows.data_ptr(), ppre,
+                 _arg(dx, "dx", p.dtype, shape, dev))
     return dx
 
 
@@ -523,16 +569,15 @@ def expert_matmul_dw(cfg: ExpertConfig, dy: torch.Tensor, x: torch.Tensor,
                      group_rows: torch.Tensor, dw: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of expert_matmul's weights (cq_expert_matmul_dw), in the
     config's out_dtype: the token type (default) or f32."""
-    R, G, WN, K = cfg.rows, cfg.experts, cfg.weight_rows, cfg.k
-    dev = _expert_buffers(cfg, group_rows, (dy, "dy", cfg.in_dtype, (R, WN)),
-                          (x, "x", cfg.in_dtype, (R, K)))
+    p = _expert_plan(cfg)
+    dev = _group_rows(p, group_rows)
+    _required(dy, "dy")
+    _required(x, "x")
+    pdy, px = _arg(dy, "dy", p.dtype, p.dy, dev), _arg(x, "x", p.dtype, p.x, dev)
     if dw is None:
-        dw = torch.empty(G, WN, K, dtype=cfg.result_dtype, device=dev)
-    _need(dw, "dw", cfg.result_dtype, (G, WN, K), dev)
-    with torch.cuda.device(dev):  # the library looks up the current device
-        rc = _lib.load().cq_expert_matmul_dw(ctypes.byref(cfg.as_c()), _ptr(dy), _ptr(x),
-                                             _ptr(group_rows), _ptr(dw), _stream(dev))
-    _lib.check(rc, "cq_expert_matmul_dw")
+        dw = torch.empty(p.w, dtype=p.result, device=dev)
+    _expert_call("cq_expert_matmul_dw", dev, p.ref, pdy, px, group_rows.data_ptr(),
+                 _arg(dw, "dw", p.result, p.w, dev))
     return dw
 
 
@@ -543,20 +588,19 @@ def expert_matmul_w4(cfg: ExpertConfig, x: torch.Tensor, codes: torch.Tensor,
     """expert_matmul with 4-bit weights (cq_expert_matmul_w4), for few rows per
     expert: codes uint8 [G, n or 2n, k/2], scales (and uint8 zeros)
     [G, n or 2n, k/group]."""
-    R, G, WN, K = cfg.rows, cfg.experts, cfg.weight_rows, cfg.k
-    cols = K // cfg.group if cfg.group > 0 else 0
-    dev = _expert_buffers(cfg, group_rows, (x, "x", cfg.in_dtype, (R, K)),
-                          (codes, "codes", torch.uint8, (G, WN, K // 2)),
-                          (scales, "scales", cfg.in_dtype, (G, WN, cols)))
-    _need(zeros, "zeros", torch.uint8, (G, WN, cols), dev)
+    p = _expert_plan(cfg)
+    dev = _group_rows(p, group_rows)
+    _required(x, "x")
+    _required(codes, "codes")
+    _required(scales, "scales")
+    px = _arg(x, "x", p.dtype, p.x, dev)
+    pc = _arg(codes, "codes", torch.uint8, p.codes, dev)
+    ps = _arg(scales, "scales", p.dtype, p.groups, dev)
+    pz = _arg(zeros, "zeros", torch.uint8, p.groups, dev)
     if y is None:
-        y = torch.empty(R, cfg.n, dtype=cfg.in_dtype, device=dev)
-    _need(y, "y", cfg.in_dtype, (R, cfg.n), dev)
-    with torch.cuda.device(dev):  # the library looks up the current device
-        rc = _lib.load().cq_expert_matmul_w4(ctypes.byref(cfg.as_c()), _ptr(x), _ptr(codes),
-                                             _ptr(scales), _ptr(zeros), _ptr(group_rows), _ptr(y),
-                                             _stream(dev))
-    _lib.check(rc, "cq_expert_matmul_w4")
+        y = torch.empty(p.y, dtype=p.dtype, device=dev)
+    _expert_call("cq_expert_matmul_w4", dev, p.ref, px, pc, ps, pz, group_rows.data_ptr(),
+                 _arg(y, "y", p.dtype, p.y, dev))
     return y
 
 

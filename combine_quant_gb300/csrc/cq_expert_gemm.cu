@@ -39,17 +39,26 @@ using async::mbar_wait;
 __device__ uint32_t g_status;  // CQ_ST_* bits of these kernels on this device
 
 constexpr int kDrainWarps = 8;             // two for each quarter of the lanes
-constexpr int kThreads = 128 + 32 * kDrainWarps;
-constexpr int kNT = 256;                   // most columns (j) of a tile
+constexpr int kScaleWarps = 4;             // mx: fetch the scales
+template <bool MX>
+constexpr int kThreads = 128 + 32 * kDrainWarps + (MX ? 32 * kScaleWarps : 0);
+// Most columns (j) of a tile. Two accumulators of 256 fill TMEM; mx needs 24
+// columns of it for two stages' scales.
+template <bool MX>
+constexpr int kNT = MX ? 240 : 256;
+template <bool MX>
+constexpr int kStepJ = MX ? 16 : 32;       // columns come in steps of
+constexpr int kScaleBytes = 3 * 512;       // mx: scales of a stage: 128 rows of A, 256 of B
 constexpr int kABytes = 128 * 128;         // A of one stage, one CTA
 constexpr uint32_t kTmemCols = 512;
 constexpr int kBand = 8;                   // tiles along i taken together, for reuse in L2
 
 template <int CG>
-constexpr int kStageBytes = kABytes + kNT / CG * 128;
-// Stages of the ring: what is left beside the results' staging and the lists.
-template <Op OP, bool ACT, int CG>
-constexpr int kStages = CG == 1 ? 4 : OP == kDx && ACT ? 5 : 6;
+constexpr int kStageBytes = kABytes + 256 / CG * 128;
+// Stages of the ring: what is left beside the results' staging, the scales and
+// the lists of 2048 experts.
+template <Op OP, bool ACT, bool MX, int CG>
+constexpr int kStages = CG == 1 ? 4 : (OP == kDx && ACT) || MX ? 5 : 6;
 
 struct Shape {
   int I, J, KK;        // extents: out columns (physical A rows), dw: out rows, contraction
@@ -59,7 +68,7 @@ struct Shape {
 };
 
 struct Bars {
-  uint64_t full[8], empty[8], tail[8], tail_full[8];
+  uint64_t full[8], empty[8], tail[8], tail_full[8];  // tail_full, mx: scales are there
   uint64_t tfull[2], tempty[2];
   uint32_t tmem;
 };
@@ -69,32 +78,33 @@ struct Tile {
   int e, begin, i0, j0, jn, nkb, kk;  // jn: real columns; kk: contraction length
 };
 
-template <Op OP, int CG>
+template <Op OP, bool MX, int CG>
 __device__ __forceinline__ Tile tile_at(const Shape& sh, const int* s_begin, const int* s_tile,
                                         int G, int t) {
+  constexpr int NT = kNT<MX>, SJ = kStepJ<MX>;
   Tile x;
   x.e = expert_of(s_tile, G, t);
   const int l = t - s_tile[x.e];
   x.begin = s_begin[x.e];
   const int rows = s_begin[x.e + 1] - x.begin;
-  const int nj = OP == kDw ? sh.tiles_j : (rows + kNT - 1) / kNT;
+  const int nj = OP == kDw ? sh.tiles_j : (rows + NT - 1) / NT;
   const int band = l / (kBand * nj), first_i = band * kBand;
   const int wide = min(kBand, sh.tiles_i - first_i), m = l - first_i * nj;
   const int ti = first_i + m % wide, tj = m / wide;
   x.i0 = ti * 128 * CG;
   if (OP == kDw) {
     x.kk = rows;
-    x.j0 = tj * kNT;
-    x.jn = min(kNT, sh.J - x.j0);
+    x.j0 = tj * NT;
+    x.jn = min(NT, sh.J - x.j0);
   } else {
-    // equal parts, in steps of 32
-    const int parts = (rows + kNT - 1) / kNT;
-    const int step = ((rows + parts - 1) / parts + 31) / 32 * 32;
+    // equal parts, in whole steps
+    const int parts = (rows + NT - 1) / NT;
+    const int step = ((rows + parts - 1) / parts + SJ - 1) / SJ * SJ;
     x.kk = sh.KK;
     x.j0 = tj * step;
     x.jn = min(step, rows - x.j0);
   }
-  x.nkb = (x.kk + 63) / 64;
+  x.nkb = (x.kk + (MX ? 127 : 63)) / (MX ? 128 : 64);
   return x;
 }
 
@@ -262,18 +272,20 @@ __device__ __forceinline__ void store_zeros(const Args& a, const Shape& sh, cons
     *reinterpret_cast<uint4*>(out + ((size_t)(v / cols) * sh.I + v % cols * per) * size) = make_uint4(0, 0, 0, 0);
 }
 
-template <Op OP, typename T, bool F32, bool ACT, int CG>
-__global__ void __launch_bounds__(kThreads, 1)
+template <Op OP, typename T, bool F32, bool ACT, bool MX, int CG>
+__global__ void __launch_bounds__(kThreads<MX>, 1)
 gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
             const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b) {
-  constexpr int S = kStages<OP, ACT, CG>;
+  constexpr int S = kStages<OP, ACT, MX, CG>;
   constexpr int SB = kStageBytes<CG>;
+  constexpr int NT = kNT<MX>, KB = MX ? 128 : 64;  // columns; contraction of a stage
   constexpr bool A_MN = OP != kForward, B_MN = OP == kDw;
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Bars bars;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = ring + S * SB;
-  int* s_begin = reinterpret_cast<int*>(staging + kDrainWarps * kStagingBytes<OP, ACT>);
+  uint8_t* s_sf = staging + kDrainWarps * kStagingBytes<OP, ACT>;
+  int* s_begin = reinterpret_cast<int*>(s_sf + (MX ? S * kScaleBytes : 0));
   int* s_tile = s_begin + a.G + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -285,7 +297,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       mbar_init(&bars.full[s], 1);
       mbar_init(&bars.empty[s], 1);
       mbar_init(&bars.tail[s], 1);
-      mbar_init(&bars.tail_full[s], CG);
+      mbar_init(&bars.tail_full[s], MX ? kScaleWarps * CG : CG);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars.tfull[b], 1);
@@ -295,8 +307,8 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
   }
   if (warp == 1) tmem_alloc<CG>(&bars.tmem, kTmemCols);
   griddep_wait();
-  const bool bad = group_scan<kThreads>(a, s_begin, s_tile, [&](int rows) {
-    return OP == kDw ? sh.tiles_i * sh.tiles_j : sh.tiles_i * ((rows + kNT - 1) / kNT);
+  const bool bad = group_scan<kThreads<MX>>(a, s_begin, s_tile, [&](int rows) {
+    return OP == kDw ? sh.tiles_i * sh.tiles_j : sh.tiles_i * ((rows + NT - 1) / NT);
   });
   if (bad && blockIdx.x == 0) atomicOr(&g_status, (uint32_t)CQ_ST_BAD_ROWS);
   if constexpr (CG == 2) {
@@ -320,14 +332,16 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
 
   // Columns of B that this CTA loads for a tile: its half of jn, in copies of
   // 32 rows (K-major) or 64 columns (MN-major).
-  auto half_cols = [&](const Tile& x) { return ((x.jn + 31) / 32 * 32) / CG; };
+  auto half_cols = [&](const Tile& x) {
+    return (x.jn + kStepJ<MX> - 1) / kStepJ<MX> * kStepJ<MX> / CG;
+  };
 
   if (warp == 0) {
     // ---- copies ----
     uint32_t s = 0, lap = 0;  // stage, times the ring has gone round
     bool ok = true;
     for (int t = first; t < n_tiles && ok; t += step) {
-      const Tile x = tile_at<OP, CG>(sh, s_begin, s_tile, a.G, t);
+      const Tile x = tile_at<OP, MX, CG>(sh, s_begin, s_tile, a.G, t);
       const int i_cta = x.i0 + (int)rank * 128;
       const int jh = half_cols(x), jb = x.j0 + (int)rank * jh;
       constexpr int kBox = B_MN ? 64 : 128;
@@ -349,7 +363,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
             bar = lead(&bars.full[s]);
             if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], bytes * CG);
           }
-          const int k0 = kb * 64;
+          const int k0 = kb * KB;
           if constexpr (OP == kForward && ACT) {
             tma_load5<CG>(sa, &map_a, k0, 0, 0, i_cta / 32, x.e, bar);
           } else if constexpr (OP == kForward) {
@@ -386,16 +400,18 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     constexpr uint32_t ka = (A_MN ? 2048 : 32) >> 4, kbs = (B_MN ? 2048 : 32) >> 4;
     const uint64_t da = desc_at(desc_base(A_MN ? 8192 : 16), smem_u32(ring));
     const uint64_t db = desc_at(desc_base(B_MN ? 8192 : 16), smem_u32(ring) + kABytes);
-    uint32_t s = 0, lap = 0, buf = 0, tail_uses[S] = {};
+    uint32_t s = 0, lap = 0, buf = 0, sf_set = 0, tail_uses[S] = {};
     bool ok = true;
     for (int t = first; t < n_tiles && ok; t += step) {
-      const Tile x = tile_at<OP, CG>(sh, s_begin, s_tile, a.G, t);
+      const Tile x = tile_at<OP, MX, CG>(sh, s_begin, s_tile, a.G, t);
       if (x.nkb == 0) continue;
       const uint32_t b = buf & 1, use = buf >> 1;
       ++buf;
       if (use > 0 && !(ok = wait(&bars.tempty[b], (use - 1) & 1, 1, true))) break;
-      const uint32_t d = tmem + b * kNT;
-      const uint32_t idesc = idesc_f16(T::kBf16, A_MN, B_MN, 128 * CG, half_cols(x) * CG);
+      const uint32_t d = tmem + b * NT;
+      const uint32_t idesc =
+          MX ? idesc_mx(a.w_dtype, a.x_dtype == kMxE5M2, 128 * CG, half_cols(x) * CG)
+             : idesc_f16(T::kBf16, A_MN, B_MN, 128 * CG, half_cols(x) * CG);
       for (int kb = 0; kb < x.nkb; ++kb) {
         if (!(ok = wait(&bars.full[s], lap & 1, 1))) break;
         if (OP == kDw && kb == x.nkb - 1 && (x.kk & 15) != 0) {
@@ -405,11 +421,23 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
             if (q == s) use_t = tail_uses[q]++;
           if (!(ok = wait(&bars.tail_full[s], use_t & 1, 1, true))) break;
         }
+        if (MX && !(ok = wait(&bars.tail_full[s], lap & 1, 1, true))) break;
         fence_after();
         if (elect_one()) {
           const uint64_t ad = da + s * (SB >> 4), bd = db + s * (SB >> 4);
-          const int left = x.kk - kb * 64;
-          if (left > 48) {
+          const int left = x.kk - kb * KB;
+          if constexpr (MX) {
+            // scales of this stage, A then B, in one of two sets of 12 columns
+            const uint32_t sf = tmem + 2 * NT + 12 * sf_set;
+            const uint64_t ds = desc_scales(smem_u32(s_sf) + s * kScaleBytes);
+            copy_scales<CG>(sf, ds);
+            copy_scales<CG>(sf + 4, ds + (512 >> 4));
+            if (half_cols(x) * CG > 128) copy_scales<CG>(sf + 8, ds + (1024 >> 4));
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (32 * q < left)
+                mma_mx<CG>(d, ad + q * ka, bd + q * kbs, idesc_sf(idesc, q), sf, sf + 4, kb > 0 || q > 0);
+          } else if (left > 48) {
             mma_f16<CG>(d, ad, bd, idesc, kb > 0);
             mma_f16<CG>(d, ad + ka, bd + kbs, idesc, true);
             mma_f16<CG>(d, ad + 2 * ka, bd + 2 * kbs, idesc, true);
@@ -422,6 +450,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
           if (kb == x.nkb - 1) commit<CG>(smem_u32(&bars.tfull[b]));
         }
         __syncwarp();
+        sf_set ^= 1;
         if (++s == S) s = 0, ++lap;
       }
     }
@@ -430,7 +459,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     uint32_t it = 0, tail_uses[S] = {};
     bool ok = true;
     for (int t = first; t < n_tiles && ok; t += step) {
-      const Tile x = tile_at<OP, CG>(sh, s_begin, s_tile, a.G, t);
+      const Tile x = tile_at<OP, MX, CG>(sh, s_begin, s_tile, a.G, t);
       it += x.nkb;
       if (x.nkb == 0 || (x.kk & 15) == 0) continue;
       const int s = (it - 1) % S;
@@ -453,6 +482,80 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
         else async::mbar_arrive(&bars.tail_full[s]);
       }
     }
+  } else if (MX && warp >= 4 + kDrainWarps) {
+    // ---- scales: one word (4 blocks of 32) a row and stage ----
+    // Line r % 32 of a 512-byte atom holds the words of rows r % 32 + 0, 32, 64,
+    // 96. A warp takes three of the twelve sets of 32 rows (four of A, eight of
+    // B), four stages at a time in registers, the next four on their way.
+    const int w = warp - 4 - kDrainWarps;
+    uint32_t s = 0, lap = 0;
+    bool ok = true;
+    const int blocks = sh.KK / 32;
+    const bool whole = a.SC % 16 == 0 && a.SC == blocks;  // 16-byte pieces, no pad column
+    for (int t = first; t < n_tiles && ok; t += step) {
+      const Tile x = tile_at<OP, MX, CG>(sh, s_begin, s_tile, a.G, t);
+      const uint8_t* rows[3];  // scale rows, NULL where there is none
+#pragma unroll
+      for (int b = 0; b < 3; ++b) {
+        const int set = w * 3 + b;
+        rows[b] = nullptr;
+        if (set < 4) {
+          int row = x.i0 + (int)rank * 128 + 32 * set + lane;  // of the tile's weight rows
+          bool in = row < sh.I;
+          if (ACT) {
+            const int o = row / 32 * 16 + (lane & 15);
+            in = o < sh.n_out;
+            row = o + (lane >= 16 ? sh.n_out : 0);
+          }
+          if (in) rows[b] = a.w_scales + ((size_t)x.e * a.N + row) * a.SC;
+        } else {
+          const int j = 32 * (set - 4) + lane;
+          if (j < x.jn) rows[b] = a.x_scales + (size_t)(x.begin + x.j0 + j) * a.SC;
+        }
+      }
+      auto fetch = [&](int kb, uint4 (&v)[3]) {
+#pragma unroll
+        for (int b = 0; b < 3; ++b) {
+          v[b] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+          if (!rows[b]) continue;
+          if (whole) {
+            if (kb * 4 < blocks) v[b] = __ldg(reinterpret_cast<const uint4*>(rows[b] + kb * 4));
+          } else {
+            uint32_t q[8];
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+              const int at = kb * 4 + 2 * h;  // SC is even: a pair is inside or outside
+              q[h] = at < blocks ? __ldg(reinterpret_cast<const uint16_t*>(rows[b] + at)) : 0x7f7fu;
+              if (at + 1 == blocks) q[h] = (q[h] & 0xffu) | 0x7f00u;  // the pad column
+            }
+            v[b] = make_uint4(q[0] | q[1] << 16, q[2] | q[3] << 16, q[4] | q[5] << 16, q[6] | q[7] << 16);
+          }
+        }
+      };
+      uint4 now[3], next[3];
+      fetch(0, next);
+      for (int kb = 0; kb < x.nkb; ++kb) {
+        if ((kb & 3) == 0) {
+#pragma unroll
+          for (int b = 0; b < 3; ++b) now[b] = next[b];
+          fetch(kb + 4, next);
+        }
+        if (lap > 0 && !(ok = wait(&bars.empty[s], (lap & 1) ^ 1, 1))) break;
+#pragma unroll
+        for (int b = 0; b < 3; ++b) {
+          const int set = w * 3 + b, c = kb & 3;
+          const uint32_t v = c == 0 ? now[b].x : c == 1 ? now[b].y : c == 2 ? now[b].z : now[b].w;
+          *reinterpret_cast<uint32_t*>(s_sf + s * kScaleBytes + set / 4 * 512 + lane * 16 + set % 4 * 4) = v;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2) arrive_cluster(leader_addr(smem_u32(&bars.tail_full[s])));
+          else async::mbar_arrive(&bars.tail_full[s]);
+        }
+        if (++s == S) s = 0, ++lap;
+      }
+    }
   } else if (warp >= 4) {
     // ---- results ----
     const int q = warp & 3, half = (warp - 4) >> 2;
@@ -460,7 +563,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     uint32_t buf = 0;
     bool ok = true;
     for (int t = first; t < n_tiles && ok; t += step) {
-      const Tile x = tile_at<OP, CG>(sh, s_begin, s_tile, a.G, t);
+      const Tile x = tile_at<OP, MX, CG>(sh, s_begin, s_tile, a.G, t);
       const int i_cta = x.i0 + (int)rank * 128;
       if (x.nkb == 0) {
         if (i_cta < sh.I) store_zeros<F32>(a, sh, x, i_cta);
@@ -470,7 +573,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       ++buf;
       if (!(ok = wait(&bars.tfull[b], use & 1, 2 + x.nkb / 65536))) break;
       fence_after();
-      const uint32_t src = tmem + b * kNT + ((uint32_t)(q * 32) << 16);
+      const uint32_t src = tmem + b * NT + ((uint32_t)(q * 32) << 16);
       for (int c0 = 32 * half; c0 < x.jn; c0 += 64)
         drain<OP, T, F32, ACT>(a, sh, x, i_cta + 32 * q, c0, src, stage);
       fence_before();
@@ -490,22 +593,23 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
 }
 
 // ---- host ----
-template <Op OP, typename T, bool F32, bool ACT, int CG>
+template <Op OP, typename T, bool F32, bool ACT, bool MX, int CG>
 cudaError_t launch_t(const Args& a, const Shape& sh, const CUtensorMap& ma, const CUtensorMap& mb,
                      cudaStream_t s) {
-  constexpr auto kernel = gemm_kernel<OP, T, F32, ACT, CG>;
-  const size_t smem = 1024 + (size_t)kStages<OP, ACT, CG> * kStageBytes<CG> +
-                      kDrainWarps * kStagingBytes<OP, ACT> + 8 * ((size_t)a.G + 1);
+  constexpr auto kernel = gemm_kernel<OP, T, F32, ACT, MX, CG>;
+  const size_t smem = 1024 + (size_t)kStages<OP, ACT, MX, CG> * kStageBytes<CG> +
+                      kDrainWarps * kStagingBytes<OP, ACT> +
+                      (MX ? kStages<OP, ACT, MX, CG> * kScaleBytes : 0) + 8 * ((size_t)a.G + 1);
   cudaError_t e = prepare_kernel<kernel>(smem);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorUnknown;
   const int64_t most = OP == kDw ? (int64_t)a.G * sh.tiles_i * sh.tiles_j
-                                 : (int64_t)sh.tiles_i * (a.R / kNT + std::min(a.G, a.R));
+                                 : (int64_t)sh.tiles_i * (a.R / kNT<MX> + std::min(a.G, a.R));
   const int clusters = (int)std::min<int64_t>(sms / CG, most);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(clusters * CG);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreads<MX>);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -537,12 +641,12 @@ cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
       const uint64_t n = N / 2, d[] = {K, 16, 2, n / 16, G}, st[] = {2 * K, 2 * n * K, 32 * K, 2 * N * K};
       const uint32_t b[] = {64, 16, 2, 4, 1};
       if (!make_map(&ma, a.w, type, 5, d, st, b)) return cudaErrorUnknown;
-      return launch_t<kForward, T, false, true, CG>(a, sh, ma, mb, s);
+      return launch_t<kForward, T, false, true, false, CG>(a, sh, ma, mb, s);
     }
     const uint64_t d[] = {K, N, G}, st[] = {2 * K, 2 * N * K};
     const uint32_t b[] = {64, 128, 1};
     if (!make_map(&ma, a.w, type, 3, d, st, b)) return cudaErrorUnknown;
-    return launch_t<kForward, T, false, false, CG>(a, sh, ma, mb, s);
+    return launch_t<kForward, T, false, false, false, CG>(a, sh, ma, mb, s);
   }
   sh.I = a.K;
   sh.tiles_i = (a.K + TI - 1) / TI;
@@ -552,17 +656,42 @@ cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
     const uint32_t b[] = {64, 64, 1}, bb[] = {64, 128};
     if (!make_map(&ma, a.w, type, 3, d, st, b) || !make_map(&mb, a.x, type, 2, db, sb, bb))
       return cudaErrorUnknown;
-    return a.pre_in ? launch_t<kDx, T, false, true, CG>(a, sh, ma, mb, s)
-                    : launch_t<kDx, T, false, false, CG>(a, sh, ma, mb, s);
+    return a.pre_in ? launch_t<kDx, T, false, true, false, CG>(a, sh, ma, mb, s)
+                    : launch_t<kDx, T, false, false, false, CG>(a, sh, ma, mb, s);
   }
   sh.J = a.N;
-  sh.tiles_j = (a.N + kNT - 1) / kNT;
+  sh.tiles_j = (a.N + kNT<false> - 1) / kNT<false>;
   const uint64_t d[] = {K, R}, st[] = {2 * K}, db[] = {N, R}, sb[] = {2 * N};
   const uint32_t b[] = {64, 64};
   if (!make_map(&ma, a.x, type, 2, d, st, b) || !make_map(&mb, a.w, type, 2, db, sb, b))
     return cudaErrorUnknown;
-  return a.out_dtype == 2 ? launch_t<kDw, T, true, false, CG>(a, sh, ma, mb, s)
-                          : launch_t<kDw, T, false, false, CG>(a, sh, ma, mb, s);
+  return a.out_dtype == 2 ? launch_t<kDw, T, true, false, false, CG>(a, sh, ma, mb, s)
+                          : launch_t<kDw, T, false, false, false, CG>(a, sh, ma, mb, s);
+}
+
+// Forward from mx fp8 operands; T is the output's type.
+template <typename T, int CG>
+cudaError_t launch_mx(const Args& a, cudaStream_t s) {
+  const uint64_t G = a.G, R = a.R, N = a.N, K = a.K;
+  CUtensorMap ma, mb;
+  Shape sh = {};
+  sh.n_out = a.act ? a.N / 2 : a.N;
+  sh.I = a.N;
+  sh.KK = a.K;
+  sh.tiles_i = (a.N + 128 * CG - 1) / (128 * CG);
+  const uint64_t db[] = {K, R}, sb[] = {K};
+  const uint32_t bb[] = {128, 128};
+  if (!make_map(&mb, a.x, kMapU8, 2, db, sb, bb)) return cudaErrorUnknown;
+  if (a.act) {
+    const uint64_t n = N / 2, d[] = {K, 16, 2, n / 16, G}, st[] = {K, n * K, 16 * K, N * K};
+    const uint32_t b[] = {128, 16, 2, 4, 1};
+    if (!make_map(&ma, a.w, kMapU8, 5, d, st, b)) return cudaErrorUnknown;
+    return launch_t<kForward, T, false, true, true, CG>(a, sh, ma, mb, s);
+  }
+  const uint64_t d[] = {K, N, G}, st[] = {K, N * K};
+  const uint32_t b[] = {128, 128, 1};
+  if (!make_map(&ma, a.w, kMapU8, 3, d, st, b)) return cudaErrorUnknown;
+  return launch_t<kForward, T, false, false, true, CG>(a, sh, ma, mb, s);
 }
 
 }  // namespace
@@ -572,6 +701,8 @@ int launch_gemm(Op op, const Args& a, cudaStream_t s) {
   if (a.R == 0) {
     if (op != kDw) return CQ_OK;
     e = cudaMemsetAsync(a.out, 0, (size_t)a.G * a.N * a.K * (a.out_dtype == 2 ? 4 : 2), s);
+  } else if (a.x_dtype >= kMxE4M3) {
+    e = a.out_dtype == 1 ? launch_mx<F16, 2>(a, s) : launch_mx<BF16, 2>(a, s);
   } else {
     e = a.x_dtype == kF16 ? launch_op<F16, 2>(op, a, s) : launch_op<BF16, 2>(op, a, s);
   }

@@ -147,6 +147,37 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
         : "memory");
 }
 
+// The same with fp8 operands and a power-of-two scale for each row of A and B
+// and 32 of the contraction; the scales' TMEM addresses are sa and sb.
+template <int CG>
+__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t sa, uint32_t sb, bool add) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.u32 p, %6, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+        : "memory");
+  else
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.u32 p, %6, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+        : "memory");
+}
+
+// 32 lines of 16 bytes of shared memory into 4 TMEM columns, the same in each
+// quarter of the lanes (the layout of scales), in both CTAs of a pair.
+template <int CG>
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
 // One arrival on `bar` (with CG 2, at the same address in both CTAs) when every
 // tcgen05 operation issued so far by this thread has completed.
 template <int CG>
@@ -219,6 +250,19 @@ __device__ __forceinline__ uint32_t idesc_f16(bool bf16, bool a_mn, bool b_mn, i
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
+
+// Descriptor of 32 unswizzled lines of 16 bytes, for copy_scales.
+__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+}
+
+// Instruction descriptor of kind::mxf8f6f4: formats 0 e4m3, 1 e5m2; e8m0 scales.
+// idesc_sf(d, i): with the scales' byte i of each 32-bit word.
+__device__ __forceinline__ uint32_t idesc_mx(int a_fmt, int b_fmt, int m, int n) {
+  return ((uint32_t)a_fmt << 7) | ((uint32_t)b_fmt << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(m >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t idesc_sf(uint32_t d, uint32_t i) { return d | (i << 4) | (i << 29); }
 
 // ---- host: tensor maps ----
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
