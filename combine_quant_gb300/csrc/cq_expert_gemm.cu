@@ -49,6 +49,7 @@ constexpr int kNT = MX ? 240 : 256;
 template <bool MX>
 constexpr int kStepJ = MX ? 16 : 32;       // columns come in steps of
 constexpr int kScaleBytes = 3 * 512;       // mx: scales of a stage: 128 rows of A, 256 of B
+constexpr int kScaleRing = 3;              // entries of four stages' scales
 constexpr int kABytes = 128 * 128;         // A of one stage, one CTA
 constexpr uint32_t kTmemCols = 512;
 constexpr int kBand = 8;                   // tiles along i taken together, for reuse in L2
@@ -68,7 +69,8 @@ struct Shape {
 };
 
 struct Bars {
-  uint64_t full[8], empty[8], tail[8], tail_full[8];  // tail_full, mx: scales are there
+  uint64_t full[8], empty[8], tail[8], tail_full[8];
+  uint64_t sfull[4], sempty[4];  // mx: scales
   uint64_t tfull[2], tempty[2];
   uint32_t tmem;
 };
@@ -285,7 +287,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = ring + S * SB;
   uint8_t* s_sf = staging + kDrainWarps * kStagingBytes<OP, ACT>;
-  int* s_begin = reinterpret_cast<int*>(s_sf + (MX ? S * kScaleBytes : 0));
+  int* s_begin = reinterpret_cast<int*>(s_sf + (MX ? kScaleRing * 4 * kScaleBytes : 0));
   int* s_tile = s_begin + a.G + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -297,7 +299,11 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       mbar_init(&bars.full[s], 1);
       mbar_init(&bars.empty[s], 1);
       mbar_init(&bars.tail[s], 1);
-      mbar_init(&bars.tail_full[s], MX ? kScaleWarps * CG : CG);
+      mbar_init(&bars.tail_full[s], CG);
+    }
+    for (int s = 0; s < kScaleRing; ++s) {
+      mbar_init(&bars.sfull[s], kScaleWarps * CG);
+      mbar_init(&bars.sempty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars.tfull[b], 1);
@@ -400,7 +406,8 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     constexpr uint32_t ka = (A_MN ? 2048 : 32) >> 4, kbs = (B_MN ? 2048 : 32) >> 4;
     const uint64_t da = desc_at(desc_base(A_MN ? 8192 : 16), smem_u32(ring));
     const uint64_t db = desc_at(desc_base(B_MN ? 8192 : 16), smem_u32(ring) + kABytes);
-    uint32_t s = 0, lap = 0, buf = 0, sf_set = 0, tail_uses[S] = {};
+    uint32_t s = 0, lap = 0, buf = 0, tail_uses[S] = {};
+    uint32_t se = 0, se_lap = 0, sf_set = 0;  // mx: entry of scales, TMEM columns of them
     bool ok = true;
     for (int t = first; t < n_tiles && ok; t += step) {
       const Tile x = tile_at<OP, MX, CG>(sh, s_begin, s_tile, a.G, t);
@@ -421,7 +428,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
             if (q == s) use_t = tail_uses[q]++;
           if (!(ok = wait(&bars.tail_full[s], use_t & 1, 1, true))) break;
         }
-        if (MX && !(ok = wait(&bars.tail_full[s], lap & 1, 1, true))) break;
+        if (MX && (kb & 3) == 0 && !(ok = wait(&bars.sfull[se], se_lap & 1, 1, true))) break;
         fence_after();
         if (elect_one()) {
           const uint64_t ad = da + s * (SB >> 4), bd = db + s * (SB >> 4);
@@ -429,7 +436,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
           if constexpr (MX) {
             // scales of this stage, A then B, in one of two sets of 12 columns
             const uint32_t sf = tmem + 2 * NT + 12 * sf_set;
-            const uint64_t ds = desc_scales(smem_u32(s_sf) + s * kScaleBytes);
+            const uint64_t ds = desc_scales(smem_u32(s_sf) + (se * 4 + (kb & 3)) * kScaleBytes);
             copy_scales<CG>(sf, ds);
             copy_scales<CG>(sf + 4, ds + (512 >> 4));
             if (half_cols(x) * CG > 128) copy_scales<CG>(sf + 8, ds + (1024 >> 4));
@@ -447,10 +454,14 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
               mma_f16<CG>(d, ad + q * ka, bd + q * kbs, idesc, kb > 0 || q > 0);
           }
           commit<CG>(smem_u32(&bars.empty[s]));
+          if (MX && ((kb & 3) == 3 || kb == x.nkb - 1)) commit<CG>(smem_u32(&bars.sempty[se]));
           if (kb == x.nkb - 1) commit<CG>(smem_u32(&bars.tfull[b]));
         }
         __syncwarp();
-        sf_set ^= 1;
+        if constexpr (MX) {
+          sf_set ^= 1;
+          if (((kb & 3) == 3 || kb == x.nkb - 1) && ++se == kScaleRing) se = 0, ++se_lap;
+        }
         if (++s == S) s = 0, ++lap;
       }
     }
@@ -486,7 +497,8 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     // ---- scales: one word (4 blocks of 32) a row and stage ----
     // Line r % 32 of a 512-byte atom holds the words of rows r % 32 + 0, 32, 64,
     // 96. A warp takes three of the twelve sets of 32 rows (four of A, eight of
-    // B), four stages at a time in registers, the next four on their way.
+    // B), four stages at a time: 16 bytes of a row per load, one fence and one
+    // arrival for four stages.
     const int w = warp - 4 - kDrainWarps;
     uint32_t s = 0, lap = 0;
     bool ok = true;
@@ -532,28 +544,27 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
           }
         }
       };
-      uint4 now[3], next[3];
-      fetch(0, next);
-      for (int kb = 0; kb < x.nkb; ++kb) {
-        if ((kb & 3) == 0) {
-#pragma unroll
-          for (int b = 0; b < 3; ++b) now[b] = next[b];
-          fetch(kb + 4, next);
-        }
-        if (lap > 0 && !(ok = wait(&bars.empty[s], (lap & 1) ^ 1, 1))) break;
+      uint4 v[3];
+      fetch(0, v);
+      for (int kb = 0; kb < x.nkb; kb += 4) {
+        if (lap > 0 && !(ok = wait(&bars.sempty[s], (lap & 1) ^ 1, 1))) break;
 #pragma unroll
         for (int b = 0; b < 3; ++b) {
-          const int set = w * 3 + b, c = kb & 3;
-          const uint32_t v = c == 0 ? now[b].x : c == 1 ? now[b].y : c == 2 ? now[b].z : now[b].w;
-          *reinterpret_cast<uint32_t*>(s_sf + s * kScaleBytes + set / 4 * 512 + lane * 16 + set % 4 * 4) = v;
+          const int set = w * 3 + b;
+          uint8_t* to = s_sf + s * 4 * kScaleBytes + set / 4 * 512 + lane * 16 + set % 4 * 4;
+          *reinterpret_cast<uint32_t*>(to) = v[b].x;
+          *reinterpret_cast<uint32_t*>(to + kScaleBytes) = v[b].y;
+          *reinterpret_cast<uint32_t*>(to + 2 * kScaleBytes) = v[b].z;
+          *reinterpret_cast<uint32_t*>(to + 3 * kScaleBytes) = v[b].w;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          if (CG == 2) arrive_cluster(leader_addr(smem_u32(&bars.tail_full[s])));
-          else async::mbar_arrive(&bars.tail_full[s]);
+          if (CG == 2) arrive_cluster(leader_addr(smem_u32(&bars.sfull[s])));
+          else async::mbar_arrive(&bars.sfull[s]);
         }
-        if (++s == S) s = 0, ++lap;
+        if (++s == kScaleRing) s = 0, ++lap;
+        fetch(kb + 4, v);
       }
     }
   } else if (warp >= 4) {
@@ -599,7 +610,7 @@ cudaError_t launch_t(const Args& a, const Shape& sh, const CUtensorMap& ma, cons
   constexpr auto kernel = gemm_kernel<OP, T, F32, ACT, MX, CG>;
   const size_t smem = 1024 + (size_t)kStages<OP, ACT, MX, CG> * kStageBytes<CG> +
                       kDrainWarps * kStagingBytes<OP, ACT> +
-                      (MX ? kStages<OP, ACT, MX, CG> * kScaleBytes : 0) + 8 * ((size_t)a.G + 1);
+                      (MX ? kScaleRing * 4 * kScaleBytes : 0) + 8 * ((size_t)a.G + 1);
   cudaError_t e = prepare_kernel<kernel>(smem);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
