@@ -77,6 +77,22 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* m, in
         : "memory");
 }
 template <int CG>
+__device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* m, int x, int y, int z,
+                                          int u, uint32_t bar) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z), "r"(u),
+        "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx"
+        "::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z),
+        "r"(u), "r"(bar)
+        : "memory");
+}
+template <int CG>
 __device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap* m, int x, int y, int z,
                                           int u, int v, uint32_t bar) {
   if constexpr (CG == 1)
