@@ -47,7 +47,7 @@ struct Shape {
   int n_out;     // outputs (with SwiGLU half the weight rows)
   int tiles_n;   // tiles along the weight rows
   int KG;        // groups of k
-  int group;
+  int shift;     // log2 of a group's length
   int vec;       // rows of scales are whole 16-byte pieces
   int stages;    // stages of the ring
 };
@@ -184,6 +184,38 @@ __device__ __forceinline__ void multiply(float (&acc)[MTW][NTMAX][4], const uint
   }
 }
 
+// This thread's byte offsets in a stage.
+struct Places {
+  uint32_t w, x, sum, scale, scale_next;
+};
+
+// All of k for one tile: false when a wait gave up.
+template <typename T, int MTW, int NT, int NTMAX, bool ZEROS, bool G32>
+__device__ __forceinline__ bool multiply_tile(float (&acc)[MTW][NTMAX][4], Bars& bars,
+                                              const uint8_t* ring, int S, uint32_t& s, uint32_t& lap,
+                                              const Places& at, int kw, int K) {
+  using St = Stage<MTW, NTMAX, ZEROS, G32>;
+  const uint32_t at_x = at.x + kw * 2 * 512 * NT;
+  for (int left = K - kw * 64; left + kw * 64 > 0; left -= 512) {
+    if (!mbar_wait(&bars.ready[s], lap & 1)) return false;
+    const uint8_t* base = ring + s * St::kBytes;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (left > 256 * c) {
+        const uint8_t* scale = base + at.scale + c * at.scale_next;
+        multiply<T, MTW, NT, NTMAX, ZEROS, G32>(
+            acc, base + c * St::kChunk + at.w, base + c * St::kChunk + (at.w ^ 16),
+            base + at_x + c * (8 * 512 * NT),
+            reinterpret_cast<const float*>(base + at.sum + c * (4 * St::kSpans * 8 * NTMAX * 4)),
+            reinterpret_cast<const float*>(scale),
+            reinterpret_cast<const float*>(scale + St::kZero - St::kScale));
+      }
+    release_slot(&bars.empty[s]);
+    if (++s == (uint32_t)S) s = 0, ++lap;
+  }
+  return true;
+}
+
 __device__ __forceinline__ void bar_mul() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kMulWarps) : "memory");
 }
@@ -241,35 +273,23 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
   if (warp < kMulWarps) {
     // ---- products ----
     const int kw = warp & 3, rq = warp >> 2;
-    const uint32_t at_w = rq * (16 * MTW * 128) + g * 128 + (((2 * kw) ^ g) << 4) + 4 * q;
-    const uint32_t at_x = St::kX + g * 64 + ((q ^ ((g >> 1) & 3)) << 4);
-    const uint32_t at_s = St::kScale + (rq * 8 + g) * (2 * MTW * 4);
+    Places at;
+    at.w = rq * (16 * MTW * 128) + g * 128 + (((2 * kw) ^ g) << 4) + 4 * q;
+    at.x = St::kX + g * 64 + ((q ^ ((g >> 1) & 3)) << 4);
+    at.sum = St::kSum + (kw * (St::kSpans * 8 * NTMAX) + 2 * q) * 4;
+    at.scale = St::kScale + ((kw * 64 >> sh.shift) * St::kGroupFloats + (rq * 8 + g) * (2 * MTW)) * 4;
+    at.scale_next = (256 >> sh.shift) * St::kGroupFloats * 4;
     for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
       const Tile x = tile_at<MTW, NTMAX, ACT>(sh, s_begin, s_tile, a.G, t);
       float acc[MTW][NTMAX][4] = {};
-      for (int st = 0; st < n_stages; ++st) {
-        if (!(ok = wait(&bars.ready[s], lap & 1))) break;
-        const uint8_t* base = ring + s * St::kBytes;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int k = c * 256 + kw * 64;  // within the stage
-          if (st * 512 + k < a.K) {
-            const uint8_t *sw0 = base + c * St::kChunk + at_w, *sw1 = base + c * St::kChunk + (at_w ^ 16);
-            const float* sum = reinterpret_cast<const float*>(base + St::kSum) +
-                               (c * 4 + kw) * (St::kSpans * 8 * NTMAX) + 2 * q;
-            const float* scale = reinterpret_cast<const float*>(base + at_s) + k / sh.group * St::kGroupFloats;
-            const float* zero = scale + (St::kZero - St::kScale) / 4;
-            const uint8_t* sx = base + at_x;
-            if (NTMAX == 1 || x.nt == 1)
-              multiply<T, MTW, 1, NTMAX, ZEROS, G32>(acc, sw0, sw1, sx + k / 32 * 512, sum, scale, zero);
-            else
-              multiply<T, MTW, NTMAX, NTMAX, ZEROS, G32>(acc, sw0, sw1, sx + k / 32 * 512 * NTMAX, sum, scale, zero);
-          }
-        }
-        release_slot(&bars.empty[s]);
-        next();
+      if (NTMAX == 1 || x.nt == 1)
+        ok = multiply_tile<T, MTW, 1, NTMAX, ZEROS, G32>(acc, bars, ring, S, s, lap, at, kw, a.K);
+      else
+        ok = multiply_tile<T, MTW, NTMAX, NTMAX, ZEROS, G32>(acc, bars, ring, S, s, lap, at, kw, a.K);
+      if (!ok) {
+        atomicOr(&g_status, (uint32_t)CQ_ST_TIMEOUT);
+        break;
       }
-      if (!ok) break;
       // Sums of the four k shares, added in order: 16 rows of every quarter at a time.
 #pragma unroll
       for (int m = 0; m < MTW; ++m) {
@@ -350,21 +370,22 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       }
     }
   } else if (warp < kMulWarps + kSumWarps + kScaleWarps) {
-    // ---- scales: a thread takes rows r and r + 64, one stage ahead ----
+    // ---- scales: a thread takes rows r and r + 64, kAhead stages ahead ----
+    constexpr int kAhead = G32 ? 2 : 4;
     constexpr int kPer = (St::kRows + 63) / 64, kW = St::kGroups / 2;  // rows; words of a row
     const uint16_t* scales = static_cast<const uint16_t*>(a.scales4);
     const int per_cta = n_tiles > (int)blockIdx.x ? (n_tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
-    const int total = per_cta * n_stages, ng = 512 / sh.group;
+    const int total = per_cta * n_stages, ng = 512 >> sh.shift;
     const int r0 = threadIdx.x - 32 * (kMulWarps + kSumWarps);
-    int cur = -1;
+    int tile = -1, st = n_stages - 1;
     size_t row_at[kPer] = {};
     bool in[kPer] = {};
-    uint32_t sv[kPer][kW], zv[kPer][kW / 2];
-    auto load = [&](int i) {
+    uint32_t sbuf[kAhead][kPer][kW], zbuf[kAhead][kPer][kW / 2];
+    auto load = [&](int i, uint32_t (&sv)[kPer][kW], uint32_t (&zv)[kPer][kW / 2]) {
       if (i >= total) return;
-      const int tile = i / n_stages, first = (i - tile * n_stages) * ng;
-      if (tile != cur) {
-        cur = tile;
+      if (++st == n_stages) st = 0, ++tile;
+      const int first = st * ng;
+      if (st == 0) {
         const Tile x = tile_at<MTW, NTMAX, ACT>(sh, s_begin, s_tile, a.G, blockIdx.x + tile * gridDim.x);
 #pragma unroll
         for (int b = 0; b < kPer; ++b) {
@@ -401,28 +422,33 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
         }
       }
     };
-    load(0);
-    for (int i = 0; i < total && ok; ++i) {
-      if (lap > 0 && !(ok = wait(&bars.empty[s], (lap & 1) ^ 1))) break;
-      uint8_t* base = ring + s * St::kBytes;
 #pragma unroll
-      for (int b = 0; b < kPer; ++b) {
-        const int r = r0 + 64 * b;
-        const int slot = (r / (16 * MTW) * 8 + r % 8) * (2 * MTW) + 2 * (r / 16 % MTW) + r / 8 % 2;
-        float* to = reinterpret_cast<float*>(base + St::kScale) + slot;
-        float* tz = reinterpret_cast<float*>(base + St::kZero) + slot;
+    for (int u = 0; u < kAhead; ++u) load(u, sbuf[u], zbuf[u]);
+    for (int i0 = 0; i0 < total && ok; i0 += kAhead) {
 #pragma unroll
-        for (int k = 0; k < St::kGroups; ++k)
-          if (k < ng) {
-            to[k * St::kGroupFloats] = k & 1 ? T::hi(sv[b][k / 2]) : T::lo(sv[b][k / 2]);
-            if (ZEROS)
-              tz[k * St::kGroupFloats] = -(kOff + (float)((zv[b][k / 4] >> (8 * (k & 3))) & 255));
-          }
+      for (int u = 0; u < kAhead; ++u) {
+        if (i0 + u >= total || !ok) break;
+        if (lap > 0 && !(ok = wait(&bars.empty[s], (lap & 1) ^ 1))) break;
+        uint8_t* base = ring + s * St::kBytes;
+#pragma unroll
+        for (int b = 0; b < kPer; ++b) {
+          const int r = r0 + 64 * b;
+          const int slot = (r / (16 * MTW) * 8 + r % 8) * (2 * MTW) + 2 * (r / 16 % MTW) + r / 8 % 2;
+          float* to = reinterpret_cast<float*>(base + St::kScale) + slot;
+          float* tz = reinterpret_cast<float*>(base + St::kZero) + slot;
+#pragma unroll
+          for (int k = 0; k < St::kGroups; ++k)
+            if (k < ng) {
+              to[k * St::kGroupFloats] = k & 1 ? T::hi(sbuf[u][b][k / 2]) : T::lo(sbuf[u][b][k / 2]);
+              if (ZEROS)
+                tz[k * St::kGroupFloats] = -(kOff + (float)((zbuf[u][b][k / 4] >> (8 * (k & 3))) & 255));
+            }
+        }
+        __syncwarp();
+        if (lane == 0) async::mbar_arrive(&bars.ready[s]);
+        next();
+        load(i0 + u + kAhead, sbuf[u], zbuf[u]);
       }
-      __syncwarp();
-      if (lane == 0) async::mbar_arrive(&bars.ready[s]);
-      next();
-      load(i + 1);
     }
   } else {
     // ---- copies of codes and x ----
@@ -459,7 +485,7 @@ cudaError_t launch_t(const Args& a, cudaStream_t s) {
   Shape sh = {};
   sh.n_out = ACT ? a.N / 2 : a.N;
   sh.tiles_n = (a.N + St::kRows - 1) / St::kRows;
-  sh.group = a.group;
+  sh.shift = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
   sh.KG = a.K / a.group;
   sh.vec = sh.KG % 8 == 0;
   const uint64_t G = a.G, R = a.R, N = a.N, K = a.K;
