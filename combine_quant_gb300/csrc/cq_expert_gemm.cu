@@ -10,8 +10,8 @@
 //
 //   forward  out = y,  i = weight rows, j = tokens, sum over k:  A = w (K-major),  B = x (K-major)
 //   dx       out = dx, i = weight cols, j = tokens, sum over n:  A = w (MN-major), B = dy (K-major)
-//   dw       out = dw, i = columns of x, j = columns of dy, sum over the expert's
-//            rows:  A = x (MN-major), B = dy (MN-major)
+//   dw       out = dw, i = columns of dy, j = columns of x, sum over the expert's
+//            rows:  A = dy (MN-major), B = x (MN-major); here j is the contiguous axis
 //
 // Warp 0 fills a ring of shared-memory stages with tiled copies (64 of the
 // contraction, 128-byte swizzle), warp 1 issues the products into one of two
@@ -66,6 +66,8 @@ struct Shape {
   int n_out;           // forward: n
   int tiles_i;         // tiles along i
   int tiles_j;         // dw: tiles along j
+  int sectors;         // dw: the result is 32-byte aligned
+  int whole;           // MN-major operands are whole blocks of 64: one copy takes two of them
 };
 
 struct Bars {
@@ -145,29 +147,55 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 template <Op OP, bool ACT>
 constexpr int kStagingBytes = OP == kDx && ACT ? 32 * 36 * 4 : 32 * 64;
 
-// Drains columns [c0, c0 + 32) of a tile: out[j][i .. i + 31] of 32 j. The
-// accumulator holds i on lanes and j on columns, memory wants i contiguous, so
-// the block is turned in shared memory (16-byte pieces of a 64-byte row, XORed
-// with bits of the row number: no bank conflicts either way) and written in
-// 16-byte stores, 64 bytes a row.
+// 32 bytes to global memory: one store of a whole sector where the address allows.
+__device__ __forceinline__ void store32(void* p, int sectors, const uint32_t* v) {
+  if (sectors) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// Drains columns [c0, c0 + 32) of a tile. dw: a lane holds 32 neighbours of one
+// row of the result and writes them, a sector at a time. The others: out[j][i ..
+// i + 31] of 32 j. The accumulator holds i on lanes and j on columns, memory
+// wants i contiguous, so the block is turned in shared memory (16-byte pieces of
+// a 64-byte row, XORed with bits of the row number: no bank conflicts either
+// way) and written in 16-byte stores, 64 bytes a row.
 template <Op OP, typename T, bool F32, bool ACT>
 __device__ __forceinline__ void drain(const Args& a, const Shape& sh, const Tile& x, int i_warp,
                                       int c0, uint32_t src, uint8_t* stage) {
   const int lane = threadIdx.x & 31;
   const int jn = x.jn - c0;  // columns that exist
-  const size_t row0 = (OP == kDw ? (size_t)x.e * sh.J + x.j0 : (size_t)(x.begin + x.j0)) + c0;
-  const uint32_t st = smem_u32(stage);
-  if constexpr (F32) {
+  if constexpr (OP == kDw) {
     uint32_t acc[32];
     tmem_ld32(src + c0, acc);
     tmem_wait();
     const int i = i_warp + lane;
-    float* out = static_cast<float*>(a.out) + row0 * sh.I + i;
-    if (i < sh.I)
+    if (i >= sh.I) return;
+    const size_t at = ((size_t)x.e * sh.I + i) * sh.J + x.j0 + c0;
+    if constexpr (F32) {
+      float* out = static_cast<float*>(a.out) + at;
 #pragma unroll
-      for (int c = 0; c < 32; ++c)
-        if (c < jn) out[(size_t)c * sh.I] = __uint_as_float(acc[c]);
-  } else if constexpr (OP == kDx && ACT) {
+      for (int c = 0; c < 32; c += 8)
+        if (c < jn) store32(out + c, sh.sectors, acc + c);
+    } else {
+      uint16_t* out = static_cast<uint16_t*>(a.out) + at;
+      uint32_t v[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        v[c] = T::pack2(__uint_as_float(acc[2 * c]), __uint_as_float(acc[2 * c + 1]));
+      store32(out, sh.sectors, v);
+      if (16 < jn) store32(out + 16, sh.sectors, v + 8);
+    }
+    return;
+  }
+  const size_t row0 = (size_t)(x.begin + x.j0) + c0;
+  const uint32_t st = smem_u32(stage);
+  if constexpr (OP == kDx && ACT) {
     const int r = lane >> 2, i = i_warp + 8 * (lane & 3);
     const size_t ld = 2 * (size_t)sh.I, first = (row0 + r) * ld + i;
     const uint16_t* pre = static_cast<const uint16_t*>(a.pre_in) + first;
@@ -264,14 +292,14 @@ __device__ __forceinline__ void drain(const Args& a, const Shape& sh, const Tile
   }
 }
 
-// Zeros for a tile of an expert without rows (dw).
+// Zeros for a tile of an expert without rows (dw): 128 rows from i0.
 template <bool F32>
 __device__ __forceinline__ void store_zeros(const Args& a, const Shape& sh, const Tile& x, int i0) {
-  const int per = F32 ? 4 : 8, size = F32 ? 4 : 2;  // elements per 16 bytes, bytes per element
-  const int cols = min(128, sh.I - i0) / per;
-  char* out = static_cast<char*>(a.out) + (((size_t)x.e * sh.J + x.j0) * sh.I + i0) * size;
-  for (int v = threadIdx.x - 128; v < x.jn * cols; v += kDrainWarps * 32)
-    *reinterpret_cast<uint4*>(out + ((size_t)(v / cols) * sh.I + v % cols * per) * size) = make_uint4(0, 0, 0, 0);
+  constexpr int kPer = F32 ? 4 : 8, kSize = F32 ? 4 : 2;  // elements of 16 bytes, bytes of one
+  const int cols = x.jn / kPer, rows = min(128, sh.I - i0);
+  char* out = static_cast<char*>(a.out) + (((size_t)x.e * sh.I + i0) * sh.J + x.j0) * kSize;
+  for (int v = threadIdx.x - 128; v < rows * cols; v += kDrainWarps * 32)
+    *reinterpret_cast<uint4*>(out + ((size_t)(v / cols) * sh.J + v % cols * kPer) * kSize) = make_uint4(0, 0, 0, 0);
 }
 
 template <Op OP, typename T, bool F32, bool ACT, bool MX, int CG>
@@ -339,7 +367,8 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
   // Columns of B that this CTA loads for a tile: its half of jn, in copies of
   // 32 rows (K-major) or 64 columns (MN-major).
   auto half_cols = [&](const Tile& x) {
-    return (x.jn + kStepJ<MX> - 1) / kStepJ<MX> * kStepJ<MX> / CG;
+    const int unit = OP == kDw && sh.whole ? 64 * CG : kStepJ<MX>;
+    return (x.jn + unit - 1) / unit * unit / CG;
   };
 
   if (warp == 0) {
@@ -350,9 +379,9 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       const Tile x = tile_at<OP, MX, CG>(sh, s_begin, s_tile, a.G, t);
       const int i_cta = x.i0 + (int)rank * 128;
       const int jh = half_cols(x), jb = x.j0 + (int)rank * jh;
-      constexpr int kBox = B_MN ? 64 : 128;
-      const int nbox = (jh + kBox - 1) / kBox;
-      const uint32_t bytes = kABytes + nbox * (kBox * 128);
+      const int box = B_MN && !sh.whole ? 64 : 128;  // columns of one copy
+      const int nbox = (jh + box - 1) / box;
+      const uint32_t bytes = kABytes + nbox * (box * 128);
       for (int kb = 0; kb < x.nkb; ++kb) {
         if (lap > 0 && !(ok = wait(&bars.empty[s], (lap & 1) ^ 1, 1))) break;
         if (elect_one()) {
@@ -375,17 +404,27 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
           } else if constexpr (OP == kForward) {
             tma_load3<CG>(sa, &map_a, k0, i_cta, x.e, bar);
           } else if constexpr (OP == kDx) {
-            tma_load3<CG>(sa, &map_a, i_cta, k0, x.e, bar);
-            tma_load3<CG>(sa + 8192, &map_a, i_cta + 64, k0, x.e, bar);
+            if (sh.whole) {
+              tma_load4<CG>(sa, &map_a, 0, k0, i_cta / 64, x.e, bar);
+            } else {
+              tma_load3<CG>(sa, &map_a, i_cta, k0, x.e, bar);
+              tma_load3<CG>(sa + 8192, &map_a, i_cta + 64, k0, x.e, bar);
+            }
           } else {
-            tma_load2<CG>(sa, &map_a, i_cta, x.begin + k0, bar);
-            tma_load2<CG>(sa + 8192, &map_a, i_cta + 64, x.begin + k0, bar);
+            if (sh.whole) {
+              tma_load3<CG>(sa, &map_a, 0, x.begin + k0, i_cta / 64, bar);
+            } else {
+              tma_load2<CG>(sa, &map_a, i_cta, x.begin + k0, bar);
+              tma_load2<CG>(sa + 8192, &map_a, i_cta + 64, x.begin + k0, bar);
+            }
           }
-          for (int b = 0; b < nbox; ++b) {
-            if constexpr (B_MN)
+          if constexpr (!B_MN) {
+            tma_load2<CG>(sb, &map_b, k0, x.begin + jb, bar);
+          } else if (sh.whole) {
+            tma_load3<CG>(sb, &map_b, 0, x.begin + k0, jb / 64, bar);
+          } else {
+            for (int b = 0; b < nbox; ++b)
               tma_load2<CG>(sb + b * 8192, &map_b, jb + b * 64, x.begin + k0, bar);
-            else
-              tma_load2<CG>(sb + b * 16384, &map_b, k0, x.begin + jb + b * 128, bar);
           }
         }
         __syncwarp();
@@ -590,7 +629,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (CG == 2) arrive_cluster(leader_addr(smem_u32(&bars.tempty[b])));
+        if (CG == 2) arrive_cluster_relaxed(leader_addr(smem_u32(&bars.tempty[b])));
         else async::mbar_arrive(&bars.tempty[b]);
       }
     }
@@ -659,23 +698,43 @@ cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
     if (!make_map(&ma, a.w, type, 3, d, st, b)) return cudaErrorUnknown;
     return launch_t<kForward, T, false, false, false, CG>(a, sh, ma, mb, s);
   }
-  sh.I = a.K;
-  sh.tiles_i = (a.K + TI - 1) / TI;
   if (op == kDx) {
+    sh.I = a.K;
+    sh.tiles_i = (a.K + TI - 1) / TI;
     sh.KK = a.N;
-    const uint64_t d[] = {K, N, G}, st[] = {2 * K, 2 * N * K}, db[] = {N, R}, sb[] = {2 * N};
-    const uint32_t b[] = {64, 64, 1}, bb[] = {64, 128};
-    if (!make_map(&ma, a.w, type, 3, d, st, b) || !make_map(&mb, a.x, type, 2, db, sb, bb))
-      return cudaErrorUnknown;
+    sh.whole = K % 64 == 0;
+    const uint64_t db[] = {N, R}, sb[] = {2 * N};
+    const uint32_t bb[] = {64, 128};
+    if (!make_map(&mb, a.x, type, 2, db, sb, bb)) return cudaErrorUnknown;
+    if (sh.whole) {
+      const uint64_t d[] = {64, N, K / 64, G}, st[] = {2 * K, 128, 2 * N * K};
+      const uint32_t b[] = {64, 64, 2, 1};
+      if (!make_map(&ma, a.w, type, 4, d, st, b)) return cudaErrorUnknown;
+    } else {
+      const uint64_t d[] = {K, N, G}, st[] = {2 * K, 2 * N * K};
+      const uint32_t b[] = {64, 64, 1};
+      if (!make_map(&ma, a.w, type, 3, d, st, b)) return cudaErrorUnknown;
+    }
     return a.pre_in ? launch_t<kDx, T, false, true, false, CG>(a, sh, ma, mb, s)
                     : launch_t<kDx, T, false, false, false, CG>(a, sh, ma, mb, s);
   }
-  sh.J = a.N;
-  sh.tiles_j = (a.N + kNT<false> - 1) / kNT<false>;
-  const uint64_t d[] = {K, R}, st[] = {2 * K}, db[] = {N, R}, sb[] = {2 * N};
-  const uint32_t b[] = {64, 64};
-  if (!make_map(&ma, a.x, type, 2, d, st, b) || !make_map(&mb, a.w, type, 2, db, sb, b))
-    return cudaErrorUnknown;
+  sh.I = a.N;
+  sh.J = a.K;
+  sh.tiles_i = (a.N + TI - 1) / TI;
+  sh.tiles_j = (a.K + kNT<false> - 1) / kNT<false>;
+  sh.sectors = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
+  sh.whole = K % 64 == 0 && N % 64 == 0;
+  if (sh.whole) {
+    const uint64_t d[] = {64, R, N / 64}, st[] = {2 * N, 128}, db[] = {64, R, K / 64}, sb[] = {2 * K, 128};
+    const uint32_t b[] = {64, 64, 2};
+    if (!make_map(&ma, a.w, type, 3, d, st, b) || !make_map(&mb, a.x, type, 3, db, sb, b))
+      return cudaErrorUnknown;
+  } else {
+    const uint64_t d[] = {N, R}, st[] = {2 * N}, db[] = {K, R}, sb[] = {2 * K};
+    const uint32_t b[] = {64, 64};
+    if (!make_map(&ma, a.w, type, 2, d, st, b) || !make_map(&mb, a.x, type, 2, db, sb, b))
+      return cudaErrorUnknown;
+  }
   return a.out_dtype == 2 ? launch_t<kDw, T, true, false, false, CG>(a, sh, ma, mb, s)
                           : launch_t<kDw, T, false, false, false, CG>(a, sh, ma, mb, s);
 }

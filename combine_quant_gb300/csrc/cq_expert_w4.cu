@@ -371,7 +371,7 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     }
   } else if (warp < kMulWarps + kSumWarps + kScaleWarps) {
     // ---- scales: a thread takes rows r and r + 64, kAhead stages ahead ----
-    constexpr int kAhead = G32 ? 2 : 4;
+    constexpr int kAhead = (G32 ? 2 : 4) / (ZEROS ? 2 : 1);
     constexpr int kPer = (St::kRows + 63) / 64, kW = St::kGroups / 2;  // rows; words of a row
     const uint16_t* scales = static_cast<const uint16_t*>(a.scales4);
     const int per_cta = n_tiles > (int)blockIdx.x ? (n_tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;

@@ -45,6 +45,12 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// The same for a barrier that passes no memory on: a release would first wait
+// for the thread's global stores.
+__device__ __forceinline__ void arrive_cluster_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // Tiled copies global -> this CTA's shared memory, completing on `bar` (of
 // this CTA or, with CG 2, of the leader).
 template <int CG>
