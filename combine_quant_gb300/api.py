@@ -487,11 +487,6 @@ def _arg(t, name, dtype, shape, dev: torch.device):
     return t.data_ptr()
 
 
-def _required(t, name):
-    if t is None:
-        raise ValueError(f"{name} is required")
-
-
 def _group_rows(p: _ExpertPlan, group_rows: torch.Tensor) -> torch.device:
     """Checks the counts; returns the device that the other tensors must be on."""
     _need(group_rows, "group_rows", torch.int64)
@@ -526,13 +521,13 @@ def expert_matmul(cfg: ExpertConfig, x: torch.Tensor, w: torch.Tensor, group_row
     [rows, 2n] receives them). `group_rows` is dispatch's expert_token_nums."""
     p = _expert_plan(cfg)
     dev = _group_rows(p, group_rows)
-    _required(x, "x")
-    _required(w, "w")
+    if x is None or w is None:
+        raise ValueError("x and w are required")
     px, pw = _arg(x, "x", p.dtype, p.x, dev), _arg(w, "w", p.dtype, p.w, dev)
     pxs = pws = None
     if p.mx:
-        _required(x_scales, "x_scales")
-        _required(w_scales, "w_scales")
+        if x_scales is None or w_scales is None:
+            raise ValueError("x_scales and w_scales are required with mx types")
         pxs = _arg(x_scales, "x_scales", torch.uint8, p.x_scales, dev)
         pws = _arg(w_scales, "w_scales", torch.uint8, p.w_scales, dev)
     elif x_scales is not None or w_scales is not None:
@@ -553,8 +548,8 @@ def expert_matmul_dx(cfg: ExpertConfig, dy: torch.Tensor, w: torch.Tensor,
     with `pre` [rows, 2k] (the input was SwiGLU of pre) the gradient of pre."""
     p = _expert_plan(cfg)
     dev = _group_rows(p, group_rows)
-    _required(dy, "dy")
-    _required(w, "w")
+    if dy is None or w is None:
+        raise ValueError("dy and w are required")
     pdy, pw = _arg(dy, "dy", p.dtype, p.dy, dev), _arg(w, "w", p.dtype, p.w, dev)
     ppre = _arg(pre, "pre", p.dtype, p.pre_k, dev)
     shape = p.x if pre is None else p.pre_k
@@ -571,8 +566,8 @@ def expert_matmul_dw(cfg: ExpertConfig, dy: torch.Tensor, x: torch.Tensor,
     config's out_dtype: the token type (default) or f32."""
     p = _expert_plan(cfg)
     dev = _group_rows(p, group_rows)
-    _required(dy, "dy")
-    _required(x, "x")
+    if dy is None or x is None:
+        raise ValueError("dy and x are required")
     pdy, px = _arg(dy, "dy", p.dtype, p.dy, dev), _arg(x, "x", p.dtype, p.x, dev)
     if dw is None:
         dw = torch.empty(p.w, dtype=p.result, device=dev)
@@ -590,9 +585,8 @@ def expert_matmul_w4(cfg: ExpertConfig, x: torch.Tensor, codes: torch.Tensor,
     [G, n or 2n, k/group]."""
     p = _expert_plan(cfg)
     dev = _group_rows(p, group_rows)
-    _required(x, "x")
-    _required(codes, "codes")
-    _required(scales, "scales")
+    if x is None or codes is None or scales is None:
+        raise ValueError("x, codes and scales are required")
     px = _arg(x, "x", p.dtype, p.x, dev)
     pc = _arg(codes, "codes", torch.uint8, p.codes, dev)
     ps = _arg(scales, "scales", p.dtype, p.groups, dev)

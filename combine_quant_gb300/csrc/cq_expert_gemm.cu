@@ -340,6 +340,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     async::mbar_fence_init();
   }
   if (warp == 1) tmem_alloc<CG>(&bars.tmem, kTmemCols);
+  griddep_launch_dependents();  // its CTAs do the above while ours still work
   griddep_wait();
   const bool bad = group_scan<kThreads<MX>>(a, s_begin, s_tile, [&](int rows) {
     return OP == kDw ? sh.tiles_i * sh.tiles_j : sh.tiles_i * ((rows + NT - 1) / NT);

@@ -20,6 +20,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cq_expert.cuh"
 #include "cq_tensor.cuh"
@@ -69,12 +70,13 @@ __device__ __forceinline__ Tile tile_at(const Shape& sh, const int* s_begin, con
   x.e = expert_of(s_tile, G, t);
   x.begin = s_begin[x.e];
   const int rows = s_begin[x.e + 1] - x.begin;
-  const int parts = (rows + 8 * NTMAX - 1) / (8 * NTMAX);
-  const int step = ((rows + parts - 1) / parts + 7) / 8 * 8;
-  const int l = t - s_tile[x.e];
-  x.j0 = l % parts * step;
-  x.jn = min(step, rows - x.j0);
-  x.o0 = l / parts * (ACT ? 32 * MTW : 64 * MTW);
+  // Whole parts and a rest (a rest of up to 8 tokens costs less than equal parts would).
+  // The parts of one set of weight rows lie tiles_n apart: in flight together, so
+  // the second finds the codes in L2, and spread over the CTAs.
+  const int l = t - s_tile[x.e], part = l / sh.tiles_n;
+  x.j0 = part * (8 * NTMAX);
+  x.jn = min(8 * NTMAX, rows - x.j0);
+  x.o0 = (l - part * sh.tiles_n) * (ACT ? 32 * MTW : 64 * MTW);
   x.nt = (x.jn + 7) / 8;
   return x;
 }
@@ -132,55 +134,60 @@ __device__ __forceinline__ void multiply(float (&acc)[MTW][NTMAX][4], const uint
                                          const uint8_t* sw1, const uint8_t* sx, const float* sum,
                                          const float* scale, const float* zero) {
   constexpr bool kBf16 = T::kBf16;
-  constexpr int kSpans = G32 ? 2 : 1;
   constexpr int kSpan = 64 * MTW;  // floats from one group's scales to the next
-  uint4 b[2][NT];
-  float2 c[kSpans][NT];
+  // H blocks of 32 of k under one scale, from block h0.
+  auto span = [&](auto first, auto blocks) {
+    constexpr int h0 = decltype(first)::value, H = decltype(blocks)::value, p = G32 ? h0 : 0;
+    uint4 b[H][NT];
+    float2 c[NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) b[h][n] = *reinterpret_cast<const uint4*>(sx + (h * NT + n) * 512);
+      for (int h = 0; h < H; ++h) b[h][n] = *reinterpret_cast<const uint4*>(sx + ((h0 + h) * NT + n) * 512);
+      c[n] = *reinterpret_cast<const float2*>(sum + p * 8 * NTMAX + 8 * n);
+    }
 #pragma unroll
-    for (int p = 0; p < kSpans; ++p)
-      c[p][n] = *reinterpret_cast<const float2*>(sum + p * 8 * NTMAX + 8 * n);
-  }
+    for (int m = 0; m < MTW; ++m) {
+      float d[NT][4];
 #pragma unroll
-  for (int m = 0; m < MTW; ++m) {
-    float d[NT][4];
+      for (int h = 0; h < H; ++h) {
+        const uint8_t* at = (h0 + h ? sw1 : sw0) + 2048 * m;
+        const uint32_t w0 = *reinterpret_cast<const uint32_t*>(at);
+        const uint32_t w1 = *reinterpret_cast<const uint32_t*>(at + 1024);
+        const uint32_t a0[4] = {codes2<kBf16, 0>(w0), codes2<kBf16, 0>(w1), codes2<kBf16, 1>(w0), codes2<kBf16, 1>(w1)};
+        const uint32_t a1[4] = {codes2<kBf16, 2>(w0), codes2<kBf16, 2>(w1), codes2<kBf16, 3>(w0), codes2<kBf16, 3>(w1)};
+        if (h == 0) {
+          float2 o = make_float2(1.f, 1.f);
+          if constexpr (ZEROS) o = *reinterpret_cast<const float2*>(zero + p * kSpan + 2 * m);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int p = G32 ? h : 0;
-      const uint8_t* at = (h ? sw1 : sw0) + 2048 * m;
-      const uint32_t w0 = *reinterpret_cast<const uint32_t*>(at);
-      const uint32_t w1 = *reinterpret_cast<const uint32_t*>(at + 1024);
-      const uint32_t a0[4] = {codes2<kBf16, 0>(w0), codes2<kBf16, 0>(w1), codes2<kBf16, 1>(w0), codes2<kBf16, 1>(w1)};
-      const uint32_t a1[4] = {codes2<kBf16, 2>(w0), codes2<kBf16, 2>(w1), codes2<kBf16, 3>(w0), codes2<kBf16, 3>(w1)};
-      if (G32 || h == 0) {
-        float2 o = make_float2(1.f, 1.f);
-        if constexpr (ZEROS) o = *reinterpret_cast<const float2*>(zero + p * kSpan + 2 * m);
+          for (int n = 0; n < NT; ++n)
+            mma<kBf16>(d[n], a0, b[h][n].x, b[h][n].y, o.x * c[n].x, o.x * c[n].y, o.y * c[n].x, o.y * c[n].y);
+        } else {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          mma<kBf16>(d[n], a0, b[h][n].x, b[h][n].y, o.x * c[p][n].x, o.x * c[p][n].y,
-                     o.y * c[p][n].x, o.y * c[p][n].y);
-      } else {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          mma<kBf16>(d[n], a0, b[h][n].x, b[h][n].y, d[n][0], d[n][1], d[n][2], d[n][3]);
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        mma<kBf16>(d[n], a1, b[h][n].z, b[h][n].w, d[n][0], d[n][1], d[n][2], d[n][3]);
-      if (G32 || h == 1) {
-        const float2 f = *reinterpret_cast<const float2*>(scale + p * kSpan + 2 * m);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          acc[m][n][0] = fmaf(f.x, d[n][0], acc[m][n][0]);
-          acc[m][n][1] = fmaf(f.x, d[n][1], acc[m][n][1]);
-          acc[m][n][2] = fmaf(f.y, d[n][2], acc[m][n][2]);
-          acc[m][n][3] = fmaf(f.y, d[n][3], acc[m][n][3]);
+          for (int n = 0; n < NT; ++n)
+            mma<kBf16>(d[n], a0, b[h][n].x, b[h][n].y, d[n][0], d[n][1], d[n][2], d[n][3]);
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          mma<kBf16>(d[n], a1, b[h][n].z, b[h][n].w, d[n][0], d[n][1], d[n][2], d[n][3]);
+      }
+      const float2 f = *reinterpret_cast<const float2*>(scale + p * kSpan + 2 * m);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        acc[m][n][0] = fmaf(f.x, d[n][0], acc[m][n][0]);
+        acc[m][n][1] = fmaf(f.x, d[n][1], acc[m][n][1]);
+        acc[m][n][2] = fmaf(f.y, d[n][2], acc[m][n][2]);
+        acc[m][n][3] = fmaf(f.y, d[n][3], acc[m][n][3]);
       }
     }
+  };
+  using std::integral_constant;
+  if constexpr (G32) {
+    span(integral_constant<int, 0>{}, integral_constant<int, 1>{});
+    asm volatile("" ::: "memory");  // the second block's loads stay behind: 80 registers
+    span(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+  } else {
+    span(integral_constant<int, 0>{}, integral_constant<int, 2>{});
   }
 }
 
@@ -199,17 +206,18 @@ __device__ __forceinline__ bool multiply_tile(float (&acc)[MTW][NTMAX][4], Bars&
   for (int left = K - kw * 64; left + kw * 64 > 0; left -= 512) {
     if (!mbar_wait(&bars.ready[s], lap & 1)) return false;
     const uint8_t* base = ring + s * St::kBytes;
+    auto chunk = [&](int c) {
+      const uint8_t* scale = base + at.scale + c * at.scale_next;
+      multiply<T, MTW, NT, NTMAX, ZEROS, G32>(
+          acc, base + c * St::kChunk + at.w, base + c * St::kChunk + (at.w ^ 16),
+          base + at_x + c * (8 * 512 * NT),
+          reinterpret_cast<const float*>(base + at.sum + c * (4 * St::kSpans * 8 * NTMAX * 4)),
+          reinterpret_cast<const float*>(scale),
+          reinterpret_cast<const float*>(scale + St::kZero - St::kScale));
+    };
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      if (left > 256 * c) {
-        const uint8_t* scale = base + at.scale + c * at.scale_next;
-        multiply<T, MTW, NT, NTMAX, ZEROS, G32>(
-            acc, base + c * St::kChunk + at.w, base + c * St::kChunk + (at.w ^ 16),
-            base + at_x + c * (8 * 512 * NT),
-            reinterpret_cast<const float*>(base + at.sum + c * (4 * St::kSpans * 8 * NTMAX * 4)),
-            reinterpret_cast<const float*>(scale),
-            reinterpret_cast<const float*>(scale + St::kZero - St::kScale));
-      }
+      if (left > 256 * c) chunk(c);
     release_slot(&bars.empty[s]);
     if (++s == (uint32_t)S) s = 0, ++lap;
   }
@@ -252,6 +260,7 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     }
     async::mbar_fence_init();
   }
+  griddep_launch_dependents();
   griddep_wait();
   const bool bad = group_scan<kThreads>(a, s_begin, s_tile, [&](int rows) {
     return sh.tiles_n * ((rows + 8 * NTMAX - 1) / (8 * NTMAX));
@@ -338,27 +347,39 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       for (int st = 0; st < n_stages; ++st) {
         if (!(ok = wait(&bars.full[s], lap & 1))) break;
         uint8_t* base = ring + s * St::kBytes;
+        for (int n = 0; n < x.nt; ++n) {
+          // blocks of 32 past k are zeros, codes and x: no harm in summing them
+          uint4 w[2][2];
+          uint8_t* at = base + St::kX + (kw * 2 * x.nt + n) * 512 + g * 64 + ((q ^ ((g >> 1) & 3)) << 4);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int k = c * 256 + kw * 64;
-          if (st * 512 + k >= a.K) continue;
-          float* sum = reinterpret_cast<float*>(base + St::kSum) + (c * 4 + kw) * (St::kSpans * 8 * NTMAX) + 2 * q;
-          for (int n = 0; n < x.nt; ++n) {
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              w[c][h] = *reinterpret_cast<const uint4*>(at + (8 * c + h) * x.nt * 512);
+          float v[2][2][4];
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              uint4* at = reinterpret_cast<uint4*>(base + St::kX + ((k / 32 + h) * x.nt + n) * 512 + g * 64 +
-                                                   ((q ^ ((g >> 1) & 3)) << 4));
-              const uint4 w = *at;
-              *at = make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632),
-                               __byte_perm(w.y, w.w, 0x5410), __byte_perm(w.y, w.w, 0x7632));
-              mma<T::kBf16>(v, ones, w.x, w.y, v[0], v[1], v[2], v[3]);
-              mma<T::kBf16>(v, ones, w.z, w.w, v[0], v[1], v[2], v[3]);
-              if (G32 || h == 1) {
-                const float f = ZEROS ? 1.f : -(kOff + 8.f);
-                if (g == 0)
-                  *reinterpret_cast<float2*>(sum + (G32 ? h : 0) * 8 * NTMAX + 8 * n) = make_float2(f * v[0], f * v[1]);
-                v[0] = v[1] = v[2] = v[3] = 0.f;
+              const uint4 u = w[c][h];
+              *reinterpret_cast<uint4*>(at + (8 * c + h) * x.nt * 512) =
+                  make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632),
+                             __byte_perm(u.y, u.w, 0x5410), __byte_perm(u.y, u.w, 0x7632));
+              mma<T::kBf16>(v[c][h], ones, u.x, u.y, 0.f, 0.f, 0.f, 0.f);
+              mma<T::kBf16>(v[c][h], ones, u.z, u.w, v[c][h][0], v[c][h][1], v[c][h][2], v[c][h][3]);
+            }
+          if (g == 0) {
+            const float f = ZEROS ? 1.f : -(kOff + 8.f);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float* sum = reinterpret_cast<float*>(base + St::kSum) +
+                           (c * 4 + kw) * (St::kSpans * 8 * NTMAX) + 2 * q + 8 * n;
+              if constexpr (G32) {
+                *reinterpret_cast<float2*>(sum) = make_float2(f * v[c][0][0], f * v[c][0][1]);
+                *reinterpret_cast<float2*>(sum + 8 * NTMAX) = make_float2(f * v[c][1][0], f * v[c][1][1]);
+              } else {
+                *reinterpret_cast<float2*>(sum) =
+                    make_float2(f * (v[c][0][0] + v[c][1][0]), f * (v[c][0][1] + v[c][1][1]));
               }
             }
           }
