@@ -72,7 +72,7 @@ struct Shape {
 
 struct Bars {
   uint64_t full[8], empty[8], tail[8], tail_full[8];
-  uint64_t sfull[4], sempty[4];  // mx: scales
+  uint64_t swritten[4], sfull[4], sempty[4];  // mx: scales written, visible to the copies, used
   uint64_t tfull[2], tempty[2];
   uint32_t tmem;
 };
@@ -330,7 +330,8 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       mbar_init(&bars.tail_full[s], CG);
     }
     for (int s = 0; s < kScaleRing; ++s) {
-      mbar_init(&bars.sfull[s], kScaleWarps * CG);
+      mbar_init(&bars.swritten[s], kScaleWarps);
+      mbar_init(&bars.sfull[s], CG);
       mbar_init(&bars.sempty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -447,7 +448,25 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     const uint64_t da = desc_at(desc_base(A_MN ? 8192 : 16), smem_u32(ring));
     const uint64_t db = desc_at(desc_base(B_MN ? 8192 : 16), smem_u32(ring) + kABytes);
     uint32_t s = 0, lap = 0, buf = 0, tail_uses[S] = {};
-    uint32_t se = 0, se_lap = 0, sf_set = 0;  // mx: entry of scales, TMEM columns of them
+    // mx: entry of scales; set of 12 TMEM columns (A then B) to fill, to use
+    uint32_t se = 0, se_lap = 0, sf_fill = 0, sf_use = 0;
+    auto scales_in = [&](int kb, int nkb, bool wide) {
+      if ((kb & 3) == 0 && !wait(&bars.sfull[se], se_lap & 1, 1, true)) return false;
+      const bool last = (kb & 3) == 3 || kb == nkb - 1;
+      fence_after();
+      if (elect_one()) {
+        const uint32_t sf = tmem + 2 * NT + 12 * sf_fill;
+        const uint64_t ds = desc_scales(smem_u32(s_sf) + (se * 4 + (kb & 3)) * kScaleBytes);
+        copy_scales<CG>(sf, ds);
+        copy_scales<CG>(sf + 4, ds + (512 >> 4));
+        if (wide) copy_scales<CG>(sf + 8, ds + (1024 >> 4));
+        if (last) commit<CG>(smem_u32(&bars.sempty[se]));
+      }
+      __syncwarp();
+      sf_fill ^= 1;
+      if (last && ++se == kScaleRing) se = 0, ++se_lap;
+      return true;
+    };
     bool ok = true;
     for (int t = first; t < n_tiles && ok; t += step) {
       const Tile x = tile_at<OP, MX, CG>(sh, s_begin, s_tile, a.G, t);
@@ -468,18 +487,16 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
             if (q == s) use_t = tail_uses[q]++;
           if (!(ok = wait(&bars.tail_full[s], use_t & 1, 1, true))) break;
         }
-        if (MX && (kb & 3) == 0 && !(ok = wait(&bars.sfull[se], se_lap & 1, 1, true))) break;
+        // mx: the next stage's scales go into the other set of TMEM columns ahead of
+        // this stage's products, which then need not wait for a copy
+        if (MX && kb == 0 && !(ok = scales_in(0, x.nkb, half_cols(x) * CG > 128))) break;
+        if (MX && kb + 1 < x.nkb && !(ok = scales_in(kb + 1, x.nkb, half_cols(x) * CG > 128))) break;
         fence_after();
         if (elect_one()) {
           const uint64_t ad = da + s * (SB >> 4), bd = db + s * (SB >> 4);
           const int left = x.kk - kb * KB;
           if constexpr (MX) {
-            // scales of this stage, A then B, in one of two sets of 12 columns
-            const uint32_t sf = tmem + 2 * NT + 12 * sf_set;
-            const uint64_t ds = desc_scales(smem_u32(s_sf) + (se * 4 + (kb & 3)) * kScaleBytes);
-            copy_scales<CG>(sf, ds);
-            copy_scales<CG>(sf + 4, ds + (512 >> 4));
-            if (half_cols(x) * CG > 128) copy_scales<CG>(sf + 8, ds + (1024 >> 4));
+            const uint32_t sf = tmem + 2 * NT + 12 * sf_use;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               if (32 * q < left)
@@ -494,14 +511,10 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
               mma_f16<CG>(d, ad + q * ka, bd + q * kbs, idesc, kb > 0 || q > 0);
           }
           commit<CG>(smem_u32(&bars.empty[s]));
-          if (MX && ((kb & 3) == 3 || kb == x.nkb - 1)) commit<CG>(smem_u32(&bars.sempty[se]));
           if (kb == x.nkb - 1) commit<CG>(smem_u32(&bars.tfull[b]));
         }
         __syncwarp();
-        if constexpr (MX) {
-          sf_set ^= 1;
-          if (((kb & 3) == 3 || kb == x.nkb - 1) && ++se == kScaleRing) se = 0, ++se_lap;
-        }
+        sf_use ^= 1;
         if (++s == S) s = 0, ++lap;
       }
     }
@@ -537,75 +550,97 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     // ---- scales: one word (4 blocks of 32) a row and stage ----
     // Line r % 32 of a 512-byte atom holds the words of rows r % 32 + 0, 32, 64,
     // 96. A warp takes three of the twelve sets of 32 rows (four of A, eight of
-    // B), four stages at a time: 16 bytes of a row per load, one fence and one
-    // arrival for four stages.
+    // B), four stages at a time: 16 bytes of a row per load, kAhead of them in
+    // flight, across tiles. The fence that the tensor copies need would wait for
+    // those loads, so warp 3 executes it, after these warps' arrivals.
+    constexpr int kAhead = 3;
     const int w = warp - 4 - kDrainWarps;
-    uint32_t s = 0, lap = 0;
-    bool ok = true;
-    const int blocks = sh.KK / 32;
+    const int blocks = sh.KK / 32, quads = (sh.KK + 511) / 512;
     const bool whole = a.SC % 16 == 0 && a.SC == blocks;  // 16-byte pieces, no pad column
-    for (int t = first; t < n_tiles && ok; t += step) {
-      const Tile x = tile_at<OP, MX, CG>(sh, s_begin, s_tile, a.G, t);
-      const uint8_t* rows[3];  // scale rows, NULL where there is none
-#pragma unroll
-      for (int b = 0; b < 3; ++b) {
-        const int set = w * 3 + b;
-        rows[b] = nullptr;
-        if (set < 4) {
-          int row = x.i0 + (int)rank * 128 + 32 * set + lane;  // of the tile's weight rows
-          bool in = row < sh.I;
-          if (ACT) {
-            const int o = row / 32 * 16 + (lane & 15);
-            in = o < sh.n_out;
-            row = o + (lane >= 16 ? sh.n_out : 0);
-          }
-          if (in) rows[b] = a.w_scales + ((size_t)x.e * a.N + row) * a.SC;
-        } else {
-          const int j = 32 * (set - 4) + lane;
-          if (j < x.jn) rows[b] = a.x_scales + (size_t)(x.begin + x.j0 + j) * a.SC;
-        }
-      }
-      auto fetch = [&](int kb, uint4 (&v)[3]) {
+    const uint8_t* rows[3];                               // scale rows, NULL where there is none
+    int t_load = first, q_load = 0;
+    auto load = [&](uint4 (&v)[3]) {
+      if (t_load >= n_tiles) return;
+      if (q_load == 0) {
+        const Tile x = tile_at<OP, MX, CG>(sh, s_begin, s_tile, a.G, t_load);
 #pragma unroll
         for (int b = 0; b < 3; ++b) {
-          v[b] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
-          if (!rows[b]) continue;
-          if (whole) {
-            if (kb * 4 < blocks) v[b] = __ldg(reinterpret_cast<const uint4*>(rows[b] + kb * 4));
-          } else {
-            uint32_t q[8];
-#pragma unroll
-            for (int h = 0; h < 8; ++h) {
-              const int at = kb * 4 + 2 * h;  // SC is even: a pair is inside or outside
-              q[h] = at < blocks ? __ldg(reinterpret_cast<const uint16_t*>(rows[b] + at)) : 0x7f7fu;
-              if (at + 1 == blocks) q[h] = (q[h] & 0xffu) | 0x7f00u;  // the pad column
+          const int set = w * 3 + b;
+          rows[b] = nullptr;
+          if (set < 4) {
+            int row = x.i0 + (int)rank * 128 + 32 * set + lane;  // of the tile's weight rows
+            bool in = row < sh.I;
+            if (ACT) {
+              const int o = row / 32 * 16 + (lane & 15);
+              in = o < sh.n_out;
+              row = o + (lane >= 16 ? sh.n_out : 0);
             }
-            v[b] = make_uint4(q[0] | q[1] << 16, q[2] | q[3] << 16, q[4] | q[5] << 16, q[6] | q[7] << 16);
+            if (in) rows[b] = a.w_scales + ((size_t)x.e * a.N + row) * a.SC;
+          } else {
+            const int j = 32 * (set - 4) + lane;
+            if (j < x.jn) rows[b] = a.x_scales + (size_t)(x.begin + x.j0 + j) * a.SC;
           }
         }
-      };
-      uint4 v[3];
-      fetch(0, v);
-      for (int kb = 0; kb < x.nkb; kb += 4) {
+      }
+#pragma unroll
+      for (int b = 0; b < 3; ++b) {
+        v[b] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+        if (!rows[b]) continue;
+        if (whole) {
+          v[b] = __ldg(reinterpret_cast<const uint4*>(rows[b] + q_load * 16));
+        } else {
+          uint32_t p[8];
+#pragma unroll
+          for (int h = 0; h < 8; ++h) {
+            const int at = q_load * 16 + 2 * h;  // SC is even: a pair is inside or outside
+            p[h] = at < blocks ? __ldg(reinterpret_cast<const uint16_t*>(rows[b] + at)) : 0x7f7fu;
+            if (at + 1 == blocks) p[h] = (p[h] & 0xffu) | 0x7f00u;  // the pad column
+          }
+          v[b] = make_uint4(p[0] | p[1] << 16, p[2] | p[3] << 16, p[4] | p[5] << 16, p[6] | p[7] << 16);
+        }
+      }
+      if (++q_load == quads) q_load = 0, t_load += step;
+    };
+    uint4 v[kAhead][3];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) load(v[u]);
+    const int total = n_tiles > first ? ((n_tiles - 1 - first) / step + 1) * quads : 0;
+    uint32_t s = 0, lap = 0;
+    bool ok = true;
+    for (int i = 0; i < total && ok; i += kAhead) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (i + u >= total || !ok) break;
         if (lap > 0 && !(ok = wait(&bars.sempty[s], (lap & 1) ^ 1, 1))) break;
 #pragma unroll
         for (int b = 0; b < 3; ++b) {
           const int set = w * 3 + b;
           uint8_t* to = s_sf + s * 4 * kScaleBytes + set / 4 * 512 + lane * 16 + set % 4 * 4;
-          *reinterpret_cast<uint32_t*>(to) = v[b].x;
-          *reinterpret_cast<uint32_t*>(to + kScaleBytes) = v[b].y;
-          *reinterpret_cast<uint32_t*>(to + 2 * kScaleBytes) = v[b].z;
-          *reinterpret_cast<uint32_t*>(to + 3 * kScaleBytes) = v[b].w;
+          *reinterpret_cast<uint32_t*>(to) = v[u][b].x;
+          *reinterpret_cast<uint32_t*>(to + kScaleBytes) = v[u][b].y;
+          *reinterpret_cast<uint32_t*>(to + 2 * kScaleBytes) = v[u][b].z;
+          *reinterpret_cast<uint32_t*>(to + 3 * kScaleBytes) = v[u][b].w;
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) {
-          if (CG == 2) arrive_cluster(leader_addr(smem_u32(&bars.sfull[s])));
-          else async::mbar_arrive(&bars.sfull[s]);
-        }
+        if (lane == 0) async::mbar_arrive(&bars.swritten[s]);
         if (++s == kScaleRing) s = 0, ++lap;
-        fetch(kb + 4, v);
+        load(v[u]);
       }
+    }
+  } else if (MX && warp == 3) {
+    // ---- the scales' way from ordinary stores to the tensor copies ----
+    const int quads = (sh.KK + 511) / 512;
+    const int total = n_tiles > first ? ((n_tiles - 1 - first) / step + 1) * quads : 0;
+    uint32_t s = 0, lap = 0;
+    for (int i = 0; i < total; ++i) {
+      if (!wait(&bars.swritten[s], lap & 1, 1)) break;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2) arrive_cluster(leader_addr(smem_u32(&bars.sfull[s])));
+        else async::mbar_arrive(&bars.sfull[s]);
+      }
+      if (++s == kScaleRing) s = 0, ++lap;
     }
   } else if (warp >= 4) {
     // ---- results ----
