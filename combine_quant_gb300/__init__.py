@@ -1,10 +1,11 @@
 """combine_quant_gb300: GB300-native MoE dispatch / combine with
-pre-communication quantisation.
+pre-communication quantisation, and the experts' products between them.
 
 The compute path is libcq.so (hand-written CUDA kernels for sm_103a behind the
 C ABI declared in include/cq.h). This package is its thin Python binding:
-``api`` marshals torch tensors into the C calls; ``workloads`` draws seeded
-synthetic inputs; ``build`` compiles the library in-tree.
+``api`` marshals torch tensors into the C calls; ``weights`` prepares quantised
+expert weights; ``workloads`` draws seeded synthetic inputs; ``build`` compiles
+the library in-tree.
 """
 from .api import (Config, DispatchResult, ExpertConfig, alloc_dispatch_outputs, alloc_workspace,  # noqa: F401
                   assist_views, check_bounded_wait, combine, combine_q8, combine_quant,
@@ -19,3 +20,4 @@ from .api import (Config, DispatchResult, ExpertConfig, alloc_dispatch_outputs, 
                   expert_matmul_w4, read_expert_status)
 from ._lib import (CQ_ST_BAD_ID, CQ_ST_BAD_MASK, CQ_ST_BAD_ROWS, CQ_ST_INTERNAL, CQ_ST_TIMEOUT,  # noqa: F401
                    CqError)
+from .weights import quantize_mx, quantize_w4  # noqa: F401

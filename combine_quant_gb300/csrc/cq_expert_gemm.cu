@@ -54,12 +54,11 @@ constexpr int kABytes = 128 * 128;         // A of one stage, one CTA
 constexpr uint32_t kTmemCols = 512;
 constexpr int kBand = 8;                   // tiles along i taken together, for reuse in L2
 
-template <int CG>
-constexpr int kStageBytes = kABytes + 256 / CG * 128;
+constexpr int kStageBytes = kABytes + 128 * 128;  // B: half of up to 256 columns
 // Stages of the ring: what is left beside the results' staging, the scales and
 // the lists of 2048 experts.
-template <Op OP, bool ACT, bool MX, int CG>
-constexpr int kStages = CG == 1 ? 4 : (OP == kDx && ACT) || MX ? 5 : 6;
+template <Op OP, bool ACT, bool MX>
+constexpr int kStages = (OP == kDx && ACT) || MX ? 5 : 6;
 
 struct Shape {
   int I, J, KK;        // extents: out columns (physical A rows), dw: out rows, contraction
@@ -82,7 +81,7 @@ struct Tile {
   int e, begin, i0, j0, jn, nkb, kk;  // jn: real columns; kk: contraction length
 };
 
-template <Op OP, bool MX, int CG>
+template <Op OP, bool MX>
 __device__ __forceinline__ Tile tile_at(const Shape& sh, const int* s_begin, const int* s_tile,
                                         int G, int t) {
   constexpr int NT = kNT<MX>, SJ = kStepJ<MX>;
@@ -95,7 +94,7 @@ __device__ __forceinline__ Tile tile_at(const Shape& sh, const int* s_begin, con
   const int band = l / (kBand * nj), first_i = band * kBand;
   const int wide = min(kBand, sh.tiles_i - first_i), m = l - first_i * nj;
   const int ti = first_i + m % wide, tj = m / wide;
-  x.i0 = ti * 128 * CG;
+  x.i0 = ti * 256;
   if (OP == kDw) {
     x.kk = rows;
     x.j0 = tj * NT;
@@ -302,12 +301,12 @@ __device__ __forceinline__ void store_zeros(const Args& a, const Shape& sh, cons
     *reinterpret_cast<uint4*>(out + ((size_t)(v / cols) * sh.J + v % cols * kPer) * kSize) = make_uint4(0, 0, 0, 0);
 }
 
-template <Op OP, typename T, bool F32, bool ACT, bool MX, int CG>
+template <Op OP, typename T, bool F32, bool ACT, bool MX>
 __global__ void __launch_bounds__(kThreads<MX>, 1)
 gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
             const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b) {
-  constexpr int S = kStages<OP, ACT, MX, CG>;
-  constexpr int SB = kStageBytes<CG>;
+  constexpr int S = kStages<OP, ACT, MX>;
+  constexpr int SB = kStageBytes;
   constexpr int NT = kNT<MX>, KB = MX ? 128 : 64;  // columns; contraction of a stage
   constexpr bool A_MN = OP != kForward, B_MN = OP == kDw;
   extern __shared__ __align__(1024) uint8_t dyn[];
@@ -319,7 +318,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
   int* s_tile = s_begin + a.G + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+  const uint32_t rank = cluster_rank();
   if (threadIdx.x == 0) {
     prefetch_map(&map_a);
     prefetch_map(&map_b);
@@ -327,50 +326,45 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       mbar_init(&bars.full[s], 1);
       mbar_init(&bars.empty[s], 1);
       mbar_init(&bars.tail[s], 1);
-      mbar_init(&bars.tail_full[s], CG);
+      mbar_init(&bars.tail_full[s], 2);
     }
     for (int s = 0; s < kScaleRing; ++s) {
       mbar_init(&bars.swritten[s], kScaleWarps);
-      mbar_init(&bars.sfull[s], CG);
+      mbar_init(&bars.sfull[s], 2);
       mbar_init(&bars.sempty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars.tfull[b], 1);
-      mbar_init(&bars.tempty[b], kDrainWarps * CG);
+      mbar_init(&bars.tempty[b], kDrainWarps * 2);
     }
     async::mbar_fence_init();
   }
-  if (warp == 1) tmem_alloc<CG>(&bars.tmem, kTmemCols);
+  if (warp == 1) tmem_alloc(&bars.tmem, kTmemCols);
   griddep_launch_dependents();  // its CTAs do the above while ours still work
   griddep_wait();
   const bool bad = group_scan<kThreads<MX>>(a, s_begin, s_tile, [&](int rows) {
     return OP == kDw ? sh.tiles_i * sh.tiles_j : sh.tiles_i * ((rows + NT - 1) / NT);
   });
   if (bad && blockIdx.x == 0) atomicOr(&g_status, (uint32_t)CQ_ST_BAD_ROWS);
-  if constexpr (CG == 2) {
-    fence_before();
-    cluster_sync();
-  } else {
-    fence_before();
-    __syncthreads();
-  }
+  fence_before();
+  cluster_sync();
   fence_after();
   const uint32_t tmem = bars.tmem;
   const int n_tiles = s_tile[a.G];
-  const int first = blockIdx.x / CG, step = gridDim.x / CG;
+  const int first = blockIdx.x / 2, step = gridDim.x / 2;
   auto wait = [&](uint64_t* bar, uint32_t parity, int rounds, bool pair = false) {
     for (int r = 0; r < rounds; ++r)
-      if (CG == 2 && pair ? wait_pair(bar, parity) : mbar_wait(bar, parity)) return true;
+      if (pair ? wait_pair(bar, parity) : mbar_wait(bar, parity)) return true;
     atomicOr(&g_status, (uint32_t)CQ_ST_TIMEOUT);
     return false;
   };
-  auto lead = [&](uint64_t* bar) { return CG == 2 ? leader_addr(smem_u32(bar)) : smem_u32(bar); };
+  auto lead = [&](uint64_t* bar) { return leader_addr(smem_u32(bar)); };
 
   // Columns of B that this CTA loads for a tile: its half of jn, in copies of
   // 32 rows (K-major) or 64 columns (MN-major).
   auto half_cols = [&](const Tile& x) {
-    const int unit = OP == kDw && sh.whole ? 64 * CG : kStepJ<MX>;
-    return (x.jn + unit - 1) / unit * unit / CG;
+    const int unit = OP == kDw && sh.whole ? 128 : kStepJ<MX>;
+    return (x.jn + unit - 1) / unit * unit / 2;
   };
 
   if (warp == 0) {
@@ -378,7 +372,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     uint32_t s = 0, lap = 0;  // stage, times the ring has gone round
     bool ok = true;
     for (int t = first; t < n_tiles && ok; t += step) {
-      const Tile x = tile_at<OP, MX, CG>(sh, s_begin, s_tile, a.G, t);
+      const Tile x = tile_at<OP, MX>(sh, s_begin, s_tile, a.G, t);
       const int i_cta = x.i0 + (int)rank * 128;
       const int jh = half_cols(x), jb = x.j0 + (int)rank * jh;
       const int box = B_MN && !sh.whole ? 64 : 128;  // columns of one copy
@@ -398,35 +392,35 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
             if (rank == 0) async::mbar_arrive(&bars.full[s]);
           } else {
             bar = lead(&bars.full[s]);
-            if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], bytes * CG);
+            if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], bytes * 2);
           }
           const int k0 = kb * KB;
           if constexpr (OP == kForward && ACT) {
-            tma_load5<CG>(sa, &map_a, k0, 0, 0, i_cta / 32, x.e, bar);
+            tma_load5(sa, &map_a, k0, 0, 0, i_cta / 32, x.e, bar);
           } else if constexpr (OP == kForward) {
-            tma_load3<CG>(sa, &map_a, k0, i_cta, x.e, bar);
+            tma_load3<2>(sa, &map_a, k0, i_cta, x.e, bar);
           } else if constexpr (OP == kDx) {
             if (sh.whole) {
-              tma_load4<CG>(sa, &map_a, 0, k0, i_cta / 64, x.e, bar);
+              tma_load4<2>(sa, &map_a, 0, k0, i_cta / 64, x.e, bar);
             } else {
-              tma_load3<CG>(sa, &map_a, i_cta, k0, x.e, bar);
-              tma_load3<CG>(sa + 8192, &map_a, i_cta + 64, k0, x.e, bar);
+              tma_load3<2>(sa, &map_a, i_cta, k0, x.e, bar);
+              tma_load3<2>(sa + 8192, &map_a, i_cta + 64, k0, x.e, bar);
             }
           } else {
             if (sh.whole) {
-              tma_load3<CG>(sa, &map_a, 0, x.begin + k0, i_cta / 64, bar);
+              tma_load3<2>(sa, &map_a, 0, x.begin + k0, i_cta / 64, bar);
             } else {
-              tma_load2<CG>(sa, &map_a, i_cta, x.begin + k0, bar);
-              tma_load2<CG>(sa + 8192, &map_a, i_cta + 64, x.begin + k0, bar);
+              tma_load2(sa, &map_a, i_cta, x.begin + k0, bar);
+              tma_load2(sa + 8192, &map_a, i_cta + 64, x.begin + k0, bar);
             }
           }
           if constexpr (!B_MN) {
-            tma_load2<CG>(sb, &map_b, k0, x.begin + jb, bar);
+            tma_load2(sb, &map_b, k0, x.begin + jb, bar);
           } else if (sh.whole) {
-            tma_load3<CG>(sb, &map_b, 0, x.begin + k0, jb / 64, bar);
+            tma_load3<2>(sb, &map_b, 0, x.begin + k0, jb / 64, bar);
           } else {
             for (int b = 0; b < nbox; ++b)
-              tma_load2<CG>(sb + b * 8192, &map_b, jb + b * 64, x.begin + k0, bar);
+              tma_load2(sb + b * 8192, &map_b, jb + b * 64, x.begin + k0, bar);
           }
         }
         __syncwarp();
@@ -457,10 +451,10 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       if (elect_one()) {
         const uint32_t sf = tmem + 2 * NT + 12 * sf_fill;
         const uint64_t ds = desc_scales(smem_u32(s_sf) + (se * 4 + (kb & 3)) * kScaleBytes);
-        copy_scales<CG>(sf, ds);
-        copy_scales<CG>(sf + 4, ds + (512 >> 4));
-        if (wide) copy_scales<CG>(sf + 8, ds + (1024 >> 4));
-        if (last) commit<CG>(smem_u32(&bars.sempty[se]));
+        copy_scales(sf, ds);
+        copy_scales(sf + 4, ds + (512 >> 4));
+        if (wide) copy_scales(sf + 8, ds + (1024 >> 4));
+        if (last) commit(smem_u32(&bars.sempty[se]));
       }
       __syncwarp();
       sf_fill ^= 1;
@@ -469,15 +463,15 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     };
     bool ok = true;
     for (int t = first; t < n_tiles && ok; t += step) {
-      const Tile x = tile_at<OP, MX, CG>(sh, s_begin, s_tile, a.G, t);
+      const Tile x = tile_at<OP, MX>(sh, s_begin, s_tile, a.G, t);
       if (x.nkb == 0) continue;
       const uint32_t b = buf & 1, use = buf >> 1;
       ++buf;
       if (use > 0 && !(ok = wait(&bars.tempty[b], (use - 1) & 1, 1, true))) break;
       const uint32_t d = tmem + b * NT;
       const uint32_t idesc =
-          MX ? idesc_mx(a.w_dtype, a.x_dtype == kMxE5M2, 128 * CG, half_cols(x) * CG)
-             : idesc_f16(T::kBf16, A_MN, B_MN, 128 * CG, half_cols(x) * CG);
+          MX ? idesc_mx(a.w_dtype, a.x_dtype == kMxE5M2, 256, half_cols(x) * 2)
+             : idesc_f16(T::kBf16, A_MN, B_MN, 256, half_cols(x) * 2);
       for (int kb = 0; kb < x.nkb; ++kb) {
         if (!(ok = wait(&bars.full[s], lap & 1, 1))) break;
         if (OP == kDw && kb == x.nkb - 1 && (x.kk & 15) != 0) {
@@ -489,8 +483,8 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
         }
         // mx: the next stage's scales go into the other set of TMEM columns ahead of
         // this stage's products, which then need not wait for a copy
-        if (MX && kb == 0 && !(ok = scales_in(0, x.nkb, half_cols(x) * CG > 128))) break;
-        if (MX && kb + 1 < x.nkb && !(ok = scales_in(kb + 1, x.nkb, half_cols(x) * CG > 128))) break;
+        if (MX && kb == 0 && !(ok = scales_in(0, x.nkb, half_cols(x) * 2 > 128))) break;
+        if (MX && kb + 1 < x.nkb && !(ok = scales_in(kb + 1, x.nkb, half_cols(x) * 2 > 128))) break;
         fence_after();
         if (elect_one()) {
           const uint64_t ad = da + s * (SB >> 4), bd = db + s * (SB >> 4);
@@ -500,18 +494,18 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               if (32 * q < left)
-                mma_mx<CG>(d, ad + q * ka, bd + q * kbs, idesc_sf(idesc, q), sf, sf + 4, kb > 0 || q > 0);
+                mma_mx(d, ad + q * ka, bd + q * kbs, idesc_sf(idesc, q), sf, sf + 4, kb > 0 || q > 0);
           } else if (left > 48) {
-            mma_f16<CG>(d, ad, bd, idesc, kb > 0);
-            mma_f16<CG>(d, ad + ka, bd + kbs, idesc, true);
-            mma_f16<CG>(d, ad + 2 * ka, bd + 2 * kbs, idesc, true);
-            mma_f16<CG>(d, ad + 3 * ka, bd + 3 * kbs, idesc, true);
+            mma_f16(d, ad, bd, idesc, kb > 0);
+            mma_f16(d, ad + ka, bd + kbs, idesc, true);
+            mma_f16(d, ad + 2 * ka, bd + 2 * kbs, idesc, true);
+            mma_f16(d, ad + 3 * ka, bd + 3 * kbs, idesc, true);
           } else {
             for (int q = 0; 16 * q < left; ++q)
-              mma_f16<CG>(d, ad + q * ka, bd + q * kbs, idesc, kb > 0 || q > 0);
+              mma_f16(d, ad + q * ka, bd + q * kbs, idesc, kb > 0 || q > 0);
           }
-          commit<CG>(smem_u32(&bars.empty[s]));
-          if (kb == x.nkb - 1) commit<CG>(smem_u32(&bars.tfull[b]));
+          commit(smem_u32(&bars.empty[s]));
+          if (kb == x.nkb - 1) commit(smem_u32(&bars.tfull[b]));
         }
         __syncwarp();
         sf_use ^= 1;
@@ -523,7 +517,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     uint32_t it = 0, tail_uses[S] = {};
     bool ok = true;
     for (int t = first; t < n_tiles && ok; t += step) {
-      const Tile x = tile_at<OP, MX, CG>(sh, s_begin, s_tile, a.G, t);
+      const Tile x = tile_at<OP, MX>(sh, s_begin, s_tile, a.G, t);
       it += x.nkb;
       if (x.nkb == 0 || (x.kk & 15) == 0) continue;
       const int s = (it - 1) % S;
@@ -542,8 +536,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
-        if (CG == 2) arrive_cluster(leader_addr(smem_u32(&bars.tail_full[s])));
-        else async::mbar_arrive(&bars.tail_full[s]);
+        arrive_cluster(leader_addr(smem_u32(&bars.tail_full[s])));
       }
     }
   } else if (MX && warp >= 4 + kDrainWarps) {
@@ -562,7 +555,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     auto load = [&](uint4 (&v)[3]) {
       if (t_load >= n_tiles) return;
       if (q_load == 0) {
-        const Tile x = tile_at<OP, MX, CG>(sh, s_begin, s_tile, a.G, t_load);
+        const Tile x = tile_at<OP, MX>(sh, s_begin, s_tile, a.G, t_load);
 #pragma unroll
         for (int b = 0; b < 3; ++b) {
           const int set = w * 3 + b;
@@ -637,8 +630,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
-        if (CG == 2) arrive_cluster(leader_addr(smem_u32(&bars.sfull[s])));
-        else async::mbar_arrive(&bars.sfull[s]);
+        arrive_cluster(leader_addr(smem_u32(&bars.sfull[s])));
       }
       if (++s == kScaleRing) s = 0, ++lap;
     }
@@ -649,7 +641,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     uint32_t buf = 0;
     bool ok = true;
     for (int t = first; t < n_tiles && ok; t += step) {
-      const Tile x = tile_at<OP, MX, CG>(sh, s_begin, s_tile, a.G, t);
+      const Tile x = tile_at<OP, MX>(sh, s_begin, s_tile, a.G, t);
       const int i_cta = x.i0 + (int)rank * 128;
       if (x.nkb == 0) {
         if (i_cta < sh.I) store_zeros<F32>(a, sh, x, i_cta);
@@ -665,25 +657,23 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (CG == 2) arrive_cluster_relaxed(leader_addr(smem_u32(&bars.tempty[b])));
-        else async::mbar_arrive(&bars.tempty[b]);
+        arrive_cluster_relaxed(leader_addr(smem_u32(&bars.tempty[b])));
       }
     }
   }
   __syncwarp();
   fence_before();
-  if constexpr (CG == 2) cluster_sync();
-  else __syncthreads();
+  cluster_sync();
   fence_after();
-  if (warp == 1) tmem_free<CG>(tmem, kTmemCols);
+  if (warp == 1) tmem_free(tmem, kTmemCols);
 }
 
 // ---- host ----
-template <Op OP, typename T, bool F32, bool ACT, bool MX, int CG>
+template <Op OP, typename T, bool F32, bool ACT, bool MX>
 cudaError_t launch_t(const Args& a, const Shape& sh, const CUtensorMap& ma, const CUtensorMap& mb,
                      cudaStream_t s) {
-  constexpr auto kernel = gemm_kernel<OP, T, F32, ACT, MX, CG>;
-  const size_t smem = 1024 + (size_t)kStages<OP, ACT, MX, CG> * kStageBytes<CG> +
+  constexpr auto kernel = gemm_kernel<OP, T, F32, ACT, MX>;
+  const size_t smem = 1024 + (size_t)kStages<OP, ACT, MX> * kStageBytes +
                       kDrainWarps * kStagingBytes<OP, ACT> +
                       (MX ? kScaleRing * 4 * kScaleBytes : 0) + 8 * ((size_t)a.G + 1);
   cudaError_t e = prepare_kernel<kernel>(smem);
@@ -692,9 +682,9 @@ cudaError_t launch_t(const Args& a, const Shape& sh, const CUtensorMap& ma, cons
   if (sms <= 0) return cudaErrorUnknown;
   const int64_t most = OP == kDw ? (int64_t)a.G * sh.tiles_i * sh.tiles_j
                                  : (int64_t)sh.tiles_i * (a.R / kNT<MX> + std::min(a.G, a.R));
-  const int clusters = (int)std::min<int64_t>(sms / CG, most);
+  const int clusters = (int)std::min<int64_t>(sms / 2, most);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(clusters * CG);
+  cfg.gridDim = dim3(clusters * 2);
   cfg.blockDim = dim3(kThreads<MX>);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -702,24 +692,23 @@ cudaError_t launch_t(const Args& a, const Shape& sh, const CUtensorMap& ma, cons
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {CG, 1, 1};
+  attr[1].val.clusterDim = {2, 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = CG == 2 ? 2 : 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, a, sh, ma, mb);
 }
 
-template <typename T, int CG>
+template <typename T>
 cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
   const MapType type = T::kBf16 ? kMapBF16 : kMapF16;
   const uint64_t G = a.G, R = a.R, N = a.N, K = a.K;
-  const int TI = 128 * CG;
   CUtensorMap ma, mb;
   Shape sh = {};
   if (op == kForward) {
     sh.n_out = a.act ? a.N / 2 : a.N;
     sh.I = a.N;
     sh.KK = a.K;
-    sh.tiles_i = (a.N + TI - 1) / TI;
+    sh.tiles_i = (a.N + 255) / 256;
     const uint64_t db[] = {K, R}, sb[] = {2 * K};
     const uint32_t bb[] = {64, 128};
     if (!make_map(&mb, a.x, type, 2, db, sb, bb)) return cudaErrorUnknown;
@@ -727,16 +716,16 @@ cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
       const uint64_t n = N / 2, d[] = {K, 16, 2, n / 16, G}, st[] = {2 * K, 2 * n * K, 32 * K, 2 * N * K};
       const uint32_t b[] = {64, 16, 2, 4, 1};
       if (!make_map(&ma, a.w, type, 5, d, st, b)) return cudaErrorUnknown;
-      return launch_t<kForward, T, false, true, false, CG>(a, sh, ma, mb, s);
+      return launch_t<kForward, T, false, true, false>(a, sh, ma, mb, s);
     }
     const uint64_t d[] = {K, N, G}, st[] = {2 * K, 2 * N * K};
     const uint32_t b[] = {64, 128, 1};
     if (!make_map(&ma, a.w, type, 3, d, st, b)) return cudaErrorUnknown;
-    return launch_t<kForward, T, false, false, false, CG>(a, sh, ma, mb, s);
+    return launch_t<kForward, T, false, false, false>(a, sh, ma, mb, s);
   }
   if (op == kDx) {
     sh.I = a.K;
-    sh.tiles_i = (a.K + TI - 1) / TI;
+    sh.tiles_i = (a.K + 255) / 256;
     sh.KK = a.N;
     sh.whole = K % 64 == 0;
     const uint64_t db[] = {N, R}, sb[] = {2 * N};
@@ -751,12 +740,12 @@ cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
       const uint32_t b[] = {64, 64, 1};
       if (!make_map(&ma, a.w, type, 3, d, st, b)) return cudaErrorUnknown;
     }
-    return a.pre_in ? launch_t<kDx, T, false, true, false, CG>(a, sh, ma, mb, s)
-                    : launch_t<kDx, T, false, false, false, CG>(a, sh, ma, mb, s);
+    return a.pre_in ? launch_t<kDx, T, false, true, false>(a, sh, ma, mb, s)
+                    : launch_t<kDx, T, false, false, false>(a, sh, ma, mb, s);
   }
   sh.I = a.N;
   sh.J = a.K;
-  sh.tiles_i = (a.N + TI - 1) / TI;
+  sh.tiles_i = (a.N + 255) / 256;
   sh.tiles_j = (a.K + kNT<false> - 1) / kNT<false>;
   sh.sectors = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
   sh.whole = K % 64 == 0 && N % 64 == 0;
@@ -771,12 +760,12 @@ cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
     if (!make_map(&ma, a.w, type, 2, d, st, b) || !make_map(&mb, a.x, type, 2, db, sb, b))
       return cudaErrorUnknown;
   }
-  return a.out_dtype == 2 ? launch_t<kDw, T, true, false, false, CG>(a, sh, ma, mb, s)
-                          : launch_t<kDw, T, false, false, false, CG>(a, sh, ma, mb, s);
+  return a.out_dtype == 2 ? launch_t<kDw, T, true, false, false>(a, sh, ma, mb, s)
+                          : launch_t<kDw, T, false, false, false>(a, sh, ma, mb, s);
 }
 
 // Forward from mx fp8 operands; T is the output's type.
-template <typename T, int CG>
+template <typename T>
 cudaError_t launch_mx(const Args& a, cudaStream_t s) {
   const uint64_t G = a.G, R = a.R, N = a.N, K = a.K;
   CUtensorMap ma, mb;
@@ -784,7 +773,7 @@ cudaError_t launch_mx(const Args& a, cudaStream_t s) {
   sh.n_out = a.act ? a.N / 2 : a.N;
   sh.I = a.N;
   sh.KK = a.K;
-  sh.tiles_i = (a.N + 128 * CG - 1) / (128 * CG);
+  sh.tiles_i = (a.N + 255) / 256;
   const uint64_t db[] = {K, R}, sb[] = {K};
   const uint32_t bb[] = {128, 128};
   if (!make_map(&mb, a.x, kMapU8, 2, db, sb, bb)) return cudaErrorUnknown;
@@ -792,12 +781,12 @@ cudaError_t launch_mx(const Args& a, cudaStream_t s) {
     const uint64_t n = N / 2, d[] = {K, 16, 2, n / 16, G}, st[] = {K, n * K, 16 * K, N * K};
     const uint32_t b[] = {128, 16, 2, 4, 1};
     if (!make_map(&ma, a.w, kMapU8, 5, d, st, b)) return cudaErrorUnknown;
-    return launch_t<kForward, T, false, true, true, CG>(a, sh, ma, mb, s);
+    return launch_t<kForward, T, false, true, true>(a, sh, ma, mb, s);
   }
   const uint64_t d[] = {K, N, G}, st[] = {K, N * K};
   const uint32_t b[] = {128, 128, 1};
   if (!make_map(&ma, a.w, kMapU8, 3, d, st, b)) return cudaErrorUnknown;
-  return launch_t<kForward, T, false, false, true, CG>(a, sh, ma, mb, s);
+  return launch_t<kForward, T, false, false, true>(a, sh, ma, mb, s);
 }
 
 }  // namespace
@@ -808,9 +797,9 @@ int launch_gemm(Op op, const Args& a, cudaStream_t s) {
     if (op != kDw) return CQ_OK;
     e = cudaMemsetAsync(a.out, 0, (size_t)a.G * a.N * a.K * (a.out_dtype == 2 ? 4 : 2), s);
   } else if (a.x_dtype >= kMxE4M3) {
-    e = a.out_dtype == 1 ? launch_mx<F16, 2>(a, s) : launch_mx<BF16, 2>(a, s);
+    e = a.out_dtype == 1 ? launch_mx<F16>(a, s) : launch_mx<BF16>(a, s);
   } else {
-    e = a.x_dtype == kF16 ? launch_op<F16, 2>(op, a, s) : launch_op<BF16, 2>(op, a, s);
+    e = a.x_dtype == kF16 ? launch_op<F16>(op, a, s) : launch_op<BF16>(op, a, s);
   }
   return e == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
 }

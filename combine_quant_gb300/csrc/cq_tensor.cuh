@@ -1,7 +1,7 @@
 // cq_tensor.cuh -- fifth-generation tensor core (tcgen05) and tiled-copy
 // (cp.async.bulk.tensor) instructions used by the expert products, and the
-// descriptors that they take. CG is the number of CTAs that work on one tile
-// (cta_group::1, or the pair of cta_group::2).
+// descriptors that they take. The products run on pairs of CTAs (cta_group::2);
+// copies with CG 1 complete on a barrier of the CTA itself.
 #pragma once
 
 #include <cuda.h>
@@ -53,19 +53,12 @@ __device__ __forceinline__ void arrive_cluster_relaxed(uint32_t bar) {
 
 // Tiled copies global -> this CTA's shared memory, completing on `bar` (of
 // this CTA or, with CG 2, of the leader).
-template <int CG>
 __device__ __forceinline__ void tma_load2(uint32_t dst, const CUtensorMap* m, int x, int y,
                                           uint32_t bar) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx"
-        "::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(bar)
-        : "memory");
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx"
+      "::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(bar)
+      : "memory");
 }
 template <int CG>
 __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* m, int x, int y, int z,
@@ -98,49 +91,28 @@ __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* m, in
         "r"(u), "r"(bar)
         : "memory");
 }
-template <int CG>
 __device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap* m, int x, int y, int z,
                                           int u, int v, uint32_t bar) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z),
-        "r"(u), "r"(v), "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx"
-        "::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst), "l"(m), "r"(x), "r"(y),
-        "r"(z), "r"(u), "r"(v), "r"(bar)
-        : "memory");
+  asm volatile(
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx"
+      "::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst), "l"(m), "r"(x), "r"(y),
+      "r"(z), "r"(u), "r"(v), "r"(bar)
+      : "memory");
 }
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
 
-template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
-  if constexpr (CG == 1)
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(dst)),
-                 "r"(cols)
-                 : "memory");
-  else
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(dst)),
-                 "r"(cols)
-                 : "memory");
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(dst)),
+               "r"(cols)
+               : "memory");
 }
-template <int CG>
 __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
-  if constexpr (CG == 1) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  } else {
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-  }
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
 }
 
 __device__ __forceinline__ void fence_before() {
@@ -152,68 +124,41 @@ __device__ __forceinline__ void fence_after() {
 
 // D (TMEM, f32) = or += A B from shared memory, 16-bit operands, 16 of the
 // contraction.
-template <int CG>
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                         bool add) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
-  else
-    asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
 }
 
 // The same with fp8 operands and a power-of-two scale for each row of A and B
 // and 32 of the contraction; the scales' TMEM addresses are sa and sb.
-template <int CG>
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t sa, uint32_t sb, bool add) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.u32 p, %6, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
-        : "memory");
-  else
-    asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.u32 p, %6, 0;\n"
-        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
-        : "memory");
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.u32 p, %6, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+      : "memory");
 }
 
 // 32 lines of 16 bytes of shared memory into 4 TMEM columns, the same in each
 // quarter of the lanes (the layout of scales), in both CTAs of a pair.
-template <int CG>
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-  if constexpr (CG == 1)
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
-  else
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 
-// One arrival on `bar` (with CG 2, at the same address in both CTAs) when every
+// One arrival on `bar`, at the same address in both CTAs of the pair, when every
 // tcgen05 operation issued so far by this thread has completed.
-template <int CG>
 __device__ __forceinline__ void commit(uint32_t bar) {
-  if constexpr (CG == 1)
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     bar)
-                 : "memory");
-  else
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-        "[%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
 }
 
 // 32 columns of this warp's 32 lanes: r[c] = TMEM[lane][col + c].

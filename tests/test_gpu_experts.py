@@ -194,6 +194,38 @@ def test_mx(shape, act, types):
     assert cq.read_expert_status() == 0
 
 
+@pytest.mark.parametrize("act", [0, 1])
+@pytest.mark.parametrize("shape", [([241, 0, 1, 30], 3, 160, 2560), ([16, 200], 0, 272, 1504), ([500], 0, 64, 3584)], ids=str)
+def test_mx_long(shape, act):
+    """Several steps of scales and tiles per CTA; odd numbers of blocks have a pad column, whose value (NaN here)
+    must not count, as must those of rows that belong to nobody."""
+    counts, spare, n, k = shape
+    gen = _rng("mx long", n, k, act)
+    used = sum(counts)
+    xc, xs = _mx(gen, False, used + spare, k)
+    wc, ws = _mx(gen, False, len(counts), n * (1 + act), k)
+    xs[:, : k // 32] -= 8
+    ws[..., : k // 32] -= 8
+    xs[:, k // 32:], ws[..., k // 32:] = 255, 255
+    xs[used:] = 255
+    cfg = cq.ExpertConfig(experts=len(counts), rows=used + spare, n=n, k=k, x_dtype=2, act=act)
+    y = cq.expert_matmul(cfg, xc.to(DEV), wc.to(DEV), _counts(counts), x_scales=xs.to(DEV), w_scales=ws.to(DEV))
+    want, bound, _, _ = ref.forward(ref.mx_values(xc, xs), ref.mx_values(wc, ws), counts, act, torch.bfloat16)
+    ref.check(y[:used], want, bound, "y")
+    assert cq.read_expert_status() == 0
+
+
+def test_mx_many_experts():
+    counts = [0, 1, 0, 2] * 512
+    gen = _rng("mx many")
+    xc, xs = _mx(gen, False, 1536, 64)
+    wc, ws = _mx(gen, False, 2048, 32, 64)
+    cfg = cq.ExpertConfig(experts=2048, rows=1536, n=32, k=64, x_dtype=2)
+    y = cq.expert_matmul(cfg, xc.to(DEV), wc.to(DEV), _counts(counts), x_scales=xs.to(DEV), w_scales=ws.to(DEV))
+    want, bound, _, _ = ref.forward(ref.mx_values(xc, xs), ref.mx_values(wc, ws), counts, 0, torch.bfloat16)
+    ref.check(y, want, bound, "y")
+
+
 # -------------------------------------------------------------------------------------------------
 # 4-bit weights
 # -------------------------------------------------------------------------------------------------
