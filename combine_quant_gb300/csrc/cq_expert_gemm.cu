@@ -58,14 +58,13 @@ constexpr int kStageBytes = kABytes + 128 * 128;  // B: half of up to 256 column
 // Stages of the ring: what is left beside the results' staging, the scales and
 // the lists of 2048 experts.
 template <Op OP, bool ACT, bool MX>
-constexpr int kStages = (OP == kDx && ACT) || MX ? 5 : 6;
+constexpr int kStages = (OP == kDx && ACT) || OP == kDw || MX ? 5 : 6;
 
 struct Shape {
   int I, J, KK;        // extents: out columns (physical A rows), dw: out rows, contraction
   int n_out;           // forward: n
   int tiles_i;         // tiles along i
   int tiles_j;         // dw: tiles along j
-  int sectors;         // dw: the result is 32-byte aligned
   int whole;           // MN-major operands are whole blocks of 64: one copy takes two of them
 };
 
@@ -111,28 +110,6 @@ __device__ __forceinline__ Tile tile_at(const Shape& sh, const int* s_begin, con
   return x;
 }
 
-// Wait for a phase that the pair's other CTA takes part in (cluster scope).
-__device__ __forceinline__ bool try_pair(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity) {
-  const uint32_t b = smem_u32(bar);
-  if (try_pair(b, parity)) return true;
-  const uint64_t t0 = async::globaltimer_ns();
-  for (uint32_t polls = 0; polls < async::kWaitMaxPolls; ++polls) {
-    if (try_pair(b, parity)) return true;
-    if (async::globaltimer_ns() - t0 > async::kWaitLimitNs) return false;
-  }
-  return false;
-}
-
 __device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + __expf(-g)); }
 
 // y = u * g / (1 + exp(-g)) in 32 bits.
@@ -143,55 +120,53 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 // Bytes of one results warp's staging buffer: 32 columns (j) of its 32 lanes
 // (i) in 16 bits, or in 32 where another factor still comes (rows of 36 floats,
 // so that neither the columns' stores nor the rows' loads meet in a bank).
+// dw: 32 rows (i) of 128 bytes.
 template <Op OP, bool ACT>
-constexpr int kStagingBytes = OP == kDx && ACT ? 32 * 36 * 4 : 32 * 64;
+constexpr int kStagingBytes = OP == kDw ? 32 * 128 : OP == kDx && ACT ? 32 * 36 * 4 : 32 * 64;
 
-// 32 bytes to global memory: one store of a whole sector where the address allows.
-__device__ __forceinline__ void store32(void* p, int sectors, const uint32_t* v) {
-  if (sectors) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
-                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+// dw: drains 128 bytes of each of this warp's 32 rows (64 columns in 16 bits, 32
+// in f32) from column c0: through shared memory, swizzled as the map of the
+// result has it, and out by a tiled copy, which also cuts off what lies outside.
+template <typename T, bool F32>
+__device__ __forceinline__ void drain_dw(const Shape& sh, const CUtensorMap* map, const Tile& x,
+                                         int i_warp, int c0, uint32_t src, uint8_t* stage) {
+  const int lane = threadIdx.x & 31;
+  uint32_t v[32];
+  if constexpr (F32) {
+    tmem_ld32(src + c0, v);
+    tmem_wait();
   } else {
-    static_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    static_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    uint32_t lo[32], hi[32];
+    tmem_ld32(src + c0, lo);
+    tmem_ld32(src + c0 + 32, hi);
+    tmem_wait();
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      v[c] = T::pack2(__uint_as_float(lo[2 * c]), __uint_as_float(lo[2 * c + 1]));
+      v[16 + c] = T::pack2(__uint_as_float(hi[2 * c]), __uint_as_float(hi[2 * c + 1]));
+    }
   }
+  tma_store_wait_read();  // of the lane that issued the last copy; nothing for the others
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+        make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (lane == 0 && i_warp < sh.I) tma_store3(map, smem_u32(stage), x.j0 + c0, i_warp, x.e);
 }
 
-// Drains columns [c0, c0 + 32) of a tile. dw: a lane holds 32 neighbours of one
-// row of the result and writes them, a sector at a time. The others: out[j][i ..
-// i + 31] of 32 j. The accumulator holds i on lanes and j on columns, memory
-// wants i contiguous, so the block is turned in shared memory (16-byte pieces of
-// a 64-byte row, XORed with bits of the row number: no bank conflicts either
-// way) and written in 16-byte stores, 64 bytes a row.
-template <Op OP, typename T, bool F32, bool ACT>
+// Drains columns [c0, c0 + 32) of a tile: out[j][i .. i + 31] of 32 j. The
+// accumulator holds i on lanes and j on columns, memory wants i contiguous, so
+// the block is turned in shared memory (16-byte pieces of a 64-byte row, XORed
+// with bits of the row number: no bank conflicts either way) and written in
+// 16-byte stores, 64 bytes a row.
+template <Op OP, typename T, bool ACT>
 __device__ __forceinline__ void drain(const Args& a, const Shape& sh, const Tile& x, int i_warp,
                                       int c0, uint32_t src, uint8_t* stage) {
   const int lane = threadIdx.x & 31;
   const int jn = x.jn - c0;  // columns that exist
-  if constexpr (OP == kDw) {
-    uint32_t acc[32];
-    tmem_ld32(src + c0, acc);
-    tmem_wait();
-    const int i = i_warp + lane;
-    if (i >= sh.I) return;
-    const size_t at = ((size_t)x.e * sh.I + i) * sh.J + x.j0 + c0;
-    if constexpr (F32) {
-      float* out = static_cast<float*>(a.out) + at;
-#pragma unroll
-      for (int c = 0; c < 32; c += 8)
-        if (c < jn) store32(out + c, sh.sectors, acc + c);
-    } else {
-      uint16_t* out = static_cast<uint16_t*>(a.out) + at;
-      uint32_t v[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        v[c] = T::pack2(__uint_as_float(acc[2 * c]), __uint_as_float(acc[2 * c + 1]));
-      store32(out, sh.sectors, v);
-      if (16 < jn) store32(out + 16, sh.sectors, v + 8);
-    }
-    return;
-  }
   const size_t row0 = (size_t)(x.begin + x.j0) + c0;
   const uint32_t st = smem_u32(stage);
   if constexpr (OP == kDx && ACT) {
@@ -304,7 +279,8 @@ __device__ __forceinline__ void store_zeros(const Args& a, const Shape& sh, cons
 template <Op OP, typename T, bool F32, bool ACT, bool MX>
 __global__ void __launch_bounds__(kThreads<MX>, 1)
 gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
-            const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b) {
+            const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+            const __grid_constant__ CUtensorMap map_out) {
   constexpr int S = kStages<OP, ACT, MX>;
   constexpr int SB = kStageBytes;
   constexpr int NT = kNT<MX>, KB = MX ? 128 : 64;  // columns; contraction of a stage
@@ -377,12 +353,13 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       const int jh = half_cols(x), jb = x.j0 + (int)rank * jh;
       const int box = B_MN && !sh.whole ? 64 : 128;  // columns of one copy
       const int nbox = (jh + box - 1) / box;
+      const bool ragged = OP == kDw && (x.kk & 15) != 0;
       const uint32_t bytes = kABytes + nbox * (box * 128);
       for (int kb = 0; kb < x.nkb; ++kb) {
         if (lap > 0 && !(ok = wait(&bars.empty[s], (lap & 1) ^ 1, 1))) break;
         if (elect_one()) {
           const uint32_t sa = smem_u32(ring + s * SB), sb = sa + kABytes;
-          const bool tail = OP == kDw && kb == x.nkb - 1 && (x.kk & 15) != 0;
+          const bool tail = ragged && kb == 0;
           uint32_t bar;
           if (tail) {
             // zeros go in before the product may read: each CTA's copies complete
@@ -394,7 +371,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
             bar = lead(&bars.full[s]);
             if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], bytes * 2);
           }
-          const int k0 = kb * KB;
+          const int k0 = (!ragged ? kb : kb == 0 ? x.nkb - 1 : kb - 1) * KB;
           if constexpr (OP == kForward && ACT) {
             tma_load5(sa, &map_a, k0, 0, 0, i_cta / 32, x.e, bar);
           } else if constexpr (OP == kForward) {
@@ -442,6 +419,27 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     const uint64_t da = desc_at(desc_base(A_MN ? 8192 : 16), smem_u32(ring));
     const uint64_t db = desc_at(desc_base(B_MN ? 8192 : 16), smem_u32(ring) + kABytes);
     uint32_t s = 0, lap = 0, buf = 0, tail_uses[S] = {};
+    // dw: where an expert's rows do not end with a step of 16, a tile begins with
+    // the stage of the last rows. It waits for warp 2's zeros in both CTAs; up to
+    // kLate other stages go before it (the ring has S - 1).
+    constexpr int kLate = 3;
+    static_assert(kLate < S, "the ring must be able to run on while a stage waits");
+    auto finish_late = [&](uint32_t late, uint32_t d, uint32_t idesc, int rows, bool add) {
+      uint32_t use_t = 0;
+#pragma unroll
+      for (int q = 0; q < S; ++q)
+        if (q == late) use_t = tail_uses[q]++;
+      if (!wait(&bars.tail_full[late], use_t & 1, 1, true)) return false;
+      fence_after();
+      if (elect_one()) {
+        const uint64_t ad = da + late * (SB >> 4), bd = db + late * (SB >> 4);
+        for (int q = 0; 16 * q < rows; ++q)
+          mma_f16(d, ad + q * ka, bd + q * kbs, idesc, add || q > 0);
+        commit(smem_u32(&bars.empty[late]));
+      }
+      __syncwarp();
+      return true;
+    };
     // mx: entry of scales; set of 12 TMEM columns (A then B) to fill, to use
     uint32_t se = 0, se_lap = 0, sf_fill = 0, sf_use = 0;
     auto scales_in = [&](int kb, int nkb, bool wide) {
@@ -472,15 +470,17 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       const uint32_t idesc =
           MX ? idesc_mx(a.w_dtype, a.x_dtype == kMxE5M2, 256, half_cols(x) * 2)
              : idesc_f16(T::kBf16, A_MN, B_MN, 256, half_cols(x) * 2);
+      const bool ragged = OP == kDw && (x.kk & 15) != 0;
+      const int lead_kb = ragged ? 1 : 0;  // the first stage whose products go in at once
+      uint32_t late = 0;
       for (int kb = 0; kb < x.nkb; ++kb) {
-        if (!(ok = wait(&bars.full[s], lap & 1, 1))) break;
-        if (OP == kDw && kb == x.nkb - 1 && (x.kk & 15) != 0) {
-          uint32_t use_t = 0;
-#pragma unroll
-          for (int q = 0; q < S; ++q)
-            if (q == s) use_t = tail_uses[q]++;
-          if (!(ok = wait(&bars.tail_full[s], use_t & 1, 1, true))) break;
+        if (ragged && kb == 0) {
+          late = s;
+          if (++s == S) s = 0, ++lap;
+          if (x.nkb == 1) ok = finish_late(late, d, idesc, x.kk, false);
+          continue;
         }
+        if (!(ok = wait(&bars.full[s], lap & 1, 1))) break;
         // mx: the next stage's scales go into the other set of TMEM columns ahead of
         // this stage's products, which then need not wait for a copy
         if (MX && kb == 0 && !(ok = scales_in(0, x.nkb, half_cols(x) * 2 > 128))) break;
@@ -488,29 +488,33 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
         fence_after();
         if (elect_one()) {
           const uint64_t ad = da + s * (SB >> 4), bd = db + s * (SB >> 4);
-          const int left = x.kk - kb * KB;
+          const int left = x.kk - (kb - lead_kb) * KB;
+          const bool add = kb > lead_kb;
           if constexpr (MX) {
             const uint32_t sf = tmem + 2 * NT + 12 * sf_use;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               if (32 * q < left)
-                mma_mx(d, ad + q * ka, bd + q * kbs, idesc_sf(idesc, q), sf, sf + 4, kb > 0 || q > 0);
+                mma_mx(d, ad + q * ka, bd + q * kbs, idesc_sf(idesc, q), sf, sf + 4, add || q > 0);
           } else if (left > 48) {
-            mma_f16(d, ad, bd, idesc, kb > 0);
+            mma_f16(d, ad, bd, idesc, add);
             mma_f16(d, ad + ka, bd + kbs, idesc, true);
             mma_f16(d, ad + 2 * ka, bd + 2 * kbs, idesc, true);
             mma_f16(d, ad + 3 * ka, bd + 3 * kbs, idesc, true);
           } else {
             for (int q = 0; 16 * q < left; ++q)
-              mma_f16(d, ad + q * ka, bd + q * kbs, idesc, kb > 0 || q > 0);
+              mma_f16(d, ad + q * ka, bd + q * kbs, idesc, add || q > 0);
           }
           commit(smem_u32(&bars.empty[s]));
-          if (kb == x.nkb - 1) commit(smem_u32(&bars.tfull[b]));
         }
         __syncwarp();
         sf_use ^= 1;
         if (++s == S) s = 0, ++lap;
+        if (ragged && kb == min(kLate, x.nkb - 1))
+          if (!(ok = finish_late(late, d, idesc, x.kk - (x.nkb - 1) * KB, true))) break;
       }
+      if (ok && elect_one()) commit(smem_u32(&bars.tfull[b]));
+      __syncwarp();
     }
   } else if (OP == kDw && warp == 2) {
     // ---- zeros over the rows past an expert's last (up to the next 16) ----
@@ -518,9 +522,9 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     bool ok = true;
     for (int t = first; t < n_tiles && ok; t += step) {
       const Tile x = tile_at<OP, MX>(sh, s_begin, s_tile, a.G, t);
+      const int s = it % S;  // a ragged tile begins with the stage of its last rows
       it += x.nkb;
       if (x.nkb == 0 || (x.kk & 15) == 0) continue;
-      const int s = (it - 1) % S;
       uint32_t use_t = 0;
 #pragma unroll
       for (int q = 0; q < S; ++q)
@@ -529,15 +533,12 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       const int r0 = (x.kk - 1) % 64 + 1, r1 = (r0 + 15) / 16 * 16;
       const int blocks = 2 + (half_cols(x) + 63) / 64;
       uint8_t* base = ring + s * SB;
-      for (int v = lane; v < blocks * (r1 - r0) * 8; v += 32) {
-        const int blk = v / ((r1 - r0) * 8), r = r0 + v / 8 % (r1 - r0);
-        *reinterpret_cast<uint4*>(base + blk * 8192 + r * 128 + (v & 7) * 16) = make_uint4(0, 0, 0, 0);
-      }
+      for (int r = r0 + (lane >> 3); r < r1; r += 4)
+        for (int b = 0; b < blocks; ++b)
+          *reinterpret_cast<uint4*>(base + b * 8192 + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) {
-        arrive_cluster(leader_addr(smem_u32(&bars.tail_full[s])));
-      }
+      if (lane == 0) arrive_cluster(leader_addr(smem_u32(&bars.tail_full[s])));
     }
   } else if (MX && warp >= 4 + kDrainWarps) {
     // ---- scales: one word (4 blocks of 32) a row and stage ----
@@ -629,9 +630,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       if (!wait(&bars.swritten[s], lap & 1, 1)) break;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) {
-        arrive_cluster(leader_addr(smem_u32(&bars.sfull[s])));
-      }
+      if (lane == 0) arrive_cluster(leader_addr(smem_u32(&bars.sfull[s])));
       if (++s == kScaleRing) s = 0, ++lap;
     }
   } else if (warp >= 4) {
@@ -652,14 +651,19 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       if (!(ok = wait(&bars.tfull[b], use & 1, 2 + x.nkb / 65536))) break;
       fence_after();
       const uint32_t src = tmem + b * NT + ((uint32_t)(q * 32) << 16);
-      for (int c0 = 32 * half; c0 < x.jn; c0 += 64)
-        drain<OP, T, F32, ACT>(a, sh, x, i_cta + 32 * q, c0, src, stage);
+      if constexpr (OP == kDw) {
+        constexpr int kCols = F32 ? 32 : 64;
+        for (int c0 = kCols * half; c0 < x.jn; c0 += 2 * kCols)
+          drain_dw<T, F32>(sh, &map_out, x, i_cta + 32 * q, c0, src, stage);
+      } else {
+        for (int c0 = 32 * half; c0 < x.jn; c0 += 64)
+          drain<OP, T, ACT>(a, sh, x, i_cta + 32 * q, c0, src, stage);
+      }
       fence_before();
       __syncwarp();
-      if (lane == 0) {
-        arrive_cluster_relaxed(leader_addr(smem_u32(&bars.tempty[b])));
-      }
+      if (lane == 0) arrive_cluster_relaxed(leader_addr(smem_u32(&bars.tempty[b])));
     }
+    if (OP == kDw) tma_store_wait();
   }
   __syncwarp();
   fence_before();
@@ -671,7 +675,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
 // ---- host ----
 template <Op OP, typename T, bool F32, bool ACT, bool MX>
 cudaError_t launch_t(const Args& a, const Shape& sh, const CUtensorMap& ma, const CUtensorMap& mb,
-                     cudaStream_t s) {
+                     const CUtensorMap& out, cudaStream_t s) {
   constexpr auto kernel = gemm_kernel<OP, T, F32, ACT, MX>;
   const size_t smem = 1024 + (size_t)kStages<OP, ACT, MX> * kStageBytes +
                       kDrainWarps * kStagingBytes<OP, ACT> +
@@ -695,7 +699,7 @@ cudaError_t launch_t(const Args& a, const Shape& sh, const CUtensorMap& ma, cons
   attr[1].val.clusterDim = {2, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, a, sh, ma, mb);
+  return cudaLaunchKernelEx(&cfg, kernel, a, sh, ma, mb, out);
 }
 
 template <typename T>
@@ -716,12 +720,12 @@ cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
       const uint64_t n = N / 2, d[] = {K, 16, 2, n / 16, G}, st[] = {2 * K, 2 * n * K, 32 * K, 2 * N * K};
       const uint32_t b[] = {64, 16, 2, 4, 1};
       if (!make_map(&ma, a.w, type, 5, d, st, b)) return cudaErrorUnknown;
-      return launch_t<kForward, T, false, true, false>(a, sh, ma, mb, s);
+      return launch_t<kForward, T, false, true, false>(a, sh, ma, mb, ma, s);
     }
     const uint64_t d[] = {K, N, G}, st[] = {2 * K, 2 * N * K};
     const uint32_t b[] = {64, 128, 1};
     if (!make_map(&ma, a.w, type, 3, d, st, b)) return cudaErrorUnknown;
-    return launch_t<kForward, T, false, false, false>(a, sh, ma, mb, s);
+    return launch_t<kForward, T, false, false, false>(a, sh, ma, mb, ma, s);
   }
   if (op == kDx) {
     sh.I = a.K;
@@ -740,14 +744,13 @@ cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
       const uint32_t b[] = {64, 64, 1};
       if (!make_map(&ma, a.w, type, 3, d, st, b)) return cudaErrorUnknown;
     }
-    return a.pre_in ? launch_t<kDx, T, false, true, false>(a, sh, ma, mb, s)
-                    : launch_t<kDx, T, false, false, false>(a, sh, ma, mb, s);
+    return a.pre_in ? launch_t<kDx, T, false, true, false>(a, sh, ma, mb, ma, s)
+                    : launch_t<kDx, T, false, false, false>(a, sh, ma, mb, ma, s);
   }
   sh.I = a.N;
   sh.J = a.K;
   sh.tiles_i = (a.N + 255) / 256;
   sh.tiles_j = (a.K + kNT<false> - 1) / kNT<false>;
-  sh.sectors = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
   sh.whole = K % 64 == 0 && N % 64 == 0;
   if (sh.whole) {
     const uint64_t d[] = {64, R, N / 64}, st[] = {2 * N, 128}, db[] = {64, R, K / 64}, sb[] = {2 * K, 128};
@@ -760,8 +763,14 @@ cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
     if (!make_map(&ma, a.w, type, 2, d, st, b) || !make_map(&mb, a.x, type, 2, db, sb, b))
       return cudaErrorUnknown;
   }
-  return a.out_dtype == 2 ? launch_t<kDw, T, true, false, false>(a, sh, ma, mb, s)
-                          : launch_t<kDw, T, false, false, false>(a, sh, ma, mb, s);
+  // The result: 128 bytes of 32 rows at a time.
+  const bool f32 = a.out_dtype == 2;
+  const uint64_t size = f32 ? 4 : 2, dd[] = {K, N, G}, sd[] = {size * K, size * N * K};
+  const uint32_t bd[] = {f32 ? 32u : 64u, 32, 1};
+  CUtensorMap md;
+  if (!make_map(&md, a.out, f32 ? kMapF32 : type, 3, dd, sd, bd)) return cudaErrorUnknown;
+  return f32 ? launch_t<kDw, T, true, false, false>(a, sh, ma, mb, md, s)
+             : launch_t<kDw, T, false, false, false>(a, sh, ma, mb, md, s);
 }
 
 // Forward from mx fp8 operands; T is the output's type.
@@ -781,12 +790,12 @@ cudaError_t launch_mx(const Args& a, cudaStream_t s) {
     const uint64_t n = N / 2, d[] = {K, 16, 2, n / 16, G}, st[] = {K, n * K, 16 * K, N * K};
     const uint32_t b[] = {128, 16, 2, 4, 1};
     if (!make_map(&ma, a.w, kMapU8, 5, d, st, b)) return cudaErrorUnknown;
-    return launch_t<kForward, T, false, true, true>(a, sh, ma, mb, s);
+    return launch_t<kForward, T, false, true, true>(a, sh, ma, mb, ma, s);
   }
   const uint64_t d[] = {K, N, G}, st[] = {K, N * K};
   const uint32_t b[] = {128, 128, 1};
   if (!make_map(&ma, a.w, kMapU8, 3, d, st, b)) return cudaErrorUnknown;
-  return launch_t<kForward, T, false, false, true>(a, sh, ma, mb, s);
+  return launch_t<kForward, T, false, false, true>(a, sh, ma, mb, ma, s);
 }
 
 }  // namespace

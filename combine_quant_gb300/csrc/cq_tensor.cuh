@@ -22,6 +22,29 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
+// async::mbar_wait for a phase that the pair's other CTA takes part in (cluster
+// scope), with the same limits.
+__device__ __forceinline__ bool try_pair(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity) {
+  const uint32_t b = smem_u32(bar);
+  if (try_pair(b, parity)) return true;
+  const uint64_t t0 = async::globaltimer_ns();
+  for (uint32_t polls = 0; polls < async::kWaitMaxPolls; ++polls) {
+    if (try_pair(b, parity)) return true;
+    if (async::globaltimer_ns() - t0 > async::kWaitLimitNs) return false;
+  }
+  return false;
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -98,6 +121,22 @@ __device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap* m, in
       "::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst), "l"(m), "r"(x), "r"(y),
       "r"(z), "r"(u), "r"(v), "r"(bar)
       : "memory");
+}
+
+// Tiled copy of this CTA's shared memory to global, and the wait for this
+// thread's copies to have read theirs, or to be complete.
+__device__ __forceinline__ void tma_store3(const CUtensorMap* m, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   m),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_wait() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
@@ -253,7 +292,7 @@ inline EncodeFn encode_fn() {
   return f;
 }
 
-enum MapType { kMapBF16, kMapF16, kMapU8 };
+enum MapType { kMapBF16, kMapF16, kMapF32, kMapU8 };
 enum MapSwizzle { kSwizzle128, kSwizzle64 };
 
 // Dims and box innermost first, in elements; strides of dims 1.. in bytes.
@@ -273,6 +312,7 @@ inline bool make_map(CUtensorMap* m, const void* p, MapType type, int nd, const 
   return f(m,
            type == kMapBF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
            : type == kMapF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+           : type == kMapF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                              : CU_TENSOR_MAP_DATA_TYPE_UINT8,
            nd, const_cast<void*>(p), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
            swizzle == kSwizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
