@@ -58,7 +58,7 @@ constexpr int kStageBytes = kABytes + 128 * 128;  // B: half of up to 256 column
 // Stages of the ring: what is left beside the results' staging, the scales and
 // the lists of 2048 experts.
 template <Op OP, bool ACT, bool MX>
-constexpr int kStages = (OP == kDx && ACT) || OP == kDw || MX ? 5 : 6;
+constexpr int kStages = (OP == kDx && ACT) || MX ? 5 : 6;
 
 struct Shape {
   int I, J, KK;        // extents: out columns (physical A rows), dw: out rows, contraction
@@ -120,37 +120,34 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 // Bytes of one results warp's staging buffer: 32 columns (j) of its 32 lanes
 // (i) in 16 bits, or in 32 where another factor still comes (rows of 36 floats,
 // so that neither the columns' stores nor the rows' loads meet in a bank).
-// dw: 32 rows (i) of 128 bytes.
+// dw: 32 rows (i) of 64 bytes.
 template <Op OP, bool ACT>
-constexpr int kStagingBytes = OP == kDw ? 32 * 128 : OP == kDx && ACT ? 32 * 36 * 4 : 32 * 64;
+constexpr int kStagingBytes = OP == kDx && ACT ? 32 * 36 * 4 : 32 * 64;
 
-// dw: drains 128 bytes of each of this warp's 32 rows (64 columns in 16 bits, 32
+// dw: drains 64 bytes of each of this warp's 32 rows (32 columns in 16 bits, 16
 // in f32) from column c0: through shared memory, swizzled as the map of the
 // result has it, and out by a tiled copy, which also cuts off what lies outside.
 template <typename T, bool F32>
 __device__ __forceinline__ void drain_dw(const Shape& sh, const CUtensorMap* map, const Tile& x,
                                          int i_warp, int c0, uint32_t src, uint8_t* stage) {
   const int lane = threadIdx.x & 31;
-  uint32_t v[32];
+  uint32_t v[16];
   if constexpr (F32) {
-    tmem_ld32(src + c0, v);
+    tmem_ld16c(src + c0, v);
     tmem_wait();
   } else {
-    uint32_t lo[32], hi[32];
-    tmem_ld32(src + c0, lo);
-    tmem_ld32(src + c0 + 32, hi);
+    uint32_t acc[32];
+    tmem_ld32(src + c0, acc);
     tmem_wait();
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      v[c] = T::pack2(__uint_as_float(lo[2 * c]), __uint_as_float(lo[2 * c + 1]));
-      v[16 + c] = T::pack2(__uint_as_float(hi[2 * c]), __uint_as_float(hi[2 * c + 1]));
-    }
+    for (int c = 0; c < 16; ++c)
+      v[c] = T::pack2(__uint_as_float(acc[2 * c]), __uint_as_float(acc[2 * c + 1]));
   }
   tma_store_wait_read();  // of the lane that issued the last copy; nothing for the others
   __syncwarp();
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
         make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
@@ -652,7 +649,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       fence_after();
       const uint32_t src = tmem + b * NT + ((uint32_t)(q * 32) << 16);
       if constexpr (OP == kDw) {
-        constexpr int kCols = F32 ? 32 : 64;
+        constexpr int kCols = F32 ? 16 : 32;
         for (int c0 = kCols * half; c0 < x.jn; c0 += 2 * kCols)
           drain_dw<T, F32>(sh, &map_out, x, i_cta + 32 * q, c0, src, stage);
       } else {
@@ -763,12 +760,12 @@ cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
     if (!make_map(&ma, a.w, type, 2, d, st, b) || !make_map(&mb, a.x, type, 2, db, sb, b))
       return cudaErrorUnknown;
   }
-  // The result: 128 bytes of 32 rows at a time.
+  // The result: 64 bytes of 32 rows at a time.
   const bool f32 = a.out_dtype == 2;
   const uint64_t size = f32 ? 4 : 2, dd[] = {K, N, G}, sd[] = {size * K, size * N * K};
-  const uint32_t bd[] = {f32 ? 32u : 64u, 32, 1};
+  const uint32_t bd[] = {f32 ? 16u : 32u, 32, 1};
   CUtensorMap md;
-  if (!make_map(&md, a.out, f32 ? kMapF32 : type, 3, dd, sd, bd)) return cudaErrorUnknown;
+  if (!make_map(&md, a.out, f32 ? kMapF32 : type, 3, dd, sd, bd, kSwizzle64)) return cudaErrorUnknown;
   return f32 ? launch_t<kDw, T, true, false, false>(a, sh, ma, mb, md, s)
              : launch_t<kDw, T, false, false, false>(a, sh, ma, mb, md, s);
 }
