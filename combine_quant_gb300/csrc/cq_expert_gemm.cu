@@ -46,8 +46,7 @@ constexpr int kThreads = 128 + 32 * kDrainWarps + (MX ? 32 * kScaleWarps : 0);
 // columns of it for two stages' scales.
 template <bool MX>
 constexpr int kNT = MX ? 240 : 256;
-template <bool MX>
-constexpr int kStepJ = MX ? 16 : 32;       // columns come in steps of
+constexpr int kStepJ = 16;                 // columns come in steps of
 constexpr int kScaleBytes = 3 * 512;       // mx: scales of a stage: 128 rows of A, 256 of B
 constexpr int kScaleRing = 3;              // entries of four stages' scales
 constexpr int kABytes = 128 * 128;         // A of one stage, one CTA
@@ -58,7 +57,7 @@ constexpr int kStageBytes = kABytes + 128 * 128;  // B: half of up to 256 column
 // Stages of the ring: what is left beside the results' staging, the scales and
 // the lists of 2048 experts.
 template <Op OP, bool ACT, bool MX>
-constexpr int kStages = (OP == kDx && ACT) || MX ? 5 : 6;
+constexpr int kStages = MX ? 5 : 6;
 
 struct Shape {
   int I, J, KK;        // extents: out columns (physical A rows), dw: out rows, contraction
@@ -83,7 +82,7 @@ struct Tile {
 template <Op OP, bool MX>
 __device__ __forceinline__ Tile tile_at(const Shape& sh, const int* s_begin, const int* s_tile,
                                         int G, int t) {
-  constexpr int NT = kNT<MX>, SJ = kStepJ<MX>;
+  constexpr int NT = kNT<MX>, SJ = kStepJ;
   Tile x;
   x.e = expert_of(s_tile, G, t);
   const int l = t - s_tile[x.e];
@@ -118,11 +117,11 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 }
 
 // Bytes of one results warp's staging buffer: 32 columns (j) of its 32 lanes
-// (i) in 16 bits, or in 32 where another factor still comes (rows of 36 floats,
-// so that neither the columns' stores nor the rows' loads meet in a bank).
+// (i) in 16 bits, or 16 in 32 bits where another factor still comes (rows of 33
+// floats, so that neither the columns' stores nor the rows' loads meet in a bank).
 // dw: 32 rows (i) of 64 bytes.
 template <Op OP, bool ACT>
-constexpr int kStagingBytes = OP == kDx && ACT ? 32 * 36 * 4 : 32 * 64;
+constexpr int kStagingBytes = OP == kDx && ACT ? 16 * 33 * 4 : 32 * 64;
 
 // dw: drains 64 bytes of each of this warp's 32 rows (32 columns in 16 bits, 16
 // in f32) from column c0: through shared memory, swizzled as the map of the
@@ -179,35 +178,33 @@ __device__ __forceinline__ void drain(const Args& a, const Shape& sh, const Tile
       u[p] = ok ? __ldg(reinterpret_cast<const uint4*>(pre + 8 * p * ld + sh.I)) : make_uint4(0, 0, 0, 0);
     }
     float* buf = reinterpret_cast<float*>(stage);
-    {
-      uint32_t acc[32];
-      tmem_ld32(src + c0, acc);
-      tmem_wait();
+    uint32_t acc[32];
+    tmem_ld32(src + c0, acc);
+    tmem_wait();
 #pragma unroll
-      for (int c = 0; c < 32; ++c) buf[c * 36 + lane] = __uint_as_float(acc[c]);
-    }
-    __syncwarp();
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const float4* at = reinterpret_cast<const float4*>(buf + (8 * p + r) * 36 + 8 * (lane & 3));
-      const float4 d0 = at[0], d1 = at[1];
-      const float d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
-      const uint32_t gw[4] = {g[p].x, g[p].y, g[p].z, g[p].w}, uw[4] = {u[p].x, u[p].y, u[p].z, u[p].w};
-      uint32_t dg[4], du[4];
+      for (int c = 0; c < 16; ++c) buf[c * 33 + lane] = __uint_as_float(acc[16 * h + c]);
+      __syncwarp();
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const float g0 = T::lo(gw[h]), g1 = T::hi(gw[h]), u0 = T::lo(uw[h]), u1 = T::hi(uw[h]);
-        const float s0 = sigmoid(g0), s1 = sigmoid(g1);
-        dg[h] = T::pack2(d[2 * h] * u0 * (s0 + g0 * s0 * (1.f - s0)),
-                         d[2 * h + 1] * u1 * (s1 + g1 * s1 * (1.f - s1)));
-        du[h] = T::pack2(d[2 * h] * g0 * s0, d[2 * h + 1] * g1 * s1);
+      for (int p = 2 * h; p < 2 * h + 2; ++p) {
+        const float* d = buf + (8 * (p - 2 * h) + r) * 33 + 8 * (lane & 3);
+        const uint32_t gw[4] = {g[p].x, g[p].y, g[p].z, g[p].w}, uw[4] = {u[p].x, u[p].y, u[p].z, u[p].w};
+        uint32_t dg[4], du[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float g0 = T::lo(gw[k]), g1 = T::hi(gw[k]), u0 = T::lo(uw[k]), u1 = T::hi(uw[k]);
+          const float s0 = sigmoid(g0), s1 = sigmoid(g1), d0 = d[2 * k], d1 = d[2 * k + 1];
+          dg[k] = T::pack2(d0 * u0 * (s0 + g0 * s0 * (1.f - s0)), d1 * u1 * (s1 + g1 * s1 * (1.f - s1)));
+          du[k] = T::pack2(d0 * g0 * s0, d1 * g1 * s1);
+        }
+        if (i < sh.I && 8 * p + r < jn) {
+          *reinterpret_cast<uint4*>(out + 8 * p * ld) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
+          *reinterpret_cast<uint4*>(out + 8 * p * ld + sh.I) = make_uint4(du[0], du[1], du[2], du[3]);
+        }
       }
-      if (i < sh.I && 8 * p + r < jn) {
-        *reinterpret_cast<uint4*>(out + 8 * p * ld) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
-        *reinterpret_cast<uint4*>(out + 8 * p * ld + sh.I) = make_uint4(du[0], du[1], du[2], du[3]);
-      }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
     uint32_t v0[16], v1[16];  // lanes 0-15 and 16-31 (SwiGLU: gates and ups of 16 outputs)
     tmem_ld16(src + c0, v0);
@@ -336,7 +333,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
   // Columns of B that this CTA loads for a tile: its half of jn, in copies of
   // 32 rows (K-major) or 64 columns (MN-major).
   auto half_cols = [&](const Tile& x) {
-    const int unit = OP == kDw && sh.whole ? 128 : kStepJ<MX>;
+    const int unit = OP != kDw ? kStepJ : sh.whole ? 128 : 32;
     return (x.jn + unit - 1) / unit * unit / 2;
   };
 
@@ -419,7 +416,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     // dw: where an expert's rows do not end with a step of 16, a tile begins with
     // the stage of the last rows. It waits for warp 2's zeros in both CTAs; up to
     // kLate other stages go before it (the ring has S - 1).
-    constexpr int kLate = 3;
+    constexpr int kLate = 2;
     static_assert(kLate < S, "the ring must be able to run on while a stage waits");
     auto finish_late = [&](uint32_t late, uint32_t d, uint32_t idesc, int rows, bool add) {
       uint32_t use_t = 0;
