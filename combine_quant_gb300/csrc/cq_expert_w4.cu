@@ -138,46 +138,58 @@ __device__ __forceinline__ void multiply(float (&acc)[MTW][NTMAX][4], const uint
   // H blocks of 32 of k under one scale, from block h0.
   auto span = [&](auto first, auto blocks) {
     constexpr int h0 = decltype(first)::value, H = decltype(blocks)::value, p = G32 ? h0 : 0;
-    uint4 b[H][NT];
-    float2 c[NT];
+    // All of a block's products side by side: MTW x NT chains in flight.
+    float d[MTW][NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int h = 0; h < H; ++h) {
+      uint4 b[NT];
+      uint32_t a0[MTW][4], a1[MTW][4];
 #pragma unroll
-      for (int h = 0; h < H; ++h) b[h][n] = *reinterpret_cast<const uint4*>(sx + ((h0 + h) * NT + n) * 512);
-      c[n] = *reinterpret_cast<const float2*>(sum + p * 8 * NTMAX + 8 * n);
-    }
+      for (int n = 0; n < NT; ++n) b[n] = *reinterpret_cast<const uint4*>(sx + ((h0 + h) * NT + n) * 512);
 #pragma unroll
-    for (int m = 0; m < MTW; ++m) {
-      float d[NT][4];
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
+      for (int m = 0; m < MTW; ++m) {
         const uint8_t* at = (h0 + h ? sw1 : sw0) + 2048 * m;
         const uint32_t w0 = *reinterpret_cast<const uint32_t*>(at);
         const uint32_t w1 = *reinterpret_cast<const uint32_t*>(at + 1024);
-        const uint32_t a0[4] = {codes2<kBf16, 0>(w0), codes2<kBf16, 0>(w1), codes2<kBf16, 1>(w0), codes2<kBf16, 1>(w1)};
-        const uint32_t a1[4] = {codes2<kBf16, 2>(w0), codes2<kBf16, 2>(w1), codes2<kBf16, 3>(w0), codes2<kBf16, 3>(w1)};
-        if (h == 0) {
+        a0[m][0] = codes2<kBf16, 0>(w0), a0[m][1] = codes2<kBf16, 0>(w1);
+        a0[m][2] = codes2<kBf16, 1>(w0), a0[m][3] = codes2<kBf16, 1>(w1);
+        a1[m][0] = codes2<kBf16, 2>(w0), a1[m][1] = codes2<kBf16, 2>(w1);
+        a1[m][2] = codes2<kBf16, 3>(w0), a1[m][3] = codes2<kBf16, 3>(w1);
+      }
+      if (h == 0) {
+        float2 c[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) c[n] = *reinterpret_cast<const float2*>(sum + p * 8 * NTMAX + 8 * n);
+#pragma unroll
+        for (int m = 0; m < MTW; ++m) {
           float2 o = make_float2(1.f, 1.f);
           if constexpr (ZEROS) o = *reinterpret_cast<const float2*>(zero + p * kSpan + 2 * m);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            mma<kBf16>(d[n], a0, b[h][n].x, b[h][n].y, o.x * c[n].x, o.x * c[n].y, o.y * c[n].x, o.y * c[n].y);
-        } else {
+            mma<kBf16>(d[m][n], a0[m], b[n].x, b[n].y, o.x * c[n].x, o.x * c[n].y, o.y * c[n].x, o.y * c[n].y);
+        }
+      } else {
+#pragma unroll
+        for (int m = 0; m < MTW; ++m)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            mma<kBf16>(d[n], a0, b[h][n].x, b[h][n].y, d[n][0], d[n][1], d[n][2], d[n][3]);
-        }
+            mma<kBf16>(d[m][n], a0[m], b[n].x, b[n].y, d[m][n][0], d[m][n][1], d[m][n][2], d[m][n][3]);
+      }
+#pragma unroll
+      for (int m = 0; m < MTW; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          mma<kBf16>(d[n], a1, b[h][n].z, b[h][n].w, d[n][0], d[n][1], d[n][2], d[n][3]);
-      }
+          mma<kBf16>(d[m][n], a1[m], b[n].z, b[n].w, d[m][n][0], d[m][n][1], d[m][n][2], d[m][n][3]);
+    }
+#pragma unroll
+    for (int m = 0; m < MTW; ++m) {
       const float2 f = *reinterpret_cast<const float2*>(scale + p * kSpan + 2 * m);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        acc[m][n][0] = fmaf(f.x, d[n][0], acc[m][n][0]);
-        acc[m][n][1] = fmaf(f.x, d[n][1], acc[m][n][1]);
-        acc[m][n][2] = fmaf(f.y, d[n][2], acc[m][n][2]);
-        acc[m][n][3] = fmaf(f.y, d[n][3], acc[m][n][3]);
+        acc[m][n][0] = fmaf(f.x, d[m][n][0], acc[m][n][0]);
+        acc[m][n][1] = fmaf(f.x, d[m][n][1], acc[m][n][1]);
+        acc[m][n][2] = fmaf(f.y, d[m][n][2], acc[m][n][2]);
+        acc[m][n][3] = fmaf(f.y, d[m][n][3], acc[m][n][3]);
       }
     }
   };
