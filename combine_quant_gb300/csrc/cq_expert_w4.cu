@@ -119,22 +119,21 @@ struct Stage {
   static constexpr int kX = 2 * kChunk;
   static constexpr int kScale = kX + 16 * 512 * NTMAX;
   static constexpr int kGroups = G32 ? 16 : 8;              // most groups of 512 of k
-  static constexpr int kGroupFloats = kRows;                // floats of one group
-  static constexpr int kZero = kScale + kGroups * kGroupFloats * 4;
-  static constexpr int kSum = kZero + (ZEROS ? kGroups * kGroupFloats * 4 : 0);
+  static constexpr int kGroupFloats = ZEROS ? 2 * kRows : kRows;  // of one group: s, or s and -(OFF + z)
+  static constexpr int kSum = kScale + kGroups * kGroupFloats * 4;
   static constexpr int kSpans = G32 ? 2 : 1;                // spans with one scale in 64 of k
   static constexpr int kBytes = (kSum + 8 * kSpans * 8 * NTMAX * 4 + 1023) / 1024 * 1024;
 };
 
 // 64 of k (two blocks of 32) of one multiplying warp. sw0, sw1: this thread's
 // code words of the two blocks (+ 2048 m, + 1024 for rows g + 8); sx: its x
-// (+ (h NT + n) 512); sum, scale, zero: of its tokens and rows.
+// (+ (h NT + n) 512); sum, scale: of its tokens and rows.
 template <typename T, int MTW, int NT, int NTMAX, bool ZEROS, bool G32>
 __device__ __forceinline__ void multiply(float (&acc)[MTW][NTMAX][4], const uint8_t* sw0,
                                          const uint8_t* sw1, const uint8_t* sx, const float* sum,
-                                         const float* scale, const float* zero) {
+                                         const float* scale) {
   constexpr bool kBf16 = T::kBf16;
-  constexpr int kSpan = 64 * MTW;  // floats from one group's scales to the next
+  constexpr int kSpan = Stage<MTW, NTMAX, ZEROS, G32>::kGroupFloats;  // from one group's scales to the next
   // H blocks of 32 of k under one scale, from block h0.
   auto span = [&](auto first, auto blocks) {
     constexpr int h0 = decltype(first)::value, H = decltype(blocks)::value, p = G32 ? h0 : 0;
@@ -163,7 +162,7 @@ __device__ __forceinline__ void multiply(float (&acc)[MTW][NTMAX][4], const uint
 #pragma unroll
         for (int m = 0; m < MTW; ++m) {
           float2 o = make_float2(1.f, 1.f);
-          if constexpr (ZEROS) o = *reinterpret_cast<const float2*>(zero + p * kSpan + 2 * m);
+          if constexpr (ZEROS) o = make_float2(scale[p * kSpan + 4 * m + 1], scale[p * kSpan + 4 * m + 3]);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
             mma<kBf16>(d[m][n], a0[m], b[n].x, b[n].y, o.x * c[n].x, o.x * c[n].y, o.y * c[n].x, o.y * c[n].y);
@@ -183,7 +182,9 @@ __device__ __forceinline__ void multiply(float (&acc)[MTW][NTMAX][4], const uint
     }
 #pragma unroll
     for (int m = 0; m < MTW; ++m) {
-      const float2 f = *reinterpret_cast<const float2*>(scale + p * kSpan + 2 * m);
+      float2 f;
+      if constexpr (ZEROS) f = make_float2(scale[p * kSpan + 4 * m], scale[p * kSpan + 4 * m + 2]);
+      else f = *reinterpret_cast<const float2*>(scale + p * kSpan + 2 * m);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         acc[m][n][0] = fmaf(f.x, d[m][n][0], acc[m][n][0]);
@@ -224,8 +225,7 @@ __device__ __forceinline__ bool multiply_tile(float (&acc)[MTW][NTMAX][4], Bars&
           acc, base + c * St::kChunk + at.w, base + c * St::kChunk + (at.w ^ 16),
           base + at_x + c * (8 * 512 * NT),
           reinterpret_cast<const float*>(base + at.sum + c * (4 * St::kSpans * 8 * NTMAX * 4)),
-          reinterpret_cast<const float*>(scale),
-          reinterpret_cast<const float*>(scale + St::kZero - St::kScale));
+          reinterpret_cast<const float*>(scale));
     };
 #pragma unroll
     for (int c = 0; c < 2; ++c)
@@ -298,7 +298,7 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     at.w = rq * (16 * MTW * 128) + g * 128 + (((2 * kw) ^ g) << 4) + 4 * q;
     at.x = St::kX + g * 64 + ((q ^ ((g >> 1) & 3)) << 4);
     at.sum = St::kSum + (kw * (St::kSpans * 8 * NTMAX) + 2 * q) * 4;
-    at.scale = St::kScale + ((kw * 64 >> sh.shift) * St::kGroupFloats + (rq * 8 + g) * (2 * MTW)) * 4;
+    at.scale = St::kScale + ((kw * 64 >> sh.shift) * St::kGroupFloats + (rq * 8 + g) * (St::kGroupFloats / 32)) * 4;
     at.scale_next = (256 >> sh.shift) * St::kGroupFloats * 4;
     for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
       const Tile x = tile_at<MTW, NTMAX, ACT>(sh, s_begin, s_tile, a.G, t);
@@ -404,8 +404,9 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     }
   } else if (warp < kMulWarps + kSumWarps + kScaleWarps) {
     // ---- scales: a thread takes rows r and r + 64, kAhead stages ahead ----
-    constexpr int kAhead = (G32 ? 2 : 4) / (ZEROS ? 2 : 1);
     constexpr int kPer = (St::kRows + 63) / 64, kW = St::kGroups / 2;  // rows; words of a row
+    constexpr int kFit = 48 / (kPer * kW * (ZEROS ? 3 : 2) / 2);       // in 48 registers
+    constexpr int kAhead = kFit > 4 ? 4 : kFit;
     const uint16_t* scales = static_cast<const uint16_t*>(a.scales4);
     const int per_cta = n_tiles > (int)blockIdx.x ? (n_tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
     const int total = per_cta * n_stages, ng = 512 >> sh.shift;
@@ -436,15 +437,25 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
         if (!in[b]) continue;
         const size_t at = row_at[b] + first;
         if (sh.vec) {
-          // 4 groups (of 128) or 8, 16 (two pieces of 8; the second may not exist)
+          // 4 groups (of 128), 8, or twice 8, the second of which may not exist
+          const uint16_t* from = scales + at;
+          const uint8_t* zfrom = a.zeros4 + at;
+          if (!G32 && ng == 4) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(from));
+            sv[b][0] = v.x, sv[b][1] = v.y;
+            if (ZEROS) zv[b][0] = __ldg(reinterpret_cast<const uint32_t*>(zfrom));
+          } else {
 #pragma unroll
-          for (int w = 0; w < kW; w += 2)
-            if (2 * w < ng && first + 2 * w < sh.KG) {
-              const uint2 v = __ldg(reinterpret_cast<const uint2*>(scales + at + 2 * w));
-              sv[b][w] = v.x;
-              sv[b][w + 1] = v.y;
-              if (ZEROS) zv[b][w / 2] = __ldg(reinterpret_cast<const uint32_t*>(a.zeros4 + at + 2 * w));
-            }
+            for (int w = 0; w < kW; w += 4)
+              if (first + 2 * w < sh.KG) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(from + 2 * w));
+                sv[b][w] = v.x, sv[b][w + 1] = v.y, sv[b][w + 2] = v.z, sv[b][w + 3] = v.w;
+                if (ZEROS) {
+                  const uint2 z = __ldg(reinterpret_cast<const uint2*>(zfrom + 2 * w));
+                  zv[b][w / 2] = z.x, zv[b][w / 2 + 1] = z.y;
+                }
+              }
+          }
         } else {
 #pragma unroll
           for (int k = 0; k < St::kGroups; ++k)
@@ -467,14 +478,18 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
         for (int b = 0; b < kPer; ++b) {
           const int r = r0 + 64 * b;
           const int slot = (r / (16 * MTW) * 8 + r % 8) * (2 * MTW) + 2 * (r / 16 % MTW) + r / 8 % 2;
-          float* to = reinterpret_cast<float*>(base + St::kScale) + slot;
-          float* tz = reinterpret_cast<float*>(base + St::kZero) + slot;
+          float* to = reinterpret_cast<float*>(base + St::kScale) + slot * (ZEROS ? 2 : 1);
 #pragma unroll
           for (int k = 0; k < St::kGroups; ++k)
             if (k < ng) {
-              to[k * St::kGroupFloats] = k & 1 ? T::hi(sbuf[u][b][k / 2]) : T::lo(sbuf[u][b][k / 2]);
-              if (ZEROS)
-                tz[k * St::kGroupFloats] = -(kOff + (float)((zbuf[u][b][k / 4] >> (8 * (k & 3))) & 255));
+              const float f = k & 1 ? T::hi(sbuf[u][b][k / 2]) : T::lo(sbuf[u][b][k / 2]);
+              if constexpr (ZEROS) {
+                // 2^23 + z has z in its last bits; all of this is exact
+                const float z = __uint_as_float(__byte_perm(zbuf[u][b][k / 4], 0x4b000000u, 0x7440 + (k & 3)));
+                *reinterpret_cast<float2*>(to + k * St::kGroupFloats) = make_float2(f, (8388608.f - kOff) - z);
+              } else {
+                to[k * St::kGroupFloats] = f;
+              }
             }
         }
         __syncwarp();
