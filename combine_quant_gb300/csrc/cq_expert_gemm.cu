@@ -109,7 +109,12 @@ __device__ __forceinline__ Tile tile_at(const Shape& sh, const int* s_begin, con
   return x;
 }
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + __expf(-g)); }
+// 1 / (1 + exp(-g)) from exp(-|g|), which cannot overflow: small values keep
+// their relative accuracy down to the subnormals.
+__device__ __forceinline__ float sigmoid(float g) {
+  const float e = __expf(-fabsf(g)), r = __fdividef(1.f, 1.f + e);
+  return g >= 0.f ? r : e * r;
+}
 
 // y = u * g / (1 + exp(-g)) in 32 bits.
 __device__ __forceinline__ float swiglu(float g, float u) {
@@ -153,6 +158,25 @@ __device__ __forceinline__ void drain_dw(const Shape& sh, const CUtensorMap* map
   if (lane == 0 && i_warp < sh.I) tma_store3(map, smem_u32(stage), x.j0 + c0, i_warp, x.e);
 }
 
+// dx through SwiGLU: a lane's 8 gates and ups of 4 of 32 columns (j), read ahead of
+// the columns' turn.
+struct Saved {
+  uint4 g[4], u[4];
+};
+__device__ __forceinline__ void load_saved(const Args& a, const Shape& sh, const Tile& x, int i_warp,
+                                           int c0, Saved& v) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, i = i_warp + 8 * (lane & 3);
+  const size_t ld = 2 * (size_t)sh.I;
+  const uint16_t* pre =
+      static_cast<const uint16_t*>(a.pre_in) + ((size_t)(x.begin + x.j0) + c0 + r) * ld + i;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const bool ok = i < sh.I && c0 + 8 * p + r < x.jn;
+    v.g[p] = ok ? __ldg(reinterpret_cast<const uint4*>(pre + 8 * p * ld)) : make_uint4(0, 0, 0, 0);
+    v.u[p] = ok ? __ldg(reinterpret_cast<const uint4*>(pre + 8 * p * ld + sh.I)) : make_uint4(0, 0, 0, 0);
+  }
+}
+
 // Drains columns [c0, c0 + 32) of a tile: out[j][i .. i + 31] of 32 j. The
 // accumulator holds i on lanes and j on columns, memory wants i contiguous, so
 // the block is turned in shared memory (16-byte pieces of a 64-byte row, XORed
@@ -160,23 +184,19 @@ __device__ __forceinline__ void drain_dw(const Shape& sh, const CUtensorMap* map
 // 16-byte stores, 64 bytes a row.
 template <Op OP, typename T, bool ACT>
 __device__ __forceinline__ void drain(const Args& a, const Shape& sh, const Tile& x, int i_warp,
-                                      int c0, uint32_t src, uint8_t* stage) {
+                                      int c0, uint32_t src, uint8_t* stage, Saved& saved) {
   const int lane = threadIdx.x & 31;
   const int jn = x.jn - c0;  // columns that exist
   const size_t row0 = (size_t)(x.begin + x.j0) + c0;
   const uint32_t st = smem_u32(stage);
   if constexpr (OP == kDx && ACT) {
     const int r = lane >> 2, i = i_warp + 8 * (lane & 3);
-    const size_t ld = 2 * (size_t)sh.I, first = (row0 + r) * ld + i;
-    const uint16_t* pre = static_cast<const uint16_t*>(a.pre_in) + first;
-    uint16_t* out = static_cast<uint16_t*>(a.out) + first;
-    uint4 g[4], u[4];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const bool ok = i < sh.I && 8 * p + r < jn;
-      g[p] = ok ? __ldg(reinterpret_cast<const uint4*>(pre + 8 * p * ld)) : make_uint4(0, 0, 0, 0);
-      u[p] = ok ? __ldg(reinterpret_cast<const uint4*>(pre + 8 * p * ld + sh.I)) : make_uint4(0, 0, 0, 0);
-    }
+    const size_t ld = 2 * (size_t)sh.I;
+    uint16_t* out = static_cast<uint16_t*>(a.out) + (row0 + r) * ld + i;
+    const Saved now = saved;
+    if (c0 + 64 < x.jn) load_saved(a, sh, x, i_warp, c0 + 64, saved);  // of this warp's next columns
+    const uint4(&g)[4] = now.g;
+    const uint4(&u)[4] = now.u;
     float* buf = reinterpret_cast<float*>(stage);
     uint32_t acc[32];
     tmem_ld32(src + c0, acc);
@@ -194,9 +214,11 @@ __device__ __forceinline__ void drain(const Args& a, const Shape& sh, const Tile
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float g0 = T::lo(gw[k]), g1 = T::hi(gw[k]), u0 = T::lo(uw[k]), u1 = T::hi(uw[k]);
+          // silu' = s + g s (1 - s) = (s + g s) - g s s
           const float s0 = sigmoid(g0), s1 = sigmoid(g1), d0 = d[2 * k], d1 = d[2 * k + 1];
-          dg[k] = T::pack2(d0 * u0 * (s0 + g0 * s0 * (1.f - s0)), d1 * u1 * (s1 + g1 * s1 * (1.f - s1)));
-          du[k] = T::pack2(d0 * g0 * s0, d1 * g1 * s1);
+          const float h0 = g0 * s0, h1 = g1 * s1;
+          dg[k] = T::pack2(d0 * u0 * fmaf(-h0, s0, s0 + h0), d1 * u1 * fmaf(-h1, s1, s1 + h1));
+          du[k] = T::pack2(d0 * h0, d1 * h1);
         }
         if (i < sh.I && 8 * p + r < jn) {
           *reinterpret_cast<uint4*>(out + 8 * p * ld) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
@@ -642,6 +664,8 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       }
       const uint32_t b = buf & 1, use = buf >> 1;
       ++buf;
+      Saved saved;
+      if (OP == kDx && ACT) load_saved(a, sh, x, i_cta + 32 * q, 32 * half, saved);
       if (!(ok = wait(&bars.tfull[b], use & 1, 2 + x.nkb / 65536))) break;
       fence_after();
       const uint32_t src = tmem + b * NT + ((uint32_t)(q * 32) << 16);
@@ -651,7 +675,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
           drain_dw<T, F32>(sh, &map_out, x, i_cta + 32 * q, c0, src, stage);
       } else {
         for (int c0 = 32 * half; c0 < x.jn; c0 += 64)
-          drain<OP, T, ACT>(a, sh, x, i_cta + 32 * q, c0, src, stage);
+          drain<OP, T, ACT>(a, sh, x, i_cta + 32 * q, c0, src, stage, saved);
       }
       fence_before();
       __syncwarp();

@@ -49,7 +49,7 @@ struct Shape {
   int tiles_n;   // tiles along the weight rows
   int KG;        // groups of k
   int shift;     // log2 of a group's length
-  int vec;       // rows of scales are whole 16-byte pieces
+  int vec;       // rows of scales are whole pieces of 8 groups (2), of 4 (1)
   int stages;    // stages of the ring
 };
 
@@ -436,7 +436,7 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
         for (int w = 0; w < kW / 2; ++w) zv[b][w] = 0;
         if (!in[b]) continue;
         const size_t at = row_at[b] + first;
-        if (sh.vec) {
+        if (sh.vec == 2) {
           // 4 groups (of 128), 8, or twice 8, the second of which may not exist
           const uint16_t* from = scales + at;
           const uint8_t* zfrom = a.zeros4 + at;
@@ -456,6 +456,14 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
                 }
               }
           }
+        } else if (sh.vec == 1) {
+#pragma unroll
+          for (int w = 0; w < kW; w += 2)
+            if (2 * w < ng && first + 2 * w < sh.KG) {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(scales + at + 2 * w));
+              sv[b][w] = v.x, sv[b][w + 1] = v.y;
+              if (ZEROS) zv[b][w / 2] = __ldg(reinterpret_cast<const uint32_t*>(a.zeros4 + at + 2 * w));
+            }
         } else {
 #pragma unroll
           for (int k = 0; k < St::kGroups; ++k)
@@ -535,7 +543,7 @@ cudaError_t launch_t(const Args& a, cudaStream_t s) {
   sh.tiles_n = (a.N + St::kRows - 1) / St::kRows;
   sh.shift = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
   sh.KG = a.K / a.group;
-  sh.vec = sh.KG % 8 == 0;
+  sh.vec = sh.KG % 8 == 0 ? 2 : sh.KG % 4 == 0 ? 1 : 0;
   const uint64_t G = a.G, R = a.R, N = a.N, K = a.K;
   CUtensorMap mw, mx[2];
   // codes: the two halves of a tile in one copy; x: 16 blocks of 32 of k in one

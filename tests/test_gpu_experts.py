@@ -146,6 +146,30 @@ def test_experts_do_not_touch_each_other(dtype):
     assert bool(torch.isnan(y[37:58]).all()) and bool(torch.isnan(gw[1]).any())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_swiglu_far_from_zero(dtype):
+    """Gates of +-0 to +-300 (exp overflows in 32 bits past 88): SwiGLU goes to u g or to 0, its gradient to d u and
+    d g or to 0, never to NaN."""
+    code, dt = DT[dtype]
+    k, n = 64, 64
+    g = torch.tensor([0.0, -0.0, 1e-3, -1e-3, 5, -5, 20, -20, 86, -86, 89, -89, 110, -110, 300, -300]).repeat(4)
+    x = torch.zeros(n, k)
+    x[:, 0], x[:, 1] = g, torch.linspace(-2, 2, n)  # row r: gate g[r], up x[r, 1], whatever the column
+    w = torch.zeros(1, 2 * n, k)
+    w[0, :n, 0], w[0, n:, 1] = 1, 1
+    x, w = x.to(dt), w.to(dt)
+    cfg = cq.ExpertConfig(experts=1, rows=n, n=n, k=k, x_dtype=code, act=1)
+    y = cq.expert_matmul(cfg, x.to(DEV), w.to(DEV), _counts([n]))
+    want, bound, p, _ = ref.forward(x, w, [n], 1, dt)
+    ref.check(y, want, bound, "y")
+    d = torch.randn(n, k, generator=_rng("far")).to(dt)
+    eye = torch.eye(k).to(dt)[None]
+    pre = p.to(dt)
+    cfg = cq.ExpertConfig(experts=1, rows=n, n=k, k=k, x_dtype=code)
+    got = cq.expert_matmul_dx(cfg, d.to(DEV), eye.to(DEV), _counts([n]), pre=pre.to(DEV))
+    ref.check(got, *ref.dx(d, eye, [n], dt, pre), "dpre")
+
+
 # -------------------------------------------------------------------------------------------------
 # MX fp8
 # -------------------------------------------------------------------------------------------------
