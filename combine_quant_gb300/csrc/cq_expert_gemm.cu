@@ -67,6 +67,12 @@ struct Shape {
   int whole;           // MN-major operands are whole blocks of 64: one copy takes two of them
 };
 
+// B by rows (K-major) in copies of 64 and of 32: an expert's last part of the
+// tokens rarely fills one of 128, and the rest would be another expert's rows.
+struct FewMaps {
+  CUtensorMap b64, b32;
+};
+
 struct Bars {
   uint64_t full[8], empty[8], tail[8], tail_full[8];
   uint64_t swritten[4], sfull[4], sempty[4];  // mx: scales written, visible to the copies, used
@@ -296,7 +302,7 @@ template <Op OP, typename T, bool F32, bool ACT, bool MX>
 __global__ void __launch_bounds__(kThreads<MX>, 1)
 gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
             const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-            const __grid_constant__ CUtensorMap map_out) {
+            const __grid_constant__ CUtensorMap map_out, const __grid_constant__ FewMaps few) {
   constexpr int S = kStages<OP, ACT, MX>;
   constexpr int SB = kStageBytes;
   constexpr int NT = kNT<MX>, KB = MX ? 128 : 64;  // columns; contraction of a stage
@@ -367,10 +373,12 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       const Tile x = tile_at<OP, MX>(sh, s_begin, s_tile, a.G, t);
       const int i_cta = x.i0 + (int)rank * 128;
       const int jh = half_cols(x), jb = x.j0 + (int)rank * jh;
-      const int box = B_MN && !sh.whole ? 64 : 128;  // columns of one copy
-      const int nbox = (jh + box - 1) / box;
       const bool ragged = OP == kDw && (x.kk & 15) != 0;
-      const uint32_t bytes = kABytes + nbox * (box * 128);
+      // B_MN: whole blocks of 64 (two per copy, or one); else 128 rows, 64, 32, or 64 + 32
+      const int n64 = (jh + 63) / 64;
+      const bool b128 = jh > 96, b64 = !b128 && jh > 32, b32 = !b128 && (jh <= 32 || jh > 64);
+      const uint32_t bytes =
+          kABytes + (B_MN ? (sh.whole ? 2 : n64) * 8192 : b128 ? 16384 : (b64 ? 8192 : 0) + (b32 ? 4096 : 0));
       for (int kb = 0; kb < x.nkb; ++kb) {
         if (lap > 0 && !(ok = wait(&bars.empty[s], (lap & 1) ^ 1, 1))) break;
         if (elect_one()) {
@@ -408,11 +416,13 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
             }
           }
           if constexpr (!B_MN) {
-            tma_load2(sb, &map_b, k0, x.begin + jb, bar);
+            if (b128) tma_load2(sb, &map_b, k0, x.begin + jb, bar);
+            if (b64) tma_load2(sb, &few.b64, k0, x.begin + jb, bar);
+            if (b32) tma_load2(sb + (b64 ? 8192 : 0), &few.b32, k0, x.begin + jb + (b64 ? 64 : 0), bar);
           } else if (sh.whole) {
             tma_load3<2>(sb, &map_b, 0, x.begin + k0, jb / 64, bar);
           } else {
-            for (int b = 0; b < nbox; ++b)
+            for (int b = 0; b < n64; ++b)
               tma_load2(sb + b * 8192, &map_b, jb + b * 64, x.begin + k0, bar);
           }
         }
@@ -693,7 +703,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
 // ---- host ----
 template <Op OP, typename T, bool F32, bool ACT, bool MX>
 cudaError_t launch_t(const Args& a, const Shape& sh, const CUtensorMap& ma, const CUtensorMap& mb,
-                     const CUtensorMap& out, cudaStream_t s) {
+                     const CUtensorMap& out, const FewMaps& few, cudaStream_t s) {
   constexpr auto kernel = gemm_kernel<OP, T, F32, ACT, MX>;
   const size_t smem = 1024 + (size_t)kStages<OP, ACT, MX> * kStageBytes +
                       kDrainWarps * kStagingBytes<OP, ACT> +
@@ -717,7 +727,15 @@ cudaError_t launch_t(const Args& a, const Shape& sh, const CUtensorMap& ma, cons
   attr[1].val.clusterDim = {2, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, a, sh, ma, mb, out);
+  return cudaLaunchKernelEx(&cfg, kernel, a, sh, ma, mb, out, few);
+}
+
+// B's maps, rows of K elements 64 (16-bit) or 128 (bytes) at a time.
+bool make_b(CUtensorMap* mb, FewMaps* few, const void* p, MapType type, uint64_t cols, uint64_t rows) {
+  const uint64_t size = type == kMapU8 ? 1 : 2, d[] = {cols, rows}, st[] = {size * cols};
+  const uint32_t inner = type == kMapU8 ? 128 : 64, b[] = {inner, 128}, b64[] = {inner, 64}, b32[] = {inner, 32};
+  return make_map(mb, p, type, 2, d, st, b) && make_map(&few->b64, p, type, 2, d, st, b64) &&
+         make_map(&few->b32, p, type, 2, d, st, b32);
 }
 
 template <typename T>
@@ -725,34 +743,31 @@ cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
   const MapType type = T::kBf16 ? kMapBF16 : kMapF16;
   const uint64_t G = a.G, R = a.R, N = a.N, K = a.K;
   CUtensorMap ma, mb;
+  FewMaps few = {};
   Shape sh = {};
   if (op == kForward) {
     sh.n_out = a.act ? a.N / 2 : a.N;
     sh.I = a.N;
     sh.KK = a.K;
     sh.tiles_i = (a.N + 255) / 256;
-    const uint64_t db[] = {K, R}, sb[] = {2 * K};
-    const uint32_t bb[] = {64, 128};
-    if (!make_map(&mb, a.x, type, 2, db, sb, bb)) return cudaErrorUnknown;
+    if (!make_b(&mb, &few, a.x, type, K, R)) return cudaErrorUnknown;
     if (a.act) {
       const uint64_t n = N / 2, d[] = {K, 16, 2, n / 16, G}, st[] = {2 * K, 2 * n * K, 32 * K, 2 * N * K};
       const uint32_t b[] = {64, 16, 2, 4, 1};
       if (!make_map(&ma, a.w, type, 5, d, st, b)) return cudaErrorUnknown;
-      return launch_t<kForward, T, false, true, false>(a, sh, ma, mb, ma, s);
+      return launch_t<kForward, T, false, true, false>(a, sh, ma, mb, ma, few, s);
     }
     const uint64_t d[] = {K, N, G}, st[] = {2 * K, 2 * N * K};
     const uint32_t b[] = {64, 128, 1};
     if (!make_map(&ma, a.w, type, 3, d, st, b)) return cudaErrorUnknown;
-    return launch_t<kForward, T, false, false, false>(a, sh, ma, mb, ma, s);
+    return launch_t<kForward, T, false, false, false>(a, sh, ma, mb, ma, few, s);
   }
   if (op == kDx) {
     sh.I = a.K;
     sh.tiles_i = (a.K + 255) / 256;
     sh.KK = a.N;
     sh.whole = K % 64 == 0;
-    const uint64_t db[] = {N, R}, sb[] = {2 * N};
-    const uint32_t bb[] = {64, 128};
-    if (!make_map(&mb, a.x, type, 2, db, sb, bb)) return cudaErrorUnknown;
+    if (!make_b(&mb, &few, a.x, type, N, R)) return cudaErrorUnknown;
     if (sh.whole) {
       const uint64_t d[] = {64, N, K / 64, G}, st[] = {2 * K, 128, 2 * N * K};
       const uint32_t b[] = {64, 64, 2, 1};
@@ -762,8 +777,8 @@ cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
       const uint32_t b[] = {64, 64, 1};
       if (!make_map(&ma, a.w, type, 3, d, st, b)) return cudaErrorUnknown;
     }
-    return a.pre_in ? launch_t<kDx, T, false, true, false>(a, sh, ma, mb, ma, s)
-                    : launch_t<kDx, T, false, false, false>(a, sh, ma, mb, ma, s);
+    return a.pre_in ? launch_t<kDx, T, false, true, false>(a, sh, ma, mb, ma, few, s)
+                    : launch_t<kDx, T, false, false, false>(a, sh, ma, mb, ma, few, s);
   }
   sh.I = a.N;
   sh.J = a.K;
@@ -787,8 +802,8 @@ cudaError_t launch_op(Op op, const Args& a, cudaStream_t s) {
   const uint32_t bd[] = {f32 ? 16u : 32u, 32, 1};
   CUtensorMap md;
   if (!make_map(&md, a.out, f32 ? kMapF32 : type, 3, dd, sd, bd, kSwizzle64)) return cudaErrorUnknown;
-  return f32 ? launch_t<kDw, T, true, false, false>(a, sh, ma, mb, md, s)
-             : launch_t<kDw, T, false, false, false>(a, sh, ma, mb, md, s);
+  return f32 ? launch_t<kDw, T, true, false, false>(a, sh, ma, mb, md, few, s)
+             : launch_t<kDw, T, false, false, false>(a, sh, ma, mb, md, few, s);
 }
 
 // Forward from mx fp8 operands; T is the output's type.
@@ -796,24 +811,23 @@ template <typename T>
 cudaError_t launch_mx(const Args& a, cudaStream_t s) {
   const uint64_t G = a.G, R = a.R, N = a.N, K = a.K;
   CUtensorMap ma, mb;
+  FewMaps few = {};
   Shape sh = {};
   sh.n_out = a.act ? a.N / 2 : a.N;
   sh.I = a.N;
   sh.KK = a.K;
   sh.tiles_i = (a.N + 255) / 256;
-  const uint64_t db[] = {K, R}, sb[] = {K};
-  const uint32_t bb[] = {128, 128};
-  if (!make_map(&mb, a.x, kMapU8, 2, db, sb, bb)) return cudaErrorUnknown;
+  if (!make_b(&mb, &few, a.x, kMapU8, K, R)) return cudaErrorUnknown;
   if (a.act) {
     const uint64_t n = N / 2, d[] = {K, 16, 2, n / 16, G}, st[] = {K, n * K, 16 * K, N * K};
     const uint32_t b[] = {128, 16, 2, 4, 1};
     if (!make_map(&ma, a.w, kMapU8, 5, d, st, b)) return cudaErrorUnknown;
-    return launch_t<kForward, T, false, true, true>(a, sh, ma, mb, ma, s);
+    return launch_t<kForward, T, false, true, true>(a, sh, ma, mb, ma, few, s);
   }
   const uint64_t d[] = {K, N, G}, st[] = {K, N * K};
   const uint32_t b[] = {128, 128, 1};
   if (!make_map(&ma, a.w, kMapU8, 3, d, st, b)) return cudaErrorUnknown;
-  return launch_t<kForward, T, false, false, true>(a, sh, ma, mb, ma, s);
+  return launch_t<kForward, T, false, false, true>(a, sh, ma, mb, ma, few, s);
 }
 
 }  // namespace
