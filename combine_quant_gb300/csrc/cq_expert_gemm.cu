@@ -1,25 +1,44 @@
 // cq_expert_gemm.cu -- grouped matrix products of the experts on the tensor
-// cores (tcgen05): forward, gradient of the input, gradient of the weights.
+// cores (tcgen05): forward (16-bit operands, or mx fp8 with block scales),
+// gradient of the input, gradient of the weights.
 //
-// One persistent kernel. An output tile is TILE_I x up to 256 elements of
-// out[j, i], i being the contiguous axis. The axis i lies on the accumulator's
-// 128 lanes (so a warp's store of one column is contiguous) and j on its
-// columns, whose number is free in steps of 16: the ragged axis of the forward
-// product and of the input's gradient, the tokens, is j, so an expert with 3
-// rows costs 16 columns, not a padded tile of 128.
+// One persistent kernel on pairs of CTAs (cta_group::2). An output tile is 256 x
+// up to 256 elements of out[j, i]. The axis i lies on the accumulator's lanes
+// (128 in each CTA) and j on its columns, whose number is free in steps of 16:
+// the ragged axis of the forward product and of the input's gradient, the
+// tokens, is j, so an expert with 3 rows costs 16 columns, not a padded tile.
 //
 //   forward  out = y,  i = weight rows, j = tokens, sum over k:  A = w (K-major),  B = x (K-major)
 //   dx       out = dx, i = weight cols, j = tokens, sum over n:  A = w (MN-major), B = dy (K-major)
 //   dw       out = dw, i = columns of dy, j = columns of x, sum over the expert's
 //            rows:  A = dy (MN-major), B = x (MN-major); here j is the contiguous axis
 //
+// Every CTA reads the counts itself and walks the same list of tiles (group_scan
+// in cq_expert.cuh): no host read, no extra launch, any counts.
+//
 // Warp 0 fills a ring of shared-memory stages with tiled copies (64 of the
-// contraction, 128-byte swizzle), warp 1 issues the products into one of two
-// TMEM accumulators, warps 4-7 drain the other one. SwiGLU: the tile's weight
-// rows are 16 gate rows, 16 up rows, 16 gate rows, ... (one 5-D copy picks them
-// up in that order), so that a gate and its up product sit 16 lanes apart in
-// one warp. dw's last rows: those of the next expert that the copy brings in
-// are overwritten with zeros by warp 2 before the product reads them.
+// contraction, or 128 bytes of fp8; 128-byte swizzle; each CTA its half of A and
+// of B), warp 1 of the first CTA issues the products into one of two TMEM
+// accumulators, warps 4-11 drain the other one. A whole warp runs each of these
+// loops and one elected lane issues: with a single thread in the loop the issue
+// itself was the bound (1560 instead of 1870 TFLOP/s at 8192^3).
+//
+// SwiGLU: a tile's weight rows are 16 gate rows, 16 up rows, 16 gate rows, ...
+// (one 5-D copy picks them up in that order), so that the 16-lane TMEM loads
+// give a thread a gate and its up product; both are f32 until the result is
+// rounded. Its gradient (dx with the saved products) multiplies in the drain.
+// dw's last rows: those of the next expert that a copy brings in are overwritten
+// with zeros by warp 2 before the products read them.
+// mx: four warps fetch the scales, tcgen05.cp puts them into TMEM a stage ahead
+// of their products.
+//
+// What bounds it: below about 280 rows an expert reading the weights, above the
+// tensor cores. Measured on one GB300 (copy 6.79 TB/s, cuBLAS bf16 1.88 PFLOP/s
+// measured): 8192^3 1.9 PFLOP/s; 32 experts of 512 rows, hidden 7168, SwiGLU with
+// n 2048: 544 us, 1.77 PFLOP/s; 64 experts, 777 rows in fp16, n 1536, k 4096:
+// 116 us, 6.2 TB/s; mx fp8, 32 experts of 480 rows: 340 us, 2.65 PFLOP/s, of 16
+// rows (n 7168, k 2048): 89 us, 5.5 TB/s; dw, 32 experts of 512 rows, 4096 x 7168:
+// 668 us, 1.44 PFLOP/s (its 1.9 GB of results and eight stages per tile).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -338,7 +357,8 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     async::mbar_fence_init();
   }
   if (warp == 1) tmem_alloc(&bars.tmem, kTmemCols);
-  griddep_launch_dependents();  // its CTAs do the above while ours still work
+  // No early release of the next kernel here: the permute kernel reads token rows
+  // before its own wait, and they may be these results.
   griddep_wait();
   const bool bad = group_scan<kThreads<MX>>(a, s_begin, s_tile, [&](int rows) {
     return OP == kDw ? sh.tiles_i * sh.tiles_j : sh.tiles_i * ((rows + NT - 1) / NT);

@@ -17,6 +17,14 @@
 // the sums of x. Warps 20-21 bring the scales as floats in the order the
 // multiplying threads read them. Warps 0-15 multiply: 4 shares of k times 4 of
 // the rows; the four k shares' sums are added in a fixed order at the end.
+//
+// mma.sync rather than tcgen05: the codes have to pass through registers anyway,
+// and a group's sum has to come back to them to meet its scale. What bounds it:
+// the codes' bytes as far as the memory goes (5.9 TB/s with the multiplying taken
+// out), in practice the multiplying warps' instructions. Measured on one GB300, 32
+// experts, hidden 7168, SwiGLU with n 2048, groups of 128 (485 MB): up to 8 rows an
+// expert 109 us (4.4 TB/s), 16 rows 139 us, every further 16 rows about 130 us; one
+// row through 8192 x 8192 15.6 us, with groups of 32 and zero points 20 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -272,7 +280,6 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     }
     async::mbar_fence_init();
   }
-  griddep_launch_dependents();
   griddep_wait();
   const bool bad = group_scan<kThreads>(a, s_begin, s_tile, [&](int rows) {
     return sh.tiles_n * ((rows + 8 * NTMAX - 1) / (8 * NTMAX));
@@ -580,7 +587,9 @@ cudaError_t launch_g(const Args& a, cudaStream_t s) {
                        : launch_t<T, MTW, NTMAX, ACT, false, false>(a, s);
 }
 
-// Tiles of 128 weight rows where they give every SM two, else of 64.
+// Tiles of 128 weight rows where they give every SM two, else of 64 (a tile of 64
+// takes about 0.6 of the time of one of 128, so it pays where SMs would idle:
+// 8192 x 8192 has 64 tiles of 128 and 128 of 64).
 template <typename T, bool ACT>
 cudaError_t launch_a(const Args& a, cudaStream_t s) {
   const int64_t rows = (int64_t)std::min(a.G, a.R) * a.N;  // most weight rows read

@@ -23,8 +23,8 @@
  *     is current when the call is made (the library sizes launches, caches
  *     per-device state and finds its built-in arrays by the current device),
  *     and every pointer refers to that device's memory. Work is enqueued on
- *     it and the call returns without synchronising (except cq_read_status
- *     and cq_read_combine_status).
+ *     it and the call returns without synchronising (except cq_read_status,
+ *     cq_read_combine_status and cq_read_expert_status).
  *   - Return 0 (CQ_OK) or a negative CQ_ERR_* code. Argument errors are found
  *     on the host before anything is enqueued; nothing is enqueued then.
  *   - Data-dependent problems found on the device (an out-of-range expert
@@ -79,7 +79,8 @@ typedef struct cq_config {
 enum {
   CQ_OK = 0,
   CQ_ERR_ARG = -1,         /* a range or divisibility rule broken, or a required pointer NULL */
-  CQ_ERR_UNSUPPORTED = -2, /* H not a multiple of 16 (32 for quant_mode 4 and 5) */
+  CQ_ERR_UNSUPPORTED = -2, /* H not a multiple of 16 (32 for quant_mode 4 and 5); an expert
+                              product's n or k likewise */
   CQ_ERR_CUDA = -3,        /* a CUDA launch or query failed */
   CQ_ERR_WORKSPACE = -4,   /* workspace smaller than cq_workspace_size() or misaligned */
   CQ_ERR_TOO_LARGE = -5    /* cq_dispatch_noalloc: the problem needs more scratch than
@@ -309,7 +310,7 @@ int cq_dispatch_noalloc(const cq_config* cfg, const void* x, const int32_t* expe
                         int64_t* expert_token_nums, float* expand_scales, void* stream);
 
 /* Synchronise `stream`, copy the workspace status word into *status and clear
- * it. One of the two calls in this library that wait for the device. */
+ * it. One of the calls of this library that wait for the device. */
 int cq_read_status(void* workspace, uint32_t* status, void* stream);
 
 /* cq_combine and cq_combine_q8 take no workspace; their status word
