@@ -404,6 +404,78 @@ def test_directional_derivative():
             assert abs(float(got) - want) < slack
 
 
+def _check_rows(got, x, w, what):
+    """Rows of products against 64 bits on the GPU, with the bounds of expert_ref."""
+    v, b = x.double() @ w.double().T, x.shape[1] * ref.EPS * (x.double().abs() @ w.double().abs().T)
+    over = (got.double() - v).abs() - ref.rounded(v, b, got.dtype)
+    assert over.max() <= 0, (what, float(over.max()))
+
+
+def test_offsets_beyond_32_bits():
+    """Weights, rows, codes and gradients of more than 2^32 bytes and 2^31 elements: the last expert's and the last
+    rows' results are right."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(8)
+    bf = dict(dtype=torch.bfloat16, device=DEV)
+    # weights and their gradient: 36 x 8192 x 8192 (2.4e9 elements), rows for the first and last experts only
+    G, n, k, counts = 36, 8192, 8192, [3] + [0] * 34 + [21]
+    w = torch.empty(G, n, k, **bf).normal_(0, 0.01, generator=gen)
+    x, dy = torch.empty(24, k, **bf).normal_(generator=gen), torch.empty(24, n, **bf).normal_(generator=gen)
+    cfg = cq.ExpertConfig(experts=G, rows=24, n=n, k=k, group=128)
+    g = _counts(counts)
+    y = cq.expert_matmul(cfg, x, w, g)
+    d = cq.expert_matmul_dx(cfg, dy, w, g)
+    for at, e in ((slice(0, 3), 0), (slice(3, 24), G - 1)):
+        _check_rows(y[at], x[at], w[e], "y")
+        _check_rows(d[at], dy[at], w[e].T, "dx")
+    dw = cq.expert_matmul_dw(cfg, dy, x, g, dw=w)  # over the weights: they are done
+    _check_rows(dw[G - 1], dy[3:].T, x[3:].T, "dw")
+    assert not bool(dw[1].any()) and not bool(dw[G - 2].any())
+    del w, dw
+    # codes: 72 x 16384 x 4096 bytes (4.8e9)
+    G, n, counts = 72, 16384, [2] + [0] * 70 + [5]
+    codes = torch.randint(0, 256, (G, n, k // 2), dtype=torch.uint8, generator=gen, device=DEV)
+    scales = torch.full((G, n, k // 128), 0.01, **bf)
+    cfg = cq.ExpertConfig(experts=G, rows=7, n=n, k=k, group=128)
+    y = cq.expert_matmul_w4(cfg, x[:7], codes, scales, _counts(counts))
+    c = codes[G - 1]
+    v = torch.stack((c & 15, c >> 4), -1).view(n, k).to(torch.bfloat16) - 8
+    want = x[2:7].double() @ v.double().T * scales[0, 0, 0].double()
+    slack = k * ref.EPS * 286 * 0.0101 * x[2:7].double().abs().sum(1, keepdim=True)
+    assert bool(((y[2:].double() - want).abs() <= ref.rounded(want, slack, torch.bfloat16)).all())
+    del codes, scales, c, v
+    # rows: 300000 x 8192 (2.5e9 elements) in, 300000 x 16 out and back
+    R, n = 300000, 16
+    x = torch.empty(R, k, **bf).normal_(generator=gen)
+    w = torch.empty(2, n, k, **bf).normal_(0, 0.01, generator=gen)
+    cfg = cq.ExpertConfig(experts=2, rows=R, n=n, k=k)
+    g = _counts([299000, 1000])
+    y = cq.expert_matmul(cfg, x, w, g)
+    _check_rows(y[-1500:-1000], x[-1500:-1000], w[0], "y")
+    _check_rows(y[-1000:], x[-1000:], w[1], "y")
+    d = cq.expert_matmul_dx(cfg, y, w, g)
+    _check_rows(d[-1000:], y[-1000:], w[1].T, "dx")
+    dw = cq.expert_matmul_dw(cfg, y, x, g)
+    _check_rows(dw[1], y[-1000:].T, x[-1000:].T, "dw")
+    assert cq.read_expert_status() == 0
+
+
+def test_misaligned_tensors_are_refused():
+    cfg, (x, dy, w, codes, scales) = _small(4, 12)
+    g = _counts([3, 3, 3, 3])
+    buf = torch.empty(12 * 64 + 8, dtype=torch.bfloat16, device=DEV)
+    for off in (1, 2, 4):
+        odd = buf[off:off + 12 * 32].view(12, 32)
+        with pytest.raises(cq.CqError) as err:
+            cq.expert_matmul(cfg, x, w, g, y=odd)
+        assert err.value.code == _lib.CQ_ERR_ARG
+        with pytest.raises(cq.CqError):
+            cq.expert_matmul_dw(cfg, odd, x, g)
+    cq.expert_matmul(cfg, x, w, g, y=buf[8:8 + 12 * 32].view(12, 32))  # 16 bytes are enough
+    cq.expert_matmul_dw(cfg, buf[8:8 + 12 * 32].view(12, 32), x, g)
+    torch.cuda.synchronize()
+
+
 def test_python_refusals():
     cfg, (x, dy, w, codes, scales) = _small(4, 12)
     g = _counts([3, 3, 3, 3])
