@@ -486,24 +486,22 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       __syncwarp();
       return true;
     };
-    // mx: entry of scales; set of 12 TMEM columns (A then B) to fill, to use
+    // mx: entry of scales; set of 12 TMEM columns (A then B) to fill, to use. Stage
+    // kb's scales are copied by one lane (copy), once they are there (waits).
     uint32_t se = 0, se_lap = 0, sf_fill = 0, sf_use = 0;
-    auto scales_in = [&](int kb, int nkb, bool wide) {
-      if ((kb & 3) == 0 && !wait(&bars.sfull[se], se_lap & 1, 1, true)) return false;
-      const bool last = (kb & 3) == 3 || kb == nkb - 1;
-      fence_after();
-      if (elect_one()) {
-        const uint32_t sf = tmem + 2 * NT + 12 * sf_fill;
-        const uint64_t ds = desc_scales(smem_u32(s_sf) + (se * 4 + (kb & 3)) * kScaleBytes);
-        copy_scales(sf, ds);
-        copy_scales(sf + 4, ds + (512 >> 4));
-        if (wide) copy_scales(sf + 8, ds + (1024 >> 4));
-        if (last) commit(smem_u32(&bars.sempty[se]));
-      }
-      __syncwarp();
+    const uint64_t sf_desc = desc_scales(smem_u32(s_sf));
+    auto scales_wait = [&](int kb) { return (kb & 3) != 0 || wait(&bars.sfull[se], se_lap & 1, 1, true); };
+    auto scales_copy = [&](int kb, int nkb, bool wide) {
+      const uint32_t sf = tmem + 2 * NT + 12 * sf_fill;
+      const uint64_t ds = sf_desc + (se * 4 + (kb & 3)) * (kScaleBytes >> 4);
+      copy_scales(sf, ds);
+      copy_scales(sf + 4, ds + (512 >> 4));
+      if (wide) copy_scales(sf + 8, ds + (1024 >> 4));
+      if ((kb & 3) == 3 || kb == nkb - 1) commit(smem_u32(&bars.sempty[se]));
+    };
+    auto scales_next = [&](int kb, int nkb) {
       sf_fill ^= 1;
-      if (last && ++se == kScaleRing) se = 0, ++se_lap;
-      return true;
+      if (((kb & 3) == 3 || kb == nkb - 1) && ++se == kScaleRing) se = 0, ++se_lap;
     };
     bool ok = true;
     for (int t = first; t < n_tiles && ok; t += step) {
@@ -529,14 +527,22 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
         if (!(ok = wait(&bars.full[s], lap & 1, 1))) break;
         // mx: the next stage's scales go into the other set of TMEM columns ahead of
         // this stage's products, which then need not wait for a copy
-        if (MX && kb == 0 && !(ok = scales_in(0, x.nkb, half_cols(x) * 2 > 128))) break;
-        if (MX && kb + 1 < x.nkb && !(ok = scales_in(kb + 1, x.nkb, half_cols(x) * 2 > 128))) break;
+        const bool more = kb + 1 < x.nkb, wide = MX && half_cols(x) * 2 > 128;
+        if (MX && kb == 0) {
+          if (!(ok = scales_wait(0))) break;
+          fence_after();
+          if (elect_one()) scales_copy(0, x.nkb, wide);
+          __syncwarp();
+          scales_next(0, x.nkb);
+        }
+        if (MX && more && !(ok = scales_wait(kb + 1))) break;
         fence_after();
         if (elect_one()) {
           const uint64_t ad = da + s * (SB >> 4), bd = db + s * (SB >> 4);
           const int left = x.kk - (kb - lead_kb) * KB;
           const bool add = kb > lead_kb;
           if constexpr (MX) {
+            if (more) scales_copy(kb + 1, x.nkb, wide);
             const uint32_t sf = tmem + 2 * NT + 12 * sf_use;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -554,7 +560,10 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
           commit(smem_u32(&bars.empty[s]));
         }
         __syncwarp();
-        sf_use ^= 1;
+        if constexpr (MX) {
+          sf_use ^= 1;
+          if (more) scales_next(kb + 1, x.nkb);
+        }
         if (++s == S) s = 0, ++lap;
         if (ragged && kb == min(kLate, x.nkb - 1))
           if (!(ok = finish_late(late, d, idesc, x.kk - (x.nkb - 1) * KB, true))) break;
