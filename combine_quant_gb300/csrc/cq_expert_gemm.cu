@@ -29,15 +29,15 @@
 // rounded. Its gradient (dx with the saved products) multiplies in the drain.
 // dw's last rows: those of the next expert that a copy brings in are overwritten
 // with zeros by warp 2 before the products read them.
-// mx: four warps fetch the scales, tcgen05.cp puts them into TMEM a stage ahead
+// mx: three warps fetch the scales, tcgen05.cp puts them into TMEM a stage ahead
 // of their products.
 //
 // What bounds it: below about 280 rows an expert reading the weights, above the
 // tensor cores. Measured on one GB300 (copy 6.79 TB/s, cuBLAS bf16 1.88 PFLOP/s
 // measured): 8192^3 1.9 PFLOP/s; 32 experts of 512 rows, hidden 7168, SwiGLU with
 // n 2048: 544 us, 1.77 PFLOP/s; 64 experts, 777 rows in fp16, n 1536, k 4096:
-// 116 us, 6.2 TB/s; mx fp8, 32 experts of 480 rows: 340 us, 2.65 PFLOP/s, of 16
-// rows (n 7168, k 2048): 89 us, 5.5 TB/s; dw, 32 experts of 512 rows, 4096 x 7168:
+// 116 us, 6.2 TB/s; mx fp8, 32 experts of 480 rows: 326 us, 2.77 PFLOP/s, of 16
+// rows (n 7168, k 2048): 87 us, 5.4 TB/s; dw, 32 experts of 512 rows, 4096 x 7168:
 // 668 us, 1.44 PFLOP/s (its 1.9 GB of results and eight stages per tile).
 #include <cuda_runtime.h>
 
@@ -58,7 +58,7 @@ using async::mbar_wait;
 __device__ uint32_t g_status;  // CQ_ST_* bits of these kernels on this device
 
 constexpr int kDrainWarps = 8;             // two for each quarter of the lanes
-constexpr int kScaleWarps = 4;             // mx: fetch the scales
+constexpr int kScaleWarps = 3;             // mx: fetch the scales, 128 rows each
 template <bool MX>
 constexpr int kThreads = 128 + 32 * kDrainWarps + (MX ? 32 * kScaleWarps : 0);
 // Most columns (j) of a tile. Two accumulators of 256 fill TMEM; mx needs 24
@@ -514,6 +514,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       const uint32_t idesc =
           MX ? idesc_mx(a.w_dtype, a.x_dtype == kMxE5M2, 256, half_cols(x) * 2)
              : idesc_f16(T::kBf16, A_MN, B_MN, 256, half_cols(x) * 2);
+      const bool wide = MX && half_cols(x) * 2 > 128;
       const bool ragged = OP == kDw && (x.kk & 15) != 0;
       const int lead_kb = ragged ? 1 : 0;  // the first stage whose products go in at once
       uint32_t late = 0;
@@ -527,7 +528,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
         if (!(ok = wait(&bars.full[s], lap & 1, 1))) break;
         // mx: the next stage's scales go into the other set of TMEM columns ahead of
         // this stage's products, which then need not wait for a copy
-        const bool more = kb + 1 < x.nkb, wide = MX && half_cols(x) * 2 > 128;
+        const bool more = kb + 1 < x.nkb;
         if (MX && kb == 0) {
           if (!(ok = scales_wait(0))) break;
           fence_after();
@@ -544,10 +545,15 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
           if constexpr (MX) {
             if (more) scales_copy(kb + 1, x.nkb, wide);
             const uint32_t sf = tmem + 2 * NT + 12 * sf_use;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (32 * q < left)
+            if (left > 96) {
+              mma_mx(d, ad, bd, idesc, sf, sf + 4, add);
+              mma_mx(d, ad + ka, bd + kbs, idesc_sf(idesc, 1), sf, sf + 4, true);
+              mma_mx(d, ad + 2 * ka, bd + 2 * kbs, idesc_sf(idesc, 2), sf, sf + 4, true);
+              mma_mx(d, ad + 3 * ka, bd + 3 * kbs, idesc_sf(idesc, 3), sf, sf + 4, true);
+            } else {
+              for (int q = 0; 32 * q < left; ++q)
                 mma_mx(d, ad + q * ka, bd + q * kbs, idesc_sf(idesc, q), sf, sf + 4, add || q > 0);
+            }
           } else if (left > 48) {
             mma_f16(d, ad, bd, idesc, add);
             mma_f16(d, ad + ka, bd + kbs, idesc, true);
@@ -598,26 +604,26 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
   } else if (MX && warp >= 4 + kDrainWarps) {
     // ---- scales: one word (4 blocks of 32) a row and stage ----
     // Line r % 32 of a 512-byte atom holds the words of rows r % 32 + 0, 32, 64,
-    // 96. A warp takes three of the twelve sets of 32 rows (four of A, eight of
-    // B), four stages at a time: 16 bytes of a row per load, kAhead of them in
-    // flight, across tiles. The fence that the tensor copies need would wait for
-    // those loads, so warp 3 executes it, after these warps' arrivals.
+    // 96. A warp takes one atom (A, or 128 rows of B), four stages at a time: a
+    // lane loads 16 bytes of each of its line's four rows and stores whole lines,
+    // which meet in no bank; kAhead such steps are in flight, across tiles. The
+    // fence that the tensor copies need would wait for those loads, so warp 3
+    // executes it, after these warps' arrivals.
     constexpr int kAhead = 3;
     const int w = warp - 4 - kDrainWarps;
     const int blocks = sh.KK / 32, quads = (sh.KK + 511) / 512;
     const bool whole = a.SC % 16 == 0 && a.SC == blocks;  // 16-byte pieces, no pad column
-    const uint8_t* rows[3];                               // scale rows, NULL where there is none
+    const uint8_t* rows[4];                               // scale rows, NULL where there is none
     int t_load = first, q_load = 0;
-    auto load = [&](uint4 (&v)[3]) {
+    auto load = [&](uint4 (&v)[4]) {
       if (t_load >= n_tiles) return;
       if (q_load == 0) {
         const Tile x = tile_at<OP, MX>(sh, s_begin, s_tile, a.G, t_load);
 #pragma unroll
-        for (int b = 0; b < 3; ++b) {
-          const int set = w * 3 + b;
+        for (int b = 0; b < 4; ++b) {
           rows[b] = nullptr;
-          if (set < 4) {
-            int row = x.i0 + (int)rank * 128 + 32 * set + lane;  // of the tile's weight rows
+          if (w == 0) {
+            int row = x.i0 + (int)rank * 128 + 32 * b + lane;  // of the tile's weight rows
             bool in = row < sh.I;
             if (ACT) {
               const int o = row / 32 * 16 + (lane & 15);
@@ -626,13 +632,13 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
             }
             if (in) rows[b] = a.w_scales + ((size_t)x.e * a.N + row) * a.SC;
           } else {
-            const int j = 32 * (set - 4) + lane;
+            const int j = 128 * (w - 1) + 32 * b + lane;
             if (j < x.jn) rows[b] = a.x_scales + (size_t)(x.begin + x.j0 + j) * a.SC;
           }
         }
       }
 #pragma unroll
-      for (int b = 0; b < 3; ++b) {
+      for (int b = 0; b < 4; ++b) {
         v[b] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
         if (!rows[b]) continue;
         if (whole) {
@@ -650,7 +656,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       }
       if (++q_load == quads) q_load = 0, t_load += step;
     };
-    uint4 v[kAhead][3];
+    uint4 v[kAhead][4];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) load(v[u]);
     const int total = n_tiles > first ? ((n_tiles - 1 - first) / step + 1) * quads : 0;
@@ -661,15 +667,12 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       for (int u = 0; u < kAhead; ++u) {
         if (i + u >= total || !ok) break;
         if (lap > 0 && !(ok = wait(&bars.sempty[s], (lap & 1) ^ 1, 1))) break;
-#pragma unroll
-        for (int b = 0; b < 3; ++b) {
-          const int set = w * 3 + b;
-          uint8_t* to = s_sf + s * 4 * kScaleBytes + set / 4 * 512 + lane * 16 + set % 4 * 4;
-          *reinterpret_cast<uint32_t*>(to) = v[u][b].x;
-          *reinterpret_cast<uint32_t*>(to + kScaleBytes) = v[u][b].y;
-          *reinterpret_cast<uint32_t*>(to + 2 * kScaleBytes) = v[u][b].z;
-          *reinterpret_cast<uint32_t*>(to + 3 * kScaleBytes) = v[u][b].w;
-        }
+        uint4* to = reinterpret_cast<uint4*>(s_sf + s * 4 * kScaleBytes + w * 512 + lane * 16);
+        const uint4(&r)[4] = v[u];
+        to[0] = make_uint4(r[0].x, r[1].x, r[2].x, r[3].x);
+        to[kScaleBytes / 16] = make_uint4(r[0].y, r[1].y, r[2].y, r[3].y);
+        to[2 * kScaleBytes / 16] = make_uint4(r[0].z, r[1].z, r[2].z, r[3].z);
+        to[3 * kScaleBytes / 16] = make_uint4(r[0].w, r[1].w, r[2].w, r[3].w);
         __syncwarp();
         if (lane == 0) async::mbar_arrive(&bars.swritten[s]);
         if (++s == kScaleRing) s = 0, ++lap;
