@@ -162,8 +162,12 @@ class _ExpertPlan:
 
 
 @functools.lru_cache(maxsize=256)
+def _plan_of(*fields) -> _ExpertPlan:
+    return _ExpertPlan(ExpertConfig(*fields))
+
+
 def _expert_plan(cfg: ExpertConfig) -> _ExpertPlan:
-    return _ExpertPlan(cfg)
+    return _plan_of(*vars(cfg).values())  # half the time of hashing and comparing the config itself
 
 
 class DispatchResult(NamedTuple):
@@ -487,6 +491,14 @@ def _arg(t, name, dtype, shape, dev: torch.device):
     return t.data_ptr()
 
 
+def _result(t, name, dtype, shape, dev: torch.device):
+    """A result tensor, the caller's (checked) or a new one, and its address."""
+    if t is not None:
+        return t, _arg(t, name, dtype, shape, dev)
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    return t, t.data_ptr()
+
+
 def _group_rows(p: _ExpertPlan, group_rows: torch.Tensor) -> torch.device:
     """Checks the counts; returns the device that the other tensors must be on."""
     _need(group_rows, "group_rows", torch.int64)
@@ -498,11 +510,12 @@ def _group_rows(p: _ExpertPlan, group_rows: torch.Tensor) -> torch.device:
 # The handle of the current stream, without building a torch.cuda.Stream around it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _expert_call(name: str, dev: torch.device, *args) -> None:
     fn = getattr(_lib.load(), name)
-    if torch.cuda.current_device() == dev.index:  # the library looks up the current device
+    if _current_device() == dev.index:  # the library looks up the current device
         rc = fn(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
@@ -532,12 +545,11 @@ def expert_matmul(cfg: ExpertConfig, x: torch.Tensor, w: torch.Tensor, group_row
         pws = _arg(w_scales, "w_scales", torch.uint8, p.w_scales, dev)
     elif x_scales is not None or w_scales is not None:
         raise ValueError("x_scales and w_scales go with mx types only")
-    if y is None:
-        y = torch.empty(p.y, dtype=p.result, device=dev)
     if pre is not None and p.act != 1:
         raise ValueError("pre goes with act 1 only")
-    _expert_call("cq_expert_matmul", dev, p.ref, px, pxs, pw, pws, group_rows.data_ptr(),
-                 _arg(y, "y", p.result, p.y, dev), _arg(pre, "pre", p.result, p.dy, dev))
+    ppre = _arg(pre, "pre", p.result, p.dy, dev)
+    y, py = _result(y, "y", p.result, p.y, dev)
+    _expert_call("cq_expert_matmul", dev, p.ref, px, pxs, pw, pws, group_rows.data_ptr(), py, ppre)
     return y
 
 
@@ -553,10 +565,8 @@ def expert_matmul_dx(cfg: ExpertConfig, dy: torch.Tensor, w: torch.Tensor,
     pdy, pw = _arg(dy, "dy", p.dtype, p.dy, dev), _arg(w, "w", p.dtype, p.w, dev)
     ppre = _arg(pre, "pre", p.dtype, p.pre_k, dev)
     shape = p.x if pre is None else p.pre_k
-    if dx is None:
-        dx = torch.empty(shape, dtype=p.dtype, device=dev)
-    _expert_call("cq_expert_matmul_dx", dev, p.ref, pdy, pw, group_rows.data_ptr(), ppre,
-                 _arg(dx, "dx", p.dtype, shape, dev))
+    dx, pdx = _result(dx, "dx", p.dtype, shape, dev)
+    _expert_call("cq_expert_matmul_dx", dev, p.ref, pdy, pw, group_rows.data_ptr(), ppre, pdx)
     return dx
 
 
@@ -569,10 +579,8 @@ def expert_matmul_dw(cfg: ExpertConfig, dy: torch.Tensor, x: torch.Tensor,
     if dy is None or x is None:
         raise ValueError("dy and x are required")
     pdy, px = _arg(dy, "dy", p.dtype, p.dy, dev), _arg(x, "x", p.dtype, p.x, dev)
-    if dw is None:
-        dw = torch.empty(p.w, dtype=p.result, device=dev)
-    _expert_call("cq_expert_matmul_dw", dev, p.ref, pdy, px, group_rows.data_ptr(),
-                 _arg(dw, "dw", p.result, p.w, dev))
+    dw, pdw = _result(dw, "dw", p.result, p.w, dev)
+    _expert_call("cq_expert_matmul_dw", dev, p.ref, pdy, px, group_rows.data_ptr(), pdw)
     return dw
 
 
@@ -591,10 +599,8 @@ def expert_matmul_w4(cfg: ExpertConfig, x: torch.Tensor, codes: torch.Tensor,
     pc = _arg(codes, "codes", torch.uint8, p.codes, dev)
     ps = _arg(scales, "scales", p.dtype, p.groups, dev)
     pz = _arg(zeros, "zeros", torch.uint8, p.groups, dev)
-    if y is None:
-        y = torch.empty(p.y, dtype=p.dtype, device=dev)
-    _expert_call("cq_expert_matmul_w4", dev, p.ref, px, pc, ps, pz, group_rows.data_ptr(),
-                 _arg(y, "y", p.dtype, p.y, dev))
+    y, py = _result(y, "y", p.dtype, p.y, dev)
+    _expert_call("cq_expert_matmul_w4", dev, p.ref, px, pc, ps, pz, group_rows.data_ptr(), py)
     return y
 
 
