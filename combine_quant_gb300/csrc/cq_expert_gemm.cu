@@ -612,10 +612,14 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     constexpr int kAhead = 3;
     const int w = warp - 4 - kDrainWarps;
     const int blocks = sh.KK / 32, quads = (sh.KK + 511) / 512;
-    const bool whole = a.SC % 16 == 0 && a.SC == blocks;  // 16-byte pieces, no pad column
-    const uint8_t* rows[4];                               // scale rows, NULL where there is none
+    // Rows of whole 16-byte pieces are read as such. Others are read as aligned words,
+    // which start 2 bytes early where a row does (SC is even): the words are shifted
+    // into place when they are stored, so that no load is waited for here. Scales past
+    // K (a pad column, a next row's) meet no product.
+    const bool whole = a.SC % 16 == 0;
+    const uint8_t* rows[4];  // scale rows, NULL where there is none
     int t_load = first, q_load = 0;
-    auto load = [&](uint4 (&v)[4]) {
+    auto load = [&](uint4 (&v)[4], uint32_t (&past)[4], uint32_t& shift) {
       if (t_load >= n_tiles) return;
       if (q_load == 0) {
         const Tile x = tile_at<OP, MX>(sh, s_begin, s_tile, a.G, t_load);
@@ -644,21 +648,28 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
         if (whole) {
           v[b] = __ldg(reinterpret_cast<const uint4*>(rows[b] + q_load * 16));
         } else {
-          uint32_t p[8];
-#pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            const int at = q_load * 16 + 2 * h;  // SC is even: a pair is inside or outside
-            p[h] = at < blocks ? __ldg(reinterpret_cast<const uint16_t*>(rows[b] + at)) : 0x7f7fu;
-            if (at + 1 == blocks) p[h] = (p[h] & 0xffu) | 0x7f00u;  // the pad column
-          }
-          v[b] = make_uint4(p[0] | p[1] << 16, p[2] | p[3] << 16, p[4] | p[5] << 16, p[6] | p[7] << 16);
+          const uint32_t early = reinterpret_cast<uintptr_t>(rows[b]) & 2;
+          const uint8_t* from = rows[b] + q_load * 16 - early;
+          const int left = blocks - q_load * 16 + (int)early, in = a.SC - q_load * 16 + (int)early;
+          auto word = [&](int h, uint32_t& to) {
+            if (4 * h >= left) return;
+            to = 4 * h + 4 <= in ? __ldg(reinterpret_cast<const uint32_t*>(from + 4 * h))
+                                 : __ldg(reinterpret_cast<const uint16_t*>(from + 4 * h));
+          };
+          word(0, v[b].x);
+          word(1, v[b].y);
+          word(2, v[b].z);
+          word(3, v[b].w);
+          if (early) word(4, past[b]);
+          shift = early * 8;
         }
       }
       if (++q_load == quads) q_load = 0, t_load += step;
     };
     uint4 v[kAhead][4];
+    uint32_t past[kAhead][4] = {}, shift[kAhead] = {};
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) load(v[u]);
+    for (int u = 0; u < kAhead; ++u) load(v[u], past[u], shift[u]);
     const int total = n_tiles > first ? ((n_tiles - 1 - first) / step + 1) * quads : 0;
     uint32_t s = 0, lap = 0;
     bool ok = true;
@@ -668,7 +679,15 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
         if (i + u >= total || !ok) break;
         if (lap > 0 && !(ok = wait(&bars.sempty[s], (lap & 1) ^ 1, 1))) break;
         uint4* to = reinterpret_cast<uint4*>(s_sf + s * 4 * kScaleBytes + w * 512 + lane * 16);
-        const uint4(&r)[4] = v[u];
+        uint4 r[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint4 f = v[u][b];
+          r[b].x = __funnelshift_r(f.x, f.y, shift[u]);
+          r[b].y = __funnelshift_r(f.y, f.z, shift[u]);
+          r[b].z = __funnelshift_r(f.z, f.w, shift[u]);
+          r[b].w = __funnelshift_r(f.w, past[u][b], shift[u]);
+        }
         to[0] = make_uint4(r[0].x, r[1].x, r[2].x, r[3].x);
         to[kScaleBytes / 16] = make_uint4(r[0].y, r[1].y, r[2].y, r[3].y);
         to[2 * kScaleBytes / 16] = make_uint4(r[0].z, r[1].z, r[2].z, r[3].z);
@@ -676,7 +695,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
         __syncwarp();
         if (lane == 0) async::mbar_arrive(&bars.swritten[s]);
         if (++s == kScaleRing) s = 0, ++lap;
-        load(v[u]);
+        load(v[u], past[u], shift[u]);
       }
     }
   } else if (MX && warp == 3) {

@@ -239,6 +239,25 @@ def test_mx_long(shape, act):
     assert cq.read_expert_status() == 0
 
 
+@pytest.mark.parametrize("k", [32, 64, 96, 192, 320, 576, 1088, 1120, 2112, 4160])
+def test_mx_scale_rows(k):
+    """Rows of scales of every length modulo 16 bytes, experts that begin at odd rows, an odd number of rows in all."""
+    counts, n = [3, 18, 1, 33], 64
+    gen = _rng("mx scale rows", k)
+    xc, xs = _mx(gen, False, sum(counts), k)
+    wc, ws = _mx(gen, False, len(counts), 2 * n, k)
+    xs[:, : k // 32] -= 8
+    ws[..., : k // 32] -= 8
+    xs[:, k // 32:], ws[..., k // 32:] = 255, 255
+    for act, w, s in ((0, wc[:, :n], ws[:, :n]), (1, wc, ws)):
+        w, s = w.contiguous(), s.contiguous()
+        cfg = cq.ExpertConfig(experts=len(counts), rows=sum(counts), n=n, k=k, x_dtype=2, act=act)
+        y = cq.expert_matmul(cfg, xc.to(DEV), w.to(DEV), _counts(counts), x_scales=xs.to(DEV), w_scales=s.to(DEV))
+        want, bound, _, _ = ref.forward(ref.mx_values(xc, xs), ref.mx_values(w, s), counts, act, torch.bfloat16)
+        ref.check(y, want, bound, "y")
+    assert cq.read_expert_status() == 0
+
+
 def test_mx_many_experts():
     counts = [0, 1, 0, 2] * 512
     gen = _rng("mx many")
