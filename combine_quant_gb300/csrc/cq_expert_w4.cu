@@ -57,7 +57,7 @@ struct Shape {
   int tiles_n;   // tiles along the weight rows
   int KG;        // groups of k
   int shift;     // log2 of a group's length
-  int vec;       // rows of scales are whole pieces of 8 groups (2), of 4 (1)
+  int vec;       // rows of scales are whole pieces of 8 groups (2), of 4 (1; or not: ANY)
   int stages;    // stages of the ring
 };
 
@@ -254,7 +254,8 @@ __device__ __forceinline__ void store1(void* p, size_t i, float v) {
   else static_cast<__half*>(p)[i] = __float2half_rn(v);
 }
 
-template <typename T, int MTW, int NTMAX, bool ACT, bool ZEROS, bool G32>
+// ANY: rows of scales of any number of groups, else of whole fours.
+template <typename T, int MTW, int NTMAX, bool ACT, bool ZEROS, bool G32, bool ANY>
 __global__ void __launch_bounds__(kThreads, 1)
 w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
           const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x1,
@@ -412,17 +413,27 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
   } else if (warp < kMulWarps + kSumWarps + kScaleWarps) {
     // ---- scales: a thread takes rows r and r + 64, kAhead stages ahead ----
     constexpr int kPer = (St::kRows + 63) / 64, kW = St::kGroups / 2;  // rows; words of a row
-    constexpr int kFit = 48 / (kPer * kW * (ZEROS ? 3 : 2) / 2);       // in 48 registers
-    constexpr int kAhead = kFit > 4 ? 4 : kFit;
+    constexpr int kZW = kW / 2 + ANY;                             // zero points: a word more
+    constexpr int kFit = 48 / (kPer * (kW + (ZEROS ? kZW : 0)));  // in 48 registers
+    constexpr int kMost = MTW == 2 && ZEROS ? 3 : 4;              // (groups of 64: 74 us against 94 with 4)
+    constexpr int kAhead = kFit > kMost ? kMost : kFit;
     const uint16_t* scales = static_cast<const uint16_t*>(a.scales4);
     const int per_cta = n_tiles > (int)blockIdx.x ? (n_tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
     const int total = per_cta * n_stages, ng = 512 >> sh.shift;
     const int r0 = threadIdx.x - 32 * (kMulWarps + kSumWarps);
-    int tile = -1, st = n_stages - 1;
+    int tile = -1, st = n_stages - 1, st_store = 0;
     size_t row_at[kPer] = {};
     bool in[kPer] = {};
-    uint32_t sbuf[kAhead][kPer][kW], zbuf[kAhead][kPer][kW / 2];
-    auto load = [&](int i, uint32_t (&sv)[kPer][kW], uint32_t (&zv)[kPer][kW / 2]) {
+    uint32_t sbuf[kAhead][kPer][kW] = {}, zbuf[kAhead][kPer][kZW] = {};
+    // ANY: aligned words are read, from where a row's part begins or up to 3 bytes before,
+    // and shifted into place when they are stored, so that nothing here waits for a load
+    // (single groups put together at once: 163 us against 94, groups of 64, zero points,
+    // 32 experts of 4 rows, 2048 x 7232). The word past a full stage's scales is the next
+    // stage's first; a tile's last stage is not full then. The rows' offsets modulo 4 are
+    // those of r0 (tiles and experts begin at multiples of 16 rows), and the tensors end
+    // at whole words.
+    const uint32_t s_shift = 16 * (r0 * sh.KG & 1), z_shift = 8 * (r0 * sh.KG & 3);
+    auto load = [&](int i, uint32_t (&sv)[kPer][kW], uint32_t (&zv)[kPer][kZW]) {
       if (i >= total) return;
       if (++st == n_stages) st = 0, ++tile;
       const int first = st * ng;
@@ -443,7 +454,19 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
         for (int w = 0; w < kW / 2; ++w) zv[b][w] = 0;
         if (!in[b]) continue;
         const size_t at = row_at[b] + first;
-        if (sh.vec == 2) {
+        if constexpr (ANY) {
+          const int n = min(ng, sh.KG - first);
+          const uint32_t* from = reinterpret_cast<const uint32_t*>(scales + at - s_shift / 16);
+#pragma unroll
+          for (int w = 0; w < kW; ++w)
+            if (4 * w < 2 * n + (int)(s_shift / 8)) sv[b][w] = __ldg(from + w);
+          if constexpr (ZEROS) {
+            const uint32_t* zfrom = reinterpret_cast<const uint32_t*>(a.zeros4 + at - z_shift / 8);
+#pragma unroll
+            for (int w = 0; w < kZW; ++w)
+              if (4 * w < n + (int)(z_shift / 8)) zv[b][w] = __ldg(zfrom + w);
+          }
+        } else if (sh.vec == 2) {
           // 4 groups (of 128), 8, or twice 8, the second of which may not exist
           const uint16_t* from = scales + at;
           const uint8_t* zfrom = a.zeros4 + at;
@@ -463,20 +486,13 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
                 }
               }
           }
-        } else if (sh.vec == 1) {
+        } else {
 #pragma unroll
           for (int w = 0; w < kW; w += 2)
             if (2 * w < ng && first + 2 * w < sh.KG) {
               const uint2 v = __ldg(reinterpret_cast<const uint2*>(scales + at + 2 * w));
               sv[b][w] = v.x, sv[b][w + 1] = v.y;
               if (ZEROS) zv[b][w / 2] = __ldg(reinterpret_cast<const uint32_t*>(a.zeros4 + at + 2 * w));
-            }
-        } else {
-#pragma unroll
-          for (int k = 0; k < St::kGroups; ++k)
-            if (k < ng && first + k < sh.KG) {
-              sv[b][k / 2] |= (uint32_t)__ldg(scales + at + k) << (16 * (k & 1));
-              if (ZEROS) zv[b][k / 4] |= (uint32_t)__ldg(a.zeros4 + at + k) << (8 * (k & 3));
             }
         }
       }
@@ -489,23 +505,37 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
         if (i0 + u >= total || !ok) break;
         if (lap > 0 && !(ok = wait(&bars.empty[s], (lap & 1) ^ 1))) break;
         uint8_t* base = ring + s * St::kBytes;
+        const int have = sh.KG - st_store * ng;  // groups from this stage on
+        if (++st_store == n_stages) st_store = 0;
 #pragma unroll
         for (int b = 0; b < kPer; ++b) {
           const int r = r0 + 64 * b;
           const int slot = (r / (16 * MTW) * 8 + r % 8) * (2 * MTW) + 2 * (r / 16 % MTW) + r / 8 % 2;
           float* to = reinterpret_cast<float*>(base + St::kScale) + slot * (ZEROS ? 2 : 1);
-#pragma unroll
-          for (int k = 0; k < St::kGroups; ++k)
-            if (k < ng) {
-              const float f = k & 1 ? T::hi(sbuf[u][b][k / 2]) : T::lo(sbuf[u][b][k / 2]);
-              if constexpr (ZEROS) {
-                // 2^23 + z has z in its last bits; all of this is exact
-                const float z = __uint_as_float(__byte_perm(zbuf[u][b][k / 4], 0x4b000000u, 0x7440 + (k & 3)));
-                *reinterpret_cast<float2*>(to + k * St::kGroupFloats) = make_float2(f, (8388608.f - kOff) - z);
-              } else {
-                to[k * St::kGroupFloats] = f;
-              }
+          auto put = [&](int k, uint32_t v, uint32_t zw) {
+            const float f = k & 1 ? T::hi(v) : T::lo(v);
+            if constexpr (ZEROS) {
+              // 2^23 + z has z in its last bits; all of this is exact
+              const float z = __uint_as_float(__byte_perm(zw, 0x4b000000u, 0x7440 + (k & 3)));
+              *reinterpret_cast<float2*>(to + k * St::kGroupFloats) = make_float2(f, (8388608.f - kOff) - z);
+            } else {
+              to[k * St::kGroupFloats] = f;
             }
+          };
+          if constexpr (!ANY) {
+#pragma unroll
+            for (int k = 0; k < St::kGroups; ++k)
+              if (k < ng) put(k, sbuf[u][b][k / 2], zbuf[u][b][k / 4]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < St::kGroups; ++k)
+              if (k < ng) {
+                const uint32_t past = k / 2 + 1 < kW ? sbuf[u][b][(k / 2 + 1) % kW] : sbuf[(u + 1) % kAhead][b][0];
+                const uint32_t v = __funnelshift_r(sbuf[u][b][k / 2], past, s_shift);
+                // past KG lies the next row's
+                put(k, k < have ? v : 0u, __funnelshift_r(zbuf[u][b][k / 4], zbuf[u][b][k / 4 + 1], z_shift));
+              }
+          }
         }
         __syncwarp();
         if (lane == 0) async::mbar_arrive(&bars.ready[s]);
@@ -541,16 +571,16 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
 }
 
 // ---- host ----
-template <typename T, int MTW, int NTMAX, bool ACT, bool ZEROS, bool G32>
+template <typename T, int MTW, int NTMAX, bool ACT, bool ZEROS, bool G32, bool ANY>
 cudaError_t launch_t(const Args& a, cudaStream_t s) {
-  constexpr auto kernel = w4_kernel<T, MTW, NTMAX, ACT, ZEROS, G32>;
+  constexpr auto kernel = w4_kernel<T, MTW, NTMAX, ACT, ZEROS, G32, ANY>;
   using St = Stage<MTW, NTMAX, ZEROS, G32>;
   Shape sh = {};
   sh.n_out = ACT ? a.N / 2 : a.N;
   sh.tiles_n = (a.N + St::kRows - 1) / St::kRows;
   sh.shift = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
   sh.KG = a.K / a.group;
-  sh.vec = sh.KG % 8 == 0 ? 2 : sh.KG % 4 == 0 ? 1 : 0;
+  sh.vec = sh.KG % 8 == 0 ? 2 : 1;
   const uint64_t G = a.G, R = a.R, N = a.N, K = a.K;
   CUtensorMap mw, mx[2];
   // codes: the two halves of a tile in one copy; x: 16 blocks of 32 of k in one
@@ -578,13 +608,21 @@ cudaError_t launch_t(const Args& a, cudaStream_t s) {
   return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, s, a, sh, mw, mx[0], mx[1]);
 }
 
+template <typename T, int MTW, int NTMAX, bool ACT, bool ZEROS, bool G32>
+cudaError_t launch_r(const Args& a, cudaStream_t s) {
+  if (a.K / a.group % 4 == 0) return launch_t<T, MTW, NTMAX, ACT, ZEROS, G32, false>(a, s);
+  // Tiles of 128 rows, zero points, groups of 32: the scales of two rows would not fit
+  // the registers (215 us against 119 in tiles of 64: 32 experts of 4 rows, 2048 x 7200).
+  return launch_t<T, ZEROS && G32 ? 1 : MTW, NTMAX, ACT, ZEROS, G32, true>(a, s);
+}
+
 template <typename T, int MTW, int NTMAX, bool ACT>
 cudaError_t launch_g(const Args& a, cudaStream_t s) {
   if (a.zeros4)
-    return a.group == 32 ? launch_t<T, MTW, NTMAX, ACT, true, true>(a, s)
-                         : launch_t<T, MTW, NTMAX, ACT, true, false>(a, s);
-  return a.group == 32 ? launch_t<T, MTW, NTMAX, ACT, false, true>(a, s)
-                       : launch_t<T, MTW, NTMAX, ACT, false, false>(a, s);
+    return a.group == 32 ? launch_r<T, MTW, NTMAX, ACT, true, true>(a, s)
+                         : launch_r<T, MTW, NTMAX, ACT, true, false>(a, s);
+  return a.group == 32 ? launch_r<T, MTW, NTMAX, ACT, false, true>(a, s)
+                       : launch_r<T, MTW, NTMAX, ACT, false, false>(a, s);
 }
 
 // Tiles of 128 weight rows where they give every SM two, else of 64 (a tile of 64

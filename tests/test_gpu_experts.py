@@ -304,6 +304,36 @@ def test_w4(shape, act, zeros, dtype):
     assert cq.read_expert_status() == 0
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group, k", [(g, g * n) for g, ns in ((32, (1, 2, 3, 15, 17, 33, 34, 35, 47)), (64, (7, 9, 18, 23)),
+                                                              (128, (3, 5, 9, 10, 11))) for n in ns])
+@pytest.mark.parametrize("wide", [0, 1])
+def test_w4_scale_rows(wide, group, k, zeros):
+    """Rows of any number of groups, in tiles of 64 rows and (wide) of 128. Every second weight row's scales begin with
+    an infinity, which must not reach the row before it."""
+    if wide and k not in (32 * 35, 32 * 47, 64 * 9, 64 * 23, 128 * 5, 128 * 11):
+        pytest.skip("the shorter list of the large weights")
+    counts, n = ([1, 0, 2] * 8, 2560) if wide else ([3, 12, 1], 80)
+    gen = _rng("w4 scale rows", k, zeros)
+    x = _rows(gen, counts, 0, k, torch.bfloat16)
+    codes = torch.randint(0, 256, (len(counts), n, k // 2), generator=gen, dtype=torch.int32).to(torch.uint8)
+    scales = (torch.rand(len(counts), n, k // group, generator=gen) * 0.25 * k ** -0.5 + 1e-3).to(torch.bfloat16)
+    z = torch.randint(0, 16, scales.shape, generator=gen, dtype=torch.int32).to(torch.uint8) if zeros else None
+    given = scales.clone()
+    given[:, 1::2, 0] = torch.inf
+    cfg = cq.ExpertConfig(experts=len(counts), rows=sum(counts), n=n, k=k, group=group)
+    y = cq.expert_matmul_w4(cfg, x.to(DEV), codes.to(DEV), given.to(DEV), _counts(counts),
+                            zeros=None if z is None else z.to(DEV))
+    cut = slice(0, None, 2 if not wide else 50)
+    codes, scales, z = codes[:, cut], scales[:, cut], z[:, cut] if zeros else None
+    w = ref.w4_values(codes, scales, z, group)
+    big = (143 + 128 + 15) * scales.double().repeat_interleave(group, -1)  # the offset codes' terms, as above
+    want, _ = ref.products(x, w, counts)
+    _, b = ref.products(x, big, counts)
+    ref.check(y[:, cut].contiguous(), want, ref.rounded(want, b, torch.bfloat16), "y")
+    assert cq.read_expert_status() == 0
+
+
 # -------------------------------------------------------------------------------------------------
 # counts, streams, refusals
 # -------------------------------------------------------------------------------------------------
