@@ -23,8 +23,8 @@
 // the codes' bytes as far as the memory goes (5.9 TB/s with the multiplying taken
 // out), in practice the multiplying warps' instructions. Measured on one GB300, 32
 // experts, hidden 7168, SwiGLU with n 2048, groups of 128 (485 MB): up to 8 rows an
-// expert 109 us (4.4 TB/s), 16 rows 139 us, every further 16 rows about 130 us; one
-// row through 8192 x 8192 15.6 us, with groups of 32 and zero points 20 us.
+// expert 107 us (4.5 TB/s), 16 rows 137 us, every further 16 rows about 130 us; one
+// row through 8192 x 8192 14.5 us, with groups of 32 and zero points 20 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
