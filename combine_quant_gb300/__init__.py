@@ -8,8 +8,8 @@ expert weights; ``workloads`` draws seeded synthetic inputs; ``build`` compiles
 the library in-tree.
 """
 from .api import (Config, DispatchResult, ExpertConfig, alloc_dispatch_outputs, alloc_workspace,  # noqa: F401
-                  assist_views, check_bounded_wait, combine, combine_q8, combine_quant,
-                  combine_ws, cq_check_bounded_wait, cq_combine, cq_combine_q8,
+                  assist_views, check_bounded_meet, check_bounded_wait, combine, combine_q8, combine_quant,
+                  combine_ws, cq_check_bounded_meet, cq_check_bounded_wait, cq_combine, cq_combine_q8,
                   cq_combine_quant, cq_combine_ws, cq_dispatch, cq_dispatch_noalloc, cq_dispatch_permute,
                   cq_dispatch_one_kernel, cq_dispatch_route, cq_dispatch_workspace_size,
                   cq_read_combine_status, cq_read_status, dispatch, dispatch_noalloc,

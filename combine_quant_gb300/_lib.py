@@ -47,7 +47,7 @@ EXPORTS = (
     "cq_dispatch_route", "cq_dispatch_permute", "cq_combine", "moe_dispatch", "moe_combine",
     "cq_read_status", "cq_strerror", "cq_dispatch_noalloc", "cq_combine_quant", "cq_combine_q8",
     "cq_read_combine_status", "cq_check_bounded_wait", "cq_combine_ws", "cq_dispatch_one_kernel",
-    "cq_check_expert_config", "cq_expert_matmul", "cq_expert_matmul_dx", "cq_expert_matmul_dw",
+    "cq_check_bounded_meet", "cq_check_expert_config", "cq_expert_matmul", "cq_expert_matmul_dx", "cq_expert_matmul_dw",
     "cq_expert_matmul_w4", "cq_read_expert_status",
 )
 
@@ -103,6 +103,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "cq_read_status": ([P, P, P], ctypes.c_int),
         "cq_read_combine_status": ([P, P], ctypes.c_int),
         "cq_check_bounded_wait": ([P, P, P], ctypes.c_int),
+        "cq_check_bounded_meet": ([P, P, P], ctypes.c_int),
         "cq_dispatch_noalloc": ([cfgp] + [P] * 13, ctypes.c_int),
         "cq_combine_quant": ([cfgp] + [P] * 5, ctypes.c_int),
         "cq_combine_q8": ([cfgp] + [P] * 9 + [i32, P, P], ctypes.c_int),

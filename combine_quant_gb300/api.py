@@ -636,16 +636,25 @@ def read_combine_status(device=None) -> int:
     return int(st.value)
 
 
+def _bounded_check(name: str, device) -> tuple[int, float]:
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    value, secs = ctypes.c_uint32(0), ctypes.c_double(0.0)
+    with torch.cuda.device(dev):
+        rc = getattr(_lib.load(), name)(ctypes.byref(value), ctypes.byref(secs), _stream(dev))
+    _lib.check(rc, name)
+    return int(value.value), float(secs.value)
+
+
 def check_bounded_wait(device=None) -> tuple[int, float]:
     """Run the library's bounded wait on a barrier nothing completes
     (cq_check_bounded_wait): returns (gave_up, seconds)."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    gave_up, secs = ctypes.c_uint32(0), ctypes.c_double(0.0)
-    with torch.cuda.device(dev):
-        rc = _lib.load().cq_check_bounded_wait(ctypes.byref(gave_up), ctypes.byref(secs),
-                                               _stream(dev))
-    _lib.check(rc, "cq_check_bounded_wait")
-    return int(gave_up.value), float(secs.value)
+    return _bounded_check("cq_check_bounded_wait", device)
+
+
+def check_bounded_meet(device=None) -> tuple[int, float]:
+    """Sixteen warps that wait apart and meet, one of which gives up
+    (cq_check_bounded_meet): returns (threads that left, seconds)."""
+    return _bounded_check("cq_check_bounded_meet", device)
 
 
 def assist_views(cfg: Config, assist_info: torch.Tensor):
@@ -691,3 +700,4 @@ cq_read_expert_status = read_expert_status
 cq_read_status = read_status
 cq_read_combine_status = read_combine_status
 cq_check_bounded_wait = check_bounded_wait
+cq_check_bounded_meet = check_bounded_meet

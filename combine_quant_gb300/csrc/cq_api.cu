@@ -469,10 +469,27 @@ __global__ void bounded_wait_probe() {
   cq::async::mbar_fence_init();
   g_wait_probe = cq::async::mbar_wait(&bar, 0) ? 0u : 1u;
 }
-}  // namespace
 
-int cq_check_bounded_wait(uint32_t* gave_up, double* seconds, void* stream) {
-  if (!gave_up || !seconds) return CQ_ERR_ARG;
+// Sixteen warps wait each by itself, twice, and meet behind each wait as the
+// multiplying warps of the 4-bit expert product do. All get through the first
+// wait; the second gives up in one of them. Counts the threads that went on
+// from the first meeting and left at the second.
+__global__ void bounded_meet_probe() {
+  __shared__ uint64_t bars[2];  // the first phase of bars[0] completes, of bars[1] never
+  if (threadIdx.x == 0) {
+    cq::async::mbar_init(&bars[0], 1);
+    cq::async::mbar_init(&bars[1], 1);
+    cq::async::mbar_fence_init();
+    cq::async::mbar_arrive(&bars[0]);
+  }
+  __syncthreads();
+  const int late = threadIdx.x / 32 == 5;
+  if (!cq::async::meet<512>(cq::async::mbar_wait_warp(&bars[0], 0))) return;
+  if (!cq::async::meet<512>(cq::async::mbar_wait_warp(&bars[late], 0))) atomicAdd(&g_wait_probe, 1u);
+}
+
+// Runs a probe in one block and reads what it left in g_wait_probe.
+int run_probe(void (*probe)(), int threads, uint32_t* value, double* seconds, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const uint32_t zero = 0;
   if (cudaMemcpyToSymbolAsync(g_wait_probe, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s) !=
@@ -480,7 +497,7 @@ int cq_check_bounded_wait(uint32_t* gave_up, double* seconds, void* stream) {
       cudaStreamSynchronize(s) != cudaSuccess)
     return CQ_ERR_CUDA;
   const auto t0 = std::chrono::steady_clock::now();
-  bounded_wait_probe<<<1, 32, 0, s>>>();
+  probe<<<1, threads, 0, s>>>();
   if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
     return CQ_ERR_CUDA;
   *seconds = std::chrono::duration<double>(std::chrono::steady_clock::now() - t0).count();
@@ -489,8 +506,19 @@ int cq_check_bounded_wait(uint32_t* gave_up, double* seconds, void* stream) {
           cudaSuccess ||
       cudaStreamSynchronize(s) != cudaSuccess)
     return CQ_ERR_CUDA;
-  *gave_up = v;
+  *value = v;
   return CQ_OK;
+}
+}  // namespace
+
+int cq_check_bounded_wait(uint32_t* gave_up, double* seconds, void* stream) {
+  if (!gave_up || !seconds) return CQ_ERR_ARG;
+  return run_probe(bounded_wait_probe, 32, gave_up, seconds, stream);
+}
+
+int cq_check_bounded_meet(uint32_t* left, double* seconds, void* stream) {
+  if (!left || !seconds) return CQ_ERR_ARG;
+  return run_probe(bounded_meet_probe, 512, left, seconds, stream);
 }
 
 const char* cq_strerror(int code) {

@@ -79,6 +79,27 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   return false;
 }
 
+// mbar_wait by all lanes of a converged warp, with one verdict for the warp: the
+// lanes read the clock one by one, so some may give up where others get through.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
+// Named barrier 1 of THREADS threads, and whether `ok` is true in all of them.
+// Warps whose waits may have given up each for itself meet here before any other
+// barrier, so that they go on, or leave, together.
+template <int THREADS>
+__device__ __forceinline__ bool meet(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.and.pred p, 1, %2, q;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(all)
+      : "r"((uint32_t)ok), "n"(THREADS)
+      : "memory");
+  return all != 0;
+}
+
 // Hand a ring slot back to the producer after this warp has read it with
 // ordinary (generic-proxy) shared-memory loads. The next write into the slot
 // is a bulk copy (async proxy), which the release/acquire pair of the empty

@@ -41,6 +41,7 @@ using namespace tensor;
 using async::mbar_arrive_expect_tx;
 using async::mbar_init;
 using async::mbar_wait;
+using async::mbar_wait_warp;
 using async::release_slot;
 
 __device__ uint32_t g_status;  // CQ_ST_* bits of these kernels on this device
@@ -225,7 +226,7 @@ __device__ __forceinline__ bool multiply_tile(float (&acc)[MTW][NTMAX][4], Bars&
   using St = Stage<MTW, NTMAX, ZEROS, G32>;
   const uint32_t at_x = at.x + kw * 2 * 512 * NT;
   for (int left = K - kw * 64; left + kw * 64 > 0; left -= 512) {
-    if (!mbar_wait(&bars.ready[s], lap & 1)) return false;
+    if (!mbar_wait_warp(&bars.ready[s], lap & 1)) return false;
     const uint8_t* base = ring + s * St::kBytes;
     auto chunk = [&](int c) {
       const uint8_t* scale = base + at.scale + c * at.scale_next;
@@ -289,7 +290,7 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
   const int n_tiles = s_tile[a.G];
   const int n_stages = (a.K + 511) / 512;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (mbar_wait(bar, parity)) return true;
+    if (mbar_wait_warp(bar, parity)) return true;
     atomicOr(&g_status, (uint32_t)CQ_ST_TIMEOUT);
     return false;
   };
@@ -315,14 +316,14 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
         ok = multiply_tile<T, MTW, 1, NTMAX, ZEROS, G32>(acc, bars, ring, S, s, lap, at, kw, a.K);
       else
         ok = multiply_tile<T, MTW, NTMAX, NTMAX, ZEROS, G32>(acc, bars, ring, S, s, lap, at, kw, a.K);
-      if (!ok) {
-        atomicOr(&g_status, (uint32_t)CQ_ST_TIMEOUT);
-        break;
-      }
+      if (!ok) atomicOr(&g_status, (uint32_t)CQ_ST_TIMEOUT);
+      // A warp that gave up attends all the same: the others would wait for it without
+      // a limit. They leave together.
+      if (!(ok = async::meet<32 * kMulWarps>(ok))) break;
       // Sums of the four k shares, added in order: 16 rows of every quarter at a time.
 #pragma unroll
       for (int m = 0; m < MTW; ++m) {
-        bar_mul();
+        if (m > 0) bar_mul();
         float* to = red + (kw * 4 + rq) * (8 * NTMAX * 20);
 #pragma unroll
         for (int n = 0; n < NTMAX; ++n)

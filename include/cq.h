@@ -331,6 +331,11 @@ int cq_read_combine_status(uint32_t* status, void* stream);
  * device stays usable afterwards. CQ_ERR_ARG for NULL outputs. */
 int cq_check_bounded_wait(uint32_t* gave_up, double* seconds, void* stream);
 
+/* Diagnostic: the same for warps that wait each by itself and then meet at a
+ * barrier (the 4-bit expert product): a wait that gives up in one warp of
+ * sixteen ends them all. *left = threads that left, 512. */
+int cq_check_bounded_meet(uint32_t* left, double* seconds, void* stream);
+
 /* Which kernels cq_dispatch runs for a config (no counterpart in the pages;
  * host only, nothing is enqueued): 1 when it runs routing and permute as one
  * kernel (a small batch: W * BS * K <= 2048, (S_r + M) * W <= 2048,
