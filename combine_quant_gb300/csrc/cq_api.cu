@@ -472,8 +472,9 @@ __global__ void bounded_wait_probe() {
 
 // Sixteen warps wait each by itself, twice, and meet behind each wait as the
 // multiplying warps of the 4-bit expert product do. All get through the first
-// wait; the second gives up in one of them. Counts the threads that went on
-// from the first meeting and left at the second.
+// wait; the second gives up in one lane of one of them. Counts the threads that
+// went on from the first meeting and left at the second, those of that warp only
+// where they had its verdict.
 __global__ void bounded_meet_probe() {
   __shared__ uint64_t bars[2];  // the first phase of bars[0] completes, of bars[1] never
   if (threadIdx.x == 0) {
@@ -483,9 +484,10 @@ __global__ void bounded_meet_probe() {
     cq::async::mbar_arrive(&bars[0]);
   }
   __syncthreads();
-  const int late = threadIdx.x / 32 == 5;
+  const bool late = threadIdx.x / 32 == 5;
   if (!cq::async::meet<512>(cq::async::mbar_wait_warp(&bars[0], 0))) return;
-  if (!cq::async::meet<512>(cq::async::mbar_wait_warp(&bars[late], 0))) atomicAdd(&g_wait_probe, 1u);
+  const bool ok = cq::async::mbar_wait_warp(&bars[threadIdx.x == 5 * 32 + 7], 0);
+  if (!cq::async::meet<512>(ok) && ok != late) atomicAdd(&g_wait_probe, 1u);
 }
 
 // Runs a probe in one block and reads what it left in g_wait_probe.

@@ -54,6 +54,7 @@ using namespace tensor;
 using async::mbar_arrive_expect_tx;
 using async::mbar_init;
 using async::mbar_wait;
+using async::mbar_wait_warp;
 
 __device__ uint32_t g_status;  // CQ_ST_* bits of these kernels on this device
 
@@ -370,9 +371,10 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
   const uint32_t tmem = bars.tmem;
   const int n_tiles = s_tile[a.G];
   const int first = blockIdx.x / 2, step = gridDim.x / 2;
+  // One verdict for the warp: the lanes go on to elect.sync and to .aligned instructions.
   auto wait = [&](uint64_t* bar, uint32_t parity, int rounds, bool pair = false) {
     for (int r = 0; r < rounds; ++r)
-      if (pair ? wait_pair(bar, parity) : mbar_wait(bar, parity)) return true;
+      if (pair ? wait_pair_warp(bar, parity) : mbar_wait_warp(bar, parity)) return true;
     atomicOr(&g_status, (uint32_t)CQ_ST_TIMEOUT);
     return false;
   };

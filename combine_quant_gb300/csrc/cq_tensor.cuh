@@ -45,6 +45,11 @@ __device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity) {
   return false;
 }
 
+// By all lanes of a converged warp, with one verdict (see async::mbar_wait_warp).
+__device__ __forceinline__ bool wait_pair_warp(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait_pair(bar, parity));
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;

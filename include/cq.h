@@ -332,8 +332,9 @@ int cq_read_combine_status(uint32_t* status, void* stream);
 int cq_check_bounded_wait(uint32_t* gave_up, double* seconds, void* stream);
 
 /* Diagnostic: the same for warps that wait each by itself and then meet at a
- * barrier (the 4-bit expert product): a wait that gives up in one warp of
- * sixteen ends them all. *left = threads that left, 512. */
+ * barrier (the 4-bit expert product): a wait that gives up in one lane is one
+ * that gave up in its warp, and ends all sixteen. *left = threads that left,
+ * 512. */
 int cq_check_bounded_meet(uint32_t* left, double* seconds, void* stream);
 
 /* Which kernels cq_dispatch runs for a config (no counterpart in the pages;
