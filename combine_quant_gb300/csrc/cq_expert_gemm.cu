@@ -97,6 +97,7 @@ struct Bars {
   uint64_t full[8], empty[8], tail[8], tail_full[8];
   uint64_t swritten[4], sfull[4], sempty[4];  // mx: scales written, visible to the copies, used
   uint64_t tfull[2], tempty[2];
+  uint64_t done;  // the products in flight when their warp gave up
   uint32_t tmem;
 };
 
@@ -355,6 +356,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       mbar_init(&bars.tfull[b], 1);
       mbar_init(&bars.tempty[b], kDrainWarps * 2);
     }
+    mbar_init(&bars.done, 1);
     async::mbar_fence_init();
   }
   if (warp == 1) tmem_alloc(&bars.tmem, kTmemCols);
@@ -390,6 +392,8 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
   if (warp == 0) {
     // ---- copies ----
     uint32_t s = 0, lap = 0;  // stage, times the ring has gone round
+    // dw, bit s: the last copies into stage s complete on tail[s]; the parity of their number
+    uint32_t on_tail = 0, tail_odd = 0;
     bool ok = true;
     for (int t = first; t < n_tiles && ok; t += step) {
       const Tile x = tile_at<OP, MX>(sh, s_begin, s_tile, a.G, t);
@@ -403,9 +407,11 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
           kABytes + (B_MN ? (sh.whole ? 2 : n64) * 8192 : b128 ? 16384 : (b64 ? 8192 : 0) + (b32 ? 4096 : 0));
       for (int kb = 0; kb < x.nkb; ++kb) {
         if (lap > 0 && !(ok = wait(&bars.empty[s], (lap & 1) ^ 1, 1))) break;
+        const bool tail = ragged && kb == 0;
+        on_tail = (on_tail & ~(1u << s)) | ((uint32_t)tail << s);
+        tail_odd ^= (uint32_t)tail << s;
         if (elect_one()) {
           const uint32_t sa = smem_u32(ring + s * SB), sb = sa + kABytes;
-          const bool tail = ragged && kb == 0;
           uint32_t bar;
           if (tail) {
             // zeros go in before the product may read: each CTA's copies complete
@@ -454,11 +460,14 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     }
     // The last use of every stage, oldest first. Done: nothing may arrive here
     // after the CTA has gone. Gave up: let the copies in flight land (with a
-    // limit) before it goes.
+    // limit) before it goes; those of both CTAs complete on the leader's barrier,
+    // for which the other CTA stays.
     for (int v = 0; v < S; ++v) {
       const uint32_t u = (s + v) % S, laps = lap + (u < s ? 1 : 0);  // uses of stage u
       if (laps == 0) continue;
       if (ok) ok = wait(&bars.empty[u], (laps - 1) & 1, 1);
+      if (ok) continue;
+      if (OP == kDw && (on_tail >> u & 1)) mbar_wait(&bars.tail[u], (tail_odd >> u & 1) ^ 1);
       else if (rank == 0) mbar_wait(&bars.full[u], (laps - 1) & 1);
     }
   } else if (warp == 1 && rank == 0) {
@@ -578,6 +587,11 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       }
       if (ok && elect_one()) commit(smem_u32(&bars.tfull[b]));
       __syncwarp();
+    }
+    if (!ok) {  // gave up: let the products in flight end (with a limit), which read both CTAs' memory
+      if (elect_one()) commit(smem_u32(&bars.done));
+      __syncwarp();
+      wait_pair(&bars.done, 0);
     }
   } else if (OP == kDw && warp == 2) {
     // ---- zeros over the rows past an expert's last (up to the next 16) ----

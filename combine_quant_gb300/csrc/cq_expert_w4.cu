@@ -562,11 +562,11 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
         next();
       }
     }
-    if (!ok) {  // gave up: let the copies in flight land (with a limit)
-      for (int v = 0; v < S; ++v) {
-        const uint32_t laps = lap + ((uint32_t)v < s ? 1 : 0);
-        if (laps > 0) mbar_wait(&bars.full[v], (laps - 1) & 1);
-      }
+    // Let the copies in flight land (with a limit): the warps that read them may have
+    // given up before this one noticed.
+    for (int v = 0; v < S; ++v) {
+      const uint32_t laps = lap + ((uint32_t)v < s ? 1 : 0);
+      if (laps > 0) mbar_wait(&bars.full[v], (laps - 1) & 1);
     }
   }
 }
