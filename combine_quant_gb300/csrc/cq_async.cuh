@@ -79,10 +79,25 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   return false;
 }
 
-// mbar_wait by all lanes of a converged warp, with one verdict for the warp: the
-// lanes read the clock one by one, so some may give up where others get through.
+// Polls try_wait with the same limits by all lanes of a converged warp, with one
+// verdict for the warp: lanes that poll and read the clock each for itself may
+// differ. The votes make every branch uniform.
+template <typename Try>
+__device__ __forceinline__ bool wait_warp(Try try_wait) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  if (__all_sync(kAll, try_wait())) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t polls = 0; polls < kWaitMaxPolls; ++polls) {
+    if (__all_sync(kAll, try_wait())) return true;
+    if (__any_sync(kAll, globaltimer_ns() - t0 > kWaitLimitNs)) return false;
+  }
+  return false;
+}
+
+// mbar_wait by a converged warp.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+  const uint32_t a = smem_u32(bar);
+  return wait_warp([=] { return mbar_try_wait(a, parity); });
 }
 
 // Named barrier 1 of THREADS threads, and whether `ok` is true in all of them.

@@ -376,7 +376,7 @@ gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
   // One verdict for the warp: the lanes go on to elect.sync and to .aligned instructions.
   auto wait = [&](uint64_t* bar, uint32_t parity, int rounds, bool pair = false) {
     for (int r = 0; r < rounds; ++r)
-      if (pair ? wait_pair_warp(bar, parity) : mbar_wait_warp(bar, parity)) return true;
+      if (pair ? wait_pair(bar, parity) : mbar_wait_warp(bar, parity)) return true;
     atomicOr(&g_status, (uint32_t)CQ_ST_TIMEOUT);
     return false;
   };

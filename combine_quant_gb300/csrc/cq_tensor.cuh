@@ -22,8 +22,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
-// async::mbar_wait for a phase that the pair's other CTA takes part in (cluster
-// scope), with the same limits.
+// async::mbar_wait_warp for a phase that the pair's other CTA takes part in
+// (cluster scope).
 __device__ __forceinline__ bool try_pair(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -36,18 +36,7 @@ __device__ __forceinline__ bool try_pair(uint32_t bar, uint32_t parity) {
 }
 __device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity) {
   const uint32_t b = smem_u32(bar);
-  if (try_pair(b, parity)) return true;
-  const uint64_t t0 = async::globaltimer_ns();
-  for (uint32_t polls = 0; polls < async::kWaitMaxPolls; ++polls) {
-    if (try_pair(b, parity)) return true;
-    if (async::globaltimer_ns() - t0 > async::kWaitLimitNs) return false;
-  }
-  return false;
-}
-
-// By all lanes of a converged warp, with one verdict (see async::mbar_wait_warp).
-__device__ __forceinline__ bool wait_pair_warp(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, wait_pair(bar, parity));
+  return async::wait_warp([=] { return try_pair(b, parity); });
 }
 
 // True in one lane of a converged warp.
