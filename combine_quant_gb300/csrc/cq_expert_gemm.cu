@@ -136,11 +136,19 @@ __device__ __forceinline__ Tile tile_at(const Shape& sh, const int* s_begin, con
   return x;
 }
 
-// 1 / (1 + exp(-g)) from exp(-|g|), which cannot overflow: small values keep
-// their relative accuracy down to the subnormals.
-__device__ __forceinline__ float sigmoid(float g) {
-  const float e = __expf(-fabsf(g)), r = __fdividef(1.f, 1.f + e);
-  return g >= 0.f ? r : e * r;
+// The gradient d of y = u * g * s, s = 1 / (1 + exp(-g)): dg = d u s (1 + g (1 - s)),
+// du = d g s, in 32 bits. With h = exp(-|g| / 2), which cannot overflow, and r =
+// 1 / (1 + h^2): s = r and 1 - s = h^2 r for g >= 0, else s = h^2 r and 1 - s = r. So
+// 1 - s is never a difference (from g = 2^24 on s rounds to 1), and for g < 0 each of
+// two factors meets one h before they meet each other: d u may leave 32 bits where
+// the result does not.
+__device__ __forceinline__ void swiglu_gradient(float d, float g, float u, float& dg, float& du) {
+  const float h = __expf(-0.5f * fabsf(g)), r = __fdividef(1.f, fmaf(h, h, 1.f));
+  const bool up = g >= 0.f;
+  const float a = up ? 1.f : h, b = up ? h : 1.f;
+  const float da = d * a, ga = g * a;
+  dg = da * (r * fmaf(g * b, b * r, 1.f)) * (u * a);
+  du = da * (ga * r);
 }
 
 // y = u * g / (1 + exp(-g)) in 32 bits.
@@ -241,11 +249,11 @@ __device__ __forceinline__ void drain(const Args& a, const Shape& sh, const Tile
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float g0 = T::lo(gw[k]), g1 = T::hi(gw[k]), u0 = T::lo(uw[k]), u1 = T::hi(uw[k]);
-          // silu' = s + g s (1 - s) = (s + g s) - g s s
-          const float s0 = sigmoid(g0), s1 = sigmoid(g1), d0 = d[2 * k], d1 = d[2 * k + 1];
-          const float h0 = g0 * s0, h1 = g1 * s1;
-          dg[k] = T::pack2(d0 * u0 * fmaf(-h0, s0, s0 + h0), d1 * u1 * fmaf(-h1, s1, s1 + h1));
-          du[k] = T::pack2(d0 * h0, d1 * h1);
+          float dg0, du0, dg1, du1;
+          swiglu_gradient(d[2 * k], g0, u0, dg0, du0);
+          swiglu_gradient(d[2 * k + 1], g1, u1, dg1, du1);
+          dg[k] = T::pack2(dg0, dg1);
+          du[k] = T::pack2(du0, du1);
         }
         if (i < sh.I && 8 * p + r < jn) {
           *reinterpret_cast<uint4*>(out + 8 * p * ld) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
