@@ -2,12 +2,13 @@
 // expert (decoding): bound by reading the codes, k / 2 bytes a weight row.
 //
 // W[i, k] = (q - z) s, one s (and z) per `group` of k. The codes go into the
-// 16-bit product of mma.m16n8k16 as exact small integers: OR-ing a nibble into
-// the fraction of a power of two gives 128 + q (bf16) or 64 + q (fp16) in one
-// instruction. Over one group sum_k (q - z) x = sum_k (OFF + q) x - (OFF + z)
-// sum_k x; the second term is what the accumulator starts from (sum_k x comes
-// from the same instruction with ones for weights), so it costs nothing per
-// weight row, and s multiplies the group's f32 sum: no rounding but f32's.
+// 16-bit product of mma.m16n8k16 exactly: OR-ing a nibble into the fraction of 1
+// gives 1 + q / OFF in one instruction, OFF = 128 (bf16) or 64 (fp16). Over one
+// group sum_k (q - z) x = OFF (sum_k (1 + q / OFF) x - (1 + z / OFF) sum_k x); the
+// second term is what the accumulator starts from (sum_k x comes from the same
+// instruction with ones for weights), so it costs nothing per weight row, s
+// multiplies the group's f32 sum, and OFF the result: no rounding but f32's. (With
+// OFF + q, the same in every bit, rows beyond 2^120 left f32's range on the way.)
 //
 // One tile: 64 MTW weight rows (SwiGLU: half gates, half ups) x up to 8 NT
 // tokens, 512 of k per stage of the ring. Warp 22 streams codes (128-byte rows)
@@ -113,11 +114,11 @@ __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t m
   return r;
 }
 
-// Nibbles i and i + 4 of a word of eight codes as OFF + q in two 16-bit halves.
+// Nibbles i and i + 4 of a word of eight codes as 1 + q / OFF in two 16-bit halves.
 template <bool kBf16, int I>
 __device__ __forceinline__ uint32_t codes2(uint32_t w) {
-  if constexpr (kBf16) return and_or(I == 0 ? w : w >> (4 * I), 0x000f000fu, 0x43004300u);  // 128 + q
-  else return and_or(I == 0 ? w << 4 : w >> (I == 0 ? 0 : 4 * I - 4), 0x00f000f0u, 0x54005400u);  // 64 + q
+  if constexpr (kBf16) return and_or(I == 0 ? w : w >> (4 * I), 0x000f000fu, 0x3f803f80u);  // 1 + q / 128
+  else return and_or(I == 0 ? w << 4 : w >> (I == 0 ? 0 : 4 * I - 4), 0x00f000f0u, 0x3c003c00u);  // 1 + q / 64
 }
 
 // Sizes of a stage: codes, x, scales (and zero points) and sums of x.
@@ -128,7 +129,7 @@ struct Stage {
   static constexpr int kX = 2 * kChunk;
   static constexpr int kScale = kX + 16 * 512 * NTMAX;
   static constexpr int kGroups = G32 ? 16 : 8;              // most groups of 512 of k
-  static constexpr int kGroupFloats = ZEROS ? 2 * kRows : kRows;  // of one group: s, or s and -(OFF + z)
+  static constexpr int kGroupFloats = ZEROS ? 2 * kRows : kRows;  // of one group: s, or s and -(1 + z / OFF)
   static constexpr int kSum = kScale + kGroups * kGroupFloats * 4;
   static constexpr int kSpans = G32 ? 2 : 1;                // spans with one scale in 64 of k
   static constexpr int kBytes = (kSum + 8 * kSpans * 8 * NTMAX * 4 + 1023) / 1024 * 1024;
@@ -338,7 +339,7 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
           float v = 0.f;
 #pragma unroll
           for (int w = 0; w < 4; ++w) v += red[((w * 4 + r) * 8 * NTMAX + j) * 20 + i];
-          return v;
+          return v * kOff;
         };
         const int i = threadIdx.x & 15;
         if constexpr (ACT) {
@@ -390,7 +391,7 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
               mma<T::kBf16>(v[c][h], ones, u.z, u.w, v[c][h][0], v[c][h][1], v[c][h][2], v[c][h][3]);
             }
           if (g == 0) {
-            const float f = ZEROS ? 1.f : -(kOff + 8.f);
+            const float f = ZEROS ? 1.f : -(1.f + 8.f / kOff);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               float* sum = reinterpret_cast<float*>(base + St::kSum) +
@@ -516,9 +517,11 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
           auto put = [&](int k, uint32_t v, uint32_t zw) {
             const float f = k & 1 ? T::hi(v) : T::lo(v);
             if constexpr (ZEROS) {
-              // 2^23 + z has z in its last bits; all of this is exact
-              const float z = __uint_as_float(__byte_perm(zw, 0x4b000000u, 0x7440 + (k & 3)));
-              *reinterpret_cast<float2*>(to + k * St::kGroupFloats) = make_float2(f, (8388608.f - kOff) - z);
+              // 2^23 / OFF + z / OFF has z in its last bits; all of this is exact
+              constexpr float kBase = 8388608.f / kOff;
+              constexpr uint32_t kBits = T::kBf16 ? 0x47800000u : 0x48000000u;  // of kBase
+              const float z = __uint_as_float(__byte_perm(zw, kBits, 0x7640 + (k & 3)));
+              *reinterpret_cast<float2*>(to + k * St::kGroupFloats) = make_float2(f, (kBase - 1.f) - z);
             } else {
               to[k * St::kGroupFloats] = f;
             }

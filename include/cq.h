@@ -430,7 +430,8 @@ int cq_expert_matmul_dw(const cq_expert_config* cfg, const void* dy, const void*
  *   scales  token type [G, n or 2n, k / group]
  *   zeros   uint8 [G, n or 2n, k / group], or NULL for z = 8
  * k % 32 == 0 and k % group == 0; x_dtype 0 or 1. An infinite x gives NaN in
- * its row (codes are summed with an offset that is taken off again).
+ * its row (codes are summed with an offset that is taken off again), and so may
+ * finite ones (bf16) whose |x| sum to more than 3e38 / 1.12 in one group.
  */
 int cq_expert_matmul_w4(const cq_expert_config* cfg, const void* x, const uint8_t* codes,
                         const void* scales, const uint8_t* zeros, const int64_t* group_rows,
