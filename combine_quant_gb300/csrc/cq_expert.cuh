@@ -111,6 +111,15 @@ __device__ __forceinline__ int expert_of(const int* tile, int G, int t) {
   return lo;
 }
 
+// y = u * g / (1 + exp(-g)) in 32 bits. exp(-g) leaves 32 bits for gates below -88 (and
+// __fdividef's range from -87.4), and u * g may where y does not. So with h =
+// exp(-|g| / 2): y = u * g / (1 + h^2) for g >= 0, else (u * h) * (g * h) / (1 + h^2).
+__device__ __forceinline__ float swiglu(float g, float u) {
+  const float h = __expf(-0.5f * fabsf(g)), r = __fdividef(1.f, fmaf(h, h, 1.f));
+  const float a = g >= 0.f ? 1.f : h;
+  return u * a * (g * a * r);
+}
+
 // Reads and clears a translation unit's status word, waiting for the stream.
 template <typename Word>
 int read_status_word(Word& word, uint32_t* status, cudaStream_t s) {

@@ -151,11 +151,6 @@ __device__ __forceinline__ void swiglu_gradient(float d, float g, float u, float
   du = da * (ga * r);
 }
 
-// y = u * g / (1 + exp(-g)) in 32 bits.
-__device__ __forceinline__ float swiglu(float g, float u) {
-  return __fdividef(u * g, 1.f + __expf(-g));
-}
-
 // Bytes of one results warp's staging buffer: 32 columns (j) of its 32 lanes
 // (i) in 16 bits, or 16 in 32 bits where another factor still comes (rows of 33
 // floats, so that neither the columns' stores nor the rows' loads meet in a bank).

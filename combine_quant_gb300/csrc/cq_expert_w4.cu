@@ -348,7 +348,7 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
             const float gv = total(r, j, i), uv = total(r + 2, j, i);
             if (o < sh.n_out)
               store1<T>(a.out, (size_t)(x.begin + x.j0 + j) * sh.n_out + o,
-                        __fdividef(uv * gv, 1.f + __expf(-gv)));
+                        swiglu(gv, uv));
           }
         } else {
           for (int v = threadIdx.x; v < x.jn * 64; v += 32 * kMulWarps) {

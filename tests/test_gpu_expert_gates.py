@@ -1,6 +1,6 @@
-"""The gradient through SwiGLU of the expert products where gates are far from 1, up to 2^100, and where two of its
-factors leave 32 bits together. The bounds are relative to the result and do not grow with the gate beyond what the
-exponential's own error does."""
+"""SwiGLU of the expert products, and its gradient, where gates and ups are far from 1: gates up to 2^100, ups whose
+product with the gate leaves 32 bits, results near the smallest that the type holds. The bounds are relative to the
+result and do not grow with the gate beyond what the exponential's own error does."""
 import pytest
 import torch
 
@@ -67,6 +67,47 @@ def test_gradient_where_two_factors_leave_32_bits():
     pre, d = torch.cat((g, sign * size), 1).bfloat16(), size.bfloat16()
     want, bound = gradient(d, pre, torch.bfloat16)
     ref.check(run_gradient(d, pre, 0), want, bound, "dpre")
+
+
+# Pairs of gate and up: u g leaves 32 bits where the result does not; 1 + e^-g is beyond 2^126; the result is 0.
+PAIRS = [(-2.0 ** 25, 1.0), (2.0 ** 25, -3.0), (-1e20, 1e20), (-400.0, 3e36), (-1e36, -1e36), (-87.5, 2.0 ** 60), (-88.0, -2.0 ** 60),
+         (-88.5, 2.0 ** 100), (-100.0, 2.0 ** 110), (-150.0, 2.0 ** 119), (-80.0, 2.0 ** 118), (2.0, 2.0 ** 118), (-0.5, 2.0 ** 118),
+         (2.0 ** 100, 2.0 ** -20), (0.0, 2.0 ** 100), (-60.0, 2.0 ** -20)]
+
+
+def _want(g, u):
+    g, u = g.double(), u.double()
+    y = u * g * torch.sigmoid(g)
+    return y, ref.rounded(y, y.abs() * exp_error(g), torch.bfloat16)
+
+
+@pytest.mark.gpu
+def test_forward_far_from_one():
+    """The same 16 results in each row's columns, from bf16 products that are exact."""
+    g, u = torch.tensor(PAIRS).bfloat16().T
+    x = torch.zeros(16, 64, dtype=torch.bfloat16)
+    x[:, 0], x[:, 1] = g, u
+    w = torch.zeros(1, 64, 64, dtype=torch.bfloat16)
+    w[0, :32, 0], w[0, 32:, 1] = 1, 1
+    cfg = cq.ExpertConfig(experts=1, rows=16, n=32, k=64, act=1)
+    y = cq.expert_matmul(cfg, x.to(DEV), w.to(DEV), torch.tensor([16], device=DEV))
+    want, bound = _want(g[:, None].expand(16, 32), u[:, None].expand(16, 32))
+    ref.check(y, want, bound, "y")
+
+
+@pytest.mark.gpu
+def test_forward_far_from_one_with_4_bit_weights():
+    """Gate and up in groups of their own: a group's offset codes give 9 - 8 = 1 times x exactly."""
+    g, u = torch.tensor(PAIRS).bfloat16().T
+    x = torch.zeros(16, 64, dtype=torch.bfloat16)
+    x[:, 0], x[:, 32] = g, u
+    codes = torch.full((1, 64, 32), 0x88, dtype=torch.uint8)
+    codes[0, :32, 0], codes[0, 32:, 16] = 0x89, 0x89
+    cfg = cq.ExpertConfig(experts=1, rows=16, n=32, k=64, act=1, group=32)
+    y = cq.expert_matmul_w4(cfg, x.to(DEV), codes.to(DEV), torch.ones(1, 64, 2, dtype=torch.bfloat16, device=DEV),
+                            torch.tensor([16], device=DEV))
+    want, bound = _want(g[:, None].expand(16, 32), u[:, None].expand(16, 32))
+    ref.check(y, want, bound, "y")
 
 
 def test_bounds_of_the_gradient_do_not_grow_with_the_gate():
