@@ -110,3 +110,28 @@ def check(got, value, bound, what=""):
     worst = int(over.argmax()) if over.numel() else 0
     assert not over.numel() or over.max() <= 0, (what, "worst at", worst, got.reshape(-1)[worst], value.reshape(-1)[worst],
                                                  bound.reshape(-1)[worst], "share over", float((over > 0).double().mean()))
+
+
+def w4_products(x, codes, scales, zeros, group, counts):
+    """The products with 4-bit weights and a bound of the kernel's own order of work, on the tensors' device.
+
+    Over a span (a group, or 64 of it) the sum of (OFF + q) x starts from -(OFF + z) times the span's sum of x, OFF 128
+    in bf16 and 64 in fp16. With A the span's sum of |x|: the start value is off by (span + 2) * 2^-23 * (OFF + 15) A,
+    the sum itself, whose parts are at most 2 (OFF + 15) A, by (span + 1) * 2^-23 times that; both meet the scale.
+    The spans' k / 32 sums at most, and the four shares of them, are added in 32 bits."""
+    span, off = min(group, 64), 128 if x.dtype == torch.bfloat16 else 64
+    k, wn = x.shape[1], codes.shape[1]
+    v = torch.zeros(sum(counts), wn, dtype=torch.float64, device=x.device)
+    b = torch.zeros_like(v)
+    for e, at in spans(counts):
+        if at.stop == at.start:
+            continue
+        q = torch.stack((codes[e] & 15, codes[e] >> 4), -1).view(wn, k // group, group).double()
+        q = q - (8.0 if zeros is None else zeros[e].double()[..., None])
+        s = scales[e].double().T[:, None]                                   # [groups, 1, wn]
+        xg = x[at].double().view(-1, k // group, group).transpose(0, 1)     # [groups, rows, group]
+        d = torch.bmm(xg, q.permute(1, 2, 0)) * s
+        err = (span + 2) * EPS * 3 * (off + 15) * xg.abs().sum(2, keepdim=True) * s.abs()
+        v[at] = d.sum(0)
+        b[at] = err.sum(0) + (k // 32 + 8) * EPS * (d.abs() + err).sum(0)
+    return v, b
