@@ -10,7 +10,7 @@ namespace expert {
 // The token type of a product's operands.
 enum { kBF16 = 0, kF16 = 1, kMxE4M3 = 2, kMxE5M2 = 3 };
 
-enum Op { kForward, kDx, kDw, kW4 };
+enum Op { kForward, kDx, kDw };
 
 struct Args {
   int32_t G, R, N, K;   // experts, rows, weight rows (2n with SwiGLU), inner length

@@ -10,7 +10,7 @@
 // multiplies the group's f32 sum, and OFF the result: no rounding but f32's. (With
 // OFF + q, the same in every bit, rows beyond 2^120 left f32's range on the way.)
 //
-// One tile: 64 MTW weight rows (SwiGLU: half gates, half ups) x up to 8 NT
+// One tile: 64 MTW weight rows (SwiGLU: half gates, half ups) x up to 16
 // tokens, 512 of k per stage of the ring. Warp 22 streams codes (128-byte rows)
 // and x (64-byte rows) with tiled copies, both swizzled so that no access below
 // meets a bank twice. Warps 16-19 put each 8 of x into the order in which the
@@ -50,6 +50,7 @@ __device__ uint32_t g_status;  // CQ_ST_* bits of these kernels on this device
 constexpr int kMulWarps = 16, kSumWarps = 4, kScaleWarps = 2;
 constexpr int kThreads = 32 * (kMulWarps + kSumWarps + kScaleWarps + 1);
 constexpr int kMaxStages = 8;
+constexpr int kMaxNT = 2;  // blocks of 8 tokens of a tile, at most
 
 // Dynamic shared memory that a CTA may use, beside a little static.
 constexpr size_t kSmemBytes = 227 * 1024 - 1024;
@@ -73,7 +74,7 @@ struct Tile {
   int e, begin, j0, jn, o0, nt;  // o0: first row of the tile (of each half)
 };
 
-template <int MTW, int NTMAX, bool ACT>
+template <int MTW, bool ACT>
 __device__ __forceinline__ Tile tile_at(const Shape& sh, const int* s_begin, const int* s_tile,
                                         int G, int t) {
   Tile x;
@@ -84,8 +85,8 @@ __device__ __forceinline__ Tile tile_at(const Shape& sh, const int* s_begin, con
   // The parts of one set of weight rows lie tiles_n apart: in flight together, so
   // the second finds the codes in L2, and spread over the CTAs.
   const int l = t - s_tile[x.e], part = l / sh.tiles_n;
-  x.j0 = part * (8 * NTMAX);
-  x.jn = min(8 * NTMAX, rows - x.j0);
+  x.j0 = part * (8 * kMaxNT);
+  x.jn = min(8 * kMaxNT, rows - x.j0);
   x.o0 = (l - part * sh.tiles_n) * (ACT ? 32 * MTW : 64 * MTW);
   x.nt = (x.jn + 7) / 8;
   return x;
@@ -122,28 +123,28 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w) {
 }
 
 // Sizes of a stage: codes, x, scales (and zero points) and sums of x.
-template <int MTW, int NTMAX, bool ZEROS, bool G32>
+template <int MTW, bool ZEROS, bool G32>
 struct Stage {
   static constexpr int kRows = 64 * MTW;
   static constexpr int kChunk = kRows * 128;                // codes of 256 of k
   static constexpr int kX = 2 * kChunk;
-  static constexpr int kScale = kX + 16 * 512 * NTMAX;
+  static constexpr int kScale = kX + 16 * 512 * kMaxNT;
   static constexpr int kGroups = G32 ? 16 : 8;              // most groups of 512 of k
   static constexpr int kGroupFloats = ZEROS ? 2 * kRows : kRows;  // of one group: s, or s and -(1 + z / OFF)
   static constexpr int kSum = kScale + kGroups * kGroupFloats * 4;
   static constexpr int kSpans = G32 ? 2 : 1;                // spans with one scale in 64 of k
-  static constexpr int kBytes = (kSum + 8 * kSpans * 8 * NTMAX * 4 + 1023) / 1024 * 1024;
+  static constexpr int kBytes = (kSum + 8 * kSpans * 8 * kMaxNT * 4 + 1023) / 1024 * 1024;
 };
 
 // 64 of k (two blocks of 32) of one multiplying warp. sw0, sw1: this thread's
 // code words of the two blocks (+ 2048 m, + 1024 for rows g + 8); sx: its x
 // (+ (h NT + n) 512); sum, scale: of its tokens and rows.
-template <typename T, int MTW, int NT, int NTMAX, bool ZEROS, bool G32>
-__device__ __forceinline__ void multiply(float (&acc)[MTW][NTMAX][4], const uint8_t* sw0,
+template <typename T, int MTW, int NT, bool ZEROS, bool G32>
+__device__ __forceinline__ void multiply(float (&acc)[MTW][kMaxNT][4], const uint8_t* sw0,
                                          const uint8_t* sw1, const uint8_t* sx, const float* sum,
                                          const float* scale) {
   constexpr bool kBf16 = T::kBf16;
-  constexpr int kSpan = Stage<MTW, NTMAX, ZEROS, G32>::kGroupFloats;  // from one group's scales to the next
+  constexpr int kSpan = Stage<MTW, ZEROS, G32>::kGroupFloats;  // from one group's scales to the next
   // H blocks of 32 of k under one scale, from block h0.
   auto span = [&](auto first, auto blocks) {
     constexpr int h0 = decltype(first)::value, H = decltype(blocks)::value, p = G32 ? h0 : 0;
@@ -168,7 +169,7 @@ __device__ __forceinline__ void multiply(float (&acc)[MTW][NTMAX][4], const uint
       if (h == 0) {
         float2 c[NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) c[n] = *reinterpret_cast<const float2*>(sum + p * 8 * NTMAX + 8 * n);
+        for (int n = 0; n < NT; ++n) c[n] = *reinterpret_cast<const float2*>(sum + p * 8 * kMaxNT + 8 * n);
 #pragma unroll
         for (int m = 0; m < MTW; ++m) {
           float2 o = make_float2(1.f, 1.f);
@@ -220,21 +221,21 @@ struct Places {
 };
 
 // All of k for one tile: false when a wait gave up.
-template <typename T, int MTW, int NT, int NTMAX, bool ZEROS, bool G32>
-__device__ __forceinline__ bool multiply_tile(float (&acc)[MTW][NTMAX][4], Bars& bars,
+template <typename T, int MTW, int NT, bool ZEROS, bool G32>
+__device__ __forceinline__ bool multiply_tile(float (&acc)[MTW][kMaxNT][4], Bars& bars,
                                               const uint8_t* ring, int S, uint32_t& s, uint32_t& lap,
                                               const Places& at, int kw, int K) {
-  using St = Stage<MTW, NTMAX, ZEROS, G32>;
+  using St = Stage<MTW, ZEROS, G32>;
   const uint32_t at_x = at.x + kw * 2 * 512 * NT;
   for (int left = K - kw * 64; left + kw * 64 > 0; left -= 512) {
     if (!mbar_wait_warp(&bars.ready[s], lap & 1)) return false;
     const uint8_t* base = ring + s * St::kBytes;
     auto chunk = [&](int c) {
       const uint8_t* scale = base + at.scale + c * at.scale_next;
-      multiply<T, MTW, NT, NTMAX, ZEROS, G32>(
+      multiply<T, MTW, NT, ZEROS, G32>(
           acc, base + c * St::kChunk + at.w, base + c * St::kChunk + (at.w ^ 16),
           base + at_x + c * (8 * 512 * NT),
-          reinterpret_cast<const float*>(base + at.sum + c * (4 * St::kSpans * 8 * NTMAX * 4)),
+          reinterpret_cast<const float*>(base + at.sum + c * (4 * St::kSpans * 8 * kMaxNT * 4)),
           reinterpret_cast<const float*>(scale));
     };
 #pragma unroll
@@ -257,14 +258,14 @@ __device__ __forceinline__ void store1(void* p, size_t i, float v) {
 }
 
 // ANY: rows of scales of any number of groups, else of whole fours.
-template <typename T, int MTW, int NTMAX, bool ACT, bool ZEROS, bool G32, bool ANY>
+template <typename T, int MTW, bool ACT, bool ZEROS, bool G32, bool ANY>
 __global__ void __launch_bounds__(kThreads, 1)
 w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
           const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x1,
           const __grid_constant__ CUtensorMap map_x2) {
-  using St = Stage<MTW, NTMAX, ZEROS, G32>;
+  using St = Stage<MTW, ZEROS, G32>;
   constexpr float kOff = T::kBf16 ? 128.f : 64.f;
-  constexpr int kRed = 4 * 4 * 8 * NTMAX * 20;  // floats of the sums' exchange
+  constexpr int kRed = 4 * 4 * 8 * kMaxNT * 20;  // floats of the sums' exchange
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Bars bars;
   const int S = sh.stages;
@@ -285,7 +286,7 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
   }
   griddep_wait();
   const bool bad = group_scan<kThreads>(a, s_begin, s_tile, [&](int rows) {
-    return sh.tiles_n * ((rows + 8 * NTMAX - 1) / (8 * NTMAX));
+    return sh.tiles_n * ((rows + 8 * kMaxNT - 1) / (8 * kMaxNT));
   });
   if (bad && blockIdx.x == 0) atomicOr(&g_status, (uint32_t)CQ_ST_BAD_ROWS);
   const int n_tiles = s_tile[a.G];
@@ -307,16 +308,16 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     Places at;
     at.w = rq * (16 * MTW * 128) + g * 128 + (((2 * kw) ^ g) << 4) + 4 * q;
     at.x = St::kX + g * 64 + ((q ^ ((g >> 1) & 3)) << 4);
-    at.sum = St::kSum + (kw * (St::kSpans * 8 * NTMAX) + 2 * q) * 4;
+    at.sum = St::kSum + (kw * (St::kSpans * 8 * kMaxNT) + 2 * q) * 4;
     at.scale = St::kScale + ((kw * 64 >> sh.shift) * St::kGroupFloats + (rq * 8 + g) * (St::kGroupFloats / 32)) * 4;
     at.scale_next = (256 >> sh.shift) * St::kGroupFloats * 4;
     for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
-      const Tile x = tile_at<MTW, NTMAX, ACT>(sh, s_begin, s_tile, a.G, t);
-      float acc[MTW][NTMAX][4] = {};
-      if (NTMAX == 1 || x.nt == 1)
-        ok = multiply_tile<T, MTW, 1, NTMAX, ZEROS, G32>(acc, bars, ring, S, s, lap, at, kw, a.K);
+      const Tile x = tile_at<MTW, ACT>(sh, s_begin, s_tile, a.G, t);
+      float acc[MTW][kMaxNT][4] = {};
+      if (x.nt == 1)
+        ok = multiply_tile<T, MTW, 1, ZEROS, G32>(acc, bars, ring, S, s, lap, at, kw, a.K);
       else
-        ok = multiply_tile<T, MTW, NTMAX, NTMAX, ZEROS, G32>(acc, bars, ring, S, s, lap, at, kw, a.K);
+        ok = multiply_tile<T, MTW, kMaxNT, ZEROS, G32>(acc, bars, ring, S, s, lap, at, kw, a.K);
       if (!ok) atomicOr(&g_status, (uint32_t)CQ_ST_TIMEOUT);
       // A warp that gave up attends all the same: the others would wait for it without
       // a limit. They leave together.
@@ -325,9 +326,9 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
 #pragma unroll
       for (int m = 0; m < MTW; ++m) {
         if (m > 0) bar_mul();
-        float* to = red + (kw * 4 + rq) * (8 * NTMAX * 20);
+        float* to = red + (kw * 4 + rq) * (8 * kMaxNT * 20);
 #pragma unroll
-        for (int n = 0; n < NTMAX; ++n)
+        for (int n = 0; n < kMaxNT; ++n)
           if (n < x.nt) {
             to[(8 * n + 2 * q) * 20 + g] = acc[m][n][0];
             to[(8 * n + 2 * q + 1) * 20 + g] = acc[m][n][1];
@@ -338,7 +339,7 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
         auto total = [&](int r, int j, int i) {
           float v = 0.f;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) v += red[((w * 4 + r) * 8 * NTMAX + j) * 20 + i];
+          for (int w = 0; w < 4; ++w) v += red[((w * 4 + r) * 8 * kMaxNT + j) * 20 + i];
           return v * kOff;
         };
         const int i = threadIdx.x & 15;
@@ -365,7 +366,7 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     constexpr uint32_t kOne = T::kBf16 ? 0x3f803f80u : 0x3c003c00u;
     const uint32_t ones[4] = {kOne, kOne, kOne, kOne};
     for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
-      const Tile x = tile_at<MTW, NTMAX, ACT>(sh, s_begin, s_tile, a.G, t);
+      const Tile x = tile_at<MTW, ACT>(sh, s_begin, s_tile, a.G, t);
       for (int st = 0; st < n_stages; ++st) {
         if (!(ok = wait(&bars.full[s], lap & 1))) break;
         uint8_t* base = ring + s * St::kBytes;
@@ -395,10 +396,10 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               float* sum = reinterpret_cast<float*>(base + St::kSum) +
-                           (c * 4 + kw) * (St::kSpans * 8 * NTMAX) + 2 * q + 8 * n;
+                           (c * 4 + kw) * (St::kSpans * 8 * kMaxNT) + 2 * q + 8 * n;
               if constexpr (G32) {
                 *reinterpret_cast<float2*>(sum) = make_float2(f * v[c][0][0], f * v[c][0][1]);
-                *reinterpret_cast<float2*>(sum + 8 * NTMAX) = make_float2(f * v[c][1][0], f * v[c][1][1]);
+                *reinterpret_cast<float2*>(sum + 8 * kMaxNT) = make_float2(f * v[c][1][0], f * v[c][1][1]);
               } else {
                 *reinterpret_cast<float2*>(sum) =
                     make_float2(f * (v[c][0][0] + v[c][1][0]), f * (v[c][0][1] + v[c][1][1]));
@@ -419,6 +420,7 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
     constexpr int kFit = 48 / (kPer * (kW + (ZEROS ? kZW : 0)));  // in 48 registers
     constexpr int kMost = MTW == 2 && ZEROS ? 3 : 4;              // (groups of 64: 74 us against 94 with 4)
     constexpr int kAhead = kFit > kMost ? kMost : kFit;
+    static_assert(!ANY || kAhead >= 2, "a row's last word comes from the next stage's buffer");
     const uint16_t* scales = static_cast<const uint16_t*>(a.scales4);
     const int per_cta = n_tiles > (int)blockIdx.x ? (n_tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
     const int total = per_cta * n_stages, ng = 512 >> sh.shift;
@@ -440,7 +442,7 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
       if (++st == n_stages) st = 0, ++tile;
       const int first = st * ng;
       if (st == 0) {
-        const Tile x = tile_at<MTW, NTMAX, ACT>(sh, s_begin, s_tile, a.G, blockIdx.x + tile * gridDim.x);
+        const Tile x = tile_at<MTW, ACT>(sh, s_begin, s_tile, a.G, blockIdx.x + tile * gridDim.x);
 #pragma unroll
         for (int b = 0; b < kPer; ++b) {
           const int r = r0 + 64 * b, half = ACT ? r / (32 * MTW) : 0, rh = r - half * 32 * MTW;
@@ -550,8 +552,8 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
   } else {
     // ---- copies of codes and x ----
     for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
-      const Tile x = tile_at<MTW, NTMAX, ACT>(sh, s_begin, s_tile, a.G, t);
-      const CUtensorMap* mx = NTMAX == 1 || x.nt == 1 ? &map_x1 : &map_x2;
+      const Tile x = tile_at<MTW, ACT>(sh, s_begin, s_tile, a.G, t);
+      const CUtensorMap* mx = x.nt == 1 ? &map_x1 : &map_x2;
       for (int st = 0; st < n_stages; ++st) {
         if (lap > 0 && !(ok = wait(&bars.empty[s], (lap & 1) ^ 1))) break;
         if (elect_one()) {
@@ -575,10 +577,10 @@ w4_kernel(const __grid_constant__ Args a, const __grid_constant__ Shape sh,
 }
 
 // ---- host ----
-template <typename T, int MTW, int NTMAX, bool ACT, bool ZEROS, bool G32, bool ANY>
+template <typename T, int MTW, bool ACT, bool ZEROS, bool G32, bool ANY>
 cudaError_t launch_t(const Args& a, cudaStream_t s) {
-  constexpr auto kernel = w4_kernel<T, MTW, NTMAX, ACT, ZEROS, G32, ANY>;
-  using St = Stage<MTW, NTMAX, ZEROS, G32>;
+  constexpr auto kernel = w4_kernel<T, MTW, ACT, ZEROS, G32, ANY>;
+  using St = Stage<MTW, ZEROS, G32>;
   Shape sh = {};
   sh.n_out = ACT ? a.N / 2 : a.N;
   sh.tiles_n = (a.N + St::kRows - 1) / St::kRows;
@@ -593,40 +595,39 @@ cudaError_t launch_t(const Args& a, cudaStream_t s) {
   const uint32_t bw[] = {128, (uint32_t)(St::kRows / halves), (uint32_t)halves, 1};
   if (!make_map(&mw, a.w, kMapU8, 4, dw, sw, bw, kSwizzle128)) return cudaErrorUnknown;
   const uint64_t dx[] = {32, R, K / 32}, sx[] = {K * 2, 64};
-  for (int i = 0; i < NTMAX; ++i) {
+  for (int i = 0; i < kMaxNT; ++i) {
     const uint32_t bx[] = {32, 8u << i, 16};
     if (!make_map(&mx[i], a.x, T::kBf16 ? kMapBF16 : kMapF16, 3, dx, sx, bx, kSwizzle64))
       return cudaErrorUnknown;
   }
-  if (NTMAX == 1) mx[1] = mx[0];
   // As many stages as fit beside the exchange of the sums and the lists.
-  const size_t fixed = 1024 + 4 * 4 * 8 * NTMAX * 20 * 4 + 8 * ((size_t)a.G + 1);
+  const size_t fixed = 1024 + 4 * 4 * 8 * kMaxNT * 20 * 4 + 8 * ((size_t)a.G + 1);
   sh.stages = (int)std::min<size_t>(kMaxStages, (kSmemBytes - fixed) / St::kBytes);
   const size_t smem = fixed + sh.stages * (size_t)St::kBytes;
   cudaError_t e = prepare_kernel<kernel>(smem);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorUnknown;
-  const int64_t most = (int64_t)sh.tiles_n * (a.R / (8 * NTMAX) + std::min(a.G, a.R));
+  const int64_t most = (int64_t)sh.tiles_n * (a.R / (8 * kMaxNT) + std::min(a.G, a.R));
   const int grid = (int)std::min<int64_t>(sms, most);
   return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, s, a, sh, mw, mx[0], mx[1]);
 }
 
-template <typename T, int MTW, int NTMAX, bool ACT, bool ZEROS, bool G32>
+template <typename T, int MTW, bool ACT, bool ZEROS, bool G32>
 cudaError_t launch_r(const Args& a, cudaStream_t s) {
-  if (a.K / a.group % 4 == 0) return launch_t<T, MTW, NTMAX, ACT, ZEROS, G32, false>(a, s);
+  if (a.K / a.group % 4 == 0) return launch_t<T, MTW, ACT, ZEROS, G32, false>(a, s);
   // Tiles of 128 rows, zero points, groups of 32: the scales of two rows would not fit
   // the registers (215 us against 119 in tiles of 64: 32 experts of 4 rows, 2048 x 7200).
-  return launch_t<T, ZEROS && G32 ? 1 : MTW, NTMAX, ACT, ZEROS, G32, true>(a, s);
+  return launch_t<T, ZEROS && G32 ? 1 : MTW, ACT, ZEROS, G32, true>(a, s);
 }
 
-template <typename T, int MTW, int NTMAX, bool ACT>
+template <typename T, int MTW, bool ACT>
 cudaError_t launch_g(const Args& a, cudaStream_t s) {
   if (a.zeros4)
-    return a.group == 32 ? launch_r<T, MTW, NTMAX, ACT, true, true>(a, s)
-                         : launch_r<T, MTW, NTMAX, ACT, true, false>(a, s);
-  return a.group == 32 ? launch_r<T, MTW, NTMAX, ACT, false, true>(a, s)
-                       : launch_r<T, MTW, NTMAX, ACT, false, false>(a, s);
+    return a.group == 32 ? launch_r<T, MTW, ACT, true, true>(a, s)
+                         : launch_r<T, MTW, ACT, true, false>(a, s);
+  return a.group == 32 ? launch_r<T, MTW, ACT, false, true>(a, s)
+                       : launch_r<T, MTW, ACT, false, false>(a, s);
 }
 
 // Tiles of 128 weight rows where they give every SM two, else of 64 (a tile of 64
@@ -635,8 +636,8 @@ cudaError_t launch_g(const Args& a, cudaStream_t s) {
 template <typename T, bool ACT>
 cudaError_t launch_a(const Args& a, cudaStream_t s) {
   const int64_t rows = (int64_t)std::min(a.G, a.R) * a.N;  // most weight rows read
-  if (rows >= 128 * 2 * (int64_t)sm_count()) return launch_g<T, 2, 2, ACT>(a, s);
-  return launch_g<T, 1, 2, ACT>(a, s);
+  if (rows >= 128 * 2 * (int64_t)sm_count()) return launch_g<T, 2, ACT>(a, s);
+  return launch_g<T, 1, ACT>(a, s);
 }
 
 }  // namespace
