@@ -33,12 +33,12 @@
 // of their products.
 //
 // What bounds it: below about 280 rows an expert reading the weights, above the
-// tensor cores. Measured on one GB300 (copy 6.79 TB/s, cuBLAS bf16 1.88 PFLOP/s
-// measured): 8192^3 1.9 PFLOP/s; 32 experts of 512 rows, hidden 7168, SwiGLU with
-// n 2048: 544 us, 1.77 PFLOP/s; 64 experts, 777 rows in fp16, n 1536, k 4096:
-// 116 us, 6.2 TB/s; mx fp8, 32 experts of 480 rows: 326 us, 2.77 PFLOP/s, of 16
-// rows (n 7168, k 2048): 87 us, 5.4 TB/s; dw, 32 experts of 512 rows, 4096 x 7168:
-// 668 us, 1.44 PFLOP/s (its 1.9 GB of results and eight stages per tile).
+// tensor cores. Measured on one GB300 (copy 6.79 TB/s): 8192^3 1.89 PFLOP/s where
+// cuBLAS ran at 2.01 in the same process; 32 experts of 512 rows, hidden 7168,
+// SwiGLU with n 2048: 553 us, 1.74 PFLOP/s; 64 experts, 777 rows in fp16, n 1536,
+// k 4096: 116 us, 6.2 TB/s; mx fp8, 32 experts of 480 rows: 344 us, 2.62 PFLOP/s,
+// of 16 rows (n 7168, k 2048): 87 us, 5.4 TB/s; dw, 32 experts of 512 rows, 4096 x
+// 7168: 663 us, 1.45 PFLOP/s (its 1.9 GB of results and eight stages per tile).
 #include <cuda_runtime.h>
 
 #include <algorithm>

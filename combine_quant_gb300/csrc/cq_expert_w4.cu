@@ -24,8 +24,10 @@
 // the codes' bytes as far as the memory goes (5.9 TB/s with the multiplying taken
 // out), in practice the multiplying warps' instructions. Measured on one GB300, 32
 // experts, hidden 7168, SwiGLU with n 2048, groups of 128 (485 MB): up to 8 rows an
-// expert 107 us (4.5 TB/s), 16 rows 137 us, every further 16 rows about 130 us; one
-// row through 8192 x 8192 14.5 us, with groups of 32 and zero points 20 us.
+// expert 112 us (4.3 TB/s), 16 rows 143 us, every further 16 rows about 130 us; one
+// row through 8192 x 8192 15.2 us, with groups of 32 and zero points 19.5 us. 23 warps
+// leave 80 registers a thread, and 34 of the 60 forms spill (172 bytes of reloads at
+// most).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -393,7 +393,7 @@ int cq_check_expert_config(const cq_expert_config* cfg);
  *   w_scales   mx: uint8 [G, n or 2n, SC]; else NULL
  *   group_rows int64 [G]
  *   y          [R, n]
- *   pre        NULL, or with act 1 [R, 2n]: receives p (for the backward pass)
+ *   pre        NULL, or with act 1 [R, 2n], the type of y: receives p (for the backward pass)
  * Products accumulate in 32 bits and are rounded once; SwiGLU takes the
  * unrounded products.
  */
@@ -437,7 +437,8 @@ int cq_expert_matmul_w4(const cq_expert_config* cfg, const void* x, const uint8_
                         const void* scales, const uint8_t* zeros, const int64_t* group_rows,
                         void* y, void* stream);
 /* Pointers of the expert products (else CQ_ERR_ARG): 16-byte aligned, group_rows
- * 8-byte. x, y, dy, pre and dx may be NULL when rows is 0. */
+ * 8-byte. x, y, dy, pre and dx may be NULL when rows is 0. A call's results must
+ * not overlap its inputs. */
 
 /* The expert products take no workspace; their status word (CQ_ST_BAD_ROWS,
  * CQ_ST_TIMEOUT) is one word per device. Synchronise `stream`, copy the word of
