@@ -17,7 +17,10 @@ from .api import (Config, DispatchResult, ExpertConfig, alloc_dispatch_outputs, 
                   moe_combine, moe_dispatch, read_combine_status, read_status,
                   cq_expert_matmul, cq_expert_matmul_dw, cq_expert_matmul_dx, cq_expert_matmul_w4,
                   cq_read_expert_status, expert_matmul, expert_matmul_dw, expert_matmul_dx,
-                  expert_matmul_w4, read_expert_status)
+                  expert_matmul_w4, read_expert_status,
+                  MoeConfig, NormConfig, NormResult, alloc_moe_workspace, cq_expert_matmul_b128,
+                  cq_expert_matmul_b128_dx, cq_moe_layer, cq_norm_grad, cq_norm_quant, expert_matmul_b128,
+                  expert_matmul_b128_dx, moe_layer, norm_grad, norm_quant)
 from ._lib import (CQ_ST_BAD_ID, CQ_ST_BAD_MASK, CQ_ST_BAD_ROWS, CQ_ST_INTERNAL, CQ_ST_TIMEOUT,  # noqa: F401
                    CqError)
-from .weights import quantize_mx, quantize_w4  # noqa: F401
+from .weights import quantize_b128, quantize_mx, quantize_w4  # noqa: F401

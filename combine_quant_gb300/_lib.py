@@ -23,6 +23,12 @@ EXPERT_CONFIG_FIELDS = (
     "experts_per_rank",
 )
 
+MOE_CONFIG_FIELDS = (
+    "tokens", "experts", "topk", "hidden", "inter", "x_dtype", "w_dtype", "mask_ndim", "out_dtype",
+)
+
+NORM_CONFIG_FIELDS = ("rows", "hidden", "x_dtype", "norm", "quant_mode", "y_dtype", "eps")
+
 CQ_OK = 0
 CQ_ERR_ARG = -1
 CQ_ERR_UNSUPPORTED = -2
@@ -48,7 +54,10 @@ EXPORTS = (
     "cq_read_status", "cq_strerror", "cq_dispatch_noalloc", "cq_combine_quant", "cq_combine_q8",
     "cq_read_combine_status", "cq_check_bounded_wait", "cq_combine_ws", "cq_dispatch_one_kernel",
     "cq_check_bounded_meet", "cq_check_expert_config", "cq_expert_matmul", "cq_expert_matmul_dx", "cq_expert_matmul_dw",
-    "cq_expert_matmul_w4", "cq_read_expert_status",
+    "cq_expert_matmul_w4", "cq_read_expert_status", "cq_check_expert_b128_config",
+    "cq_expert_matmul_b128", "cq_expert_matmul_b128_dx", "cq_check_moe_config",
+    "cq_moe_workspace_size", "cq_moe_layer", "cq_check_norm_config", "cq_norm_workspace_size",
+    "cq_norm_quant", "cq_norm_grad",
 )
 
 
@@ -58,6 +67,14 @@ class CqConfig(ctypes.Structure):
 
 class CqExpertConfig(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int32) for f in EXPERT_CONFIG_FIELDS]
+
+
+class CqMoeConfig(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in MOE_CONFIG_FIELDS]
+
+
+class CqNormConfig(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_float if f == "eps" else ctypes.c_int32) for f in NORM_CONFIG_FIELDS]
 
 
 class CqError(RuntimeError):
@@ -80,7 +97,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             "(the CUDA path has no fallback)")
     L = ctypes.CDLL(path)
     P, cfgp = ctypes.c_void_p, ctypes.POINTER(CqConfig)
-    ecfgp = ctypes.POINTER(CqExpertConfig)
+    ecfgp, mcfgp, ncfgp = (ctypes.POINTER(c) for c in (CqExpertConfig, CqMoeConfig, CqNormConfig))
     i32, i64, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     sig = {
         "cq_check_config": ([cfgp], ctypes.c_int),
@@ -112,6 +129,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "cq_expert_matmul_dx": ([ecfgp] + [P] * 6, ctypes.c_int),
         "cq_expert_matmul_dw": ([ecfgp] + [P] * 5, ctypes.c_int),
         "cq_expert_matmul_w4": ([ecfgp] + [P] * 7, ctypes.c_int),
+        "cq_check_expert_b128_config": ([ecfgp], ctypes.c_int),
+        "cq_expert_matmul_b128": ([ecfgp] + [P] * 9, ctypes.c_int),
+        "cq_expert_matmul_b128_dx": ([ecfgp] + [P] * 8, ctypes.c_int),
+        "cq_check_moe_config": ([mcfgp], ctypes.c_int),
+        "cq_moe_workspace_size": ([mcfgp], sz),
+        "cq_moe_layer": ([mcfgp] + [P] * 10 + [sz, P], ctypes.c_int),
+        "cq_check_norm_config": ([ncfgp], ctypes.c_int),
+        "cq_norm_workspace_size": ([ncfgp], sz),
+        "cq_norm_quant": ([ncfgp] + [P] * 8, ctypes.c_int),
+        "cq_norm_grad": ([ncfgp] + [P] * 7 + [sz, P], ctypes.c_int),
         "cq_read_expert_status": ([P, P], ctypes.c_int),
         "cq_strerror": ([ctypes.c_int], ctypes.c_char_p),
     }

@@ -116,6 +116,10 @@ class ExpertConfig:
     def check(self) -> int:
         return _lib.load().cq_check_expert_config(ctypes.byref(self.as_c()))
 
+    def check_b128(self) -> int:
+        """The rules of the products from fp8 with scales per 128 (cq_check_expert_b128_config)."""
+        return _lib.load().cq_check_expert_b128_config(ctypes.byref(self.as_c()))
+
     @property
     def weight_rows(self) -> int:
         return 2 * self.n if self.act == 1 else self.n
@@ -159,6 +163,9 @@ class _ExpertPlan:
         self.x_scales, self.w_scales = (R, cfg.scale_cols), (G, WN, cfg.scale_cols)
         self.codes = (G, WN, K // 2)
         self.groups = (G, WN, K // cfg.group if cfg.group > 0 else 0)
+        nb, kb = -(-cfg.n // 128), -(-K // 128)  # b128: blocks; the halves of act 1 have their own
+        self.row_scales, self.y_scales, self.dy_scales = (R, kb), (R, nb), (R, nb * (2 if cfg.act == 1 else 1))
+        self.block_scales = (G, self.dy_scales[1], kb)
 
 
 @functools.lru_cache(maxsize=256)
@@ -168,6 +175,121 @@ def _plan_of(*fields) -> _ExpertPlan:
 
 def _expert_plan(cfg: ExpertConfig) -> _ExpertPlan:
     return _plan_of(*vars(cfg).values())  # half the time of hashing and comparing the config itself
+
+
+@dataclass(frozen=True)
+class MoeConfig:
+    """Attributes of the whole layer for a few tokens (cq_moe_config in include/cq.h)."""
+    tokens: int
+    experts: int
+    topk: int
+    hidden: int
+    inter: int
+    x_dtype: int = 0       # 0 bf16, 1 fp16
+    w_dtype: int = 0       # weights: 0 the type of x, 1 fp8 e4m3 with a scale per 128 x 128
+    mask_ndim: int = 0     # 1 per token, 2 per (token, slot)
+    out_dtype: int = 0     # y: 0 the type of x, 1 f32
+
+    def as_c(self) -> _lib.CqMoeConfig:
+        return _c_moe_config(self)
+
+    def check(self) -> int:
+        return _lib.load().cq_check_moe_config(ctypes.byref(self.as_c()))
+
+    @property
+    def workspace_size(self) -> int:
+        return int(_lib.load().cq_moe_workspace_size(ctypes.byref(self.as_c())))
+
+
+@functools.lru_cache(maxsize=256)
+def _c_moe_config(cfg: MoeConfig) -> _lib.CqMoeConfig:
+    return _lib.CqMoeConfig(**asdict(cfg))
+
+
+@dataclass(frozen=True)
+class NormConfig:
+    """Attributes of the norm with quantised rows (cq_norm_config in include/cq.h)."""
+    rows: int
+    hidden: int
+    x_dtype: int = 0       # 0 bf16, 1 fp16
+    norm: int = 1          # 1 root-mean-square norm, 0 none
+    quant_mode: int = 0    # 0 no codes, else dispatch's modes 2 to 5
+    y_dtype: int = 0       # fp8 codes of modes 3-5: 0 e4m3fn, 1 e5m2
+    eps: float = 1e-6
+
+    def as_c(self) -> _lib.CqNormConfig:
+        return _c_norm_config(self)
+
+    def check(self) -> int:
+        return _lib.load().cq_check_norm_config(ctypes.byref(self.as_c()))
+
+    @property
+    def workspace_size(self) -> int:
+        """Bytes of norm_grad's workspace."""
+        return int(_lib.load().cq_norm_workspace_size(ctypes.byref(self.as_c())))
+
+
+@functools.lru_cache(maxsize=256)
+def _c_norm_config(cfg: NormConfig) -> _lib.CqNormConfig:
+    return _lib.CqNormConfig(**asdict(cfg))
+
+
+_TOKEN_TYPES = (torch.bfloat16, torch.float16)
+
+
+class _MoePlan:
+    """What the calls derive from a layer's config, kept per distinct config."""
+
+    def __init__(self, cfg: MoeConfig):
+        T, G, K, H, N = cfg.tokens, cfg.experts, cfg.topk, cfg.hidden, cfg.inter
+        _lib.check(cfg.check(), "MoeConfig")
+        self.struct = cfg.as_c()
+        self.ref = ctypes.byref(self.struct)
+        self.x, self.ids = (T, H), (T, K)
+        self.w13, self.w2 = (G, 2 * N, H), (G, H, N)
+        hb, nb = -(-H // 128), -(-N // 128)
+        self.w13_scales, self.w2_scales = (G, 2 * nb, hb), (G, hb, nb)
+        self.mask = {0: None, 1: (T,), 2: (T, K)}[cfg.mask_ndim]
+        self.fp8 = cfg.w_dtype == 1
+        self.dtype = _TOKEN_TYPES[cfg.x_dtype]
+        self.wdtype = torch.uint8 if self.fp8 else self.dtype
+        self.out = torch.float32 if cfg.out_dtype == 1 else self.dtype
+        self.workspace = cfg.workspace_size
+
+
+class _NormPlan:
+    """What the calls derive from a norm's config, kept per distinct config."""
+
+    def __init__(self, cfg: NormConfig):
+        _lib.check(cfg.check(), "NormConfig")
+        self.struct = cfg.as_c()
+        self.ref = ctypes.byref(self.struct)
+        R, H = cfg.rows, cfg.hidden
+        self.mode, self.norm = cfg.quant_mode, cfg.norm
+        self.dtype = _TOKEN_TYPES[cfg.x_dtype]
+        self.rows, self.row = (R, H), (H,)
+        self.codes = torch.int8 if cfg.quant_mode == 2 else torch.uint8
+        self.scales, self.scale_dtype = {
+            0: (None, None), 2: ((R,), torch.float32), 3: ((R, -(-H // 128)), torch.float32),
+        }.get(cfg.quant_mode, ((R, (H // 32 + 1) // 2 * 2), torch.uint8))
+        self.workspace = cfg.workspace_size
+
+
+@functools.lru_cache(maxsize=256)
+def _moe_plan_of(*fields) -> _MoePlan:
+    return _MoePlan(MoeConfig(*fields))
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_plan_of(*fields) -> _NormPlan:
+    return _NormPlan(NormConfig(*fields))
+
+
+class NormResult(NamedTuple):
+    y: Optional[torch.Tensor]       # [R, H] token type
+    sum: Optional[torch.Tensor]     # [R, H] token type: x + residual
+    codes: Optional[torch.Tensor]   # [R, H] int8 / uint8 (fp8 bytes)
+    scales: Optional[torch.Tensor]  # f32 [R] or [R, Ceil(H, 128)], or uint8 [R, Align2(H / 32)]
 
 
 class DispatchResult(NamedTuple):
@@ -604,6 +726,154 @@ def expert_matmul_w4(cfg: ExpertConfig, x: torch.Tensor, codes: torch.Tensor,
     return y
 
 
+def expert_matmul_b128(cfg: ExpertConfig, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
+                       w_scales: torch.Tensor, group_rows: torch.Tensor,
+                       pre: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                       y_scales: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """expert_matmul from fp8 rows with one f32 scale per 128 columns (dispatch
+    mode 3) and fp8 weights with one per 128 x 128 block (cq_expert_matmul_b128):
+    y [rows, n], with `y_scales` [rows, Ceil(n, 128)] (receives them) e4m3 codes."""
+    p = _expert_plan(cfg)
+    dev = _group_rows(p, group_rows)
+    if x is None or w is None or x_scales is None or w_scales is None:
+        raise ValueError("x, x_scales, w and w_scales are required")
+    px, pw = _arg(x, "x", torch.uint8, p.x, dev), _arg(w, "w", torch.uint8, p.w, dev)
+    pxs = _arg(x_scales, "x_scales", torch.float32, p.row_scales, dev)
+    pws = _arg(w_scales, "w_scales", torch.float32, p.block_scales, dev)
+    if pre is not None and p.act != 1:
+        raise ValueError("pre goes with act 1 only")
+    ppre = _arg(pre, "pre", p.result, p.dy, dev)
+    pys = _arg(y_scales, "y_scales", torch.float32, p.y_scales, dev)
+    y, py = _result(y, "y", p.result if y_scales is None else torch.uint8, p.y, dev)
+    _expert_call("cq_expert_matmul_b128", dev, p.ref, px, pxs, pw, pws, group_rows.data_ptr(), py, pys, ppre)
+    return y
+
+
+def expert_matmul_b128_dx(cfg: ExpertConfig, dy: torch.Tensor, dy_scales: torch.Tensor,
+                          w: torch.Tensor, w_scales: torch.Tensor, group_rows: torch.Tensor,
+                          pre: Optional[torch.Tensor] = None,
+                          dx: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of expert_matmul_b128's input (cq_expert_matmul_b128_dx) from dy in
+    fp8 [rows, n or 2n] with a scale per 128 columns (of each half with act 1):
+    [rows, k], or with `pre` [rows, 2k] (the input was SwiGLU of pre) the gradient
+    of pre."""
+    p = _expert_plan(cfg)
+    dev = _group_rows(p, group_rows)
+    if dy is None or w is None or dy_scales is None or w_scales is None:
+        raise ValueError("dy, dy_scales, w and w_scales are required")
+    pdy, pw = _arg(dy, "dy", torch.uint8, p.dy, dev), _arg(w, "w", torch.uint8, p.w, dev)
+    pds = _arg(dy_scales, "dy_scales", torch.float32, p.dy_scales, dev)
+    pws = _arg(w_scales, "w_scales", torch.float32, p.block_scales, dev)
+    ppre = _arg(pre, "pre", p.result, p.pre_k, dev)
+    dx, pdx = _result(dx, "dx", p.result, p.x if pre is None else p.pre_k, dev)
+    _expert_call("cq_expert_matmul_b128_dx", dev, p.ref, pdy, pds, pw, pws, group_rows.data_ptr(), ppre, pdx)
+    return dx
+
+
+def _workspace(t: Optional[torch.Tensor], nbytes: int, dev: torch.device) -> tuple[torch.Tensor, int, int]:
+    """A workspace, the caller's (checked) or a new one, its address and its bytes."""
+    if t is None:
+        t = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        _need(t, "workspace", torch.uint8, None, dev)
+    return t, t.data_ptr(), t.numel()
+
+
+def alloc_moe_workspace(cfg: MoeConfig, device) -> torch.Tensor:
+    """A workspace for moe_layer (no initialisation needed)."""
+    return torch.empty(_moe_plan_of(*vars(cfg).values()).workspace, dtype=torch.uint8, device=device)
+
+
+def moe_layer(cfg: MoeConfig, x: torch.Tensor, expert_ids: torch.Tensor, expert_scales: torch.Tensor,
+              w13: torch.Tensor, w2: torch.Tensor, w13_scales: Optional[torch.Tensor] = None,
+              w2_scales: Optional[torch.Tensor] = None,
+              x_active_mask: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None,
+              y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The whole layer for up to 64 tokens (cq_moe_layer): gate and up products,
+    SwiGLU, down product and the weighted sum of each token's experts, y [T, H].
+    A workspace that the caller passes must not serve two calls at once."""
+    p = _moe_plan_of(*vars(cfg).values())
+    if x is None or expert_ids is None or expert_scales is None or w13 is None or w2 is None:
+        raise ValueError("x, expert_ids, expert_scales, w13 and w2 are required")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    dev = x.device
+    if p.fp8 != (w13_scales is not None) or p.fp8 != (w2_scales is not None):
+        raise ValueError("w13_scales and w2_scales go with w_dtype 1, which needs them")
+    if (p.mask is not None) != (x_active_mask is not None):
+        raise ValueError("x_active_mask goes with mask_ndim 1 or 2, which need it")
+    px = _arg(x, "x", p.dtype, p.x, dev)
+    pids = _arg(expert_ids, "expert_ids", torch.int32, p.ids, dev)
+    psc = _arg(expert_scales, "expert_scales", torch.float32, p.ids, dev)
+    pm = _arg(x_active_mask, "x_active_mask", torch.uint8, p.mask, dev)
+    p13, p2 = _arg(w13, "w13", p.wdtype, p.w13, dev), _arg(w2, "w2", p.wdtype, p.w2, dev)
+    s13 = _arg(w13_scales, "w13_scales", torch.float32, p.w13_scales, dev)
+    s2 = _arg(w2_scales, "w2_scales", torch.float32, p.w2_scales, dev)
+    y, py = _result(y, "y", p.out, p.x, dev)
+    ws, pws, nws = _workspace(workspace, p.workspace, dev)
+    _expert_call("cq_moe_layer", dev, p.ref, px, pids, psc, pm, p13, s13, p2, s2, py, pws, nws)
+    return y
+
+
+def norm_quant(cfg: NormConfig, x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+               residual: Optional[torch.Tensor] = None, with_y: bool = True,
+               with_sum: Optional[bool] = None, out: Optional[NormResult] = None) -> NormResult:
+    """The residual's addition, the root-mean-square norm (cfg.norm) and rows
+    quantised by dispatch's mode cfg.quant_mode (cq_norm_quant). `with_y`: the rows
+    in 16 bits too; `with_sum` (default: where there is a residual): x + residual.
+    `out` gives the results' tensors instead (None: not written; sum may be x or
+    residual itself)."""
+    p = _norm_plan_of(*vars(cfg).values())
+    if x is None:
+        raise ValueError("x is required")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if weight is not None and not p.norm:
+        raise ValueError("weight goes with norm 1 only")
+    dev = x.device
+    px = _arg(x, "x", p.dtype, p.rows, dev)
+    pr = _arg(residual, "residual", p.dtype, p.rows, dev)
+    pw = _arg(weight, "weight", p.dtype, p.row, dev)
+    if out is None:
+        if with_sum is None:
+            with_sum = residual is not None
+        new = lambda want, dtype, shape: torch.empty(shape, dtype=dtype, device=dev) if want else None  # noqa: E731
+        out = NormResult(new(with_y or p.mode == 0, p.dtype, p.rows), new(with_sum, p.dtype, p.rows),
+                         new(p.mode != 0, p.codes, p.rows), new(p.mode != 0, p.scale_dtype, p.scales))
+    if p.mode == 0 and (out.y is None or out.codes is not None or out.scales is not None):
+        raise ValueError("quant_mode 0 gives y, and neither codes nor scales")
+    if p.mode != 0 and (out.codes is None or out.scales is None):
+        raise ValueError("codes and scales are required with this quant_mode")
+    py, psum = _arg(out.y, "y", p.dtype, p.rows, dev), _arg(out.sum, "sum", p.dtype, p.rows, dev)
+    pc = _arg(out.codes, "codes", p.codes, p.rows, dev)
+    ps = _arg(out.scales, "scales", p.scale_dtype, p.scales, dev)
+    _expert_call("cq_norm_quant", dev, p.ref, px, pr, pw, psum, py, pc, ps)
+    return out
+
+
+def norm_grad(cfg: NormConfig, dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+              dsum: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+              dw: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+              ) -> tuple[torch.Tensor, torch.Tensor]:
+    """Gradients through the norm (cq_norm_grad): (dx [rows, hidden], dw f32
+    [hidden]) from dy, the norm's input x (norm_quant's sum) and, added to dx, the
+    gradient `dsum` of the sum's other uses. dx may be dy or dsum itself."""
+    p = _norm_plan_of(*vars(cfg).values())
+    if dy is None or x is None:
+        raise ValueError("dy and x are required")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    dev = x.device
+    px, pdy = _arg(x, "x", p.dtype, p.rows, dev), _arg(dy, "dy", p.dtype, p.rows, dev)
+    pw, pds = _arg(weight, "weight", p.dtype, p.row, dev), _arg(dsum, "dsum", p.dtype, p.rows, dev)
+    dx, pdx = _result(dx, "dx", p.dtype, p.rows, dev)
+    dw, pdw = _result(dw, "dw", torch.float32, p.row, dev)
+    ws, pws, nws = _workspace(workspace, p.workspace, dev)
+    _expert_call("cq_norm_grad", dev, p.ref, pdy, px, pw, pds, pdx, pdw, pws, nws)
+    return dx, dw
+
+
 def read_expert_status(device=None) -> int:
     """Synchronise the current stream of `device`, return and clear the expert
     products' status bits (CQ_ST_BAD_ROWS, CQ_ST_TIMEOUT) of that device."""
@@ -696,6 +966,11 @@ cq_expert_matmul = expert_matmul
 cq_expert_matmul_dx = expert_matmul_dx
 cq_expert_matmul_dw = expert_matmul_dw
 cq_expert_matmul_w4 = expert_matmul_w4
+cq_expert_matmul_b128 = expert_matmul_b128
+cq_expert_matmul_b128_dx = expert_matmul_b128_dx
+cq_moe_layer = moe_layer
+cq_norm_quant = norm_quant
+cq_norm_grad = norm_grad
 cq_read_expert_status = read_expert_status
 cq_read_status = read_status
 cq_read_combine_status = read_combine_status

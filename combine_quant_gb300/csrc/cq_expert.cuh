@@ -120,6 +120,21 @@ __device__ __forceinline__ float swiglu(float g, float u) {
   return u * a * (g * a * r);
 }
 
+// The gradient d of y = u * g * s, s = 1 / (1 + exp(-g)): dg = d u s (1 + g (1 - s)),
+// du = d g s, in 32 bits. With h = exp(-|g| / 2), which cannot overflow, and r =
+// 1 / (1 + h^2): s = r and 1 - s = h^2 r for g >= 0, else s = h^2 r and 1 - s = r. So
+// 1 - s is never a difference (from g = 2^24 on s rounds to 1), and for g < 0 each of
+// two factors meets one h before they meet each other: d u may leave 32 bits where
+// the result does not.
+__device__ __forceinline__ void swiglu_gradient(float d, float g, float u, float& dg, float& du) {
+  const float h = __expf(-0.5f * fabsf(g)), r = __fdividef(1.f, fmaf(h, h, 1.f));
+  const bool up = g >= 0.f;
+  const float a = up ? 1.f : h, b = up ? h : 1.f;
+  const float da = d * a, ga = g * a;
+  dg = da * (r * fmaf(g * b, b * r, 1.f)) * (u * a);
+  du = da * (ga * r);
+}
+
 // Reads and clears a translation unit's status word, waiting for the stream.
 template <typename Word>
 int read_status_word(Word& word, uint32_t* status, cudaStream_t s) {
@@ -141,6 +156,8 @@ int launch_gemm(Op op, const Args& a, cudaStream_t s);
 int launch_w4(const Args& a, cudaStream_t s);
 int gemm_status(uint32_t* status, cudaStream_t s);
 int w4_status(uint32_t* status, cudaStream_t s);
+int b128_status(uint32_t* status, cudaStream_t s);
+int layer_status(uint32_t* status, cudaStream_t s);
 
 }  // namespace expert
 }  // namespace cq

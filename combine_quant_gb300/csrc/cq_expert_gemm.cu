@@ -136,21 +136,6 @@ __device__ __forceinline__ Tile tile_at(const Shape& sh, const int* s_begin, con
   return x;
 }
 
-// The gradient d of y = u * g * s, s = 1 / (1 + exp(-g)): dg = d u s (1 + g (1 - s)),
-// du = d g s, in 32 bits. With h = exp(-|g| / 2), which cannot overflow, and r =
-// 1 / (1 + h^2): s = r and 1 - s = h^2 r for g >= 0, else s = h^2 r and 1 - s = r. So
-// 1 - s is never a difference (from g = 2^24 on s rounds to 1), and for g < 0 each of
-// two factors meets one h before they meet each other: d u may leave 32 bits where
-// the result does not.
-__device__ __forceinline__ void swiglu_gradient(float d, float g, float u, float& dg, float& du) {
-  const float h = __expf(-0.5f * fabsf(g)), r = __fdividef(1.f, fmaf(h, h, 1.f));
-  const bool up = g >= 0.f;
-  const float a = up ? 1.f : h, b = up ? h : 1.f;
-  const float da = d * a, ga = g * a;
-  dg = da * (r * fmaf(g * b, b * r, 1.f)) * (u * a);
-  du = da * (ga * r);
-}
-
 // Bytes of one results warp's staging buffer: 32 columns (j) of its 32 lanes
 // (i) in 16 bits, or 16 in 32 bits where another factor still comes (rows of 33
 // floats, so that neither the columns' stores nor the rows' loads meet in a bank).

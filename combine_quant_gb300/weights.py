@@ -2,7 +2,8 @@
 are loaded (torch operations on the weights' device; no part of a call).
 
 ``quantize_mx``: fp8 codes with one power-of-two scale per 32 of the last axis,
-for ``expert_matmul`` with mx types. ``quantize_w4``: 4-bit codes with group
+for ``expert_matmul`` with mx types. ``quantize_b128``: fp8 codes with one f32
+scale per block of 128 x 128, for ``expert_matmul_b128`` and ``moe_layer``. ``quantize_w4``: 4-bit codes with group
 scales, for ``expert_matmul_w4``.
 """
 from __future__ import annotations
@@ -29,6 +30,26 @@ def quantize_mx(w: torch.Tensor, e5m2: bool = False) -> tuple[torch.Tensor, torc
     scales = torch.zeros(*w.shape[:-1], (k // 32 + 1) // 2 * 2, dtype=torch.uint8, device=w.device)
     scales[..., : k // 32] = (e + 127).to(torch.uint8)
     return codes.reshape(w.shape), scales
+
+
+def quantize_b128(w: torch.Tensor, halves: int = 1, e5m2: bool = False) -> tuple[torch.Tensor, torch.Tensor]:
+    """Codes uint8 [..., n, k] and f32 scales [..., halves Ceil(n / halves, 128), Ceil(k, 128)], one
+    per block of 128 x 128 of each half (``halves`` 2: gates and ups): max|w| over the fp8 type's
+    largest value, 0 for a block of zeros; codes round w over the scale to nearest."""
+    n, k = w.shape[-2:]
+    if halves not in (1, 2) or n % halves != 0:
+        raise ValueError(f"halves must be 1, or 2 with an even number of rows, got {halves} and {n}")
+    dtype, largest = _FP8[bool(e5m2)]
+    n //= halves
+    nb, kb = -(-n // 128), -(-k // 128)
+    b = w.float().reshape(-1, n, k)
+    b = torch.nn.functional.pad(b, (0, kb * 128 - k, 0, nb * 128 - n)).view(-1, nb, 128, kb, 128)
+    m = b.abs().amax((2, 4))
+    # a smallest scale whose reciprocal is finite: smaller blocks round to zeros
+    s = torch.where(m > 0, (m / largest).clamp(min=2.0 ** -126), 0.0)
+    q = b / torch.where(s > 0, s, 1.0)[:, :, None, :, None]
+    codes = q.clamp(-largest, largest).to(dtype).view(torch.uint8).view(-1, nb * 128, kb * 128)[:, :n, :k]
+    return codes.reshape(w.shape).contiguous(), s.reshape(*w.shape[:-2], halves * nb, kb)
 
 
 def quantize_w4(w: torch.Tensor, group: int = 128, zeros: bool = False

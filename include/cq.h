@@ -436,14 +436,158 @@ int cq_expert_matmul_dw(const cq_expert_config* cfg, const void* dy, const void*
 int cq_expert_matmul_w4(const cq_expert_config* cfg, const void* x, const uint8_t* codes,
                         const void* scales, const uint8_t* zeros, const int64_t* group_rows,
                         void* y, void* stream);
+/*
+ * cq_expert_matmul_b128: cq_expert_matmul from fp8 rows with one f32 scale per
+ * 128 columns, as dispatch mode 3 writes them, and fp8 weights with one f32
+ * scale per block of 128 x 128:
+ *   p[i] = sum over blocks B of 128 of k: xs[r, B] ws[e, i / 128, B] * sum over j in B of x[r, j] w[e, i, j]
+ * The config's x_dtype is 2 (e4m3) or 3 (e5m2), w_dtype 0 or 1 likewise; k need
+ * only be a multiple of 16 (the last block may be short, as n's).
+ *   x          codes [R, k]
+ *   x_scales   f32 [R, KB], KB = Ceil(k, 128)
+ *   w          codes [G, n or 2n, k]
+ *   w_scales   f32 [G, NB or 2 NB, KB], NB = Ceil(n, 128); with act 1 the gates'
+ *              NB rows of blocks first, then the ups' (each half has blocks of its own)
+ *   y          [R, n] of out_dtype (bf16 or fp16), or where y_scales is given e4m3 codes
+ *   y_scales   NULL, or f32 [R, NB]: y's scales per 128 columns, by the rule of
+ *              dispatch mode 3 (codes round v * (448 / max|v|), the scale is the
+ *              reciprocal of that quotient), taken of the unrounded values
+ *   pre        NULL, or with act 1 [R, 2n] of out_dtype: receives p
+ * Products are summed in 32 bits within a block, and the scaled blocks in 32 bits.
+ */
+int cq_expert_matmul_b128(const cq_expert_config* cfg, const void* x, const float* x_scales,
+                          const void* w, const float* w_scales, const int64_t* group_rows, void* y,
+                          float* y_scales, void* pre, void* stream);
+
+/*
+ * cq_expert_matmul_b128_dx: the gradient of its input, d[r, :] = W[e]^T dy[r, :],
+ * from the same weights and scales and from dy in fp8:
+ *   dy         codes [R, n or 2n] (x_dtype 2 or 3)
+ *   dy_scales  f32 [R, NB or 2 NB], one per 128 columns; with act 1 of each half
+ *              by itself (cq_norm_quant on 2 R rows of n columns writes them so)
+ *   pre, dx    as for cq_expert_matmul_dx, of out_dtype (bf16 or fp16)
+ * The gradient of the weights is cq_expert_matmul_dw on 16-bit rows: scales along
+ * the rows' own axis cannot be taken out of a sum over rows.
+ */
+int cq_expert_matmul_b128_dx(const cq_expert_config* cfg, const void* dy, const float* dy_scales,
+                             const void* w, const float* w_scales, const int64_t* group_rows,
+                             const void* pre, void* dx, void* stream);
+
+/* Validate an expert config for the two calls above; as cq_check_expert_config. */
+int cq_check_expert_b128_config(const cq_expert_config* cfg);
+
 /* Pointers of the expert products (else CQ_ERR_ARG): 16-byte aligned, group_rows
- * 8-byte. x, y, dy, pre and dx may be NULL when rows is 0. A call's results must
- * not overlap its inputs. */
+ * 8-byte, f32 scales of the b128 products 4-byte. x, y, dy, pre and dx (and the
+ * scales of rows) may be NULL when rows is 0. A call's results must not overlap
+ * its inputs. */
+
+/*
+ * cq_moe_layer -- the whole layer for a few tokens (decoding), in two kernels:
+ * no dispatch, no rows in between.
+ *   y[t] = sum over j < K of w[t, j] * W2[e] SwiGLU(W13[e] x[t]),  e = ids[t, j]
+ * What it reads is the weights of the experts that the tokens name, each once
+ * for up to 32 tokens (their second 32 from L2). Expert ids count from 0 to
+ * experts - 1; a shared expert is one more column of ids with weight 1. The same
+ * id twice in a token counts twice.
+ */
+typedef struct cq_moe_config {
+  int32_t tokens;    /* T in [0, 64] */
+  int32_t experts;   /* G in [1, 2048] */
+  int32_t topk;      /* K in [1, 16] */
+  int32_t hidden;    /* H in [16, 65536], H % 16 == 0 */
+  int32_t inter;     /* I in [16, 65536], I % 16 == 0 */
+  int32_t x_dtype;   /* 0 bf16, 1 fp16: x, 16-bit weights */
+  int32_t w_dtype;   /* weights: 0 the type of x, 1 fp8 e4m3 with a scale per 128 x 128 */
+  int32_t mask_ndim; /* 0 none, 1 per token [T], 2 per pair [T, K] */
+  int32_t out_dtype; /* y: 0 the type of x, 1 f32 */
+} cq_moe_config;
+
+/* Validate; CQ_OK, CQ_ERR_ARG or CQ_ERR_UNSUPPORTED (H or I not a multiple of 16). */
+int cq_check_moe_config(const cq_moe_config* cfg);
+size_t cq_moe_workspace_size(const cq_moe_config* cfg); /* bytes; 0 for an invalid config */
+
+/*   x             [T, H]
+ *   expert_ids    int32 [T, K]; an active id outside [0, experts) is skipped and
+ *                 sets CQ_ST_BAD_ID (cq_read_expert_status)
+ *   expert_scales f32 [T, K] routing weights
+ *   x_active_mask uint8 [T] or [T, K], required with mask_ndim 1 or 2, else NULL;
+ *                 a token without an active pair gives 0
+ *   w13           [G, 2I, H], gate rows first; w2 [G, H, I]
+ *   w13_scales    f32 [G, 2 Ceil(I, 128), Ceil(H, 128)], w2_scales f32 [G, Ceil(H, 128),
+ *                 Ceil(I, 128)] with w_dtype 1 (blocks as in cq_expert_matmul_b128), else NULL
+ *   y             [T, H]
+ *   workspace     >= cq_moe_workspace_size() bytes, 256-byte aligned; needs no
+ *                 initialisation and keeps nothing between calls, but calls that
+ *                 may overlap on the GPU need one each
+ * Alignment: x, weights and y 16 bytes, the others by their type. Results must not
+ * overlap inputs. Products are summed in 32 bits, SwiGLU and the weighted sum taken
+ * of unrounded products. Between the two products SwiGLU's result is held as the
+ * sum of two numbers of x's type (16 bits or more of precision), so with fp16
+ * it is infinite above 65504.
+ */
+int cq_moe_layer(const cq_moe_config* cfg, const void* x, const int32_t* expert_ids,
+                 const float* expert_scales, const uint8_t* x_active_mask, const void* w13,
+                 const float* w13_scales, const void* w2, const float* w2_scales, void* y,
+                 void* workspace, size_t workspace_bytes, void* stream);
 
 /* The expert products take no workspace; their status word (CQ_ST_BAD_ROWS,
- * CQ_ST_TIMEOUT) is one word per device. Synchronise `stream`, copy the word of
+ * CQ_ST_TIMEOUT; of cq_moe_layer CQ_ST_BAD_ID) is one word per device. Synchronise `stream`, copy the word of
  * the current device into *status and clear it. */
 int cq_read_expert_status(uint32_t* status, void* stream);
+
+/*
+ * cq_norm_quant -- what comes before the layer: the residual's addition, the
+ * root-mean-square norm, and the rows quantised as dispatch quantises them, so
+ * that cq_expert_matmul_b128 and cq_expert_matmul (mx) can take them without a
+ * dispatch (a shared expert, experts = 1). Without the norm it quantises any
+ * rows: SwiGLU's results, the gradients for cq_expert_matmul_b128_dx.
+ *   s = x + residual;   v = s * weight / sqrt(mean(s^2) + eps)   (norm 0: v = s)
+ */
+typedef struct cq_norm_config {
+  int32_t rows;       /* R >= 0 */
+  int32_t hidden;     /* H in [16, 8192], H % 16 == 0 (H % 32 == 0 for quant_mode 4 and 5) */
+  int32_t x_dtype;    /* 0 bf16, 1 fp16: x, residual, weight, sum, y and their gradients */
+  int32_t norm;       /* 1 root-mean-square norm, 0 none */
+  int32_t quant_mode; /* 0 no codes; 2, 3, 4, 5 as in cq_config (no smooth scales) */
+  int32_t y_dtype;    /* fp8 codes of modes 3-5: 0 e4m3fn, 1 e5m2; 0 otherwise */
+  float eps;          /* >= 0 */
+} cq_norm_config;
+
+/* Validate; CQ_OK, CQ_ERR_ARG or CQ_ERR_UNSUPPORTED (H not a multiple of 16 or 32). */
+int cq_check_norm_config(const cq_norm_config* cfg);
+
+/*   x         [R, H]
+ *   residual  [R, H] or NULL
+ *   weight    [H]; NULL: ones. Must be NULL with norm 0.
+ *   sum       NULL, or [R, H]: receives s rounded; may be x or residual itself
+ *   y         NULL (with quant_mode != 0), or [R, H]: receives v rounded
+ *   codes     [R, H] int8 (mode 2) or fp8; NULL with quant_mode 0
+ *   scales    f32 [R] (mode 2), f32 [R, Ceil(H, 128)] (mode 3), uint8 [R, Align2(H / 32)]
+ *             (4, 5; pad column 0); NULL with quant_mode 0
+ * Sums are f32 and v is not rounded before it is quantised. Pointers 16-byte
+ * aligned, f32 scales 4-byte, mx scales 1. Results other than sum must not
+ * overlap inputs.
+ */
+int cq_norm_quant(const cq_norm_config* cfg, const void* x, const void* residual,
+                  const void* weight, void* sum, void* y, void* codes, void* scales, void* stream);
+
+/*
+ * cq_norm_grad: gradients of v = x weight r, r = 1 / sqrt(mean(x^2) + eps), where x
+ * is the norm's input (the saved sum). Quantisation passes its gradient on.
+ *   dy      [R, H]
+ *   dsum    NULL, or [R, H]: gradient of the sum's other uses, added to dx
+ *   dx      [R, H]: r (dy weight - x r^2 mean(dy weight x)) + dsum (also the residual's
+ *           gradient); may be dy or dsum itself
+ *   dw      NULL, or f32 [H]: sum over rows of dy x r. A fixed order of addition.
+ *   workspace  with dw: >= cq_norm_workspace_size() bytes, 256-byte aligned; needs
+ *              no initialisation; calls that may overlap on the GPU need one each
+ * norm 1; quant_mode and y_dtype are ignored. weight NULL: ones. Pointers 16-byte
+ * aligned, dw 4-byte.
+ */
+size_t cq_norm_workspace_size(const cq_norm_config* cfg);
+int cq_norm_grad(const cq_norm_config* cfg, const void* dy, const void* x, const void* weight,
+                 const void* dsum, void* dx, float* dw, void* workspace, size_t workspace_bytes,
+                 void* stream);
 
 /* Static description of an error code. */
 const char* cq_strerror(int code);
