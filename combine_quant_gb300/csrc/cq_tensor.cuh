@@ -46,6 +46,13 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Shared-memory address in the pair's CTA `rank` for one of this CTA.
+__device__ __forceinline__ uint32_t addr_in(uint32_t a, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+
 // Shared-memory address of the pair's CTA 0 (the leader) for one of this CTA.
 __device__ __forceinline__ uint32_t leader_addr(uint32_t a) {
   uint32_t r;
@@ -166,7 +173,17 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
       : "memory");
 }
 
-// The same with fp8 operands and a power-of-two scale for each row of A and B
+// The same with fp8 operands, 32 of the contraction.
+__device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        bool add) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+
+// With fp8 operands and a power-of-two scale for each row of A and B
 // and 32 of the contraction; the scales' TMEM addresses are sa and sb.
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t sa, uint32_t sb, bool add) {
@@ -260,6 +277,13 @@ __device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t addr) {
 __device__ __forceinline__ uint32_t idesc_f16(bool bf16, bool a_mn, bool b_mn, int m, int n) {
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// Instruction descriptor of kind::f8f6f4: f32 accumulators, formats 0 e4m3, 1 e5m2,
+// A optionally MN-major, M x N.
+__device__ __forceinline__ uint32_t idesc_fp8(int a_fmt, int b_fmt, bool a_mn, int m, int n) {
+  return (1u << 4) | ((uint32_t)a_fmt << 7) | ((uint32_t)b_fmt << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // Descriptor of 32 unswizzled lines of 16 bytes, for copy_scales.
