@@ -3,23 +3,23 @@
 // forward (SwiGLU, results in 16 bits or in fp8 with scales) and the gradient of
 // the input.
 //
-// A persistent kernel on pairs of CTAs, as cq_expert_gemm.cu's: a tile is 256
-// weight rows (the accumulator's lanes, 128 in each CTA) by up to 256 tokens (its
-// columns, in steps of 16), copies by warp 0, products by warp 1 of the first CTA.
-// What differs is that a scale holds for 128 of the contraction only:
+// A persistent kernel on pairs of CTAs, as cq_expert_gemm.cu's, with copies by warp 0
+// and products by warp 1 of the first CTA. What differs is that a scale holds for 128
+// of the contraction only:
 //
-//   acc[i, j] += (xs[j, B] ws[B]) * sum over k in B of w[i, k] x[j, k]
+//   acc[j, i] += (xs[j, B] ws[B]) * sum over k in B of x[j, k] w[i, k]
 //
-// So every stage (128 of the contraction, four products) goes into a TMEM
-// accumulator of its own, two in turn, and eight warps take it from there into
-// registers, scaled: 128 sums a thread, all of a tile. The scales of the columns are
-// the vector: with lane r / 4 + 8 h of the accumulator and columns 8 n + 2 c + b a
-// thread (16x256b loads) needs 32 scales for 128 sums, not 128 as it would with a
-// lane each; pairs of columns multiply in packed f32x2 instructions. Warps 2 and 3
-// fetch the scales, four blocks at a time; where a CTA's weight rows have one block
-// scale it is multiplied in there, with SwiGLU (gate and up rows) by the reader.
+// So every stage (128 of the contraction, four products) goes into a TMEM accumulator
+// of its own, two in turn, and eight warps take it from there into registers, scaled:
+// 128 sums a thread, all of a tile. That is what bounds it, and why tokens lie on the
+// accumulator's lanes here (up to 128 in each CTA) and weight rows on its columns: a
+// lane's factor is one number per 128 columns. With tokens on the columns the factors
+// are a vector to be read for every block (measured: 813 us where this takes XX, at 512
+// rows an expert), though a ragged expert then wastes no lanes.
 //
-// dx: A = w with its columns on the lanes (MN-major), the contraction runs over n.
+// SwiGLU: the columns are 16 gates, 16 ups, 16 gates, ... (one 5-D copy). fp8 results:
+// a group of 128 outputs is a thread's own columns, with SwiGLU those of two threads.
+// dx: B = w with its columns along N (MN-major), the contraction runs over n.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -49,69 +49,71 @@ struct B128Args : Args {
   int32_t blocks;       // of the contraction
   int32_t half_blocks;  // dx: of one half of it; forward: all
   int32_t half_len;     // the contraction's length, dx: of one half
+  int32_t out_cols;     // columns of the result: n, or (dx) k
+  int32_t tiles_i;
   int32_t vec;          // rows of xs are whole 16-byte pieces
-  int32_t I, tiles_i;   // rows of A: weight rows, or (dx) columns of w
+  int32_t wide;         // rows of the results (and of saved products) are whole 32-byte pieces
 };
 
-constexpr int kNT = 256;                   // most columns of a tile
-constexpr int kStages = 5;
-constexpr int kABytes = 128 * 128;         // A of one stage, one CTA
-constexpr int kStageBytes = 2 * kABytes;   // B: half of up to 256 columns
+constexpr int kStages = 6;
+constexpr int kABytes = 128 * 128;         // A (tokens) of one stage, one CTA
+constexpr int kStageBytes = 2 * kABytes;   // B: half of up to 256 weight rows
+constexpr int kNT = 256;                   // TMEM columns of an accumulator
 constexpr int kDrainWarps = 8;             // two for each quarter of the lanes
 constexpr int kThreads = 128 + 32 * kDrainWarps;
 // Registers: 384 threads are launched with 168 each (64512); the drain warps keep 128
 // sums and need 224, the others 56, which is the same total.
 constexpr int kOtherRegs = 56, kDrainRegs = 224;
 static_assert(128 * kOtherRegs + 32 * kDrainWarps * kDrainRegs <= 168 * kThreads, "setmaxnreg would wait forever");
-constexpr int kEntry = 4;                  // blocks in an entry of the scales' ring
-constexpr int kScaleRing = 3;
-constexpr int kScaleFloats = kEntry * kNT + 2 * kEntry;  // columns', then gates' and ups'
-constexpr int kStaging = 16 * 33 * 4;      // bytes of a drain warp's staging buffer
 constexpr uint32_t kTmemCols = 512;
 constexpr int kBand = 8;                   // tiles along i taken together, for reuse in L2
 
-struct FewMaps {
-  CUtensorMap b64, b32;
+struct RowMaps {
+  CUtensorMap b128, b64, b32;
 };
 
 struct Bars {
   uint64_t full[kStages], empty[kStages];
-  uint64_t sfull[kScaleRing], sempty[kScaleRing];
   uint64_t tfull[2], tempty[2];
-  uint64_t top[2];  // fp8 results: the columns' largest values of a half of the warps
+  uint64_t top[4];  // fp8 results: the largest values of a quarter's two warps
   uint64_t done;    // the products in flight when their warp gave up
   uint32_t tmem;
 };
 
 struct Tile {
-  int e, begin, i0, j0, jn;
+  int e, row0, rows;  // first token row and rows of the tile
+  int i0, cols;       // first output and accumulator columns (of B, both CTAs)
 };
 
+// GATES: a tile is 128 outputs, else 256. Columns in steps of 64 (16 outputs a CTA) or 32.
+template <bool GATES>
 __device__ __forceinline__ Tile tile_at(const B128Args& a, const int* s_begin, const int* s_tile, int t) {
   Tile x;
   x.e = expert_of(s_tile, a.G, t);
   const int l = t - s_tile[x.e];
-  x.begin = s_begin[x.e];
-  const int rows = s_begin[x.e + 1] - x.begin;
-  const int parts = (rows + kNT - 1) / kNT;
+  const int begin = s_begin[x.e], rows = s_begin[x.e + 1] - begin;
+  const int parts = (rows + 255) / 256;
   const int band = l / (kBand * parts), first_i = band * kBand;
   const int wide = min(kBand, a.tiles_i - first_i), m = l - first_i * parts;
   const int ti = first_i + m % wide, tj = m / wide;
-  x.i0 = ti * 256;
-  const int step = ((rows + parts - 1) / parts + 15) / 16 * 16;  // equal parts, in whole steps
-  x.j0 = tj * step;
-  x.jn = min(step, rows - x.j0);
+  const int step = (rows + parts - 1) / parts;  // equal parts
+  x.row0 = begin + tj * step;
+  x.rows = min(step, rows - tj * step);
+  constexpr int kOuts = GATES ? 128 : 256;
+  x.i0 = ti * kOuts;
+  const int outs = (min(kOuts, a.out_cols - x.i0) + 31) / 32 * 32;
+  x.cols = GATES ? 2 * outs : outs;
   return x;
 }
-
-// Columns of B that a CTA loads for a tile: its half.
-__device__ __forceinline__ int half_cols(const Tile& x) { return (x.jn + 15) / 16 * 8; }
 
 using Pair = unsigned long long;  // two floats
 __device__ __forceinline__ Pair pair_of(uint32_t lo, uint32_t hi) {
   Pair p;
   asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(lo), "r"(hi));
   return p;
+}
+__device__ __forceinline__ Pair pair_of(float lo, float hi) {
+  return pair_of(__float_as_uint(lo), __float_as_uint(hi));
 }
 __device__ __forceinline__ float lo_of(Pair p) { return __uint_as_float((uint32_t)p); }
 __device__ __forceinline__ float hi_of(Pair p) { return __uint_as_float((uint32_t)(p >> 32)); }
@@ -120,250 +122,90 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-  Pair d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ void ld_pairs(uint32_t addr, Pair& a, Pair& b) {
-  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
-}
 
-// Where column j's scale lies among its 32: a thread's 8 (c = j / 2 % 4) side by side.
-__device__ __forceinline__ int scale_place(int j) {
-  return (j & ~31) | ((j >> 1 & 3) << 3) | ((j >> 3 & 3) << 1) | (j & 1);
-}
-
-// 32 columns of a warp's 32 lanes, as pairs of columns: v[2 n + h] lanes 0-15, v[8 + 2 n + h]
-// lanes 16-31; row lane / 4 + 8 h, columns 8 n + 2 (lane % 4), + 1.
-struct Block {
-  uint32_t lo[16], hi[16];
-};
-__device__ __forceinline__ void load_block(uint32_t src, Block& v) {
-  tmem_ld16(src, v.lo);
-  tmem_ld16(src + (16u << 16), v.hi);
-}
-
-template <bool ACT>
-__device__ __forceinline__ void add_block(const Block& v, uint32_t scales, Pair wg, Pair wu, Pair (&acc)[16]) {
-  Pair s[4];
-  ld_pairs(scales, s[0], s[1]);
-  ld_pairs(scales + 16, s[2], s[3]);
+// acc += 32 columns, the first 16 times sg, the others times su.
+__device__ __forceinline__ void add_scaled(const uint32_t (&v)[32], Pair sg, Pair su, Pair (&acc)[16]) {
 #pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    const Pair sg = ACT ? mul2(s[n], wg) : s[n], su = ACT ? mul2(s[n], wu) : s[n];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = 4 * n + 2 * h;
-      acc[2 * n + h] = fma2(pair_of(v.lo[k], v.lo[k + 1]), sg, acc[2 * n + h]);
-      acc[8 + 2 * n + h] = fma2(pair_of(v.hi[k], v.hi[k + 1]), su, acc[8 + 2 * n + h]);
-    }
+  for (int k = 0; k < 16; ++k) acc[k] = fma2(pair_of(v[2 * k], v[2 * k + 1]), k < 8 ? sg : su, acc[k]);
+}
+
+// 32 bytes to or from global memory: one access, or two where a row need not begin
+// on 32 bytes.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+__device__ __forceinline__ void load32(const void* p, uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = __ldg(static_cast<const uint4*>(p)), b = __ldg(static_cast<const uint4*>(p) + 1);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
   }
 }
 
-// ---- results of 32 columns from c0, out of registers ----
-
-// 16-bit results: turned in shared memory (16-byte pieces, XORed with bits of the
-// row number), out in 16-byte stores. act: gates and ups of 16 outputs.
+// 16 values (8 pairs) rounded to 16 bits.
 template <typename T>
-__device__ __forceinline__ void store_rows(const Pair (&v)[16], uint16_t* out, size_t ld, int i, bool in,
-                                           int jn, uint8_t* stage) {
-  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-  const uint32_t st = smem_u32(stage);
-  auto pack = [&](int k) { return T::pack2(lo_of(v[k]), hi_of(v[k])); };
+__device__ __forceinline__ void store16(uint16_t* p, const Pair* v, bool wide) {
+  uint32_t w[8];
 #pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    const int j = 8 * n + (lane & 7);
-    st_matrix_t(st + j * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4), pack(2 * n), pack(2 * n + 1),
-                pack(8 + 2 * n), pack(8 + 2 * n + 1));
-  }
-  __syncwarp();
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const int j = 8 * p + r;
-    const uint4 w = async::ld_shared_v4(stage + j * 64 + ((c ^ ((j >> 1) & 3)) << 4));
-    if (in && j < jn) *reinterpret_cast<uint4*>(out + (size_t)j * ld + i) = w;
-  }
-  __syncwarp();
+  for (int k = 0; k < 8; ++k) w[k] = T::pack2(lo_of(v[k]), hi_of(v[k]));
+  store32(p, w, wide);
 }
 
-// The same for 16 outputs (SwiGLU): rows of 32 bytes.
-template <typename T>
-__device__ __forceinline__ void store_half_rows(const Pair (&y)[8], uint16_t* out, size_t ld, int i, bool in,
-                                                int jn, uint8_t* stage) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t st = smem_u32(stage);
-  auto pack = [&](int k) { return T::pack2(lo_of(y[k]), hi_of(y[k])); };
+__device__ __forceinline__ float top_of(const Pair* v, float top) {  // 8 pairs
 #pragma unroll
-  for (int n = 0; n < 4; n += 2) {
-    const int j = 8 * (n + (lane >> 4)) + (lane & 7);
-    st_matrix_t(st + j * 32 + ((((lane >> 3) & 1) ^ ((j >> 2) & 1)) << 4), pack(2 * n), pack(2 * n + 1),
-                pack(2 * n + 2), pack(2 * n + 3));
-  }
-  __syncwarp();
-  const int r2 = lane >> 1, c2 = lane & 1;
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const int j = 16 * p + r2;
-    const uint4 w = async::ld_shared_v4(stage + j * 32 + ((c2 ^ ((j >> 2) & 1)) << 4));
-    if (in && j < jn) *reinterpret_cast<uint4*>(out + (size_t)j * ld + i + 8 * c2) = w;
-  }
-  __syncwarp();
+  for (int k = 0; k < 8; ++k) top = fmaxf(top, fmaxf(fabsf(lo_of(v[k])), fabsf(hi_of(v[k]))));
+  return top;
 }
 
-// The largest |v| of each of 32 columns over a warp's lanes: lane 4 (2 n + b) + c gets
-// column 8 n + 2 c + b. Each step halves the columns that a lane looks after.
-template <int N>
-__device__ __forceinline__ float column_tops(const Pair (&v)[N]) {
-  const int lane = threadIdx.x & 31;
-  float t[8];  // 2 n + b
+// 16 values times mult in e4m3.
+__device__ __forceinline__ uint4 codes16(const Pair* v, float mult) {
+  uint32_t w[4];
 #pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    float a = fmaxf(fabsf(lo_of(v[2 * n])), fabsf(lo_of(v[2 * n + 1])));
-    float b = fmaxf(fabsf(hi_of(v[2 * n])), fabsf(hi_of(v[2 * n + 1])));
-    if constexpr (N == 16) {
-      a = fmaxf(a, fmaxf(fabsf(lo_of(v[8 + 2 * n])), fabsf(lo_of(v[8 + 2 * n + 1]))));
-      b = fmaxf(b, fmaxf(fabsf(hi_of(v[8 + 2 * n])), fabsf(hi_of(v[8 + 2 * n + 1]))));
-    }
-    t[2 * n] = a;
-    t[2 * n + 1] = b;
+  for (int k = 0; k < 4; ++k) {
+    auto two = [&](Pair p) { return permute_detail::e4m3x2(__fmul_rn(lo_of(p), mult), __fmul_rn(hi_of(p), mult)); };
+    w[k] = two(v[2 * k]) | (two(v[2 * k + 1]) << 16);
   }
-#pragma unroll
-  for (int o = 4; o; o >>= 1) {  // lane bits 4, 3, 2
-    const bool up = lane & (4 * o);
-#pragma unroll
-    for (int k = 0; k < o; ++k) {
-      const float keep = up ? t[k + o] : t[k], give = up ? t[k] : t[k + o];
-      t[k] = fmaxf(keep, __shfl_xor_sync(~0u, give, 4 * o));
-    }
-  }
-  return t[0];
-}
-
-// fp8 results: codes of v times the column's `mult` (the lane of column_tops has it),
-// 16 or 32 outputs; bytes into rows of 48, out in 16-byte stores.
-template <int N>
-__device__ __forceinline__ void store_codes(const Pair (&v)[N], float mult, uint8_t* out, size_t ld, int i,
-                                            int left, int jn, uint8_t* stage) {
-  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-#pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    const float m0 = __shfl_sync(~0u, mult, 8 * n + c), m1 = __shfl_sync(~0u, mult, 8 * n + 4 + c);
-    uint8_t* to = stage + (8 * n + 2 * c) * 48 + r;
-#pragma unroll
-    for (int p = 0; p < N / 8; ++p)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const Pair w = v[8 * p + 2 * n + h];
-        const uint32_t q = permute_detail::e4m3x2(__fmul_rn(lo_of(w), m0), __fmul_rn(hi_of(w), m1));
-        to[16 * p + 8 * h] = (uint8_t)q;
-        to[16 * p + 8 * h + 48] = (uint8_t)(q >> 8);
-      }
-  }
-  __syncwarp();
-  if (lane < jn) {
-#pragma unroll
-    for (int p = 0; p < N / 8; ++p)
-      if (16 * p < left)
-        *reinterpret_cast<uint4*>(out + (size_t)lane * ld + i + 16 * p) =
-            async::ld_shared_v4(stage + lane * 48 + 16 * p);
-  }
-  __syncwarp();
-}
-
-// dx through SwiGLU: a lane's 8 gates and ups of 4 of 32 columns, read ahead.
-struct Saved {
-  uint4 g[4], u[4];
-};
-__device__ __forceinline__ void load_saved(const B128Args& a, const Tile& x, int i_warp, int c0, Saved& v) {
-  const int lane = threadIdx.x & 31, r = lane >> 2, i = i_warp + 8 * (lane & 3);
-  const size_t ld = 2 * (size_t)a.I;
-  const uint16_t* pre =
-      static_cast<const uint16_t*>(a.pre_in) + ((size_t)(x.begin + x.j0) + c0 + r) * ld + i;
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const bool ok = i < a.I && c0 + 8 * p + r < x.jn;
-    v.g[p] = ok ? __ldg(reinterpret_cast<const uint4*>(pre + 8 * p * ld)) : make_uint4(0, 0, 0, 0);
-    v.u[p] = ok ? __ldg(reinterpret_cast<const uint4*>(pre + 8 * p * ld + a.I)) : make_uint4(0, 0, 0, 0);
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void store_gradients(const B128Args& a, const Pair (&v)[16], const Saved& s,
-                                                uint16_t* out, int i_warp, int jn, uint8_t* stage) {
-  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3, i = i_warp + 8 * c;
-  const size_t ld = 2 * (size_t)a.I;
-  float* buf = reinterpret_cast<float*>(stage);  // 16 columns, rows of 33 floats
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {  // rows r + 8 k
-        const Pair w = v[8 * (k >> 1) + 2 * (2 * half + n) + (k & 1)];
-        float* to = buf + (8 * n + 2 * c) * 33 + 8 * k + r;
-        to[0] = lo_of(w);
-        to[33] = hi_of(w);
-      }
-    __syncwarp();
-#pragma unroll
-    for (int p = 2 * half; p < 2 * half + 2; ++p) {
-      const float* d = buf + (8 * (p - 2 * half) + r) * 33 + 8 * c;
-      const uint32_t gw[4] = {s.g[p].x, s.g[p].y, s.g[p].z, s.g[p].w};
-      const uint32_t uw[4] = {s.u[p].x, s.u[p].y, s.u[p].z, s.u[p].w};
-      uint32_t dg[4], du[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float dg0, du0, dg1, du1;
-        swiglu_gradient(d[2 * k], T::lo(gw[k]), T::lo(uw[k]), dg0, du0);
-        swiglu_gradient(d[2 * k + 1], T::hi(gw[k]), T::hi(uw[k]), dg1, du1);
-        dg[k] = T::pack2(dg0, dg1);
-        du[k] = T::pack2(du0, du1);
-      }
-      if (i < a.I && 8 * p + r < jn) {
-        uint16_t* to = out + (size_t)(8 * p + r) * ld + i;
-        *reinterpret_cast<uint4*>(to) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
-        *reinterpret_cast<uint4*>(to + a.I) = make_uint4(du[0], du[1], du[2], du[3]);
-      }
-    }
-    __syncwarp();
-  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // DX: the input's gradient. ACT: forward with SwiGLU, or the gradient through it.
 // OUT8: results in fp8 with scales.
 template <bool DX, typename T, bool ACT, bool OUT8>
 __global__ void __launch_bounds__(kThreads, 1)
-b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensorMap map_a,
-            const __grid_constant__ CUtensorMap map_b, const __grid_constant__ FewMaps few) {
-  constexpr bool kGates = ACT && !DX;  // two block scales a CTA
+b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensorMap map_w,
+            const __grid_constant__ RowMaps rows_map) {
+  constexpr bool kGates = ACT && !DX;
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Bars bars;
+  __shared__ float s_top[OUT8 && kGates ? 2 * 2 * 128 : 1];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
-  uint8_t* staging = ring + kStages * kStageBytes;
-  float* s_scales = reinterpret_cast<float*>(staging + kDrainWarps * kStaging);
-  float* s_top = s_scales + kScaleRing * kScaleFloats;  // OUT8: [2][8][256]
-  int* s_begin = reinterpret_cast<int*>(s_top + (OUT8 ? 2 * 8 * kNT : 0));
+  int* s_begin = reinterpret_cast<int*>(ring + kStages * kStageBytes);
   int* s_tile = s_begin + a.G + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   if (threadIdx.x == 0) {
-    prefetch_map(&map_a);
-    prefetch_map(&map_b);
+    prefetch_map(&map_w);
+    prefetch_map(&rows_map.b128);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars.full[s], 1);
       mbar_init(&bars.empty[s], 1);
     }
-    for (int s = 0; s < kScaleRing; ++s) {
-      mbar_init(&bars.sfull[s], 2);
-      mbar_init(&bars.sempty[s], kDrainWarps);
-    }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars.tfull[b], 1);
       mbar_init(&bars.tempty[b], kDrainWarps * 2);
-      mbar_init(&bars.top[b], kGates ? 8 : 4);
     }
+    for (int q = 0; q < 4; ++q) mbar_init(&bars.top[q], 2);
     mbar_init(&bars.done, 1);
     async::mbar_fence_init();
   }
@@ -372,7 +214,7 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
   // own wait, and they may be these results.
   griddep_wait();
   const bool bad = group_scan<kThreads>(
-      a, s_begin, s_tile, [&](int rows) { return a.tiles_i * ((rows + kNT - 1) / kNT); });
+      a, s_begin, s_tile, [&](int rows) { return a.tiles_i * ((rows + 255) / 256); });
   if (bad && blockIdx.x == 0) atomicOr(&g_status, (uint32_t)CQ_ST_BAD_ROWS);
   fence_before();
   cluster_sync();
@@ -396,11 +238,12 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
       uint32_t s = 0, lap = 0;  // stage, times the ring has gone round
       bool ok = true;
       for (int t = first; t < n_tiles && ok; t += step) {
-        const Tile x = tile_at(a, s_begin, s_tile, t);
-        const int i_cta = x.i0 + (int)rank * 128;
-        const int jh = half_cols(x), jb = x.j0 + (int)rank * jh;
+        const Tile x = tile_at<kGates>(a, s_begin, s_tile, t);
+        // tokens: each CTA its half, in copies of 128 rows, 64, 32, or 64 + 32
+        const int jh = (x.rows + 1) / 2, row = x.row0 + (int)rank * jh;
         const bool b128 = jh > 96, b64 = !b128 && jh > 32, b32 = !b128 && (jh <= 32 || jh > 64);
         const uint32_t bytes = kABytes + (b128 ? 16384 : (b64 ? 8192 : 0) + (b32 ? 4096 : 0));
+        const int i = x.i0 + (int)rank * x.cols / (kGates ? 4 : 2);  // this CTA's half of the columns
         int half = 0, k0 = 0;
         for (int kb = 0; kb < a.blocks; ++kb) {
           if (lap > 0 && !(ok = wait(&bars.empty[s], (lap & 1) ^ 1))) break;
@@ -408,12 +251,12 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
             const uint32_t sa = smem_u32(ring + s * kStageBytes), sb = sa + kABytes;
             const uint32_t bar = lead(&bars.full[s]);
             if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], bytes * 2);
-            if constexpr (kGates) tma_load5(sa, &map_a, k0, 0, 0, i_cta / 32, x.e, bar);
-            else if constexpr (DX) tma_load4<2>(sa, &map_a, i_cta, k0, half, x.e, bar);
-            else tma_load3<2>(sa, &map_a, k0, i_cta, x.e, bar);
-            if (b128) tma_load3<2>(sb, &map_b, k0, half, x.begin + jb, bar);
-            if (b64) tma_load3<2>(sb, &few.b64, k0, half, x.begin + jb, bar);
-            if (b32) tma_load3<2>(sb + (b64 ? 8192 : 0), &few.b32, k0, half, x.begin + jb + (b64 ? 64 : 0), bar);
+            if constexpr (kGates) tma_load5(sb, &map_w, k0, 0, 0, i / 16, x.e, bar);
+            else if constexpr (DX) tma_load4<2>(sb, &map_w, i, k0, half, x.e, bar);
+            else tma_load3<2>(sb, &map_w, k0, i, x.e, bar);
+            if (b128) tma_load3<2>(sa, &rows_map.b128, k0, half, row, bar);
+            if (b64) tma_load3<2>(sa, &rows_map.b64, k0, half, row, bar);
+            if (b32) tma_load3<2>(sa + (b64 ? 8192 : 0), &rows_map.b32, k0, half, row + (b64 ? 64 : 0), bar);
           }
           __syncwarp();
           k0 += 128;
@@ -432,14 +275,14 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
       }
     } else if (warp == 1 && rank == 0) {
       // ---- products ----
-      constexpr uint32_t ka = (DX ? 4096 : 32) >> 4, kbs = 32 >> 4;
+      constexpr uint32_t ka = 32 >> 4, kbs = (DX ? 4096 : 32) >> 4;
       const uint64_t da = desc_at(desc_base(16), smem_u32(ring));
       const uint64_t db = desc_at(desc_base(16), smem_u32(ring) + kABytes);
       uint32_t s = 0, lap = 0, buf = 0;
       bool ok = true;
       for (int t = first; t < n_tiles && ok; t += step) {
-        const Tile x = tile_at(a, s_begin, s_tile, t);
-        const uint32_t idesc = idesc_fp8(a.w_dtype, a.x_dtype == kMxE5M2, DX, 256, half_cols(x) * 2);
+        const Tile x = tile_at<kGates>(a, s_begin, s_tile, t);
+        const uint32_t idesc = idesc_fp8(a.x_dtype == kMxE5M2, a.w_dtype, DX, 256, x.cols);
         int left = a.half_len;
         for (int kb = 0; kb < a.blocks; ++kb) {
           const uint32_t b = buf & 1, use = buf >> 1;
@@ -472,203 +315,195 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
         __syncwarp();
         wait_pair(&bars.done, 0);
       }
-    } else if (warp >= 2) {
-      // ---- scales: a lane has every 64th column, four blocks at a time ----
-      const int l64 = (warp - 2) * 32 + lane;
-      const int entries = (a.blocks + kEntry - 1) / kEntry;
-      int t_load = first, q_load = 0;
-      Tile x = {};
-      auto load = [&](float (&v)[4][4], float (&w)[4], float& w2) {
-        if (t_load >= n_tiles) return;
-        if (q_load == 0) x = tile_at(a, s_begin, s_tile, t_load);
-        const int b0 = q_load * kEntry, nb = min(kEntry, a.blocks - b0);
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const int j = l64 + 64 * m;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[m][k] = 0.f;
-          if (j >= x.jn) continue;
-          const float* p = a.xs + (size_t)(x.begin + x.j0 + j) * a.blocks + b0;
-          if (a.vec) {
-            const float4 f = __ldg(reinterpret_cast<const float4*>(p));
-            v[m][0] = f.x, v[m][1] = f.y, v[m][2] = f.z, v[m][3] = f.w;
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (k < nb) v[m][k] = __ldg(p + k);
-          }
-        }
-        const int i_cta = x.i0 + (int)rank * 128;
-        w2 = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = 0.f;
-        if constexpr (kGates) {
-          // lanes 0-3 the gates' four, 4-7 the ups'
-          const int half = lane >> 2, k = lane & 3, ob = i_cta / 256;
-          if (half < 2 && k < nb && ob < a.nb)
-            w2 = __ldg(a.ws + ((size_t)x.e * 2 * a.nb + half * a.nb + ob) * a.kb + b0 + k);
-        } else if (i_cta < a.I) {
-          const size_t at = DX ? ((size_t)x.e * a.blocks + b0) * a.kb + i_cta / 128
-                               : ((size_t)x.e * a.nb + i_cta / 128) * a.kb + b0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < nb) w[k] = __ldg(a.ws + at + (size_t)k * (DX ? a.kb : 1));
-        }
-        if (++q_load == entries) q_load = 0, t_load += step;
-      };
-      float v[4][4], w[4], w2;  // the entry in flight
-      load(v, w, w2);
-      const int64_t total = n_tiles > first ? (int64_t)((n_tiles - 1 - first) / step + 1) * entries : 0;
-      uint32_t s = 0, lap = 0;
-      for (int64_t i = 0; i < total; ++i) {
-        if (lap > 0 && !wait(&bars.sempty[s], (lap & 1) ^ 1)) break;
-        float* to = s_scales + s * kScaleFloats;
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            to[k * kNT + scale_place(l64 + 64 * m)] = kGates ? v[m][k] : v[m][k] * w[k];
-        if (kGates && warp == 2 && lane < 8) to[kEntry * kNT + lane] = w2;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.sfull[s]);
-        if (++s == kScaleRing) s = 0, ++lap;
-        load(v, w, w2);
-      }
     }
   } else {
     // ---- scaled sums, and results ----
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDrainRegs));
-    const int q = warp & 3, half = (warp - 4) >> 2, c = lane & 3;
-    uint8_t* stage = staging + (warp - 4) * kStaging;
-    uint32_t buf = 0, se = 0, se_lap = 0, nth = 0;  // nth: tiles so far
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const bool wide = a.wide;
+    uint32_t buf = 0, nth = 0;  // nth: tiles so far
+    // Factors of four blocks, read four blocks ahead: the row's, and the weights' in
+    // lanes 0-3 (with SwiGLU the ups' in lanes 4-7).
+    float4 xn = {};
+    float wn = 0.f;
+    auto fetch = [&](const Tile& x, int b0) {
+      const int jh = (x.rows + 1) / 2, j = min((int)rank * jh + 32 * q + lane, x.rows - 1);
+      const float* p = a.xs + (size_t)(x.row0 + j) * a.blocks + b0;
+      const int left = a.blocks - b0;
+      if (a.vec) {
+        xn = __ldg(reinterpret_cast<const float4*>(p));
+      } else {
+        xn.x = __ldg(p);
+        if (left > 1) xn.y = __ldg(p + 1);
+        if (left > 2) xn.z = __ldg(p + 2);
+        if (left > 3) xn.w = __ldg(p + 3);
+      }
+      const int k = lane & 3, which = lane >> 2;
+      wn = 0.f;
+      if (k >= left) return;
+      if constexpr (kGates) {
+        if (which < 2) wn = __ldg(a.ws + ((size_t)x.e * 2 * a.nb + which * a.nb + x.i0 / 128) * a.kb + b0 + k);
+      } else {
+        const int ib = x.i0 / 128 + half;  // the block of this warp's columns
+        if (which == 0 && ib * 128 < a.out_cols)
+          wn = __ldg(DX ? a.ws + ((size_t)x.e * a.blocks + b0 + k) * a.kb + ib
+                        : a.ws + ((size_t)x.e * a.nb + ib) * a.kb + b0 + k);
+      }
+    };
     bool ok = true;
+    Tile x = {}, next = {};
+    if (first < n_tiles) {
+      next = tile_at<kGates>(a, s_begin, s_tile, first);
+      fetch(next, 0);
+    }
     for (int t = first; t < n_tiles && ok; t += step) {
-      const Tile x = tile_at(a, s_begin, s_tile, t);
-      const int i_cta = x.i0 + (int)rank * 128, i_warp = i_cta + 32 * q;
+      x = next;
+      const int jh = (x.rows + 1) / 2, rows = rank ? x.rows - jh : jh;  // of this CTA
+      // chunks of 32 columns of this warp's 128; none where its lanes hold no tokens
+      const int chunks = 32 * q < rows ? min(4, max(0, (x.cols - 128 * half + 31) / 32)) : 0;
       Pair acc[4][16];
 #pragma unroll
       for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int k = 0; k < 16; ++k) acc[m][k] = 0;
-      const int mine = min(4, max(0, (x.jn - 32 * half + 63) / 64));  // chunks of 32 columns
+      float4 xc = {};
+      float wc = 0.f;
       for (int kb = 0; kb < a.blocks; ++kb) {
         const uint32_t b = buf & 1, use = buf >> 1;
         ++buf;
-        if ((kb & 3) == 0 && !(ok = wait(&bars.sfull[se], se_lap & 1))) break;
-        const float* sc = s_scales + se * kScaleFloats;
-        Pair wg = 0, wu = 0;
-        if (kGates) {
-          const uint32_t g = __float_as_uint(sc[kEntry * kNT + (kb & 3)]), u = __float_as_uint(sc[kEntry * kNT + 4 + (kb & 3)]);
-          wg = pair_of(g, g);
-          wu = pair_of(u, u);
+        if ((kb & 3) == 0) {
+          xc = xn;
+          wc = wn;
+          if (kb + 4 < a.blocks) {
+            fetch(x, kb + 4);
+          } else if (t + step < n_tiles) {
+            next = tile_at<kGates>(a, s_begin, s_tile, t + step);
+            fetch(next, 0);
+          }
         }
-        const uint32_t scales = smem_u32(sc + (kb & 3) * kNT + 32 * half + 8 * c);
+        const float sg = xc.x * __shfl_sync(~0u, wc, kb & 3);
+        const float su = kGates ? xc.x * __shfl_sync(~0u, wc, 4 + (kb & 3)) : sg;
+        const Pair pg = pair_of(sg, sg), pu = pair_of(su, su);
+        xc.x = xc.y, xc.y = xc.z, xc.z = xc.w;
         if (!(ok = wait(&bars.tfull[b], use & 1))) break;
         fence_after();
-        const uint32_t src = tmem + b * kNT + ((uint32_t)(q * 32) << 16) + 32 * half;
-        Block v[2];
-        if (mine > 0) load_block(src, v[0]);
+        const uint32_t src = tmem + b * kNT + ((uint32_t)(q * 32) << 16) + 128 * half;
+        uint32_t v[2][32];
+        if (chunks > 0) tmem_ld32(src, v[0]);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          if (m >= mine) break;
+          if (m >= chunks) break;
           tmem_wait();
-          if (m + 1 < 4 && m + 1 < mine) load_block(src + 64 * (m + 1), v[(m + 1) & 1]);
-          if (m + 1 == mine) {  // the accumulator is read
+          if (m + 1 < 4 && m + 1 < chunks) {
+            tmem_ld32(src + 32 * (m + 1), v[(m + 1) & 1]);
+          } else {  // the accumulator is read
             fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster_relaxed(lead(&bars.tempty[b]));
           }
-          add_block<kGates>(v[m & 1], scales + 256 * m, wg, wu, acc[m]);
+          add_scaled(v[m & 1], pg, pu, acc[m]);
         }
-        if (mine == 0) {
+        if (chunks == 0) {
           __syncwarp();
           if (lane == 0) arrive_cluster_relaxed(lead(&bars.tempty[b]));
         }
-        if ((kb & 3) == 3 || kb == a.blocks - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.sempty[se]);
-          if (++se == kScaleRing) se = 0, ++se_lap;
-        }
       }
       if (!ok) break;
-      const size_t row0 = (size_t)(x.begin + x.j0) + 32 * half;
-      if constexpr (DX && ACT) {
+      const int j = 32 * q + lane;
+      const bool real = j < rows;
+      const size_t row = (size_t)(x.row0 + (int)rank * jh + j);
+      if constexpr (kGates) {
+        const int o0 = x.i0 + 64 * half;  // a chunk is 16 outputs
+        float top = 0.f;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          if (m >= mine) break;
-          Saved saved;
-          load_saved(a, x, i_warp, 32 * half + 64 * m, saved);
-          store_gradients<T>(a, acc[m], saved, static_cast<uint16_t*>(a.out) + (row0 + 64 * m) * 2 * a.I, i_warp,
-                             x.jn - 32 * half - 64 * m, stage);
-        }
-      } else {
-        const int o = kGates ? i_warp / 2 : i_warp, n_out = kGates ? a.n : a.I;  // outputs
-        const bool in = o < n_out;
-        float tops[4];
+          if (m >= chunks) break;
+          const int o = o0 + 16 * m;
+          const bool in = real && o < a.n;
+          if (a.pre_out && in) {
+            uint16_t* pre = static_cast<uint16_t*>(a.pre_out) + row * 2 * a.n + o;
+            store16<T>(pre, acc[m], wide);
+            store16<T>(pre + a.n, acc[m] + 8, wide);
+          }
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          if (m >= mine) break;
-          const int jn = x.jn - 32 * half - 64 * m;
-          const size_t row = row0 + 64 * m;
-          if constexpr (kGates) {
-            if (a.pre_out) {  // the first two pieces are gates, the others ups
-              const int i = o + 8 * (c & 1) + (c & 2 ? a.n : 0);
-              store_rows<T>(acc[m], static_cast<uint16_t*>(a.pre_out) + row * 2 * a.n, 2 * (size_t)a.n, i, in, jn, stage);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float y0 = swiglu(lo_of(acc[m][k]), lo_of(acc[m][8 + k]));
-              const float y1 = swiglu(hi_of(acc[m][k]), hi_of(acc[m][8 + k]));
-              acc[m][k] = pair_of(__float_as_uint(y0), __float_as_uint(y1));
-            }
-            const Pair(&y)[8] = reinterpret_cast<const Pair(&)[8]>(acc[m]);
-            if constexpr (OUT8) tops[m] = column_tops(y);
-            else store_half_rows<T>(y, static_cast<uint16_t*>(a.out) + row * a.n, a.n, o, in, jn, stage);
-          } else {
-            if constexpr (OUT8) tops[m] = column_tops(acc[m]);
-            else store_rows<T>(acc[m], static_cast<uint16_t*>(a.out) + row * n_out, n_out, i_warp + 8 * c, i_warp + 8 * c < n_out, jn, stage);
+          for (int k = 0; k < 8; ++k)
+            acc[m][k] = pair_of(swiglu(lo_of(acc[m][k]), lo_of(acc[m][8 + k])),
+                                swiglu(hi_of(acc[m][k]), hi_of(acc[m][8 + k])));
+          if constexpr (OUT8) {
+            if (o < a.n) top = top_of(acc[m], top);
+          } else if (in) {
+            store16<T>(static_cast<uint16_t*>(a.out) + row * a.n + o, acc[m], wide);
           }
         }
         if constexpr (OUT8) {
-          // A group of 128 outputs is on the lanes of one CTA, with SwiGLU on those of both:
-          // the warps leave their columns' largest values with all who need them. Two buffers
-          // by the tiles' turn: who writes the next but one has seen all arrive for the next,
-          // and they had read this one.
-          const int from = kGates ? (int)rank * 4 + q : q;
-          const int col = 8 * (lane >> 3) + 2 * c + ((lane >> 2) & 1);  // of column_tops
-          float* tb = s_top + (nth & 1) * 8 * kNT + 32 * half + col;
+          // The other half of the group's outputs is with the other warp of this quarter.
+          // Two buffers by the tiles' turn: who writes the next but one has seen the other
+          // arrive for the next, and that one had read this one.
+          float* tb = s_top + (nth & 1) * 256 + 32 * q + lane;
+          tb[128 * half] = top;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.top[q]);
+          if (!(ok = wait(&bars.top[q], nth & 1))) break;
+          top = fmaxf(top, tb[128 * (half ^ 1)]);
+          const float s = __fdiv_rn(448.f, top), mult = top == 0.f ? 0.f : s;
+          if (half == 0 && real) a.ys[row * a.nb + x.i0 / 128] = __fdiv_rn(1.f, s);
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            if (m >= mine) break;
-            tb[from * kNT + 64 * m] = tops[m];
-            if (kGates) {
-              const uint32_t to = addr_in(smem_u32(tb + from * kNT + 64 * m), rank ^ 1);
-              asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(tops[m]) : "memory");
+            const int o = o0 + 16 * m;
+            if (m >= chunks || !real || o >= a.n) break;
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + row * a.n + o) = codes16(acc[m], mult);
+          }
+        }
+      } else {
+        const int i0 = x.i0 + 128 * half, left = real ? a.out_cols - i0 : 0;
+        if constexpr (DX && ACT) {
+          const uint16_t* pre = static_cast<const uint16_t*>(a.pre_in) + row * 2 * a.out_cols + i0;
+          uint16_t* out = static_cast<uint16_t*>(a.out) + row * 2 * a.out_cols + i0;
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int c = 32 * m + 16 * h;
+              if (m >= chunks || c >= left) break;
+              uint32_t g[8], u[8];
+              load32(pre + c, g, wide);
+              load32(pre + a.out_cols + c, u, wide);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const Pair d = acc[m][8 * h + k];
+                float dg0, du0, dg1, du1;
+                swiglu_gradient(lo_of(d), T::lo(g[k]), T::lo(u[k]), dg0, du0);
+                swiglu_gradient(hi_of(d), T::hi(g[k]), T::hi(u[k]), dg1, du1);
+                g[k] = T::pack2(dg0, dg1);
+                u[k] = T::pack2(du0, du1);
+              }
+              store32(out + c, g, wide);
+              store32(out + a.out_cols + c, u, wide);
             }
           }
-          __syncwarp();
-          if (lane == 0) {
-            if (kGates) arrive_cluster(addr_in(smem_u32(&bars.top[half]), rank ^ 1));
-            arrive_cluster(addr_in(smem_u32(&bars.top[half]), rank));
-          }
-          if (!(ok = wait(&bars.top[half], nth & 1, true))) break;
+        } else if constexpr (OUT8) {
+          float top = 0.f;
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            if (m >= mine) break;
-            float top = 0.f;
+          for (int m = 0; m < 4; ++m)
 #pragma unroll
-            for (int k = 0; k < (kGates ? 8 : 4); ++k) top = fmaxf(top, tb[k * kNT + 64 * m]);
-            const float s = __fdiv_rn(448.f, top), mult = top == 0.f ? 0.f : s;
-            const int jn = x.jn - 32 * half - 64 * m;
-            const size_t row = row0 + 64 * m;
-            if (q == 0 && (!kGates || rank == 0) && o < n_out && col < jn)
-              a.ys[(row + col) * a.nb + o / 128] = __fdiv_rn(1.f, s);
-            uint8_t* out = static_cast<uint8_t*>(a.out) + row * n_out;
-            if constexpr (kGates)
-              store_codes(reinterpret_cast<const Pair(&)[8]>(acc[m]), mult, out, n_out, o, n_out - o, jn, stage);
-            else
-              store_codes(acc[m], mult, out, n_out, o, n_out - o, jn, stage);
-          }
+            for (int h = 0; h < 2; ++h)
+              if (m < chunks && 32 * m + 16 * h < left) top = top_of(acc[m] + 8 * h, top);
+          const float s = __fdiv_rn(448.f, top), mult = top == 0.f ? 0.f : s;
+          if (left > 0) a.ys[row * a.nb + i0 / 128] = __fdiv_rn(1.f, s);
+          uint8_t* out = static_cast<uint8_t*>(a.out) + row * a.out_cols + i0;
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (m < chunks && 32 * m + 16 * h < left)
+                *reinterpret_cast<uint4*>(out + 32 * m + 16 * h) = codes16(acc[m] + 8 * h, mult);
+        } else {
+          uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.out_cols + i0;
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (m < chunks && 32 * m + 16 * h < left) store16<T>(out + 32 * m + 16 * h, acc[m] + 8 * h, wide);
         }
       }
       ++nth;
@@ -683,15 +518,14 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
 
 // ---- host ----
 template <bool DX, typename T, bool ACT, bool OUT8>
-cudaError_t launch_t(const B128Args& a, const CUtensorMap& ma, const CUtensorMap& mb, const FewMaps& few, cudaStream_t s) {
+cudaError_t launch_t(const B128Args& a, const CUtensorMap& mw, const RowMaps& mr, cudaStream_t s) {
   constexpr auto kernel = b128_kernel<DX, T, ACT, OUT8>;
-  const size_t smem = 1024 + kStages * kStageBytes + kDrainWarps * kStaging + kScaleRing * kScaleFloats * 4 +
-                      (OUT8 ? 2 * 8 * kNT * 4 : 0) + 8 * ((size_t)a.G + 1);
+  const size_t smem = 1024 + kStages * kStageBytes + 8 * ((size_t)a.G + 1);
   cudaError_t e = prepare_kernel<kernel>(smem);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorUnknown;
-  const int64_t most = (int64_t)a.tiles_i * (a.R / kNT + std::min(a.G, a.R));
+  const int64_t most = (int64_t)a.tiles_i * (a.R / 256 + std::min(a.G, a.R));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min<int64_t>(sms / 2, most) * 2);
   cfg.blockDim = dim3(kThreads);
@@ -704,43 +538,47 @@ cudaError_t launch_t(const B128Args& a, const CUtensorMap& ma, const CUtensorMap
   attr[1].val.clusterDim = {2, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, a, ma, mb, few);
+  return cudaLaunchKernelEx(&cfg, kernel, a, mw, mr);
 }
 
 template <typename T>
 cudaError_t launch_type(bool dx, B128Args& a, cudaStream_t s) {
   const uint64_t G = a.G, R = a.R, N = a.N, K = a.K, n = a.n, halves = N / n;
-  CUtensorMap ma, mb;
-  FewMaps few = {};
+  const bool act = a.act && !dx;
+  CUtensorMap mw;
+  RowMaps mr;
   a.blocks = dx ? (int)halves * a.nb : a.kb;
   a.half_blocks = dx ? a.nb : a.kb;
   a.half_len = dx ? a.n : a.K;
-  a.vec = a.blocks % 4 == 0 && reinterpret_cast<uintptr_t>(a.xs) % 16 == 0;
-  a.I = dx ? a.K : a.N;
-  a.tiles_i = (a.I + 255) / 256;
+  a.out_cols = dx ? a.K : a.n;
+  a.tiles_i = act ? a.nb : (a.out_cols + 255) / 256;
+  auto whole = [](const void* p, int64_t row, int unit) { return (reinterpret_cast<uintptr_t>(p) | row) % unit == 0; };
+  a.vec = whole(a.xs, 4 * (int64_t)a.blocks, 16);
+  // every 16 values of a result's row begin on 32 bytes if the first do
+  a.wide = whole(a.out, 0, 32) && whole(a.pre_in, 0, 32) && whole(a.pre_out, 0, 32);
   {  // rows: of both halves side by side for dx
     const uint64_t len = a.half_len, h = dx ? halves : 1, d[] = {len, h, R}, st[] = {len, len * h};
     const uint32_t b[] = {128, 1, 128}, b64[] = {128, 1, 64}, b32[] = {128, 1, 32};
-    if (!make_map(&mb, a.x, kMapU8, 3, d, st, b) || !make_map(&few.b64, a.x, kMapU8, 3, d, st, b64) ||
-        !make_map(&few.b32, a.x, kMapU8, 3, d, st, b32))
+    if (!make_map(&mr.b128, a.x, kMapU8, 3, d, st, b) || !make_map(&mr.b64, a.x, kMapU8, 3, d, st, b64) ||
+        !make_map(&mr.b32, a.x, kMapU8, 3, d, st, b32))
       return cudaErrorUnknown;
   }
   if (dx) {
     const uint64_t d[] = {K, n, halves, G}, st[] = {K, n * K, N * K};
     const uint32_t b[] = {128, 128, 1, 1};
-    if (!make_map(&ma, a.w, kMapU8, 4, d, st, b)) return cudaErrorUnknown;
-    return a.pre_in ? launch_t<true, T, true, false>(a, ma, mb, few, s) : launch_t<true, T, false, false>(a, ma, mb, few, s);
+    if (!make_map(&mw, a.w, kMapU8, 4, d, st, b)) return cudaErrorUnknown;
+    return a.pre_in ? launch_t<true, T, true, false>(a, mw, mr, s) : launch_t<true, T, false, false>(a, mw, mr, s);
   }
-  if (a.act) {  // a tile's rows: 16 gates, 16 ups, 16 gates, ...
+  if (act) {  // columns: 16 gates, 16 ups, 16 gates, ...
     const uint64_t d[] = {K, 16, 2, n / 16, G}, st[] = {K, n * K, 16 * K, N * K};
     const uint32_t b[] = {128, 16, 2, 4, 1};
-    if (!make_map(&ma, a.w, kMapU8, 5, d, st, b)) return cudaErrorUnknown;
-    return a.ys ? launch_t<false, T, true, true>(a, ma, mb, few, s) : launch_t<false, T, true, false>(a, ma, mb, few, s);
+    if (!make_map(&mw, a.w, kMapU8, 5, d, st, b)) return cudaErrorUnknown;
+    return a.ys ? launch_t<false, T, true, true>(a, mw, mr, s) : launch_t<false, T, true, false>(a, mw, mr, s);
   }
   const uint64_t d[] = {K, N, G}, st[] = {K, N * K};
   const uint32_t b[] = {128, 128, 1};
-  if (!make_map(&ma, a.w, kMapU8, 3, d, st, b)) return cudaErrorUnknown;
-  return a.ys ? launch_t<false, T, false, true>(a, ma, mb, few, s) : launch_t<false, T, false, false>(a, ma, mb, few, s);
+  if (!make_map(&mw, a.w, kMapU8, 3, d, st, b)) return cudaErrorUnknown;
+  return a.ys ? launch_t<false, T, false, true>(a, mw, mr, s) : launch_t<false, T, false, false>(a, mw, mr, s);
 }
 
 int validate(const cq_expert_config* c) {

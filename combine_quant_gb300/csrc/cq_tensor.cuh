@@ -46,13 +46,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Shared-memory address in the pair's CTA `rank` for one of this CTA.
-__device__ __forceinline__ uint32_t addr_in(uint32_t a, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-  return r;
-}
-
 // Shared-memory address of the pair's CTA 0 (the leader) for one of this CTA.
 __device__ __forceinline__ uint32_t leader_addr(uint32_t a) {
   uint32_t r;
@@ -280,9 +273,9 @@ __device__ __forceinline__ uint32_t idesc_f16(bool bf16, bool a_mn, bool b_mn, i
 }
 
 // Instruction descriptor of kind::f8f6f4: f32 accumulators, formats 0 e4m3, 1 e5m2,
-// A optionally MN-major, M x N.
-__device__ __forceinline__ uint32_t idesc_fp8(int a_fmt, int b_fmt, bool a_mn, int m, int n) {
-  return (1u << 4) | ((uint32_t)a_fmt << 7) | ((uint32_t)b_fmt << 10) | ((a_mn ? 1u : 0u) << 15) |
+// B optionally MN-major, M x N.
+__device__ __forceinline__ uint32_t idesc_fp8(int a_fmt, int b_fmt, bool b_mn, int m, int n) {
+  return (1u << 4) | ((uint32_t)a_fmt << 7) | ((uint32_t)b_fmt << 10) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
