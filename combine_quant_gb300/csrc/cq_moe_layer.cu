@@ -1,95 +1,618 @@
 // cq_moe_layer.cu -- the whole layer for a few tokens: gate and up products with
 // SwiGLU (up_kernel), down product with the weighted sum (down_kernel).
 //
-// The simplest form: a warp a result.
-#include <cuda_fp8.h>
+// The weights of the experts that the tokens name are read once, and that is the bound:
+// both kernels stream them through a ring of shared memory (tiled copies by one warp)
+// and multiply on the way with mma.sync, whose 8 columns suit a few tokens and whose
+// rate a stream from memory does not reach. Eight warps take 64 bytes of a row each;
+// with k in an order of the thread's choice (its 16 bytes of a row against the same 16
+// bytes of a token) one 16-byte load feeds two to four products.
+//
+// Every CTA sorts the (token, expert) pairs itself into items: an expert and up to 8 NB
+// of its tokens, ascending. A token that names an expert twice is one pair with both
+// weights. up_kernel: an item's tile of 16 (32) gates and their ups is one CTA's work;
+// its warps' shares of k are added in shared memory, in order. down_kernel: a tile of 32
+// (64) output rows is one cluster's work: the CTAs share the stages of all items evenly,
+// each keeps the weighted sums of all tokens, and the CTAs' sums are added through
+// distributed shared memory, in order. Results do not depend on timing.
+//
+// Between the two SwiGLU's results are held as two numbers of the token type, whose sum
+// keeps 16 bits or more: rounding them to one would add an error as large as y's own
+// rounding. The second kernel's copies of weights start before the first one has ended.
+#include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "cq_expert.cuh"
+#include "cq_tensor.cuh"
 
 namespace cq {
 namespace expert {
 namespace {
 
+using namespace tensor;
+using async::mbar_arrive_expect_tx;
+using async::mbar_init;
+using async::mbar_wait;
+using async::mbar_wait_warp;
+
 __device__ uint32_t g_status;  // CQ_ST_* bits of these kernels on this device
 
 struct LayerArgs {
   int32_t T, G, K, H, I, mask_ndim, out_f32;
+  int32_t stages, cluster;   // of the ring; CTAs that share a tile (down_kernel)
   const uint16_t* x;
   const int32_t* ids;
   const float* scales;
   const uint8_t* mask;
-  const void* w13;
   const float* w13_scales;
-  const void* w2;
   const float* w2_scales;
-  float* h;  // [T * K, I]
+  uint16_t* h;  // [2][T * K][I]: both numbers
   void* y;
 };
 
-__device__ __forceinline__ int expert_of_pair(const LayerArgs& a, int p) {
-  if (a.mask_ndim && !a.mask[a.mask_ndim == 1 ? p / a.K : p]) return -1;
-  const int e = a.ids[p];
-  if ((unsigned)e < (unsigned)a.G) return e;
-  atomicOr(&g_status, (uint32_t)CQ_ST_BAD_ID);
-  return -1;
+constexpr int kWarps = 8;                 // that multiply; one more copies
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kStageW = 16384;            // weights of a stage
+constexpr int kMaxPairs = 64 * 16, kMaxItems = kMaxPairs + 32;
+
+// A stage: 4 / RG boxes of 32 RG rows of 128 bytes; its k.
+template <bool FP8, int RG>
+constexpr int kChunk = (FP8 ? 512 : 256) / RG;
+// Bytes from one token's part of a stage to the next: 16 bytes a thread from rows that
+// a quarter of a warp reads together must lie in different banks.
+template <bool FP8, int RG>
+constexpr int kPitch = 2 * kChunk<FP8, RG> + (FP8 ? 16 : 64);
+
+struct Items {
+  int n;                        // items
+  uint16_t e[kMaxItems], off[kMaxItems];  // expert, first pair
+  uint8_t m[kMaxItems];         // pairs
+  uint8_t tok[kMaxPairs];       // of each pair the token and its weight
+  float weight[kMaxPairs];
+  int scan[2][kWarps + 1];
+};
+
+// Sorts the pairs (all threads). `masks`: scratch of G 64-bit words.
+template <int PER>
+__device__ __forceinline__ void sort_pairs(const LayerArgs& a, Items& it, unsigned long long* masks, bool report) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, P = a.T * a.K;
+  for (int e = t; e < a.G; e += kThreads) masks[e] = 0;
+  __syncthreads();
+  auto id_of = [&](int p) {  // or -1
+    if (a.mask_ndim && !a.mask[a.mask_ndim == 1 ? p / a.K : p]) return -1;
+    const int e = a.ids[p];
+    return (unsigned)e < (unsigned)a.G ? e : -2;
+  };
+  for (int p = t; p < P; p += kThreads) {
+    const int e = id_of(p);
+    if (e >= 0) atomicOr(masks + e, 1ull << (p / a.K));
+    else if (e == -2 && report) atomicOr(&g_status, (uint32_t)CQ_ST_BAD_ID);
+  }
+  __syncthreads();
+  const int per = (a.G + kThreads - 1) / kThreads, e0 = min(a.G, t * per), e1 = min(a.G, e0 + per);
+  int pairs = 0, items = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int c = __popcll(masks[e]);
+    pairs += c;
+    items += (c + PER - 1) / PER;
+  }
+  int rp = pairs, ri = items;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int vp = __shfl_up_sync(~0u, rp, o), vi = __shfl_up_sync(~0u, ri, o);
+    if (lane >= o) rp += vp, ri += vi;
+  }
+  if (lane == 31) it.scan[0][warp] = rp, it.scan[1][warp] = ri;
+  __syncthreads();
+  int p0 = rp - pairs, i0 = ri - items;
+  for (int w = 0; w < warp; ++w) p0 += it.scan[0][w], i0 += it.scan[1][w];
+  for (int e = e0; e < e1; ++e) {
+    unsigned long long m = masks[e];
+    int left = __popcll(m);
+    for (; left > 0; left -= PER, ++i0) {
+      const int c = min(left, PER);
+      it.e[i0] = (uint16_t)e;
+      it.off[i0] = (uint16_t)p0;
+      it.m[i0] = (uint8_t)c;
+      for (int k = 0; k < c; ++k, ++p0, m &= m - 1) {
+        const int tok = __ffsll((long long)m) - 1;
+        float w = 0.f;
+        for (int j = 0; j < a.K; ++j)
+          if (id_of(tok * a.K + j) == e) w += a.scales[tok * a.K + j];
+        it.tok[p0] = (uint8_t)tok;
+        it.weight[p0] = w;
+      }
+    }
+  }
+  if (t == kThreads - 1) it.n = i0;
+  __syncthreads();
 }
 
-template <typename T, bool FP8>
-__device__ __forceinline__ float weight_at(const void* w, size_t at) {
-  if (FP8) return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(w)[at], __NV_E4M3)));
-  return T::lo(static_cast<const uint16_t*>(w)[at]);
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
 
-template <typename T, bool FP8>
-__global__ void __launch_bounds__(256) up_kernel(const __grid_constant__ LayerArgs a) {
-  griddep_wait();
-  const int lane = threadIdx.x & 31, hb = (a.H + 127) / 128, ib = (a.I + 127) / 128;
-  const int total = a.T * a.K * a.I;
-  for (int task = blockIdx.x * 8 + (threadIdx.x >> 5); task < total; task += gridDim.x * 8) {
-    const int p = task / a.I, i = task % a.I, e = expert_of_pair(a, p);
-    if (e < 0) continue;
-    float v[2];
-    for (int half = 0; half < 2; ++half) {
-      float sum = 0.f;
-      for (int j = lane; j < a.H; j += 32) {
-        float w = weight_at<T, FP8>(a.w13, ((size_t)e * 2 * a.I + half * a.I + i) * a.H + j);
-        if (FP8) w *= a.w13_scales[((size_t)e * 2 * ib + half * ib + i / 128) * hb + j / 128];
-        sum = fmaf(w, T::lo(a.x[(size_t)(p / a.K) * a.H + j]), sum);
-      }
-      v[half] = warp_sum(sum);
-    }
-    if (lane == 0) a.h[(size_t)p * a.I + i] = swiglu(v[0], v[1]);
+template <typename T>
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  if constexpr (T::kBf16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four e4m3 codes as two words of 16-bit numbers, exactly. bf16: exponent and fraction
+// put where bf16 has them are the value times 2^-120 (also below the normal range).
+template <typename T>
+__device__ __forceinline__ void decode4(uint32_t q, uint32_t& lo, uint32_t& hi) {
+  if constexpr (T::kBf16) {
+    const uint32_t y = __byte_perm(q, 0, 0x1404), z = __byte_perm(q, 0, 0x3424);  // a code in each upper byte
+    lo = (y & 0x80008000u) | ((y >> 4) & 0x07f007f0u);
+    hi = (z & 0x80008000u) | ((z >> 4) & 0x07f007f0u);
+    constexpr uint32_t k2to120 = 0x7b807b80u;
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(k2to120));
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(hi) : "r"(k2to120));
+  } else {
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(q));
   }
 }
 
-template <typename T, bool FP8>
-__global__ void __launch_bounds__(256) down_kernel(const __grid_constant__ LayerArgs a) {
-  griddep_wait();
-  const int lane = threadIdx.x & 31, hb = (a.H + 127) / 128, ib = (a.I + 127) / 128;
-  const int total = a.T * a.H;
-  for (int task = blockIdx.x * 8 + (threadIdx.x >> 5); task < total; task += gridDim.x * 8) {
-    const int t = task / a.H, o = task % a.H;
-    float y = 0.f;
-    for (int k = 0; k < a.K; ++k) {
-      const int p = t * a.K + k, e = expert_of_pair(a, p);
-      if (e < 0) continue;
-      float sum = 0.f;
-      for (int j = lane; j < a.I; j += 32) {
-        float w = weight_at<T, FP8>(a.w2, ((size_t)e * a.H + o) * a.I + j);
-        if (FP8) w *= a.w2_scales[((size_t)e * hb + o / 128) * ib + j / 128];
-        sum = fmaf(w, a.h[(size_t)p * a.I + j], sum);
+// Row of a box that row g of a fragment stands for: rows whose 16-byte pieces a quarter of
+// a warp reads together differ in bit 2, which the swizzle turns into the other 64 bytes.
+__device__ __forceinline__ int fragment_row(int g) { return ((g & 1) << 2) | (g >> 1); }
+
+// Two fragments of 16 rows (at r0, r1 of a box) times up to 8 NB tokens over this warp's
+// 64 bytes of the rows. `b`: shared address of token 0's part for this thread's column
+// group; PARTS: the tokens' numbers are sums of PARTS numbers. `in`: the thread's k exist.
+// FP8: s0, s1 are the fragments' factors here; nan collects codes that are NaN (bf16,
+// whose decoding does not know them): bit 7 of a byte, by fragment and upper rows.
+template <typename T, bool FP8, int NB, int PARTS>
+__device__ __forceinline__ void multiply(uint32_t box, int r0, int r1, int half, uint32_t b, int pitch, int part_bytes, bool in,
+                                         int n8, float s0, float s1, float (&acc)[2][NB][4], uint32_t (&nan)[4]) {
+  const int lane = threadIdx.x & 31, row = fragment_row(lane >> 2), c = lane & 3;
+  const uint32_t piece = ((half * 4 + c) ^ row) << 4;
+  uint4 w[2][2];
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) w[f][u] = lds16(box + ((f ? r1 : r0) + 8 * u + row) * 128 + piece);
+  constexpr int kSteps = FP8 ? 4 : 2;  // products of 16 k
+  uint32_t v[2][2][2 * kSteps];
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t q[4] = {w[f][u].x, w[f][u].y, w[f][u].z, w[f][u].w};
+      if constexpr (FP8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (T::kBf16) nan[2 * f + u] |= (q[k] & 0x7f7f7f7fu) + 0x01010101u;
+          decode4<T>(q[k], v[f][u][2 * k], v[f][u][2 * k + 1]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[f][u][k] = q[k];
       }
-      y = fmaf(a.scales[p], warp_sum(sum), y);
     }
-    if (lane != 0) continue;
-    if (a.out_f32) static_cast<float*>(a.y)[task] = y;
-    else static_cast<uint16_t*>(a.y)[task] = (uint16_t)T::pack2(y, 0.f);
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    if (n >= n8) break;
+    float sum[2][4] = {};
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+      const uint32_t at = b + (8 * n + (lane >> 2)) * pitch + p * part_bytes;
+      uint32_t x[2 * kSteps];
+#pragma unroll
+      for (int k = 0; k < kSteps / 2; ++k) {
+        const uint4 t = in ? lds16(at + 16 * k) : make_uint4(0, 0, 0, 0);
+        x[4 * k] = t.x, x[4 * k + 1] = t.y, x[4 * k + 2] = t.z, x[4 * k + 3] = t.w;
+      }
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          mma16<T>(FP8 ? sum[f] : acc[f][n], v[f][0][2 * k], v[f][1][2 * k], v[f][0][2 * k + 1], v[f][1][2 * k + 1],
+                   x[2 * k], x[2 * k + 1]);
+    }
+    if constexpr (FP8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[0][n][i] = fmaf(sum[0][i], s0, acc[0][n][i]);
+        acc[1][n][i] = fmaf(sum[1][i], s1, acc[1][n][i]);
+      }
+    }
   }
+}
+
+// Rows with a NaN code have NaN sums.
+template <int NB>
+__device__ __forceinline__ void spread_nan(uint32_t (&nan)[4], float (&acc)[2][NB][4]) {
+  uint32_t all = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) all |= (nan[k] & 0x80808080u) ? 1u << k : 0u;
+  all |= __shfl_xor_sync(~0u, all, 1);
+  all |= __shfl_xor_sync(~0u, all, 2);
+  if (all) {
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (all >> (2 * f + (i >> 1)) & 1) acc[f][n][i] = __uint_as_float(0x7fffffffu);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) nan[k] = 0;
+}
+
+struct Ring {
+  uint64_t full[8], empty[8];
+};
+
+// The rings' start: barriers, and shared memory that sort_pairs used handed to the copies.
+__device__ __forceinline__ void init_ring(Ring& r, int stages) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&r.full[s], 1);
+      mbar_init(&r.empty[s], kWarps);
+    }
+    async::mbar_fence_init();
+  }
+}
+
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
+  if (mbar_wait_warp(bar, parity)) return true;
+  atomicOr(&g_status, (uint32_t)CQ_ST_TIMEOUT);
+  return false;
+}
+
+// Copies in flight when a wait gave up land (with a limit) before the CTA goes.
+__device__ __forceinline__ void end_copies(Ring& r, int stages, uint32_t s, uint32_t lap) {
+  for (int v = 0; v < stages; ++v) {
+    const uint32_t u = (s + v) % stages, laps = lap + (u < s ? 1 : 0);
+    if (laps > 0) mbar_wait(&r.full[u], (laps - 1) & 1);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint16_t rounded(float v) {
+  return (uint16_t)T::pack2(v, 0.f);
+}
+
+// Gate and up products and SwiGLU. NB: token blocks of 8; RG: row groups.
+template <typename T, bool FP8, int NB, int RG>
+__global__ void __launch_bounds__(kThreads, RG == 1 ? 2 : 1)
+up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorMap map) {
+  constexpr int KC = kChunk<FP8, RG>, PITCH = kPitch<FP8, RG>, kSegs = 8 / RG, M = 8 * NB;
+  constexpr int kOuts = 16 * RG, kRows = 32 * RG, kBoxes = 4 / RG, kBoxK = KC / kBoxes;
+  constexpr int kStage = kStageW + M * PITCH;
+  extern __shared__ __align__(1024) uint8_t dyn[];
+  __shared__ Ring ring;
+  __shared__ Items items;
+  uint8_t* stage0 = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+  // weights of all stages (1024-byte aligned), then the tokens' parts, then the warps' sums
+  uint8_t* tokens0 = stage0 + a.stages * kStageW;
+  float* red = reinterpret_cast<float*>(stage0 + a.stages * kStage);  // [segs][rows][M + 1]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  init_ring(ring, a.stages);
+  if (threadIdx.x == 0) prefetch_map(&map);
+  griddep_wait();
+  griddep_launch_dependents();  // the down kernel reads results only after its own wait
+  sort_pairs<M>(a, items, reinterpret_cast<unsigned long long*>(stage0), blockIdx.x == 0);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
+  const int tiles = (a.I + kOuts - 1) / kOuts, units = items.n * tiles;
+  const int n_stages = (a.H + KC - 1) / KC;
+  uint32_t s = 0, lap = 0;
+  if (warp == kWarps) {
+    // ---- copies ----
+    bool ok = true;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const int item = u / tiles, i0 = u % tiles * kOuts, m = items.m[item];
+      const uint16_t* row = a.x + (size_t)items.tok[items.off[item] + min(lane, m - 1)] * a.H;
+      for (int k = 0; k < n_stages; ++k) {
+        if (lap > 0 && !(ok = wait_warp(&ring.empty[s], (lap & 1) ^ 1))) break;
+        const uint32_t bytes = 2 * min(KC, a.H - k * KC);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&ring.full[s], kStageW + m * bytes);
+          for (int b = 0; b < kBoxes; ++b)
+            tma_load4<1>(smem_u32(stage0 + s * kStageW + b * kRows * 128), &map, k * KC + b * kBoxK, i0, 0, items.e[item],
+                         smem_u32(&ring.full[s]));
+        }
+        __syncwarp();
+        if (lane < m) async::bulk_load(tokens0 + s * M * PITCH + lane * PITCH, row + k * KC, bytes, &ring.full[s]);
+        if (++s == a.stages) s = 0, ++lap;
+      }
+    }
+    if (!ok) end_copies(ring, a.stages, s, lap);
+    return;
+  }
+  // ---- products ----
+  const int seg = warp / RG, group = warp % RG, c = lane & 3;
+  const int box = seg >> 1, half = seg & 1;
+  const int kt = seg * (FP8 ? 64 : 32) + c * (FP8 ? 16 : 8);  // this thread's first k of a stage
+  const int kb = (a.H + 127) / 128, ib = (a.I + 127) / 128;
+  // FP8: factors of 32 stages, a lane each; those of the next unit are read ahead
+  float gn = 0.f, un = 0.f;
+  auto factors = [&](int u, int first, float& g, float& w) {
+    const int block = ((first + lane) * KC + seg * 64) / 128;
+    if (!FP8 || u >= units || first + lane >= n_stages || block >= kb) return;
+    const float* p = a.w13_scales + ((size_t)items.e[u / tiles] * 2 * ib + u % tiles * kOuts / 128) * kb + block;
+    g = __ldg(p);
+    w = __ldg(p + (size_t)ib * kb);
+  };
+  factors(blockIdx.x, 0, gn, un);
+  bool ok = true;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const int item = u / tiles, m = items.m[item], n8 = (m + 7) / 8, off = items.off[item];
+    float acc[2][NB][4] = {};
+    uint32_t nan[4] = {};
+    float g = gn, w = un;
+    factors(u + gridDim.x, 0, gn, un);
+    for (int k = 0; k < n_stages; ++k) {
+      if (FP8 && k > 0 && (k & 31) == 0) factors(u, k, g, w);
+      const float sg = FP8 ? __shfl_sync(~0u, g, k & 31) : 1.f, su = FP8 ? __shfl_sync(~0u, w, k & 31) : 1.f;
+      if (!(ok = wait_warp(&ring.full[s], lap & 1))) break;
+      multiply<T, FP8, NB, 1>(smem_u32(stage0 + s * kStageW + box * kRows * 128), 16 * group, kOuts + 16 * group, half,
+                              smem_u32(tokens0 + s * M * PITCH) + 2 * kt, PITCH, 0, k * KC + kt < a.H, n8, sg, su, acc, nan);
+      async::release_slot(&ring.empty[s]);
+      if (++s == a.stages) s = 0, ++lap;
+    }
+    if (FP8 && T::kBf16) spread_nan(nan, acc);
+    // the warps' shares: red[seg][row][token]
+    const int row = 32 * group + fragment_row(lane >> 2);
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          red[(seg * kRows + row + 16 * f + 8 * (i >> 1)) * (M + 1) + 8 * n + 2 * c + (i & 1)] = acc[f][n][i];
+    if (!async::meet<32 * kWarps>(ok)) break;
+    const int i0 = u % tiles * kOuts;
+    for (int v = threadIdx.x; v < kOuts * m; v += 32 * kWarps) {
+      const int o = v % kOuts, j = v / kOuts;
+      if (i0 + o >= a.I) continue;
+      const float* p = red + (32 * (o / 16) + o % 16) * (M + 1) + j;
+      float pg = 0.f, pu = 0.f;
+#pragma unroll
+      for (int q = 0; q < kSegs; ++q) {
+        pg += p[q * kRows * (M + 1)];
+        pu += p[(q * kRows + 16) * (M + 1)];
+      }
+      const float r = swiglu(pg, pu);
+      const uint16_t hi = rounded<T>(r);
+      const float lo = r - T::lo(hi);
+      uint16_t* to = a.h + (size_t)(off + j) * a.I + i0 + o;
+      to[0] = hi;
+      // an infinite first number would make the second NaN
+      to[(size_t)a.T * a.K * a.I] = rounded<T>(fabsf(T::lo(hi)) <= 3.402823466e38f ? lo : 0.f);
+    }
+    if (!async::meet<32 * kWarps>(true)) break;
+  }
+}
+
+// Down product and weighted sum.
+template <typename T, bool FP8, int NB, int RG>
+__global__ void __launch_bounds__(kThreads, RG == 1 ? 2 : 1)
+down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorMap map) {
+  constexpr int KC = kChunk<FP8, RG>, PITCH = kPitch<FP8, RG>, kSegs = 8 / RG, M = 8 * NB;
+  constexpr int kRows = 32 * RG, kBoxes = 4 / RG, kBoxK = KC / kBoxes, kLine = kRows + 1;
+  constexpr int kTokens = 2 * M * PITCH;  // both numbers
+  extern __shared__ __align__(1024) uint8_t dyn[];
+  __shared__ Ring ring;
+  __shared__ Items items;
+  uint8_t* stage0 = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+  uint8_t* tokens0 = stage0 + a.stages * kStageW;
+  float* sums = reinterpret_cast<float*>(tokens0 + a.stages * kTokens);  // [segs][T][kLine]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = a.cluster > 1 ? (int)cluster_rank() : 0;
+  const int o0 = blockIdx.x / a.cluster * kRows;
+  init_ring(ring, a.stages);
+  if (threadIdx.x == 0) prefetch_map(&map);
+  // ids, mask and weights were complete before the up kernel let this one start
+  sort_pairs<M>(a, items, reinterpret_cast<unsigned long long*>(stage0), false);
+  for (int v = threadIdx.x; v < kSegs * a.T * kLine; v += kThreads) sums[v] = 0.f;
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
+  const int per = (a.I + KC - 1) / KC, total = items.n * per;
+  const int begin = (int)((int64_t)total * rank / a.cluster), end = (int)((int64_t)total * (rank + 1) / a.cluster);
+  uint32_t s = 0, lap = 0;
+  if (warp == kWarps) {
+    // ---- copies: weights of as many stages as the ring has before the wait for h ----
+    auto load_weights = [&](int v, int st) {
+      const int item = v / per, k = v % per;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&ring.full[st], kStageW + items.m[item] * 4 * min(KC, a.I - k * KC));
+        for (int b = 0; b < kBoxes; ++b)
+          tma_load3<1>(smem_u32(stage0 + st * kStageW + b * kRows * 128), &map, k * KC + b * kBoxK, o0, items.e[item],
+                       smem_u32(&ring.full[st]));
+      }
+      __syncwarp();
+    };
+    auto load_tokens = [&](int v, int st) {
+      const int item = v / per, k = v % per;
+      if (lane >= items.m[item]) return;
+      const uint32_t bytes = 2 * min(KC, a.I - k * KC);
+      const uint16_t* row = a.h + (size_t)(items.off[item] + lane) * a.I + k * KC;
+      uint8_t* to = tokens0 + st * kTokens + lane * PITCH;
+      async::bulk_load(to, row, bytes, &ring.full[st]);
+      async::bulk_load(to + M * PITCH, row + (size_t)a.T * a.K * a.I, bytes, &ring.full[st]);
+    };
+    const int ahead = min(a.stages, end - begin);
+    for (int v = 0; v < ahead; ++v) load_weights(begin + v, v);
+    griddep_wait();
+    for (int v = 0; v < ahead; ++v) load_tokens(begin + v, v);
+    s = ahead == a.stages ? 0 : ahead;
+    lap = ahead == a.stages ? 1 : 0;
+    bool ok = true;
+    for (int v = begin + ahead; v < end; ++v) {
+      if (!(ok = wait_warp(&ring.empty[s], (lap & 1) ^ 1))) break;
+      load_weights(v, s);
+      load_tokens(v, s);
+      if (++s == a.stages) s = 0, ++lap;
+    }
+    if (!ok) end_copies(ring, a.stages, s, lap);
+  } else {
+    // ---- products ----
+    const int seg = warp / RG, group = warp % RG, c = lane & 3;
+    const int box = seg >> 1, half = seg & 1;
+    const int kt = seg * (FP8 ? 64 : 32) + c * (FP8 ? 16 : 8);
+    const int hb = (a.H + 127) / 128, ib = (a.I + 127) / 128;
+    float fn = 0.f;
+    auto factors = [&](int item, int first, float& f) {
+      const int block = ((first + lane) * KC + seg * 64) / 128;
+      if (!FP8 || item >= items.n || first + lane >= per || block >= ib) return;
+      f = __ldg(a.w2_scales + ((size_t)items.e[item] * hb + o0 / 128) * ib + block);
+    };
+    if (begin < end) factors(begin / per, 0, fn);
+    bool ok = true;
+    for (int v = begin; v < end && ok;) {
+      const int item = v / per, m = items.m[item], n8 = (m + 7) / 8, off = items.off[item];
+      const int k0 = v % per, k1 = min(per, k0 + end - v);
+      float acc[2][NB][4] = {};
+      uint32_t nan[4] = {};
+      float f = fn;
+      factors(item + 1, 0, fn);
+      if (FP8 && k0 >= 32) factors(item, k0 & ~31, f);
+      for (int k = k0; k < k1; ++k) {
+        if (FP8 && k > k0 && (k & 31) == 0) factors(item, k, f);
+        const float sf = FP8 ? __shfl_sync(~0u, f, k & 31) : 1.f;
+        if (!(ok = wait_warp(&ring.full[s], lap & 1))) break;
+        multiply<T, FP8, NB, 2>(smem_u32(stage0 + s * kStageW + box * kRows * 128), 32 * group, 32 * group + 16, half,
+                                smem_u32(tokens0 + s * kTokens) + 2 * kt, PITCH, M * PITCH, k * KC + kt < a.I, n8, sf, sf,
+                                acc, nan);
+        async::release_slot(&ring.empty[s]);
+        if (++s == a.stages) s = 0, ++lap;
+      }
+      v += k1 - k0;
+      if (FP8 && T::kBf16) spread_nan(nan, acc);
+      // an item's tokens all differ, and a warp's rows are its own
+      const int row = 32 * group + fragment_row(lane >> 2);
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int j = 8 * n + 2 * c + i;
+          if (j >= m) continue;
+          const float wt = items.weight[off + j];
+          float* to = sums + (seg * a.T + items.tok[off + j]) * kLine + row;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) to[8 * r] = fmaf(wt, acc[r >> 1][n][2 * (r & 1) + i], to[8 * r]);
+        }
+    }
+  }
+  __syncthreads();
+  for (int v = threadIdx.x; v < a.T * kLine; v += kThreads) {
+    float t = sums[v];
+#pragma unroll
+    for (int q = 1; q < kSegs; ++q) t += sums[q * a.T * kLine + v];
+    sums[v] = t;
+  }
+  if (a.cluster > 1) cluster_sync();
+  else __syncthreads();
+  // The tile's results, shared out among the CTAs.
+  for (int v = rank * kThreads + threadIdx.x; v < a.T * kRows; v += a.cluster * kThreads) {
+    const int t = v / kRows, o = v % kRows;
+    float r = 0.f;
+    if (a.cluster > 1) {
+      for (int q = 0; q < a.cluster; ++q) {
+        float w;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w) : "r"(addr_in(smem_u32(sums + t * kLine + o), q)) : "memory");
+        r += w;
+      }
+    } else {
+      r = sums[t * kLine + o];
+    }
+    if (o0 + o >= a.H) continue;
+    const size_t at = (size_t)t * a.H + o0 + o;
+    if (a.out_f32) static_cast<float*>(a.y)[at] = r;
+    else static_cast<uint16_t*>(a.y)[at] = rounded<T>(r);
+  }
+  if (a.cluster > 1) cluster_sync();
+}
+
+// ---- host ----
+template <typename T, bool FP8, int NB, int RG>
+cudaError_t launch_t(LayerArgs a, const void* w13, const void* w2, cudaStream_t s) {
+  constexpr int kRows = 32 * RG, M = 8 * NB, PITCH = kPitch<FP8, RG>;
+  const MapType type = FP8 ? kMapU8 : T::kBf16 ? kMapBF16 : kMapF16;
+  const uint64_t es = FP8 ? 1 : 2, H = a.H, I = a.I, G = a.G;
+  CUtensorMap m13, m2;
+  {
+    const uint64_t d[] = {H, I, 2, G}, st[] = {es * H, es * I * H, es * 2 * I * H};
+    const uint32_t b[] = {(uint32_t)(128 / es), 16 * RG, 2, 1};
+    if (!make_map(&m13, w13, type, 4, d, st, b)) return cudaErrorUnknown;
+  }
+  {
+    const uint64_t d[] = {I, H, G}, st[] = {es * I, es * I * H};
+    const uint32_t b[] = {(uint32_t)(128 / es), (uint32_t)kRows, 1};
+    if (!make_map(&m2, w2, type, 3, d, st, b)) return cudaErrorUnknown;
+  }
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorUnknown;
+  constexpr int kPerSm = RG == 1 ? 2 : 1;  // CTAs a SM by shared memory
+  const size_t room = (227 * 1024) / kPerSm - sizeof(Items) - 2048;
+  auto fit = [&](size_t rest, size_t stage) {  // stages of the ring
+    return (int)std::min<size_t>(8, (room - 1024 - rest) / stage);
+  };
+  const size_t masks = 8 * (size_t)a.G;  // sort_pairs' scratch lies in the ring: 16 KB at most
+  cudaError_t e;
+  {
+    constexpr auto kernel = up_kernel<T, FP8, NB, RG>;
+    constexpr size_t stage = kStageW + M * PITCH, rest = 4 * 256 * (M + 1);
+    a.stages = fit(rest, stage);
+    const size_t smem = 1024 + a.stages * stage + rest;
+    if (a.stages < 2 || smem < masks) return cudaErrorInvalidValue;
+    if ((e = prepare_kernel<kernel>(smem)) != cudaSuccess) return e;
+    const int64_t most = (int64_t)std::min(a.G, a.T * a.K) * ((a.I + 16 * RG - 1) / (16 * RG)) * (a.T > M ? 2 : 1);
+    e = launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(most, sms * kPerSm)), dim3(kThreads), smem, s, a, m13);
+    if (e != cudaSuccess) return e;
+  }
+  {
+    constexpr auto kernel = down_kernel<T, FP8, NB, RG>;
+    constexpr size_t stage = kStageW + 2 * M * PITCH;
+    const size_t rest = 4 * (size_t)(8 / RG) * a.T * (kRows + 1);
+    a.stages = fit(rest, stage);
+    const size_t smem = 1024 + a.stages * stage + rest;
+    if (a.stages < 2 || smem < masks) return cudaErrorInvalidValue;
+    if ((e = prepare_kernel<kernel>(smem)) != cudaSuccess) return e;
+    const int tiles = (a.H + kRows - 1) / kRows;
+    a.cluster = 1;
+    while (a.cluster < 8 && tiles * a.cluster < 2 * sms) a.cluster *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tiles * a.cluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)a.cluster, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a, m2);
+  }
+}
+
+// Few tokens: small tiles, so that all SMs have work, two CTAs each. More tokens: tiles
+// of twice the rows, since every tile fetches its tokens' rows.
+template <typename T, bool FP8>
+cudaError_t launch(const LayerArgs& a, const void* w13, const void* w2, cudaStream_t s) {
+  if (a.T <= 8) return launch_t<T, FP8, 1, 1>(a, w13, w2, s);
+  if (a.T <= 16) return launch_t<T, FP8, 2, 2>(a, w13, w2, s);
+  return launch_t<T, FP8, 4, 2>(a, w13, w2, s);
 }
 
 int validate(const cq_moe_config* c) {
@@ -103,13 +626,6 @@ int validate(const cq_moe_config* c) {
 }
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-template <typename T, bool FP8>
-cudaError_t launch(const LayerArgs& a, cudaStream_t s) {
-  const dim3 g(152 * 8), b(256);
-  const cudaError_t e = launch_pdl(up_kernel<T, FP8>, g, b, 0, s, a);
-  return e == cudaSuccess ? launch_pdl(down_kernel<T, FP8>, g, b, 0, s, a) : e;
-}
 
 }  // namespace
 
@@ -159,16 +675,14 @@ int cq_moe_layer(const cq_moe_config* cfg, const void* x, const int32_t* expert_
   a.ids = expert_ids;
   a.scales = expert_scales;
   a.mask = x_active_mask;
-  a.w13 = w13;
   a.w13_scales = w13_scales;
-  a.w2 = w2;
   a.w2_scales = w2_scales;
-  a.h = static_cast<float*>(workspace);
+  a.h = static_cast<uint16_t*>(workspace);
   a.y = y;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = cfg->x_dtype == 1
-                            ? (cfg->w_dtype ? launch<cq::F16, true>(a, s) : launch<cq::F16, false>(a, s))
-                            : (cfg->w_dtype ? launch<cq::BF16, true>(a, s) : launch<cq::BF16, false>(a, s));
+                            ? (cfg->w_dtype ? launch<cq::F16, true>(a, w13, w2, s) : launch<cq::F16, false>(a, w13, w2, s))
+                            : (cfg->w_dtype ? launch<cq::BF16, true>(a, w13, w2, s) : launch<cq::BF16, false>(a, w13, w2, s));
   return e == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
 }
 

@@ -46,6 +46,13 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Shared-memory address in the cluster's CTA `rank` for one of this CTA.
+__device__ __forceinline__ uint32_t addr_in(uint32_t a, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+
 // Shared-memory address of the pair's CTA 0 (the leader) for one of this CTA.
 __device__ __forceinline__ uint32_t leader_addr(uint32_t a) {
   uint32_t r;
