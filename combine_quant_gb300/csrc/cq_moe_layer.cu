@@ -4,15 +4,15 @@
 // The weights of the experts that the tokens name are read once, and that is the bound:
 // both kernels stream them through a ring of shared memory (tiled copies by one warp)
 // and multiply on the way with mma.sync, whose 8 columns suit a few tokens and whose
-// rate a stream from memory does not reach. Eight warps take 64 bytes of a row each;
+// rate a stream from memory does not reach. Warps take 64 bytes of a row each;
 // with k in an order of the thread's choice (its 16 bytes of a row against the same 16
 // bytes of a token) one 16-byte load feeds two to four products.
 //
 // Every CTA sorts the (token, expert) pairs itself into items: an expert and up to 8 NB
 // of its tokens, ascending. A token that names an expert twice is one pair with both
-// weights. up_kernel: an item's tile of 16 (32) gates and their ups is one CTA's work;
+// weights. up_kernel: an item's tile of 16 (64) gates and their ups is one CTA's work;
 // its warps' shares of k are added in shared memory, in order. down_kernel: a tile of 32
-// (64) output rows is one cluster's work: the CTAs share the stages of all items evenly,
+// (128) output rows is one cluster's work: the CTAs share the stages of all items evenly,
 // each keeps the weighted sums of all tokens, and the CTAs' sums are added through
 // distributed shared memory, in order. Results do not depend on timing.
 //
@@ -51,14 +51,24 @@ struct LayerArgs {
   void* y;
 };
 
-constexpr int kWarps = 8;                 // that multiply; one more copies
-constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kStageW = 16384;            // weights of a stage
+// Row groups of 32 rows in a tile: 1, or 4. A stage is boxes of 32 RG rows of 128 bytes;
+// a warp takes a row group and half of a box. One more warp copies.
+template <int RG>
+constexpr int kBoxes = RG == 1 ? 4 : 2;
+template <int RG>
+constexpr int kSegs = 2 * kBoxes<RG>;
+template <int RG>
+constexpr int kWarps = kSegs<RG> * RG;
+template <int RG>
+constexpr int kThreads = 32 * (kWarps<RG> + 1);
+template <int RG>
+constexpr int kStageW = kBoxes<RG> * 32 * RG * 128;  // weights of a stage
+constexpr int kMaxWarps = kWarps<4> + 1;
 constexpr int kMaxPairs = 64 * 16, kMaxItems = kMaxPairs + 32;
 
-// A stage: 4 / RG boxes of 32 RG rows of 128 bytes; its k.
+// k of a stage.
 template <bool FP8, int RG>
-constexpr int kChunk = (FP8 ? 512 : 256) / RG;
+constexpr int kChunk = kBoxes<RG> * (FP8 ? 128 : 64);
 // Bytes from one token's part of a stage to the next: 16 bytes a thread from rows that
 // a quarter of a warp reads together must lie in different banks.
 template <bool FP8, int RG>
@@ -70,11 +80,11 @@ struct Items {
   uint8_t m[kMaxItems];         // pairs
   uint8_t tok[kMaxPairs];       // of each pair the token and its weight
   float weight[kMaxPairs];
-  int scan[2][kWarps + 1];
+  int scan[2][kMaxWarps];
 };
 
 // Sorts the pairs (all threads). `masks`: scratch of G 64-bit words.
-template <int PER>
+template <int PER, int kThreads>
 __device__ __forceinline__ void sort_pairs(const LayerArgs& a, Items& it, unsigned long long* masks, bool report) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, P = a.T * a.K;
   for (int e = t; e < a.G; e += kThreads) masks[e] = 0;
@@ -149,15 +159,16 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Four e4m3 codes as two words of 16-bit numbers, exactly. bf16: exponent and fraction
-// put where bf16 has them are the value times 2^-120 (also below the normal range).
+// Four e4m3 codes as two words of 16-bit numbers, exactly. bf16: a code with its sign
+// spread over the byte above it, shifted by four and cut to sign, exponent and fraction
+// where bf16 has them, is the value times 2^-120 (also below the normal range).
 template <typename T>
 __device__ __forceinline__ void decode4(uint32_t q, uint32_t& lo, uint32_t& hi) {
   if constexpr (T::kBf16) {
-    const uint32_t y = __byte_perm(q, 0, 0x1404), z = __byte_perm(q, 0, 0x3424);  // a code in each upper byte
-    lo = (y & 0x80008000u) | ((y >> 4) & 0x07f007f0u);
-    hi = (z & 0x80008000u) | ((z >> 4) & 0x07f007f0u);
     constexpr uint32_t k2to120 = 0x7b807b80u;
+    asm("prmt.b32 %0, %2, 0, 0x9180;\n prmt.b32 %1, %2, 0, 0xb3a2;" : "=&r"(lo), "=r"(hi) : "r"(q));
+    lo = (lo << 4) & 0x87f087f0u;
+    hi = (hi << 4) & 0x87f087f0u;
     asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(k2to120));
     asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(hi) : "r"(k2to120));
   } else {
@@ -260,11 +271,11 @@ struct Ring {
 };
 
 // The rings' start: barriers, and shared memory that sort_pairs used handed to the copies.
-__device__ __forceinline__ void init_ring(Ring& r, int stages) {
+__device__ __forceinline__ void init_ring(Ring& r, int stages, int warps) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&r.full[s], 1);
-      mbar_init(&r.empty[s], kWarps);
+      mbar_init(&r.empty[s], warps);
     }
     async::mbar_fence_init();
   }
@@ -291,30 +302,30 @@ __device__ __forceinline__ uint16_t rounded(float v) {
 
 // Gate and up products and SwiGLU. NB: token blocks of 8; RG: row groups.
 template <typename T, bool FP8, int NB, int RG>
-__global__ void __launch_bounds__(kThreads, RG == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads<RG>, RG == 1 ? 2 : 1)
 up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorMap map) {
-  constexpr int KC = kChunk<FP8, RG>, PITCH = kPitch<FP8, RG>, kSegs = 8 / RG, M = 8 * NB;
-  constexpr int kOuts = 16 * RG, kRows = 32 * RG, kBoxes = 4 / RG, kBoxK = KC / kBoxes;
-  constexpr int kStage = kStageW + M * PITCH;
+  constexpr int KC = kChunk<FP8, RG>, PITCH = kPitch<FP8, RG>, SEGS = kSegs<RG>, M = 8 * NB, WARPS = kWarps<RG>;
+  constexpr int kOuts = 16 * RG, kRows = 32 * RG, BOXES = kBoxes<RG>, kBoxK = KC / BOXES, SW = kStageW<RG>;
+  constexpr int kStage = SW + M * PITCH;
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Ring ring;
   __shared__ Items items;
   uint8_t* stage0 = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
   // weights of all stages (1024-byte aligned), then the tokens' parts, then the warps' sums
-  uint8_t* tokens0 = stage0 + a.stages * kStageW;
+  uint8_t* tokens0 = stage0 + a.stages * SW;
   float* red = reinterpret_cast<float*>(stage0 + a.stages * kStage);  // [segs][rows][M + 1]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  init_ring(ring, a.stages);
+  init_ring(ring, a.stages, WARPS);
   if (threadIdx.x == 0) prefetch_map(&map);
   griddep_wait();
   griddep_launch_dependents();  // the down kernel reads results only after its own wait
-  sort_pairs<M>(a, items, reinterpret_cast<unsigned long long*>(stage0), blockIdx.x == 0);
+  sort_pairs<M, kThreads<RG>>(a, items, reinterpret_cast<unsigned long long*>(stage0), blockIdx.x == 0);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
   const int tiles = (a.I + kOuts - 1) / kOuts, units = items.n * tiles;
   const int n_stages = (a.H + KC - 1) / KC;
   uint32_t s = 0, lap = 0;
-  if (warp == kWarps) {
+  if (warp == WARPS) {
     // ---- copies ----
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
@@ -324,9 +335,9 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
         if (lap > 0 && !(ok = wait_warp(&ring.empty[s], (lap & 1) ^ 1))) break;
         const uint32_t bytes = 2 * min(KC, a.H - k * KC);
         if (lane == 0) {
-          mbar_arrive_expect_tx(&ring.full[s], kStageW + m * bytes);
-          for (int b = 0; b < kBoxes; ++b)
-            tma_load4<1>(smem_u32(stage0 + s * kStageW + b * kRows * 128), &map, k * KC + b * kBoxK, i0, 0, items.e[item],
+          mbar_arrive_expect_tx(&ring.full[s], SW + m * bytes);
+          for (int b = 0; b < BOXES; ++b)
+            tma_load4<1>(smem_u32(stage0 + s * SW + b * kRows * 128), &map, k * KC + b * kBoxK, i0, 0, items.e[item],
                          smem_u32(&ring.full[s]));
         }
         __syncwarp();
@@ -363,7 +374,7 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
       if (FP8 && k > 0 && (k & 31) == 0) factors(u, k, g, w);
       const float sg = FP8 ? __shfl_sync(~0u, g, k & 31) : 1.f, su = FP8 ? __shfl_sync(~0u, w, k & 31) : 1.f;
       if (!(ok = wait_warp(&ring.full[s], lap & 1))) break;
-      multiply<T, FP8, NB, 1>(smem_u32(stage0 + s * kStageW + box * kRows * 128), 16 * group, kOuts + 16 * group, half,
+      multiply<T, FP8, NB, 1>(smem_u32(stage0 + s * SW + box * kRows * 128), 16 * group, kOuts + 16 * group, half,
                               smem_u32(tokens0 + s * M * PITCH) + 2 * kt, PITCH, 0, k * KC + kt < a.H, n8, sg, su, acc, nan);
       async::release_slot(&ring.empty[s]);
       if (++s == a.stages) s = 0, ++lap;
@@ -378,15 +389,15 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           red[(seg * kRows + row + 16 * f + 8 * (i >> 1)) * (M + 1) + 8 * n + 2 * c + (i & 1)] = acc[f][n][i];
-    if (!async::meet<32 * kWarps>(ok)) break;
+    if (!async::meet<32 * WARPS>(ok)) break;
     const int i0 = u % tiles * kOuts;
-    for (int v = threadIdx.x; v < kOuts * m; v += 32 * kWarps) {
+    for (int v = threadIdx.x; v < kOuts * m; v += 32 * WARPS) {
       const int o = v % kOuts, j = v / kOuts;
       if (i0 + o >= a.I) continue;
       const float* p = red + (32 * (o / 16) + o % 16) * (M + 1) + j;
       float pg = 0.f, pu = 0.f;
 #pragma unroll
-      for (int q = 0; q < kSegs; ++q) {
+      for (int q = 0; q < SEGS; ++q) {
         pg += p[q * kRows * (M + 1)];
         pu += p[(q * kRows + 16) * (M + 1)];
       }
@@ -398,44 +409,47 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
       // an infinite first number would make the second NaN
       to[(size_t)a.T * a.K * a.I] = rounded<T>(fabsf(T::lo(hi)) <= 3.402823466e38f ? lo : 0.f);
     }
-    if (!async::meet<32 * kWarps>(true)) break;
+    if (!async::meet<32 * WARPS>(true)) break;
   }
 }
 
 // Down product and weighted sum.
 template <typename T, bool FP8, int NB, int RG>
-__global__ void __launch_bounds__(kThreads, RG == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads<RG>, RG == 1 ? 2 : 1)
 down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorMap map) {
-  constexpr int KC = kChunk<FP8, RG>, PITCH = kPitch<FP8, RG>, kSegs = 8 / RG, M = 8 * NB;
-  constexpr int kRows = 32 * RG, kBoxes = 4 / RG, kBoxK = KC / kBoxes, kLine = kRows + 1;
+  constexpr int KC = kChunk<FP8, RG>, PITCH = kPitch<FP8, RG>, SEGS = kSegs<RG>, M = 8 * NB, WARPS = kWarps<RG>;
+  constexpr int kRows = 32 * RG, BOXES = kBoxes<RG>, kBoxK = KC / BOXES, kLine = kRows + 1, SW = kStageW<RG>;
   constexpr int kTokens = 2 * M * PITCH;  // both numbers
+  // Sums of every share of k, or (many tokens and rows) one that the shares add to in turn.
+  constexpr bool kTurns = RG > 1;
+  constexpr int kSums = kTurns ? 1 : SEGS;
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Ring ring;
   __shared__ Items items;
   uint8_t* stage0 = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
-  uint8_t* tokens0 = stage0 + a.stages * kStageW;
-  float* sums = reinterpret_cast<float*>(tokens0 + a.stages * kTokens);  // [segs][T][kLine]
+  uint8_t* tokens0 = stage0 + a.stages * SW;
+  float* sums = reinterpret_cast<float*>(tokens0 + a.stages * kTokens);  // [kSums][T][kLine]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = a.cluster > 1 ? (int)cluster_rank() : 0;
   const int o0 = blockIdx.x / a.cluster * kRows;
-  init_ring(ring, a.stages);
+  init_ring(ring, a.stages, WARPS);
   if (threadIdx.x == 0) prefetch_map(&map);
   // ids, mask and weights were complete before the up kernel let this one start
-  sort_pairs<M>(a, items, reinterpret_cast<unsigned long long*>(stage0), false);
-  for (int v = threadIdx.x; v < kSegs * a.T * kLine; v += kThreads) sums[v] = 0.f;
+  sort_pairs<M, kThreads<RG>>(a, items, reinterpret_cast<unsigned long long*>(stage0), false);
+  for (int v = threadIdx.x; v < kSums * a.T * kLine; v += kThreads<RG>) sums[v] = 0.f;
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
   const int per = (a.I + KC - 1) / KC, total = items.n * per;
   const int begin = (int)((int64_t)total * rank / a.cluster), end = (int)((int64_t)total * (rank + 1) / a.cluster);
   uint32_t s = 0, lap = 0;
-  if (warp == kWarps) {
+  if (warp == WARPS) {
     // ---- copies: weights of as many stages as the ring has before the wait for h ----
     auto load_weights = [&](int v, int st) {
       const int item = v / per, k = v % per;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&ring.full[st], kStageW + items.m[item] * 4 * min(KC, a.I - k * KC));
-        for (int b = 0; b < kBoxes; ++b)
-          tma_load3<1>(smem_u32(stage0 + st * kStageW + b * kRows * 128), &map, k * KC + b * kBoxK, o0, items.e[item],
+        mbar_arrive_expect_tx(&ring.full[st], SW + items.m[item] * 4 * min(KC, a.I - k * KC));
+        for (int b = 0; b < BOXES; ++b)
+          tma_load3<1>(smem_u32(stage0 + st * SW + b * kRows * 128), &map, k * KC + b * kBoxK, o0, items.e[item],
                        smem_u32(&ring.full[st]));
       }
       __syncwarp();
@@ -489,7 +503,7 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
         if (FP8 && k > k0 && (k & 31) == 0) factors(item, k, f);
         const float sf = FP8 ? __shfl_sync(~0u, f, k & 31) : 1.f;
         if (!(ok = wait_warp(&ring.full[s], lap & 1))) break;
-        multiply<T, FP8, NB, 2>(smem_u32(stage0 + s * kStageW + box * kRows * 128), 32 * group, 32 * group + 16, half,
+        multiply<T, FP8, NB, 2>(smem_u32(stage0 + s * SW + box * kRows * 128), 32 * group, 32 * group + 16, half,
                                 smem_u32(tokens0 + s * kTokens) + 2 * kt, PITCH, M * PITCH, k * KC + kt < a.I, n8, sf, sf,
                                 acc, nan);
         async::release_slot(&ring.empty[s]);
@@ -499,30 +513,42 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
       if (FP8 && T::kBf16) spread_nan(nan, acc);
       // an item's tokens all differ, and a warp's rows are its own
       const int row = 32 * group + fragment_row(lane >> 2);
+      auto add = [&] {
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int j = 8 * n + 2 * c + i;
-          if (j >= m) continue;
-          const float wt = items.weight[off + j];
-          float* to = sums + (seg * a.T + items.tok[off + j]) * kLine + row;
+          for (int i = 0; i < 2; ++i) {
+            const int j = 8 * n + 2 * c + i;
+            if (j >= m) continue;
+            const float wt = items.weight[off + j];
+            float* to = sums + ((kTurns ? 0 : seg * a.T) + items.tok[off + j]) * kLine + row;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) to[8 * r] = fmaf(wt, acc[r >> 1][n][2 * (r & 1) + i], to[8 * r]);
+            for (int r = 0; r < 4; ++r) to[8 * r] = fmaf(wt, acc[r >> 1][n][2 * (r & 1) + i], to[8 * r]);
+          }
+      };
+      if constexpr (kTurns) {
+        for (int q = 0; q < SEGS && ok; ++q) {
+          if (q == seg) add();
+          ok = async::meet<32 * WARPS>(ok);
         }
+      } else {
+        add();
+      }
     }
   }
   __syncthreads();
-  for (int v = threadIdx.x; v < a.T * kLine; v += kThreads) {
-    float t = sums[v];
+  if constexpr (!kTurns) {
+    for (int v = threadIdx.x; v < a.T * kLine; v += kThreads<RG>) {
+      float t = sums[v];
 #pragma unroll
-    for (int q = 1; q < kSegs; ++q) t += sums[q * a.T * kLine + v];
-    sums[v] = t;
+      for (int q = 1; q < SEGS; ++q) t += sums[q * a.T * kLine + v];
+      sums[v] = t;
+    }
   }
   if (a.cluster > 1) cluster_sync();
   else __syncthreads();
   // The tile's results, shared out among the CTAs.
-  for (int v = rank * kThreads + threadIdx.x; v < a.T * kRows; v += a.cluster * kThreads) {
+  for (int v = rank * kThreads<RG> + threadIdx.x; v < a.T * kRows; v += a.cluster * kThreads<RG>) {
     const int t = v / kRows, o = v % kRows;
     float r = 0.f;
     if (a.cluster > 1) {
@@ -570,19 +596,19 @@ cudaError_t launch_t(LayerArgs a, const void* w13, const void* w2, cudaStream_t 
   cudaError_t e;
   {
     constexpr auto kernel = up_kernel<T, FP8, NB, RG>;
-    constexpr size_t stage = kStageW + M * PITCH, rest = 4 * 256 * (M + 1);
+    constexpr size_t stage = kStageW<RG> + M * PITCH, rest = 4 * kSegs<RG> * kRows * (M + 1);
     a.stages = fit(rest, stage);
     const size_t smem = 1024 + a.stages * stage + rest;
     if (a.stages < 2 || smem < masks) return cudaErrorInvalidValue;
     if ((e = prepare_kernel<kernel>(smem)) != cudaSuccess) return e;
     const int64_t most = (int64_t)std::min(a.G, a.T * a.K) * ((a.I + 16 * RG - 1) / (16 * RG)) * (a.T > M ? 2 : 1);
-    e = launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(most, sms * kPerSm)), dim3(kThreads), smem, s, a, m13);
+    e = launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(most, sms * kPerSm)), dim3(kThreads<RG>), smem, s, a, m13);
     if (e != cudaSuccess) return e;
   }
   {
     constexpr auto kernel = down_kernel<T, FP8, NB, RG>;
-    constexpr size_t stage = kStageW + 2 * M * PITCH;
-    const size_t rest = 4 * (size_t)(8 / RG) * a.T * (kRows + 1);
+    constexpr size_t stage = kStageW<RG> + 2 * M * PITCH;
+    const size_t rest = 4 * (size_t)(RG > 1 ? 1 : kSegs<RG>) * a.T * (kRows + 1);
     a.stages = fit(rest, stage);
     const size_t smem = 1024 + a.stages * stage + rest;
     if (a.stages < 2 || smem < masks) return cudaErrorInvalidValue;
@@ -592,7 +618,7 @@ cudaError_t launch_t(LayerArgs a, const void* w13, const void* w2, cudaStream_t 
     while (a.cluster < 8 && tiles * a.cluster < 2 * sms) a.cluster *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(tiles * a.cluster);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreads<RG>);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -607,12 +633,12 @@ cudaError_t launch_t(LayerArgs a, const void* w13, const void* w2, cudaStream_t 
 }
 
 // Few tokens: small tiles, so that all SMs have work, two CTAs each. More tokens: tiles
-// of twice the rows, since every tile fetches its tokens' rows.
+// of four times the rows, since every tile fetches its tokens' rows, and sixteen warps.
 template <typename T, bool FP8>
 cudaError_t launch(const LayerArgs& a, const void* w13, const void* w2, cudaStream_t s) {
   if (a.T <= 8) return launch_t<T, FP8, 1, 1>(a, w13, w2, s);
-  if (a.T <= 16) return launch_t<T, FP8, 2, 2>(a, w13, w2, s);
-  return launch_t<T, FP8, 4, 2>(a, w13, w2, s);
+  if (a.T <= 16) return launch_t<T, FP8, 2, 4>(a, w13, w2, s);
+  return launch_t<T, FP8, 4, 4>(a, w13, w2, s);
 }
 
 int validate(const cq_moe_config* c) {
