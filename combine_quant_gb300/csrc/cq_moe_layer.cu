@@ -41,6 +41,7 @@ __device__ uint32_t g_status;  // CQ_ST_* bits of these kernels on this device
 struct LayerArgs {
   int32_t T, G, K, H, I, mask_ndim, out_f32;
   int32_t stages, cluster;   // of the ring; CTAs that share a tile (down_kernel)
+  int32_t whole;             // rows of x (h) are whole blocks of 64: one copy takes a stage's
   const uint16_t* x;
   const int32_t* ids;
   const float* scales;
@@ -63,41 +64,52 @@ template <int RG>
 constexpr int kThreads = 32 * (kWarps<RG> + 1);
 template <int RG>
 constexpr int kStageW = kBoxes<RG> * 32 * RG * 128;  // weights of a stage
+// Sums of every share of k, or (many tokens and rows) one that the shares add to in turn.
+template <int RG>
+constexpr bool kTurns = RG > 1;
 constexpr int kMaxWarps = kWarps<4> + 1;
 constexpr int kMaxPairs = 64 * 16, kMaxItems = kMaxPairs + 32;
 
 // k of a stage.
 template <bool FP8, int RG>
 constexpr int kChunk = kBoxes<RG> * (FP8 ? 128 : 64);
-// Bytes from one token's part of a stage to the next: 16 bytes a thread from rows that
-// a quarter of a warp reads together must lie in different banks.
+// Rows of 16-bit numbers lie in a stage as blocks of 64 of their k: 128-byte lines, the
+// block's rows one after the other, swizzled as the copies have it.
 template <bool FP8, int RG>
-constexpr int kPitch = 2 * kChunk<FP8, RG> + (FP8 ? 16 : 64);
+constexpr int kBlocks = kChunk<FP8, RG> / 64;
 
 struct Items {
   int n;                        // items
   uint16_t e[kMaxItems], off[kMaxItems];  // expert, first pair
   uint8_t m[kMaxItems];         // pairs
-  uint8_t tok[kMaxPairs];       // of each pair the token and its weight
+  uint8_t tok[kMaxPairs + 32];  // of each pair the token and its weight (zeros behind the last)
   float weight[kMaxPairs];
   int scan[2][kMaxWarps];
 };
 
-// Sorts the pairs (all threads). `masks`: scratch of G 64-bit words.
+// Sorts the pairs (all threads). `scratch`: 10 bytes an expert and 8 a pair.
 template <int PER, int kThreads>
-__device__ __forceinline__ void sort_pairs(const LayerArgs& a, Items& it, unsigned long long* masks, bool report) {
+__device__ __forceinline__ void sort_pairs(const LayerArgs& a, Items& it, uint8_t* scratch, bool report) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, P = a.T * a.K;
+  unsigned long long* masks = reinterpret_cast<unsigned long long*>(scratch);  // tokens of each expert
+  int* ids = reinterpret_cast<int*>(masks + a.G);
+  float* scales = reinterpret_cast<float*>(ids + P);
+  uint16_t* first = reinterpret_cast<uint16_t*>(scales + P);  // pair of each expert
   for (int e = t; e < a.G; e += kThreads) masks[e] = 0;
+  for (int p = t; p < P + 32; p += kThreads) it.tok[p] = 0;
   __syncthreads();
-  auto id_of = [&](int p) {  // or -1
-    if (a.mask_ndim && !a.mask[a.mask_ndim == 1 ? p / a.K : p]) return -1;
-    const int e = a.ids[p];
-    return (unsigned)e < (unsigned)a.G ? e : -2;
-  };
   for (int p = t; p < P; p += kThreads) {
-    const int e = id_of(p);
+    int e = -1;
+    if (!a.mask_ndim || a.mask[a.mask_ndim == 1 ? p / a.K : p]) {
+      e = a.ids[p];
+      if ((unsigned)e >= (unsigned)a.G) {
+        if (report) atomicOr(&g_status, (uint32_t)CQ_ST_BAD_ID);
+        e = -1;
+      }
+    }
+    ids[p] = e;
+    scales[p] = a.scales[p];
     if (e >= 0) atomicOr(masks + e, 1ull << (p / a.K));
-    else if (e == -2 && report) atomicOr(&g_status, (uint32_t)CQ_ST_BAD_ID);
   }
   __syncthreads();
   const int per = (a.G + kThreads - 1) / kThreads, e0 = min(a.G, t * per), e1 = min(a.G, e0 + per);
@@ -117,24 +129,31 @@ __device__ __forceinline__ void sort_pairs(const LayerArgs& a, Items& it, unsign
   int p0 = rp - pairs, i0 = ri - items;
   for (int w = 0; w < warp; ++w) p0 += it.scan[0][w], i0 += it.scan[1][w];
   for (int e = e0; e < e1; ++e) {
-    unsigned long long m = masks[e];
-    int left = __popcll(m);
-    for (; left > 0; left -= PER, ++i0) {
-      const int c = min(left, PER);
+    first[e] = (uint16_t)p0;
+    for (int left = __popcll(masks[e]); left > 0; left -= PER, ++i0) {
       it.e[i0] = (uint16_t)e;
       it.off[i0] = (uint16_t)p0;
-      it.m[i0] = (uint8_t)c;
-      for (int k = 0; k < c; ++k, ++p0, m &= m - 1) {
-        const int tok = __ffsll((long long)m) - 1;
-        float w = 0.f;
-        for (int j = 0; j < a.K; ++j)
-          if (id_of(tok * a.K + j) == e) w += a.scales[tok * a.K + j];
-        it.tok[p0] = (uint8_t)tok;
-        it.weight[p0] = w;
-      }
+      it.m[i0] = (uint8_t)min(left, PER);
+      p0 += min(left, PER);
     }
   }
   if (t == kThreads - 1) it.n = i0;
+  __syncthreads();
+  for (int p = t; p < P; p += kThreads) {
+    const int e = ids[p], tok = p / a.K;
+    if (e < 0) continue;
+    float w = 0.f;
+    bool before = false;
+    for (int j = tok * a.K; j < tok * a.K + a.K; ++j) {
+      if (ids[j] != e) continue;
+      before |= j < p;
+      w += scales[j];
+    }
+    if (before) continue;
+    const int at = first[e] + __popcll(masks[e] & ((1ull << tok) - 1));
+    it.tok[at] = (uint8_t)tok;
+    it.weight[at] = w;
+  }
   __syncthreads();
 }
 
@@ -144,19 +163,27 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   return v;
 }
 
-template <typename T>
+// d += a b, or (FIRST) d = a b.
+template <typename T, bool FIRST>
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                       uint32_t b1) {
-  if constexpr (T::kBf16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
-        "%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
-        "%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+#define CQ_MMA(type)                                                                                              \
+  if constexpr (FIRST)                                                                                            \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." type "." type                                                     \
+        ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"                                  \
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                                             \
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));                                            \
+  else                                                                                                            \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." type "." type                                                     \
+        ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"                                      \
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                                             \
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1))
+  if constexpr (T::kBf16) {
+    CQ_MMA("bf16");
+  } else {
+    CQ_MMA("f16");
+  }
+#undef CQ_MMA
 }
 
 // Four e4m3 codes as two words of 16-bit numbers, exactly. bf16: a code with its sign
@@ -182,14 +209,23 @@ __device__ __forceinline__ void decode4(uint32_t q, uint32_t& lo, uint32_t& hi) 
 // a warp reads together differ in bit 2, which the swizzle turns into the other 64 bytes.
 __device__ __forceinline__ int fragment_row(int g) { return ((g & 1) << 2) | (g >> 1); }
 
+// The token of a block of 8 that column j of a fragment stands for, for the same reason
+// (fp8 weights take 32 bytes of a token's line, where neighbouring rows do not meet).
+template <bool FP8>
+__device__ __forceinline__ int fragment_column(int j) {
+  return FP8 ? j : fragment_row(j);
+}
+
 // Two fragments of 16 rows (at r0, r1 of a box) times up to 8 NB tokens over this warp's
-// 64 bytes of the rows. `b`: shared address of token 0's part for this thread's column
-// group; PARTS: the tokens' numbers are sums of PARTS numbers. `in`: the thread's k exist.
-// FP8: s0, s1 are the fragments' factors here; nan collects codes that are NaN (bf16,
-// whose decoding does not know them): bit 7 of a byte, by fragment and upper rows.
+// 64 bytes of the rows. `lines`: shared address of the tokens' lines of this k, row[n] the
+// line of this thread's token of block n. PARTS: the tokens' numbers are sums of so many,
+// part_bytes apart. FP8: s0, s1 are the fragments' factors here; nan collects codes that
+// are NaN (bf16, whose decoding does not know them): bit 7 of a byte, by fragment and
+// upper rows.
 template <typename T, bool FP8, int NB, int PARTS>
-__device__ __forceinline__ void multiply(uint32_t box, int r0, int r1, int half, uint32_t b, int pitch, int part_bytes, bool in,
-                                         int n8, float s0, float s1, float (&acc)[2][NB][4], uint32_t (&nan)[4]) {
+__device__ __forceinline__ void multiply(uint32_t box, int r0, int r1, int half, uint32_t lines, const int (&token)[NB],
+                                         int part_bytes, int n8, float s0, float s1, float (&acc)[2][NB][4],
+                                         uint32_t (&nan)[4]) {
   const int lane = threadIdx.x & 31, row = fragment_row(lane >> 2), c = lane & 3;
   const uint32_t piece = ((half * 4 + c) ^ row) << 4;
   uint4 w[2][2];
@@ -204,36 +240,43 @@ __device__ __forceinline__ void multiply(uint32_t box, int r0, int r1, int half,
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const uint32_t q[4] = {w[f][u].x, w[f][u].y, w[f][u].z, w[f][u].w};
-      if constexpr (FP8) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (T::kBf16) nan[2 * f + u] |= (q[k] & 0x7f7f7f7fu) + 0x01010101u;
-          decode4<T>(q[k], v[f][u][2 * k], v[f][u][2 * k + 1]);
-        }
-      } else {
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (FP8) decode4<T>(q[k], v[f][u][2 * k], v[f][u][2 * k + 1]);
+        else v[f][u][k] = q[k];
+      }
+      if constexpr (FP8 && T::kBf16) {
+        uint32_t t[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[f][u][k] = q[k];
+        for (int k = 0; k < 4; ++k) t[k] = (q[k] & 0x7f7f7f7fu) + 0x01010101u;
+        nan[2 * f + u] |= (t[0] | t[1] | t[2]) | t[3];
       }
     }
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
     if (n >= n8) break;
-    float sum[2][4] = {};
+    float sum[2][4];
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
-      const uint32_t at = b + (8 * n + (lane >> 2)) * pitch + p * part_bytes;
+      const uint32_t line = lines + token[n] * 128 + p * part_bytes;
       uint32_t x[2 * kSteps];
 #pragma unroll
       for (int k = 0; k < kSteps / 2; ++k) {
-        const uint4 t = in ? lds16(at + 16 * k) : make_uint4(0, 0, 0, 0);
+        const int at = FP8 ? 2 * c + k : half * 4 + c;
+        const uint4 t = lds16(line + ((at ^ (token[n] & 7)) << 4));
         x[4 * k] = t.x, x[4 * k + 1] = t.y, x[4 * k + 2] = t.z, x[4 * k + 3] = t.w;
       }
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
-          mma16<T>(FP8 ? sum[f] : acc[f][n], v[f][0][2 * k], v[f][1][2 * k], v[f][0][2 * k + 1], v[f][1][2 * k + 1],
-                   x[2 * k], x[2 * k + 1]);
+        for (int f = 0; f < 2; ++f) {
+          const uint32_t(&q)[2][2 * kSteps] = v[f];
+          if (FP8 && p == 0 && k == 0)
+            mma16<T, true>(sum[f], q[0][0], q[1][0], q[0][1], q[1][1], x[0], x[1]);
+          else
+            mma16<T, false>(FP8 ? sum[f] : acc[f][n], q[0][2 * k], q[1][2 * k], q[0][2 * k + 1], q[1][2 * k + 1], x[2 * k],
+                            x[2 * k + 1]);
+        }
     }
     if constexpr (FP8) {
 #pragma unroll
@@ -270,6 +313,12 @@ struct Ring {
   uint64_t full[8], empty[8];
 };
 
+struct TokenMaps {
+  CUtensorMap rows8, rows16, rows32;
+};
+// Lines that an item of m pairs is copied as.
+__device__ __forceinline__ int lines_of(int m) { return m <= 8 ? 8 : m <= 16 ? 16 : 32; }
+
 // The rings' start: barriers, and shared memory that sort_pairs used handed to the copies.
 __device__ __forceinline__ void init_ring(Ring& r, int stages, int warps) {
   if (threadIdx.x == 0) {
@@ -303,23 +352,24 @@ __device__ __forceinline__ uint16_t rounded(float v) {
 // Gate and up products and SwiGLU. NB: token blocks of 8; RG: row groups.
 template <typename T, bool FP8, int NB, int RG>
 __global__ void __launch_bounds__(kThreads<RG>, RG == 1 ? 2 : 1)
-up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorMap map) {
-  constexpr int KC = kChunk<FP8, RG>, PITCH = kPitch<FP8, RG>, SEGS = kSegs<RG>, M = 8 * NB, WARPS = kWarps<RG>;
+up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorMap map,
+          const __grid_constant__ CUtensorMap map_x) {
+  constexpr int KC = kChunk<FP8, RG>, BLOCKS = kBlocks<FP8, RG>, SEGS = kSegs<RG>, M = 8 * NB, WARPS = kWarps<RG>;
   constexpr int kOuts = 16 * RG, kRows = 32 * RG, BOXES = kBoxes<RG>, kBoxK = KC / BOXES, SW = kStageW<RG>;
-  constexpr int kStage = SW + M * PITCH;
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Ring ring;
   __shared__ Items items;
   uint8_t* stage0 = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
   // weights of all stages (1024-byte aligned), then the tokens' parts, then the warps' sums
+  const int lines = (a.T + 7) / 8 * 8, kTokens = BLOCKS * lines * 128;  // all tokens' lines
   uint8_t* tokens0 = stage0 + a.stages * SW;
-  float* red = reinterpret_cast<float*>(stage0 + a.stages * kStage);  // [segs][rows][M + 1]
+  float* red = reinterpret_cast<float*>(tokens0 + a.stages * kTokens);  // [segs][rows][M + 1]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   init_ring(ring, a.stages, WARPS);
   if (threadIdx.x == 0) prefetch_map(&map);
   griddep_wait();
   griddep_launch_dependents();  // the down kernel reads results only after its own wait
-  sort_pairs<M, kThreads<RG>>(a, items, reinterpret_cast<unsigned long long*>(stage0), blockIdx.x == 0);
+  sort_pairs<M, kThreads<RG>>(a, items, stage0, blockIdx.x == 0);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
   const int tiles = (a.I + kOuts - 1) / kOuts, units = items.n * tiles;
@@ -329,19 +379,21 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
     // ---- copies ----
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      const int item = u / tiles, i0 = u % tiles * kOuts, m = items.m[item];
-      const uint16_t* row = a.x + (size_t)items.tok[items.off[item] + min(lane, m - 1)] * a.H;
+      const int item = u / tiles, i0 = u % tiles * kOuts;
       for (int k = 0; k < n_stages; ++k) {
         if (lap > 0 && !(ok = wait_warp(&ring.empty[s], (lap & 1) ^ 1))) break;
-        const uint32_t bytes = 2 * min(KC, a.H - k * KC);
         if (lane == 0) {
-          mbar_arrive_expect_tx(&ring.full[s], SW + m * bytes);
+          const uint32_t bar = smem_u32(&ring.full[s]), to = smem_u32(tokens0 + s * kTokens);
+          mbar_arrive_expect_tx(&ring.full[s], SW + kTokens);
           for (int b = 0; b < BOXES; ++b)
-            tma_load4<1>(smem_u32(stage0 + s * SW + b * kRows * 128), &map, k * KC + b * kBoxK, i0, 0, items.e[item],
-                         smem_u32(&ring.full[s]));
+            tma_load4<1>(smem_u32(stage0 + s * SW + b * kRows * 128), &map, k * KC + b * kBoxK, i0, 0, items.e[item], bar);
+          if (a.whole) {
+            tma_load3<1>(to, &map_x, 0, 0, k * BLOCKS, bar);
+          } else {
+            for (int b = 0; b < BLOCKS; ++b) tma_load3<1>(to + b * lines * 128, &map_x, k * KC + b * 64, 0, 0, bar);
+          }
         }
         __syncwarp();
-        if (lane < m) async::bulk_load(tokens0 + s * M * PITCH + lane * PITCH, row + k * KC, bytes, &ring.full[s]);
         if (++s == a.stages) s = 0, ++lap;
       }
     }
@@ -351,7 +403,6 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
   // ---- products ----
   const int seg = warp / RG, group = warp % RG, c = lane & 3;
   const int box = seg >> 1, half = seg & 1;
-  const int kt = seg * (FP8 ? 64 : 32) + c * (FP8 ? 16 : 8);  // this thread's first k of a stage
   const int kb = (a.H + 127) / 128, ib = (a.I + 127) / 128;
   // FP8: factors of 32 stages, a lane each; those of the next unit are read ahead
   float gn = 0.f, un = 0.f;
@@ -368,6 +419,9 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
     const int item = u / tiles, m = items.m[item], n8 = (m + 7) / 8, off = items.off[item];
     float acc[2][NB][4] = {};
     uint32_t nan[4] = {};
+    int token[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) token[n] = items.tok[off + 8 * n + fragment_column<FP8>(lane >> 2)];
     float g = gn, w = un;
     factors(u + gridDim.x, 0, gn, un);
     for (int k = 0; k < n_stages; ++k) {
@@ -375,21 +429,35 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
       const float sg = FP8 ? __shfl_sync(~0u, g, k & 31) : 1.f, su = FP8 ? __shfl_sync(~0u, w, k & 31) : 1.f;
       if (!(ok = wait_warp(&ring.full[s], lap & 1))) break;
       multiply<T, FP8, NB, 1>(smem_u32(stage0 + s * SW + box * kRows * 128), 16 * group, kOuts + 16 * group, half,
-                              smem_u32(tokens0 + s * M * PITCH) + 2 * kt, PITCH, 0, k * KC + kt < a.H, n8, sg, su, acc, nan);
+                              smem_u32(tokens0 + s * kTokens + (FP8 ? seg : box) * lines * 128), token, 0, n8, sg, su, acc, nan);
       async::release_slot(&ring.empty[s]);
       if (++s == a.stages) s = 0, ++lap;
     }
     if (FP8 && T::kBf16) spread_nan(nan, acc);
-    // the warps' shares: red[seg][row][token]
+    // the warps' shares: red[seg][row][token], or one sum that they add to in turn
     const int row = 32 * group + fragment_row(lane >> 2);
+    auto put = [&](bool first) {
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+      for (int f = 0; f < 2; ++f)
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          red[(seg * kRows + row + 16 * f + 8 * (i >> 1)) * (M + 1) + 8 * n + 2 * c + (i & 1)] = acc[f][n][i];
-    if (!async::meet<32 * WARPS>(ok)) break;
+          for (int i = 0; i < 4; ++i) {
+            float* to = red + ((kTurns<RG> ? 0 : seg * kRows) + row + 16 * f + 8 * (i >> 1)) * (M + 1) + 8 * n +
+                        fragment_column<FP8>(2 * c + (i & 1));
+            *to = first ? acc[f][n][i] : *to + acc[f][n][i];
+          }
+    };
+    if constexpr (kTurns<RG>) {
+      for (int q = 0; q < SEGS && ok; ++q) {
+        if (q == seg) put(q == 0);
+        ok = async::meet<32 * WARPS>(ok);
+      }
+    } else {
+      put(true);
+      ok = async::meet<32 * WARPS>(ok);
+    }
+    if (!ok) break;
     const int i0 = u % tiles * kOuts;
     for (int v = threadIdx.x; v < kOuts * m; v += 32 * WARPS) {
       const int o = v % kOuts, j = v / kOuts;
@@ -397,7 +465,7 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
       const float* p = red + (32 * (o / 16) + o % 16) * (M + 1) + j;
       float pg = 0.f, pu = 0.f;
 #pragma unroll
-      for (int q = 0; q < SEGS; ++q) {
+      for (int q = 0; q < (kTurns<RG> ? 1 : SEGS); ++q) {
         pg += p[q * kRows * (M + 1)];
         pu += p[(q * kRows + 16) * (M + 1)];
       }
@@ -416,13 +484,12 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
 // Down product and weighted sum.
 template <typename T, bool FP8, int NB, int RG>
 __global__ void __launch_bounds__(kThreads<RG>, RG == 1 ? 2 : 1)
-down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorMap map) {
-  constexpr int KC = kChunk<FP8, RG>, PITCH = kPitch<FP8, RG>, SEGS = kSegs<RG>, M = 8 * NB, WARPS = kWarps<RG>;
+down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorMap map,
+            const __grid_constant__ TokenMaps map_h) {
+  constexpr int KC = kChunk<FP8, RG>, BLOCKS = kBlocks<FP8, RG>, SEGS = kSegs<RG>, M = 8 * NB, WARPS = kWarps<RG>;
   constexpr int kRows = 32 * RG, BOXES = kBoxes<RG>, kBoxK = KC / BOXES, kLine = kRows + 1, SW = kStageW<RG>;
-  constexpr int kTokens = 2 * M * PITCH;  // both numbers
-  // Sums of every share of k, or (many tokens and rows) one that the shares add to in turn.
-  constexpr bool kTurns = RG > 1;
-  constexpr int kSums = kTurns ? 1 : SEGS;
+  constexpr int kTokens = BLOCKS * 2 * M * 128;  // both numbers' lines
+  constexpr int kSums = kTurns<RG> ? 1 : SEGS;
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Ring ring;
   __shared__ Items items;
@@ -435,7 +502,7 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
   init_ring(ring, a.stages, WARPS);
   if (threadIdx.x == 0) prefetch_map(&map);
   // ids, mask and weights were complete before the up kernel let this one start
-  sort_pairs<M, kThreads<RG>>(a, items, reinterpret_cast<unsigned long long*>(stage0), false);
+  sort_pairs<M, kThreads<RG>>(a, items, stage0, false);
   for (int v = threadIdx.x; v < kSums * a.T * kLine; v += kThreads<RG>) sums[v] = 0.f;
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
@@ -447,21 +514,26 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
     auto load_weights = [&](int v, int st) {
       const int item = v / per, k = v % per;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&ring.full[st], SW + items.m[item] * 4 * min(KC, a.I - k * KC));
+        mbar_arrive_expect_tx(&ring.full[st], SW + BLOCKS * 2 * 128 * lines_of(items.m[item]));
         for (int b = 0; b < BOXES; ++b)
           tma_load3<1>(smem_u32(stage0 + st * SW + b * kRows * 128), &map, k * KC + b * kBoxK, o0, items.e[item],
                        smem_u32(&ring.full[st]));
       }
       __syncwarp();
     };
-    auto load_tokens = [&](int v, int st) {
-      const int item = v / per, k = v % per;
-      if (lane >= items.m[item]) return;
-      const uint32_t bytes = 2 * min(KC, a.I - k * KC);
-      const uint16_t* row = a.h + (size_t)(items.off[item] + lane) * a.I + k * KC;
-      uint8_t* to = tokens0 + st * kTokens + lane * PITCH;
-      async::bulk_load(to, row, bytes, &ring.full[st]);
-      async::bulk_load(to + M * PITCH, row + (size_t)a.T * a.K * a.I, bytes, &ring.full[st]);
+    auto load_tokens = [&](int v, int st) {  // an item's rows of h lie together
+      const int item = v / per, k = v % per, rows = lines_of(items.m[item]);
+      const CUtensorMap* from = rows == 8 ? &map_h.rows8 : rows == 16 ? &map_h.rows16 : &map_h.rows32;
+      const uint32_t to = smem_u32(tokens0 + st * kTokens), bar = smem_u32(&ring.full[st]);
+      if (lane == 0) {
+        if (a.whole) {
+          tma_load4<1>(to, from, 0, items.off[item], 0, k * BLOCKS, bar);
+        } else {
+          for (int b = 0; b < BLOCKS; ++b)
+            tma_load4<1>(to + b * 2 * rows * 128, from, k * KC + b * 64, items.off[item], 0, 0, bar);
+        }
+      }
+      __syncwarp();
     };
     const int ahead = min(a.stages, end - begin);
     for (int v = 0; v < ahead; ++v) load_weights(begin + v, v);
@@ -481,7 +553,9 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
     // ---- products ----
     const int seg = warp / RG, group = warp % RG, c = lane & 3;
     const int box = seg >> 1, half = seg & 1;
-    const int kt = seg * (FP8 ? 64 : 32) + c * (FP8 ? 16 : 8);
+    int token[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) token[n] = 8 * n + fragment_column<FP8>(lane >> 2);
     const int hb = (a.H + 127) / 128, ib = (a.I + 127) / 128;
     float fn = 0.f;
     auto factors = [&](int item, int first, float& f) {
@@ -493,7 +567,7 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
     bool ok = true;
     for (int v = begin; v < end && ok;) {
       const int item = v / per, m = items.m[item], n8 = (m + 7) / 8, off = items.off[item];
-      const int k0 = v % per, k1 = min(per, k0 + end - v);
+      const int k0 = v % per, k1 = min(per, k0 + end - v), part = lines_of(m) * 128;
       float acc[2][NB][4] = {};
       uint32_t nan[4] = {};
       float f = fn;
@@ -504,8 +578,7 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
         const float sf = FP8 ? __shfl_sync(~0u, f, k & 31) : 1.f;
         if (!(ok = wait_warp(&ring.full[s], lap & 1))) break;
         multiply<T, FP8, NB, 2>(smem_u32(stage0 + s * SW + box * kRows * 128), 32 * group, 32 * group + 16, half,
-                                smem_u32(tokens0 + s * kTokens) + 2 * kt, PITCH, M * PITCH, k * KC + kt < a.I, n8, sf, sf,
-                                acc, nan);
+                                smem_u32(tokens0 + s * kTokens + (FP8 ? seg : box) * 2 * part), token, part, n8, sf, sf, acc, nan);
         async::release_slot(&ring.empty[s]);
         if (++s == a.stages) s = 0, ++lap;
       }
@@ -518,15 +591,15 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
         for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int j = 8 * n + 2 * c + i;
+            const int j = 8 * n + fragment_column<FP8>(2 * c + i);
             if (j >= m) continue;
             const float wt = items.weight[off + j];
-            float* to = sums + ((kTurns ? 0 : seg * a.T) + items.tok[off + j]) * kLine + row;
+            float* to = sums + ((kTurns<RG> ? 0 : seg * a.T) + items.tok[off + j]) * kLine + row;
 #pragma unroll
             for (int r = 0; r < 4; ++r) to[8 * r] = fmaf(wt, acc[r >> 1][n][2 * (r & 1) + i], to[8 * r]);
           }
       };
-      if constexpr (kTurns) {
+      if constexpr (kTurns<RG>) {
         for (int q = 0; q < SEGS && ok; ++q) {
           if (q == seg) add();
           ok = async::meet<32 * WARPS>(ok);
@@ -537,7 +610,7 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
     }
   }
   __syncthreads();
-  if constexpr (!kTurns) {
+  if constexpr (!kTurns<RG>) {
     for (int v = threadIdx.x; v < a.T * kLine; v += kThreads<RG>) {
       float t = sums[v];
 #pragma unroll
@@ -571,10 +644,11 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
 // ---- host ----
 template <typename T, bool FP8, int NB, int RG>
 cudaError_t launch_t(LayerArgs a, const void* w13, const void* w2, cudaStream_t s) {
-  constexpr int kRows = 32 * RG, M = 8 * NB, PITCH = kPitch<FP8, RG>;
+  constexpr int kRows = 32 * RG, M = 8 * NB, BLOCKS = kBlocks<FP8, RG>;
   const MapType type = FP8 ? kMapU8 : T::kBf16 ? kMapBF16 : kMapF16;
   const uint64_t es = FP8 ? 1 : 2, H = a.H, I = a.I, G = a.G;
-  CUtensorMap m13, m2;
+  CUtensorMap m13, m2, mx;
+  TokenMaps mh;
   {
     const uint64_t d[] = {H, I, 2, G}, st[] = {es * H, es * I * H, es * 2 * I * H};
     const uint32_t b[] = {(uint32_t)(128 / es), 16 * RG, 2, 1};
@@ -585,6 +659,27 @@ cudaError_t launch_t(LayerArgs a, const void* w13, const void* w2, cudaStream_t 
     const uint32_t b[] = {(uint32_t)(128 / es), (uint32_t)kRows, 1};
     if (!make_map(&m2, w2, type, 3, d, st, b)) return cudaErrorUnknown;
   }
+  const MapType token = T::kBf16 ? kMapBF16 : kMapF16;
+  const uint32_t lines = (a.T + 7) / 8 * 8;
+  const bool whole_x = H % 64 == 0, whole_h = I % 64 == 0;
+  {
+    const uint64_t d[] = {whole_x ? 64 : H, (uint64_t)a.T, whole_x ? H / 64 : 1}, st[] = {2 * H, whole_x ? 128 : 2 * H * a.T};
+    const uint32_t b[] = {64, lines, whole_x ? (uint32_t)BLOCKS : 1};
+    if (!make_map(&mx, a.x, token, 3, d, st, b)) return cudaErrorUnknown;
+  }
+  {
+    const uint64_t P = (uint64_t)a.T * a.K, d[] = {whole_h ? 64 : I, P, 2, whole_h ? I / 64 : 1};
+    const uint64_t st[] = {2 * I, 2 * I * P, whole_h ? 128 : 4 * I * P};
+    CUtensorMap* const to[] = {&mh.rows8, &mh.rows16, &mh.rows32};
+    for (int k = 0; k < 3; ++k) {
+      if (8 << k > M) {
+        *to[k] = mh.rows8;
+        continue;
+      }
+      const uint32_t b[] = {64, 8u << k, 2, whole_h ? (uint32_t)BLOCKS : 1};
+      if (!make_map(to[k], a.h, token, 4, d, st, b)) return cudaErrorUnknown;
+    }
+  }
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorUnknown;
   constexpr int kPerSm = RG == 1 ? 2 : 1;  // CTAs a SM by shared memory
@@ -592,26 +687,29 @@ cudaError_t launch_t(LayerArgs a, const void* w13, const void* w2, cudaStream_t 
   auto fit = [&](size_t rest, size_t stage) {  // stages of the ring
     return (int)std::min<size_t>(8, (room - 1024 - rest) / stage);
   };
-  const size_t masks = 8 * (size_t)a.G;  // sort_pairs' scratch lies in the ring: 16 KB at most
+  const size_t scratch = 10 * (size_t)a.G + 8 * (size_t)(a.T * a.K);  // sort_pairs', in the ring: 29 KB at most
   cudaError_t e;
   {
     constexpr auto kernel = up_kernel<T, FP8, NB, RG>;
-    constexpr size_t stage = kStageW<RG> + M * PITCH, rest = 4 * kSegs<RG> * kRows * (M + 1);
+    constexpr size_t rest = 4 * (kTurns<RG> ? 1 : kSegs<RG>) * kRows * (M + 1);
+    const size_t stage = kStageW<RG> + BLOCKS * lines * 128;
     a.stages = fit(rest, stage);
+    a.whole = whole_x;
     const size_t smem = 1024 + a.stages * stage + rest;
-    if (a.stages < 2 || smem < masks) return cudaErrorInvalidValue;
+    if (a.stages < 2 || smem < scratch + 1024) return cudaErrorInvalidValue;
     if ((e = prepare_kernel<kernel>(smem)) != cudaSuccess) return e;
     const int64_t most = (int64_t)std::min(a.G, a.T * a.K) * ((a.I + 16 * RG - 1) / (16 * RG)) * (a.T > M ? 2 : 1);
-    e = launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(most, sms * kPerSm)), dim3(kThreads<RG>), smem, s, a, m13);
+    e = launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(most, sms * kPerSm)), dim3(kThreads<RG>), smem, s, a, m13, mx);
     if (e != cudaSuccess) return e;
   }
   {
     constexpr auto kernel = down_kernel<T, FP8, NB, RG>;
-    constexpr size_t stage = kStageW<RG> + 2 * M * PITCH;
-    const size_t rest = 4 * (size_t)(RG > 1 ? 1 : kSegs<RG>) * a.T * (kRows + 1);
+    constexpr size_t stage = kStageW<RG> + BLOCKS * 2 * M * 128;
+    const size_t rest = 4 * (size_t)(kTurns<RG> ? 1 : kSegs<RG>) * a.T * (kRows + 1);
     a.stages = fit(rest, stage);
+    a.whole = whole_h;
     const size_t smem = 1024 + a.stages * stage + rest;
-    if (a.stages < 2 || smem < masks) return cudaErrorInvalidValue;
+    if (a.stages < 2 || smem < scratch + 1024) return cudaErrorInvalidValue;
     if ((e = prepare_kernel<kernel>(smem)) != cudaSuccess) return e;
     const int tiles = (a.H + kRows - 1) / kRows;
     a.cluster = 1;
@@ -628,7 +726,7 @@ cudaError_t launch_t(LayerArgs a, const void* w13, const void* w2, cudaStream_t 
     attr[1].val.clusterDim = {(unsigned)a.cluster, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, a, m2);
+    return cudaLaunchKernelEx(&cfg, kernel, a, m2, mh);
   }
 }
 
