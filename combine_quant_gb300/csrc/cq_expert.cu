@@ -143,7 +143,7 @@ int cq_read_expert_status(uint32_t* status, void* stream) {
   if (!status) return CQ_ERR_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint32_t all = 0;
-  for (auto read : {gemm_status, w4_status, b128_status, layer_status}) {
+  for (auto read : {gemm_status, w4_status, b128_status, layer_status, norm_status}) {
     uint32_t v = 0;
     const int rc = read(&v, s);
     if (rc != CQ_OK) return rc;

@@ -158,6 +158,7 @@ int gemm_status(uint32_t* status, cudaStream_t s);
 int w4_status(uint32_t* status, cudaStream_t s);
 int b128_status(uint32_t* status, cudaStream_t s);
 int layer_status(uint32_t* status, cudaStream_t s);
+int norm_status(uint32_t* status, cudaStream_t s);
 
 }  // namespace expert
 }  // namespace cq

@@ -1,9 +1,13 @@
 // cq_norm.cu -- the norm before the layer with the residual's addition and the
 // rows in fp8 or int8 (norm_kernel), and its gradient (grad_kernel, sum_kernel).
 //
-// A block takes a row; a thread holds two units of 16 columns, as the permute
-// kernels do, and quantises them with their code (cq_permute_impl.cuh), so that
-// codes and scales follow dispatch's rules exactly.
+// Both read and write each value once, and that bounds them. norm_kernel: a block takes
+// a row; a thread holds two units of 16 columns, as the permute kernels do, and
+// quantises them with their code (cq_permute_impl.cuh), so that codes and scales follow
+// dispatch's rules exactly. grad_kernel: persistent blocks, rows by bulk copies into a
+// ring of shared memory, so that the next rows are on their way while two sums over a
+// row wait at a barrier; a thread keeps one unit and its columns' share of dw.
+#include "cq_expert.cuh"
 #include "cq_permute_impl.cuh"
 
 namespace cq {
@@ -12,7 +16,12 @@ namespace {
 
 using namespace permute_detail;
 
-constexpr int kMaxParts = 304;  // partial sums of dw: at most so many blocks (two per SM)
+// grad_kernel's blocks: 8192 columns a SM, which holds up to 8 of them; each leaves a row
+// of partial sums of dw.
+constexpr int kSms = 152, kMaxStages = 8;
+constexpr int kRing = 200 * 1024;  // bytes of a SM's rings
+
+__device__ uint32_t g_status;  // CQ_ST_TIMEOUT of grad_kernel on this device
 
 struct NormArgs {
   int32_t H, norm;
@@ -28,7 +37,7 @@ struct NormArgs {
 };
 
 struct GradArgs {
-  int32_t R, H;
+  int32_t R, H, stages;
   float eps;
   const uint16_t* dy;
   const uint16_t* x;
@@ -153,111 +162,132 @@ __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ NormA
 
 // dx, and each block's share of dw: rows blockIdx.x, + gridDim.x, ...
 template <class T>
-__global__ void __launch_bounds__(256) grad_kernel(const __grid_constant__ GradArgs a) {
-  __shared__ float sums[4][8];
-  const int nt = blockDim.x;
-  griddep_wait();
-  float w[2][16], dw[2][16];
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int u = threadIdx.x + q * nt;
-#pragma unroll
-    for (int t = 0; t < 16; ++t) w[q][t] = 1.f, dw[q][t] = 0.f;
-    if (a.weight && 16 * u < a.H) {
-      uint4 v[2];
-      load_unit(a.weight, u, v);
-      unpack16<T>(v, w[q]);
-    }
+__global__ void __launch_bounds__(512) grad_kernel(const __grid_constant__ GradArgs a) {
+  extern __shared__ __align__(128) uint8_t ring[];  // [stages][x, dy, dsum][H]
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ float sums[3][2][16];
+  const int nt = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool mine = 16 * threadIdx.x < a.H;
+  const uint32_t line = 2 * a.H, entry = (a.dsum ? 3 : 2) * line;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1);
+    mbar_fence_init();
   }
-  for (int row = blockIdx.x; row < a.R; row += gridDim.x) {
+  __syncthreads();
+  griddep_wait();
+  auto load = [&](int row, int s) {
+    uint8_t* to = ring + s * entry;
     const size_t at = (size_t)row * a.H;
-    float x[2][16], d[2][16];
-    float ss = 0.f, sd = 0.f;
+    mbar_arrive_expect_tx(&full[s], entry);
+    bulk_load(to, a.x + at, line, &full[s]);
+    bulk_load(to + line, a.dy + at, line, &full[s]);
+    if (a.dsum) bulk_load(to + 2 * line, a.dsum + at, line, &full[s]);
+  };
+  if (threadIdx.x == 0)
+    for (int s = 0; s < a.stages && blockIdx.x + s * gridDim.x < a.R; ++s) load(blockIdx.x + s * gridDim.x, s);
+  uint4 wv[2] = {};
+  if (a.weight && mine) load_unit(a.weight, threadIdx.x, wv);
+  float dw[16] = {};
+  int s = 0, lap = 0, turn = 0;
+  bool ok = true;
+  for (int row = blockIdx.x; row < a.R; row += gridDim.x) {
+    ok = mbar_wait_warp(&full[s], lap & 1);
+    uint4 xv[2] = {}, dv[2] = {}, sv[2] = {};
+    if (ok && mine) {
+      const uint8_t* from = ring + s * entry + 32 * threadIdx.x;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int u = threadIdx.x + q * nt;
-#pragma unroll
-      for (int t = 0; t < 16; ++t) x[q][t] = d[q][t] = 0.f;
-      if (16 * u >= a.H) continue;
-      uint4 v[2];
-      load_unit(a.x + at, u, v);
-      unpack16<T>(v, x[q]);
-      load_unit(a.dy + at, u, v);
-      unpack16<T>(v, d[q]);
-#pragma unroll
-      for (int t = 0; t < 16; ++t) {
-        ss = fmaf(x[q][t], x[q][t], ss);
-        sd = fmaf(d[q][t] * w[q][t], x[q][t], sd);
+      for (int k = 0; k < 2; ++k) {
+        xv[k] = ld_shared_v4(from + 16 * k);
+        dv[k] = ld_shared_v4(from + line + 16 * k);
+        if (a.dsum) sv[k] = ld_shared_v4(from + 2 * line + 16 * k);
       }
     }
-    __syncthreads();
-    ss = block_sum(ss, sums[0], nt);
-    sd = block_sum(sd, sums[1], nt);
-    float r = 1.f;
-    const float m = square_scale(ss, a.eps);
-    if (m != 1.f) {
+    float x[16], d[16], w[16];
+    unpack16<T>(xv, x);
+    unpack16<T>(dv, d);
+    if (a.weight) {
+      unpack16<T>(wv, w);
+    } else {
+#pragma unroll
+      for (int t = 0; t < 16; ++t) w[t] = 1.f;
+    }
+    // sums of (x m)^2 and dy w (x m) over the row, the same in every thread
+    auto reduce = [&](float m, float& ss, float& sd, float (&buf)[2][16], bool& go) {
       ss = sd = 0.f;
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int t = 0; t < 16; ++t) {
+        const float v = x[t] * m;
+        ss = fmaf(v, v, ss);
+        sd = fmaf(d[t] * w[t], v, sd);
+      }
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
-          ss = fmaf(x[q][t] * m, x[q][t] * m, ss);
-          sd = fmaf(d[q][t] * w[q][t], x[q][t] * m, sd);
-        }
-      ss = block_sum(ss, sums[2], nt);
-      sd = block_sum(sd, sums[3], nt);
+      for (int o = 16; o; o >>= 1) {
+        ss += __shfl_xor_sync(kFull, ss, o);
+        sd += __shfl_xor_sync(kFull, sd, o);
+      }
+      if (lane == 0) buf[0][warp] = ss, buf[1][warp] = sd;
+      go = __syncthreads_and(go);
+      ss = sd = 0.f;
+      for (int k = 0; k < (nt >> 5); ++k) ss += buf[0][k], sd += buf[1][k];
+    };
+    // this thread's reads of the row come before the copy that follows into its place
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    float ss, sd;
+    reduce(1.f, ss, sd, sums[turn], ok);
+    if (!ok) break;  // in every thread
+    turn ^= 1;
+    if (threadIdx.x == 0) {
+      const int64_t next = row + (int64_t)a.stages * gridDim.x;
+      if (next < a.R) load((int)next, s);
+    }
+    if (++s == a.stages) s = 0, ++lap;
+    const float m = square_scale(ss, a.eps);
+    if (m != 1.f) {
+      bool all = true;
+      __syncthreads();  // sums[2] of an earlier row is read
+      reduce(m, ss, sd, sums[2], all);
     }
     // with xs = x m: x r = xs rs, and r^2 x mean(dy w x) = xs rs * (rs mean(dy w xs))
-    const float rs = 1.f / sqrtf(ss / a.H + a.eps * m * m);
-    r = m * rs;
-    const float c = rs * (sd / a.H);
+    const float rs = 1.f / sqrtf(ss / a.H + a.eps * m * m), r = m * rs, c = rs * (sd / a.H);
+    float o[16], e[16];
+    unpack16<T>(sv, e);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int u = threadIdx.x + q * nt;
-      if (16 * u >= a.H) continue;
-      float o[16];
-#pragma unroll
-      for (int t = 0; t < 16; ++t) {
-        const float hat = x[q][t] * m * rs;
-        dw[q][t] = fmaf(d[q][t], hat, dw[q][t]);
-        o[t] = r * (d[q][t] * w[q][t] - hat * c);
-      }
-      if (a.dsum) {
-        uint4 v[2];
-        float s[16];
-        load_unit(a.dsum + at, u, v);
-        unpack16<T>(v, s);
-#pragma unroll
-        for (int t = 0; t < 16; ++t) o[t] += s[t];
-      }
-      store_unit<T>(a.dx + at, u, o);
+    for (int t = 0; t < 16; ++t) {
+      const float hat = x[t] * m * rs;
+      dw[t] = fmaf(d[t], hat, dw[t]);
+      o[t] = r * (d[t] * w[t] - hat * c) + e[t];
     }
+    if (mine) store_unit<T>(a.dx + (size_t)row * a.H, threadIdx.x, o);
   }
-  if (!a.part) return;
+  if (!ok) {
+    if (threadIdx.x == 0) {  // copies in flight land (with a limit) before the block goes
+      atomicOr(&g_status, (uint32_t)CQ_ST_TIMEOUT);
+      for (int k = 0; k < a.stages; ++k) mbar_wait(&full[(s + k) % a.stages], (lap + (s + k) / a.stages) & 1);
+    }
+    return;
+  }
+  if (a.part && mine) {
+    float4* to = reinterpret_cast<float4*>(a.part + (size_t)blockIdx.x * a.H + 16 * threadIdx.x);
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int u = threadIdx.x + q * nt;
-    if (16 * u >= a.H) continue;
-    float4* to = reinterpret_cast<float4*>(a.part + (size_t)blockIdx.x * a.H + 16 * u);
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      to[t] = make_float4(dw[q][4 * t], dw[q][4 * t + 1], dw[q][4 * t + 2], dw[q][4 * t + 3]);
+    for (int t = 0; t < 4; ++t) to[t] = make_float4(dw[4 * t], dw[4 * t + 1], dw[4 * t + 2], dw[4 * t + 3]);
   }
 }
 
-// dw[h] = the blocks' shares, eight runs of them each in order, then the runs in order.
-__global__ void __launch_bounds__(256) sum_kernel(const float* part, float* dw, int parts, int H) {
-  __shared__ float s[8][32];
+// dw[h] = the blocks' shares: 32 runs of them each in order, then the runs in order.
+__global__ void __launch_bounds__(1024) sum_kernel(const float* part, float* dw, int parts, int H) {
+  __shared__ float s[32][33];
   const int c = threadIdx.x & 31, g = threadIdx.x >> 5, h = blockIdx.x * 32 + c;
   griddep_wait();
   float v = 0.f;
-  const int per = (parts + 7) / 8;
-  if (h < H)
+  const int per = (parts + 31) / 32;
+  if (h < H) {
+#pragma unroll 8
     for (int p = g * per; p < min(parts, (g + 1) * per); ++p) v += part[(size_t)p * H + h];
+  }
   s[g][c] = v;
   __syncthreads();
   if (g == 0 && h < H) {
-    for (int k = 1; k < 8; ++k) v += s[k][c];
+    for (int k = 1; k < 32; ++k) v += s[k][c];
     dw[h] = v;
   }
 }
@@ -292,10 +322,34 @@ cudaError_t launch_norm(int q, const NormArgs& a, int rows, cudaStream_t s) {
   }
 }
 
-int parts_of(const cq_norm_config* c) { return c->rows < kMaxParts ? c->rows : kMaxParts; }
+// grad_kernel's blocks a SM, and in all.
+int per_sm(const cq_norm_config* c) {
+  const int n = 8192 / c->hidden;
+  return n < 1 ? 1 : n > 8 ? 8 : n;
+}
+int parts_of(const cq_norm_config* c) {
+  const int n = kSms * per_sm(c);
+  return c->rows < n ? c->rows : n;
+}
+
+template <class T>
+cudaError_t launch_grad(GradArgs a, int parts, int per, cudaStream_t s) {
+  constexpr auto kernel = grad_kernel<T>;
+  const int entry = (a.dsum ? 3 : 2) * 2 * a.H;
+  a.stages = kRing / per / entry;
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
+  const size_t smem = (size_t)a.stages * entry;
+  const cudaError_t e = cq::prepare_kernel<kernel>(smem);
+  if (e != cudaSuccess) return e;
+  return cq::launch_pdl(kernel, dim3(parts), dim3((a.H / 16 + 31) / 32 * 32), smem, s, a);
+}
 
 }  // namespace
 }  // namespace norm
+
+namespace expert {
+int norm_status(uint32_t* status, cudaStream_t s) { return read_status_word(norm::g_status, status, s); }
+}  // namespace expert
 }  // namespace cq
 
 using namespace cq::norm;
@@ -370,12 +424,10 @@ int cq_norm_grad(const cq_norm_config* cfg, const void* dy, const void* x, const
   a.dsum = static_cast<const uint16_t*>(dsum);
   a.dx = static_cast<uint16_t*>(dx);
   a.part = dw ? static_cast<float*>(workspace) : nullptr;
-  const int parts = parts_of(cfg);
-  const dim3 g(parts), b(threads_for(a.H));
-  cudaError_t e = cfg->x_dtype == 1 ? cq::launch_pdl(grad_kernel<cq::F16>, g, b, 0, s, a)
-                                    : cq::launch_pdl(grad_kernel<cq::BF16>, g, b, 0, s, a);
+  const int parts = parts_of(cfg), per = per_sm(cfg);
+  cudaError_t e = cfg->x_dtype == 1 ? launch_grad<cq::F16>(a, parts, per, s) : launch_grad<cq::BF16>(a, parts, per, s);
   if (e == cudaSuccess && dw)
-    e = cq::launch_pdl(sum_kernel, dim3((a.H + 31) / 32), dim3(256), 0, s, a.part, dw, parts, a.H);
+    e = cq::launch_pdl(sum_kernel, dim3((a.H + 31) / 32), dim3(1024), 0, s, a.part, dw, parts, a.H);
   return e == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
 }
 

@@ -90,7 +90,7 @@ def norm(x, residual, weight, eps):
     return s, v, NORM / 2 + 8 * 2.0 ** -24
 
 
-def norm_grad(dy, x, weight, dsum, eps, dtype, parts=304):
+def norm_grad(dy, x, weight, dsum, eps, dtype):
     x, dy = x.double(), dy.double()
     w = weight.double() if weight is not None else torch.ones(x.shape[1], dtype=torch.float64)
     r = 1 / torch.sqrt((x * x).mean(1, keepdim=True) + eps)
@@ -103,7 +103,7 @@ def norm_grad(dy, x, weight, dsum, eps, dtype, parts=304):
         dx, b = dx + dsum.double(), b + 2.0 ** -24 * (dx + dsum.double()).abs()
     dw = (dy * x * r).sum(0)
     rows = x.shape[0]
-    # each block's rows in order, eight runs of blocks, the runs: that many additions
-    steps = (rows + parts - 1) // parts + (min(rows, parts) + 7) // 8 + 8
+    # each block's rows in order, 32 runs of blocks, the runs: that many additions. 152 to 1216 blocks, at most one a row
+    steps = (rows + 151) // 152 + (min(rows, 1216) + 31) // 32 + 32
     bw = (steps * 2.0 ** -24 + NORM + 4 * 2.0 ** -24) * (dy * x * r).abs().sum(0)
     return dx, ref.rounded(dx, b, dtype), dw, bw + 1e-30
