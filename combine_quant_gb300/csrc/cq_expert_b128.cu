@@ -51,7 +51,6 @@ struct B128Args : Args {
   int32_t half_len;     // the contraction's length, dx: of one half
   int32_t out_cols;     // columns of the result: n, or (dx) k
   int32_t tiles_i;
-  int32_t vec;          // rows of xs are whole 16-byte pieces
   int32_t wide;         // rows of the results (and of saved products) are whole 32-byte pieces
 };
 
@@ -65,6 +64,10 @@ constexpr int kThreads = 128 + 32 * kDrainWarps;
 // sums and need 224, the others 56, which is the same total.
 constexpr int kOtherRegs = 56, kDrainRegs = 224;
 static_assert(128 * kOtherRegs + 32 * kDrainWarps * kDrainRegs <= 168 * kThreads, "setmaxnreg would wait forever");
+constexpr int kFew = 128;                  // most rows of a tile with tokens on the columns
+constexpr int kEntry = 4;                  // blocks in an entry of the scales' ring
+constexpr int kScaleRing = 4;
+constexpr int kScaleFloats = kEntry * 128 + kEntry * 2;  // the rows', and two of the weights
 constexpr uint32_t kTmemCols = 512;
 constexpr int kBand = 8;                   // tiles along i taken together, for reuse in L2
 
@@ -75,6 +78,7 @@ struct RowMaps {
 struct Bars {
   uint64_t full[kStages], empty[kStages];
   uint64_t tfull[2], tempty[2];
+  uint64_t sfull[kScaleRing], sempty[kScaleRing];
   uint64_t top[4];  // fp8 results: the largest values of a quarter's two warps
   uint64_t done;    // the products in flight when their warp gave up
   uint32_t tmem;
@@ -82,11 +86,13 @@ struct Bars {
 
 struct Tile {
   int e, row0, rows;  // first token row and rows of the tile
-  int i0, cols;       // first output and accumulator columns (of B, both CTAs)
+  int i0, cols;       // first output and weight rows (both CTAs)
+  bool few;           // tokens on the accumulator's columns
+  int jh;             // tokens of the first CTA
 };
 
 // GATES: a tile is 128 outputs, else 256. Columns in steps of 64 (16 outputs a CTA) or 32.
-template <bool GATES>
+template <bool GATES, bool OUT8>
 __device__ __forceinline__ Tile tile_at(const B128Args& a, const int* s_begin, const int* s_tile, int t) {
   Tile x;
   x.e = expert_of(s_tile, a.G, t);
@@ -103,6 +109,9 @@ __device__ __forceinline__ Tile tile_at(const B128Args& a, const int* s_begin, c
   x.i0 = ti * kOuts;
   const int outs = (min(kOuts, a.out_cols - x.i0) + 31) / 32 * 32;
   x.cols = GATES ? 2 * outs : outs;
+  x.few = !OUT8 && x.rows <= kFew;
+  x.jh = (x.rows + 1) / 2;
+  if (x.few) x.jh = (x.jh + 7) / 8 * 8;
   return x;
 }
 
@@ -127,6 +136,22 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
 __device__ __forceinline__ void add_scaled(const uint32_t (&v)[32], Pair sg, Pair su, Pair (&acc)[16]) {
 #pragma unroll
   for (int k = 0; k < 16; ++k) acc[k] = fma2(pair_of(v[2 * k], v[2 * k + 1]), k < 8 ? sg : su, acc[k]);
+}
+
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ void ld_pairs(uint32_t addr, Pair& a, Pair& b) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void copy4_async(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// An arrival on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void arrive_on_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // 32 bytes to or from global memory: one access, or two where a row need not begin
@@ -189,7 +214,8 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
   __shared__ Bars bars;
   __shared__ float s_top[OUT8 && kGates ? 2 * 2 * 128 : 1];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
-  int* s_begin = reinterpret_cast<int*>(ring + kStages * kStageBytes);
+  float* s_scales = reinterpret_cast<float*>(ring + kStages * kStageBytes);
+  int* s_begin = reinterpret_cast<int*>(s_scales + kScaleRing * kScaleFloats);
   int* s_tile = s_begin + a.G + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -206,6 +232,10 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
       mbar_init(&bars.tempty[b], kDrainWarps * 2);
     }
     for (int q = 0; q < 4; ++q) mbar_init(&bars.top[q], 2);
+    for (int s = 0; s < kScaleRing; ++s) {
+      mbar_init(&bars.sfull[s], 64);
+      mbar_init(&bars.sempty[s], kDrainWarps);
+    }
     mbar_init(&bars.done, 1);
     async::mbar_fence_init();
   }
@@ -238,9 +268,9 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
       uint32_t s = 0, lap = 0;  // stage, times the ring has gone round
       bool ok = true;
       for (int t = first; t < n_tiles && ok; t += step) {
-        const Tile x = tile_at<kGates>(a, s_begin, s_tile, t);
+        const Tile x = tile_at<kGates, OUT8>(a, s_begin, s_tile, t);
         // tokens: each CTA its half, in copies of 128 rows, 64, 32, or 64 + 32
-        const int jh = (x.rows + 1) / 2, row = x.row0 + (int)rank * jh;
+        const int jh = x.jh, row = x.row0 + (int)rank * jh;
         const bool b128 = jh > 96, b64 = !b128 && jh > 32, b32 = !b128 && (jh <= 32 || jh > 64);
         const uint32_t bytes = kABytes + (b128 ? 16384 : (b64 ? 8192 : 0) + (b32 ? 4096 : 0));
         const int i = x.i0 + (int)rank * x.cols / (kGates ? 4 : 2);  // this CTA's half of the columns
@@ -281,8 +311,11 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
       uint32_t s = 0, lap = 0, buf = 0;
       bool ok = true;
       for (int t = first; t < n_tiles && ok; t += step) {
-        const Tile x = tile_at<kGates>(a, s_begin, s_tile, t);
-        const uint32_t idesc = idesc_fp8(a.x_dtype == kMxE5M2, a.w_dtype, DX, 256, x.cols);
+        const Tile x = tile_at<kGates, OUT8>(a, s_begin, s_tile, t);
+        const int xf = a.x_dtype == kMxE5M2, wf = a.w_dtype;
+        const uint32_t idesc = x.few ? idesc_fp8(wf, xf, DX, false, 256, 2 * x.jh) : idesc_fp8(xf, wf, false, DX, 256, x.cols);
+        const uint64_t first_op = x.few ? db : da, second_op = x.few ? da : db;
+        const uint32_t k1 = x.few ? kbs : ka, k2 = x.few ? ka : kbs;
         int left = a.half_len;
         for (int kb = 0; kb < a.blocks; ++kb) {
           const uint32_t b = buf & 1, use = buf >> 1;
@@ -291,15 +324,15 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
           if (!(ok = wait(&bars.full[s], lap & 1))) break;
           fence_after();
           if (elect_one()) {
-            const uint64_t ad = da + s * (kStageBytes >> 4), bd = db + s * (kStageBytes >> 4);
+            const uint64_t ad = first_op + s * (kStageBytes >> 4), bd = second_op + s * (kStageBytes >> 4);
             const uint32_t d = tmem + b * kNT;
             if (left > 96) {
               mma_fp8(d, ad, bd, idesc, false);
-              mma_fp8(d, ad + ka, bd + kbs, idesc, true);
-              mma_fp8(d, ad + 2 * ka, bd + 2 * kbs, idesc, true);
-              mma_fp8(d, ad + 3 * ka, bd + 3 * kbs, idesc, true);
+              mma_fp8(d, ad + k1, bd + k2, idesc, true);
+              mma_fp8(d, ad + 2 * k1, bd + 2 * k2, idesc, true);
+              mma_fp8(d, ad + 3 * k1, bd + 3 * k2, idesc, true);
             } else {
-              for (int q = 0; 32 * q < left; ++q) mma_fp8(d, ad + q * ka, bd + q * kbs, idesc, q > 0);
+              for (int q = 0; 32 * q < left; ++q) mma_fp8(d, ad + q * k1, bd + q * k2, idesc, q > 0);
             }
             commit(smem_u32(&bars.empty[s]));
             commit(smem_u32(&bars.tfull[b]));
@@ -315,50 +348,145 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
         __syncwarp();
         wait_pair(&bars.done, 0);
       }
+    } else if (warp >= 2) {
+      // ---- scales, four blocks an entry: of this CTA's tokens (tokens on the columns: of all),
+      // and of the weights the two blocks of columns, or gates' and ups'. What is not there
+      // keeps what the memory held: no stored result meets it ----
+      const int l64 = (warp - 2) * 32 + lane;
+      const uint32_t base = smem_u32(s_scales);
+      uint32_t s = 0, lap = 0;
+      bool ok = true;
+      for (int t = first; t < n_tiles && ok; t += step) {
+        const Tile x = tile_at<kGates, OUT8>(a, s_begin, s_tile, t);
+        const int j0 = x.few ? 0 : (int)rank * x.jh, rows = x.few ? x.rows : rank ? x.rows - x.jh : x.jh;
+        const float* xs = a.xs + (size_t)(x.row0 + j0 + l64) * a.blocks;
+        const int k = lane >> 1, which = lane & 1, ib = x.i0 / 128 + (kGates ? 0 : which);
+        const bool weights = warp == 2 && lane < 2 * kEntry && ib * 128 < a.out_cols;
+        const float* ws = DX ? a.ws + ((size_t)x.e * a.blocks + k) * a.kb + ib
+                             : a.ws + ((size_t)x.e * (kGates ? 2 * a.nb : a.nb) + (kGates ? which * a.nb : 0) + ib) * a.kb + k;
+        for (int b0 = 0; b0 < a.blocks; b0 += kEntry) {
+          if (lap > 0 && !(ok = wait(&bars.sempty[s], (lap & 1) ^ 1))) break;
+          const uint32_t to = base + s * kScaleFloats * 4;
+          const int nb = min(kEntry, a.blocks - b0);
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            if (l64 + 64 * m < rows)
+              for (int c = 0; c < nb; ++c)
+                copy4_async(to + (c * 128 + l64 + 64 * m) * 4, xs + (size_t)(64 * m) * a.blocks + b0 + c);
+          if (weights && k < nb) copy4_async(to + (kEntry * 128 + lane) * 4, ws + (size_t)b0 * (DX ? a.kb : 1));
+          arrive_on_copies(&bars.sfull[s]);
+          if (++s == kScaleRing) s = 0, ++lap;
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
     // ---- scaled sums, and results ----
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDrainRegs));
     const int q = warp & 3, half = (warp - 4) >> 2;
     const bool wide = a.wide;
-    uint32_t buf = 0, nth = 0;  // nth: tiles so far
-    // Factors of four blocks, read four blocks ahead: the row's, and the weights' in
-    // lanes 0-3 (with SwiGLU the ups' in lanes 4-7).
-    float4 xn = {};
-    float wn = 0.f;
-    auto fetch = [&](const Tile& x, int b0) {
-      const int jh = (x.rows + 1) / 2, j = min((int)rank * jh + 32 * q + lane, x.rows - 1);
-      const float* p = a.xs + (size_t)(x.row0 + j) * a.blocks + b0;
-      const int left = a.blocks - b0;
-      if (a.vec) {
-        xn = __ldg(reinterpret_cast<const float4*>(p));
-      } else {
-        xn.x = __ldg(p);
-        if (left > 1) xn.y = __ldg(p + 1);
-        if (left > 2) xn.z = __ldg(p + 2);
-        if (left > 3) xn.w = __ldg(p + 3);
-      }
-      const int k = lane & 3, which = lane >> 2;
-      wn = 0.f;
-      if (k >= left) return;
-      if constexpr (kGates) {
-        if (which < 2) wn = __ldg(a.ws + ((size_t)x.e * 2 * a.nb + which * a.nb + x.i0 / 128) * a.kb + b0 + k);
-      } else {
-        const int ib = x.i0 / 128 + half;  // the block of this warp's columns
-        if (which == 0 && ib * 128 < a.out_cols)
-          wn = __ldg(DX ? a.ws + ((size_t)x.e * a.blocks + b0 + k) * a.kb + ib
-                        : a.ws + ((size_t)x.e * a.nb + ib) * a.kb + b0 + k);
-      }
-    };
+    uint32_t buf = 0, se = 0, se_lap = 0, nth = 0;  // nth: tiles so far
+    // what a warp does for every block is kept short: longer code is fetched too slowly
+    const uint32_t release[2] = {lead(&bars.tempty[0]), lead(&bars.tempty[1])};
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     bool ok = true;
-    Tile x = {}, next = {};
-    if (first < n_tiles) {
-      next = tile_at<kGates>(a, s_begin, s_tile, first);
-      fetch(next, 0);
-    }
     for (int t = first; t < n_tiles && ok; t += step) {
-      x = next;
-      const int jh = (x.rows + 1) / 2, rows = rank ? x.rows - jh : jh;  // of this CTA
+      const Tile x = tile_at<kGates, OUT8>(a, s_begin, s_tile, t);
+      if (!OUT8 && x.few) {
+        // ---- tokens on the columns, weight rows on the lanes ----
+        const int c0 = half * x.jh, chunks = (x.jh + 15) / 16;  // this warp's columns, 16 a chunk
+        Pair sum[4][8];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sum[m][k] = 0;
+        const int l = 32 * q + lane;
+        // this lane's of an entry's two weights
+        const int which = kGates ? lane >> 4 : (x.i0 + (int)rank * x.cols / 2 + l) / 128 - x.i0 / 128;
+        for (int b0 = 0; b0 < a.blocks && ok; b0 += kEntry) {
+          if (!(ok = wait(&bars.sfull[se], se_lap & 1))) break;
+          const float* sc = s_scales + se * kScaleFloats;
+          const int nb = min(kEntry, a.blocks - b0);
+#pragma unroll 1
+          for (int k = 0; k < nb; ++k) {
+            const uint32_t b = buf & 1;
+            const float w = sc[kEntry * 128 + 2 * k + which];
+            const Pair pw = pair_of(w, w);
+            const uint32_t xs = smem_u32(sc + k * 128 + c0), src = lanes + b * kNT + c0;
+            if (!(ok = wait(&bars.tfull[b], (buf >> 1) & 1))) break;
+            ++buf;
+            fence_after();
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {  // 32 columns
+              if (2 * m >= chunks) break;
+              uint32_t v[32];
+              tmem_ld32(src + 32 * m, v);
+              tmem_wait();
+              if (2 * m + 2 >= chunks) {  // the accumulator is read
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster_relaxed(release[b]);
+              }
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (2 * m + h >= chunks) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  Pair s0, s1;
+                  ld_pairs(xs + (32 * m + 16 * h + 4 * i) * 4, s0, s1);
+                  Pair(&to)[8] = sum[2 * m + h];
+                  to[2 * i] = fma2(pair_of(v[16 * h + 4 * i], v[16 * h + 4 * i + 1]), mul2(s0, pw), to[2 * i]);
+                  to[2 * i + 1] = fma2(pair_of(v[16 * h + 4 * i + 2], v[16 * h + 4 * i + 3]), mul2(s1, pw), to[2 * i + 1]);
+                }
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.sempty[se]);
+          if (++se == kScaleRing) se = 0, ++se_lap;
+        }
+        if (!ok) break;
+        // Lanes lie along the results' rows: 2 bytes each, 64 (SwiGLU: 32) together.
+        const int i = kGates ? x.i0 + (int)rank * x.cols / 4 + 16 * q + (lane & 15) : x.i0 + (int)rank * x.cols / 2 + l;
+        const bool in = l < x.cols / 2 && i < a.out_cols;
+        const int count = in ? min(x.jh, x.rows - c0) : 0;  // of this warp's tokens
+        const size_t ld = kGates || (DX && ACT) ? 2 * (size_t)a.out_cols : a.out_cols;
+        const size_t at = ((size_t)x.row0 + c0) * ld + i;
+        uint16_t* out = static_cast<uint16_t*>(a.out) + (kGates ? ((size_t)x.row0 + c0) * a.n + i : at);
+        uint16_t* pre = static_cast<uint16_t*>(kGates ? a.pre_out : const_cast<void*>(a.pre_in)) + at + (kGates && lane >= 16 ? a.n : 0);
+        const bool saves = kGates && a.pre_out;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          if (m >= chunks) break;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float v = k & 1 ? hi_of(sum[m][k / 2]) : lo_of(sum[m][k / 2]);
+            const bool here = 16 * m + k < count;
+            if constexpr (kGates) {
+              const float u = __shfl_xor_sync(~0u, v, 16);
+              if (here && saves) *pre = (uint16_t)T::pack2(v, 0.f);
+              if (here && lane < 16) *out = (uint16_t)T::pack2(swiglu(v, u), 0.f);
+              pre += ld;
+              out += a.n;
+            } else if constexpr (DX && ACT) {
+              if (here) {
+                float dg, du;
+                swiglu_gradient(v, T::lo(__ldg(pre)), T::lo(__ldg(pre + a.out_cols)), dg, du);
+                out[0] = (uint16_t)T::pack2(dg, 0.f);
+                out[a.out_cols] = (uint16_t)T::pack2(du, 0.f);
+              }
+              pre += ld;
+              out += ld;
+            } else {
+              if (here) *out = (uint16_t)T::pack2(v, 0.f);
+              out += ld;
+            }
+          }
+        }
+        ++nth;
+        continue;
+      }
+      const int jh = x.jh, rows = rank ? x.rows - jh : jh;  // of this CTA
       // chunks of 32 columns of this warp's 128; none where its lanes hold no tokens
       const int chunks = 32 * q < rows ? min(4, max(0, (x.cols - 128 * half + 31) / 32)) : 0;
       Pair acc[4][16];
@@ -366,47 +494,42 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
       for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int k = 0; k < 16; ++k) acc[m][k] = 0;
-      float4 xc = {};
-      float wc = 0.f;
-      for (int kb = 0; kb < a.blocks; ++kb) {
-        const uint32_t b = buf & 1, use = buf >> 1;
-        ++buf;
-        if ((kb & 3) == 0) {
-          xc = xn;
-          wc = wn;
-          if (kb + 4 < a.blocks) {
-            fetch(x, kb + 4);
-          } else if (t + step < n_tiles) {
-            next = tile_at<kGates>(a, s_begin, s_tile, t + step);
-            fetch(next, 0);
-          }
-        }
-        const float sg = xc.x * __shfl_sync(~0u, wc, kb & 3);
-        const float su = kGates ? xc.x * __shfl_sync(~0u, wc, 4 + (kb & 3)) : sg;
-        const Pair pg = pair_of(sg, sg), pu = pair_of(su, su);
-        xc.x = xc.y, xc.y = xc.z, xc.z = xc.w;
-        if (!(ok = wait(&bars.tfull[b], use & 1))) break;
-        fence_after();
-        const uint32_t src = tmem + b * kNT + ((uint32_t)(q * 32) << 16) + 128 * half;
-        uint32_t v[2][32];
-        if (chunks > 0) tmem_ld32(src, v[0]);
+      for (int b0 = 0; b0 < a.blocks && ok; b0 += kEntry) {
+        if (!(ok = wait(&bars.sfull[se], se_lap & 1))) break;
+        const float* sc = s_scales + se * kScaleFloats;
+        const int nb = min(kEntry, a.blocks - b0);
+#pragma unroll 1
+        for (int k = 0; k < nb; ++k) {
+          const uint32_t b = buf & 1;
+          const float xv = sc[k * 128 + 32 * q + lane];
+          const float* wc = sc + kEntry * 128 + 2 * k;
+          const float sg = xv * wc[kGates ? 0 : half], su = kGates ? xv * wc[1] : sg;
+          const Pair pg = pair_of(sg, sg), pu = pair_of(su, su);
+          const uint32_t src = lanes + b * kNT + 128 * half;
+          if (!(ok = wait(&bars.tfull[b], (buf >> 1) & 1))) break;
+          ++buf;
+          fence_after();
+          if (chunks > 0) {
+            uint32_t v[32];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          if (m >= chunks) break;
-          tmem_wait();
-          if (m + 1 < 4 && m + 1 < chunks) {
-            tmem_ld32(src + 32 * (m + 1), v[(m + 1) & 1]);
-          } else {  // the accumulator is read
-            fence_before();
+            for (int m = 0; m < 4; ++m) {
+              tmem_ld32(src + 32 * m, v);
+              tmem_wait();
+              if (m == 3) {
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster_relaxed(release[b]);
+              }
+              add_scaled(v, pg, pu, acc[m]);
+            }
+          } else {
             __syncwarp();
-            if (lane == 0) arrive_cluster_relaxed(lead(&bars.tempty[b]));
+            if (lane == 0) arrive_cluster_relaxed(release[b]);
           }
-          add_scaled(v[m & 1], pg, pu, acc[m]);
         }
-        if (chunks == 0) {
-          __syncwarp();
-          if (lane == 0) arrive_cluster_relaxed(lead(&bars.tempty[b]));
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.sempty[se]);
+        if (++se == kScaleRing) se = 0, ++se_lap;
       }
       if (!ok) break;
       const int j = 32 * q + lane;
@@ -520,7 +643,7 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
 template <bool DX, typename T, bool ACT, bool OUT8>
 cudaError_t launch_t(const B128Args& a, const CUtensorMap& mw, const RowMaps& mr, cudaStream_t s) {
   constexpr auto kernel = b128_kernel<DX, T, ACT, OUT8>;
-  const size_t smem = 1024 + kStages * kStageBytes + 8 * ((size_t)a.G + 1);
+  const size_t smem = 1024 + kStages * kStageBytes + kScaleRing * kScaleFloats * 4 + 8 * ((size_t)a.G + 1);
   cudaError_t e = prepare_kernel<kernel>(smem);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
@@ -553,7 +676,6 @@ cudaError_t launch_type(bool dx, B128Args& a, cudaStream_t s) {
   a.out_cols = dx ? a.K : a.n;
   a.tiles_i = act ? a.nb : (a.out_cols + 255) / 256;
   auto whole = [](const void* p, int64_t row, int unit) { return (reinterpret_cast<uintptr_t>(p) | row) % unit == 0; };
-  a.vec = whole(a.xs, 4 * (int64_t)a.blocks, 16);
   // every 16 values of a result's row begin on 32 bytes if the first do
   a.wide = whole(a.out, 0, 32) && whole(a.pre_in, 0, 32) && whole(a.pre_out, 0, 32);
   {  // rows: of both halves side by side for dx

@@ -280,10 +280,10 @@ __device__ __forceinline__ uint32_t idesc_f16(bool bf16, bool a_mn, bool b_mn, i
 }
 
 // Instruction descriptor of kind::f8f6f4: f32 accumulators, formats 0 e4m3, 1 e5m2,
-// B optionally MN-major, M x N.
-__device__ __forceinline__ uint32_t idesc_fp8(int a_fmt, int b_fmt, bool b_mn, int m, int n) {
-  return (1u << 4) | ((uint32_t)a_fmt << 7) | ((uint32_t)b_fmt << 10) | ((b_mn ? 1u : 0u) << 16) |
-         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+// optionally MN-major, M x N.
+__device__ __forceinline__ uint32_t idesc_fp8(int a_fmt, int b_fmt, bool a_mn, bool b_mn, int m, int n) {
+  return (1u << 4) | ((uint32_t)a_fmt << 7) | ((uint32_t)b_fmt << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // Descriptor of 32 unswizzled lines of 16 bytes, for copy_scales.
