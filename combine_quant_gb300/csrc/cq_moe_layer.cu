@@ -60,14 +60,19 @@ template <int RG>
 constexpr int kSegs = 2 * kBoxes<RG>;
 template <int RG>
 constexpr int kWarps = kSegs<RG> * RG;
+// With sixteen warps that multiply, three more that do nothing fill the copying warp's
+// warpgroup, so that registers can be moved: of 640 x 96 the multiplying warps get 112 a
+// thread, the others 32, the same in all.
 template <int RG>
-constexpr int kThreads = 32 * (kWarps<RG> + 1);
+constexpr int kThreads = 32 * (kWarps<RG> + (RG == 1 ? 1 : 4));
+constexpr int kOtherRegs = 32, kProductRegs = 112;
+static_assert(128 * kOtherRegs + 32 * kWarps<4> * kProductRegs <= 96 * kThreads<4>, "setmaxnreg would wait forever");
 template <int RG>
 constexpr int kStageW = kBoxes<RG> * 32 * RG * 128;  // weights of a stage
 // Sums of every share of k, or (many tokens and rows) one that the shares add to in turn.
 template <int RG>
 constexpr bool kTurns = RG > 1;
-constexpr int kMaxWarps = kWarps<4> + 1;
+constexpr int kMaxWarps = kThreads<4> / 32;
 constexpr int kMaxPairs = 64 * 16, kMaxItems = kMaxPairs + 32;
 
 // k of a stage.
@@ -252,38 +257,47 @@ __device__ __forceinline__ void multiply(uint32_t box, int r0, int r1, int half,
         nan[2 * f + u] |= (t[0] | t[1] | t[2]) | t[3];
       }
     }
+  // Two blocks of tokens side by side: a product waits for the one before it in its sum.
+  constexpr int kSide = NB > 2 ? 2 : 1;
 #pragma unroll
-  for (int n = 0; n < NB; ++n) {
+  for (int n = 0; n < NB; n += kSide) {
     if (n >= n8) break;
-    float sum[2][4];
+    float sum[kSide][2][4];
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
-      const uint32_t line = lines + token[n] * 128 + p * part_bytes;
-      uint32_t x[2 * kSteps];
+      uint32_t x[kSide][2 * kSteps];
 #pragma unroll
-      for (int k = 0; k < kSteps / 2; ++k) {
-        const int at = FP8 ? 2 * c + k : half * 4 + c;
-        const uint4 t = lds16(line + ((at ^ (token[n] & 7)) << 4));
-        x[4 * k] = t.x, x[4 * k + 1] = t.y, x[4 * k + 2] = t.z, x[4 * k + 3] = t.w;
+      for (int b = 0; b < kSide; ++b) {
+        const uint32_t line = lines + token[n + b] * 128 + p * part_bytes;
+#pragma unroll
+        for (int k = 0; k < kSteps / 2; ++k) {
+          const int at = FP8 ? 2 * c + k : half * 4 + c;
+          const uint4 t = lds16(line + ((at ^ (token[n + b] & 7)) << 4));
+          x[b][4 * k] = t.x, x[b][4 * k + 1] = t.y, x[b][4 * k + 2] = t.z, x[b][4 * k + 3] = t.w;
+        }
       }
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const uint32_t(&q)[2][2 * kSteps] = v[f];
-          if (FP8 && p == 0 && k == 0)
-            mma16<T, true>(sum[f], q[0][0], q[1][0], q[0][1], q[1][1], x[0], x[1]);
-          else
-            mma16<T, false>(FP8 ? sum[f] : acc[f][n], q[0][2 * k], q[1][2 * k], q[0][2 * k + 1], q[1][2 * k + 1], x[2 * k],
-                            x[2 * k + 1]);
-        }
+        for (int b = 0; b < kSide; ++b)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const uint32_t(&q)[2][2 * kSteps] = v[f];
+            if (FP8 && p == 0 && k == 0)
+              mma16<T, true>(sum[b][f], q[0][0], q[1][0], q[0][1], q[1][1], x[b][0], x[b][1]);
+            else
+              mma16<T, false>(FP8 ? sum[b][f] : acc[f][n + b], q[0][2 * k], q[1][2 * k], q[0][2 * k + 1], q[1][2 * k + 1],
+                              x[b][2 * k], x[b][2 * k + 1]);
+          }
     }
     if constexpr (FP8) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[0][n][i] = fmaf(sum[0][i], s0, acc[0][n][i]);
-        acc[1][n][i] = fmaf(sum[1][i], s1, acc[1][n][i]);
-      }
+      for (int b = 0; b < kSide; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[0][n + b][i] = fmaf(sum[b][0][i], s0, acc[0][n + b][i]);
+          acc[1][n + b][i] = fmaf(sum[b][1][i], s1, acc[1][n + b][i]);
+        }
     }
   }
 }
@@ -328,6 +342,13 @@ __device__ __forceinline__ void init_ring(Ring& r, int stages, int warps) {
     }
     async::mbar_fence_init();
   }
+}
+
+template <int RG, bool PRODUCTS>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (RG == 1) return;
+  if constexpr (PRODUCTS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kProductRegs));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
 }
 
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
@@ -375,7 +396,9 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
   const int tiles = (a.I + kOuts - 1) / kOuts, units = items.n * tiles;
   const int n_stages = (a.H + KC - 1) / KC;
   uint32_t s = 0, lap = 0;
-  if (warp == WARPS) {
+  if (warp >= WARPS) {
+    set_registers<RG, false>();
+    if (warp > WARPS) return;
     // ---- copies ----
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
@@ -401,6 +424,7 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
     return;
   }
   // ---- products ----
+  set_registers<RG, true>();
   const int seg = warp / RG, group = warp % RG, c = lane & 3;
   const int box = seg >> 1, half = seg & 1;
   const int kb = (a.H + 127) / 128, ib = (a.I + 127) / 128;
@@ -509,7 +533,9 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
   const int per = (a.I + KC - 1) / KC, total = items.n * per;
   const int begin = (int)((int64_t)total * rank / a.cluster), end = (int)((int64_t)total * (rank + 1) / a.cluster);
   uint32_t s = 0, lap = 0;
-  if (warp == WARPS) {
+  if (warp >= WARPS) {
+    set_registers<RG, false>();
+    if (warp == WARPS) {
     // ---- copies: weights of as many stages as the ring has before the wait for h ----
     auto load_weights = [&](int v, int st) {
       const int item = v / per, k = v % per;
@@ -549,8 +575,10 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
       if (++s == a.stages) s = 0, ++lap;
     }
     if (!ok) end_copies(ring, a.stages, s, lap);
+    }
   } else {
     // ---- products ----
+    set_registers<RG, true>();
     const int seg = warp / RG, group = warp % RG, c = lane & 3;
     const int box = seg >> 1, half = seg & 1;
     int token[NB];
@@ -621,22 +649,25 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
   if (a.cluster > 1) cluster_sync();
   else __syncthreads();
   // The tile's results, shared out among the CTAs.
-  for (int v = rank * kThreads<RG> + threadIdx.x; v < a.T * kRows; v += a.cluster * kThreads<RG>) {
-    const int t = v / kRows, o = v % kRows;
-    float r = 0.f;
-    if (a.cluster > 1) {
-      for (int q = 0; q < a.cluster; ++q) {
-        float w;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w) : "r"(addr_in(smem_u32(sums + t * kLine + o), q)) : "memory");
-        r += w;
+  constexpr int kMany = 32 * WARPS;
+  if (warp < WARPS) {
+    for (int v = rank * kMany + threadIdx.x; v < a.T * kRows; v += a.cluster * kMany) {
+      const int t = v / kRows, o = v % kRows;
+      float r = 0.f;
+      if (a.cluster > 1) {
+        for (int q = 0; q < a.cluster; ++q) {
+          float w;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w) : "r"(addr_in(smem_u32(sums + t * kLine + o), q)) : "memory");
+          r += w;
+        }
+      } else {
+        r = sums[t * kLine + o];
       }
-    } else {
-      r = sums[t * kLine + o];
+      if (o0 + o >= a.H) continue;
+      const size_t at = (size_t)t * a.H + o0 + o;
+      if (a.out_f32) static_cast<float*>(a.y)[at] = r;
+      else static_cast<uint16_t*>(a.y)[at] = rounded<T>(r);
     }
-    if (o0 + o >= a.H) continue;
-    const size_t at = (size_t)t * a.H + o0 + o;
-    if (a.out_f32) static_cast<float*>(a.y)[at] = r;
-    else static_cast<uint16_t*>(a.y)[at] = rounded<T>(r);
   }
   if (a.cluster > 1) cluster_sync();
 }
