@@ -63,7 +63,8 @@ constexpr int kThreads = 128 + 32 * kDrainWarps;
 // Registers: 384 threads are launched with 168 each (64512); the drain warps keep 128
 // sums and need 224, the others 56, which is the same total.
 constexpr int kOtherRegs = 56, kDrainRegs = 224;
-static_assert(128 * kOtherRegs + 32 * kDrainWarps * kDrainRegs <= 168 * kThreads, "setmaxnreg would wait forever");
+constexpr int kAllRegs = 128 * kOtherRegs + 32 * kDrainWarps * kDrainRegs;
+static_assert(kAllRegs <= 168 * kThreads, "setmaxnreg would wait forever");
 constexpr int kFew = 128;                  // most rows of a tile with tokens on the columns
 constexpr int kEntry = 4;                  // blocks in an entry of the scales' ring
 constexpr int kScaleRing = 4;
@@ -645,6 +646,7 @@ cudaError_t launch_t(const B128Args& a, const CUtensorMap& mw, const RowMaps& mr
   constexpr auto kernel = b128_kernel<DX, T, ACT, OUT8>;
   const size_t smem = 1024 + kStages * kStageBytes + kScaleRing * kScaleFloats * 4 + 8 * ((size_t)a.G + 1);
   cudaError_t e = prepare_kernel<kernel>(smem);
+  if (e == cudaSuccess) e = check_registers<kernel>(kThreads, kAllRegs);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorUnknown;

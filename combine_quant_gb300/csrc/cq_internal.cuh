@@ -214,6 +214,23 @@ cudaError_t prepare_kernel(size_t smem) {
   return cudaSuccess;
 }
 
+// A kernel that moves registers between its warps (setmaxnreg) waits forever for more than
+// it was launched with: cudaErrorInvalidConfiguration if `Kernel` with `threads` a block
+// has fewer than `total`. Asked once per kernel.
+template <auto Kernel>
+cudaError_t check_registers(int threads, int total) {
+  static std::atomic<int> regs;
+  int n = regs.load(std::memory_order_relaxed);
+  if (n <= 0) {
+    cudaFuncAttributes attr;
+    const cudaError_t e = cudaFuncGetAttributes(&attr, Kernel);
+    if (e != cudaSuccess) return e;
+    n = (attr.numRegs + 7) / 8 * 8;
+    regs.store(n, std::memory_order_relaxed);
+  }
+  return n * threads >= total ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+
 // Number of SMs of the current device (cached per device; 0 on error).
 inline int sm_count() {
   static std::atomic<int> cached[kMaxDevices];

@@ -52,7 +52,7 @@ struct LayerArgs {
   void* y;
 };
 
-// Row groups of 32 rows in a tile: 1, or 4. A stage is boxes of 32 RG rows of 128 bytes;
+// Row groups of 32 rows in a tile: 1, or 4 (down_kernel: 3 or 4). A stage is boxes of 32 RG rows of 128 bytes;
 // a warp takes a row group and half of a box. One more warp copies.
 template <int RG>
 constexpr int kBoxes = RG == 1 ? 4 : 2;
@@ -60,13 +60,17 @@ template <int RG>
 constexpr int kSegs = 2 * kBoxes<RG>;
 template <int RG>
 constexpr int kWarps = kSegs<RG> * RG;
-// With sixteen warps that multiply, three more that do nothing fill the copying warp's
-// warpgroup, so that registers can be moved: of 640 x 96 the multiplying warps get 112 a
-// thread, the others 32, the same in all.
+// With twelve or sixteen warps that multiply, three more that do nothing fill the copying
+// warp's warpgroup, so that registers can be moved: of 640 x 96 (512 x 128) the multiplying
+// warps get 112 (160) a thread, the others 32, the same in all.
 template <int RG>
 constexpr int kThreads = 32 * (kWarps<RG> + (RG == 1 ? 1 : 4));
-constexpr int kOtherRegs = 32, kProductRegs = 112;
-static_assert(128 * kOtherRegs + 32 * kWarps<4> * kProductRegs <= 96 * kThreads<4>, "setmaxnreg would wait forever");
+constexpr int kOtherRegs = 32;
+template <int RG>
+constexpr int kProductRegs = RG == 3 ? 160 : 112;
+template <int RG>
+constexpr int kAllRegs = 128 * kOtherRegs + 32 * kWarps<RG> * kProductRegs<RG>;
+static_assert(kAllRegs<4> <= 96 * kThreads<4> && kAllRegs<3> <= 128 * kThreads<3>, "setmaxnreg would wait forever");
 template <int RG>
 constexpr int kStageW = kBoxes<RG> * 32 * RG * 128;  // weights of a stage
 // Sums of every share of k, or (many tokens and rows) one that the shares add to in turn.
@@ -347,7 +351,7 @@ __device__ __forceinline__ void init_ring(Ring& r, int stages, int warps) {
 template <int RG, bool PRODUCTS>
 __device__ __forceinline__ void set_registers() {
   if constexpr (RG == 1) return;
-  if constexpr (PRODUCTS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kProductRegs));
+  if constexpr (PRODUCTS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kProductRegs<RG>));
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
 }
 
@@ -587,11 +591,12 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
 #pragma unroll
     for (int n = 0; n < NB; ++n) token[n] = 8 * n + fragment_column<FP8>(lane >> 2);
     const int hb = (a.H + 127) / 128, ib = (a.I + 127) / 128;
+    const int ob = min((o0 + 32 * group) / 128, hb - 1);  // the block of this warp's rows
     float fn = 0.f;
     auto factors = [&](int item, int first, float& f) {
       const int block = ((first + lane) * KC + seg * 64) / 128;
       if (!FP8 || item >= items.n || first + lane >= per || block >= ib) return;
-      f = __ldg(a.w2_scales + ((size_t)items.e[item] * hb + o0 / 128) * ib + block);
+      f = __ldg(a.w2_scales + ((size_t)items.e[item] * hb + ob) * ib + block);
     };
     if (begin < end) factors(begin / per, 0, fn);
     bool ok = true;
@@ -675,103 +680,125 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
 }
 
 // ---- host ----
+// The down kernel's grid: tiles, and as many CTAs a tile as are all on the GPU at once: a
+// second wave pays its start again (1 token, hidden 7168: 134 us with 4, 117 with 1; 64
+// tokens, fp8: 529 with 8, 491 with 2).
+struct DownGrid {
+  int tiles, cluster;
+  DownGrid(int H, int rows, int slots) : tiles((H + rows - 1) / rows), cluster(1) {
+    while (cluster < 8 && tiles * (cluster + 1) <= slots) ++cluster;
+  }
+};
+
+struct Maps {
+  CUtensorMap w13, w2, x;
+  TokenMaps h;
+};
+
+// Stages of a ring: what fits beside `rest` with `ctas` a SM.
+int fit_stages(size_t rest, size_t stage, int ctas) {
+  const size_t room = (227 * 1024) / ctas - sizeof(Items) - 2048;
+  return (int)std::min<size_t>(8, (room - 1024 - rest) / stage);
+}
+
 template <typename T, bool FP8, int NB, int RG>
-cudaError_t launch_t(LayerArgs a, const void* w13, const void* w2, cudaStream_t s) {
-  constexpr int kRows = 32 * RG, M = 8 * NB, BLOCKS = kBlocks<FP8, RG>;
-  const MapType type = FP8 ? kMapU8 : T::kBf16 ? kMapBF16 : kMapF16;
-  const uint64_t es = FP8 ? 1 : 2, H = a.H, I = a.I, G = a.G;
-  CUtensorMap m13, m2, mx;
-  TokenMaps mh;
+cudaError_t launch_up(LayerArgs a, const Maps& maps, int sms, cudaStream_t s) {
+  constexpr auto kernel = up_kernel<T, FP8, NB, RG>;
+  constexpr int kRows = 32 * RG, M = 8 * NB, kPerSm = RG == 1 ? 2 : 1;
+  constexpr size_t rest = 4 * (kTurns<RG> ? 1 : kSegs<RG>) * kRows * (M + 1);
+  const size_t stage = kStageW<RG> + kBlocks<FP8, RG> * ((a.T + 7) / 8 * 8) * 128;
+  a.stages = fit_stages(rest, stage, kPerSm);
+  a.whole = a.H % 64 == 0;
+  const size_t smem = 1024 + a.stages * stage + rest;
+  // sort_pairs' scratch lies in the ring: 29 KB at most
+  if (a.stages < 2 || smem < 1024 + 10 * (size_t)a.G + 8 * (size_t)(a.T * a.K)) return cudaErrorInvalidValue;
+  cudaError_t e = prepare_kernel<kernel>(smem);
+  if (e == cudaSuccess && RG > 1) e = check_registers<kernel>(kThreads<RG>, kAllRegs<RG>);
+  if (e != cudaSuccess) return e;
+  const int64_t most = (int64_t)std::min(a.G, a.T * a.K) * ((a.I + 16 * RG - 1) / (16 * RG)) * (a.T > M ? 2 : 1);
+  return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(most, sms * kPerSm)), dim3(kThreads<RG>), smem, s, a, maps.w13,
+                    maps.x);
+}
+
+template <typename T, bool FP8, int NB, int RG>
+cudaError_t launch_down(LayerArgs a, const Maps& maps, int sms, cudaStream_t s) {
+  constexpr auto kernel = down_kernel<T, FP8, NB, RG>;
+  constexpr int kRows = 32 * RG, M = 8 * NB, kPerSm = RG == 1 ? 2 : 1;
+  constexpr size_t stage = kStageW<RG> + kBlocks<FP8, RG> * 2 * M * 128;
+  const size_t rest = 4 * (size_t)(kTurns<RG> ? 1 : kSegs<RG>) * a.T * (kRows + 1);
+  a.stages = fit_stages(rest, stage, kPerSm);
+  a.whole = a.I % 64 == 0;
+  const size_t smem = 1024 + a.stages * stage + rest;
+  if (a.stages < 2 || smem < 1024 + 10 * (size_t)a.G + 8 * (size_t)(a.T * a.K)) return cudaErrorInvalidValue;
+  cudaError_t e = prepare_kernel<kernel>(smem);
+  if (e == cudaSuccess && RG > 1) e = check_registers<kernel>(kThreads<RG>, kAllRegs<RG>);
+  if (e != cudaSuccess) return e;
+  const DownGrid g(a.H, kRows, kPerSm * sms);
+  a.cluster = g.cluster;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(g.tiles * g.cluster);
+  cfg.blockDim = dim3(kThreads<RG>);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)g.cluster, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a, maps.w2, maps.h);
+}
+
+// RU, RD: row groups of the two kernels.
+template <typename T, bool FP8, int NB, int RU, int RD>
+cudaError_t launch_t(const LayerArgs& a, const void* w13, const void* w2, int sms, cudaStream_t s) {
+  constexpr int M = 8 * NB;
+  const MapType type = FP8 ? kMapU8 : T::kBf16 ? kMapBF16 : kMapF16, token = T::kBf16 ? kMapBF16 : kMapF16;
+  const uint64_t es = FP8 ? 1 : 2, H = a.H, I = a.I, G = a.G, P = (uint64_t)a.T * a.K;
+  Maps m;
   {
     const uint64_t d[] = {H, I, 2, G}, st[] = {es * H, es * I * H, es * 2 * I * H};
-    const uint32_t b[] = {(uint32_t)(128 / es), 16 * RG, 2, 1};
-    if (!make_map(&m13, w13, type, 4, d, st, b)) return cudaErrorUnknown;
+    const uint32_t b[] = {(uint32_t)(128 / es), 16 * RU, 2, 1};
+    if (!make_map(&m.w13, w13, type, 4, d, st, b)) return cudaErrorUnknown;
   }
   {
     const uint64_t d[] = {I, H, G}, st[] = {es * I, es * I * H};
-    const uint32_t b[] = {(uint32_t)(128 / es), (uint32_t)kRows, 1};
-    if (!make_map(&m2, w2, type, 3, d, st, b)) return cudaErrorUnknown;
-  }
-  const MapType token = T::kBf16 ? kMapBF16 : kMapF16;
-  const uint32_t lines = (a.T + 7) / 8 * 8;
-  const bool whole_x = H % 64 == 0, whole_h = I % 64 == 0;
-  {
-    const uint64_t d[] = {whole_x ? 64 : H, (uint64_t)a.T, whole_x ? H / 64 : 1}, st[] = {2 * H, whole_x ? 128 : 2 * H * a.T};
-    const uint32_t b[] = {64, lines, whole_x ? (uint32_t)BLOCKS : 1};
-    if (!make_map(&mx, a.x, token, 3, d, st, b)) return cudaErrorUnknown;
+    const uint32_t b[] = {(uint32_t)(128 / es), 32 * RD, 1};
+    if (!make_map(&m.w2, w2, type, 3, d, st, b)) return cudaErrorUnknown;
   }
   {
-    const uint64_t P = (uint64_t)a.T * a.K, d[] = {whole_h ? 64 : I, P, 2, whole_h ? I / 64 : 1};
-    const uint64_t st[] = {2 * I, 2 * I * P, whole_h ? 128 : 4 * I * P};
-    CUtensorMap* const to[] = {&mh.rows8, &mh.rows16, &mh.rows32};
-    for (int k = 0; k < 3; ++k) {
-      if (8 << k > M) {
-        *to[k] = mh.rows8;
-        continue;
-      }
-      const uint32_t b[] = {64, 8u << k, 2, whole_h ? (uint32_t)BLOCKS : 1};
-      if (!make_map(to[k], a.h, token, 4, d, st, b)) return cudaErrorUnknown;
-    }
+    const bool whole = H % 64 == 0;
+    const uint64_t d[] = {whole ? 64 : H, (uint64_t)a.T, whole ? H / 64 : 1}, st[] = {2 * H, whole ? 128 : 2 * H * a.T};
+    const uint32_t b[] = {64, (uint32_t)(a.T + 7) / 8 * 8, whole ? (uint32_t)kBlocks<FP8, RU> : 1};
+    if (!make_map(&m.x, a.x, token, 3, d, st, b)) return cudaErrorUnknown;
   }
-  const int sms = sm_count();
-  if (sms <= 0) return cudaErrorUnknown;
-  constexpr int kPerSm = RG == 1 ? 2 : 1;  // CTAs a SM by shared memory
-  const size_t room = (227 * 1024) / kPerSm - sizeof(Items) - 2048;
-  auto fit = [&](size_t rest, size_t stage) {  // stages of the ring
-    return (int)std::min<size_t>(8, (room - 1024 - rest) / stage);
-  };
-  const size_t scratch = 10 * (size_t)a.G + 8 * (size_t)(a.T * a.K);  // sort_pairs', in the ring: 29 KB at most
-  cudaError_t e;
-  {
-    constexpr auto kernel = up_kernel<T, FP8, NB, RG>;
-    constexpr size_t rest = 4 * (kTurns<RG> ? 1 : kSegs<RG>) * kRows * (M + 1);
-    const size_t stage = kStageW<RG> + BLOCKS * lines * 128;
-    a.stages = fit(rest, stage);
-    a.whole = whole_x;
-    const size_t smem = 1024 + a.stages * stage + rest;
-    if (a.stages < 2 || smem < scratch + 1024) return cudaErrorInvalidValue;
-    if ((e = prepare_kernel<kernel>(smem)) != cudaSuccess) return e;
-    const int64_t most = (int64_t)std::min(a.G, a.T * a.K) * ((a.I + 16 * RG - 1) / (16 * RG)) * (a.T > M ? 2 : 1);
-    e = launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(most, sms * kPerSm)), dim3(kThreads<RG>), smem, s, a, m13, mx);
-    if (e != cudaSuccess) return e;
+  const bool whole = I % 64 == 0;
+  const uint64_t d[] = {whole ? 64 : I, P, 2, whole ? I / 64 : 1};
+  const uint64_t st[] = {2 * I, 2 * I * P, whole ? 128 : 4 * I * P};
+  CUtensorMap* const to[] = {&m.h.rows8, &m.h.rows16, &m.h.rows32};
+  for (int k = 0; k < 3 && 8 << k <= M; ++k) {
+    const uint32_t b[] = {64, 8u << k, 2, whole ? (uint32_t)kBlocks<FP8, RD> : 1};
+    if (!make_map(to[k], a.h, token, 4, d, st, b)) return cudaErrorUnknown;
   }
-  {
-    constexpr auto kernel = down_kernel<T, FP8, NB, RG>;
-    constexpr size_t stage = kStageW<RG> + BLOCKS * 2 * M * 128;
-    const size_t rest = 4 * (size_t)(kTurns<RG> ? 1 : kSegs<RG>) * a.T * (kRows + 1);
-    a.stages = fit(rest, stage);
-    a.whole = whole_h;
-    const size_t smem = 1024 + a.stages * stage + rest;
-    if (a.stages < 2 || smem < scratch + 1024) return cudaErrorInvalidValue;
-    if ((e = prepare_kernel<kernel>(smem)) != cudaSuccess) return e;
-    const int tiles = (a.H + kRows - 1) / kRows;
-    a.cluster = 1;
-    // as many CTAs a tile as are all on the GPU at once: a second wave pays its start again
-    // (1 token, hidden 7168: 134 us with 4, 117 with 1; 64 tokens, fp8: 529 with 8, 491 with 2)
-    while (a.cluster < 8 && tiles * (a.cluster + 1) <= kPerSm * sms) ++a.cluster;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(tiles * a.cluster);
-    cfg.blockDim = dim3(kThreads<RG>);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {(unsigned)a.cluster, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, a, m2, mh);
-  }
+  const cudaError_t e = launch_up<T, FP8, NB, RU>(a, m, sms, s);
+  return e == cudaSuccess ? launch_down<T, FP8, NB, RD>(a, m, sms, s) : e;
 }
 
 // Few tokens: small tiles, so that all SMs have work, two CTAs each. More tokens: tiles
 // of four times the rows, since every tile fetches its tokens' rows, and sixteen warps.
+// The down kernel takes tiles of 96 rows where those and their clusters cover more SMs
+// (hidden 7168: 150 of 152 instead of 112; 64 tokens, fp8: 491 -> XX us).
 template <typename T, bool FP8>
 cudaError_t launch(const LayerArgs& a, const void* w13, const void* w2, cudaStream_t s) {
-  if (a.T <= 8) return launch_t<T, FP8, 1, 1>(a, w13, w2, s);
-  if (a.T <= 16) return launch_t<T, FP8, 2, 4>(a, w13, w2, s);
-  return launch_t<T, FP8, 4, 4>(a, w13, w2, s);
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorUnknown;
+  if (a.T <= 8) return launch_t<T, FP8, 1, 1, 1>(a, w13, w2, sms, s);
+  const DownGrid g3(a.H, 96, sms), g4(a.H, 128, sms);
+  const bool three = g3.tiles * g3.cluster > g4.tiles * g4.cluster;
+  if (a.T <= 16)
+    return three ? launch_t<T, FP8, 2, 4, 3>(a, w13, w2, sms, s) : launch_t<T, FP8, 2, 4, 4>(a, w13, w2, sms, s);
+  return three ? launch_t<T, FP8, 4, 4, 3>(a, w13, w2, sms, s) : launch_t<T, FP8, 4, 4, 4>(a, w13, w2, sms, s);
 }
 
 int validate(const cq_moe_config* c) {

@@ -1,11 +1,12 @@
 """One MoE layer on the package: dispatch, the experts (gate and up products with
 SwiGLU, down product), combine -- forward and backward in 16 bits, forward with
-rows and weights in mx fp8, and forward with 4-bit weights.
+rows and weights in mx fp8, in fp8 with scales per 128, with 4-bit weights, and
+for a few tokens the whole layer as one call.
 
     python examples/moe_layer.py [--ranks 8] [--experts 4] [--tokens 8] [--topk 8]
-                                 [--hidden 7168] [--inter 2048]
+                                 [--hidden 7168] [--inter 2048] [--all]
 
-Runs the four on one set of inputs, prints how far each is from the layer in 64
+Runs the first three and the backward pass (--all: every form) on one set of inputs, prints how far each is from the layer in 64
 bits on a few tokens, and the time of a call of each.
 """
 import argparse
@@ -74,6 +75,32 @@ def forward_mx(cfg, x, ids, scales, w13, w2):
     return cq.combine(cfg, rows, out.assist_info, scales)
 
 
+def forward_b128(cfg, x, ids, scales, w13, w2):
+    """The same with dispatch's rows in fp8 with a scale per 128 (quant_mode 3) and
+    such weights (codes, scales) for both products: the first one's result leaves in
+    fp8 with its scales, as the second one takes it."""
+    up, down = expert_configs(cfg, w2[0].shape[2])
+    up = replace(up, x_dtype=2 + cfg.y_dtype, out_dtype=cfg.x_dtype)
+    down = replace(down, x_dtype=2, out_dtype=cfg.x_dtype)
+    out = cq.dispatch(cfg, x, ids, expert_scales=scales)
+    hs = torch.empty(up.rows, -(-up.n // 128), dtype=torch.float32, device=x.device)
+    h = cq.expert_matmul_b128(up, out.expand_x, out.dynamic_scales, *w13, out.expert_token_nums, y_scales=hs)
+    rows = cq.expert_matmul_b128(down, h, hs, *w2, out.expert_token_nums)
+    return cq.combine(cfg, rows, out.assist_info, scales)
+
+
+def few_tokens(cfg, x, ids, scales, w13, w2):
+    """All ranks' tokens, 64 at most, through the layer in one call. Weights in the token
+    type, or (codes, scales) in fp8 with a scale per 128 x 128."""
+    fp8 = isinstance(w13, tuple)
+    (w13, s13), (w2, s2) = (w13, w2) if fp8 else ((w13, None), (w2, None))
+    few = cq.MoeConfig(tokens=cfg.ep_world_size * cfg.max_bs, experts=w13.shape[0], topk=cfg.topk, hidden=cfg.hidden,
+                       inter=w2.shape[2], x_dtype=cfg.x_dtype, w_dtype=int(fp8))
+    y = cq.moe_layer(few, x.view(-1, cfg.hidden), ids.view(-1, cfg.topk), scales.view(-1, cfg.topk), w13, w2,
+                     w13_scales=s13, w2_scales=s2)
+    return y.view(x.shape)
+
+
 def forward_w4(cfg, x, ids, scales, w13, w2, group):
     """The same with 4-bit weights (codes, scales, zero points or None) for both products."""
     up, down = expert_configs(cfg, w2[0].shape[2] * 2, group=group)
@@ -124,10 +151,13 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     for name, value in (("ranks", 8), ("experts", 4), ("tokens", 8), ("topk", 8), ("hidden", 7168), ("inter", 2048)):
         ap.add_argument("--" + name, type=int, default=value)
+    ap.add_argument("--all", action="store_true", help="fp8 with scales per 128 and the call for a few tokens too")
     a = ap.parse_args()
     cfg, x, ids, scales, w13, w2 = make_inputs(a.ranks, a.experts, a.tokens, a.topk, a.hidden, a.inter)
     mx = replace(cfg, quant_mode=5)
     w13_mx = weights.quantize_mx(w13)
+    b128 = replace(cfg, quant_mode=3)
+    w13_8, w2_8 = (weights.quantize_b128(w13, halves=2), weights.quantize_b128(w2)) if a.all else (None, None)
     group = 128 if a.hidden % 128 == 0 and a.inter % 128 == 0 else 32
     w13_4, w2_4 = weights.quantize_w4(w13, group), weights.quantize_w4(w2, group)
     few = slice(0, 3)
@@ -139,6 +169,11 @@ def main():
         "mx fp8 forward": lambda: forward_mx(mx, x, ids, scales, w13_mx, w2),
         "4-bit forward": lambda: forward_w4(cfg, x, ids, scales, w13_4, w2_4, group),
     }
+    if a.all:
+        calls["fp8 b128 forward"] = lambda: forward_b128(b128, x, ids, scales, w13_8, w2_8)
+    if a.all and a.ranks * a.tokens <= 64:
+        calls["few tokens"] = lambda: few_tokens(cfg, x, ids, scales, w13, w2)
+        calls["few tokens fp8"] = lambda: few_tokens(cfg, x, ids, scales, w13_8, w2_8)
     for name, call in calls.items():
         off = float((call()[0, few].double() - want).norm() / want.norm())
         print(f"{name:16s} {_time(call):9.1f} us   off by {off:.2g} of the 64-bit layer")
