@@ -19,9 +19,17 @@
 // Between the two SwiGLU's results are held as two numbers of the token type, whose sum
 // keeps 16 bits or more: rounding them to one would add an error as large as y's own
 // rounding. The second kernel's copies of weights start before the first one has ended.
+//
+// fp8 weights and more than 8 tokens: the products are bound by instructions, and a code
+// becomes an fp16 number in half of one, a bf16 number in two and a half. So the products
+// run in fp16 there, whose range powers of two provide: each token's row is scaled by one
+// (scale_kernel, where tokens are bf16; exact but for values 2^-38 below the row's largest),
+// SwiGLU's results by one for 64 of a pair, which the down product's warps multiply back.
+// These are rounded to fp16 once, to 11 bits: an eighth of bf16's rounding of y.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cq_expert.cuh"
 #include "cq_tensor.cuh"
@@ -48,7 +56,10 @@ struct LayerArgs {
   const uint8_t* mask;
   const float* w13_scales;
   const float* w2_scales;
-  uint16_t* h;  // [2][T * K][I]: both numbers
+  uint16_t* h;  // [2][T * K][I]: both numbers; scaled: [T * K][I]
+  float* h_scales;           // scaled: [T * K][units of 64]
+  float* x_scales;           // scaled, bf16 tokens: [T], else NULL
+  uint16_t* x16;             // and their rows [T][H]
   void* y;
 };
 
@@ -73,6 +84,9 @@ constexpr int kAllRegs = 128 * kOtherRegs + 32 * kWarps<RG> * kProductRegs<RG>;
 static_assert(kAllRegs<4> <= 96 * kThreads<4> && kAllRegs<3> <= 128 * kThreads<3>, "setmaxnreg would wait forever");
 template <int RG>
 constexpr int kStageW = kBoxes<RG> * 32 * RG * 128;  // weights of a stage
+// Products in fp16 with powers of two taken out.
+template <bool FP8, int RG>
+constexpr bool kScaled = FP8 && RG > 1;
 // Sums of every share of k, or (many tokens and rows) one that the shares add to in turn.
 template <int RG>
 constexpr bool kTurns = RG > 1;
@@ -231,10 +245,11 @@ __device__ __forceinline__ int fragment_column(int j) {
 // part_bytes apart. FP8: s0, s1 are the fragments' factors here; nan collects codes that
 // are NaN (bf16, whose decoding does not know them): bit 7 of a byte, by fragment and
 // upper rows.
-template <typename T, bool FP8, int NB, int PARTS>
+// COLUMNS: a token's factor meets them, `column` in the token's lane.
+template <typename T, bool FP8, int NB, int PARTS, bool COLUMNS = false>
 __device__ __forceinline__ void multiply(uint32_t box, int r0, int r1, int half, uint32_t lines, const int (&token)[NB],
                                          int part_bytes, int n8, float s0, float s1, float (&acc)[2][NB][4],
-                                         uint32_t (&nan)[4]) {
+                                         uint32_t (&nan)[4], float column = 1.f) {
   const int lane = threadIdx.x & 31, row = fragment_row(lane >> 2), c = lane & 3;
   const uint32_t piece = ((half * 4 + c) ^ row) << 4;
   uint4 w[2][2];
@@ -296,12 +311,18 @@ __device__ __forceinline__ void multiply(uint32_t box, int r0, int r1, int half,
     }
     if constexpr (FP8) {
 #pragma unroll
-      for (int b = 0; b < kSide; ++b)
+      for (int b = 0; b < kSide; ++b) {
+        float f0[2] = {s0, s0}, f1[2] = {s1, s1};
+        if constexpr (COLUMNS) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) f0[i] = f1[i] = s0 * __shfl_sync(~0u, column, 8 * (n + b) + 2 * c + i);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          acc[0][n + b][i] = fmaf(sum[b][0][i], s0, acc[0][n + b][i]);
-          acc[1][n + b][i] = fmaf(sum[b][1][i], s1, acc[1][n + b][i]);
+          acc[0][n + b][i] = fmaf(sum[b][0][i], f0[i & 1], acc[0][n + b][i]);
+          acc[1][n + b][i] = fmaf(sum[b][1][i], f1[i & 1], acc[1][n + b][i]);
         }
+      }
     }
   }
 }
@@ -374,6 +395,47 @@ __device__ __forceinline__ uint16_t rounded(float v) {
   return (uint16_t)T::pack2(v, 0.f);
 }
 
+// The exponent of the power of two that brings the finite value m > 0 into [2^14, 2^15); at
+// most 110, so that the reciprocal times a block's scale stays a normal number.
+__device__ __forceinline__ int f16_exponent(float m) { return m > 0.f ? min(110, 14 - ilogbf(m)) : 0; }
+
+// bf16 rows times a power of two each, in fp16, and its reciprocal: a block a row.
+// Infinities and NaN stay what they are.
+__global__ void __launch_bounds__(256) scale_kernel(const uint16_t* x, uint16_t* to, float* scales, int H) {
+  __shared__ float tops[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint4* row = reinterpret_cast<const uint4*>(x + (size_t)blockIdx.x * H);
+  uint4* out = reinterpret_cast<uint4*>(to + (size_t)blockIdx.x * H);
+  griddep_wait();
+  float top = 0.f;
+  for (int v = threadIdx.x; v < H / 8; v += 256) {
+    const uint4 q = row[v];
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float a = fabsf(BF16::lo(w[k])), b = fabsf(BF16::hi(w[k]));
+      if (a <= 3.402823466e38f) top = fmaxf(top, a);
+      if (b <= 3.402823466e38f) top = fmaxf(top, b);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  if (lane == 0) tops[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) top = fmaxf(top, tops[k]);
+  const int e = f16_exponent(top);
+  for (int v = threadIdx.x; v < H / 8; v += 256) {
+    const uint4 q = row[v];
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = F16::pack2(ldexpf(BF16::lo(w[k]), e), ldexpf(BF16::hi(w[k]), e));
+    out[v] = make_uint4(r[0], r[1], r[2], r[3]);
+  }
+  if (threadIdx.x == 0) scales[blockIdx.x] = ldexpf(1.f, -e);
+}
+
 // Gate and up products and SwiGLU. NB: token blocks of 8; RG: row groups.
 template <typename T, bool FP8, int NB, int RG>
 __global__ void __launch_bounds__(kThreads<RG>, RG == 1 ? 2 : 1)
@@ -397,6 +459,7 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
   sort_pairs<M, kThreads<RG>>(a, items, stage0, blockIdx.x == 0);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
+  using M16 = std::conditional_t<kScaled<FP8, RG>, F16, T>;  // of the products
   const int tiles = (a.I + kOuts - 1) / kOuts, units = items.n * tiles;
   const int n_stages = (a.H + KC - 1) / KC;
   // the same number of units for every CTA that has any, so that all end together
@@ -458,12 +521,12 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
       if (FP8 && k > 0 && (k & 31) == 0) factors(u, k, g, w);
       const float sg = FP8 ? __shfl_sync(~0u, g, k & 31) : 1.f, su = FP8 ? __shfl_sync(~0u, w, k & 31) : 1.f;
       if (!(ok = wait_warp(&ring.full[s], lap & 1))) break;
-      multiply<T, FP8, NB, 1>(smem_u32(stage0 + s * SW + box * kRows * 128), 16 * group, kOuts + 16 * group, half,
+      multiply<M16, FP8, NB, 1>(smem_u32(stage0 + s * SW + box * kRows * 128), 16 * group, kOuts + 16 * group, half,
                               smem_u32(tokens0 + s * kTokens + (FP8 ? seg : box) * lines * 128), token, 0, n8, sg, su, acc, nan);
       async::release_slot(&ring.empty[s]);
       if (++s == a.stages) s = 0, ++lap;
     }
-    if (FP8 && T::kBf16) spread_nan(nan, acc);
+    if (FP8 && M16::kBf16) spread_nan(nan, acc);
     // the warps' shares: red[seg][row][token], or one sum that they add to in turn
     const int row = 32 * group + fragment_row(lane >> 2);
     auto put = [&](bool first) {
@@ -499,13 +562,39 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
         pg += p[q * kRows * (M + 1)];
         pu += p[(q * kRows + 16) * (M + 1)];
       }
-      const float r = swiglu(pg, pu);
-      const uint16_t hi = rounded<T>(r);
-      const float lo = r - T::lo(hi);
-      uint16_t* to = a.h + (size_t)(off + j) * a.I + i0 + o;
-      to[0] = hi;
-      // an infinite first number would make the second NaN
-      to[(size_t)a.T * a.K * a.I] = rounded<T>(fabsf(T::lo(hi)) <= 3.402823466e38f ? lo : 0.f);
+      if constexpr (kScaled<FP8, RG>) {
+        const float f = a.x_scales ? a.x_scales[items.tok[off + j]] : 1.f;
+        const_cast<float*>(p)[0] = swiglu(pg * f, pu * f);
+      } else {
+        const float r = swiglu(pg, pu);
+        const uint16_t hi = rounded<T>(r);
+        const float lo = r - T::lo(hi);
+        uint16_t* to = a.h + (size_t)(off + j) * a.I + i0 + o;
+        to[0] = hi;
+        // an infinite first number would make the second NaN
+        to[(size_t)a.T * a.K * a.I] = rounded<T>(fabsf(T::lo(hi)) <= 3.402823466e38f ? lo : 0.f);
+      }
+    }
+    if constexpr (kScaled<FP8, RG>) {
+      // a pair's 64 results and their power of two: a warp
+      if (!async::meet<32 * WARPS>(true)) break;
+      for (int j = warp; j < m; j += WARPS) {
+        float r[2], top = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int o = 32 * k + lane;
+          r[k] = i0 + o < a.I ? red[(32 * (o / 16) + o % 16) * (M + 1) + j] : 0.f;
+          if (fabsf(r[k]) <= 3.402823466e38f) top = fmaxf(top, fabsf(r[k]));
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        const int e = f16_exponent(top);
+        uint16_t* to = a.h + (size_t)(off + j) * a.I + i0 + lane;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (i0 + 32 * k + lane < a.I) to[32 * k] = rounded<F16>(ldexpf(r[k], e));
+        if (lane == 0) a.h_scales[(size_t)(off + j) * tiles + i0 / 64] = ldexpf(1.f, -e);
+      }
     }
     if (!async::meet<32 * WARPS>(true)) break;
   }
@@ -518,7 +607,9 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
             const __grid_constant__ TokenMaps map_h) {
   constexpr int KC = kChunk<FP8, RG>, BLOCKS = kBlocks<FP8, RG>, SEGS = kSegs<RG>, M = 8 * NB, WARPS = kWarps<RG>;
   constexpr int kRows = 32 * RG, BOXES = kBoxes<RG>, kBoxK = KC / BOXES, kLine = kRows + 1, SW = kStageW<RG>;
-  constexpr int kTokens = BLOCKS * 2 * M * 128;  // both numbers' lines
+  constexpr bool SCALED = kScaled<FP8, RG>;
+  constexpr int PARTS = SCALED ? 1 : 2, kTokens = BLOCKS * PARTS * M * 128;  // the numbers' lines
+  using M16 = std::conditional_t<SCALED, F16, T>;  // of the products
   constexpr int kSums = kTurns<RG> ? 1 : SEGS;
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Ring ring;
@@ -546,7 +637,7 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
     auto load_weights = [&](int v, int st) {
       const int item = v / per, k = v % per;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&ring.full[st], SW + BLOCKS * 2 * 128 * lines_of(items.m[item]));
+        mbar_arrive_expect_tx(&ring.full[st], SW + BLOCKS * PARTS * 128 * lines_of(items.m[item]));
         for (int b = 0; b < BOXES; ++b)
           tma_load3<1>(smem_u32(stage0 + st * SW + b * kRows * 128), &map, k * KC + b * kBoxK, o0, items.e[item],
                        smem_u32(&ring.full[st]));
@@ -562,7 +653,7 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
           tma_load4<1>(to, from, 0, items.off[item], 0, k * BLOCKS, bar);
         } else {
           for (int b = 0; b < BLOCKS; ++b)
-            tma_load4<1>(to + b * 2 * rows * 128, from, k * KC + b * 64, items.off[item], 0, 0, bar);
+            tma_load4<1>(to + b * PARTS * rows * 128, from, k * KC + b * 64, items.off[item], 0, 0, bar);
         }
       }
       __syncwarp();
@@ -599,6 +690,16 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
       f = __ldg(a.w2_scales + ((size_t)items.e[item] * hb + ob) * ib + block);
     };
     if (begin < end) factors(begin / per, 0, fn);
+    // scaled: h's powers of two, a pair a lane, of this warp's 64 k of a stage
+    const int units = (a.I + 63) / 64;
+    float column = 1.f;
+    auto columns = [&](int v) {
+      if (!SCALED || v >= end) return;
+      const int item = v / per, unit = v % per * BLOCKS + seg;
+      if (lane < items.m[item] && unit < units) column = __ldg(a.h_scales + (size_t)(items.off[item] + lane) * units + unit);
+    };
+    if (SCALED) griddep_wait();
+    columns(begin);
     bool ok = true;
     for (int v = begin; v < end && ok;) {
       const int item = v / per, m = items.m[item], n8 = (m + 7) / 8, off = items.off[item];
@@ -610,15 +711,17 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
       if (FP8 && k0 >= 32) factors(item, k0 & ~31, f);
       for (int k = k0; k < k1; ++k) {
         if (FP8 && k > k0 && (k & 31) == 0) factors(item, k, f);
-        const float sf = FP8 ? __shfl_sync(~0u, f, k & 31) : 1.f;
+        const float sf = FP8 ? __shfl_sync(~0u, f, k & 31) : 1.f, now = column;
+        columns(v + k - k0 + 1);
         if (!(ok = wait_warp(&ring.full[s], lap & 1))) break;
-        multiply<T, FP8, NB, 2>(smem_u32(stage0 + s * SW + box * kRows * 128), 32 * group, 32 * group + 16, half,
-                                smem_u32(tokens0 + s * kTokens + (FP8 ? seg : box) * 2 * part), token, part, n8, sf, sf, acc, nan);
+        multiply<M16, FP8, NB, PARTS, SCALED>(smem_u32(stage0 + s * SW + box * kRows * 128), 32 * group, 32 * group + 16, half,
+                                              smem_u32(tokens0 + s * kTokens + (FP8 ? seg : box) * PARTS * part), token, part,
+                                              n8, sf, sf, acc, nan, now);
         async::release_slot(&ring.empty[s]);
         if (++s == a.stages) s = 0, ++lap;
       }
       v += k1 - k0;
-      if (FP8 && T::kBf16) spread_nan(nan, acc);
+      if (FP8 && M16::kBf16) spread_nan(nan, acc);
       // an item's tokens all differ, and a warp's rows are its own
       const int row = 32 * group + fragment_row(lane >> 2);
       auto add = [&] {
@@ -724,7 +827,7 @@ template <typename T, bool FP8, int NB, int RG>
 cudaError_t launch_down(LayerArgs a, const Maps& maps, int sms, cudaStream_t s) {
   constexpr auto kernel = down_kernel<T, FP8, NB, RG>;
   constexpr int kRows = 32 * RG, M = 8 * NB, kPerSm = RG == 1 ? 2 : 1;
-  constexpr size_t stage = kStageW<RG> + kBlocks<FP8, RG> * 2 * M * 128;
+  constexpr size_t stage = kStageW<RG> + kBlocks<FP8, RG> * (kScaled<FP8, RG> ? 1 : 2) * M * 128;
   const size_t rest = 4 * (size_t)(kTurns<RG> ? 1 : kSegs<RG>) * a.T * (kRows + 1);
   a.stages = fit_stages(rest, stage, kPerSm);
   a.whole = a.I % 64 == 0;
@@ -752,9 +855,19 @@ cudaError_t launch_down(LayerArgs a, const Maps& maps, int sms, cudaStream_t s) 
 
 // RU, RD: row groups of the two kernels.
 template <typename T, bool FP8, int NB, int RU, int RD>
-cudaError_t launch_t(const LayerArgs& a, const void* w13, const void* w2, int sms, cudaStream_t s) {
+cudaError_t launch_t(LayerArgs a, const void* w13, const void* w2, int sms, cudaStream_t s) {
   constexpr int M = 8 * NB;
-  const MapType type = FP8 ? kMapU8 : T::kBf16 ? kMapBF16 : kMapF16, token = T::kBf16 ? kMapBF16 : kMapF16;
+  constexpr bool kScale = kScaled<FP8, RD>;
+  static_assert(kScaled<FP8, RU> == kScale, "both kernels hold h alike");
+  const MapType type = FP8 ? kMapU8 : T::kBf16 ? kMapBF16 : kMapF16, token = T::kBf16 && !kScale ? kMapBF16 : kMapF16;
+  const void* x = a.x;
+  if (kScale && T::kBf16) {
+    x = a.x16;
+    const cudaError_t e = launch_pdl(scale_kernel, dim3(a.T), dim3(256), 0, s, a.x, a.x16, a.x_scales, a.H);
+    if (e != cudaSuccess) return e;
+  } else {
+    a.x_scales = nullptr;
+  }
   const uint64_t es = FP8 ? 1 : 2, H = a.H, I = a.I, G = a.G, P = (uint64_t)a.T * a.K;
   Maps m;
   {
@@ -771,14 +884,14 @@ cudaError_t launch_t(const LayerArgs& a, const void* w13, const void* w2, int sm
     const bool whole = H % 64 == 0;
     const uint64_t d[] = {whole ? 64 : H, (uint64_t)a.T, whole ? H / 64 : 1}, st[] = {2 * H, whole ? 128 : 2 * H * a.T};
     const uint32_t b[] = {64, (uint32_t)(a.T + 7) / 8 * 8, whole ? (uint32_t)kBlocks<FP8, RU> : 1};
-    if (!make_map(&m.x, a.x, token, 3, d, st, b)) return cudaErrorUnknown;
+    if (!make_map(&m.x, x, token, 3, d, st, b)) return cudaErrorUnknown;
   }
   const bool whole = I % 64 == 0;
-  const uint64_t d[] = {whole ? 64 : I, P, 2, whole ? I / 64 : 1};
+  const uint64_t d[] = {whole ? 64 : I, P, kScale ? 1 : 2, whole ? I / 64 : 1};
   const uint64_t st[] = {2 * I, 2 * I * P, whole ? 128 : 4 * I * P};
   CUtensorMap* const to[] = {&m.h.rows8, &m.h.rows16, &m.h.rows32};
   for (int k = 0; k < 3 && 8 << k <= M; ++k) {
-    const uint32_t b[] = {64, 8u << k, 2, whole ? (uint32_t)kBlocks<FP8, RD> : 1};
+    const uint32_t b[] = {64, 8u << k, kScale ? 1 : 2, whole ? (uint32_t)kBlocks<FP8, RD> : 1};
     if (!make_map(to[k], a.h, token, 4, d, st, b)) return cudaErrorUnknown;
   }
   const cudaError_t e = launch_up<T, FP8, NB, RU>(a, m, sms, s);
@@ -813,6 +926,18 @@ int validate(const cq_moe_config* c) {
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// The workspace: h, and for fp8 weights its scales, the tokens' and the scaled tokens.
+struct Layout {
+  size_t h_scales, x_scales, x16, bytes;
+  explicit Layout(const cq_moe_config& c) {
+    const size_t P = (size_t)c.tokens * c.topk;
+    h_scales = align256(4 * P * c.inter);
+    x_scales = h_scales + (c.w_dtype ? align256(4 * P * ((c.inter + 63) / 64)) : 0);
+    x16 = x_scales + (c.w_dtype ? 256 : 0);  // 64 floats
+    bytes = x16 + (c.w_dtype ? align256(2 * (size_t)c.tokens * c.hidden) : 0) + 256;
+  }
+};
+
 }  // namespace
 
 int layer_status(uint32_t* status, cudaStream_t s) { return read_status_word(g_status, status, s); }
@@ -828,7 +953,7 @@ int cq_check_moe_config(const cq_moe_config* cfg) { return validate(cfg); }
 
 size_t cq_moe_workspace_size(const cq_moe_config* cfg) {
   if (validate(cfg) != CQ_OK) return 0;
-  return cq::align256(4 * (size_t)cfg->tokens * cfg->topk * cfg->inter) + 256;
+  return Layout(*cfg).bytes;
 }
 
 int cq_moe_layer(const cq_moe_config* cfg, const void* x, const int32_t* expert_ids,
@@ -863,7 +988,12 @@ int cq_moe_layer(const cq_moe_config* cfg, const void* x, const int32_t* expert_
   a.mask = x_active_mask;
   a.w13_scales = w13_scales;
   a.w2_scales = w2_scales;
-  a.h = static_cast<uint16_t*>(workspace);
+  const Layout at(*cfg);
+  char* ws = static_cast<char*>(workspace);
+  a.h = reinterpret_cast<uint16_t*>(ws);
+  a.h_scales = reinterpret_cast<float*>(ws + at.h_scales);
+  a.x_scales = reinterpret_cast<float*>(ws + at.x_scales);
+  a.x16 = reinterpret_cast<uint16_t*>(ws + at.x16);
   a.y = y;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = cfg->x_dtype == 1

@@ -54,9 +54,13 @@ def check_codes(codes, scales, v, bv, what="", e5m2=False):
         assert bool((over <= 0).all()), (what, b, float(over.max()))
 
 
-def layer(x, ids, scales, mask, w13, w2, out_dtype, h_dtype):
+def layer(x, ids, scales, mask, w13, w2, out_dtype, h_dtype, scaled=False):
     """(y, bound) of the whole layer; ids < 0 or masked pairs count nothing. Between the products h is held as two
-    numbers of h_dtype: the second is rounded, and what is left is 2^-2p of h, or half the smallest subnormal."""
+    numbers of h_dtype: the second is rounded, and what is left is 2^-2p of h, or half the smallest subnormal.
+    `scaled` (fp8 weights, more than 8 tokens): x times a power of two that brings its row's largest value to 2^14 at
+    least is rounded to fp16, exact for bf16 and fp16 values but below the normal range, where half a step is 2^-25, so
+    2^-39 of that largest value; h is rounded to fp16 with such a factor for 64 of it: 2^-11 of a value, 2^-39 of the 64's
+    largest (of all of h's here)."""
     t, k = ids.shape
     y = torch.zeros(t, w2.shape[1], dtype=torch.float64)
     b = torch.zeros_like(y)
@@ -66,8 +70,13 @@ def layer(x, ids, scales, mask, w13, w2, out_dtype, h_dtype):
             if e < 0 or e >= w13.shape[0] or (mask is not None and not bool(mask[i, j])):
                 continue
             p, bp = ref.products(x[i: i + 1].double(), w13[e: e + 1], [1], slack(x.shape[1]))
+            if scaled:
+                bp = bp + 2.0 ** -39 * x[i].double().abs().max() * w13[e].abs().sum(1)
             h, bh = ref.swiglu(p, bp)
-            bh = bh + ref.U[h_dtype] ** 2 * (h.abs() + bh) + ref.TINY[h_dtype]
+            if scaled:
+                bh = bh + 2.0 ** -11 * (h.abs() + bh) + 2.0 ** -39 * (h.abs() + bh).max()
+            else:
+                bh = bh + ref.U[h_dtype] ** 2 * (h.abs() + bh) + ref.TINY[h_dtype]
             v = (h @ w2[e].T)[0]
             # twice the terms: two numbers a value
             bv = (bh @ w2[e].abs().T)[0] + 2 * h.shape[1] * slack(h.shape[1]) * ((h.abs() + bh) @ w2[e].abs().T)[0]

@@ -45,7 +45,8 @@ def _run(cfg, x, ids, sc, w13, w2, mask=None, **kw):
 def _check(cfg, got, x, ids, sc, w13, w2, mask=None):
     dt = DT[cfg.x_dtype]
     pairs = None if mask is None else mask if mask.dim() == 2 else mask[:, None].expand(ids.shape)
-    y, bound = around.layer(x, ids, sc, pairs, _values(w13, 2), _values(w2, 1), torch.float32 if cfg.out_dtype else dt, dt)
+    y, bound = around.layer(x, ids, sc, pairs, _values(w13, 2), _values(w2, 1), torch.float32 if cfg.out_dtype else dt, dt,
+                            scaled=cfg.w_dtype == 1 and cfg.tokens > 8)
     ref.check(got, y, bound)
 
 
@@ -162,6 +163,42 @@ def test_large_and_small_gates():
         t = ((x.float() * scale).bfloat16(), ids, sc, w13, w2)
         cfg = cq.MoeConfig(T, G, K, H, N, out_dtype=1)
         _check(cfg, _run(cfg, *t), *t)
+
+
+@pytest.mark.parametrize("scale", [1e9, 1e-10])
+@pytest.mark.parametrize("T", [3, 12, 40])
+def test_rows_far_from_one(T, scale):
+    """bf16 tokens and SwiGLU results beyond fp16's range, fp8 weights: no infinity on the way, small results kept."""
+    G, K, H, N = 3, 2, 208, 144
+    x, ids, sc, w13, w2 = _inputs("far", T, G, K, H, N, 0, True)
+    x = x.double() * scale
+    x[0] *= 1e-3
+    t = (x.bfloat16(), ids, sc, w13, w2)
+    cfg = cq.MoeConfig(T, G, K, H, N, w_dtype=1, out_dtype=1)
+    _check(cfg, _run(cfg, *t), *t)
+
+
+def test_infinities_among_many_tokens():
+    """The same among more than 8 tokens, whose rows and results are scaled: an infinite token spoils its own row
+    alone, a NaN code of a weight the columns that it feeds."""
+    T, G, K, H, N = 20, 2, 1, 272, 144
+    x, ids, sc, w13, w2 = _inputs("inf2", T, G, K, H, N, 0, True)
+    ids[:] = 0
+    cfg = cq.MoeConfig(T, G, K, H, N, w_dtype=1)
+    clean = _run(cfg, x, ids, sc, w13, w2)
+    bad = x.clone()
+    bad[2, 5] = float("inf")
+    y = _run(cfg, bad, ids, sc, w13, w2)
+    keep = [t for t in range(T) if t != 2]
+    assert torch.equal(y[keep], clean[keep]) and not torch.isfinite(y[2]).any()
+    c2 = w2[0].clone()
+    c2[0, 33, 70] = 0xff
+    y = _run(cfg, x, ids, sc, w13, (c2, w2[1]))
+    other = [o for o in range(H) if o != 33]
+    assert torch.isnan(y[:, 33]).all() and torch.equal(y[:, other], clean[:, other])
+    c13 = w13[0].clone()
+    c13[0, 20, 3] = 0x7f
+    assert torch.isnan(_run(cfg, x, ids, sc, (c13, w13[1]), w2)).all()
 
 
 def test_streams_graphs_and_repeats():
