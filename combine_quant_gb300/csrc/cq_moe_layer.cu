@@ -20,7 +20,7 @@
 // keeps 16 bits or more: rounding them to one would add an error as large as y's own
 // rounding. The second kernel's copies of weights start before the first one has ended.
 //
-// fp8 weights and more than 8 tokens: the products are bound by instructions, and a code
+// fp8 weights and large tiles: the products are bound by instructions, and a code
 // becomes an fp16 number in half of one, a bf16 number in two and a half. So the products
 // run in fp16 there, whose range powers of two provide: each token's row is scaled by one
 // (scale_kernel, where tokens are bf16; exact but for values 2^-38 below the row's largest),
@@ -898,15 +898,19 @@ cudaError_t launch_t(LayerArgs a, const void* w13, const void* w2, int sms, cuda
   return e == cudaSuccess ? launch_down<T, FP8, NB, RD>(a, m, sms, s) : e;
 }
 
-// Few tokens: small tiles, so that all SMs have work, two CTAs each. More tokens: tiles
-// of four times the rows, since every tile fetches its tokens' rows, and sixteen warps.
+// Tiles of 128 rows and sixteen warps, one CTA a SM, where that gives each SM a unit of the
+// up kernel (hidden 7168, inter 2048, bf16, 8 tokens: 366 us against 383 with tiles of 32
+// rows and two CTAs a SM; fp8, 2 tokens: 131 against 132, 8 tokens: 244 against 269), else
+// the small ones (hidden 1024, inter 512, 8 tokens: 14.3 against 19.2). fp16 tokens with
+// fp8 weights need no cheaper decoding: small tiles up to 4 tokens (2: 112 against 128).
 // The down kernel takes tiles of 96 rows where those and their clusters cover more SMs
-// (hidden 7168: 150 of 152 instead of 112; 64 tokens, fp8: 491 -> XX us).
+// (hidden 7168: 150 of 152 instead of 112; 64 tokens, bf16: 524 -> 494 us).
 template <typename T, bool FP8>
 cudaError_t launch(const LayerArgs& a, const void* w13, const void* w2, cudaStream_t s) {
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorUnknown;
-  if (a.T <= 8) return launch_t<T, FP8, 1, 1, 1>(a, w13, w2, sms, s);
+  const bool units = (int64_t)std::min(a.G, a.T * a.K) * ((a.I + 63) / 64) >= sms;
+  if (a.T <= 8 && (!units || (FP8 && !T::kBf16 && a.T <= 4))) return launch_t<T, FP8, 1, 1, 1>(a, w13, w2, sms, s);
   const DownGrid g3(a.H, 96, sms), g4(a.H, 128, sms);
   const bool three = g3.tiles * g3.cluster > g4.tiles * g4.cluster;
   if (a.T <= 16)

@@ -482,8 +482,8 @@ int cq_check_expert_b128_config(const cq_expert_config* cfg);
  * its inputs. */
 
 /*
- * cq_moe_layer -- the whole layer for a few tokens (decoding), in two kernels (three
- * with fp8 weights, bf16 tokens and more than 8 of them): no dispatch, no rows in between.
+ * cq_moe_layer -- the whole layer for a few tokens (decoding), in two kernels (fp8
+ * weights and bf16 tokens: three at most): no dispatch, no rows in between.
  *   y[t] = sum over j < K of w[t, j] * W2[e] SwiGLU(W13[e] x[t]),  e = ids[t, j]
  * What it reads is the weights of the experts that the tokens name, each once
  * for up to 32 tokens (their second 32 from L2). Expert ids count from 0 to
@@ -523,8 +523,8 @@ size_t cq_moe_workspace_size(const cq_moe_config* cfg); /* bytes; 0 for an inval
  * overlap inputs. Products are summed in 32 bits, SwiGLU and the weighted sum taken
  * of unrounded products. Between the two products SwiGLU's result is held as the
  * sum of two numbers of x's type (16 bits or more of precision), so with fp16
- * it is infinite above 65504; with fp8 weights and more than 8 tokens as one fp16
- * number (11 bits) with a power of two for 64 of them.
+ * it is infinite above 65504. With fp8 weights it may be held as one fp16 number
+ * (11 bits) with a power of two for 64 of them instead.
  */
 int cq_moe_layer(const cq_moe_config* cfg, const void* x, const int32_t* expert_ids,
                  const float* expert_scales, const uint8_t* x_active_mask, const void* w13,

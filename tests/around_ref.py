@@ -57,7 +57,7 @@ def check_codes(codes, scales, v, bv, what="", e5m2=False):
 def layer(x, ids, scales, mask, w13, w2, out_dtype, h_dtype, scaled=False):
     """(y, bound) of the whole layer; ids < 0 or masked pairs count nothing. Between the products h is held as two
     numbers of h_dtype: the second is rounded, and what is left is 2^-2p of h, or half the smallest subnormal.
-    `scaled` (fp8 weights, more than 8 tokens): x times a power of two that brings its row's largest value to 2^14 at
+    `scaled` (fp8 weights, where the kernel may do so): x times a power of two that brings its row's largest value to 2^14 at
     least is rounded to fp16, exact for bf16 and fp16 values but below the normal range, where half a step is 2^-25, so
     2^-39 of that largest value; h is rounded to fp16 with such a factor for 64 of it: 2^-11 of a value, 2^-39 of the 64's
     largest (of all of h's here)."""

@@ -46,7 +46,7 @@ def _check(cfg, got, x, ids, sc, w13, w2, mask=None):
     dt = DT[cfg.x_dtype]
     pairs = None if mask is None else mask if mask.dim() == 2 else mask[:, None].expand(ids.shape)
     y, bound = around.layer(x, ids, sc, pairs, _values(w13, 2), _values(w2, 1), torch.float32 if cfg.out_dtype else dt, dt,
-                            scaled=cfg.w_dtype == 1 and cfg.tokens > 8)
+                            scaled=cfg.w_dtype == 1)
     ref.check(got, y, bound)
 
 
@@ -85,10 +85,12 @@ def test_all_tokens_at_one_expert(T, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("shape", [(2, 4, 2, 7168, 256), (5, 3, 2, 256, 4112), (20, 2, 2, 2064, 2064)], ids=str)
-def test_long_rows(shape, fp8):
-    t = _inputs("long", *shape, 0, fp8)
-    cfg = cq.MoeConfig(*shape, w_dtype=int(fp8), out_dtype=1)
+@pytest.mark.parametrize("x_dtype", [0, 1])
+@pytest.mark.parametrize("shape", [(2, 4, 2, 7168, 256), (5, 3, 2, 256, 4112), (20, 2, 2, 2064, 2064), (1, 40, 8, 144, 1296),
+                                   (3, 30, 6, 272, 1024), (8, 30, 2, 96, 720)], ids=str)
+def test_long_rows(shape, x_dtype, fp8):
+    t = _inputs("long", *shape, x_dtype, fp8)
+    cfg = cq.MoeConfig(*shape, x_dtype=x_dtype, w_dtype=int(fp8), out_dtype=1)
     _check(cfg, _run(cfg, *t), *t)
 
 
@@ -179,7 +181,7 @@ def test_rows_far_from_one(T, scale):
 
 
 def test_infinities_among_many_tokens():
-    """The same among more than 8 tokens, whose rows and results are scaled: an infinite token spoils its own row
+    """The same with rows and results that are scaled: an infinite token spoils its own row
     alone, a NaN code of a weight the columns that it feeds."""
     T, G, K, H, N = 20, 2, 1, 272, 144
     x, ids, sc, w13, w2 = _inputs("inf2", T, G, K, H, N, 0, True)
