@@ -583,27 +583,30 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
         if constexpr (DX && ACT) {
           const uint16_t* pre = static_cast<const uint16_t*>(a.pre_in) + row * 2 * a.out_cols + i0;
           uint16_t* out = static_cast<uint16_t*>(a.out) + row * 2 * a.out_cols + i0;
+          uint32_t g[2][8], u[2][8];  // the next 16 columns' are read ahead
+          auto load = [&](int k) {
+            if (32 * chunks <= 16 * k || 16 * k >= left) return;
+            load32(pre + 16 * k, g[k & 1], wide);
+            load32(pre + a.out_cols + 16 * k, u[k & 1], wide);
+          };
+          load(0);
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
+          for (int k = 0; k < 8; ++k) {
+            if (k + 1 < 8) load(k + 1);
+            if (32 * chunks <= 16 * k || 16 * k >= left) continue;
+            uint32_t(&gk)[8] = g[k & 1];
+            uint32_t(&uk)[8] = u[k & 1];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int c = 32 * m + 16 * h;
-              if (m >= chunks || c >= left) break;
-              uint32_t g[8], u[8];
-              load32(pre + c, g, wide);
-              load32(pre + a.out_cols + c, u, wide);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const Pair d = acc[m][8 * h + k];
-                float dg0, du0, dg1, du1;
-                swiglu_gradient(lo_of(d), T::lo(g[k]), T::lo(u[k]), dg0, du0);
-                swiglu_gradient(hi_of(d), T::hi(g[k]), T::hi(u[k]), dg1, du1);
-                g[k] = T::pack2(dg0, dg1);
-                u[k] = T::pack2(du0, du1);
-              }
-              store32(out + c, g, wide);
-              store32(out + a.out_cols + c, u, wide);
+            for (int c = 0; c < 8; ++c) {
+              const Pair d = acc[k / 2][8 * (k & 1) + c];
+              float dg0, du0, dg1, du1;
+              swiglu_gradient(lo_of(d), T::lo(gk[c]), T::lo(uk[c]), dg0, du0);
+              swiglu_gradient(hi_of(d), T::hi(gk[c]), T::hi(uk[c]), dg1, du1);
+              gk[c] = T::pack2(dg0, dg1);
+              uk[c] = T::pack2(du0, du1);
             }
+            store32(out + 16 * k, gk, wide);
+            store32(out + a.out_cols + 16 * k, uk, wide);
           }
         } else if constexpr (OUT8) {
           float top = 0.f;

@@ -87,9 +87,10 @@ constexpr int kStageW = kBoxes<RG> * 32 * RG * 128;  // weights of a stage
 // Products in fp16 with powers of two taken out.
 template <bool FP8, int RG>
 constexpr bool kScaled = FP8 && RG > 1;
-// Sums of every share of k, or (many tokens and rows) one that the shares add to in turn.
-template <int RG>
-constexpr bool kTurns = RG > 1;
+// Sums of every share of k, or (more than 16 tokens, large tiles) one that the shares add to
+// in turn.
+template <int RG, int NB>
+constexpr bool kTurns = RG > 1 && NB > 2;
 constexpr int kMaxWarps = kThreads<4> / 32;
 constexpr int kMaxPairs = 64 * 16, kMaxItems = kMaxPairs + 32;
 
@@ -536,12 +537,12 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
         for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float* to = red + ((kTurns<RG> ? 0 : seg * kRows) + row + 16 * f + 8 * (i >> 1)) * (M + 1) + 8 * n +
+            float* to = red + ((kTurns<RG, NB> ? 0 : seg * kRows) + row + 16 * f + 8 * (i >> 1)) * (M + 1) + 8 * n +
                         fragment_column<FP8>(2 * c + (i & 1));
             *to = first ? acc[f][n][i] : *to + acc[f][n][i];
           }
     };
-    if constexpr (kTurns<RG>) {
+    if constexpr (kTurns<RG, NB>) {
       for (int q = 0; q < SEGS && ok; ++q) {
         if (q == seg) put(q == 0);
         ok = async::meet<32 * WARPS>(ok);
@@ -558,7 +559,7 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
       const float* p = red + (32 * (o / 16) + o % 16) * (M + 1) + j;
       float pg = 0.f, pu = 0.f;
 #pragma unroll
-      for (int q = 0; q < (kTurns<RG> ? 1 : SEGS); ++q) {
+      for (int q = 0; q < (kTurns<RG, NB> ? 1 : SEGS); ++q) {
         pg += p[q * kRows * (M + 1)];
         pu += p[(q * kRows + 16) * (M + 1)];
       }
@@ -610,7 +611,7 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
   constexpr bool SCALED = kScaled<FP8, RG>;
   constexpr int PARTS = SCALED ? 1 : 2, kTokens = BLOCKS * PARTS * M * 128;  // the numbers' lines
   using M16 = std::conditional_t<SCALED, F16, T>;  // of the products
-  constexpr int kSums = kTurns<RG> ? 1 : SEGS;
+  constexpr int kSums = kTurns<RG, NB> ? 1 : SEGS;
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Ring ring;
   __shared__ Items items;
@@ -732,12 +733,12 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
             const int j = 8 * n + fragment_column<FP8>(2 * c + i);
             if (j >= m) continue;
             const float wt = items.weight[off + j];
-            float* to = sums + ((kTurns<RG> ? 0 : seg * a.T) + items.tok[off + j]) * kLine + row;
+            float* to = sums + ((kTurns<RG, NB> ? 0 : seg * a.T) + items.tok[off + j]) * kLine + row;
 #pragma unroll
             for (int r = 0; r < 4; ++r) to[8 * r] = fmaf(wt, acc[r >> 1][n][2 * (r & 1) + i], to[8 * r]);
           }
       };
-      if constexpr (kTurns<RG>) {
+      if constexpr (kTurns<RG, NB>) {
         for (int q = 0; q < SEGS && ok; ++q) {
           if (q == seg) add();
           ok = async::meet<32 * WARPS>(ok);
@@ -748,7 +749,7 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
     }
   }
   __syncthreads();
-  if constexpr (!kTurns<RG>) {
+  if constexpr (!kTurns<RG, NB>) {
     for (int v = threadIdx.x; v < a.T * kLine; v += kThreads<RG>) {
       float t = sums[v];
 #pragma unroll
@@ -808,7 +809,7 @@ template <typename T, bool FP8, int NB, int RG>
 cudaError_t launch_up(LayerArgs a, const Maps& maps, int sms, cudaStream_t s) {
   constexpr auto kernel = up_kernel<T, FP8, NB, RG>;
   constexpr int kRows = 32 * RG, M = 8 * NB, kPerSm = RG == 1 ? 2 : 1;
-  constexpr size_t rest = 4 * (kTurns<RG> ? 1 : kSegs<RG>) * kRows * (M + 1);
+  constexpr size_t rest = 4 * (kTurns<RG, NB> ? 1 : kSegs<RG>) * kRows * (M + 1);
   const size_t stage = kStageW<RG> + kBlocks<FP8, RG> * ((a.T + 7) / 8 * 8) * 128;
   a.stages = fit_stages(rest, stage, kPerSm);
   a.whole = a.H % 64 == 0;
@@ -828,7 +829,7 @@ cudaError_t launch_down(LayerArgs a, const Maps& maps, int sms, cudaStream_t s) 
   constexpr auto kernel = down_kernel<T, FP8, NB, RG>;
   constexpr int kRows = 32 * RG, M = 8 * NB, kPerSm = RG == 1 ? 2 : 1;
   constexpr size_t stage = kStageW<RG> + kBlocks<FP8, RG> * (kScaled<FP8, RG> ? 1 : 2) * M * 128;
-  const size_t rest = 4 * (size_t)(kTurns<RG> ? 1 : kSegs<RG>) * a.T * (kRows + 1);
+  const size_t rest = 4 * (size_t)(kTurns<RG, NB> ? 1 : kSegs<RG>) * a.T * (kRows + 1);
   a.stages = fit_stages(rest, stage, kPerSm);
   a.whole = a.I % 64 == 0;
   const size_t smem = 1024 + a.stages * stage + rest;
