@@ -67,7 +67,7 @@ constexpr int kAllRegs = 128 * kOtherRegs + 32 * kDrainWarps * kDrainRegs;
 static_assert(kAllRegs <= 168 * kThreads, "setmaxnreg would wait forever");
 constexpr int kFew = 128;                  // most rows of a tile with tokens on the columns
 constexpr int kEntry = 4;                  // blocks in an entry of the scales' ring
-constexpr int kScaleRing = 4;
+constexpr int kScaleRing = 3;
 constexpr int kScaleFloats = kEntry * 128 + kEntry * 2;  // the rows', and two of the weights
 constexpr uint32_t kTmemCols = 512;
 constexpr int kBand = 8;                   // tiles along i taken together, for reuse in L2
@@ -80,6 +80,7 @@ struct Bars {
   uint64_t full[kStages], empty[kStages];
   uint64_t tfull[2], tempty[2];
   uint64_t sfull[kScaleRing], sempty[kScaleRing];
+  uint64_t few_top[2];  // the same of tokens on the columns, by the warps' half
   uint64_t top[4];  // fp8 results: the largest values of a quarter's two warps
   uint64_t done;    // the products in flight when their warp gave up
   uint32_t tmem;
@@ -110,7 +111,8 @@ __device__ __forceinline__ Tile tile_at(const B128Args& a, const int* s_begin, c
   x.i0 = ti * kOuts;
   const int outs = (min(kOuts, a.out_cols - x.i0) + 31) / 32 * 32;
   x.cols = GATES ? 2 * outs : outs;
-  x.few = !OUT8 && x.rows <= kFew;
+  // (fp8 results: unless a group of 128 outputs would end within a CTA's rows)
+  x.few = x.rows <= kFew && (!OUT8 || GATES || x.cols <= 128 || x.cols == 256);
   x.jh = (x.rows + 1) / 2;
   if (x.few) x.jh = (x.jh + 7) / 8 * 8;
   return x;
@@ -214,6 +216,7 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Bars bars;
   __shared__ float s_top[OUT8 && kGates ? 2 * 2 * 128 : 1];
+  __shared__ float s_few[OUT8 ? 2 * 8 * kFew : 1];  // [turn][warp][token]
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
   float* s_scales = reinterpret_cast<float*>(ring + kStages * kStageBytes);
   int* s_begin = reinterpret_cast<int*>(s_scales + kScaleRing * kScaleFloats);
@@ -233,6 +236,7 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
       mbar_init(&bars.tempty[b], kDrainWarps * 2);
     }
     for (int q = 0; q < 4; ++q) mbar_init(&bars.top[q], 2);
+    for (int h = 0; h < 2; ++h) mbar_init(&bars.few_top[h], 8);
     for (int s = 0; s < kScaleRing; ++s) {
       mbar_init(&bars.sfull[s], 64);
       mbar_init(&bars.sempty[s], kDrainWarps);
@@ -386,14 +390,14 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDrainRegs));
     const int q = warp & 3, half = (warp - 4) >> 2;
     const bool wide = a.wide;
-    uint32_t buf = 0, se = 0, se_lap = 0, nth = 0;  // nth: tiles so far
+    uint32_t buf = 0, se = 0, se_lap = 0, nth = 0, nth_few = 0;  // nth: tiles so far
     // what a warp does for every block is kept short: longer code is fetched too slowly
     const uint32_t release[2] = {lead(&bars.tempty[0]), lead(&bars.tempty[1])};
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     bool ok = true;
     for (int t = first; t < n_tiles && ok; t += step) {
       const Tile x = tile_at<kGates, OUT8>(a, s_begin, s_tile, t);
-      if (!OUT8 && x.few) {
+      if (x.few) {
         // ---- tokens on the columns, weight rows on the lanes ----
         const int c0 = half * x.jh, chunks = (x.jh + 15) / 16;  // this warp's columns, 16 a chunk
         Pair sum[4][8];
@@ -450,6 +454,71 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
         // Lanes lie along the results' rows: 2 bytes each, 64 (SwiGLU: 32) together.
         const int i = kGates ? x.i0 + (int)rank * x.cols / 4 + 16 * q + (lane & 15) : x.i0 + (int)rank * x.cols / 2 + l;
         const bool in = l < x.cols / 2 && i < a.out_cols;
+        if constexpr (OUT8) {
+          // The largest value of each token's group: over the lanes, then over the quarters and
+          // (one group on both CTAs' lanes) the CTAs. Every warp tells both CTAs. Two buffers by
+          // the tiles' turn: who writes the next but one has seen all arrive for the next, and
+          // they had read this one.
+          const bool joint = kGates || x.cols <= 128, mine = in && (!kGates || lane < 16);
+          float* tb = s_few + (nth_few & 1) * 8 * kFew + c0;
+          const int from = joint ? (int)rank * 4 + q : q;
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            if (m >= chunks) break;
+            float tops = 0.f;  // of token 16 m + lane
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              Pair& p = sum[m][k / 2];
+              float v = k & 1 ? hi_of(p) : lo_of(p);
+              if constexpr (kGates) {
+                const float u = __shfl_xor_sync(~0u, v, 16);
+                if (a.pre_out && in && 16 * m + k < x.jh && c0 + 16 * m + k < x.rows)
+                  static_cast<uint16_t*>(a.pre_out)[((size_t)x.row0 + c0 + 16 * m + k) * 2 * a.n + (lane >= 16 ? a.n : 0) + i] =
+                      (uint16_t)T::pack2(v, 0.f);
+                v = swiglu(v, u);  // of use in lanes 0-15
+                p = k & 1 ? pair_of(lo_of(p), v) : pair_of(v, hi_of(p));
+              }
+              const float t = permute_detail::warp_max(mine ? fabsf(v) : 0.f);
+              if (lane == k) tops = t;
+            }
+            if (lane < 16 && 16 * m + lane < x.jh) {
+              tb[from * kFew + 16 * m + lane] = tops;
+              if (joint)
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr_in(smem_u32(tb + from * kFew + 16 * m + lane), rank ^ 1)),
+                             "f"(tops)
+                             : "memory");
+            }
+          }
+          __syncwarp();
+          if (lane == 0) {
+            arrive_cluster(addr_in(smem_u32(&bars.few_top[half]), rank ^ 1));
+            arrive_cluster(addr_in(smem_u32(&bars.few_top[half]), rank));
+          }
+          if (!(ok = wait(&bars.few_top[half], nth_few & 1, true))) break;
+          ++nth_few;
+          uint8_t* out = static_cast<uint8_t*>(a.out) + ((size_t)x.row0 + c0) * a.out_cols + i;
+          const int group = joint ? x.i0 / 128 : x.i0 / 128 + (int)rank;
+          const bool writes = q == 0 && (!joint || rank == 0) && group < a.nb;
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            if (m >= chunks) break;
+            const int j = 16 * m + (lane & 15);
+            float top = 0.f;
+            if (j < x.jh)
+              for (int w = 0; w < (joint ? 8 : 4); ++w) top = fmaxf(top, tb[w * kFew + j]);
+            const float s = __fdiv_rn(448.f, top), mult = top == 0.f ? 0.f : s;
+            if (writes && lane < 16 && j < x.jh && c0 + j < x.rows) a.ys[((size_t)x.row0 + c0 + j) * a.nb + group] = __fdiv_rn(1.f, s);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float v = k & 1 ? hi_of(sum[m][k / 2]) : lo_of(sum[m][k / 2]);
+              const float f = __shfl_sync(~0u, mult, k);
+              if (mine && 16 * m + k < x.jh && c0 + 16 * m + k < x.rows)
+                out[(size_t)(16 * m + k) * a.out_cols] = (uint8_t)permute_detail::e4m3x2(__fmul_rn(v, f), 0.f);
+            }
+          }
+          ++nth;
+          continue;
+        }
         const int count = in ? min(x.jh, x.rows - c0) : 0;  // of this warp's tokens
         const size_t ld = kGates || (DX && ACT) ? 2 * (size_t)a.out_cols : a.out_cols;
         const size_t at = ((size_t)x.row0 + c0) * ld + i;

@@ -163,6 +163,25 @@ def test_many_experts_and_running_sums():
     ref.check(y, want, bound)
 
 
+@pytest.mark.parametrize("act", [0, 1])
+def test_many_experts_into_fp8(act):
+    """The longest lists of experts beside the results' exchange, and tiles of few rows."""
+    counts = [0] * 2048
+    for e in (0, 3, 700, 2047):
+        counts[e] = 5 + e % 7
+    n, k = 272, 160
+    t = _inputs("many8", counts, 0, k, 1 + act, n, k, 2, 0)
+    cfg = cq.ExpertConfig(experts=2048, rows=sum(counts), n=n, k=k, x_dtype=2, act=act)
+    s = torch.empty(sum(counts), 3, device=DEV)
+    q = cq.expert_matmul_b128(cfg, *(a.to(DEV) for a in t), _counts(counts), y_scales=s)
+    live = [e for e, c in enumerate(counts) if c]
+    xv = around.rows_values(t[0], t[1])
+    wv = around.block_values(t[2][live], t[3][live], 1 + act)
+    v, bv = ref.products(xv, wv, [counts[e] for e in live], around.slack(k))
+    around.check_codes(q, s, *(ref.swiglu(v, bv) if act else (v, bv)))
+    assert cq.read_expert_status() == 0
+
+
 @pytest.mark.parametrize("bad,cut", [([3, -2, 4, 1], [3, 0, 4, 1]), ([3, 20, 4, 1], [3, 9, 0, 0]),
                                      ([1 << 40, 1, 1, 1], [12, 0, 0, 0])])
 def test_bad_counts_are_cut_and_reported(bad, cut):
