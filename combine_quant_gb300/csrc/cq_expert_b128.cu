@@ -401,7 +401,7 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDrainRegs));
     const int q = warp & 3, half = (warp - 4) >> 2;
     const bool wide = a.wide;
-    uint32_t buf = 0, se = 0, se_lap = 0, nth = 0, nth_few = 0;  // nth: tiles so far
+    uint32_t buf = 0, se = 0, se_lap = 0, nth = 0, nth_few = 0;  // tiles so far, of either kind
     // what a warp does for every block is kept short: longer code is fetched too slowly
     const uint32_t release[2] = {lead(&bars.tempty[0]), lead(&bars.tempty[1])};
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
@@ -527,7 +527,6 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
                 out[(size_t)(16 * m + k) * a.out_cols] = (uint8_t)permute_detail::e4m3x2(__fmul_rn(v, f), 0.f);
             }
           }
-          ++nth;
           continue;
         }
         const int count = in ? min(x.jh, x.rows - c0) : 0;  // of this warp's tokens
@@ -564,7 +563,6 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
             }
           }
         }
-        ++nth;
         continue;
       }
       const int jh = x.jh, rows = rank ? x.rows - jh : jh;  // of this CTA

@@ -149,6 +149,25 @@ def test_long_rows(counts, n, k, act):
     ref.check(*_finite(y, want, bound, torch.bfloat16))
 
 
+@pytest.mark.parametrize("act", [0, 1])
+def test_long_and_short_tiles_in_turn(act):
+    """Every pair of CTAs gets tiles of both kinds, with tokens on the lanes and on the columns, one after the other: what
+    they hand over in shared memory goes by counts of its own."""
+    counts, n, k = [200, 20, 5, 300, 128, 129] * 4, 2048, 144
+    t = _inputs("turns", counts, 0, k, 1 + act, n, k, 2, 0)
+    d = [a.to(DEV) for a in t]
+    cfg = cq.ExpertConfig(experts=len(counts), rows=sum(counts), n=n, k=k, x_dtype=2, act=act)
+    y = cq.expert_matmul_b128(cfg, *d, _counts(counts))
+    s = torch.empty(sum(counts), 16, device=DEV)
+    q = cq.expert_matmul_b128(cfg, *d, _counts(counts), y_scales=s)
+    assert cq.read_expert_status() == 0
+    xv, wv = _values(t, 2, 0, 1 + act, sum(counts))
+    want, bound, _, _ = ref.forward(xv, wv, counts, act, torch.bfloat16, around.slack(k))
+    ref.check(*_finite(y, want, bound, torch.bfloat16))
+    v, bv = ref.products(xv, wv, counts, around.slack(k))
+    around.check_codes(q, s, *(ref.swiglu(v, bv) if act else (v, bv)))
+
+
 def test_many_experts_and_running_sums():
     """As expert_token_nums gives them with expert_token_nums_type 0."""
     gen = _gen("many")
