@@ -114,6 +114,18 @@ __device__ __forceinline__ bool meet(bool ok) {
       : "memory");
   return all != 0;
 }
+// The same at named barrier `id`.
+template <int THREADS>
+__device__ __forceinline__ bool meet(bool ok, int id) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.and.pred p, %2, %3, q;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(all)
+      : "r"((uint32_t)ok), "r"(id), "n"(THREADS)
+      : "memory");
+  return all != 0;
+}
 
 // Hand a ring slot back to the producer after this warp has read it with
 // ordinary (generic-proxy) shared-memory loads. The next write into the slot

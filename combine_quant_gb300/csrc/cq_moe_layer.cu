@@ -11,7 +11,7 @@
 // Every CTA sorts the (token, expert) pairs itself into items: an expert and up to 8 NB
 // of its tokens, ascending. A token that names an expert twice is one pair with both
 // weights. up_kernel: an item's tile of 16 (64) gates and their ups is one CTA's work;
-// its warps' shares of k are added in shared memory, in order. down_kernel: a tile of 32
+// its warps' shares of k are added through shared memory, in order. down_kernel: a tile of 32
 // (96, 128) output rows is one cluster's work: the CTAs share the stages of all items
 // evenly, each keeps the weighted sums of all tokens, and the CTAs' sums are added
 // through distributed shared memory, in order. Results do not depend on timing. The
@@ -34,8 +34,8 @@
 // 461 -> 367 us).
 //
 // Measured on one GB300 (copy 6.78 TB/s), hidden 7168, inter 2048, 8 of 32 experts, in a
-// graph: 1 token, bf16: 111 us, 6.4 TB/s; 16 tokens: 411 us, 6.9 TB/s; 64 tokens: 478 us,
-// 5.9 TB/s; fp8 weights: 71 us (5.0), 229 us (6.2), 354 us (4.0). Hidden 1024, inter 512, 4
+// graph: 1 token, bf16: 111 us, 6.4 TB/s; 16 tokens: 411 us, 6.9 TB/s; 64 tokens: 479 us,
+// 5.9 TB/s; fp8 weights: 71 us (5.0), 232 us (6.1), 332 us (4.2). Hidden 1024, inter 512, 4
 // tokens: 13 us, most of it the start and end of two kernels.
 #include <cuda_runtime.h>
 
@@ -98,12 +98,23 @@ constexpr int kStageW = kBoxes<RG> * 32 * RG * 128;  // weights of a stage
 // Products in fp16 with powers of two taken out.
 template <bool FP8, int RG>
 constexpr bool kScaled = FP8 && RG > 1;
-// Sums of every share of k, or (more than 16 tokens, large tiles) one that the shares add to
-// in turn; in the down kernel one for two shares.
+// The down kernel's sums: of every share of k, or (more than 16 tokens, large tiles) one that
+// two shares add to in turn. Lines of 4 floats more than rows: neighbouring tokens' lines
+// then begin four banks apart.
 template <int RG, int NB>
 constexpr bool kTurns = RG > 1 && NB > 2;
 template <int RG, int NB>
 constexpr int kDownSums = kTurns<RG, NB> ? kSegs<RG> / 2 : kSegs<RG>;
+template <int RG>
+constexpr int kDownLine = 32 * RG + 4;
+// The up kernel's shares of k meet in shared memory: small tiles, [share][row][token]; large
+// ones, boxes of 16 bytes a lane that the warps of a row group hand over, and what a
+// tile's largest values are found with.
+template <int RG, int NB>
+constexpr int kBoxLines = NB / 2;  // 16-byte pieces a lane and box
+template <int RG, int NB>
+constexpr int kUpFloats = RG == 1 ? kSegs<RG> * 32 * (8 * NB + 1)
+                                  : kWarps<RG> * (NB == 2 ? 3 : 1) * kBoxLines<RG, NB> * 128 + 2 * RG * 32;
 constexpr int kMaxWarps = kThreads<4> / 32;
 constexpr int kMaxPairs = 64 * 16, kMaxItems = kMaxPairs + 32;
 
@@ -129,6 +140,7 @@ template <int PER, int kThreads>
 __device__ __forceinline__ void sort_pairs(const LayerArgs& a, Items& it, uint8_t* scratch, bool report) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, P = a.T * a.K;
   unsigned long long* masks = reinterpret_cast<unsigned long long*>(scratch);  // tokens of each expert
+  uint32_t* words = reinterpret_cast<uint32_t*>(scratch);
   int* ids = reinterpret_cast<int*>(masks + a.G);
   float* scales = reinterpret_cast<float*>(ids + P);
   uint16_t* first = reinterpret_cast<uint16_t*>(scales + P);  // pair of each expert
@@ -146,7 +158,7 @@ __device__ __forceinline__ void sort_pairs(const LayerArgs& a, Items& it, uint8_
     }
     ids[p] = e;
     scales[p] = a.scales[p];
-    if (e >= 0) atomicOr(masks + e, 1ull << (p / a.K));
+    if (e >= 0) atomicOr(words + 2 * e + p / a.K / 32, 1u << (p / a.K % 32));
   }
   __syncthreads();
   const int per = (a.G + kThreads - 1) / kThreads, e0 = min(a.G, t * per), e1 = min(a.G, e0 + per);
@@ -450,6 +462,124 @@ __global__ void __launch_bounds__(256) scale_kernel(const uint16_t* x, uint16_t*
   if (threadIdx.x == 0) scales[blockIdx.x] = ldexpf(1.f, -e);
 }
 
+// A result of SwiGLU as two numbers of the token type.
+template <typename T>
+__device__ __forceinline__ void store_two(const LayerArgs& a, int pair, int i, float r) {
+  const uint16_t hi = rounded<T>(r);
+  uint16_t* to = a.h + (size_t)pair * a.I + i;
+  to[0] = hi;
+  // an infinite first number would make the second NaN
+  to[(size_t)a.T * a.K * a.I] = rounded<T>(fabsf(T::lo(hi)) <= 3.402823466e38f ? r - T::lo(hi) : 0.f);
+}
+
+// Large tiles: the four shares of k of a row group are added, SwiGLU, and the results
+// stored. Of a row group's sums (2 fragments, NB blocks of tokens) each of its warps ends
+// with a quarter: a block of tokens, or (NB 2) the upper or lower rows of one. The others
+// hand it theirs through boxes of shared memory, 16 bytes a lane, warp seg + r in step r.
+// (Adding to one array in turn, where the lanes met in the banks, took 3 us a tile: 43
+// tokens, 17 experts, hidden 2064, inter 752, fp8: 62 us, now 54; 64 tokens, hidden 7168,
+// inter 2048: 350, now 332.) All warps come through the same barriers whatever `ok` is; the result is
+// false where a warp that waits at them gave up.
+template <typename T, bool FP8, int NB, int RG>
+__device__ __forceinline__ bool finish(const LayerArgs& a, const Items& items, int item, int i0, bool ok, int turn,
+                                       float* red, float (&acc)[2][NB][4]) {
+  constexpr int WARPS = kWarps<RG>, PIECES = kBoxLines<RG, NB>;
+  constexpr bool kAll = NB == 2;  // all three boxes of a warp at once
+  static_assert(kSegs<RG> == 4 && (NB == 2 || NB == 4));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 3, seg = warp / RG, group = warp % RG;
+  const int m = items.m[item], n8 = (m + 7) / 8, off = items.off[item];
+  const int block = NB == 4 ? seg : seg >> 1;  // this warp's tokens
+  float4* boxes = reinterpret_cast<float4*>(red) + lane;
+  float* tops = red + WARPS * (kAll ? 3 : 1) * PIECES * 128 + turn * RG * 32;  // [group (and rows' half)][token]
+  auto box = [&](int to, int r) { return boxes + (((kAll ? r - 1 : 0) * RG + group) * 4 + to) * PIECES * 32; };
+  // piece p of quarter q: NB 4, fragment p's four; NB 2, both fragments' of the upper or lower rows
+  auto piece = [&](int q, int p) {
+    if constexpr (NB == 4) return make_float4(acc[p][q][0], acc[p][q][1], acc[p][q][2], acc[p][q][3]);
+    const int n = q >> 1, i = 2 * (q & 1);
+    return make_float4(acc[0][n][i], acc[0][n][i + 1], acc[1][n][i], acc[1][n][i + 1]);
+  };
+  float4 mine[PIECES];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p)
+      if (q == seg) mine[p] = piece(q, p);
+#pragma unroll
+  for (int r = 1; r < 4; ++r) {
+    const int to = (seg + r) & 3;
+    float4* there = box(to, r);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q == to && (NB == 4 ? q : q >> 1) < n8)
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p) there[32 * p] = piece(q, p);
+    if (kAll && r < 3) continue;
+    ok = async::meet<32 * 4>(ok, 2 + group);
+    if (block < n8) {
+#pragma unroll
+      for (int b = kAll ? 1 : r; b <= r; ++b)
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p) {
+          const float4 v = box(seg, b)[32 * p];
+          mine[p].x += v.x, mine[p].y += v.y, mine[p].z += v.z, mine[p].w += v.w;
+        }
+    }
+    ok = async::meet<32 * 4>(ok, 2 + group);  // the boxes are read
+  }
+  // value [h][i]: row fragment_row(lane / 4) + 8 * (NB 4: h, else seg & 1), token 8 block + column(2 c + i)
+  constexpr int HALVES = NB / 2;
+  float v[HALVES][2];
+  const int first = 16 * group + fragment_row(lane >> 2) + (NB == 4 ? 0 : 8 * (seg & 1));
+  const bool in = i0 + 16 * group < a.I && block < n8;  // whole groups: I is a multiple of 16
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = 8 * block + fragment_column<FP8>(2 * c + i);
+    const float f = kScaled<FP8, RG> && a.x_scales && in && j < m ? a.x_scales[items.tok[off + j]] : 1.f;
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h) {
+      float g, w;
+      if constexpr (NB == 4) {
+        const float gs[4] = {mine[0].x, mine[0].y, mine[0].z, mine[0].w};
+        const float us[4] = {mine[1].x, mine[1].y, mine[1].z, mine[1].w};
+        g = gs[2 * h + i], w = us[2 * h + i];
+      } else {
+        g = i ? mine[0].y : mine[0].x, w = i ? mine[0].w : mine[0].z;
+      }
+      v[h][i] = swiglu(g * f, w * f);
+      if (!kScaled<FP8, RG> && in && j < m) store_two<T>(a, off + j, i0 + first + 8 * h, v[h][i]);
+    }
+  }
+  if constexpr (kScaled<FP8, RG>) {
+    // a pair's 64 results have one power of two
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float top = 0.f;
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h)
+        if (in && fabsf(v[h][i]) <= 3.402823466e38f) top = fmaxf(top, fabsf(v[h][i]));
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+      // NB 2: the two warps of a block of tokens have a line each
+      if (lane < 4) tops[(group * (4 / NB) + (NB == 4 ? 0 : seg & 1)) * 8 * NB + 8 * block + fragment_column<FP8>(2 * c + i)] = top;
+    }
+    ok = async::meet<32 * WARPS>(ok);
+    const int units = (a.I + 63) / 64;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = 8 * block + fragment_column<FP8>(2 * c + i);
+      float top = 0.f;
+#pragma unroll
+      for (int q = 0; q < RG * (4 / NB); ++q) top = fmaxf(top, tops[q * 8 * NB + j]);
+      if (!in || j >= m) continue;
+      const int e = f16_exponent(top);
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) a.h[(size_t)(off + j) * a.I + i0 + first + 8 * h] = rounded<F16>(ldexpf(v[h][i], e));
+      if (group == 0 && lane < 4 && (NB == 4 || !(seg & 1))) a.h_scales[(size_t)(off + j) * units + i0 / 64] = ldexpf(1.f, -e);
+    }
+  }
+  return ok;
+}
+
 // Gate and up products and SwiGLU. NB: token blocks of 8; RG: row groups.
 template <typename T, bool FP8, int NB, int RG>
 __global__ void __launch_bounds__(kThreads<RG>, RG == 1 ? 2 : 1)
@@ -522,6 +652,7 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
   };
   factors(blockIdx.x, 0, gn, un);
   bool ok = true;
+  int turn = 0;
   for (int u = blockIdx.x < step ? blockIdx.x : units; u < units; u += step) {
     const int item = u / tiles, m = items.m[item], n8 = (m + 7) / 8, off = items.off[item];
     float acc[2][NB][4] = {};
@@ -541,74 +672,33 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
       if (++s == a.stages) s = 0, ++lap;
     }
     if (FP8 && M16::kBf16) spread_nan(nan, acc);
-    // the warps' shares: red[seg][row][token], or one sum that they add to in turn
-    const int row = 32 * group + fragment_row(lane >> 2);
-    auto put = [&](bool first) {
-#pragma unroll
-      for (int f = 0; f < 2; ++f)
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float* to = red + ((kTurns<RG, NB> ? 0 : seg * kRows) + row + 16 * f + 8 * (i >> 1)) * (M + 1) + 8 * n +
-                        fragment_column<FP8>(2 * c + (i & 1));
-            *to = first ? acc[f][n][i] : *to + acc[f][n][i];
-          }
-    };
-    if constexpr (kTurns<RG, NB>) {
-      for (int q = 0; q < SEGS && ok; ++q) {
-        if (q == seg) put(q == 0);
-        ok = async::meet<32 * WARPS>(ok);
-      }
-    } else {
-      put(true);
-      ok = async::meet<32 * WARPS>(ok);
-    }
-    if (!ok) break;
     const int i0 = u % tiles * kOuts;
+    if constexpr (RG > 1) {
+      if (!(ok = finish<T, FP8, NB, RG>(a, items, item, i0, ok, turn, red, acc))) break;
+      turn ^= 1;
+      continue;
+    }
+    // the warps' shares: red[seg][row][token]
+    const int row = 32 * group + fragment_row(lane >> 2);
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          red[(seg * kRows + row + 16 * f + 8 * (i >> 1)) * (M + 1) + 8 * n + fragment_column<FP8>(2 * c + (i & 1))] = acc[f][n][i];
+    if (!(ok = async::meet<32 * WARPS>(ok))) break;
     for (int v = threadIdx.x; v < kOuts * m; v += 32 * WARPS) {
       const int o = v % kOuts, j = v / kOuts;
       if (i0 + o >= a.I) continue;
       const float* p = red + (32 * (o / 16) + o % 16) * (M + 1) + j;
       float pg = 0.f, pu = 0.f;
 #pragma unroll
-      for (int q = 0; q < (kTurns<RG, NB> ? 1 : SEGS); ++q) {
+      for (int q = 0; q < SEGS; ++q) {
         pg += p[q * kRows * (M + 1)];
         pu += p[(q * kRows + 16) * (M + 1)];
       }
-      if constexpr (kScaled<FP8, RG>) {
-        const float f = a.x_scales ? a.x_scales[items.tok[off + j]] : 1.f;
-        const_cast<float*>(p)[0] = swiglu(pg * f, pu * f);
-      } else {
-        const float r = swiglu(pg, pu);
-        const uint16_t hi = rounded<T>(r);
-        const float lo = r - T::lo(hi);
-        uint16_t* to = a.h + (size_t)(off + j) * a.I + i0 + o;
-        to[0] = hi;
-        // an infinite first number would make the second NaN
-        to[(size_t)a.T * a.K * a.I] = rounded<T>(fabsf(T::lo(hi)) <= 3.402823466e38f ? lo : 0.f);
-      }
-    }
-    if constexpr (kScaled<FP8, RG>) {
-      // a pair's 64 results and their power of two: a warp
-      if (!async::meet<32 * WARPS>(true)) break;
-      for (int j = warp; j < m; j += WARPS) {
-        float r[2], top = 0.f;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int o = 32 * k + lane;
-          r[k] = i0 + o < a.I ? red[(32 * (o / 16) + o % 16) * (M + 1) + j] : 0.f;
-          if (fabsf(r[k]) <= 3.402823466e38f) top = fmaxf(top, fabsf(r[k]));
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        const int e = f16_exponent(top);
-        uint16_t* to = a.h + (size_t)(off + j) * a.I + i0 + lane;
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (i0 + 32 * k + lane < a.I) to[32 * k] = rounded<F16>(ldexpf(r[k], e));
-        if (lane == 0) a.h_scales[(size_t)(off + j) * tiles + i0 / 64] = ldexpf(1.f, -e);
-      }
+      store_two<T>(a, off + j, i0 + o, swiglu(pg, pu));
     }
     if (!async::meet<32 * WARPS>(true)) break;
   }
@@ -620,7 +710,7 @@ __global__ void __launch_bounds__(kThreads<RG>, RG == 1 ? 2 : 1)
 down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorMap map,
             const __grid_constant__ TokenMaps map_h) {
   constexpr int KC = kChunk<FP8, RG>, BLOCKS = kBlocks<FP8, RG>, M = 8 * NB, WARPS = kWarps<RG>;
-  constexpr int kRows = 32 * RG, BOXES = kBoxes<RG>, kBoxK = KC / BOXES, kLine = kRows + 1, SW = kStageW<RG>;
+  constexpr int kRows = 32 * RG, BOXES = kBoxes<RG>, kBoxK = KC / BOXES, kLine = kDownLine<RG>, SW = kStageW<RG>;
   constexpr bool SCALED = kScaled<FP8, RG>;
   constexpr int PARTS = SCALED ? 1 : 2, kTokens = BLOCKS * PARTS * M * 128;  // the numbers' lines
   using M16 = std::conditional_t<SCALED, F16, T>;  // of the products
@@ -715,6 +805,7 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
     if (SCALED) griddep_wait();
     columns(begin);
     bool ok = true;
+    int turn = 0;
     for (int v = begin; v < end && ok;) {
       const int item = v / per, m = items.m[item], n8 = (m + 7) / 8, off = items.off[item];
       const int k0 = v % per, k1 = min(per, k0 + end - v), part = lines_of(m) * 128;
@@ -752,10 +843,13 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
           }
       };
       if constexpr (kTurns<RG, NB>) {
-        for (int q = 0; q < 2 && ok; ++q) {
-          if (q == (seg & 1)) add();
-          ok = async::meet<32 * WARPS>(ok);
-        }
+        // two warps share rows and sums: the first to add is the other one for the next item,
+        // so that they meet once an item
+        const bool leads = ((seg ^ turn) & 1) == 0;
+        turn ^= 1;
+        if (leads) add();
+        ok = async::meet<64>(ok, 2 + 2 * group + (seg >> 1));
+        if (!leads && ok) add();
       } else {
         add();
       }
@@ -819,8 +913,8 @@ int fit_stages(size_t rest, size_t stage, int ctas) {
 template <typename T, bool FP8, int NB, int RG>
 cudaError_t launch_up(LayerArgs a, const Maps& maps, int sms, cudaStream_t s) {
   constexpr auto kernel = up_kernel<T, FP8, NB, RG>;
-  constexpr int kRows = 32 * RG, M = 8 * NB, kPerSm = RG == 1 ? 2 : 1;
-  constexpr size_t rest = 4 * (kTurns<RG, NB> ? 1 : kSegs<RG>) * kRows * (M + 1);
+  constexpr int M = 8 * NB, kPerSm = RG == 1 ? 2 : 1;
+  constexpr size_t rest = 4 * kUpFloats<RG, NB>;
   const size_t stage = kStageW<RG> + kBlocks<FP8, RG> * ((a.T + 7) / 8 * 8) * 128;
   a.stages = fit_stages(rest, stage, kPerSm);
   a.whole = a.H % 64 == 0;
@@ -840,7 +934,7 @@ cudaError_t launch_down(LayerArgs a, const Maps& maps, int sms, cudaStream_t s) 
   constexpr auto kernel = down_kernel<T, FP8, NB, RG>;
   constexpr int kRows = 32 * RG, M = 8 * NB, kPerSm = RG == 1 ? 2 : 1;
   constexpr size_t stage = kStageW<RG> + kBlocks<FP8, RG> * (kScaled<FP8, RG> ? 1 : 2) * M * 128;
-  const size_t rest = 4 * (size_t)kDownSums<RG, NB> * a.T * (kRows + 1);
+  const size_t rest = 4 * (size_t)kDownSums<RG, NB> * a.T * kDownLine<RG>;
   a.stages = fit_stages(rest, stage, kPerSm);
   a.whole = a.I % 64 == 0;
   const size_t smem = 1024 + a.stages * stage + rest;
