@@ -244,6 +244,35 @@ inline int sm_count() {
   return n;
 }
 
+// Clusters of `cluster` CTAs (2 to 8) of `Kernel` that the current device holds at once (0 on
+// error). A cluster stays within a part of the GPU, so that may be fewer CTAs than the SMs
+// hold. The first answer of each device is kept: a kernel's CTAs take the same share of a SM
+// in every launch.
+template <auto Kernel>
+int active_clusters(int cluster, int threads, size_t smem) {
+  static std::atomic<int> cached[kMaxDevices][9];
+  int dev = 0;
+  if (cluster < 1 || cluster > 8 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  int n = cached[dev][cluster].load(std::memory_order_relaxed);
+  if (n <= 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {(unsigned)cluster, 1, 1};
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (prepare_kernel<Kernel>(smem) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    cached[dev][cluster].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 // Resident CTAs per SM of `Kernel` at `threads` threads and `smem` bytes of
 // dynamic shared memory on the current device. The last query of each
 // device is cached (the launchers ask with the same sizes call after call).

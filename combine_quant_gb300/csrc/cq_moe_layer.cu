@@ -34,8 +34,8 @@
 // 461 -> 367 us).
 //
 // Measured on one GB300 (copy 6.78 TB/s), hidden 7168, inter 2048, 8 of 32 experts, in a
-// graph: 1 token, bf16: 111 us, 6.4 TB/s; 16 tokens: 411 us, 6.9 TB/s; 64 tokens: 479 us,
-// 5.9 TB/s; fp8 weights: 71 us (5.0), 232 us (6.1), 332 us (4.2). Hidden 1024, inter 512, 4
+// graph: 1 token, bf16: 111 us, 6.4 TB/s; 16 tokens: 411 us, 6.9 TB/s; 64 tokens: 468 us,
+// 6.0 TB/s; fp8 weights: 71 us (5.0), 225 us (6.1), 322 us (4.4). Hidden 1024, inter 512, 4
 // tokens: 13 us, most of it the start and end of two kernels.
 #include <cuda_runtime.h>
 
@@ -901,16 +901,6 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
 }
 
 // ---- host ----
-// The down kernel's grid: tiles, and as many CTAs a tile as are all on the GPU at once: a
-// second wave pays its start again (1 token, hidden 7168: 134 us with 4, 117 with 1; 64
-// tokens, fp8: 529 with 8, 491 with 2).
-struct DownGrid {
-  int tiles, cluster;
-  DownGrid(int H, int rows, int slots) : tiles((H + rows - 1) / rows), cluster(1) {
-    while (cluster < 8 && tiles * (cluster + 1) <= slots) ++cluster;
-  }
-};
-
 struct Maps {
   CUtensorMap w13, w2, x;
   TokenMaps h;
@@ -941,23 +931,43 @@ cudaError_t launch_up(LayerArgs a, const Maps& maps, int sms, cudaStream_t s) {
                     maps.x);
 }
 
+// The down kernel's launch: tiles, and as many CTAs a tile as are all on the GPU at once: a
+// second wave pays its start again (1 token, hidden 7168: 134 us with 4, 117 with 1; 64
+// tokens, fp8: 529 with 8, 491 with 2). Clusters that the SMs would hold need not all find a
+// place (hidden 2064, 17 tiles: 15 clusters of 8; 54 us, with 22 tiles and clusters of 6: 40).
+template <typename T, bool FP8, int NB, int RG>
+struct Down {
+  static constexpr auto kernel = down_kernel<T, FP8, NB, RG>;
+  static constexpr int kRows = 32 * RG, kPerSm = RG == 1 ? 2 : 1;
+  int tiles, cluster = 1, stages;
+  size_t smem;
+  Down(const LayerArgs& a, int sms) : tiles((a.H + kRows - 1) / kRows) {
+    constexpr size_t stage = kStageW<RG> + kBlocks<FP8, RG> * (kScaled<FP8, RG> ? 1 : 2) * 8 * NB * 128;
+    const size_t rest = 4 * (size_t)kDownSums<RG, NB> * a.T * kDownLine<RG>;
+    stages = fit_stages(rest, stage, kPerSm);
+    smem = 1024 + stages * stage + rest;
+    for (int c = std::min(8, kPerSm * sms / tiles); c > 1; --c)
+      if (tiles <= active_clusters<kernel>(c, kThreads<RG>, smem)) {
+        cluster = c;
+        break;
+      }
+  }
+};
+
 template <typename T, bool FP8, int NB, int RG>
 cudaError_t launch_down(LayerArgs a, const Maps& maps, int sms, cudaStream_t s) {
-  constexpr auto kernel = down_kernel<T, FP8, NB, RG>;
-  constexpr int kRows = 32 * RG, M = 8 * NB, kPerSm = RG == 1 ? 2 : 1;
-  constexpr size_t stage = kStageW<RG> + kBlocks<FP8, RG> * (kScaled<FP8, RG> ? 1 : 2) * M * 128;
-  const size_t rest = 4 * (size_t)kDownSums<RG, NB> * a.T * kDownLine<RG>;
-  a.stages = fit_stages(rest, stage, kPerSm);
+  const Down<T, FP8, NB, RG> d(a, sms);
+  constexpr auto kernel = d.kernel;
+  const size_t smem = d.smem;
+  a.stages = d.stages;
+  a.cluster = d.cluster;
   a.whole = a.I % 64 == 0;
-  const size_t smem = 1024 + a.stages * stage + rest;
   if (a.stages < 2 || smem < 1024 + 10 * (size_t)a.G + 8 * (size_t)(a.T * a.K)) return cudaErrorInvalidValue;
   cudaError_t e = prepare_kernel<kernel>(smem);
   if (e == cudaSuccess && RG > 1) e = check_registers<kernel>(kThreads<RG>, kAllRegs<RG>);
   if (e != cudaSuccess) return e;
-  const DownGrid g(a.H, kRows, kPerSm * sms);
-  a.cluster = g.cluster;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(g.tiles * g.cluster);
+  cfg.gridDim = dim3(d.tiles * d.cluster);
   cfg.blockDim = dim3(kThreads<RG>);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -965,7 +975,7 @@ cudaError_t launch_down(LayerArgs a, const Maps& maps, int sms, cudaStream_t s) 
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {(unsigned)g.cluster, 1, 1};
+  attr[1].val.clusterDim = {(unsigned)d.cluster, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, a, maps.w2, maps.h);
@@ -1016,6 +1026,14 @@ cudaError_t launch_t(LayerArgs a, const void* w13, const void* w2, int sms, cuda
   return e == cudaSuccess ? launch_down<T, FP8, NB, RD>(a, m, sms, s) : e;
 }
 
+template <typename T, bool FP8, int NB>
+cudaError_t launch_large(const LayerArgs& a, const void* w13, const void* w2, int sms, cudaStream_t s) {
+  const Down<T, FP8, NB, 3> d3(a, sms);
+  const Down<T, FP8, NB, 4> d4(a, sms);
+  return d3.tiles * d3.cluster > d4.tiles * d4.cluster ? launch_t<T, FP8, NB, 4, 3>(a, w13, w2, sms, s)
+                                                       : launch_t<T, FP8, NB, 4, 4>(a, w13, w2, sms, s);
+}
+
 // Tiles of 128 rows and sixteen warps, one CTA a SM, where that gives each SM a unit of the
 // up kernel (hidden 7168, inter 2048, bf16, 8 tokens: 366 us against 383 with tiles of 32
 // rows and two CTAs a SM; fp8, 2 tokens: 131 against 132, 8 tokens: 244 against 269), else
@@ -1029,11 +1047,7 @@ cudaError_t launch(const LayerArgs& a, const void* w13, const void* w2, cudaStre
   if (sms <= 0) return cudaErrorUnknown;
   const bool units = (int64_t)std::min(a.G, a.T * a.K) * ((a.I + 63) / 64) >= sms;
   if (a.T <= 8 && (!units || (FP8 && !T::kBf16 && a.T <= 4))) return launch_t<T, FP8, 1, 1, 1>(a, w13, w2, sms, s);
-  const DownGrid g3(a.H, 96, sms), g4(a.H, 128, sms);
-  const bool three = g3.tiles * g3.cluster > g4.tiles * g4.cluster;
-  if (a.T <= 16)
-    return three ? launch_t<T, FP8, 2, 4, 3>(a, w13, w2, sms, s) : launch_t<T, FP8, 2, 4, 4>(a, w13, w2, sms, s);
-  return three ? launch_t<T, FP8, 4, 4, 3>(a, w13, w2, sms, s) : launch_t<T, FP8, 4, 4, 4>(a, w13, w2, sms, s);
+  return a.T <= 16 ? launch_large<T, FP8, 2>(a, w13, w2, sms, s) : launch_large<T, FP8, 4>(a, w13, w2, sms, s);
 }
 
 int validate(const cq_moe_config* c) {
