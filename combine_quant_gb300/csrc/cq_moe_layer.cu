@@ -34,8 +34,8 @@
 // 461 -> 367 us).
 //
 // Measured on one GB300 (copy 6.78 TB/s), hidden 7168, inter 2048, 8 of 32 experts, in a
-// graph: 1 token, bf16: 111 us, 6.4 TB/s; 16 tokens: 411 us, 6.9 TB/s; 64 tokens: 468 us,
-// 6.0 TB/s; fp8 weights: 71 us (5.0), 225 us (6.1), 322 us (4.4). Hidden 1024, inter 512, 4
+// graph: 1 token, bf16: 111 us, 6.4 TB/s; 16 tokens: 411 us, 6.9 TB/s; 64 tokens: 460 us,
+// 6.1 TB/s; fp8 weights: 71 us (5.0), 226 us (6.2), 305 us (4.6). Hidden 1024, inter 512, 4
 // tokens: 13 us, most of it the start and end of two kernels.
 #include <cuda_runtime.h>
 
@@ -132,10 +132,15 @@ struct Items {
   uint8_t m[kMaxItems];         // pairs
   uint8_t tok[kMaxPairs + 32];  // of each pair the token and its weight (zeros behind the last)
   float weight[kMaxPairs];
-  int scan[2][kMaxWarps];
+  uint32_t scan[kMaxWarps];
+  int plan[2];                  // units, and a CTA's distance between its own
+  int twice;                    // a token names an expert twice
 };
 
-// Sorts the pairs (all threads). `scratch`: 10 bytes an expert and 8 a pair.
+// Sorts the pairs (all threads; a barrier has to follow). `scratch`: 10 bytes an expert and 8 a
+// pair. Its latency is paid twice a call, so the ids are on their way before anything else, and
+// a thread keeps its pairs in registers; only where a token names an expert twice are the
+// token's others looked at.
 template <int PER, int kThreads>
 __device__ __forceinline__ void sort_pairs(const LayerArgs& a, Items& it, uint8_t* scratch, bool report) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, P = a.T * a.K;
@@ -144,39 +149,55 @@ __device__ __forceinline__ void sort_pairs(const LayerArgs& a, Items& it, uint8_
   int* ids = reinterpret_cast<int*>(masks + a.G);
   float* scales = reinterpret_cast<float*>(ids + P);
   uint16_t* first = reinterpret_cast<uint16_t*>(scales + P);  // pair of each expert
+  constexpr int kMine = (kMaxPairs + kThreads - 1) / kThreads;
+  int mine[kMine];
+  float weight[kMine] = {};
+#pragma unroll
+  for (int v = 0; v < kMine; ++v) {
+    const int p = t + v * kThreads;
+    mine[v] = -1;
+    if (p >= P) continue;
+    const bool on = !a.mask_ndim || a.mask[a.mask_ndim == 1 ? p / a.K : p];
+    weight[v] = a.scales[p];
+    const int e = a.ids[p];
+    if (on) mine[v] = e;
+    if (on && (unsigned)e >= (unsigned)a.G) {
+      if (report) atomicOr(&g_status, (uint32_t)CQ_ST_BAD_ID);
+      mine[v] = -1;
+    }
+  }
   for (int e = t; e < a.G; e += kThreads) masks[e] = 0;
   for (int p = t; p < P + 32; p += kThreads) it.tok[p] = 0;
+  if (t == 0) it.twice = 0;
   __syncthreads();
-  for (int p = t; p < P; p += kThreads) {
-    int e = -1;
-    if (!a.mask_ndim || a.mask[a.mask_ndim == 1 ? p / a.K : p]) {
-      e = a.ids[p];
-      if ((unsigned)e >= (unsigned)a.G) {
-        if (report) atomicOr(&g_status, (uint32_t)CQ_ST_BAD_ID);
-        e = -1;
-      }
-    }
-    ids[p] = e;
-    scales[p] = a.scales[p];
-    if (e >= 0) atomicOr(words + 2 * e + p / a.K / 32, 1u << (p / a.K % 32));
+#pragma unroll
+  for (int v = 0; v < kMine; ++v) {
+    const int p = t + v * kThreads, tok = p / a.K;
+    if (p >= P) break;
+    ids[p] = mine[v];
+    scales[p] = weight[v];
+    if (mine[v] >= 0 && atomicOr(words + 2 * mine[v] + tok / 32, 1u << (tok % 32)) >> (tok % 32) & 1) it.twice = 1;
   }
   __syncthreads();
   const int per = (a.G + kThreads - 1) / kThreads, e0 = min(a.G, t * per), e1 = min(a.G, e0 + per);
-  int pairs = 0, items = 0;
+  // pairs below, items above: both stay below 2^16
+  static_assert(kMaxItems < 1 << 15);
+  uint32_t counts = 0;
   for (int e = e0; e < e1; ++e) {
     const int c = __popcll(masks[e]);
-    pairs += c;
-    items += (c + PER - 1) / PER;
+    counts += c + ((c + PER - 1) / PER << 16);
   }
-  int rp = pairs, ri = items;
+  uint32_t sum = counts;
+#pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int vp = __shfl_up_sync(~0u, rp, o), vi = __shfl_up_sync(~0u, ri, o);
-    if (lane >= o) rp += vp, ri += vi;
+    const uint32_t v = __shfl_up_sync(~0u, sum, o);
+    if (lane >= o) sum += v;
   }
-  if (lane == 31) it.scan[0][warp] = rp, it.scan[1][warp] = ri;
+  if (lane == 31) it.scan[warp] = sum;
   __syncthreads();
-  int p0 = rp - pairs, i0 = ri - items;
-  for (int w = 0; w < warp; ++w) p0 += it.scan[0][w], i0 += it.scan[1][w];
+  static_assert(kMaxWarps <= 32);
+  sum += __reduce_add_sync(~0u, lane < warp ? it.scan[lane] : 0u);
+  int p0 = (sum - counts) & 0xffff, i0 = (sum - counts) >> 16;
   for (int e = e0; e < e1; ++e) {
     first[e] = (uint16_t)p0;
     for (int left = __popcll(masks[e]); left > 0; left -= PER, ++i0) {
@@ -188,22 +209,25 @@ __device__ __forceinline__ void sort_pairs(const LayerArgs& a, Items& it, uint8_
   }
   if (t == kThreads - 1) it.n = i0;
   __syncthreads();
-  for (int p = t; p < P; p += kThreads) {
-    const int e = ids[p], tok = p / a.K;
+#pragma unroll
+  for (int v = 0; v < kMine; ++v) {
+    const int p = t + v * kThreads, e = mine[v], tok = p / a.K;
     if (e < 0) continue;
-    float w = 0.f;
-    bool before = false;
-    for (int j = tok * a.K; j < tok * a.K + a.K; ++j) {
-      if (ids[j] != e) continue;
-      before |= j < p;
-      w += scales[j];
+    float w = 0.f + weight[v];
+    if (it.twice) {
+      w = 0.f;
+      bool before = false;
+      for (int j = tok * a.K; j < tok * a.K + a.K; ++j) {
+        if (ids[j] != e) continue;
+        before |= j < p;
+        w += scales[j];
+      }
+      if (before) continue;
     }
-    if (before) continue;
     const int at = first[e] + __popcll(masks[e] & ((1ull << tok) - 1));
     it.tok[at] = (uint8_t)tok;
     it.weight[at] = w;
   }
-  __syncthreads();
 }
 
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
@@ -613,13 +637,16 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
   griddep_wait();
   griddep_launch_dependents();  // the down kernel reads results only after its own wait
   sort_pairs<M, kThreads<RG>>(a, items, stage0, blockIdx.x == 0);
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  __syncthreads();
   using M16 = std::conditional_t<kScaled<FP8, RG>, F16, T>;  // of the products
   const int tiles = (a.I + kOuts - 1) / kOuts, units = items.n * tiles;
   const int n_stages = (a.H + KC - 1) / KC;
   // the same number of units for every CTA that has any, so that all end together
   const int rounds = max(1, (units + (int)gridDim.x - 1) / (int)gridDim.x), step = (units + rounds - 1) / rounds;
+  if (threadIdx.x == 0) items.plan[0] = units, items.plan[1] = step;
+  // read there: the products need their registers (116 spilled bytes: 330 us, 8: 305)
+  const volatile int* plan = items.plan;
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
   uint32_t s = 0, lap = 0;
   if (warp >= WARPS) {
     set_registers<RG, false>();
@@ -657,15 +684,14 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
   float gn = 0.f, un = 0.f;
   auto factors = [&](int u, int first, float& g, float& w) {
     const int block = ((first + lane) * KC + seg * 64) / 128;
-    if (!FP8 || u >= units || first + lane >= n_stages || block >= kb) return;
+    if (!FP8 || u >= plan[0] || first + lane >= n_stages || block >= kb) return;
     const float* p = a.w13_scales + ((size_t)items.e[u / tiles] * 2 * ib + u % tiles * kOuts / 128) * kb + block;
     g = __ldg(p);
     w = __ldg(p + (size_t)ib * kb);
   };
   factors(blockIdx.x, 0, gn, un);
   bool ok = true;
-  int turn = 0;
-  for (int u = blockIdx.x < step ? blockIdx.x : units; u < units; u += step) {
+  for (int u = blockIdx.x < step ? blockIdx.x : units, turn = 0; u < plan[0]; u += plan[1], turn ^= 1) {
     const int item = u / tiles, m = items.m[item], n8 = (m + 7) / 8, off = items.off[item];
     float acc[2][NB][4] = {};
     uint32_t nan[4] = {};
@@ -673,7 +699,7 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
 #pragma unroll
     for (int n = 0; n < NB; ++n) token[n] = items.tok[off + 8 * n + fragment_column<FP8>(lane >> 2)];
     float g = gn, w = un;
-    factors(u + step, 0, gn, un);
+    factors(u + plan[1], 0, gn, un);
     for (int k = 0; k < n_stages; ++k) {
       if (FP8 && k > 0 && (k & 31) == 0) factors(u, k, g, w);
       const float sg = FP8 ? __shfl_sync(~0u, g, k & 31) : 1.f, su = FP8 ? __shfl_sync(~0u, w, k & 31) : 1.f;
@@ -687,7 +713,6 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
     const int i0 = u % tiles * kOuts;
     if constexpr (RG > 1) {
       if (!(ok = finish<T, FP8, NB, RG>(a, items, item, i0, ok, turn, red, acc))) break;
-      turn ^= 1;
       continue;
     }
     // the warps' shares: red[seg][row][token]
