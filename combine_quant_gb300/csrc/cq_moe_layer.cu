@@ -17,8 +17,8 @@
 // through distributed shared memory, in order. Results do not depend on timing. The
 // second kernel's copies of weights start before the first one has ended.
 //
-// Tokens' rows come a stage at a time by one tiled copy: all tokens' (up), an item's, which
-// lie together (down). Row by row, 256 bytes each, the copies were the bound (64 tokens,
+// Tokens' rows come a stage at a time by one tiled copy: all tokens' (up; fp8 weights: only
+// an item's, by three warps), an item's, which lie together (down). Row by row, 256 bytes each, the copies were the bound (64 tokens,
 // bf16: 852 -> 563 us).
 //
 // Between the two SwiGLU's results are held as two numbers of the token type, whose sum
@@ -35,7 +35,7 @@
 //
 // Measured on one GB300 (copy 6.78 TB/s), hidden 7168, inter 2048, 8 of 32 experts, in a
 // graph: 1 token, bf16: 111 us, 6.4 TB/s; 16 tokens: 411 us, 6.9 TB/s; 64 tokens: 460 us,
-// 6.1 TB/s; fp8 weights: 71 us (5.0), 226 us (6.2), 305 us (4.6). Hidden 1024, inter 512, 4
+// 6.1 TB/s; fp8 weights: 71 us (5.0), 226 us (6.2), 303 us (4.7). Hidden 1024, inter 512, 4
 // tokens: 13 us, most of it the start and end of two kernels.
 #include <cuda_runtime.h>
 
@@ -125,6 +125,13 @@ constexpr int kChunk = kBoxes<RG> * (FP8 ? 128 : 64);
 // block's rows one after the other, swizzled as the copies have it.
 template <bool FP8, int RG>
 constexpr int kBlocks = kChunk<FP8, RG> / 64;
+
+// Tokens' lines of a stage in the up kernel: an item's, which the threads gather (fp8 weights,
+// large tiles), or all tokens', by one tiled copy.
+template <bool FP8, int NB, int RG>
+__host__ __device__ constexpr int up_lines(int T) {
+  return kScaled<FP8, RG> ? 8 * NB : (T + 7) / 8 * 8;
+}
 
 struct Items {
   int n;                        // items
@@ -420,11 +427,20 @@ struct TokenMaps {
 // Lines that an item of m pairs is copied as.
 __device__ __forceinline__ int lines_of(int m) { return m <= 8 ? 8 : m <= 16 ? 16 : 32; }
 
+// 16 bytes, or zeros where `bytes` is 0.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// An arrival on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void arrive_on_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // The rings' start: barriers, and shared memory that sort_pairs used handed to the copies.
-__device__ __forceinline__ void init_ring(Ring& r, int stages, int warps) {
+__device__ __forceinline__ void init_ring(Ring& r, int stages, int warps, int fills = 1) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
-      mbar_init(&r.full[s], 1);
+      mbar_init(&r.full[s], fills);
       mbar_init(&r.empty[s], warps);
     }
     async::mbar_fence_init();
@@ -628,11 +644,12 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
   __shared__ Items items;
   uint8_t* stage0 = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
   // weights of all stages (1024-byte aligned), then the tokens' parts, then the warps' sums
-  const int lines = (a.T + 7) / 8 * 8, kTokens = BLOCKS * lines * 128;  // all tokens' lines
+  constexpr bool kGather = kScaled<FP8, RG>;
+  const int lines = up_lines<FP8, NB, RG>(a.T), kTokens = BLOCKS * lines * 128;
   uint8_t* tokens0 = stage0 + a.stages * SW;
   float* red = reinterpret_cast<float*>(tokens0 + a.stages * kTokens);  // [segs][rows][M + 1]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  init_ring(ring, a.stages, WARPS);
+  init_ring(ring, a.stages, WARPS, kGather ? 1 + 96 : 1);
   if (threadIdx.x == 0) prefetch_map(&map);
   griddep_wait();
   griddep_launch_dependents();  // the down kernel reads results only after its own wait
@@ -650,22 +667,47 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
   uint32_t s = 0, lap = 0;
   if (warp >= WARPS) {
     set_registers<RG, false>();
-    if (warp > WARPS) return;
-    // ---- copies ----
     bool ok = true;
+    if (warp > WARPS) {
+      if constexpr (kGather) {
+        // ---- an item's tokens, a warp a row: the others' lines would be as many bytes as the
+        // weights (9 tokens, 26 experts, hidden 2528, inter 1008: 56 us, now 54; four rows by a
+        // gathering tiled copy: 64 tokens 361 us where all tokens' took 321). bf16 weights gain
+        // nothing (64 tokens: 460 us, so 465) ----
+        static_assert(KC == 8 * 32);
+        const int piece = lane;
+        const uint32_t to0 = smem_u32(tokens0) + (piece >> 3) * lines * 128;
+        for (int u = blockIdx.x < step ? blockIdx.x : units; u < units && ok; u += step) {
+          const int item = u / tiles, m = items.m[item];
+          const uint8_t* tok = items.tok + items.off[item];
+          for (int k = 0; k < n_stages; ++k) {
+            if (lap > 0 && !(ok = wait_warp(&ring.empty[s], (lap & 1) ^ 1))) break;
+            const int col = k * KC + piece * 8;
+            const uint32_t bytes = col < a.H ? 16 : 0, to = to0 + s * kTokens;
+            const uint16_t* from = a.x + (bytes ? col : 0);
+            for (int j = warp - WARPS - 1; j < m; j += 3)
+              copy16_async(to + j * 128 + (((piece ^ j) & 7) << 4), from + (size_t)tok[j] * a.H, bytes);
+            arrive_on_copies(&ring.full[s]);
+            if (++s == a.stages) s = 0, ++lap;
+          }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+      }
+      return;
+    }
+    // ---- copies ----
     for (int u = blockIdx.x < step ? blockIdx.x : units; u < units && ok; u += step) {
       const int item = u / tiles, i0 = u % tiles * kOuts;
       for (int k = 0; k < n_stages; ++k) {
         if (lap > 0 && !(ok = wait_warp(&ring.empty[s], (lap & 1) ^ 1))) break;
         if (lane == 0) {
           const uint32_t bar = smem_u32(&ring.full[s]), to = smem_u32(tokens0 + s * kTokens);
-          mbar_arrive_expect_tx(&ring.full[s], SW + kTokens);
+          mbar_arrive_expect_tx(&ring.full[s], SW + (kGather ? 0 : kTokens));
           for (int b = 0; b < BOXES; ++b)
             tma_load4<1>(smem_u32(stage0 + s * SW + b * kRows * 128), &map, k * KC + b * kBoxK, i0, 0, items.e[item], bar);
-          if (a.whole) {
-            tma_load3<1>(to, &map_x, 0, 0, k * BLOCKS, bar);
-          } else {
-            for (int b = 0; b < BLOCKS; ++b) tma_load3<1>(to + b * lines * 128, &map_x, k * KC + b * 64, 0, 0, bar);
+          if constexpr (!kGather) {
+            if (a.whole) tma_load3<1>(to, &map_x, 0, 0, k * BLOCKS, bar);
+            else for (int b = 0; b < BLOCKS; ++b) tma_load3<1>(to + b * lines * 128, &map_x, k * KC + b * 64, 0, 0, bar);
           }
         }
         __syncwarp();
@@ -697,7 +739,10 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
     uint32_t nan[4] = {};
     int token[NB];
 #pragma unroll
-    for (int n = 0; n < NB; ++n) token[n] = items.tok[off + 8 * n + fragment_column<FP8>(lane >> 2)];
+    for (int n = 0; n < NB; ++n) {
+      const int j = 8 * n + fragment_column<FP8>(lane >> 2);
+      token[n] = kGather ? j : items.tok[off + j];
+    }
     float g = gn, w = un;
     factors(u + plan[1], 0, gn, un);
     for (int k = 0; k < n_stages; ++k) {
@@ -942,7 +987,7 @@ cudaError_t launch_up(LayerArgs a, const Maps& maps, int sms, cudaStream_t s) {
   constexpr auto kernel = up_kernel<T, FP8, NB, RG>;
   constexpr int M = 8 * NB, kPerSm = RG == 1 ? 2 : 1;
   constexpr size_t rest = 4 * kUpFloats<RG, NB>;
-  const size_t stage = kStageW<RG> + kBlocks<FP8, RG> * ((a.T + 7) / 8 * 8) * 128;
+  const size_t stage = kStageW<RG> + kBlocks<FP8, RG> * up_lines<FP8, NB, RG>(a.T) * 128;
   a.stages = fit_stages(rest, stage, kPerSm);
   a.whole = a.H % 64 == 0;
   const size_t smem = 1024 + a.stages * stage + rest;
@@ -1013,16 +1058,15 @@ cudaError_t launch_t(LayerArgs a, const void* w13, const void* w2, int sms, cuda
   constexpr bool kScale = kScaled<FP8, RD>;
   static_assert(kScaled<FP8, RU> == kScale, "both kernels hold h alike");
   const MapType type = FP8 ? kMapU8 : T::kBf16 ? kMapBF16 : kMapF16, token = T::kBf16 && !kScale ? kMapBF16 : kMapF16;
-  const void* x = a.x;
   if (kScale && T::kBf16) {
-    x = a.x16;
     const cudaError_t e = launch_pdl(scale_kernel, dim3(a.T), dim3(256), 0, s, a.x, a.x16, a.x_scales, a.H);
     if (e != cudaSuccess) return e;
+    a.x = a.x16;
   } else {
     a.x_scales = nullptr;
   }
   const uint64_t es = FP8 ? 1 : 2, H = a.H, I = a.I, G = a.G, P = (uint64_t)a.T * a.K;
-  Maps m;
+  Maps m = {};
   {
     const uint64_t d[] = {H, I, 2, G}, st[] = {es * H, es * I * H, es * 2 * I * H};
     const uint32_t b[] = {(uint32_t)(128 / es), 16 * RU, 2, 1};
@@ -1033,11 +1077,11 @@ cudaError_t launch_t(LayerArgs a, const void* w13, const void* w2, int sms, cuda
     const uint32_t b[] = {(uint32_t)(128 / es), 32 * RD, 1};
     if (!make_map(&m.w2, w2, type, 3, d, st, b)) return cudaErrorUnknown;
   }
-  {
+  if (!kScale) {
     const bool whole = H % 64 == 0;
     const uint64_t d[] = {whole ? 64 : H, (uint64_t)a.T, whole ? H / 64 : 1}, st[] = {2 * H, whole ? 128 : 2 * H * a.T};
     const uint32_t b[] = {64, (uint32_t)(a.T + 7) / 8 * 8, whole ? (uint32_t)kBlocks<FP8, RU> : 1};
-    if (!make_map(&m.x, x, token, 3, d, st, b)) return cudaErrorUnknown;
+    if (!make_map(&m.x, a.x, token, 3, d, st, b)) return cudaErrorUnknown;
   }
   const bool whole = I % 64 == 0;
   const uint64_t d[] = {whole ? 64 : I, P, kScale ? 1 : 2, whole ? I / 64 : 1};
