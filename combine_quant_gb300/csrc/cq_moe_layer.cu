@@ -11,7 +11,8 @@
 // Every CTA sorts the (token, expert) pairs itself into items: an expert and up to 8 NB
 // of its tokens, ascending. A token that names an expert twice is one pair with both
 // weights. up_kernel: an item's tile of 16 (64) gates and their ups is one CTA's work;
-// its warps' shares of k are added through shared memory, in order. down_kernel: a tile of 32
+// its warps' shares of k are added through shared memory, in order (few
+// units: a cluster's work, whose CTAs take shares of k too). down_kernel: a tile of 32
 // (96, 128) output rows is one cluster's work: the CTAs share the stages of all items
 // evenly, each keeps the weighted sums of all tokens, and the CTAs' sums are added
 // through distributed shared memory, in order. Results do not depend on timing. The
@@ -59,7 +60,7 @@ __device__ uint32_t g_status;  // CQ_ST_* bits of these kernels on this device
 
 struct LayerArgs {
   int32_t T, G, K, H, I, mask_ndim, out_f32;
-  int32_t stages, cluster;   // of the ring; CTAs that share a tile (down_kernel)
+  int32_t stages, cluster;   // of the ring; CTAs that share a tile (down_kernel) or a unit (up_kernel)
   int32_t whole;             // rows of x (h) are whole blocks of 64: one copy takes a stage's
   const uint16_t* x;
   const int32_t* ids;
@@ -534,7 +535,7 @@ __device__ __forceinline__ void store_two(const LayerArgs& a, int pair, int i, f
 // false where a warp that waits at them gave up.
 template <typename T, bool FP8, int NB, int RG>
 __device__ __forceinline__ bool finish(const LayerArgs& a, const Items& items, int item, int i0, bool ok, int turn,
-                                       float* red, float (&acc)[2][NB][4]) {
+                                       float* red, float4* far, float (&acc)[2][NB][4]) {
   constexpr int WARPS = kWarps<RG>, PIECES = kBoxLines<RG, NB>;
   constexpr bool kAll = NB == 2;  // all three boxes of a warp at once
   static_assert(kSegs<RG> == 4 && (NB == 2 || NB == 4));
@@ -577,6 +578,29 @@ __device__ __forceinline__ bool finish(const LayerArgs& a, const Items& items, i
         }
     }
     ok = async::meet<32 * 4>(ok, 2 + group);  // the boxes are read
+  }
+  if (a.cluster > 1) {
+    // The CTAs' shares, in order; the first one's ring, which nothing uses any more, takes them.
+    const uint32_t rank = cluster_rank();
+    cluster_wait();
+    if (rank > 0 && block < n8) {
+#pragma unroll
+      for (int p = 0; p < PIECES; ++p)
+        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         addr_in(smem_u32(far + (((rank - 1) * WARPS + warp) * PIECES + p) * 32 + lane), 0)),
+                     "f"(mine[p].x), "f"(mine[p].y), "f"(mine[p].z), "f"(mine[p].w)
+                     : "memory");
+    }
+    cluster_sync();
+    if (rank > 0) return ok;
+    if (block < n8) {
+      for (int r = 1; r < a.cluster; ++r)
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p) {
+          const float4 v = far[(((r - 1) * WARPS + warp) * PIECES + p) * 32 + lane];
+          mine[p].x += v.x, mine[p].y += v.y, mine[p].z += v.z, mine[p].w += v.w;
+        }
+    }
   }
   // value [h][i]: row fragment_row(lane / 4) + 8 * (NB 4: h, else seg & 1), token 8 block + column(2 c + i)
   constexpr int HALVES = NB / 2;
@@ -656,9 +680,11 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
   sort_pairs<M, kThreads<RG>>(a, items, stage0, blockIdx.x == 0);
   using M16 = std::conditional_t<kScaled<FP8, RG>, F16, T>;  // of the products
   const int tiles = (a.I + kOuts - 1) / kOuts, units = items.n * tiles;
-  const int n_stages = (a.H + KC - 1) / KC;
+  const int all_stages = (a.H + KC - 1) / KC, cta = blockIdx.x / a.cluster, ctas = gridDim.x / a.cluster;
+  const int rank = a.cluster > 1 ? (int)cluster_rank() : 0;
+  const int first_stage = all_stages * rank / a.cluster, n_stages = all_stages * (rank + 1) / a.cluster;
   // the same number of units for every CTA that has any, so that all end together
-  const int rounds = max(1, (units + (int)gridDim.x - 1) / (int)gridDim.x), step = (units + rounds - 1) / rounds;
+  const int rounds = max(1, (units + ctas - 1) / ctas), step = (units + rounds - 1) / rounds;
   if (threadIdx.x == 0) items.plan[0] = units, items.plan[1] = step;
   // read there: the products need their registers (116 spilled bytes: 330 us, 8: 305)
   const volatile int* plan = items.plan;
@@ -677,10 +703,10 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
         static_assert(KC == 8 * 32);
         const int piece = lane;
         const uint32_t to0 = smem_u32(tokens0) + (piece >> 3) * lines * 128;
-        for (int u = blockIdx.x < step ? blockIdx.x : units; u < units && ok; u += step) {
+        for (int u = cta < step ? cta : units; u < units && ok; u += step) {
           const int item = u / tiles, m = items.m[item];
           const uint8_t* tok = items.tok + items.off[item];
-          for (int k = 0; k < n_stages; ++k) {
+          for (int k = first_stage; k < n_stages; ++k) {
             if (lap > 0 && !(ok = wait_warp(&ring.empty[s], (lap & 1) ^ 1))) break;
             const int col = k * KC + piece * 8;
             const uint32_t bytes = col < a.H ? 16 : 0, to = to0 + s * kTokens;
@@ -696,9 +722,9 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
       return;
     }
     // ---- copies ----
-    for (int u = blockIdx.x < step ? blockIdx.x : units; u < units && ok; u += step) {
+    for (int u = cta < step ? cta : units; u < units && ok; u += step) {
       const int item = u / tiles, i0 = u % tiles * kOuts;
-      for (int k = 0; k < n_stages; ++k) {
+      for (int k = first_stage; k < n_stages; ++k) {
         if (lap > 0 && !(ok = wait_warp(&ring.empty[s], (lap & 1) ^ 1))) break;
         if (lane == 0) {
           const uint32_t bar = smem_u32(&ring.full[s]), to = smem_u32(tokens0 + s * kTokens);
@@ -731,9 +757,9 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
     g = __ldg(p);
     w = __ldg(p + (size_t)ib * kb);
   };
-  factors(blockIdx.x, 0, gn, un);
+  factors(cta, first_stage & ~31, gn, un);
   bool ok = true;
-  for (int u = blockIdx.x < step ? blockIdx.x : units, turn = 0; u < plan[0]; u += plan[1], turn ^= 1) {
+  for (int u = cta < step ? cta : units, turn = 0; u < plan[0]; u += plan[1], turn ^= 1) {
     const int item = u / tiles, m = items.m[item], n8 = (m + 7) / 8, off = items.off[item];
     float acc[2][NB][4] = {};
     uint32_t nan[4] = {};
@@ -744,9 +770,9 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
       token[n] = kGather ? j : items.tok[off + j];
     }
     float g = gn, w = un;
-    factors(u + plan[1], 0, gn, un);
-    for (int k = 0; k < n_stages; ++k) {
-      if (FP8 && k > 0 && (k & 31) == 0) factors(u, k, g, w);
+    factors(u + plan[1], 0, gn, un);  // (more than one unit: a cluster of 1)
+    for (int k = first_stage; k < n_stages; ++k) {
+      if (FP8 && k > first_stage && (k & 31) == 0) factors(u, k, g, w);
       const float sg = FP8 ? __shfl_sync(~0u, g, k & 31) : 1.f, su = FP8 ? __shfl_sync(~0u, w, k & 31) : 1.f;
       if (!(ok = wait_warp(&ring.full[s], lap & 1))) break;
       multiply<M16, FP8, NB, 1>(smem_u32(stage0 + s * SW + box * kRows * 128), 16 * group, kOuts + 16 * group, half,
@@ -757,7 +783,8 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
     if (FP8 && M16::kBf16) spread_nan(nan, acc);
     const int i0 = u % tiles * kOuts;
     if constexpr (RG > 1) {
-      if (!(ok = finish<T, FP8, NB, RG>(a, items, item, i0, ok, turn, red, acc))) break;
+      if (a.cluster > 1) cluster_arrive();  // done with the ring
+      if (!(ok = finish<T, FP8, NB, RG>(a, items, item, i0, ok, turn, red, reinterpret_cast<float4*>(stage0), acc))) break;
       continue;
     }
     // the warps' shares: red[seg][row][token]
@@ -996,15 +1023,41 @@ cudaError_t launch_up(LayerArgs a, const Maps& maps, int sms, cudaStream_t s) {
   cudaError_t e = prepare_kernel<kernel>(smem);
   if (e == cudaSuccess && RG > 1) e = check_registers<kernel>(kThreads<RG>, kAllRegs<RG>);
   if (e != cudaSuccess) return e;
-  const int64_t most = (int64_t)std::min(a.G, a.T * a.K) * ((a.I + 16 * RG - 1) / (16 * RG)) * (a.T > M ? 2 : 1);
-  return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(most, sms * kPerSm)), dim3(kThreads<RG>), smem, s, a, maps.w13,
-                    maps.x);
+  // An expert's tokens make one item, and one more for every M of them.
+  const int experts = std::min(a.G, a.T * a.K), items = experts + (a.T > M ? a.T * a.K / M : 0);
+  const int64_t most = (int64_t)items * ((a.I + 16 * RG - 1) / (16 * RG));
+  // Few units: clusters share the stages of one, as many CTAs as find a place at once, two
+  // stages each at least (46 tokens, 6 experts, hidden 5840, inter 288, 16-bit
+  // weights: 48 us, so 35; 40 tokens, 3 experts, hidden 4096, inter 384, fp8: 31, so 20).
+  a.cluster = 1;
+  if (RG > 1 && 2 * most <= sms)
+    for (int c = (int)std::min<int64_t>({8, sms / most, (a.H + kChunk<FP8, RG> - 1) / kChunk<FP8, RG> / 2}); c > 1; --c)
+      if ((size_t)(c - 1) * kWarps<RG> * kBoxLines<RG, NB> * 512 <= a.stages * stage &&
+          most + (c > 2) <= active_clusters<kernel>(c, kThreads<RG>, smem)) {
+        a.cluster = c;
+        break;
+      }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(most, sms * kPerSm) * a.cluster));
+  cfg.blockDim = dim3(kThreads<RG>);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)a.cluster, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, maps.w13, maps.x);
 }
 
 // The down kernel's launch: tiles, and as many CTAs a tile as are all on the GPU at once: a
 // second wave pays its start again (1 token, hidden 7168: 134 us with 4, 117 with 1; 64
 // tokens, fp8: 529 with 8, 491 with 2). Clusters that the SMs would hold need not all find a
-// place (hidden 2064, 17 tiles: 15 clusters of 8; 54 us, with 22 tiles and clusters of 6: 40).
+// place (hidden 2064, 17 tiles: 15 clusters of 8; 54 us, with 22 tiles and clusters of 6:
+// 40), and while the up kernel ends, one fewer may (hidden 5840, 46 tiles, as many clusters of
+// 3: 49 us; 61 of 2: 38).
 template <typename T, bool FP8, int NB, int RG>
 struct Down {
   static constexpr auto kernel = down_kernel<T, FP8, NB, RG>;
@@ -1017,7 +1070,7 @@ struct Down {
     stages = fit_stages(rest, stage, kPerSm);
     smem = 1024 + stages * stage + rest;
     for (int c = std::min(8, kPerSm * sms / tiles); c > 1; --c)
-      if (tiles <= active_clusters<kernel>(c, kThreads<RG>, smem)) {
+      if (tiles + (c > 2) <= active_clusters<kernel>(c, kThreads<RG>, smem)) {
         cluster = c;
         break;
       }

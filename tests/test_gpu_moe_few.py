@@ -94,6 +94,37 @@ def test_long_rows(shape, x_dtype, fp8):
     _check(cfg, _run(cfg, *t), *t)
 
 
+# Few experts and long rows: several CTAs share a unit of the first product, up to eight of
+# them, with uneven shares; one expert's tokens make two items; masks leave experts empty.
+FEW_UNITS = [(9, 1, 1, 4112, 16), (12, 3, 2, 2064, 48), (16, 2, 1, 7168, 144), (20, 2, 2, 8208, 96), (33, 1, 1, 5136, 208),
+             (46, 6, 3, 5840, 288), (64, 2, 2, 1040, 80), (64, 3, 2, 9232, 64)]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("x_dtype", [0, 1])
+@pytest.mark.parametrize("shape", FEW_UNITS, ids=str)
+def test_units_shared_by_ctas(shape, x_dtype, fp8):
+    T, G, K, H, N = shape
+    t = _inputs("few units", T, G, K, H, N, x_dtype, fp8)
+    mask = (torch.rand(T, K, generator=_gen("mask", shape)) < 0.6).to(torch.uint8)
+    for m in (None, mask):
+        cfg = cq.MoeConfig(T, G, K, H, N, x_dtype=x_dtype, w_dtype=int(fp8), out_dtype=1, mask_ndim=0 if m is None else 2)
+        y = _run(cfg, *t, mask=m)
+        _check(cfg, y, *t, mask=m)
+        assert torch.equal(y, _run(cfg, *t, mask=m))
+    assert cq.read_expert_status() == 0
+
+
+# Numbers of tiles whose clusters do not all find a place at once, and just do.
+@pytest.mark.parametrize("shape", [(43, 5, 3, 2064, 112), (9, 4, 2, 2528, 80), (2, 3, 1, 1872, 80), (19, 4, 4, 5840, 48)], ids=str)
+@pytest.mark.parametrize("fp8", [False, True])
+def test_tiles_and_places(shape, fp8):
+    T, G, K, H, N = shape
+    t = _inputs("places", T, G, K, H, N, 1, fp8)
+    cfg = cq.MoeConfig(T, G, K, H, N, x_dtype=1, w_dtype=int(fp8))
+    _check(cfg, _run(cfg, *t), *t)
+
+
 @pytest.mark.parametrize("ndim", [1, 2])
 def test_masks(ndim):
     """Masked pairs take no part, whatever their ids; a token without an active pair gives 0."""
