@@ -18,9 +18,9 @@
 // through distributed shared memory, in order. Results do not depend on timing. The
 // second kernel's copies of weights start before the first one has ended.
 //
-// Tokens' rows come a stage at a time by one tiled copy: all tokens' (up; fp8 weights: only
-// an item's, by three warps), an item's, which lie together (down). Row by row, 256 bytes each, the copies were the bound (64 tokens,
-// bf16: 852 -> 563 us).
+// Tokens' rows come a stage at a time by one tiled copy: all tokens' (up; fp8 weights:
+// only an item's, by three warps), an item's, which lie together (down). Row by row, 256
+// bytes each, the copies were the bound (64 tokens, bf16: 852 -> 563 us).
 //
 // Between the two SwiGLU's results are held as two numbers of the token type, whose sum
 // keeps 16 bits or more: rounding them to one would add an error as large as y's own
@@ -1158,9 +1158,12 @@ cudaError_t launch_large(const LayerArgs& a, const void* w13, const void* w2, in
 
 // Tiles of 128 rows and sixteen warps, one CTA a SM, where that gives each SM a unit of the
 // up kernel (hidden 7168, inter 2048, bf16, 8 tokens: 366 us against 383 with tiles of 32
-// rows and two CTAs a SM; fp8, 2 tokens: 131 against 132, 8 tokens: 244 against 269), else
-// the small ones (hidden 1024, inter 512, 8 tokens: 14.3 against 19.2). fp16 tokens with
-// fp8 weights need no cheaper decoding: small tiles up to 4 tokens (2: 112 against 128).
+// rows and two CTAs a SM; fp8, 2 tokens: 131 against 132, 8 tokens: 244 against 269; fp16
+// tokens with fp8 weights need no cheaper decoding: small tiles up to 4 tokens (2: 112 against
+// 128)). With fewer units and up to 8 tokens, the small ones where rows are short (hidden 1024,
+// inter 512, 8 tokens: 14.2 against 15.0) or bf16 tokens would be scaled first (fp8, hidden
+// 4096, inter 512, 8 tokens: 18 against 23), else clusters of large ones (hidden 7168, inter
+// 1024, 1 token: 17 against 21; hidden 1552, inter 384, 2 tokens: 16 against 17).
 // The down kernel takes tiles of 96 rows where those and their clusters cover more SMs
 // (hidden 7168: 150 of 152 instead of 112; 64 tokens, bf16: 524 -> 494 us).
 template <typename T, bool FP8>
@@ -1168,7 +1171,8 @@ cudaError_t launch(const LayerArgs& a, const void* w13, const void* w2, cudaStre
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorUnknown;
   const bool units = (int64_t)std::min(a.G, a.T * a.K) * ((a.I + 63) / 64) >= sms;
-  if (a.T <= 8 && (!units || (FP8 && !T::kBf16 && a.T <= 4))) return launch_t<T, FP8, 1, 1, 1>(a, w13, w2, sms, s);
+  const bool small = units ? FP8 && !T::kBf16 && a.T <= 4 : (FP8 && T::kBf16) || a.H < 1536;
+  if (a.T <= 8 && small) return launch_t<T, FP8, 1, 1, 1>(a, w13, w2, sms, s);
   return a.T <= 16 ? launch_large<T, FP8, 2>(a, w13, w2, sms, s) : launch_large<T, FP8, 4>(a, w13, w2, sms, s);
 }
 
