@@ -31,8 +31,11 @@
 // run in fp16 there, whose range powers of two provide: each token's row is scaled by one
 // (scale_kernel, where tokens are bf16; exact but for values 2^-38 below the row's largest),
 // SwiGLU's results by one for 64 of a pair, which the down product's warps multiply back.
-// These are rounded to fp16 once, to 11 bits: an eighth of bf16's rounding of y (64 tokens:
-// 461 -> 367 us).
+// Where y is bf16 these are rounded to fp16 once, to 11 bits: an eighth of y's own rounding
+// (64 tokens: 461 -> 367 us). Where y is fp16 or f32 that would be as much as y's rounding or
+// thousands of times it, so there two numbers stay, 22 bits of a value and 2^-39 of the 64's
+// largest (64 tokens, f32 y: 339 us, with one number 307; 16 tokens: 238, 229; 43 tokens,
+// hidden 2064, inter 752, fp16: 39.5, 37.8).
 //
 // Measured on one GB300 (copy 6.78 TB/s), hidden 7168, inter 2048, 8 of 32 experts, in a
 // graph: 1 token, bf16: 111 us, 6.4 TB/s; 16 tokens: 411 us, 6.9 TB/s; 64 tokens: 460 us,
@@ -62,13 +65,14 @@ struct LayerArgs {
   int32_t T, G, K, H, I, mask_ndim, out_f32;
   int32_t stages, cluster;   // of the ring; CTAs that share a tile (down_kernel) or a unit (up_kernel)
   int32_t whole;             // rows of x (h) are whole blocks of 64: one copy takes a stage's
+  int32_t two;               // scaled: h as two numbers
   const uint16_t* x;
   const int32_t* ids;
   const float* scales;
   const uint8_t* mask;
   const float* w13_scales;
   const float* w2_scales;
-  uint16_t* h;  // [2][T * K][I]: both numbers; scaled: [T * K][I]
+  uint16_t* h;  // [2][T * K][I]: both numbers, or [T * K][I]
   float* h_scales;           // scaled: [T * K][units of 64]
   float* x_scales;           // scaled, bf16 tokens: [T], else NULL
   uint16_t* x16;             // and their rows [T][H]
@@ -515,14 +519,14 @@ __global__ void __launch_bounds__(256) scale_kernel(const uint16_t* x, uint16_t*
   if (threadIdx.x == 0) scales[blockIdx.x] = ldexpf(1.f, -e);
 }
 
-// A result of SwiGLU as two numbers of the token type.
+// A result of SwiGLU as two numbers of type T, or as the first alone.
 template <typename T>
-__device__ __forceinline__ void store_two(const LayerArgs& a, int pair, int i, float r) {
+__device__ __forceinline__ void store_h(const LayerArgs& a, int pair, int i, float r, bool two) {
   const uint16_t hi = rounded<T>(r);
   uint16_t* to = a.h + (size_t)pair * a.I + i;
   to[0] = hi;
   // an infinite first number would make the second NaN
-  to[(size_t)a.T * a.K * a.I] = rounded<T>(fabsf(T::lo(hi)) <= 3.402823466e38f ? r - T::lo(hi) : 0.f);
+  if (two) to[(size_t)a.T * a.K * a.I] = rounded<T>(fabsf(T::lo(hi)) <= 3.402823466e38f ? r - T::lo(hi) : 0.f);
 }
 
 // Large tiles: the four shares of k of a row group are added, SwiGLU, and the results
@@ -622,7 +626,7 @@ __device__ __forceinline__ bool finish(const LayerArgs& a, const Items& items, i
         g = i ? mine[0].y : mine[0].x, w = i ? mine[0].w : mine[0].z;
       }
       v[h][i] = swiglu(g * f, w * f);
-      if (!kScaled<FP8, RG> && in && j < m) store_two<T>(a, off + j, i0 + first + 8 * h, v[h][i]);
+      if (!kScaled<FP8, RG> && in && j < m) store_h<T>(a, off + j, i0 + first + 8 * h, v[h][i], true);
     }
   }
   if constexpr (kScaled<FP8, RG>) {
@@ -649,7 +653,7 @@ __device__ __forceinline__ bool finish(const LayerArgs& a, const Items& items, i
       if (!in || j >= m) continue;
       const int e = f16_exponent(top);
 #pragma unroll
-      for (int h = 0; h < HALVES; ++h) a.h[(size_t)(off + j) * a.I + i0 + first + 8 * h] = rounded<F16>(ldexpf(v[h][i], e));
+      for (int h = 0; h < HALVES; ++h) store_h<F16>(a, off + j, i0 + first + 8 * h, ldexpf(v[h][i], e), a.two);
       if (group == 0 && lane < 4 && (NB == 4 || !(seg & 1))) a.h_scales[(size_t)(off + j) * units + i0 / 64] = ldexpf(1.f, -e);
     }
   }
@@ -807,21 +811,21 @@ up_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorM
         pg += p[q * kRows * (M + 1)];
         pu += p[(q * kRows + 16) * (M + 1)];
       }
-      store_two<T>(a, off + j, i0 + o, swiglu(pg, pu));
+      store_h<T>(a, off + j, i0 + o, swiglu(pg, pu), true);
     }
     if (!async::meet<32 * WARPS>(true)) break;
   }
 }
 
-// Down product and weighted sum.
-template <typename T, bool FP8, int NB, int RG>
+// Down product and weighted sum. TWO: h as two numbers.
+template <typename T, bool FP8, int NB, int RG, bool TWO>
 __global__ void __launch_bounds__(kThreads<RG>, RG == 1 ? 2 : 1)
 down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorMap map,
             const __grid_constant__ TokenMaps map_h) {
   constexpr int KC = kChunk<FP8, RG>, BLOCKS = kBlocks<FP8, RG>, M = 8 * NB, WARPS = kWarps<RG>;
   constexpr int kRows = 32 * RG, BOXES = kBoxes<RG>, kBoxK = KC / BOXES, kLine = kDownLine<RG>, SW = kStageW<RG>;
   constexpr bool SCALED = kScaled<FP8, RG>;
-  constexpr int PARTS = SCALED ? 1 : 2, kTokens = BLOCKS * PARTS * M * 128;  // the numbers' lines
+  constexpr int PARTS = TWO ? 2 : 1, kTokens = BLOCKS * PARTS * M * 128;  // the numbers' lines
   using M16 = std::conditional_t<SCALED, F16, T>;  // of the products
   constexpr int kSums = kDownSums<RG, NB>;
   extern __shared__ __align__(1024) uint8_t dyn[];
@@ -1058,14 +1062,14 @@ cudaError_t launch_up(LayerArgs a, const Maps& maps, int sms, cudaStream_t s) {
 // place (hidden 2064, 17 tiles: 15 clusters of 8; 54 us, with 22 tiles and clusters of 6:
 // 40), and while the up kernel ends, one fewer may (hidden 5840, 46 tiles, as many clusters of
 // 3: 49 us; 61 of 2: 38).
-template <typename T, bool FP8, int NB, int RG>
+template <typename T, bool FP8, int NB, int RG, bool TWO>
 struct Down {
-  static constexpr auto kernel = down_kernel<T, FP8, NB, RG>;
+  static constexpr auto kernel = down_kernel<T, FP8, NB, RG, TWO>;
   static constexpr int kRows = 32 * RG, kPerSm = RG == 1 ? 2 : 1;
   int tiles, cluster = 1, stages;
   size_t smem;
   Down(const LayerArgs& a, int sms) : tiles((a.H + kRows - 1) / kRows) {
-    constexpr size_t stage = kStageW<RG> + kBlocks<FP8, RG> * (kScaled<FP8, RG> ? 1 : 2) * 8 * NB * 128;
+    constexpr size_t stage = kStageW<RG> + kBlocks<FP8, RG> * (TWO ? 2 : 1) * 8 * NB * 128;
     const size_t rest = 4 * (size_t)kDownSums<RG, NB> * a.T * kDownLine<RG>;
     stages = fit_stages(rest, stage, kPerSm);
     smem = 1024 + stages * stage + rest;
@@ -1077,9 +1081,9 @@ struct Down {
   }
 };
 
-template <typename T, bool FP8, int NB, int RG>
+template <typename T, bool FP8, int NB, int RG, bool TWO>
 cudaError_t launch_down(LayerArgs a, const Maps& maps, int sms, cudaStream_t s) {
-  const Down<T, FP8, NB, RG> d(a, sms);
+  const Down<T, FP8, NB, RG, TWO> d(a, sms);
   constexpr auto kernel = d.kernel;
   const size_t smem = d.smem;
   a.stages = d.stages;
@@ -1105,11 +1109,12 @@ cudaError_t launch_down(LayerArgs a, const Maps& maps, int sms, cudaStream_t s) 
 }
 
 // RU, RD: row groups of the two kernels.
-template <typename T, bool FP8, int NB, int RU, int RD>
+template <typename T, bool FP8, int NB, int RU, int RD, bool TWO>
 cudaError_t launch_t(LayerArgs a, const void* w13, const void* w2, int sms, cudaStream_t s) {
   constexpr int M = 8 * NB;
   constexpr bool kScale = kScaled<FP8, RD>;
-  static_assert(kScaled<FP8, RU> == kScale, "both kernels hold h alike");
+  static_assert(kScaled<FP8, RU> == kScale && (TWO || kScale), "both kernels hold h alike");
+  a.two = TWO;
   const MapType type = FP8 ? kMapU8 : T::kBf16 ? kMapBF16 : kMapF16, token = T::kBf16 && !kScale ? kMapBF16 : kMapF16;
   if (kScale && T::kBf16) {
     const cudaError_t e = launch_pdl(scale_kernel, dim3(a.T), dim3(256), 0, s, a.x, a.x16, a.x_scales, a.H);
@@ -1137,23 +1142,30 @@ cudaError_t launch_t(LayerArgs a, const void* w13, const void* w2, int sms, cuda
     if (!make_map(&m.x, a.x, token, 3, d, st, b)) return cudaErrorUnknown;
   }
   const bool whole = I % 64 == 0;
-  const uint64_t d[] = {whole ? 64 : I, P, kScale ? 1 : 2, whole ? I / 64 : 1};
+  const uint64_t d[] = {whole ? 64 : I, P, TWO ? 2 : 1, whole ? I / 64 : 1};
   const uint64_t st[] = {2 * I, 2 * I * P, whole ? 128 : 4 * I * P};
   CUtensorMap* const to[] = {&m.h.rows8, &m.h.rows16, &m.h.rows32};
   for (int k = 0; k < 3 && 8 << k <= M; ++k) {
-    const uint32_t b[] = {64, 8u << k, kScale ? 1 : 2, whole ? (uint32_t)kBlocks<FP8, RD> : 1};
+    const uint32_t b[] = {64, 8u << k, TWO ? 2 : 1, whole ? (uint32_t)kBlocks<FP8, RD> : 1};
     if (!make_map(to[k], a.h, token, 4, d, st, b)) return cudaErrorUnknown;
   }
   const cudaError_t e = launch_up<T, FP8, NB, RU>(a, m, sms, s);
-  return e == cudaSuccess ? launch_down<T, FP8, NB, RD>(a, m, sms, s) : e;
+  return e == cudaSuccess ? launch_down<T, FP8, NB, RD, TWO>(a, m, sms, s) : e;
+}
+
+template <typename T, bool FP8, int NB, bool TWO>
+cudaError_t launch_tiles(const LayerArgs& a, const void* w13, const void* w2, int sms, cudaStream_t s) {
+  const Down<T, FP8, NB, 3, TWO> d3(a, sms);
+  const Down<T, FP8, NB, 4, TWO> d4(a, sms);
+  return d3.tiles * d3.cluster > d4.tiles * d4.cluster ? launch_t<T, FP8, NB, 4, 3, TWO>(a, w13, w2, sms, s)
+                                                       : launch_t<T, FP8, NB, 4, 4, TWO>(a, w13, w2, sms, s);
 }
 
 template <typename T, bool FP8, int NB>
 cudaError_t launch_large(const LayerArgs& a, const void* w13, const void* w2, int sms, cudaStream_t s) {
-  const Down<T, FP8, NB, 3> d3(a, sms);
-  const Down<T, FP8, NB, 4> d4(a, sms);
-  return d3.tiles * d3.cluster > d4.tiles * d4.cluster ? launch_t<T, FP8, NB, 4, 3>(a, w13, w2, sms, s)
-                                                       : launch_t<T, FP8, NB, 4, 4>(a, w13, w2, sms, s);
+  if constexpr (FP8 && T::kBf16)
+    if (!a.out_f32) return launch_tiles<T, FP8, NB, false>(a, w13, w2, sms, s);
+  return launch_tiles<T, FP8, NB, true>(a, w13, w2, sms, s);
 }
 
 // Tiles of 128 rows and sixteen warps, one CTA a SM, where that gives each SM a unit of the
@@ -1172,7 +1184,7 @@ cudaError_t launch(const LayerArgs& a, const void* w13, const void* w2, cudaStre
   if (sms <= 0) return cudaErrorUnknown;
   const bool units = (int64_t)std::min(a.G, a.T * a.K) * ((a.I + 63) / 64) >= sms;
   const bool small = units ? FP8 && !T::kBf16 && a.T <= 4 : (FP8 && T::kBf16) || a.H < 1536;
-  if (a.T <= 8 && small) return launch_t<T, FP8, 1, 1, 1>(a, w13, w2, sms, s);
+  if (a.T <= 8 && small) return launch_t<T, FP8, 1, 1, 1, true>(a, w13, w2, sms, s);
   return a.T <= 16 ? launch_large<T, FP8, 2>(a, w13, w2, sms, s) : launch_large<T, FP8, 4>(a, w13, w2, sms, s);
 }
 

@@ -523,8 +523,11 @@ size_t cq_moe_workspace_size(const cq_moe_config* cfg); /* bytes; 0 for an inval
  * overlap inputs. Products are summed in 32 bits, SwiGLU and the weighted sum taken
  * of unrounded products. Between the two products SwiGLU's result is held as the
  * sum of two numbers of x's type (16 bits or more of precision), so with fp16
- * it is infinite above 65504. With fp8 weights it may be held as one fp16 number
- * (11 bits) with a power of two for 64 of them instead.
+ * it is infinite above 65504. With fp8 weights it may be held in fp16 with a
+ * power of two for 64 of them instead: as two numbers (22 bits, and 2^-39 of the
+ * 64's largest) where y is fp16 or f32, as one (11 bits) where y is bf16. bf16 x
+ * is then fp16 with a power of two for its row (off by 2^-39 of the row's largest
+ * value at most). Which of the forms a call takes depends on its sizes.
  */
 int cq_moe_layer(const cq_moe_config* cfg, const void* x, const int32_t* expert_ids,
                  const float* expert_scales, const uint8_t* x_active_mask, const void* w13,
