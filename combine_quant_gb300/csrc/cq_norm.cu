@@ -179,9 +179,9 @@ __global__ void __launch_bounds__(512) grad_kernel(const __grid_constant__ GradA
   }
   __syncthreads();
   griddep_wait();
-  auto load = [&](int row, int s) {
+  auto load = [&](int64_t row, int s) {
     uint8_t* to = ring + s * entry;
-    const size_t at = (size_t)row * a.H;
+    const size_t at = row * a.H;
     mbar_arrive_expect_tx(&full[s], entry);
     bulk_load(to, a.x + at, line, &full[s]);
     bulk_load(to + line, a.dy + at, line, &full[s]);
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(512) grad_kernel(const __grid_constant__ GradA
   float dw[16] = {};
   int s = 0, lap = 0, turn = 0;
   bool ok = true;
-  for (int row = blockIdx.x; row < a.R; row += gridDim.x) {
+  for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x) {  // (the last step may pass 2^31)
     ok = mbar_wait_warp(&full[s], lap & 1);
     uint4 xv[2] = {}, dv[2] = {}, sv[2] = {};
     if (ok && mine) {
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(512) grad_kernel(const __grid_constant__ GradA
     turn ^= 1;
     if (threadIdx.x == 0) {
       const int64_t next = row + (int64_t)a.stages * gridDim.x;
-      if (next < a.R) load((int)next, s);
+      if (next < a.R) load(next, s);
     }
     if (++s == a.stages) s = 0, ++lap;
     const float m = square_scale(ss, a.eps);
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(512) grad_kernel(const __grid_constant__ GradA
       dw[t] = fmaf(d[t], hat, dw[t]);
       o[t] = r * (d[t] * w[t] - hat * c) + e[t];
     }
-    if (mine) store_unit<T>(a.dx + (size_t)row * a.H, threadIdx.x, o);
+    if (mine) store_unit<T>(a.dx + row * a.H, threadIdx.x, o);
   }
   if (!ok) {
     if (threadIdx.x == 0) {  // copies in flight land (with a limit) before the block goes
