@@ -104,6 +104,9 @@ struct Tile {
   int jh;             // tokens of the first CTA
 };
 
+// Tiles of at most 256 that an expert's rows make: equal parts (unsigned: rows + 255 may pass 2^31).
+__device__ __forceinline__ int parts_of(int rows) { return (int)(((uint32_t)rows + 255) / 256); }
+
 // GATES: a tile is 128 outputs, else 256. Columns in steps of 64 (16 outputs a CTA) or 32.
 template <bool GATES, bool OUT8>
 __device__ __forceinline__ Tile tile_at(const B128Args& a, const int* s_begin, const int* s_tile, int t) {
@@ -111,11 +114,11 @@ __device__ __forceinline__ Tile tile_at(const B128Args& a, const int* s_begin, c
   x.e = expert_of(s_tile, a.G, t);
   const int l = t - s_tile[x.e];
   const int begin = s_begin[x.e], rows = s_begin[x.e + 1] - begin;
-  const int parts = (rows + 255) / 256;
+  const int parts = parts_of(rows);
   const int band = l / (kBand * parts), first_i = band * kBand;
   const int wide = min(kBand, a.tiles_i - first_i), m = l - first_i * parts;
   const int ti = first_i + m % wide, tj = m / wide;
-  const int step = (rows + parts - 1) / parts;  // equal parts
+  const int step = (int)(((uint32_t)rows + parts - 1) / parts);
   x.row0 = begin + tj * step;
   x.rows = min(step, rows - tj * step);
   constexpr int kOuts = GATES ? 128 : 256;
@@ -259,8 +262,7 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
   // No early release of the next kernel: the permute kernel reads token rows before its
   // own wait, and they may be these results.
   griddep_wait();
-  const bool bad = group_scan<kThreads>(
-      a, s_begin, s_tile, [&](int rows) { return a.tiles_i * ((rows + 255) / 256); });
+  const bool bad = group_scan<kThreads>(a, s_begin, s_tile, [&](int rows) { return a.tiles_i * parts_of(rows); });
   if (bad && blockIdx.x == 0) atomicOr(&g_status, (uint32_t)CQ_ST_BAD_ROWS);
   fence_before();
   cluster_sync();

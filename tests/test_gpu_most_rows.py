@@ -35,3 +35,31 @@ def test_norm_gradient():
     assert not bool(dx[first:-last].any())
     del rows, grad, dx
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dx", [False, True])
+def test_products_from_fp8_rows(dx):
+    """One expert with all rows but 3: more than 2^31 - 256 of them."""
+    _room(120)
+    n = k = 16
+    spare, some = 3, 600
+    gen = torch.Generator().manual_seed(12)
+    codes = torch.randint(1, 100, (some, 16), generator=gen, dtype=torch.int32).to(torch.uint8)
+    w = torch.randint(1, 100, (2, n, k), generator=gen, dtype=torch.int32).to(torch.uint8)
+    s, ws = torch.rand(some, 1, generator=gen) + 0.5, torch.rand(2, 1, 1, generator=gen) + 0.5
+    x, xs = torch.zeros(MOST, 16, dtype=torch.uint8, device=DEV), torch.ones(MOST, 1, device=DEV)
+    x[-some:], xs[-some:] = codes.to(DEV), s.to(DEV)
+    nums = torch.tensor([MOST - spare, spare], dtype=torch.int64, device=DEV)
+    cfg = cq.ExpertConfig(experts=2, rows=MOST, n=n, k=k, x_dtype=2)
+    out = torch.full((MOST, 16), 77.0, dtype=torch.bfloat16, device=DEV)
+    if dx:
+        cq.expert_matmul_b128_dx(cfg, x, xs, w.to(DEV), ws.to(DEV), nums, dx=out)
+    else:
+        cq.expert_matmul_b128(cfg, x, xs, w.to(DEV), ws.to(DEV), nums, y=out)
+    assert cq.read_expert_status() == 0
+    v, wv = around.rows_values(codes, s), around.block_values(w, ws)
+    want, bound = ref.products(v, wv.transpose(1, 2) if dx else wv, [some - spare, spare], around.slack(16))
+    ref.check(out[-some:], want, ref.rounded(want, bound, torch.bfloat16))
+    assert not bool(out[:-some].any())
+    del x, xs, out
+    torch.cuda.empty_cache()
