@@ -907,13 +907,15 @@ down_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtenso
       f = __ldg(a.w2_scales + ((size_t)items.e[item] * hb + ob) * ib + block);
     };
     if (begin < end) factors(begin / per, 0, fn);
-    // scaled: h's powers of two, a pair a lane, of this warp's 64 k of a stage
+    // scaled: h's powers of two, a pair a lane, of this warp's 64 k of a stage. Ordinary loads: the
+    // up kernel may still write them while this kernel starts, and a read-only load need not stay
+    // behind the wait.
     const int units = (a.I + 63) / 64;
     float column = 1.f;
     auto columns = [&](int v) {
       if (!SCALED || v >= end) return;
       const int item = v / per, unit = v % per * BLOCKS + seg;
-      if (lane < items.m[item] && unit < units) column = __ldg(a.h_scales + (size_t)(items.off[item] + lane) * units + unit);
+      if (lane < items.m[item] && unit < units) column = a.h_scales[(size_t)(items.off[item] + lane) * units + unit];
     };
     if (SCALED) griddep_wait();
     columns(begin);
