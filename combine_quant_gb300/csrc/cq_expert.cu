@@ -2,9 +2,8 @@
 // contract). Every argument rule is checked before anything is enqueued; the
 // kernels are in cq_expert_gemm.cu (tensor cores) and cq_expert_w4.cu (4-bit
 // weights).
-#include <initializer_list>
-
 #include "cq_expert.cuh"
+#include "cq_status.h"
 
 namespace cq {
 namespace expert {
@@ -142,15 +141,11 @@ int cq_expert_matmul_w4(const cq_expert_config* cfg, const void* x, const uint8_
 int cq_read_expert_status(uint32_t* status, void* stream) {
   if (!status) return CQ_ERR_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  uint32_t all = 0;
-  for (auto read : {gemm_status, w4_status, b128_status, layer_status, norm_status}) {
-    uint32_t v = 0;
-    const int rc = read(&v, s);
-    if (rc != CQ_OK) return rc;
-    all |= v;
-  }
-  *status = all;
-  return CQ_OK;
+  constexpr int (*kWords[])(uint32_t*, cudaStream_t) = {gemm_status, w4_status, b128_status, layer_status, norm_status};
+  return cq::collect_status(
+      (int)(sizeof kWords / sizeof *kWords), [&](int i, uint32_t* read) { return kWords[i](read, s); },
+      [&] { return cudaStreamSynchronize(s) == cudaSuccess ? CQ_OK : CQ_ERR_CUDA; },
+      [&](int i) { return kWords[i](nullptr, s); }, status);
 }
 
 }  // extern "C"

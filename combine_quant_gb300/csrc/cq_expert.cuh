@@ -135,30 +135,29 @@ __device__ __forceinline__ void swiglu_gradient(float d, float g, float u, float
   du = da * (ga * r);
 }
 
-// Reads and clears a translation unit's status word, waiting for the stream.
+// A translation unit's status word: its copy into *read is enqueued, or (read NULL) it is
+// cleared, waiting for the stream.
 template <typename Word>
-int read_status_word(Word& word, uint32_t* status, cudaStream_t s) {
-  uint32_t v = 0;
+int status_word(Word& word, uint32_t* read, cudaStream_t s) {
   const uint32_t zero = 0;
-  if (cudaMemcpyFromSymbolAsync(&v, word, sizeof v, 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-      cudaStreamSynchronize(s) != cudaSuccess)
-    return CQ_ERR_CUDA;
-  *status = v;
-  if (v &&
-      (cudaMemcpyToSymbolAsync(word, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-       cudaStreamSynchronize(s) != cudaSuccess))
-    return CQ_ERR_CUDA;
-  return CQ_OK;
+  cudaError_t e;
+  if (read) {
+    e = cudaMemcpyFromSymbolAsync(read, word, sizeof zero, 0, cudaMemcpyDeviceToHost, s);
+  } else {
+    e = cudaMemcpyToSymbolAsync(word, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  }
+  return e == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
 }
 
-// Launchers, and the status words of their kernels (read and cleared).
+// Launchers, and the status words of their kernels (status_word).
 int launch_gemm(Op op, const Args& a, cudaStream_t s);
 int launch_w4(const Args& a, cudaStream_t s);
-int gemm_status(uint32_t* status, cudaStream_t s);
-int w4_status(uint32_t* status, cudaStream_t s);
-int b128_status(uint32_t* status, cudaStream_t s);
-int layer_status(uint32_t* status, cudaStream_t s);
-int norm_status(uint32_t* status, cudaStream_t s);
+int gemm_status(uint32_t* read, cudaStream_t s);
+int w4_status(uint32_t* read, cudaStream_t s);
+int b128_status(uint32_t* read, cudaStream_t s);
+int layer_status(uint32_t* read, cudaStream_t s);
+int norm_status(uint32_t* read, cudaStream_t s);
 
 }  // namespace expert
 }  // namespace cq

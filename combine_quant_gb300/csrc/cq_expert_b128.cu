@@ -838,7 +838,7 @@ int launch(bool dx, B128Args& a, cudaStream_t s) {
 
 }  // namespace
 
-int b128_status(uint32_t* status, cudaStream_t s) { return read_status_word(g_status, status, s); }
+int b128_status(uint32_t* read, cudaStream_t s) { return status_word(g_status, read, s); }
 
 }  // namespace expert
 }  // namespace cq

@@ -652,7 +652,7 @@ int launch_w4(const Args& a, cudaStream_t s) {
   return e == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
 }
 
-int w4_status(uint32_t* status, cudaStream_t s) { return read_status_word(g_status, status, s); }
+int w4_status(uint32_t* read, cudaStream_t s) { return status_word(g_status, read, s); }
 
 }  // namespace expert
 }  // namespace cq

@@ -1216,7 +1216,7 @@ struct Layout {
 
 }  // namespace
 
-int layer_status(uint32_t* status, cudaStream_t s) { return read_status_word(g_status, status, s); }
+int layer_status(uint32_t* read, cudaStream_t s) { return status_word(g_status, read, s); }
 
 }  // namespace expert
 }  // namespace cq

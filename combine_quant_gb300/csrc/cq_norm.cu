@@ -352,7 +352,7 @@ cudaError_t launch_grad(GradArgs a, int parts, int per, cudaStream_t s) {
 }  // namespace norm
 
 namespace expert {
-int norm_status(uint32_t* status, cudaStream_t s) { return read_status_word(norm::g_status, status, s); }
+int norm_status(uint32_t* read, cudaStream_t s) { return status_word(norm::g_status, read, s); }
 }  // namespace expert
 }  // namespace cq
 

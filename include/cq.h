@@ -537,7 +537,8 @@ int cq_moe_layer(const cq_moe_config* cfg, const void* x, const int32_t* expert_
 /* The expert products take no workspace; their status word (CQ_ST_BAD_ROWS,
  * CQ_ST_TIMEOUT; of cq_moe_layer CQ_ST_BAD_ID, of cq_norm_grad CQ_ST_TIMEOUT) is one
  * word per device. Synchronise `stream`, copy the word of
- * the current device into *status and clear it. */
+ * the current device into *status and clear it. An error before *status is
+ * written has cleared nothing; one in clearing leaves *status complete. */
 int cq_read_expert_status(uint32_t* status, void* stream);
 
 /*
