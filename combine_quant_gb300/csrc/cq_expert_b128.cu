@@ -209,6 +209,11 @@ __device__ __forceinline__ float top_of(const Pair* v, float top) {  // 8 pairs
   return top;
 }
 
+// What a group's values are multiplied by for their codes, of s = 448 / their largest: 0 where s
+// is infinite (a largest value of 0, or below 1.3e-36), as the scale 1 / s is; 0 * infinity
+// would be a NaN code.
+__device__ __forceinline__ float code_factor(float s) { return s <= 3.402823466e38f ? s : 0.f; }
+
 // 16 values times mult in e4m3.
 __device__ __forceinline__ uint4 codes16(const Pair* v, float mult) {
   uint32_t w[4];
@@ -519,7 +524,7 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
             float top = 0.f;
             if (j < x.jh)
               for (int w = 0; w < (joint ? 8 : 4); ++w) top = fmaxf(top, tb[w * kFew + j]);
-            const float s = __fdiv_rn(448.f, top), mult = top == 0.f ? 0.f : s;
+            const float s = __fdiv_rn(448.f, top), mult = code_factor(s);
             if (writes && lane < 16 && j < x.jh && c0 + j < x.rows) a.ys[((size_t)x.row0 + c0 + j) * a.nb + group] = __fdiv_rn(1.f, s);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
@@ -661,7 +666,7 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
           if (lane == 0) mbar_arrive(&bars.top[q]);
           if (!(ok = wait(&bars.top[q], nth & 1))) break;
           top = fmaxf(top, tb[128 * (half ^ 1)]);
-          const float s = __fdiv_rn(448.f, top), mult = top == 0.f ? 0.f : s;
+          const float s = __fdiv_rn(448.f, top), mult = code_factor(s);
           if (half == 0 && real) a.ys[row * a.nb + x.i0 / 128] = __fdiv_rn(1.f, s);
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
@@ -707,7 +712,7 @@ b128_kernel(const __grid_constant__ B128Args a, const __grid_constant__ CUtensor
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               if (m < chunks && 32 * m + 16 * h < left) top = top_of(acc[m] + 8 * h, top);
-          const float s = __fdiv_rn(448.f, top), mult = top == 0.f ? 0.f : s;
+          const float s = __fdiv_rn(448.f, top), mult = code_factor(s);
           if (left > 0) a.ys[row * a.nb + i0 / 128] = __fdiv_rn(1.f, s);
           uint8_t* out = static_cast<uint8_t*>(a.out) + row * a.out_cols + i0;
 #pragma unroll

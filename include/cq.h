@@ -451,7 +451,8 @@ int cq_expert_matmul_w4(const cq_expert_config* cfg, const void* x, const uint8_
  *   y          [R, n] of out_dtype (bf16 or fp16), or where y_scales is given e4m3 codes
  *   y_scales   NULL, or f32 [R, NB]: y's scales per 128 columns, by the rule of
  *              dispatch mode 3 (codes round v * (448 / max|v|), the scale is the
- *              reciprocal of that quotient), taken of the unrounded values
+ *              reciprocal of that quotient), taken of the unrounded values; where
+ *              that quotient is infinite (max|v| below 1.3e-36) codes and scale are zeros
  *   pre        NULL, or with act 1 [R, 2n] of out_dtype: receives p
  * Products are summed in 32 bits within a block, and the scaled blocks in 32 bits.
  */
@@ -570,7 +571,10 @@ int cq_check_norm_config(const cq_norm_config* cfg);
  *   codes     [R, H] int8 (mode 2) or fp8; NULL with quant_mode 0
  *   scales    f32 [R] (mode 2), f32 [R, Ceil(H, 128)] (mode 3), uint8 [R, Align2(H / 32)]
  *             (4, 5; pad column 0); NULL with quant_mode 0
- * Sums are f32 and v is not rounded before it is quantised. Pointers 16-byte
+ * Sums are f32 and v is not rounded before it is quantised. Mode 3 is dispatch's to
+ * the bit, also where 448 / max|v| (e5m2: 57344 / max|v|) of a group is infinite,
+ * max|v| below 1.3e-36 (1.7e-34): its scale is 0, and an exact 0 has a NaN code
+ * there. Pointers 16-byte
  * aligned, f32 scales 4-byte, mx scales 1. Results other than sum must not
  * overlap inputs.
  */
