@@ -33,6 +33,24 @@ bool row_ptr(const cq_expert_config* c, const void* p) {
 }
 bool ptr(const void* p) { return p && aligned(p, 16); }
 
+// Page-locked words of this thread for the status copies: copies to other memory wait each
+// by itself (five words: 54 us a call of cq_read_expert_status from Python, 21 with one wait).
+constexpr int kStatusWords = 5;
+uint32_t* host_words() {
+  struct Words {
+    uint32_t* p = nullptr;
+    ~Words() {
+      if (p) cudaFreeHost(p);
+    }
+  };
+  static thread_local Words words;
+  if (!words.p && cudaHostAlloc(reinterpret_cast<void**>(&words.p), 4 * kStatusWords, cudaHostAllocPortable) != cudaSuccess) {
+    cudaGetLastError();
+    words.p = nullptr;
+  }
+  return words.p;
+}
+
 Args base_args(const cq_expert_config* c, const int64_t* group_rows) {
   Args a = {};
   a.G = c->experts;
@@ -142,8 +160,11 @@ int cq_read_expert_status(uint32_t* status, void* stream) {
   if (!status) return CQ_ERR_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   constexpr int (*kWords[])(uint32_t*, cudaStream_t) = {gemm_status, w4_status, b128_status, layer_status, norm_status};
+  static_assert(sizeof kWords / sizeof *kWords == kStatusWords);
+  uint32_t* host = host_words();
+  if (!host) return CQ_ERR_CUDA;
   return cq::collect_status(
-      (int)(sizeof kWords / sizeof *kWords), [&](int i, uint32_t* read) { return kWords[i](read, s); },
+      kStatusWords, host, [&](int i, uint32_t* read) { return kWords[i](read, s); },
       [&] { return cudaStreamSynchronize(s) == cudaSuccess ? CQ_OK : CQ_ERR_CUDA; },
       [&](int i) { return kWords[i](nullptr, s); }, status);
 }

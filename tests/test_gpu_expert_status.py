@@ -1,0 +1,32 @@
+"""One status for all products' kernels: bits of two of them read together and cleared, from any thread."""
+import threading
+
+import pytest
+import torch
+
+import combine_quant_gb300 as cq
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+
+
+def _two_faults():
+    z = lambda *s: torch.zeros(*s, dtype=torch.uint8, device=DEV)  # noqa: E731
+    one = torch.ones(1, 1, device=DEV)
+    cq.moe_layer(cq.MoeConfig(1, 2, 1, 16, 16), torch.zeros(1, 16, dtype=torch.bfloat16, device=DEV),
+                 torch.tensor([[5]], dtype=torch.int32, device=DEV), one, torch.zeros(2, 32, 16, dtype=torch.bfloat16, device=DEV),
+                 torch.zeros(2, 16, 16, dtype=torch.bfloat16, device=DEV))
+    cq.expert_matmul_b128(cq.ExpertConfig(experts=1, rows=1, n=16, k=16, x_dtype=2), z(1, 16), one, z(1, 16, 16), one[None],
+                          torch.tensor([2], device=DEV))
+    return cq.read_expert_status(), cq.read_expert_status()
+
+
+def test_bits_of_two_kernels():
+    cq.read_expert_status()
+    want = (cq.CQ_ST_BAD_ID | cq.CQ_ST_BAD_ROWS, 0)
+    assert _two_faults() == want
+    got = []
+    t = threading.Thread(target=lambda: got.append(_two_faults()))
+    t.start()
+    t.join()
+    assert got == [want]

@@ -11,8 +11,9 @@ SOURCE = r"""
 #include "cq_status.h"
 // calls 0..n-1 read, n waits, n + 1 + i clears word i; call `bad` (-1: none) fails with -7
 extern "C" int run(int n, uint32_t* words, int bad, uint32_t* status) {
+  static uint32_t copies[8];
   return cq::collect_status(
-      n, [&](int i, uint32_t* read) { if (i == bad) return -7; *read = words[i]; return 0; },
+      n, copies, [&](int i, uint32_t* read) { if (i == bad) return -7; *read = words[i]; return 0; },
       [&] { return bad == n ? -7 : 0; },
       [&](int i) { if (n + 1 + i == bad) return -7; words[i] = 0; return 0; }, status);
 }
