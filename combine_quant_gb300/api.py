@@ -792,6 +792,7 @@ def moe_layer(cfg: MoeConfig, x: torch.Tensor, expert_ids: torch.Tensor, expert_
               y: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The whole layer for up to 64 tokens (cq_moe_layer): gate and up products,
     SwiGLU, down product and the weighted sum of each token's experts, y [T, H].
+    fp8 weights are e4m3 codes (e5m2 ones are uint8 too and are not told apart).
     A workspace that the caller passes must not serve two calls at once."""
     p = _moe_plan_of(*vars(cfg).values())
     if x is None or expert_ids is None or expert_scales is None or w13 is None or w2 is None:

@@ -29,8 +29,9 @@
 // fp8 weights and large tiles: the products are bound by instructions, and a code
 // becomes an fp16 number in half of one, a bf16 number in two and a half. So the products
 // run in fp16 there, whose range powers of two provide: each token's row is scaled by one
-// (scale_kernel, where tokens are bf16; exact but for values 2^-38 below the row's largest),
-// SwiGLU's results by one for 64 of a pair, which the down product's warps multiply back.
+// (scale_kernel, where tokens are bf16: exact down to 2^-31 of the row's largest value, below
+// that off by 2^-39 of it at most, or by 2^-135 in rows below 2^-96), SwiGLU's results by one for
+// 64 of a pair, which the down product's warps multiply back.
 // Where y is bf16 these are rounded to fp16 once, to 11 bits: an eighth of y's own rounding
 // (64 tokens: 461 -> 367 us). Where y is fp16 or f32 that would be as much as y's rounding or
 // thousands of times it, so there two numbers stay, 22 bits of a value and 2^-39 of the 64's
@@ -479,7 +480,8 @@ __device__ __forceinline__ uint16_t rounded(float v) {
 }
 
 // The exponent of the power of two that brings the finite value m > 0 into [2^14, 2^15); at
-// most 110, so that the reciprocal times a block's scale stays a normal number.
+// most 110 (m below 2^-96 stays below 2^14), so that the reciprocal times a block's scale stays
+// a normal number.
 __device__ __forceinline__ int f16_exponent(float m) { return m > 0.f ? min(110, 14 - ilogbf(m)) : 0; }
 
 // bf16 rows times a power of two each, in fp16, and its reciprocal: a block a row.
@@ -1173,8 +1175,9 @@ cudaError_t launch_large(const LayerArgs& a, const void* w13, const void* w2, in
 // Tiles of 128 rows and sixteen warps, one CTA a SM, where that gives each SM a unit of the
 // up kernel (hidden 7168, inter 2048, bf16, 8 tokens: 366 us against 383 with tiles of 32
 // rows and two CTAs a SM; fp8, 2 tokens: 131 against 132, 8 tokens: 244 against 269; fp16
-// tokens with fp8 weights need no cheaper decoding: small tiles up to 4 tokens (2: 112 against
-// 128)). With fewer units and up to 8 tokens, the small ones where rows are short (hidden 1024,
+// tokens with fp8 weights need no cheaper decoding: small tiles up to 4 tokens (2 tokens,
+// hidden 512, inter 1536: 20 against 23; hidden 4096, inter 1408: 57 against 60; hidden 7168,
+// inter 2048: 107 against 104)). With fewer units and up to 8 tokens, the small ones where rows are short (hidden 1024,
 // inter 512, 8 tokens: 14.2 against 15.0) or bf16 tokens would be scaled first (fp8, hidden
 // 4096, inter 512, 8 tokens: 18 against 23), else clusters of large ones (hidden 7168, inter
 // 1024, 1 token: 17 against 21; hidden 1552, inter 384, 2 tokens: 16 against 17).

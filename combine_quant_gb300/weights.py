@@ -3,8 +3,8 @@ are loaded (torch operations on the weights' device; no part of a call).
 
 ``quantize_mx``: fp8 codes with one power-of-two scale per 32 of the last axis,
 for ``expert_matmul`` with mx types. ``quantize_b128``: fp8 codes with one f32
-scale per block of 128 x 128, for ``expert_matmul_b128`` and ``moe_layer``. ``quantize_w4``: 4-bit codes with group
-scales, for ``expert_matmul_w4``.
+scale per block of 128 x 128, for ``expert_matmul_b128`` and (e4m3 only) ``moe_layer``. ``quantize_w4``: 4-bit codes
+with group scales, for ``expert_matmul_w4``.
 """
 from __future__ import annotations
 

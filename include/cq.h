@@ -513,7 +513,8 @@ size_t cq_moe_workspace_size(const cq_moe_config* cfg); /* bytes; 0 for an inval
  *   expert_scales f32 [T, K] routing weights
  *   x_active_mask uint8 [T] or [T, K], required with mask_ndim 1 or 2, else NULL;
  *                 a token without an active pair gives 0
- *   w13           [G, 2I, H], gate rows first; w2 [G, H, I]
+ *   w13           [G, 2I, H], gate rows first; w2 [G, H, I]; w_dtype 1: e4m3 codes (e5m2
+ *                 codes look the same and are not told apart)
  *   w13_scales    f32 [G, 2 Ceil(I, 128), Ceil(H, 128)], w2_scales f32 [G, Ceil(H, 128),
  *                 Ceil(I, 128)] with w_dtype 1 (blocks as in cq_expert_matmul_b128), else NULL
  *   y             [T, H]
@@ -528,7 +529,7 @@ size_t cq_moe_workspace_size(const cq_moe_config* cfg); /* bytes; 0 for an inval
  * power of two for 64 of them instead: as two numbers (22 bits, and 2^-39 of the
  * 64's largest) where y is fp16 or f32, as one (11 bits) where y is bf16. bf16 x
  * is then fp16 with a power of two for its row (off by 2^-39 of the row's largest
- * value at most). Which of the forms a call takes depends on its sizes.
+ * value at most; for rows, or 64 results, below 2^-96 by 2^-135). Which of the forms a call takes depends on its sizes.
  */
 int cq_moe_layer(const cq_moe_config* cfg, const void* x, const int32_t* expert_ids,
                  const float* expert_scales, const uint8_t* x_active_mask, const void* w13,
