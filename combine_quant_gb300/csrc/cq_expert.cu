@@ -39,8 +39,9 @@ constexpr int kStatusWords = 5;
 uint32_t* host_words() {
   struct Words {
     uint32_t* p = nullptr;
-    ~Words() {
-      if (p) cudaFreeHost(p);
+    ~Words() {  // a thread may end while another one captures a graph, which this must not end
+      cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+      if (p && cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess) cudaFreeHost(p);
     }
   };
   static thread_local Words words;

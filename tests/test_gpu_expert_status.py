@@ -30,3 +30,28 @@ def test_bits_of_two_kernels():
     t.start()
     t.join()
     assert got == [want]
+
+
+def test_a_thread_that_read_the_status_ends_during_a_capture():
+    """Its page-locked words are released without harm to the graph that another thread captures."""
+    read, end = threading.Event(), threading.Event()
+
+    def work():
+        cq.read_expert_status()
+        read.set()
+        end.wait()
+    t = threading.Thread(target=work)
+    t.start()
+    read.wait()
+    x = torch.ones(64, device=DEV)
+    x * 2
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = x * 2
+        end.set()
+        t.join()
+        z = y + 1
+    g.replay()
+    torch.cuda.synchronize()
+    assert bool((z == 3).all())
