@@ -1177,10 +1177,11 @@ cudaError_t launch_large(const LayerArgs& a, const void* w13, const void* w2, in
 // rows and two CTAs a SM; fp8, 2 tokens: 131 against 132, 8 tokens: 244 against 269; fp16
 // tokens with fp8 weights need no cheaper decoding: small tiles up to 4 tokens (2 tokens,
 // hidden 512, inter 1536: 20 against 23; hidden 4096, inter 1408: 57 against 60; hidden 7168,
-// inter 2048: 107 against 104)). With fewer units and up to 8 tokens, the small ones where rows are short (hidden 1024,
-// inter 512, 8 tokens: 14.2 against 15.0) or bf16 tokens would be scaled first (fp8, hidden
-// 4096, inter 512, 8 tokens: 18 against 23), else clusters of large ones (hidden 7168, inter
-// 1024, 1 token: 17 against 21; hidden 1552, inter 384, 2 tokens: 16 against 17).
+// inter 2048: 107 against 104)). With fewer units and up to 8 tokens, the small ones where rows
+// are short (hidden 1024, inter 512, 8 tokens: 14.2 against 15.0) or bf16 tokens would be scaled
+// first (fp8, hidden 4096, inter 512, 8 tokens: 18 against 23), else clusters of large ones
+// (hidden 7168, inter 1024, 1 token: 17 against 21; hidden 1552, inter 384, 2 tokens: 16 against
+// 17).
 // The down kernel takes tiles of 96 rows where those and their clusters cover more SMs
 // (hidden 7168: 150 of 152 instead of 112; 64 tokens, bf16: 524 -> 494 us).
 template <typename T, bool FP8>
