@@ -529,7 +529,8 @@ size_t cq_moe_workspace_size(const cq_moe_config* cfg); /* bytes; 0 for an inval
  * power of two for 64 of them instead: as two numbers (22 bits, and 2^-39 of the
  * 64's largest) where y is fp16 or f32, as one (11 bits) where y is bf16. bf16 x
  * is then fp16 with a power of two for its row (off by 2^-39 of the row's largest
- * value at most; for rows, or 64 results, below 2^-96 by 2^-135). Which of the forms a call takes depends on its sizes.
+ * value at most; for rows, or 64 results, below 2^-96 by 2^-135). Which of the
+ * forms a call takes depends on its sizes.
  */
 int cq_moe_layer(const cq_moe_config* cfg, const void* x, const int32_t* expert_ids,
                  const float* expert_scales, const uint8_t* x_active_mask, const void* w13,
