@@ -9,7 +9,7 @@
 // row wait at a barrier; a thread keeps one unit and its columns' share of dw.
 //
 // Measured on one GB300 (copy 6.78 TB/s), 16384 x 7168 bf16: residual, sum, y and fp8 rows
-// 167 us, 6.4 TB/s; gradient with the residual's 164 us, 5.7 TB/s (408 us with a row read
+// 167 us, 6.4 TB/s; gradient with the residual's 162 us, 5.8 TB/s (408 us with a row read
 // after the other).
 #include "cq_expert.cuh"
 #include "cq_permute_impl.cuh"
